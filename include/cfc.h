@@ -17,6 +17,11 @@
  *   cfc_kloop_forward_backward_static
  *                       forward + backward for callers that cannot allocate
  *                       device memory (fixed workspace inside the library);
+ *   cfc_gdr_*           the gated delta rule, a matrix-state recurrence for long
+ *                       sequences: forward, backward, and its form for the next
+ *                       tokens of decoding sequences (FP32, bf16);
+ *   cfc_rmsnorm_*       root-mean-square norm of a residual stream, forward
+ *                       (optionally to 8 bits with scales) and backward;
  *   helpers             workspace sizes, status strings, the device error
  *                       word and its self-test, per-kernel event tracing.
  *
@@ -266,6 +271,105 @@ int cfc_grn_backward(const float* h, int B, int K, int hidden, int head_mid, int
                      const float* probs, const float* saved, const float* grad_probs, const float* lambda,
                      const float* grad_h_carry, float* grad_h, float* per_sample_scratch, float* grad_params,
                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated delta rule (FP32 and BF16 modes; CFC_MATH_TF32 gives CFC_ERR_MODE).
+ * Each sequence and value head h keeps a state S [d_k, d_v], zero or
+ * initial_state at first, and per token t does
+ *   S <- exp(g_t) S,  u = beta_t (v_t - S^T k_t),  S <- S + k_t u^T,
+ *   o_t = scale S^T q_t.
+ * Value head h uses query and key head h / (n_v_heads / n_k_heads).  g <= 0 is
+ * the log-decay (-inf, and anything below -110, is a factor of zero: a reset);
+ * for a bounded state beta |k|^2 stays in [0, 2].
+ *
+ * Shapes, rows being all tokens of all sequences one after another:
+ *   q, k  [rows, n_k_heads, d_k], v [rows, n_v_heads, d_v]: float (FP32) or
+ *         bfloat16 (BF16); the head and width axes are dense, rows are
+ *         *_stride elements apart (at least heads * width, a multiple of 16
+ *         bytes), so they may be parts of one projection's output
+ *   g, beta [rows, n_v_heads]: float in both modes
+ *   o, grad_o, grad_v like v but dense; grad_q, grad_k like q, k but dense;
+ *   grad_g, grad_beta [rows, n_v_heads] in the type of q (float or bfloat16)
+ *   states [n_seq, n_v_heads, d_k, d_v]: float in both modes
+ * Sequences: with seq_offsets NULL, n_seq sequences of rows / n_seq tokens;
+ * else seq_offsets is a DEVICE array of n_seq + 1 non-decreasing row numbers,
+ * seq_offsets[0] = 0 and seq_offsets[n_seq] = rows, and sequence i has the rows
+ * from seq_offsets[i] up to seq_offsets[i + 1] (none is allowed).  Offsets
+ * outside [0, rows] are held to it: nothing outside the tensors is touched.
+ * Sizes: d_k a multiple of 8 in [8, 128], d_v a multiple of 8 in [8, 256],
+ * n_v_heads a multiple of n_k_heads and at most 4096, 1 <= n_seq <= 2^20,
+ * 0 <= rows <= 2^30.  q, k, v, o, states, grad_o, grad_q, grad_k, grad_v and
+ * the workspace are 16-byte aligned, the rest 4-byte aligned.
+ *
+ * FP32: products of two TF32 values an operand, fp32-accurate.  BF16: products
+ * take bf16 operands and sum in fp32; the running state is fp32, and where a
+ * final_state is asked for, every operand on the way to it keeps 17
+ * significant bits, so that the state is good to about 1e-5 (o and the
+ * gradients, which leave in bf16, to their own rounding). */
+
+/* Device workspace of the two calls (save != 0: of a forward that a backward
+ * follows, and of that backward).  Host-only; 0 for unsupported sizes. */
+size_t cfc_gdr_workspace_bytes(long long rows, int n_seq, int n_k_heads, int n_v_heads, int d_k, int d_v, int math,
+                               int save);
+
+/* Forward over whole sequences.  initial_state and final_state may be NULL, or
+ * the same buffer.  save != 0: keeps in the workspace what the backward reads. */
+int cfc_gdr_forward(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                    long long v_stride, const float* g, const float* beta, const int* seq_offsets, int n_seq,
+                    long long rows, int n_k_heads, int n_v_heads, int d_k, int d_v, float scale, int math,
+                    const float* initial_state, void* o, float* final_state, int save, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Backward of the forward that filled `workspace` (same inputs, save != 0).
+ * grad_final_state may be NULL (zero), grad_initial_state too (not written).
+ * All outputs are overwritten; grad_q and grad_k are summed over the value
+ * heads of a group in a fixed order. */
+int cfc_gdr_backward(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                     long long v_stride, const float* g, const float* beta, const int* seq_offsets, int n_seq,
+                     long long rows, int n_k_heads, int n_v_heads, int d_k, int d_v, float scale, int math,
+                     const void* grad_o, const float* grad_final_state, void* grad_q, void* grad_k, void* grad_v,
+                     void* grad_g, void* grad_beta, float* grad_initial_state, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* The next `tokens` tokens of each of n_seq sequences (rows = n_seq * tokens):
+ * sequence i's state is slots[i] of `state` [n_slots, n_v_heads, d_k, d_v]
+ * (slots NULL: i), updated in place.  No two sequences may share a slot.  A
+ * sequence whose slot is outside [0, n_slots) has no state: its o is zero and
+ * nothing is kept.  All arithmetic is fp32. */
+int cfc_gdr_step(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                 long long v_stride, const float* g, const float* beta, int n_seq, int tokens, int n_k_heads,
+                 int n_v_heads, int d_k, int d_v, float scale, int math, float* state, long long n_slots,
+                 const int* slots, void* o, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm of a residual stream (FP32 and BF16 modes).
+ *   s = x + residual rounded to the stored type (s = x where residual is NULL),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s rstd weight.
+ * x, residual, y, residual_out, grad_y, grad_residual_out, grad_x [rows, d] in
+ * the mode's type; weight, grad_weight [d], rstd [rows] float.  1 <= d <= 32768.
+ * Pointers 16-byte aligned (rstd and y8_scale: 4).
+ *
+ * Forward: y and/or y8 (at least one); residual_out (= s) and rstd optional,
+ * both needed by the backward.  y8 [rows, d] holds e4m3 values y / c with one
+ * scale c for each group of y8_group columns (a divisor of d; d: one a row),
+ * y8_scale [rows, d / y8_group] float, c = max |y| of the group / 448, from y
+ * before its own rounding; c = 1 for a group of zeros.  residual_out may be
+ * the buffer of x or residual. */
+int cfc_rmsnorm_forward(const void* x, const void* residual, const float* weight, long long rows, int d, float eps,
+                        int math, void* y, void* residual_out, float* rstd, void* y8, float* y8_scale, int y8_group,
+                        void* stream);
+
+/* Device workspace of the backward; 0 for unsupported sizes.  Host-only. */
+size_t cfc_rmsnorm_workspace_bytes(long long rows, int d);
+
+/* Backward from the stream s and rstd of the forward: grad_x is the gradient
+ * of s, hence of x and of residual: the norm's own plus grad_residual_out (the
+ * gradient that reaches s from later layers; NULL: none).  grad_weight is the
+ * sum over rows (0 for rows = 0), its partial sums added by reduce_axis0.
+ * grad_x may be the buffer of grad_y or grad_residual_out. */
+int cfc_rmsnorm_backward(const void* s, const float* weight, const float* rstd, const void* grad_y,
+                         const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
+                         float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 /* reduce_axis0 for `count` independent matrices with one launch per kernel
  * configuration (the pages' training step calls the reducer 17 times, once per

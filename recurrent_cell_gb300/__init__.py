@@ -76,6 +76,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.cfc_grn_backward.restype = i32
     lib.cfc_kloop_forward_backward_static.argtypes = [vp] * 6 + [i32] * 6 + [vp] * 3 + [vp] * 6 + [vp]
     lib.cfc_kloop_forward_backward_static.restype = i32
+    gdr_in = [vp, i64, vp, i64, vp, i64, vp, vp]
+    lib.cfc_gdr_workspace_bytes.argtypes = [i64] + [i32] * 7
+    lib.cfc_gdr_workspace_bytes.restype = sz
+    lib.cfc_gdr_forward.argtypes = (gdr_in + [vp, i32, i64] + [i32] * 4 + [ctypes.c_float, i32] + [vp] * 3
+                                    + [i32, vp, sz, vp])
+    lib.cfc_gdr_forward.restype = i32
+    lib.cfc_gdr_backward.argtypes = (gdr_in + [vp, i32, i64] + [i32] * 4 + [ctypes.c_float, i32] + [vp] * 9
+                                     + [sz, vp])
+    lib.cfc_gdr_backward.restype = i32
+    lib.cfc_gdr_step.argtypes = gdr_in + [i32] * 6 + [ctypes.c_float, i32, vp, i64, vp, vp, vp]
+    lib.cfc_gdr_step.restype = i32
+    lib.cfc_rmsnorm_forward.argtypes = [vp] * 3 + [i64, i32, ctypes.c_float, i32] + [vp] * 5 + [i32, vp]
+    lib.cfc_rmsnorm_forward.restype = i32
+    lib.cfc_rmsnorm_workspace_bytes.argtypes = [i64, i32]
+    lib.cfc_rmsnorm_workspace_bytes.restype = sz
+    lib.cfc_rmsnorm_backward.argtypes = [vp] * 5 + [i64, i32, i32] + [vp] * 3 + [sz, vp]
+    lib.cfc_rmsnorm_backward.restype = i32
     lib.cfc_kloop_grad_splits.argtypes = [i32] * 6
     lib.cfc_kloop_grad_splits.restype = i32
     lib.cfc_device_error.argtypes = [i32]
@@ -319,6 +336,150 @@ def cfc_tau_kloop_backward(x, h0, W_in, W_rec, b, tau, dt, h_seq, grad_W_in, gra
         _ptr(per_sample_scratch, "per_sample_scratch", f32, (B, N)),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("cfc_tau_kloop_backward", status)
+
+
+def cfc_gdr_workspace_bytes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math=MATH_BF16, save=False) -> int:
+    return int(load_library().cfc_gdr_workspace_bytes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math,
+                                                      1 if save else 0))
+
+
+def _rows(t, name, dtype, lead, heads, width):
+    """Pointer and row stride of t [*lead, heads, width], whose rows may be
+    parts of wider ones (dense in heads and width, evenly spaced over lead)."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != len(lead) + 2 or shape[-1] != width or shape[-2] != heads or tuple(shape[:-2]) != lead:
+        raise ValueError(f"{name} must have shape {(*lead, heads, width)}, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * width
+    strides = t.stride()
+    ld = strides[-3] if shape[-3] != 1 or len(lead) == 1 else strides[0]
+    if (strides[-1] != 1 or (heads > 1 and strides[-2] != width)
+            or (len(lead) == 2 and lead[0] > 1 and strides[0] != lead[1] * ld)):
+        raise ValueError(f"{name} must be dense in its last two axes, with evenly spaced rows")
+    return t.data_ptr(), ld
+
+
+def _gdr_inputs(q, k, v, g, beta, seq_offsets, math):
+    """Sizes and leading C arguments that the three calls share."""
+    torch = _torch()
+    st, f32 = _storage_dtype(math), torch.float32
+    if q.dim() < 2 or v.dim() < 2:
+        raise ValueError("q, k and v need a heads and a width axis")
+    hk, dk = q.shape[-2:]
+    hv, dv = v.shape[-2:]
+    lead = tuple(v.shape[:-2])
+    if len(lead) != (2 if seq_offsets is None else 1):
+        raise ValueError("v must be [sequences, tokens, heads, d_v], or [rows, heads, d_v] with seq_offsets")
+    args = [*_rows(q, "q", st, lead, hk, dk), *_rows(k, "k", st, lead, hk, dk), *_rows(v, "v", st, lead, hv, dv),
+            _ptr(g, "g", f32, (*lead, hv)), _ptr(beta, "beta", f32, (*lead, hv))]
+    return st, lead, hk, hv, dk, dv, args
+
+
+def _gdr_sequences(lead, seq_offsets):
+    if seq_offsets is None:
+        return None, lead[0], lead[0] * lead[1]
+    if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets must hold n_seq + 1 row numbers")
+    return _ptr(seq_offsets, "seq_offsets", _torch().int32), seq_offsets.numel() - 1, lead[0]
+
+
+def cfc_gdr_forward(q, k, v, g, beta, o, workspace, scale=None, seq_offsets=None, initial_state=None, final_state=None,
+                    save=False, math=MATH_BF16, stream=None):
+    """Gated delta rule over whole sequences: q, k [sequences, tokens, k_heads,
+    d_k], v and o [sequences, tokens, v_heads, d_v], g, beta [sequences, tokens,
+    v_heads]; or [rows, ...] packed, with int32 seq_offsets [sequences + 1] on
+    the device.  scale: d_k ** -0.5 if None."""
+    f32 = _torch().float32
+    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, seq_offsets, math)
+    off, n, rows = _gdr_sequences(lead, seq_offsets)
+    status = load_library().cfc_gdr_forward(
+        *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
+        _ptr(initial_state, "initial_state", f32, (n, hv, dk, dv), optional=True), _ptr(o, "o", st, (*lead, hv, dv)),
+        _ptr(final_state, "final_state", f32, (n, hv, dk, dv), optional=True), 1 if save else 0,
+        _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
+    _check("cfc_gdr_forward", status)
+
+
+def cfc_gdr_backward(q, k, v, g, beta, grad_o, grad_q, grad_k, grad_v, grad_g, grad_beta, workspace, scale=None,
+                     seq_offsets=None, grad_final_state=None, grad_initial_state=None, math=MATH_BF16, stream=None):
+    """Backward of the cfc_gdr_forward(save=True) that filled ``workspace``;
+    every gradient is overwritten, all in the type of q."""
+    f32 = _torch().float32
+    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, seq_offsets, math)
+    off, n, rows = _gdr_sequences(lead, seq_offsets)
+    status = load_library().cfc_gdr_backward(
+        *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
+        _ptr(grad_o, "grad_o", st, (*lead, hv, dv)),
+        _ptr(grad_final_state, "grad_final_state", f32, (n, hv, dk, dv), optional=True),
+        _ptr(grad_q, "grad_q", st, (*lead, hk, dk)), _ptr(grad_k, "grad_k", st, (*lead, hk, dk)),
+        _ptr(grad_v, "grad_v", st, (*lead, hv, dv)), _ptr(grad_g, "grad_g", st, (*lead, hv)),
+        _ptr(grad_beta, "grad_beta", st, (*lead, hv)),
+        _ptr(grad_initial_state, "grad_initial_state", f32, (n, hv, dk, dv), optional=True),
+        _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
+    _check("cfc_gdr_backward", status)
+
+
+def cfc_gdr_step(q, k, v, g, beta, state, o, slots=None, scale=None, math=MATH_BF16, stream=None):
+    """The next tokens of decoding sequences (shapes as for cfc_gdr_forward,
+    [sequences, tokens, ...]): sequence i's state is ``state[slots[i]]``
+    (int32 on the device; ``state[i]`` if None), updated in place."""
+    torch = _torch()
+    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, None, math)
+    n_slots = state.shape[0]
+    status = load_library().cfc_gdr_step(
+        *args, lead[0], lead[1], hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
+        _ptr(state, "state", torch.float32, (n_slots, hv, dk, dv)), n_slots,
+        _ptr(slots, "slots", torch.int32, lead[:1], optional=True), _ptr(o, "o", st, (*lead, hv, dv)),
+        _stream(stream))
+    _check("cfc_gdr_step", status)
+
+
+def cfc_rmsnorm_workspace_bytes(rows: int, d: int) -> int:
+    return int(load_library().cfc_rmsnorm_workspace_bytes(rows, d))
+
+
+def cfc_rmsnorm_forward(x, weight, y=None, residual=None, residual_out=None, rstd=None, y8=None, y8_scale=None,
+                        eps=1e-6, math=MATH_BF16, stream=None):
+    """Norm of the stream x + residual [rows, d]: y in the stored type and/or
+    y8 (float8_e4m3fn or uint8) with y8_scale [rows, groups], one scale for
+    each d / groups columns."""
+    torch = _torch()
+    st, f32 = _storage_dtype(math), torch.float32
+    rows, d = shape = tuple(x.shape)
+    group = d
+    if y8 is not None:
+        if y8.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"y8 must be torch.float8_e4m3fn or torch.uint8, got {y8.dtype}")
+        if y8_scale is None or y8_scale.dim() != 2 or y8_scale.shape[1] < 1 or d % y8_scale.shape[1]:
+            raise ValueError("y8 needs y8_scale [rows, groups], with groups a divisor of d")
+        group = d // y8_scale.shape[1]
+    status = load_library().cfc_rmsnorm_forward(
+        _ptr(x, "x", st), _ptr(residual, "residual", st, shape, optional=True), _ptr(weight, "weight", f32, (d,)),
+        rows, d, eps, math, _ptr(y, "y", st, shape, optional=True),
+        _ptr(residual_out, "residual_out", st, shape, optional=True), _ptr(rstd, "rstd", f32, (rows,), optional=True),
+        _ptr(y8, "y8", None, shape, optional=True),
+        _ptr(y8_scale, "y8_scale", f32, (rows, d // group), optional=True) if y8 is not None else None, group,
+        _stream(stream))
+    _check("cfc_rmsnorm_forward", status)
+
+
+def cfc_rmsnorm_backward(s, weight, rstd, grad_y, grad_x, grad_weight, workspace, grad_residual_out=None,
+                         math=MATH_BF16, stream=None):
+    """Backward from the stream s (the forward's residual_out, or its x) and
+    rstd: grad_x, the gradient of s, and grad_weight."""
+    torch = _torch()
+    st, f32 = _storage_dtype(math), torch.float32
+    rows, d = shape = tuple(s.shape)
+    status = load_library().cfc_rmsnorm_backward(
+        _ptr(s, "s", st), _ptr(weight, "weight", f32, (d,)), _ptr(rstd, "rstd", f32, (rows,)),
+        _ptr(grad_y, "grad_y", st, shape), _ptr(grad_residual_out, "grad_residual_out", st, shape, optional=True),
+        rows, d, math, _ptr(grad_x, "grad_x", st, shape), _ptr(grad_weight, "grad_weight", f32, (d,)),
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("cfc_rmsnorm_backward", status)
 
 
 def reduce_axis0_multi(per_batch, out, stream=None):

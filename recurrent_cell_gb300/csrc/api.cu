@@ -112,6 +112,11 @@ bool make_layout(int B, int K, int n_in, int n_hid, int math, int grad_path, Lay
   return true;
 }
 
+// Limits of the gated delta rule and the norm (32-bit block and row counts).
+constexpr long long kMaxGdrRows = 1ll << 30;
+constexpr int kMaxGdrSeqs = 1 << 20;
+constexpr int kMaxRmsWidth = 32768;
+
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -366,6 +371,167 @@ int reduce_axis0_multi(const float* const* per_batch, const int* n_batch, const 
     if (!al4(out[i]) || (per_batch[i] && !al4(per_batch[i]))) return CFC_ERR_ALIGN;
   }
   cudaError_t e = launch_reduce_multi(per_batch, n_batch, n_tail, out, count, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
+}
+
+// --- gated delta rule --------------------------------------------------------
+size_t cfc_gdr_workspace_bytes(long long rows, int n_seq, int n_k_heads, int n_v_heads, int d_k, int d_v, int math,
+                               int save) {
+  if (rows < 0 || rows > kMaxGdrRows || n_seq < 1 || n_seq > kMaxGdrSeqs ||
+      !gdr_shape_supported(n_k_heads, n_v_heads, d_k, d_v, math))
+    return 0;
+  return gdr_workspace(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math, save);
+}
+
+static int gdr_check_sizes(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, bool packed) {
+  if (math != CFC_MATH_FP32 && math != CFC_MATH_BF16) return CFC_ERR_MODE;
+  if (!gdr_shape_supported(hk, hv, dk, dv, math)) return CFC_ERR_SHAPE;
+  if (n_seq < 1 || n_seq > kMaxGdrSeqs || rows < 0 || rows > kMaxGdrRows) return CFC_ERR_SHAPE;
+  if (!packed && rows % n_seq != 0) return CFC_ERR_SHAPE;
+  // blocks of a launch: one per chunk (or 16 value columns) and head
+  if ((rows / 64 + n_seq) * hv > 0x7fffffffll || (long long)n_seq * hv * ((dv + 15) / 16) > 0x7fffffffll)
+    return CFC_ERR_SHAPE;
+  return CFC_OK;
+}
+
+// Rows at least as far apart as they are wide, whole 16-byte vectors.
+static bool gdr_stride_ok(long long ld, int width, int math) {
+  return ld >= width && ld % (math == CFC_MATH_BF16 ? 8 : 4) == 0;
+}
+
+int cfc_gdr_forward(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                    long long v_stride, const float* g, const float* beta, const int* seq_offsets, int n_seq,
+                    long long rows, int n_k_heads, int n_v_heads, int d_k, int d_v, float scale, int math,
+                    const float* initial_state, void* o, float* final_state, int save, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const int st = gdr_check_sizes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math, seq_offsets != nullptr);
+  if (st != CFC_OK) return st;
+  if (rows > 0 && (!q || !k || !v || !g || !beta || !o)) return CFC_ERR_NULL;
+  if (!gdr_stride_ok(q_stride, n_k_heads * d_k, math) || !gdr_stride_ok(k_stride, n_k_heads * d_k, math) ||
+      !gdr_stride_ok(v_stride, n_v_heads * d_v, math))
+    return CFC_ERR_SHAPE;
+  if (!workspace || workspace_bytes < gdr_workspace(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math, save != 0))
+    return CFC_ERR_WORKSPACE;
+  const void* ptrs[] = {q, k, v, initial_state, o, final_state, workspace};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return CFC_ERR_ALIGN;
+  const void* ptrs4[] = {g, beta, seq_offsets};
+  for (const void* p : ptrs4)
+    if (p && !al4(p)) return CFC_ERR_ALIGN;
+  GdrArgs a{};
+  a.q = q; a.k = k; a.v = v; a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride;
+  a.g = g; a.beta = beta; a.off = seq_offsets; a.n_seq = n_seq; a.rows = rows;
+  a.hk = n_k_heads; a.hv = n_v_heads; a.dk = d_k; a.dv = d_v; a.scale = scale; a.math = math; a.save = save != 0;
+  a.init = initial_state; a.final_state = final_state; a.o = o; a.ws = static_cast<char*>(workspace);
+  const cudaError_t e = launch_gdr_forward(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
+}
+
+int cfc_gdr_backward(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                     long long v_stride, const float* g, const float* beta, const int* seq_offsets, int n_seq,
+                     long long rows, int n_k_heads, int n_v_heads, int d_k, int d_v, float scale, int math,
+                     const void* grad_o, const float* grad_final_state, void* grad_q, void* grad_k, void* grad_v,
+                     void* grad_g, void* grad_beta, float* grad_initial_state, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const int st = gdr_check_sizes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math, seq_offsets != nullptr);
+  if (st != CFC_OK) return st;
+  if (rows > 0 && (!q || !k || !v || !g || !beta || !grad_o || !grad_q || !grad_k || !grad_v || !grad_g || !grad_beta))
+    return CFC_ERR_NULL;
+  if (!gdr_stride_ok(q_stride, n_k_heads * d_k, math) || !gdr_stride_ok(k_stride, n_k_heads * d_k, math) ||
+      !gdr_stride_ok(v_stride, n_v_heads * d_v, math))
+    return CFC_ERR_SHAPE;
+  if (!workspace || workspace_bytes < gdr_workspace(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math, 1))
+    return CFC_ERR_WORKSPACE;
+  const void* ptrs[] = {q, k, v, grad_o, grad_final_state, grad_q, grad_k, grad_v, grad_initial_state, workspace};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return CFC_ERR_ALIGN;
+  const void* ptrs4[] = {g, beta, seq_offsets, grad_g, grad_beta};
+  for (const void* p : ptrs4)
+    if (p && !al4(p)) return CFC_ERR_ALIGN;
+  GdrArgs a{};
+  a.q = q; a.k = k; a.v = v; a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride;
+  a.g = g; a.beta = beta; a.off = seq_offsets; a.n_seq = n_seq; a.rows = rows;
+  a.hk = n_k_heads; a.hv = n_v_heads; a.dk = d_k; a.dv = d_v; a.scale = scale; a.math = math; a.save = 1;
+  a.ws = static_cast<char*>(workspace);
+  GdrGrads r{grad_o, grad_final_state, grad_q, grad_k, grad_v, grad_g, grad_beta, grad_initial_state};
+  const cudaError_t e = launch_gdr_backward(a, r, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
+}
+
+int cfc_gdr_step(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                 long long v_stride, const float* g, const float* beta, int n_seq, int tokens, int n_k_heads,
+                 int n_v_heads, int d_k, int d_v, float scale, int math, float* state, long long n_slots,
+                 const int* slots, void* o, void* stream) {
+  if (math != CFC_MATH_FP32 && math != CFC_MATH_BF16) return CFC_ERR_MODE;
+  if (!gdr_shape_supported(n_k_heads, n_v_heads, d_k, d_v, math)) return CFC_ERR_SHAPE;
+  if (n_seq < 0 || tokens < 0 || n_slots < 0 || (long long)n_seq * tokens > kMaxGdrRows) return CFC_ERR_SHAPE;
+  if ((long long)n_seq * n_v_heads * ((d_v + 15) / 16) > 0x7fffffffll) return CFC_ERR_SHAPE;
+  if (!slots && n_slots < n_seq) return CFC_ERR_SHAPE;
+  if (n_seq == 0 || tokens == 0) return CFC_OK;
+  if (!q || !k || !v || !g || !beta || !o || (n_slots > 0 && !state)) return CFC_ERR_NULL;
+  if (!gdr_stride_ok(q_stride, n_k_heads * d_k, math) || !gdr_stride_ok(k_stride, n_k_heads * d_k, math) ||
+      !gdr_stride_ok(v_stride, n_v_heads * d_v, math))
+    return CFC_ERR_SHAPE;
+  const void* ptrs[] = {q, k, v, state, o};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return CFC_ERR_ALIGN;
+  const void* ptrs4[] = {g, beta, slots};
+  for (const void* p : ptrs4)
+    if (p && !al4(p)) return CFC_ERR_ALIGN;
+  GdrStepArgs a{};
+  a.q = q; a.k = k; a.v = v; a.ldq = q_stride; a.ldk = k_stride; a.ldv = v_stride;
+  a.g = g; a.beta = beta; a.state = state; a.slots = slots; a.n_slots = n_slots; a.o = o;
+  a.n_seq = n_seq; a.tokens = tokens; a.hk = n_k_heads; a.hv = n_v_heads; a.dk = d_k; a.dv = d_v;
+  a.math = math; a.scale = scale;
+  const cudaError_t e = launch_gdr_step(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
+}
+
+// --- residual RMS norm ---------------------------------------------------------
+static int rms_check(long long rows, int d, int math) {
+  if (math != CFC_MATH_FP32 && math != CFC_MATH_BF16) return CFC_ERR_MODE;
+  if (rows < 0 || rows > (1ll << 40) || d < 1 || d > kMaxRmsWidth) return CFC_ERR_SHAPE;
+  return CFC_OK;
+}
+
+size_t cfc_rmsnorm_workspace_bytes(long long rows, int d) {
+  if (rms_check(rows, d, CFC_MATH_FP32) != CFC_OK) return 0;
+  return rmsnorm_workspace(rows, d);
+}
+
+int cfc_rmsnorm_forward(const void* x, const void* residual, const float* weight, long long rows, int d, float eps,
+                        int math, void* y, void* residual_out, float* rstd, void* y8, float* y8_scale, int y8_group,
+                        void* stream) {
+  const int st = rms_check(rows, d, math);
+  if (st != CFC_OK) return st;
+  if (y8 && (y8_group < 1 || y8_group > d || d % y8_group != 0)) return CFC_ERR_SHAPE;
+  if (rows == 0) return CFC_OK;
+  if (!x || !weight || (!y && !y8) || (y8 && !y8_scale)) return CFC_ERR_NULL;
+  const void* ptrs[] = {x, residual, weight, y, residual_out, y8};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return CFC_ERR_ALIGN;
+  if ((rstd && !al4(rstd)) || (y8_scale && !al4(y8_scale))) return CFC_ERR_ALIGN;
+  const cudaError_t e =
+      launch_rmsnorm_forward(x, residual, weight, rows, d, eps, math, y, residual_out, rstd,
+                             static_cast<uint8_t*>(y8), y8_scale, y8 ? y8_group : d, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
+}
+
+int cfc_rmsnorm_backward(const void* s, const float* weight, const float* rstd, const void* grad_y,
+                         const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
+                         float* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = rms_check(rows, d, math);
+  if (st != CFC_OK) return st;
+  if (!grad_weight) return CFC_ERR_NULL;
+  if (rows > 0 && (!s || !weight || !rstd || !grad_y || !grad_x)) return CFC_ERR_NULL;
+  if (!workspace || workspace_bytes < rmsnorm_workspace(rows, d)) return CFC_ERR_WORKSPACE;
+  const void* ptrs[] = {s, weight, grad_y, grad_residual_out, grad_x, grad_weight, workspace};
+  for (const void* p : ptrs)
+    if (p && !al16(p)) return CFC_ERR_ALIGN;
+  if (rstd && !al4(rstd)) return CFC_ERR_ALIGN;
+  const cudaError_t e =
+      launch_rmsnorm_backward(s, weight, rstd, grad_y, grad_residual_out, rows, d, math, grad_x, grad_weight,
+                              static_cast<float*>(workspace), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CFC_OK : CFC_ERR_LAUNCH;
 }
 

@@ -237,6 +237,55 @@ int tc_wgrad_blocks(int n_in, int n_hid);
 // tensor-core kernels; blocks until the device is idle.
 int read_device_error(int clear);
 
+// Gated delta rule over whole sequences (cfc_gdr.cu, cfc_gdr_bwd.cu) and for
+// the next tokens (cfc_gdr_step.cu); sizes and pointers already checked.
+struct GdrArgs {
+  const void *q, *k, *v;
+  long long ldq, ldk, ldv;        // elements from one row to the next
+  const float *g, *beta;
+  const int* off;                 // n_seq + 1 row offsets, or NULL
+  int n_seq;
+  long long rows;
+  int hk, hv, dk, dv;
+  float scale;
+  int math, save;
+  const float* init;
+  float* final_state;
+  void* o;
+  char* ws;
+};
+struct GdrGrads {
+  const void* grad_o;
+  const float* grad_final;
+  void *grad_q, *grad_k, *grad_v, *grad_g, *grad_beta;
+  float* grad_init;
+};
+struct GdrStepArgs {
+  const void *q, *k, *v;
+  long long ldq, ldk, ldv;
+  const float *g, *beta;
+  float* state;
+  const int* slots;
+  long long n_slots;
+  void* o;
+  int n_seq, tokens, hk, hv, dk, dv, math;
+  float scale;
+};
+bool gdr_shape_supported(int hk, int hv, int dk, int dv, int math);
+size_t gdr_workspace(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
+cudaError_t launch_gdr_forward(const GdrArgs& g, cudaStream_t s);
+cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_t s);
+cudaError_t launch_gdr_step(const GdrStepArgs& g, cudaStream_t s);
+
+// Residual RMS norm (cfc_rmsnorm.cu).
+size_t rmsnorm_workspace(long long rows, int d);
+cudaError_t launch_rmsnorm_forward(const void* x, const void* residual, const float* w, long long rows, int d, float eps,
+                                   int math, void* y, void* residual_out, float* rstd, uint8_t* y8, float* y8_scale,
+                                   int group, cudaStream_t s);
+cudaError_t launch_rmsnorm_backward(const void* s, const float* w, const float* rstd, const void* grad_y,
+                                    const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
+                                    float* grad_w, float* part, cudaStream_t st);
+
 cudaError_t launch_wgrad_simt(const Layout& L, const CfcArgs& a, float* out, int n_split,
                               long long rows_per_split, cudaStream_t s);
 

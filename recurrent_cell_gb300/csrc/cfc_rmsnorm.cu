@@ -1,0 +1,482 @@
+// cfc_rmsnorm.cu -- root-mean-square norm of a residual stream, forward and
+// backward.
+//
+//   s = round(x + residual)        (the stream, in the stored type)
+//   n = s rstd,  rstd = 1 / sqrt(mean(s^2) + eps),  y = n w
+//   y8 = e4m3(y / c) with c = max|y| / 448 over each group of columns
+//   grad_s = grad_residual_out + rstd (dn - n mean(dn n)),  dn = grad_y w
+//   grad_w = sum over rows of grad_y n
+//
+// The stream is rounded before it is normalised: what the next layer adds to
+// and what the backward reads is then what was normalised.  Everything else is
+// fp32 and rounded once, on its way out.
+//
+// Memory is the bound in both directions (about one operation a byte), so a
+// row is read once and kept in registers: L threads a row, up to kNV 16-byte
+// vectors each, sums by shuffles (and one shared-memory exchange where a row
+// takes more than a warp).  Blocks are persistent and keep their columns'
+// weights, and in the backward their columns' grad_w, in registers.
+#include <cuda_fp8.h>
+
+#include "cfc_internal.cuh"
+
+namespace cfc {
+namespace rms {
+
+struct Args {
+  const void *x, *residual, *grad_y, *grad_s;
+  const float *w, *rstd_in;
+  void *y, *s_out, *grad_x;
+  float *rstd, *scale, *part;
+  uint8_t* y8;
+  long long rows;
+  int d, group;
+  float eps;
+};
+
+template <class E> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  using T = float4;
+  __device__ static __forceinline__ void get(float (&f)[4], const float4& v) { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+  __device__ static __forceinline__ float4 make(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+  __device__ static __forceinline__ float round(float v) { return v; }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  using T = uint4;
+  __device__ static __forceinline__ void get(float (&f)[8], const uint4& v) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ uint4 make(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ static __forceinline__ float round(float v) { return round_bf16(v); }
+};
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// c = max / 448, so that the largest value of the group becomes e4m3's largest;
+// 1 for a group of zeros, and never below the smallest normal number.
+__device__ __forceinline__ float scale_of(float most) {
+  return most > 0.f ? fmaxf(most * (1.f / 448.f), 1.17549435e-38f) : (most == 0.f ? 1.f : most);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {    // a NaN stays
+  return a != a ? a : (b != b ? b : fmaxf(a, b));
+}
+__device__ __forceinline__ uint8_t e4m3(float v) {
+  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+struct Sum { __device__ static __forceinline__ float of(float a, float b) { return a + b; } };
+struct Max { __device__ static __forceinline__ float of(float a, float b) { return max_nan(a, b); } };
+
+// Over the L threads of a row.  For L > 32 the warps' values go through
+// `part`, one of two buffers in turn, so one barrier is enough.
+template <class Op, int L>
+__device__ __forceinline__ float over_row(float v, float (*part)[32], int& turn) {
+#pragma unroll
+  for (int m = (L < 32 ? L : 32) / 2; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
+  if constexpr (L > 32) {
+    const int warp = threadIdx.x >> 5, first = warp & ~(L / 32 - 1);
+    if ((threadIdx.x & 31) == 0) part[turn][warp] = v;
+    __syncthreads();
+    v = part[turn][first];
+#pragma unroll
+    for (int i = 1; i < L / 32; ++i) v = Op::of(v, part[turn][first + i]);
+    turn ^= 1;
+  }
+  return v;
+}
+
+constexpr int kNV = 4;
+template <int L> constexpr int threads_of() { return L > 256 ? L : 256; }
+
+template <class E, int L, int NV>
+__global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm(Args a) {
+  using V = Vec<E>;
+  using T = typename V::T;
+  constexpr int N = V::N, RPB = threads_of<L>() / L;
+  __shared__ float part[2][32];
+  int turn = 0;
+  const int l = threadIdx.x % L, rg = threadIdx.x / L;
+  const int nvec = a.d / N;
+  float w[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 f = j * L + l < nvec ? __ldg(reinterpret_cast<const float4*>(a.w + (j * L + l) * N + e))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
+    }
+  const float inv_d = 1.f / (float)a.d;
+  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
+    const long long row = base + rg;
+    const bool on = row < a.rows;
+    const T* x = reinterpret_cast<const T*>(static_cast<const E*>(a.x) + row * a.d);
+    const T* r = reinterpret_cast<const T*>(static_cast<const E*>(a.residual) + row * a.d);
+    float s[NV][N];
+    float sq = 0.f;
+    T xv[NV], rv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on && j * L + l < nvec) {
+        xv[j] = __ldcs(x + j * L + l);
+        if (a.residual) rv[j] = __ldcs(r + j * L + l);
+      }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = on && j * L + l < nvec;
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[j][e] = 0.f;
+      if (in) {
+        V::get(s[j], xv[j]);
+        if (a.residual) {
+          float t[N];
+          V::get(t, rv[j]);
+#pragma unroll
+          for (int e = 0; e < N; ++e) s[j][e] = V::round(s[j][e] + t[e]);
+        }
+        if (a.s_out) reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d)[j * L + l] = V::make(s[j]);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) sq = fmaf(s[j][e], s[j][e], sq);
+    }
+    sq = over_row<Sum, L>(sq, part, turn);
+    const float rstd = 1.f / sqrtf(fmaf(sq, inv_d, a.eps));
+    if (a.rstd && on && l == 0) a.rstd[row] = rstd;
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        s[j][e] = s[j][e] * rstd * w[j][e];
+        most = max_nan(most, fabsf(s[j][e]));
+      }
+      if (a.y && on && j * L + l < nvec) reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d)[j * L + l] = V::make(s[j]);
+    }
+    if (a.y8) {
+      const int gl = a.group / N;       // threads that share a scale, unless the row does
+      if (a.group == a.d) most = over_row<Max, L>(most, part, turn);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = j * L + l;
+        float c = most;
+        if (a.group != a.d) {
+          c = 0.f;
+#pragma unroll
+          for (int e = 0; e < N; ++e) c = max_nan(c, fabsf(s[j][e]));
+          for (int m = gl / 2; m > 0; m >>= 1) c = max_nan(c, __shfl_xor_sync(0xffffffffu, c, m));
+        }
+        c = scale_of(c);
+        const float inv = 1.f / c;
+        if (on && at < nvec) {
+          if (a.group == a.d ? at == 0 : (at & (gl - 1)) == 0) a.scale[row * (a.d / a.group) + at * N / a.group] = c;
+          uint32_t u[N / 4];
+#pragma unroll
+          for (int e = 0; e < N / 4; ++e)
+            u[e] = (uint32_t)e4m3(s[j][4 * e] * inv) | (uint32_t)e4m3(s[j][4 * e + 1] * inv) << 8 |
+                   (uint32_t)e4m3(s[j][4 * e + 2] * inv) << 16 | (uint32_t)e4m3(s[j][4 * e + 3] * inv) << 24;
+          uint32_t* p = reinterpret_cast<uint32_t*>(a.y8 + row * a.d + (long long)at * N);
+          if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+          else *p = u[0];
+        }
+      }
+    }
+  }
+}
+
+template <class E, int L, int NV>
+__global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm_bwd(Args a) {
+  using V = Vec<E>;
+  using T = typename V::T;
+  constexpr int N = V::N, RPB = threads_of<L>() / L;
+  extern __shared__ float sums[];                // [RPB][d] where a block has several rows
+  __shared__ float part[2][32];
+  int turn = 0;
+  const int l = threadIdx.x % L, rg = threadIdx.x / L;
+  const int nvec = a.d / N;
+  float w[NV][N], gw[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 f = j * L + l < nvec ? __ldg(reinterpret_cast<const float4*>(a.w + (j * L + l) * N + e))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
+      gw[j][e] = gw[j][e + 1] = gw[j][e + 2] = gw[j][e + 3] = 0.f;
+    }
+  const float inv_d = 1.f / (float)a.d;
+  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
+    const long long row = base + rg;
+    const bool on = row < a.rows;
+    const long long at = row * a.d;
+    T sv[NV], gv[NV], rv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on && j * L + l < nvec) {
+        sv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.x) + at) + j * L + l);
+        gv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.grad_y) + at) + j * L + l);
+        if (a.grad_s) rv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.grad_s) + at) + j * L + l);
+      }
+    const float rstd = on ? a.rstd_in[row] : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on && j * L + l < nvec) {
+        float s[N], gy[N];
+        V::get(s, sv[j]);
+        V::get(gy, gv[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float n = s[e] * rstd;
+          gw[j][e] = fmaf(gy[e], n, gw[j][e]);
+          dot = fmaf(gy[e] * w[j][e], n, dot);
+        }
+      }
+    dot = over_row<Sum, L>(dot, part, turn) * inv_d;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on && j * L + l < nvec) {
+        float s[N], gy[N], o[N];
+        V::get(s, sv[j]);
+        V::get(gy, gv[j]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = rstd * (gy[e] * w[j][e] - s[e] * rstd * dot);
+        if (a.grad_s) {
+          float t[N];
+          V::get(t, rv[j]);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] += t[e];
+        }
+        reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at)[j * L + l] = V::make(o);
+      }
+  }
+  // The block's row of partial sums, its row groups in order.
+  float* out = a.part + (long long)blockIdx.x * a.d;
+  if constexpr (RPB == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j * L + l < nvec)
+#pragma unroll
+        for (int e = 0; e < N; ++e) out[(j * L + l) * N + e] = gw[j][e];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j * L + l < nvec)
+#pragma unroll
+        for (int e = 0; e < N; ++e) sums[rg * a.d + (j * L + l) * N + e] = gw[j][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d; i += threads_of<L>()) {
+      float v = sums[i];
+      for (int g = 1; g < RPB; ++g) v += sums[g * a.d + i];
+      out[i] = v;
+    }
+  }
+}
+
+// Rows that are no whole number of 16-byte vectors, or longer than the
+// registers hold: one block a row, element by element, each row read again
+// from cache for its second pass.
+constexpr int kAnyThreads = 256;
+
+template <class E>
+__global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
+  __shared__ float part[2][32];
+  int turn = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const E* x = static_cast<const E*>(a.x) + row * a.d;
+    const E* r = static_cast<const E*>(a.residual) + row * a.d;
+    auto stream = [&](int i) {
+      float v = load1(x + i);
+      if (a.residual) v = Vec<E>::round(v + load1(r + i));
+      return v;
+    };
+    float sq = 0.f;
+    for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
+      const float v = stream(i);
+      sq = fmaf(v, v, sq);
+    }
+    sq = over_row<Sum, kAnyThreads>(sq, part, turn);
+    const float rstd = 1.f / sqrtf(fmaf(sq, 1.f / (float)a.d, a.eps));
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
+      const float v = stream(i);
+      if (a.y) store1(static_cast<E*>(a.y) + row * a.d + i, v * rstd * a.w[i]);
+      if (a.s_out && !a.y8) store1(static_cast<E*>(a.s_out) + row * a.d + i, v);
+    }
+    if (a.y8) {
+      for (int g0 = 0; g0 < a.d; g0 += a.group) {
+        float most = 0.f;
+        for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads)
+          most = max_nan(most, fabsf(stream(i) * rstd * a.w[i]));
+        most = scale_of(over_row<Max, kAnyThreads>(most, part, turn));
+        const float inv = 1.f / most;
+        if (threadIdx.x == 0) a.scale[row * (a.d / a.group) + g0 / a.group] = most;
+        for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads) {
+          const float v = stream(i);
+          a.y8[row * a.d + i] = e4m3(v * rstd * a.w[i] * inv);
+          if (a.s_out) store1(static_cast<E*>(a.s_out) + row * a.d + i, v);
+        }
+      }
+    }
+  }
+}
+
+template <class E>
+__global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
+  extern __shared__ float gw[];                  // [d], thread i % 256 owns column i
+  __shared__ float part[2][32];
+  int turn = 0;
+  for (int i = threadIdx.x; i < a.d; i += kAnyThreads) gw[i] = 0.f;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const E* s = static_cast<const E*>(a.x) + row * a.d;
+    const E* gy = static_cast<const E*>(a.grad_y) + row * a.d;
+    const float rstd = a.rstd_in[row];
+    float dot = 0.f;
+    for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
+      const float n = load1(s + i) * rstd, g = load1(gy + i);
+      gw[i] = fmaf(g, n, gw[i]);
+      dot = fmaf(g * a.w[i], n, dot);
+    }
+    dot = over_row<Sum, kAnyThreads>(dot, part, turn) / (float)a.d;
+    for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
+      float o = rstd * (load1(gy + i) * a.w[i] - load1(s + i) * rstd * dot);
+      if (a.grad_s) o += load1(static_cast<const E*>(a.grad_s) + row * a.d + i);
+      store1(static_cast<E*>(a.grad_x) + row * a.d + i, o);
+    }
+  }
+  for (int i = threadIdx.x; i < a.d; i += kAnyThreads) a.part[(long long)blockIdx.x * a.d + i] = gw[i];
+}
+
+// Blocks of the backward: at most kMaxBlocks rows of partial sums.
+constexpr int kMaxBlocks = 4 * kNumSMs;
+
+template <class E, int L, int NV>
+static cudaError_t fwd(const Args& a, cudaStream_t st) {
+  constexpr int RPB = threads_of<L>() / L;
+  const long long need = (a.rows + RPB - 1) / RPB, most = (L > 256 ? 3 : 5) * kNumSMs;
+  TraceScope tr("k_rmsnorm", st);
+  k_rmsnorm<E, L, NV><<<(unsigned)(need < most ? need : most), threads_of<L>(), 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <class E, int L, int NV>
+static cudaError_t bwd(const Args& a, int* blocks, cudaStream_t st) {
+  constexpr int RPB = threads_of<L>() / L;
+  const long long need = (a.rows + RPB - 1) / RPB, most = (L > 256 ? 2 : 4) * kNumSMs;
+  *blocks = (int)(need < most ? need : most);
+  const size_t bytes = RPB > 1 ? (size_t)RPB * a.d * 4 : 0;
+  if (bytes > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd<E, L, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+  }
+  TraceScope tr("k_rmsnorm_bwd", st);
+  k_rmsnorm_bwd<E, L, NV><<<*blocks, threads_of<L>(), bytes, st>>>(a);
+  return cudaGetLastError();
+}
+
+// L: the fewest threads a row that leave each at most kNV vectors.
+template <class E, class F>
+static cudaError_t by_row(const Args& a, F f) {
+  const int nvec = a.d / Vec<E>::N;
+  auto nv = [&](int L) { return (nvec + L - 1) / L; };
+#define CFC_RMS_L(LV)                                                      \
+  if (nv(LV) <= kNV) {                                                     \
+    if (nv(LV) <= 1) return f.template operator()<LV, 1>();                \
+    if (nv(LV) <= 2) return f.template operator()<LV, 2>();                \
+    return f.template operator()<LV, 4>();                                 \
+  }
+  CFC_RMS_L(32)
+  CFC_RMS_L(64)
+  CFC_RMS_L(128)
+  CFC_RMS_L(256)
+  CFC_RMS_L(512)
+#undef CFC_RMS_L
+  return cudaErrorNotSupported;
+}
+
+template <class E> struct Fwd {
+  const Args& a; cudaStream_t st;
+  template <int L, int NV> cudaError_t operator()() { return fwd<E, L, NV>(a, st); }
+};
+template <class E> struct Bwd {
+  const Args& a; int* blocks; cudaStream_t st;
+  template <int L, int NV> cudaError_t operator()() { return bwd<E, L, NV>(a, blocks, st); }
+};
+
+template <class E>
+static cudaError_t forward(const Args& a, cudaStream_t st) {
+  const bool group_ok = !a.y8 || a.group == a.d || a.group == 32 || a.group == 64 || a.group == 128;
+  cudaError_t e = cudaErrorNotSupported;
+  if (a.d % 8 == 0 && group_ok) e = by_row<E>(a, Fwd<E>{a, st});
+  if (e != cudaErrorNotSupported) return e;
+  TraceScope tr("k_rmsnorm_any", st);
+  k_rmsnorm_any<E><<<(unsigned)(a.rows < 8 * kNumSMs ? a.rows : 8 * kNumSMs), kAnyThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <class E>
+static cudaError_t backward(const Args& a, float* grad_w, cudaStream_t st) {
+  int blocks = 0;
+  cudaError_t e = cudaErrorNotSupported;
+  if (a.rows == 0) e = cudaSuccess;              // grad_w = 0
+  else if (a.d % 8 == 0) e = by_row<E>(a, Bwd<E>{a, &blocks, st});
+  if (e == cudaErrorNotSupported) {
+    const size_t bytes = (size_t)a.d * 4;
+    if (bytes > 48 * 1024) {
+      e = cudaFuncSetAttribute(k_rmsnorm_bwd_any<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+      if (e != cudaSuccess) return e;
+    }
+    blocks = (int)(a.rows < kMaxBlocks ? a.rows : kMaxBlocks);
+    TraceScope tr("k_rmsnorm_bwd_any", st);
+    k_rmsnorm_bwd_any<E><<<blocks, kAnyThreads, bytes, st>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  ReduceOut o{};
+  o.nseg = 1;
+  o.ptr[0] = grad_w;
+  return launch_reduce(a.part, blocks, a.d, a.d, o, st);
+}
+
+}  // namespace rms
+
+size_t rmsnorm_workspace(long long rows, int d) {
+  const long long n = rows < rms::kMaxBlocks ? rows : rms::kMaxBlocks;
+  return ((size_t)(n > 0 ? n : 1) * d * 4 + 255) & ~size_t(255);
+}
+
+cudaError_t launch_rmsnorm_forward(const void* x, const void* residual, const float* w, long long rows, int d, float eps,
+                                   int math, void* y, void* residual_out, float* rstd, uint8_t* y8, float* y8_scale,
+                                   int group, cudaStream_t st) {
+  rms::Args a{};
+  a.x = x; a.residual = residual; a.w = w; a.rows = rows; a.d = d; a.eps = eps;
+  a.y = y; a.s_out = residual_out; a.rstd = rstd; a.y8 = y8; a.scale = y8_scale; a.group = group;
+  return math == CFC_MATH_BF16 ? rms::forward<__nv_bfloat16>(a, st) : rms::forward<float>(a, st);
+}
+
+cudaError_t launch_rmsnorm_backward(const void* s, const float* w, const float* rstd, const void* grad_y,
+                                    const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
+                                    float* grad_w, float* part, cudaStream_t st) {
+  rms::Args a{};
+  a.x = s; a.w = w; a.rstd_in = rstd; a.grad_y = grad_y; a.grad_s = grad_residual_out; a.rows = rows; a.d = d;
+  a.grad_x = grad_x; a.part = part;
+  return math == CFC_MATH_BF16 ? rms::backward<__nv_bfloat16>(a, grad_w, st) : rms::backward<float>(a, grad_w, st);
+}
+
+}  // namespace cfc

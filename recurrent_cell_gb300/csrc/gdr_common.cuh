@@ -1,0 +1,303 @@
+// gdr_common.cuh -- what the gated-delta-rule kernels share: sequence and
+// workspace indexing, asynchronous tile copies, and warp-level matrix products
+// (mma.sync fragments) in the two precision modes.
+//
+// The rule, per sequence and value head, with a state S [d_k, d_v]:
+//   S <- exp(g_t) S,  u_t = beta_t (v_t - S^T k_t),  S <- S + k_t u_t^T,
+//   o_t = scale S^T q_t.
+// Over a chunk of C = 64 tokens, with G the running sum of g inside the chunk
+// and S0 the state before it:
+//   R_i = beta_i (v_i - exp(G_i) S0^T k_i)
+//   U   = T R,  T = (I + A)^{-1},  A_ij = beta_i exp(G_i - G_j) k_i.k_j  (j < i)
+//   O_i = scale exp(G_i) S0^T q_i + sum_{j<=i} P_ij U_j,
+//         P_ij = scale exp(G_i - G_j) q_i.k_j
+//   S1  = exp(G_C) S0 + sum_i exp(G_C - G_i) k_i U_i^T.
+// T and P depend on q, k, g and beta alone, so one kernel forms them for all
+// chunks at once; only S0 -> S1 is serial.  exp is only ever taken of sums of
+// g over tokens that follow one another, never of their negatives, so nothing
+// overflows whatever the decays are.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cfc_internal.cuh"
+
+namespace cfc {
+namespace gdr {
+
+constexpr int kC = 64;          // tokens of a chunk
+constexpr int kMaxDk = 128;     // key width limit: the state's rows stay in one block's registers
+constexpr int kMaxDv = 256;
+// Per chunk and head: exp(G), exp(G_C - G), beta, G as two floats, exp(G_C).
+constexpr int kVec = 384;
+constexpr int kVecEG = 0, kVecEGL = 64, kVecBeta = 128, kVecGHi = 192, kVecGLo = 256, kVecD = 320;
+
+// Log-decays below this are a zero factor in fp32 all the same
+// (exp(-104) underflows); holding them here keeps -inf out of differences.
+constexpr float kMinG = -110.f;
+
+struct Shape {
+  const int* off;     // n_seq + 1 row offsets, or NULL: n_seq sequences of rows / n_seq rows
+  int n_seq;
+  long long rows;
+  int hk, hv, dk, dv;
+  float scale;
+};
+
+// Rows of sequence n.  Offsets are held inside [0, rows], so nothing outside
+// the tensors is touched whatever the array holds.
+__device__ __forceinline__ void seq_range(const Shape& s, int n, long long* start, int* len) {
+  if (s.off) {
+    long long a = s.off[n], b = s.off[n + 1];
+    a = a < 0 ? 0 : (a > s.rows ? s.rows : a);
+    b = b < a ? a : (b > s.rows ? s.rows : b);
+    *start = a;
+    *len = (int)(b - a);
+  } else {
+    const long long t = s.rows / s.n_seq;
+    *start = n * t;
+    *len = (int)t;
+  }
+}
+
+// Chunk slots: sequence n's chunks are slots start_n / 64 + n, ...: the slots
+// of different sequences never meet and need no prefix sum over lengths.
+__host__ __device__ __forceinline__ long long slot_base(long long start, int n) { return start / kC + n; }
+__host__ __device__ __forceinline__ long long slot_count(long long rows, int n_seq) { return rows / kC + n_seq; }
+
+// The chunk of a slot: false if the slot is none.  A sequence's slots may
+// begin before an empty neighbour's, so the search is over slot_base, which
+// rises strictly with n.
+__device__ __forceinline__ bool slot_chunk(const Shape& s, long long slot, int* n_out, long long* start, int* len,
+                                           int* c) {
+  int lo = 0, hi = s.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    long long a;
+    int l;
+    seq_range(s, mid, &a, &l);
+    if (slot_base(a, mid) <= slot) lo = mid; else hi = mid - 1;
+  }
+  seq_range(s, lo, start, len);
+  const long long d = slot - slot_base(*start, lo);
+  *n_out = lo;
+  *c = (int)d;
+  return d >= 0 && d * kC < *len;
+}
+
+// ------------------------------------------------------------ async copies
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;   // 0: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// rows x cols elements (cols x sizeof(E) a multiple of 16) from rows `stride`
+// apart into rows `ld` apart; rows past row_end and columns past col_end are
+// zeros.  col_end is a multiple of 16 bytes.
+template <class E, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void load_tile(E* dst, int ld, const E* src, long long stride, int row_end, int col_end,
+                                          int tid) {
+  constexpr int V = 16 / sizeof(E);
+  constexpr int PER = COLS / V;
+  for (int i = tid; i < ROWS * PER; i += THREADS) {
+    const int r = i / PER, c = (i % PER) * V;
+    const bool on = r < row_end && c < col_end;
+    cp16(dst + r * ld + c, on ? src + r * stride + c : src, on);
+  }
+}
+
+// Shared rows -> global rows (16-byte pieces).
+template <class E, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void store_tile(E* dst, long long stride, const E* src, int ld, int row_end, int col_end,
+                                           int tid) {
+  constexpr int V = 16 / sizeof(E);
+  constexpr int PER = COLS / V;
+  for (int i = tid; i < ROWS * PER; i += THREADS) {
+    const int r = i / PER, c = (i % PER) * V;
+    if (r < row_end && c < col_end)
+      *reinterpret_cast<uint4*>(dst + r * stride + c) = *reinterpret_cast<const uint4*>(src + r * ld + c);
+  }
+}
+
+// ------------------------------------------------------------ warp products
+// A matrix in shared memory.  In bf16 an operand made of fp32 values can be
+// held as two planes, x = hi + lo with both in bf16 (17 significant bits): the
+// products hi*hi + lo*hi + hi*lo then keep the serial state at fp32-like
+// accuracy (4e-6 relative measured), where one plane leaves 3e-3.
+template <class E>
+struct Mat {
+  E* p;
+  int ld;
+  int plane;   // elements from the hi to the lo plane
+};
+
+// Fragments of D[16 x 8] += A[16 x k] B[k x 8]: lane = 4 g + t holds rows g and
+// g + 8, columns 2t and 2t + 1 of D.  load_b* fetches two adjacent 8-column
+// tiles at once.
+struct MBf16 {
+  using E = __nv_bfloat16;
+  static constexpr int kMode = CFC_MATH_BF16;
+  static constexpr int KS = 16;       // k of one product step
+  static constexpr int PAD = 8;       // 16 bytes: rows of an 8x8 block hit different banks
+  static constexpr int STAGES = 2;
+  template <int PL> struct A { uint32_t r[PL][4]; };
+  template <int PL> struct B { uint32_t r[PL][4]; };
+
+  __device__ static __forceinline__ void ldm(uint32_t (&r)[4], const E* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
+  }
+  __device__ static __forceinline__ void ldmt(uint32_t (&r)[4], const E* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
+  }
+  // A[m][k], k contiguous
+  template <int PL>
+  __device__ static __forceinline__ void load_a(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
+    const E* p = m.p + (m0 + (lane & 15)) * m.ld + k0 + (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) ldm(a.r[i], p + i * m.plane);
+  }
+  // A[m][k] stored [k][m]
+  template <int PL>
+  __device__ static __forceinline__ void load_at(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
+    const E* p = m.p + (k0 + (lane & 7) + (lane >> 4) * 8) * m.ld + m0 + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) ldmt(a.r[i], p + i * m.plane);
+  }
+  // B[k][n] stored [n][k], n0 .. n0 + 15
+  template <int PL>
+  __device__ static __forceinline__ void load_bn(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
+    const E* p = m.p + (n0 + (lane & 7) + (lane >> 4) * 8) * m.ld + k0 + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) ldm(b.r[i], p + i * m.plane);
+  }
+  // B[k][n] stored [k][n]
+  template <int PL>
+  __device__ static __forceinline__ void load_bk(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
+    const E* p = m.p + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * m.ld + n0 + (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) ldmt(b.r[i], p + i * m.plane);
+  }
+  __device__ static __forceinline__ void mma1(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
+    if constexpr (PA == 2) mma1(d, a.r[1], b.r[0][2 * h], b.r[0][2 * h + 1]);
+    if constexpr (PB == 2) mma1(d, a.r[0], b.r[1][2 * h], b.r[1][2 * h + 1]);
+    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
+  }
+  // two adjacent values of a row
+  template <int PL>
+  __device__ static __forceinline__ void put2(const Mat<E>& m, int row, int col, float v0, float v1) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+    *reinterpret_cast<__nv_bfloat162*>(m.p + row * m.ld + col) = h;
+    if constexpr (PL == 2)
+      *reinterpret_cast<__nv_bfloat162*>(m.p + m.plane + row * m.ld + col) =
+          __floats2bfloat162_rn(v0 - __bfloat162float(h.x), v1 - __bfloat162float(h.y));
+  }
+  __device__ static __forceinline__ float2 get2(const E* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+  }
+};
+
+// FP32: operands stay fp32 in shared memory and are split in registers into
+// two TF32 values (22 significant bits); three TF32 products per step.
+struct MFp32 {
+  using E = float;
+  static constexpr int kMode = CFC_MATH_FP32;
+  static constexpr int KS = 8;
+  static constexpr int PAD = 4;
+  static constexpr int STAGES = 1;
+  template <int PL> struct A { uint32_t h[4], l[4]; };
+  template <int PL> struct B { uint32_t h[4], l[4]; };
+
+  __device__ static __forceinline__ uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+  }
+  __device__ static __forceinline__ void split(uint32_t& h, uint32_t& l, float x) {
+    h = tf32(x);
+    l = tf32(x - __uint_as_float(h));
+  }
+  template <int PL>
+  __device__ static __forceinline__ void load_a(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
+    const E* p = m.p + (m0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
+    split(a.h[0], a.l[0], p[0]);
+    split(a.h[1], a.l[1], p[8 * m.ld]);
+    split(a.h[2], a.l[2], p[4]);
+    split(a.h[3], a.l[3], p[8 * m.ld + 4]);
+  }
+  template <int PL>
+  __device__ static __forceinline__ void load_at(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
+    const E* p = m.p + (k0 + (lane & 3)) * m.ld + m0 + (lane >> 2);
+    split(a.h[0], a.l[0], p[0]);
+    split(a.h[1], a.l[1], p[8]);
+    split(a.h[2], a.l[2], p[4 * m.ld]);
+    split(a.h[3], a.l[3], p[4 * m.ld + 8]);
+  }
+  template <int PL>
+  __device__ static __forceinline__ void load_bn(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
+    const E* p = m.p + (n0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
+    split(b.h[0], b.l[0], p[0]);
+    split(b.h[1], b.l[1], p[4]);
+    split(b.h[2], b.l[2], p[8 * m.ld]);
+    split(b.h[3], b.l[3], p[8 * m.ld + 4]);
+  }
+  template <int PL>
+  __device__ static __forceinline__ void load_bk(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
+    const E* p = m.p + (k0 + (lane & 3)) * m.ld + n0 + (lane >> 2);
+    split(b.h[0], b.l[0], p[0]);
+    split(b.h[1], b.l[1], p[4 * m.ld]);
+    split(b.h[2], b.l[2], p[8]);
+    split(b.h[3], b.l[3], p[4 * m.ld + 8]);
+  }
+  __device__ static __forceinline__ void mma1(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
+    mma1(d, a.l, b.h[2 * h], b.h[2 * h + 1]);
+    mma1(d, a.h, b.l[2 * h], b.l[2 * h + 1]);
+    mma1(d, a.h, b.h[2 * h], b.h[2 * h + 1]);
+  }
+  template <int PL>
+  __device__ static __forceinline__ void put2(const Mat<E>& m, int row, int col, float v0, float v1) {
+    *reinterpret_cast<float2*>(m.p + row * m.ld + col) = make_float2(v0, v1);
+  }
+  __device__ static __forceinline__ float2 get2(const E* p) { return *reinterpret_cast<const float2*>(p); }
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ------------------------------------------------------------ workspace
+// Per (slot, value head): T (1 or 2 planes), P, the vectors; when the backward
+// is to follow also the state before the chunk (S0^T [d_v, d_k], in the
+// operand type the products read it in) and U^T [d_v, 64]; and the backward's
+// own dS1^T, dR^T, and per-value-head dq, dk where heads are shared.
+struct Workspace {
+  size_t off_t, off_p, off_vec, off_s0, off_u, off_ds, off_dr, off_dq, off_dk, total;
+  int t_planes;
+};
+Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
+
+}  // namespace gdr
+}  // namespace cfc
