@@ -136,15 +136,23 @@ def cfc_selftest_timeout(max_polls: int = 1000, stream=None) -> None:
     _check("cfc_selftest_timeout", load_library().cfc_selftest_timeout(int(max_polls), _stream(stream)))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object: the
+        # binding is most of a small call's time
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -153,14 +161,13 @@ def _ptr(t, name, dtype=None, shape=None, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -351,7 +358,7 @@ def _rows(t, name, dtype, lead, heads, width):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape = t.shape
-    if len(shape) != len(lead) + 2 or shape[-1] != width or shape[-2] != heads or tuple(shape[:-2]) != lead:
+    if shape != (*lead, heads, width):
         raise ValueError(f"{name} must have shape {(*lead, heads, width)}, got {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), heads * width
@@ -371,7 +378,7 @@ def _gdr_inputs(q, k, v, g, beta, seq_offsets, math):
         raise ValueError("q, k and v need a heads and a width axis")
     hk, dk = q.shape[-2:]
     hv, dv = v.shape[-2:]
-    lead = tuple(v.shape[:-2])
+    lead = v.shape[:-2]
     if len(lead) != (2 if seq_offsets is None else 1):
         raise ValueError("v must be [sequences, tokens, heads, d_v], or [rows, heads, d_v] with seq_offsets")
     args = [*_rows(q, "q", st, lead, hk, dk), *_rows(k, "k", st, lead, hk, dk), *_rows(v, "v", st, lead, hv, dv),
@@ -449,7 +456,7 @@ def cfc_rmsnorm_forward(x, weight, y=None, residual=None, residual_out=None, rst
     each d / groups columns."""
     torch = _torch()
     st, f32 = _storage_dtype(math), torch.float32
-    rows, d = shape = tuple(x.shape)
+    rows, d = shape = x.shape
     group = d
     if y8 is not None:
         if y8.dtype not in (torch.float8_e4m3fn, torch.uint8):
@@ -473,7 +480,7 @@ def cfc_rmsnorm_backward(s, weight, rstd, grad_y, grad_x, grad_weight, workspace
     rstd: grad_x, the gradient of s, and grad_weight."""
     torch = _torch()
     st, f32 = _storage_dtype(math), torch.float32
-    rows, d = shape = tuple(s.shape)
+    rows, d = shape = s.shape
     status = load_library().cfc_rmsnorm_backward(
         _ptr(s, "s", st), _ptr(weight, "weight", f32, (d,)), _ptr(rstd, "rstd", f32, (rows,)),
         _ptr(grad_y, "grad_y", st, shape), _ptr(grad_residual_out, "grad_residual_out", st, shape, optional=True),

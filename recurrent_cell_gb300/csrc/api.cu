@@ -157,8 +157,9 @@ int cfc_device_error(int clear) {
   const int b = read_tc_kloop_error(clear);
   const int c = read_tc_bwd_error(clear);
   const int d = read_tc_solo_error(clear);
-  if (a < 0 || b < 0 || c < 0 || d < 0) return CFC_ERR_DEVICE;
-  return (a || b || c || d) ? 1 : 0;
+  const int g = read_gdr_error(clear);
+  if (a < 0 || b < 0 || c < 0 || d < 0 || g < 0) return CFC_ERR_DEVICE;
+  return (a || b || c || d || g) ? 1 : 0;
 }
 
 int cfc_selftest_timeout(int max_polls, void* stream) {

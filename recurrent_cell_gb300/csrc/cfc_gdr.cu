@@ -10,6 +10,7 @@
 // is then a chain of latencies, and every block shortens it by itself), wide
 // tiles where the heads alone fill the GPU (then the tiles' shared operands
 // are read fewer times).
+#include <cstdlib>
 #include "gdr_common.cuh"
 
 namespace cfc {
@@ -29,28 +30,39 @@ struct FwdArgs {
   int ntile;
 };
 
+__device__ int g_gdr_error = 0;   // a bounded wait gave up
+
 // ------------------------------------------------------------------- prep
 template <class P, int DK>
 struct PrepSmem {
   using E = typename P::E;
   static constexpr int LDK = DK + P::PAD;
-  static constexpr int LDA = kC + 1;
-  E k[kC * LDK], q[kC * LDK];
-  float a[kC * LDA];      // A, then T
-  float x[32 * 33];       // A21 T11 of the last join
-  float ghi[kC], glo[kC], beta[kC];
+  static constexpr int LDA = kC + 4;      // fp32 rows of A and T
+  static constexpr int LDT = kLdt<P>;
+  static constexpr size_t kTile = sizeof(E) * kC * LDK;
+  static constexpr size_t kA = sizeof(float) * kC * LDA, kP = kTPlanes<P> * sizeof(E) * kC * LDT;
+  // k, then A and T; q, then P: the products are done when the others begin
+  static constexpr size_t kOffQ = kTile > kA ? kTile : kA;
+  static constexpr size_t kOffG = kOffQ + (kTile > kP ? kTile : kP);
+  static constexpr size_t kBytes = kOffG + 3 * kC * sizeof(float);
 };
+
 
 // T = (I + A)^{-1} of the unit lower triangular I + A: 16 x 16 diagonal blocks
 // by forward substitution (one warp each, a column a lane), then pairs of
-// blocks joined by T21 = -T22 A21 T11.  All in fp32: products of T feed the
-// state, and its entries reach far above A's when keys repeat.
+// blocks joined by T21 = -T22 A21 T11 with fp32-accurate products.  T stays in
+// fp32 until it is stored: its entries reach far above A's when keys repeat.
 template <class P, int DK, int PL>
-__global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
+__global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   using E = typename P::E;
   using S = PrepSmem<P, DK>;
-  S& sm = *reinterpret_cast<S*>(smem_raw);
+  E* ks = reinterpret_cast<E*>(smem_raw);
+  E* qs = reinterpret_cast<E*>(smem_raw + S::kOffQ);
+  float* am = reinterpret_cast<float*>(smem_raw);
+  E* ps = qs;
+  float* ghi = reinterpret_cast<float*>(smem_raw + S::kOffG);
+  float *glo = ghi + kC, *bet = glo + kC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % a.s.hv;
   const long long slot = blockIdx.x / a.s.hv;
@@ -60,10 +72,10 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
   const long long row0 = start + (long long)c * kC;
   const int rows = min(kC, len - c * kC);
   const int hq = h / (a.s.hv / a.s.hk);
-  load_tile<E, kC, DK, 128>(sm.k, S::LDK, static_cast<const E*>(a.k) + row0 * a.ldk + (long long)hq * a.s.dk, a.ldk,
-                            rows, a.s.dk, tid);
-  load_tile<E, kC, DK, 128>(sm.q, S::LDK, static_cast<const E*>(a.q) + row0 * a.ldq + (long long)hq * a.s.dk, a.ldq,
-                            rows, a.s.dk, tid);
+  load_tile<E, kC, DK, 128>(ks, S::LDK, static_cast<const E*>(a.k) + row0 * a.ldk + (long long)hq * a.s.dk, a.ldk, rows,
+                            a.s.dk, tid);
+  load_tile<E, kC, DK, 128>(qs, S::LDK, static_cast<const E*>(a.q) + row0 * a.ldq + (long long)hq * a.s.dk, a.ldq, rows,
+                            a.s.dk, tid);
   cp_commit();
   const long long id = slot * a.s.hv + h;
   float* vec = a.vec + id * kVec;
@@ -74,9 +86,9 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 2 * lane + i;
-      x[i] = r < rows ? (double)fmaxf(a.g[(row0 + r) * a.s.hv + h], kMinG) : 0.0;
-      // fmaxf drops a NaN: put it back
-      if (r < rows && isnan(a.g[(row0 + r) * a.s.hv + h])) x[i] = (double)a.g[(row0 + r) * a.s.hv + h];
+      const float v = r < rows ? a.g[(row0 + r) * a.s.hv + h] : 0.f;
+      x[i] = v < kMinG ? kMinG : v;          // a NaN stays
+      bet[r] = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
     }
     double run = x[0] + x[1];
 #pragma unroll
@@ -90,13 +102,11 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
     for (int i = 0; i < 2; ++i) {
       const int r = 2 * lane + i;
       const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
-      const float b = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
-      sm.ghi[r] = hi;
-      sm.glo[r] = lo;
-      sm.beta[r] = b;
+      ghi[r] = hi;
+      glo[r] = lo;
       vec[kVecEG + r] = expf((float)G[i]);
       vec[kVecEGL + r] = expf((float)(total - G[i]));
-      vec[kVecBeta + r] = b;
+      vec[kVecBeta + r] = bet[r];
       vec[kVecGHi + r] = hi;
       vec[kVecGLo + r] = lo;
     }
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
   __syncthreads();
 
   // Rows 16 warp .. of q k^T and k k^T, columns up to the diagonal block.
-  const Mat<E> mk{sm.k, S::LDK, 0}, mq{sm.q, S::LDK, 0};
+  const Mat<E> mk{ks, S::LDK, 0}, mq{qs, S::LDK, 0};
   const int m0 = warp * 16, g = lane >> 2, t2 = (lane & 3) * 2;
   float aq[8][4] = {}, ak[8][4] = {};
   for (int k0 = 0; k0 < DK; k0 += P::KS) {
@@ -125,30 +135,34 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
       }
     }
   }
-  E* pout = reinterpret_cast<E*>(a.p) + id * (kC * kC);
+  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int rr = 0; rr < 2; ++rr) {
+    const int i = m0 + g + rr * 8;
+    const float hi = ghi[i], lo = glo[i], be = bet[i];
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-      const int i = m0 + g + rr * 8;
-      float pv[2];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        const int col = j * 8 + t2 + cc;
-        float l = 0.f;
-        if (col <= i) l = expf((sm.ghi[i] - sm.ghi[col]) + (sm.glo[i] - sm.glo[col]));
-        pv[cc] = col <= i ? a.s.scale * l * aq[j][rr * 2 + cc] : 0.f;
-        sm.a[i * S::LDA + col] = col < i ? sm.beta[i] * l * ak[j][rr * 2 + cc] : 0.f;
-      }
-      P::template put2<1>(Mat<E>{pout, kC, 0}, i, j * 8 + t2, pv[0], pv[1]);
+    for (int j = 0; j < 8; ++j) {
+      const int col = j * 8 + t2;
+      const float2 h2 = *reinterpret_cast<const float2*>(ghi + col), l2 = *reinterpret_cast<const float2*>(glo + col);
+      const float l0 = col <= i ? expf((hi - h2.x) + (lo - l2.x)) : 0.f;
+      const float l1 = col < i ? expf((hi - h2.y) + (lo - l2.y)) : 0.f;
+      P::template put2<PL>(Mat<E>{ps, S::LDT, kC * S::LDT}, i, col, col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f,
+                          col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f);
+      *reinterpret_cast<float2*>(am + i * S::LDA + col) =
+          make_float2(col < i ? be * l0 * ak[j][rr * 2] : 0.f, col + 1 < i ? be * l1 * ak[j][rr * 2 + 1] : 0.f);
     }
   }
   __syncthreads();
-
+  {
+    E* out = reinterpret_cast<E*>(a.p) + id * (kTPlanes<P> * kC * S::LDT);
+    constexpr int V = 16 / sizeof(E);
+    for (int i = tid; i < PL * kC * S::LDT / V; i += 128)
+      reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(ps)[i];
+  }
   // Diagonal blocks.
   if (lane < 16) {
     float x[16];
-    const float* blk = sm.a + (m0)*S::LDA + m0;
+    const float* blk = am + m0 * S::LDA + m0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float v = i == lane ? 1.f : 0.f;
@@ -157,302 +171,381 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
       x[i] = v;
     }
     __syncwarp(0xffffu);
-    for (int i = 0; i < 16; ++i) sm.a[(m0 + i) * S::LDA + m0 + lane] = x[i];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) am[(m0 + i) * S::LDA + m0 + lane] = x[i];
   }
   __syncthreads();
-  // 16 -> 32: warps 0, 1 the first pair, 2, 3 the second; y = A21 T11, then -T22 y.
-  {
-    const int b0 = (warp >> 1) * 32, half = tid & 63;
-    const int r = half >> 2, c4 = (half & 3) * 4;
-    float y[4] = {};
-    for (int m = 0; m < 16; ++m) {
-      const float av = sm.a[(b0 + 16 + r) * S::LDA + b0 + m];
+  const int r0 = g, r1 = g + 8;
+  // 16 -> 32: warps 0 and 1, a pair each; y = A21 T11, then -T22 y.
+  if (warp < 2) {
+    float* t21 = am + (warp * 32 + 16) * S::LDA + warp * 32;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = fmaf(av, sm.a[(b0 + m) * S::LDA + b0 + c4 + e], y[e]);
+    for (int pass = 0; pass < 2; ++pass) {
+      float d[2][4] = {};
+      const float* fa = pass == 0 ? t21 : t21 + 16;
+      const float* fb = pass == 0 ? t21 - 16 * S::LDA : t21;
+      const Mat<float> ma{const_cast<float*>(fa), S::LDA, 0}, mb{const_cast<float*>(fb), S::LDA, 0};
+#pragma unroll
+      for (int k0 = 0; k0 < 16; k0 += 8) {
+        MFp32::A<1> xa;
+        MFp32::B<1> xb;
+        MFp32::load_a(xa, ma, 0, k0, lane);
+        MFp32::load_bk(xb, mb, 0, k0, lane);
+        MFp32::mma(d[0], xa, xb, 0);
+        MFp32::mma(d[1], xa, xb, 1);
+      }
+      __syncwarp();
+      const float sg = pass == 0 ? 1.f : -1.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<float2*>(t21 + r0 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
+        *reinterpret_cast<float2*>(t21 + r1 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+      }
+      __syncwarp();
     }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sm.a[(b0 + 16 + r) * S::LDA + b0 + c4 + e] = y[e];
-    __syncthreads();
-    float z[4] = {};
-    for (int m = 0; m < 16; ++m) {
-      const float tv = sm.a[(b0 + 16 + r) * S::LDA + b0 + 16 + m];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] = fmaf(-tv, sm.a[(b0 + 16 + m) * S::LDA + b0 + c4 + e], z[e]);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sm.a[(b0 + 16 + r) * S::LDA + b0 + c4 + e] = z[e];
-    __syncthreads();
   }
-  // 32 -> 64
+  __syncthreads();
+  // 32 -> 64: warp w the rows 16 (w & 1) and the columns 16 (w >> 1) of each product.
   {
-    const int r = tid >> 2, c8 = (tid & 3) * 8;
-    float y[8] = {};
-    for (int m = 0; m < 32; ++m) {
-      const float av = sm.a[(32 + r) * S::LDA + m];
+    float* t21 = am + 32 * S::LDA + (warp >> 1) * 16;
+    float* mine = t21 + (warp & 1) * 16 * S::LDA;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(av, sm.a[m * S::LDA + c8 + e], y[e]);
+    for (int pass = 0; pass < 2; ++pass) {
+      float d[2][4] = {};
+      const float* fa = am + (32 + (warp & 1) * 16) * S::LDA + (pass == 0 ? 0 : 32);
+      const float* fb = pass == 0 ? am + (warp >> 1) * 16 : t21;
+      const Mat<float> ma{const_cast<float*>(fa), S::LDA, 0}, mb{const_cast<float*>(fb), S::LDA, 0};
+#pragma unroll
+      for (int k0 = 0; k0 < 32; k0 += 8) {
+        MFp32::A<1> xa;
+        MFp32::B<1> xb;
+        MFp32::load_a(xa, ma, 0, k0, lane);
+        MFp32::load_bk(xb, mb, 0, k0, lane);
+        MFp32::mma(d[0], xa, xb, 0);
+        MFp32::mma(d[1], xa, xb, 1);
+      }
+      __syncthreads();
+      const float sg = pass == 0 ? 1.f : -1.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<float2*>(mine + r0 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
+        *reinterpret_cast<float2*>(mine + r1 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+      }
+      __syncthreads();
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sm.x[r * 33 + c8 + e] = y[e];
-    __syncthreads();
-    float z[8] = {};
-    for (int m = 0; m < 32; ++m) {
-      const float tv = sm.a[(32 + r) * S::LDA + 32 + m];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = fmaf(-tv, sm.x[m * 33 + c8 + e], z[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sm.a[(32 + r) * S::LDA + c8 + e] = z[e];
-    __syncthreads();
   }
-  E* tout = reinterpret_cast<E*>(a.t) + id * (2 * kC * kC);
-  const Mat<E> mt{tout, kC, kC * kC};
-  for (int i = tid; i < kC * kC / 2; i += 128) {
-    const int r = i / (kC / 2), col = (i % (kC / 2)) * 2;
-    P::template put2<PL>(mt, r, col, sm.a[r * S::LDA + col], sm.a[r * S::LDA + col + 1]);
+  E* tout = reinterpret_cast<E*>(a.t) + id * (kTPlanes<P> * kC * S::LDT);
+  const Mat<E> mt{tout, S::LDT, kC * S::LDT};
+  for (int i = tid; i < kC * kC / 4; i += 128) {
+    const int r = i / (kC / 4), col = (i % (kC / 4)) * 4;
+    float4 v = *reinterpret_cast<const float4*>(am + r * S::LDA + col);
+    if (r == col) v.x = 0.f;            // T - I: the products add R itself in fp32
+    if (r == col + 1) v.y = 0.f;
+    if (r == col + 2) v.z = 0.f;
+    if (r == col + 3) v.w = 0.f;
+    P::template put4<PL>(mt, r, col, v);
   }
 }
 
 // ------------------------------------------------------------------- scan
-// WM x 4 warps: warp (wm, wn) holds 16 MT value columns (rows of S^T) by a
-// quarter of the key width, and forms a quarter of the tokens of R, U and O.
-// Operands that all four need pass through shared memory: three barriers a
-// chunk.  PL = 2: the operands of the serial chain in two planes.
-template <class P, int DK, int MT, int WM, int PL>
+// Chain warps: (wm, wn) holds 16 MT value columns (rows of S^T) by a quarter
+// of the key width, and forms a quarter of the tokens of R and U.  Operands
+// that all four quarters need pass through shared memory.  SPLIT: as many
+// warps again form the outputs beside the chain (what few heads need: the
+// chain's length is the time); else the chain's warps form them too.  Two more
+// warps fetch the next chunk.  PL = 2: the operands of the
+// serial chain in two planes.
+template <class P, int DK, int MT, int WM, int PL, bool SPLIT>
 struct ScanCfg {
   using E = typename P::E;
-  static constexpr int DVT = 16 * MT * WM, THREADS = 128 * WM;
-  static constexpr int LDK = DK + P::PAD, LDT = kC + P::PAD, LDV = DVT + P::PAD;
+  static constexpr int DVT = 16 * MT * WM, CHAIN = 128 * WM, WORK = SPLIT ? 2 * CHAIN : CHAIN, FETCH = 64,
+                       THREADS = WORK + FETCH;
+  static constexpr int LDK = DK + P::PAD, LDT = kLdt<P>, LDV = DVT + P::PAD;
   static constexpr int NTS = DK / 32;                 // 8-column tiles of S^T a warp
   static constexpr int ST = P::STAGES;
   static constexpr int kQ = kC * LDK;                 // elements of each staged operand
-  static constexpr int kT = PL * kC * LDT, kP = kC * LDT, kV = kC * LDV;
-  static constexpr int STAGE = 2 * kQ + kT + kP + kV;
-  static constexpr int SOP = PL * DVT * LDK, ROP = PL * DVT * LDT, UOP = DVT * LDT;
+  static constexpr int kT = PL * kC * LDT, kP = kT, kV = kC * LDV;
+  static constexpr int STAGE = 2 * kQ + kT + kP + kV + kVec * (int)(4 / sizeof(E));
+  static constexpr int SOP = PL * DVT * LDK, ROP = PL * DVT * LDT, UOP = ROP;
   // U and its decayed copy lie over the state operand, which is free by then
-  static constexpr bool ALIAS = (size_t)(ST * STAGE + SOP + 2 * ROP + UOP + kV) * sizeof(E) + 2 * kVec * 4 > 227u * 1024u;
+  static constexpr bool ALIAS = (size_t)(ST * STAGE + SOP + 2 * ROP + UOP + kV) * sizeof(E) + 64 > 227u * 1024u;
   static constexpr int ELEMS = ST * STAGE + (ALIAS ? (SOP > UOP + ROP ? SOP : UOP + ROP) : SOP + UOP + ROP) + ROP + kV;
-  static constexpr size_t BYTES = (size_t)ELEMS * sizeof(E) + (size_t)ST * kVec * 4;
+  static constexpr size_t BYTES = (size_t)ELEMS * sizeof(E) + 64;
   static constexpr bool FITS = BYTES <= 227u * 1024u;
 };
 
-template <class P, int DK, int MT, int WM, int PL>
-__global__ void __launch_bounds__(128 * WM) k_gdr_scan(FwdArgs a) {
+template <class P, int DK, int MT, int WM, int PL, bool SPLIT>
+__global__ void __launch_bounds__(ScanCfg<P, DK, MT, WM, PL, SPLIT>::THREADS) k_gdr_scan(FwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  using C = ScanCfg<P, DK, MT, WM, PL>;
+  using C = ScanCfg<P, DK, MT, WM, PL, SPLIT>;
   using E = typename P::E;
   constexpr int NTS = C::NTS, ST = C::ST;
-  float* vecs = reinterpret_cast<float*>(smem_raw);
-  E* stage = reinterpret_cast<E*>(vecs + ST * kVec);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw);
+  uint64_t* empty = full + 2;
+  E* stage = reinterpret_cast<E*>(smem_raw + 64);
   E* sop_p = stage + ST * C::STAGE;
   E* uop_p = C::ALIAS ? sop_p : sop_p + C::SOP;
   E* ukop_p = uop_p + C::UOP;
   E* rop_p = sop_p + (C::ELEMS - ST * C::STAGE - C::ROP - C::kV);
   E* ost = rop_p + C::ROP;
-  const Mat<E> sop{sop_p, C::LDK, C::DVT * C::LDK}, rop{rop_p, C::LDT, C::DVT * C::LDT}, uop{uop_p, C::LDT, 0},
+  const Mat<E> sop{sop_p, C::LDK, C::DVT * C::LDK}, rop{rop_p, C::LDT, C::DVT * C::LDT}, uop{uop_p, C::LDT, C::DVT * C::LDT},
       ukop{ukop_p, C::LDT, C::DVT * C::LDT};
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wn = warp & 3, wm = warp >> 2;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % a.ntile;
   const long long sh = blockIdx.x / a.ntile;
   const int h = (int)(sh % a.s.hv), n = (int)(sh / a.s.hv);
   const int hq = h / (a.s.hv / a.s.hk);
   const int dk = a.s.dk, dv = a.s.dv, dv0 = tile * C::DVT, dvn = min(C::DVT, dv - dv0);
-  const int m0 = wm * 16 * MT;
   long long start;
   int len;
   seq_range(a.s, n, &start, &len);
   const int nc = (len + kC - 1) / kC;
   const long long slot0 = slot_base(start, n);
-  const E* q = static_cast<const E*>(a.q) + start * a.ldq + (long long)hq * dk;
-  const E* k = static_cast<const E*>(a.k) + start * a.ldk + (long long)hq * dk;
-  const E* v = static_cast<const E*>(a.v) + start * a.ldv + (long long)h * dv + dv0;
-  E* o = static_cast<E*>(a.o) + (start * a.s.hv + h) * dv + dv0;
-  const long long ldo = (long long)a.s.hv * dv;
 
-  auto fetch = [&](int c, int st) {
-    E* b = stage + st * C::STAGE;
-    const int rows = min(kC, len - c * kC);
-    const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
-    load_tile<E, kC, DK, C::THREADS>(b, C::LDK, k + r0 * a.ldk, a.ldk, rows, dk, tid);
-    load_tile<E, kC, DK, C::THREADS>(b + C::kQ, C::LDK, q + r0 * a.ldq, a.ldq, rows, dk, tid);
-    load_tile<E, kC, C::DVT, C::THREADS>(b + 2 * C::kQ, C::LDV, v + r0 * a.ldv, a.ldv, rows, dvn, tid);
-    const E* tp = reinterpret_cast<const E*>(a.t) + id * (2 * kC * kC);
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ + C::kV + i * kC * C::LDT, C::LDT, tp + i * kC * kC, kC, kC, kC,
-                                       tid);
-    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ + C::kV + C::kT, C::LDT,
-                                     reinterpret_cast<const E*>(a.p) + id * (kC * kC), kC, kC, kC, tid);
-    for (int i = tid; i < kVec / 4; i += C::THREADS) cp16(vecs + st * kVec + i * 4, a.vec + id * kVec + i * 4, true);
-    cp_commit();
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(full + i, C::FETCH + 1);
+      tc::mbar_init(empty + i, C::WORK / 32);
+    }
+    tc::mbar_init_fence();
+  }
+  __syncthreads();
+
+  bool lost = false;        // a wait gave up: no more waiting, the results are void
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!lost && !tc::mbar_wait(bar, parity, kPolls)) {
+      lost = true;
+      atomicExch(&g_gdr_error, 1);
+    }
   };
 
-  float s[MT][NTS][4];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
-        s[mt][nt][e] = a.init && r < dvn && col < dk ? a.init[(sh * dk + col) * dv + dv0 + r] : 0.f;
+  if (tid >= C::WORK) {     // ---- the fetching warps
+    const int ft = tid - C::WORK;
+    const E* q = static_cast<const E*>(a.q) + start * a.ldq + (long long)hq * dk;
+    const E* k = static_cast<const E*>(a.k) + start * a.ldk + (long long)hq * dk;
+    const E* v = static_cast<const E*>(a.v) + start * a.ldv + (long long)h * dv + dv0;
+    constexpr uint32_t tb = C::kT * sizeof(E), pb = C::kP * sizeof(E);
+    for (int c = 0; c < nc; ++c) {
+      const int st = ST == 2 ? (c & 1) : 0;
+      if (c >= ST) wait(empty + st, (c / ST - 1) & 1);
+      E* b = stage + st * C::STAGE;
+      const int rows = min(kC, len - c * kC);
+      const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
+      if (ft == 0) {
+        E* x = b + 2 * C::kQ + C::kV;
+        bar_arrive_tx(full + st, tb + pb + kVec * 4);
+        bulk_load(x, reinterpret_cast<const E*>(a.t) + id * (kTPlanes<P> * kC * C::LDT), tb, full + st);
+        bulk_load(x + C::kT, reinterpret_cast<const E*>(a.p) + id * (kTPlanes<P> * kC * C::LDT), pb, full + st);
+        bulk_load(x + C::kT + C::kP, a.vec + id * kVec, kVec * 4, full + st);
       }
+      load_tile<E, kC, DK, C::FETCH>(b, C::LDK, k + r0 * a.ldk, a.ldk, rows, dk, ft);
+      load_tile<E, kC, DK, C::FETCH>(b + C::kQ, C::LDK, q + r0 * a.ldq, a.ldq, rows, dk, ft);
+      load_tile<E, kC, C::DVT, C::FETCH>(b + 2 * C::kQ, C::LDV, v + r0 * a.ldv, a.ldv, rows, dvn, ft);
+      bar_arrive_cp(full + st);
+    }
+    return;
+  }
 
-  if (nc > 0) fetch(0, 0);
-  for (int c = 0; c < nc; ++c) {
-    const int st = ST == 2 ? (c & 1) : 0;
-    E* b = stage + st * C::STAGE;
-    const Mat<E> mk{b, C::LDK, 0}, mq{b + C::kQ, C::LDK, 0}, mt_{b + 2 * C::kQ + C::kV, C::LDT, kC * C::LDT},
-        mp{b + 2 * C::kQ + C::kV + C::kT, C::LDT, 0};
-    const E* vs = b + 2 * C::kQ;
-    const float* vec = vecs + st * kVec;
-    const int rows = min(kC, len - c * kC);
-    cp_wait<0>();
+  const bool chain = tid < C::CHAIN, outs = !SPLIT || !chain;
+  const int wn = warp & 3, wm = (warp >> 2) % WM, m0 = wm * 16 * MT, otid = SPLIT ? tid - C::CHAIN : tid;
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  E* o = static_cast<E*>(a.o) + (start * a.s.hv + h) * dv + dv0;
+  const long long ldo = (long long)a.s.hv * dv;
+  float s[MT][NTS][4];
+  if (chain)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NTS; ++nt)
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr)
-          P::template put2<PL>(sop, m0 + mt * 16 + g + rr * 8, wn * (DK / 4) + nt * 8 + t2, s[mt][nt][2 * rr],
-                               s[mt][nt][2 * rr + 1]);
-    __syncthreads();
-    if (ST == 2 && c + 1 < nc) fetch(c + 1, (c + 1) & 1);
-    if (c > 0)
-      store_tile<E, kC, C::DVT, C::THREADS>(o + (long long)(c - 1) * kC * ldo, ldo, ost, C::LDV, kC, dvn, tid);
-    if (a.save)
-      store_tile<E, C::DVT, DK, C::THREADS>(
-          reinterpret_cast<E*>(a.s0) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * dk, dk, sop_p, C::LDK, dvn, dk, tid);
+        for (int e = 0; e < 4; ++e) {
+          const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
+          s[mt][nt][e] = a.init && r < dvn && col < dk ? a.init[(sh * dk + col) * dv + dv0 + r] : 0.f;
+        }
+
+  for (int c = 0; c < nc; ++c) {
+    const int st = ST == 2 ? (c & 1) : 0;
+    E* b = stage + st * C::STAGE;
+    E* x = b + 2 * C::kQ + C::kV;
+    const Mat<E> mk{b, C::LDK, 0}, mq{b + C::kQ, C::LDK, 0}, mt_{x, C::LDT, kC * C::LDT}, mp{x + C::kT, C::LDT, kC * C::LDT};
+    const E* vs = b + 2 * C::kQ;
+    const float* vec = reinterpret_cast<const float*>(x + C::kT + C::kP);
+    if (chain)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr)
+            P::template put2<PL>(sop, m0 + mt * 16 + g + rr * 8, wn * (DK / 4) + nt * 8 + t2, s[mt][nt][2 * rr],
+                                 s[mt][nt][2 * rr + 1]);
+    wait(full + st, (c / ST) & 1);
+    group_sync<1, C::WORK>();
+    if (!SPLIT && c > 0)
+      store_tile<E, kC, C::DVT, C::CHAIN>(o + (long long)(c - 1) * kC * ldo, ldo, ost, C::LDV, kC, dvn, otid);
+    if (outs && a.save)
+      store_tile<E, C::DVT, DK, C::CHAIN>(
+          reinterpret_cast<E*>(a.s0) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * dk, dk, sop_p, C::LDK, dvn, dk, otid);
 
     // S0^T k and S0^T q of this warp's 16 tokens
-    float ar[MT][2][4] = {}, ao[MT][2][4] = {};
+    float ar[MT][2][4] = {}, al[MT][2][4] = {}, ao[MT][2][4] = {};
 #pragma unroll
     for (int k0 = 0; k0 < DK; k0 += P::KS) {
       typename P::template B<1> bk, bq;
-      P::load_bn(bk, mk, wn * 16, k0, lane);
-      P::load_bn(bq, mq, wn * 16, k0, lane);
+      if (chain) P::load_bn(bk, mk, wn * 16, k0, lane);
+      if (outs) P::load_bn(bq, mq, wn * 16, k0, lane);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         typename P::template A<PL> fa;
         P::load_a(fa, sop, m0 + mt * 16, k0, lane);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          P::mma(ar[mt][hf], fa, bk, hf);
+          if (chain) P::mma(ar[mt][hf], al[mt][hf], fa, bk, hf);
           // the outputs leave in the stored type: one plane of the state is enough
-          if constexpr (PL == 2) P::mma1(ao[mt][hf], fa.r[0], bq.r[0][2 * hf], bq.r[0][2 * hf + 1]);
-          else P::mma(ao[mt][hf], fa, bq, hf);
+          if (outs) P::mma_hi(ao[mt][hf], fa, bq, hf);
         }
       }
     }
+    const int i0 = wn * 16 + t2;
+    float au[MT][2][4];
+    if (chain) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int i = wn * 16 + hf * 8 + t2;
-      const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
-      const float2 be = *reinterpret_cast<const float2*>(vec + kVecBeta + i);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = m0 + mt * 16 + g + rr * 8;
-          const float v0 = to_f(vs[i * C::LDV + r]), v1 = to_f(vs[(i + 1) * C::LDV + r]);
-          P::template put2<PL>(rop, r, i, be.x * (v0 - eg.x * ar[mt][hf][2 * rr]),
-                               be.y * (v1 - eg.y * ar[mt][hf][2 * rr + 1]));
-          ao[mt][hf][2 * rr] *= a.s.scale * eg.x;
-          ao[mt][hf][2 * rr + 1] *= a.s.scale * eg.y;
-        }
-    }
-    __syncthreads();
-    // U = T R
-    float au[MT][2][4] = {};
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      if (k0 >= wn * 16 + 16) break;
-      typename P::template B<PL> bt;
-      P::load_bn(bt, mt_, wn * 16, k0, lane);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        typename P::template A<PL> fa;
-        P::load_a(fa, rop, m0 + mt * 16, k0, lane);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) P::mma(au[mt][hf], fa, bt, hf);
-      }
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int i = wn * 16 + hf * 8 + t2;
-      const float2 el = *reinterpret_cast<const float2*>(vec + kVecEGL + i);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = m0 + mt * 16 + g + rr * 8;
-          const float u0 = au[mt][hf][2 * rr], u1 = au[mt][hf][2 * rr + 1];
-          P::template put2<1>(uop, r, i, u0, u1);
-          P::template put2<PL>(ukop, r, i, el.x * u0, el.y * u1);
-        }
-    }
-    __syncthreads();
-    if (a.save)
-      store_tile<E, C::DVT, kC, C::THREADS>(
-          reinterpret_cast<E*>(a.u) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * kC, kC, uop_p, C::LDT, dvn, kC, tid);
-    // O += P U
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      if (k0 >= wn * 16 + 16) break;
-      typename P::template B<1> bp;
-      P::load_bn(bp, mp, wn * 16, k0, lane);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        typename P::template A<1> fa;
-        P::load_a(fa, uop, m0 + mt * 16, k0, lane);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) P::mma(ao[mt][hf], fa, bp, hf);
-      }
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          put(ost + (wn * 16 + hf * 8 + t2 + (e & 1)) * C::LDV + m0 + mt * 16 + g + (e >> 1) * 8, ao[mt][hf][e]);
-    // S1 = exp(G_C) S0 + sum_i exp(G_C - G_i) U_i k_i^T
-    const float d = vec[kVecD];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= d;
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      typename P::template A<PL> fa[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) P::load_a(fa[mt], ukop, m0 + mt * 16, k0, lane);
-#pragma unroll
-      for (int j = 0; j < NTS / 2; ++j) {
-        typename P::template B<1> bk;
-        P::load_bk(bk, mk, wn * (DK / 4) + j * 16, k0, lane);
+      for (int hf = 0; hf < 2; ++hf) {
+        const int i = i0 + hf * 8;
+        const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
+        const float2 be = *reinterpret_cast<const float2*>(vec + kVecBeta + i);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) P::mma(s[mt][2 * j + hf], fa[mt], bk, hf);
+          for (int rr = 0; rr < 2; ++rr) {
+            const int r = m0 + mt * 16 + g + rr * 8;
+            const float v0 = to_f(vs[i * C::LDV + r]), v1 = to_f(vs[(i + 1) * C::LDV + r]);
+            float s0 = ar[mt][hf][2 * rr], s1 = ar[mt][hf][2 * rr + 1];
+            if constexpr (P::two_sums(PL, 1)) { s0 += al[mt][hf][2 * rr]; s1 += al[mt][hf][2 * rr + 1]; }
+            // U = R + (T - I) R: R itself stays fp32
+            au[mt][hf][2 * rr] = be.x * (v0 - eg.x * s0);
+            au[mt][hf][2 * rr + 1] = be.y * (v1 - eg.y * s1);
+            P::template put2<PL>(rop, r, i, au[mt][hf][2 * rr], au[mt][hf][2 * rr + 1]);
+          }
       }
     }
-    if (ST == 1 || C::ALIAS) __syncthreads();
-    if (ST == 1 && c + 1 < nc) fetch(c + 1, 0);
-    (void)rows;
+    if (outs)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i0 + hf * 8);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            ao[mt][hf][2 * rr] *= a.s.scale * eg.x;
+            ao[mt][hf][2 * rr + 1] *= a.s.scale * eg.y;
+          }
+      }
+    if (chain) {
+      group_sync<2, C::CHAIN>();
+      float aw[MT][2][4] = {};
+#pragma unroll
+      for (int k0 = 0; k0 < kC; k0 += P::KS) {
+        if (k0 >= wn * 16 + 16) break;
+        typename P::template B<PL> bt;
+        P::load_bn(bt, mt_, wn * 16, k0, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          typename P::template A<PL> fa;
+          P::load_a(fa, rop, m0 + mt * 16, k0, lane);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) P::mma(au[mt][hf], aw[mt][hf], fa, bt, hf);
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int i = i0 + hf * 8;
+        const float2 el = *reinterpret_cast<const float2*>(vec + kVecEGL + i);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            const int r = m0 + mt * 16 + g + rr * 8;
+            float u0 = au[mt][hf][2 * rr], u1 = au[mt][hf][2 * rr + 1];
+            if constexpr (P::two_sums(PL, PL)) { u0 += aw[mt][hf][2 * rr]; u1 += aw[mt][hf][2 * rr + 1]; }
+            P::template put2<PL>(uop, r, i, u0, u1);
+            P::template put2<PL>(ukop, r, i, el.x * u0, el.y * u1);
+          }
+      }
+    }
+    group_sync<1, C::WORK>();
+    if (outs && a.save)
+      store_tile<E, C::DVT, kC, C::CHAIN>(
+          reinterpret_cast<E*>(a.u) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * kC, kC, uop_p, C::LDT, dvn, kC, otid);
+    if (outs) {
+      // O += P U
+#pragma unroll
+      for (int k0 = 0; k0 < kC; k0 += P::KS) {
+        if (k0 >= wn * 16 + 16) break;
+        typename P::template B<PL> bp;
+        P::load_bn(bp, mp, wn * 16, k0, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          typename P::template A<PL> fa;
+          P::load_a(fa, uop, m0 + mt * 16, k0, lane);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) P::mma(ao[mt][hf], fa, bp, hf);
+        }
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            put(ost + (i0 + hf * 8 + (e & 1)) * C::LDV + m0 + mt * 16 + g + (e >> 1) * 8, ao[mt][hf][e]);
+    }
+    if (chain) {
+      // S1 = exp(G_C) S0 + sum_i exp(G_C - G_i) U_i k_i^T
+      const float d = vec[kVecD];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] *= d;
+#pragma unroll
+      for (int k0 = 0; k0 < kC; k0 += P::KS) {
+        typename P::template A<PL> fa[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) P::load_a(fa[mt], ukop, m0 + mt * 16, k0, lane);
+#pragma unroll
+        for (int j = 0; j < NTS / 2; ++j) {
+          typename P::template B<1> bk;
+          P::load_bk(bk, mk, wn * (DK / 4) + j * 16, k0, lane);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) P::mma(s[mt][2 * j + hf], fa[mt], bk, hf);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(empty + st);
+    if (SPLIT) {
+      if (!chain) {
+        group_sync<3, C::CHAIN>();
+        store_tile<E, kC, C::DVT, C::CHAIN>(o + (long long)c * kC * ldo, ldo, ost, C::LDV, len - c * kC, dvn, otid);
+        group_sync<3, C::CHAIN>();     // ost is written again in the next chunk
+      }
+    } else if (C::ALIAS) {
+      group_sync<1, C::WORK>();
+    }
   }
-  if (nc > 0) {
-    __syncthreads();
-    store_tile<E, kC, C::DVT, C::THREADS>(o + (long long)(nc - 1) * kC * ldo, ldo, ost, C::LDV, len - (nc - 1) * kC, dvn,
-                                          tid);
+  if (lost)                  // copies that may still be on their way
+    for (int i = 0; i < ST; ++i) tc::mbar_wait(full + i, 0, kPolls);
+  if (!SPLIT && nc > 0) {
+    group_sync<1, C::WORK>();
+    store_tile<E, kC, C::DVT, C::CHAIN>(o + (long long)(nc - 1) * kC * ldo, ldo, ost, C::LDV, len - (nc - 1) * kC, dvn,
+                                        otid);
   }
-  if (a.final_state) {
+  if (chain && a.final_state) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -468,7 +561,7 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan(FwdArgs a) {
 template <class P, int DK, int PL>
 static cudaError_t launch_prep(const FwdArgs& a, cudaStream_t st) {
   const long long blocks = slot_count(a.s.rows, a.s.n_seq) * a.s.hv;
-  const size_t bytes = sizeof(PrepSmem<P, DK>);
+  const size_t bytes = PrepSmem<P, DK>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(k_gdr_prep<P, DK, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_prep", st);
@@ -476,17 +569,18 @@ static cudaError_t launch_prep(const FwdArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <class P, int DK, int MT, int WM, int PL>
+template <class P, int DK, int MT, int WM, int PL, bool SPLIT>
 static cudaError_t launch_scan(FwdArgs a, cudaStream_t st) {
-  using C = ScanCfg<P, DK, MT, WM, PL>;
+  using C = ScanCfg<P, DK, MT, WM, PL, SPLIT>;
   static_assert(C::FITS, "shared memory");
+  static_assert(!(SPLIT && C::ALIAS), "the output warps still read the state when U is written");
   a.ntile = (a.s.dv + C::DVT - 1) / C::DVT;
   const long long blocks = (long long)a.s.n_seq * a.s.hv * a.ntile;
-  cudaError_t e =
-      cudaFuncSetAttribute(k_gdr_scan<P, DK, MT, WM, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan<P, DK, MT, WM, PL, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan", st);
-  k_gdr_scan<P, DK, MT, WM, PL><<<(unsigned)blocks, C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan<P, DK, MT, WM, PL, SPLIT><<<(unsigned)blocks, C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -501,11 +595,14 @@ static cudaError_t forward(const FwdArgs& a, cudaStream_t st) {
   auto blocks = [&](int w) { return heads * ((a.s.dv + w - 1) / w); };
   if constexpr (P::kMode == CFC_MATH_BF16) {
     if constexpr (PL == 1)
-      if (a.s.dv > 64 && blocks(128) >= 114) return launch_scan<P, DK, 2, 4, PL>(a, st);
-    if (a.s.dv > 32 && blocks(64) >= 114) return launch_scan<P, DK, 2, 2, PL>(a, st);
+      if (a.s.dv > 64 && blocks(128) >= 114) {
+        if (getenv("GDR_X")) return launch_scan<P, DK, 4, 2, PL, false>(a, st);
+        return launch_scan<P, DK, 2, 4, PL, false>(a, st);
+      }
+    if (a.s.dv > 32 && blocks(64) >= 114) return launch_scan<P, DK, 2, 2, PL, false>(a, st);
   }
-  if (a.s.dv > 16 && blocks(32) >= 114) return launch_scan<P, DK, 1, 2, PL>(a, st);
-  return launch_scan<P, DK, 1, 1, PL>(a, st);
+  if (a.s.dv > 16 && blocks(32) >= 114) return launch_scan<P, DK, 1, 2, PL, true>(a, st);
+  return launch_scan<P, DK, 1, 1, PL, true>(a, st);
 }
 
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -516,8 +613,10 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
   const size_t slots = (size_t)slot_count(rows, n_seq) * hv;
   size_t off = 0;
   auto take = [&](size_t* at, size_t bytes) { *at = off; off = up256(off + bytes); };
-  take(&w.off_t, slots * 2 * kC * kC * e);
-  take(&w.off_p, slots * kC * kC * e);
+  const bool bf = math == CFC_MATH_BF16;
+  const size_t row = bf ? kLdt<MBf16> : kLdt<MFp32>;
+  take(&w.off_t, slots * (bf ? kTPlanes<MBf16> : kTPlanes<MFp32>) * kC * row * e);
+  take(&w.off_p, slots * (bf ? kTPlanes<MBf16> : kTPlanes<MFp32>) * kC * row * e);
   take(&w.off_vec, slots * kVec * 4);
   if (save) {
     take(&w.off_s0, slots * dk * dv * e);
@@ -534,6 +633,16 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
 }
 
 }  // namespace gdr
+
+int read_gdr_error(int clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, gdr::g_gdr_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
+  if (clear && v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(gdr::g_gdr_error, &zero, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
+  }
+  return v;
+}
 
 bool gdr_shape_supported(int hk, int hv, int dk, int dv, int math) {
   return hk >= 1 && hv >= hk && hv % hk == 0 && hv <= 4096 && dk >= 8 && dk <= gdr::kMaxDk && dk % 8 == 0 && dv >= 8 &&

@@ -104,10 +104,11 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
     const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
     load_tile<E, kC, DK, C::THREADS>(b, C::LDK, k + r0 * a.ldk, a.ldk, rows, dk, tid);
     load_tile<E, kC, DK, C::THREADS>(b + C::kQ, C::LDK, q + r0 * a.ldq, a.ldq, rows, dk, tid);
-    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ, C::LDT, reinterpret_cast<const E*>(a.t) + id * (2 * kC * kC), kC,
-                                     kC, kC, tid);
-    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ + C::kT, C::LDT, reinterpret_cast<const E*>(a.p) + id * (kC * kC),
-                                     kC, kC, kC, tid);
+    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ, C::LDT,
+                                     reinterpret_cast<const E*>(a.t) + id * (kTPlanes<P> * kC * C::LDT), C::LDT, kC, kC,
+                                     tid);
+    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ + C::kT, C::LDT, reinterpret_cast<const E*>(a.p) + id * (kTPlanes<P> * kC * C::LDT),
+                                     C::LDT, kC, kC, tid);
     load_tile<E, kC, C::DVT, C::THREADS>(b + 2 * C::kQ + 2 * C::kT, C::LDV, go + r0 * ldo, ldo, rows, dvn, tid);
     for (int i = tid; i < kVec / 4; i += C::THREADS) cp16(vecs + st * kVec + i * 4, a.vec + id * kVec + i * 4, true);
     cp_commit();
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
     store_tile<E, C::DVT, DK, C::THREADS>(reinterpret_cast<E*>(a.ds) + (id * dv + dv0) * dk, dk, sop_p, C::LDK, dvn, dk,
                                           tid);
     // dU of this warp's 16 tokens
-    float ak[MT][2][4] = {}, ap[MT][2][4] = {};
+    float ak[MT][2][4] = {}, ap[MT][2][4] = {}, ar[MT][2][4];
 #pragma unroll
     for (int k0 = 0; k0 < DK; k0 += P::KS) {
       typename P::template B<1> bk;
@@ -182,16 +183,16 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
           const int r = m0 + mt * 16 + g + rr * 8;
-          P::template put2<1>(uop, r, i, el.x * ak[mt][hf][2 * rr] + ap[mt][hf][2 * rr],
-                              el.y * ak[mt][hf][2 * rr + 1] + ap[mt][hf][2 * rr + 1]);
+          // dR = dU + (T - I)^T dU: dU itself stays fp32
+          ar[mt][hf][2 * rr] = el.x * ak[mt][hf][2 * rr] + ap[mt][hf][2 * rr];
+          ar[mt][hf][2 * rr + 1] = el.y * ak[mt][hf][2 * rr + 1] + ap[mt][hf][2 * rr + 1];
+          P::template put2<1>(uop, r, i, ar[mt][hf][2 * rr], ar[mt][hf][2 * rr + 1]);
           P::template put2<1>(dop, r, i, a.s.scale * eg.x * to_f(mo.p[i * C::LDV + r]),
                               a.s.scale * eg.y * to_f(mo.p[(i + 1) * C::LDV + r]));
         }
     }
     __syncthreads();
-    // dR = T^T dU
     E* gst = mo.p;
-    float ar[MT][2][4] = {};
 #pragma unroll
     for (int k0 = 0; k0 < kC; k0 += P::KS) {
       if (k0 + P::KS <= wn * 16) continue;
@@ -282,7 +283,8 @@ struct GradSmem {
   E go[ST][kC * LDV], v[ST][kC * LDV];
   E u[ST][DVS * LDT], dr[ST][DVS * LDT];
   E s0[ST][DVS * LDK], ds[ST][DVS * LDK];
-  E dp[kC * LDT], da[kC * LDT], dm[kC * LDT];
+  static constexpr int PL = kTPlanes<P>;
+  E dp[PL * kC * LDT], da[PL * kC * LDT], dm[PL * kC * LDT];    // 17 bits in bf16: dg is a difference of large sums
   float vec[kVec];
   float dot[4][2][kC];    // q.dq, k.dk, k.E, k.dS1 U by half of the key width
   float drv[4][kC];
@@ -409,9 +411,9 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
         da[cc] = col + cc < i ? -l * aa[j][2 * rr + cc] : 0.f;
       }
       const float be = vec[kVecBeta + i];
-      P::template put2<1>(Mat<E>{sm.dp, S::LDT, 0}, i, col, dp[0], dp[1]);
-      P::template put2<1>(Mat<E>{sm.da, S::LDT, 0}, i, col, da[0], da[1]);
-      P::template put2<1>(Mat<E>{sm.dm, S::LDT, 0}, i, col, be * da[0], be * da[1]);
+      P::template put2<S::PL>(Mat<E>{sm.dp, S::LDT, kC * S::LDT}, i, col, dp[0], dp[1]);
+      P::template put2<S::PL>(Mat<E>{sm.da, S::LDT, kC * S::LDT}, i, col, da[0], da[1]);
+      P::template put2<S::PL>(Mat<E>{sm.dm, S::LDT, kC * S::LDT}, i, col, be * da[0], be * da[1]);
     }
   float dus[2] = {0.f, 0.f};
 #pragma unroll
@@ -432,12 +434,12 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
   }
   __syncthreads();
   {
-    const Mat<E> mk{sm.k, S::LDK, 0}, mq{sm.q, S::LDK, 0}, mp{sm.dp, S::LDT, 0}, ma{sm.da, S::LDT, 0},
-        mm{sm.dm, S::LDT, 0};
+    const Mat<E> mk{sm.k, S::LDK, 0}, mq{sm.q, S::LDK, 0}, mp{sm.dp, S::LDT, kC * S::LDT},
+        ma{sm.da, S::LDT, kC * S::LDT}, mm{sm.dm, S::LDT, kC * S::LDT};
 #pragma unroll
     for (int k0 = 0; k0 < kC; k0 += P::KS) {
       if (k0 < wr * 16 + 16) {
-        typename P::template A<1> fp, fa;
+        typename P::template A<S::PL> fp, fa;
         P::load_a(fp, mp, wr * 16, k0, lane);
         P::load_a(fa, ma, wr * 16, k0, lane);
 #pragma unroll
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
         }
       }
       if (k0 + P::KS > wr * 16) {
-        typename P::template A<1> fp, fm;
+        typename P::template A<S::PL> fp, fm;
         P::load_at(fp, mp, wr * 16, k0, lane);
         P::load_at(fm, mm, wr * 16, k0, lane);
 #pragma unroll

@@ -30,7 +30,7 @@ constexpr int kStepThreads = 256;
 
 // RPT rows of the state a thread: rows rg, rg + RG, ... of RG row groups.
 template <class E, int TDV, int RPT>
-__global__ void __launch_bounds__(kStepThreads) k_gdr_step(StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
   constexpr int AC = TDV / 4;                   // threads across the columns
   constexpr int RG = kStepThreads / AC;
   constexpr int WARPS = kStepThreads / 32;
@@ -158,10 +158,10 @@ cudaError_t launch_gdr_step(const GdrStepArgs& g, cudaStream_t st) {
              g.tokens, g.hk, g.hv, g.dk, g.dv, 0, g.scale};
   // Few heads: narrow tiles, so that every SM takes part; many: whole rows.
   const long long heads = (long long)g.n_seq * g.hv;
-  const bool wide = heads * ((g.dv + 127) / 128) >= 2 * kNumSMs && g.dv > 64;
+  const bool wide = g.dv > 32 && heads * ((g.dv + 63) / 64) >= 4 * kNumSMs;
   if (g.math == CFC_MATH_BF16)
-    return wide ? launch<__nv_bfloat16, 128>(a, g.n_seq, st) : launch<__nv_bfloat16, 32>(a, g.n_seq, st);
-  return wide ? launch<float, 128>(a, g.n_seq, st) : launch<float, 32>(a, g.n_seq, st);
+    return wide ? launch<__nv_bfloat16, 64>(a, g.n_seq, st) : launch<__nv_bfloat16, 32>(a, g.n_seq, st);
+  return wide ? launch<float, 64>(a, g.n_seq, st) : launch<float, 32>(a, g.n_seq, st);
 }
 
 }  // namespace cfc

@@ -271,6 +271,7 @@ struct GdrStepArgs {
   int n_seq, tokens, hk, hv, dk, dv, math;
   float scale;
 };
+int read_gdr_error(int clear);
 bool gdr_shape_supported(int hk, int hv, int dk, int dv, int math);
 size_t gdr_workspace(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 cudaError_t launch_gdr_forward(const GdrArgs& g, cudaStream_t s);

@@ -12,10 +12,11 @@
 // fp32 and rounded once, on its way out.
 //
 // Memory is the bound in both directions (about one operation a byte), so a
-// row is read once and kept in registers: L threads a row, up to kNV 16-byte
-// vectors each, sums by shuffles (and one shared-memory exchange where a row
-// takes more than a warp).  Blocks are persistent and keep their columns'
-// weights, and in the backward their columns' grad_w, in registers.
+// row is read once and kept in registers: a warp a row up to 2 vectors of 16
+// bytes a lane, a block a row beyond that, of as many warps as leave each
+// thread 2 (long rows: 4) vectors.  Blocks are persistent: they keep their
+// columns' weights, and in the backward their columns' grad_w, in registers,
+// and load the next row before they finish the present one.
 #include <cuda_fp8.h>
 
 #include "cfc_internal.cuh"
@@ -76,75 +77,100 @@ __device__ __forceinline__ float scale_of(float most) {
   return most > 0.f ? fmaxf(most * (1.f / 448.f), 1.17549435e-38f) : (most == 0.f ? 1.f : most);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {    // a NaN stays
-  return a != a ? a : (b != b ? b : fmaxf(a, b));
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 __device__ __forceinline__ uint8_t e4m3(float v) {
   return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 struct Sum { __device__ static __forceinline__ float of(float a, float b) { return a + b; } };
 struct Max { __device__ static __forceinline__ float of(float a, float b) { return max_nan(a, b); } };
 
-// Over the L threads of a row.  For L > 32 the warps' values go through
-// `part`, one of two buffers in turn, so one barrier is enough.
-template <class Op, int L>
+// Over a row: a warp's shuffles and, where the row is a block's, its warps'
+// values through `part`, two buffers in turn, so one barrier is enough.
+template <class Op, bool WARP>
 __device__ __forceinline__ float over_row(float v, float (*part)[32], int& turn) {
 #pragma unroll
-  for (int m = (L < 32 ? L : 32) / 2; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
-  if constexpr (L > 32) {
-    const int warp = threadIdx.x >> 5, first = warp & ~(L / 32 - 1);
-    if ((threadIdx.x & 31) == 0) part[turn][warp] = v;
+  for (int m = 16; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
+  if constexpr (!WARP) {
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = v;
     __syncthreads();
-    v = part[turn][first];
-#pragma unroll
-    for (int i = 1; i < L / 32; ++i) v = Op::of(v, part[turn][first + i]);
+    v = part[turn][0];
+    const int warps = blockDim.x >> 5;
+    for (int i = 1; i < warps; ++i) v = Op::of(v, part[turn][i]);
     turn ^= 1;
   }
   return v;
 }
 
-constexpr int kNV = 4;
-template <int L> constexpr int threads_of() { return L > 256 ? L : 256; }
+constexpr int kWarpRows = 8;      // rows of a block whose rows are warps
 
-template <class E, int L, int NV>
-__global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm(Args a) {
+// A thread's vectors of a row: j * L + l, L the threads of the row.
+template <class E, int NV, bool WARP>
+struct Row {
   using V = Vec<E>;
   using T = typename V::T;
-  constexpr int N = V::N, RPB = threads_of<L>() / L;
-  __shared__ float part[2][32];
-  int turn = 0;
-  const int l = threadIdx.x % L, rg = threadIdx.x / L;
-  const int nvec = a.d / N;
-  float w[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 f = j * L + l < nvec ? __ldg(reinterpret_cast<const float4*>(a.w + (j * L + l) * N + e))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-      w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
-    }
-  const float inv_d = 1.f / (float)a.d;
-  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
-    const long long row = base + rg;
-    const bool on = row < a.rows;
-    const T* x = reinterpret_cast<const T*>(static_cast<const E*>(a.x) + row * a.d);
-    const T* r = reinterpret_cast<const T*>(static_cast<const E*>(a.residual) + row * a.d);
-    float s[NV][N];
-    float sq = 0.f;
-    T xv[NV], rv[NV];
+  static constexpr int N = V::N;
+  int l, L, nvec;
+  __device__ __forceinline__ Row(int d) {
+    L = WARP ? 32 : blockDim.x;
+    l = WARP ? threadIdx.x & 31 : threadIdx.x;
+    nvec = d / N;
+  }
+  __device__ __forceinline__ int at(int j) const { return j * L + l; }
+  __device__ __forceinline__ bool in(int j) const { return at(j) < nvec; }
+  __device__ __forceinline__ void load(T (&v)[NV], const void* p, long long row, long long rows, int d) const {
+    const T* q = reinterpret_cast<const T*>(static_cast<const E*>(p) + row * d);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (on && j * L + l < nvec) {
-        xv[j] = __ldcs(x + j * L + l);
-        if (a.residual) rv[j] = __ldcs(r + j * L + l);
+      if (row < rows && in(j)) v[j] = __ldcs(q + at(j));
+  }
+  __device__ __forceinline__ void weights(float (&w)[NV][N], const float* p) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < N; e += 4) {
+        const float4 f = in(j) ? __ldg(reinterpret_cast<const float4*>(p + at(j) * N + e))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
       }
+  }
+};
+
+// Threads of a block at most: what leaves each the registers it needs.
+template <int NV, bool WARP, bool BWD>
+constexpr int most_threads() { return WARP ? 32 * kWarpRows : (NV > 2 && BWD ? 384 : 512); }
+
+template <class E, int NV, bool WARP>
+__global__ void __launch_bounds__(most_threads<NV, WARP, false>()) k_rmsnorm(Args a) {
+  using R = Row<E, NV, WARP>;
+  using V = typename R::V;
+  using T = typename R::T;
+  constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
+  __shared__ float part[2][32];
+  int turn = 0;
+  const R r(a.d);
+  float w[NV][N];
+  r.weights(w, a.w);
+  const float inv_d = 1.f / (float)a.d;
+  const long long step = (long long)gridDim.x * RPB;
+  long long row = (long long)blockIdx.x * RPB + (WARP ? threadIdx.x >> 5 : 0);
+  T xv[NV], rv[NV];
+  r.load(xv, a.x, row, a.rows, a.d);
+  if (a.residual) r.load(rv, a.residual, row, a.rows, a.d);
+  for (; row < a.rows; row += step) {
+    float s[NV][N];
+    float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = on && j * L + l < nvec;
 #pragma unroll
       for (int e = 0; e < N; ++e) s[j][e] = 0.f;
-      if (in) {
+      if (r.in(j)) {
         V::get(s[j], xv[j]);
         if (a.residual) {
           float t[N];
@@ -152,14 +178,16 @@ __global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm(Args a) {
 #pragma unroll
           for (int e = 0; e < N; ++e) s[j][e] = V::round(s[j][e] + t[e]);
         }
-        if (a.s_out) reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d)[j * L + l] = V::make(s[j]);
+        if (a.s_out) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d) + r.at(j), V::make(s[j]));
       }
 #pragma unroll
       for (int e = 0; e < N; ++e) sq = fmaf(s[j][e], s[j][e], sq);
     }
-    sq = over_row<Sum, L>(sq, part, turn);
+    r.load(xv, a.x, row + step, a.rows, a.d);
+    if (a.residual) r.load(rv, a.residual, row + step, a.rows, a.d);
+    sq = over_row<Sum, WARP>(sq, part, turn);
     const float rstd = 1.f / sqrtf(fmaf(sq, inv_d, a.eps));
-    if (a.rstd && on && l == 0) a.rstd[row] = rstd;
+    if (a.rstd && r.l == 0) a.rstd[row] = rstd;
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -168,14 +196,14 @@ __global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm(Args a) {
         s[j][e] = s[j][e] * rstd * w[j][e];
         most = max_nan(most, fabsf(s[j][e]));
       }
-      if (a.y && on && j * L + l < nvec) reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d)[j * L + l] = V::make(s[j]);
+      if (a.y && r.in(j)) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), V::make(s[j]));
     }
     if (a.y8) {
       const int gl = a.group / N;       // threads that share a scale, unless the row does
-      if (a.group == a.d) most = over_row<Max, L>(most, part, turn);
+      if (a.group == a.d) most = over_row<Max, WARP>(most, part, turn);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int at = j * L + l;
+        const int at = r.at(j);
         float c = most;
         if (a.group != a.d) {
           c = 0.f;
@@ -185,106 +213,99 @@ __global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm(Args a) {
         }
         c = scale_of(c);
         const float inv = 1.f / c;
-        if (on && at < nvec) {
+        if (r.in(j)) {
           if (a.group == a.d ? at == 0 : (at & (gl - 1)) == 0) a.scale[row * (a.d / a.group) + at * N / a.group] = c;
           uint32_t u[N / 4];
 #pragma unroll
           for (int e = 0; e < N / 4; ++e)
-            u[e] = (uint32_t)e4m3(s[j][4 * e] * inv) | (uint32_t)e4m3(s[j][4 * e + 1] * inv) << 8 |
-                   (uint32_t)e4m3(s[j][4 * e + 2] * inv) << 16 | (uint32_t)e4m3(s[j][4 * e + 3] * inv) << 24;
+            u[e] = e4m3x2(s[j][4 * e] * inv, s[j][4 * e + 1] * inv) |
+                   e4m3x2(s[j][4 * e + 2] * inv, s[j][4 * e + 3] * inv) << 16;
           uint32_t* p = reinterpret_cast<uint32_t*>(a.y8 + row * a.d + (long long)at * N);
-          if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-          else *p = u[0];
+          if constexpr (N == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(u[0], u[1]));
+          else __stcs(p, u[0]);
         }
       }
     }
   }
 }
 
-template <class E, int L, int NV>
-__global__ void __launch_bounds__(threads_of<L>()) k_rmsnorm_bwd(Args a) {
-  using V = Vec<E>;
-  using T = typename V::T;
-  constexpr int N = V::N, RPB = threads_of<L>() / L;
+template <class E, int NV, bool WARP>
+__global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(Args a) {
+  using R = Row<E, NV, WARP>;
+  using V = typename R::V;
+  using T = typename R::T;
+  constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
   extern __shared__ float sums[];                // [RPB][d] where a block has several rows
   __shared__ float part[2][32];
   int turn = 0;
-  const int l = threadIdx.x % L, rg = threadIdx.x / L;
-  const int nvec = a.d / N;
-  float w[NV][N], gw[NV][N];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 f = j * L + l < nvec ? __ldg(reinterpret_cast<const float4*>(a.w + (j * L + l) * N + e))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-      w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
-      gw[j][e] = gw[j][e + 1] = gw[j][e + 2] = gw[j][e + 3] = 0.f;
-    }
+  const R r(a.d);
+  float w[NV][N], gw[NV][N] = {};
+  r.weights(w, a.w);
   const float inv_d = 1.f / (float)a.d;
-  for (long long base = (long long)blockIdx.x * RPB; base < a.rows; base += (long long)gridDim.x * RPB) {
-    const long long row = base + rg;
-    const bool on = row < a.rows;
+  const long long step = (long long)gridDim.x * RPB;
+  long long row = (long long)blockIdx.x * RPB + (WARP ? threadIdx.x >> 5 : 0);
+  T sv[NV], gv[NV], rv[NV];
+  float rstd = 0.f;
+  auto fetch = [&](long long row) {
+    r.load(sv, a.x, row, a.rows, a.d);
+    r.load(gv, a.grad_y, row, a.rows, a.d);
+    if (a.grad_s) r.load(rv, a.grad_s, row, a.rows, a.d);
+    if (row < a.rows) rstd = a.rstd_in[row];
+  };
+  fetch(row);
+  for (; row < a.rows; row += step) {
     const long long at = row * a.d;
-    T sv[NV], gv[NV], rv[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (on && j * L + l < nvec) {
-        sv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.x) + at) + j * L + l);
-        gv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.grad_y) + at) + j * L + l);
-        if (a.grad_s) rv[j] = __ldcs(reinterpret_cast<const T*>(static_cast<const E*>(a.grad_s) + at) + j * L + l);
-      }
-    const float rstd = on ? a.rstd_in[row] : 0.f;
+    // n = s rstd and dn = grad_y w of the row
+    float n[NV][N], dn[NV][N];
+    T cv[NV];
+    const float rs = rstd;
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (on && j * L + l < nvec) {
-        float s[N], gy[N];
-        V::get(s, sv[j]);
-        V::get(gy, gv[j]);
+      if (r.in(j)) {
+        V::get(n[j], sv[j]);
+        V::get(dn[j], gv[j]);
+        cv[j] = rv[j];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float n = s[e] * rstd;
-          gw[j][e] = fmaf(gy[e], n, gw[j][e]);
-          dot = fmaf(gy[e] * w[j][e], n, dot);
+          n[j][e] *= rs;
+          gw[j][e] = fmaf(dn[j][e], n[j][e], gw[j][e]);
+          dn[j][e] *= w[j][e];
+          dot = fmaf(dn[j][e], n[j][e], dot);
         }
       }
-    dot = over_row<Sum, L>(dot, part, turn) * inv_d;
+    fetch(row + step);
+    dot = over_row<Sum, WARP>(dot, part, turn) * inv_d;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (on && j * L + l < nvec) {
-        float s[N], gy[N], o[N];
-        V::get(s, sv[j]);
-        V::get(gy, gv[j]);
+      if (r.in(j)) {
+        float o[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = rstd * (gy[e] * w[j][e] - s[e] * rstd * dot);
+        for (int e = 0; e < N; ++e) o[e] = rs * (dn[j][e] - n[j][e] * dot);
         if (a.grad_s) {
           float t[N];
-          V::get(t, rv[j]);
+          V::get(t, cv[j]);
 #pragma unroll
           for (int e = 0; e < N; ++e) o[e] += t[e];
         }
-        reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at)[j * L + l] = V::make(o);
+        __stcs(reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at) + r.at(j), V::make(o));
       }
   }
-  // The block's row of partial sums, its row groups in order.
+  // The block's row of partial sums, its rows' warps in order.
   float* out = a.part + (long long)blockIdx.x * a.d;
-  if constexpr (RPB == 1) {
+  float* to = WARP ? sums + (threadIdx.x >> 5) * a.d : out;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (j * L + l < nvec)
+  for (int j = 0; j < NV; ++j)
+    if (r.in(j))
 #pragma unroll
-        for (int e = 0; e < N; ++e) out[(j * L + l) * N + e] = gw[j][e];
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (j * L + l < nvec)
-#pragma unroll
-        for (int e = 0; e < N; ++e) sums[rg * a.d + (j * L + l) * N + e] = gw[j][e];
+      for (int e = 0; e < N; e += 4)
+        *reinterpret_cast<float4*>(to + r.at(j) * N + e) =
+            make_float4(gw[j][e], gw[j][e + 1], gw[j][e + 2], gw[j][e + 3]);
+  if constexpr (WARP) {
     __syncthreads();
-    for (int i = threadIdx.x; i < a.d; i += threads_of<L>()) {
+    for (int i = threadIdx.x; i < a.d; i += 32 * kWarpRows) {
       float v = sums[i];
-      for (int g = 1; g < RPB; ++g) v += sums[g * a.d + i];
+      for (int g = 1; g < kWarpRows; ++g) v += sums[g * a.d + i];
       out[i] = v;
     }
   }
@@ -312,7 +333,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
       const float v = stream(i);
       sq = fmaf(v, v, sq);
     }
-    sq = over_row<Sum, kAnyThreads>(sq, part, turn);
+    sq = over_row<Sum, false>(sq, part, turn);
     const float rstd = 1.f / sqrtf(fmaf(sq, 1.f / (float)a.d, a.eps));
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
@@ -325,7 +346,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
         float most = 0.f;
         for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads)
           most = max_nan(most, fabsf(stream(i) * rstd * a.w[i]));
-        most = scale_of(over_row<Max, kAnyThreads>(most, part, turn));
+        most = scale_of(over_row<Max, false>(most, part, turn));
         const float inv = 1.f / most;
         if (threadIdx.x == 0) a.scale[row * (a.d / a.group) + g0 / a.group] = most;
         for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads) {
@@ -354,7 +375,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
       gw[i] = fmaf(g, n, gw[i]);
       dot = fmaf(g * a.w[i], n, dot);
     }
-    dot = over_row<Sum, kAnyThreads>(dot, part, turn) / (float)a.d;
+    dot = over_row<Sum, false>(dot, part, turn) / (float)a.d;
     for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
       float o = rstd * (load1(gy + i) * a.w[i] - load1(s + i) * rstd * dot);
       if (a.grad_s) o += load1(static_cast<const E*>(a.grad_s) + row * a.d + i);
@@ -367,63 +388,58 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
 // Blocks of the backward: at most kMaxBlocks rows of partial sums.
 constexpr int kMaxBlocks = 4 * kNumSMs;
 
-template <class E, int L, int NV>
-static cudaError_t fwd(const Args& a, cudaStream_t st) {
-  constexpr int RPB = threads_of<L>() / L;
-  const long long need = (a.rows + RPB - 1) / RPB, most = (L > 256 ? 3 : 5) * kNumSMs;
+// Blocks that the SMs hold at once, `regs` registers a thread.
+static int resident(int threads, int regs) {
+  const int n = 65536 / (threads * regs), m = 2048 / threads;
+  return (n < m ? n : m) > 0 ? (n < m ? n : m) : 1;
+}
+
+template <class E, int NV, bool WARP>
+static cudaError_t fwd(const Args& a, int threads, cudaStream_t st) {
+  constexpr int RPB = WARP ? kWarpRows : 1;
+  const long long need = (a.rows + RPB - 1) / RPB, most = (long long)resident(threads, NV > 2 ? 128 : 80) * kNumSMs;
   TraceScope tr("k_rmsnorm", st);
-  k_rmsnorm<E, L, NV><<<(unsigned)(need < most ? need : most), threads_of<L>(), 0, st>>>(a);
+  k_rmsnorm<E, NV, WARP><<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
   return cudaGetLastError();
 }
-template <class E, int L, int NV>
-static cudaError_t bwd(const Args& a, int* blocks, cudaStream_t st) {
-  constexpr int RPB = threads_of<L>() / L;
-  const long long need = (a.rows + RPB - 1) / RPB, most = (L > 256 ? 2 : 4) * kNumSMs;
+template <class E, int NV, bool WARP>
+static cudaError_t bwd(const Args& a, int threads, int* blocks, cudaStream_t st) {
+  constexpr int RPB = WARP ? kWarpRows : 1;
+  const long long need = (a.rows + RPB - 1) / RPB;
+  long long most = (long long)resident(threads, NV > 2 ? 168 : 112) * kNumSMs;
+  if (most > kMaxBlocks) most = kMaxBlocks;
   *blocks = (int)(need < most ? need : most);
-  const size_t bytes = RPB > 1 ? (size_t)RPB * a.d * 4 : 0;
-  if (bytes > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd<E, L, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-  }
   TraceScope tr("k_rmsnorm_bwd", st);
-  k_rmsnorm_bwd<E, L, NV><<<*blocks, threads_of<L>(), bytes, st>>>(a);
+  k_rmsnorm_bwd<E, NV, WARP><<<*blocks, threads, WARP ? (size_t)RPB * a.d * 4 : 0, st>>>(a);
   return cudaGetLastError();
 }
 
-// L: the fewest threads a row that leave each at most kNV vectors.
-template <class E, class F>
+// The variant by row length: f.operator()<NV, WARP>(threads).
+template <class E, bool BWD, class F>
 static cudaError_t by_row(const Args& a, F f) {
   const int nvec = a.d / Vec<E>::N;
-  auto nv = [&](int L) { return (nvec + L - 1) / L; };
-#define CFC_RMS_L(LV)                                                      \
-  if (nv(LV) <= kNV) {                                                     \
-    if (nv(LV) <= 1) return f.template operator()<LV, 1>();                \
-    if (nv(LV) <= 2) return f.template operator()<LV, 2>();                \
-    return f.template operator()<LV, 4>();                                 \
-  }
-  CFC_RMS_L(32)
-  CFC_RMS_L(64)
-  CFC_RMS_L(128)
-  CFC_RMS_L(256)
-  CFC_RMS_L(512)
-#undef CFC_RMS_L
+  auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
+  if (nvec <= 32) return f.template operator()<1, true>(32 * kWarpRows);
+  if (nvec <= 64) return f.template operator()<2, true>(32 * kWarpRows);
+  if (threads(2) <= most_threads<2, false, BWD>()) return f.template operator()<2, false>(threads(2));
+  if (threads(4) <= most_threads<4, false, BWD>()) return f.template operator()<4, false>(threads(4));
   return cudaErrorNotSupported;
 }
 
 template <class E> struct Fwd {
   const Args& a; cudaStream_t st;
-  template <int L, int NV> cudaError_t operator()() { return fwd<E, L, NV>(a, st); }
+  template <int NV, bool WARP> cudaError_t operator()(int threads) { return fwd<E, NV, WARP>(a, threads, st); }
 };
 template <class E> struct Bwd {
   const Args& a; int* blocks; cudaStream_t st;
-  template <int L, int NV> cudaError_t operator()() { return bwd<E, L, NV>(a, blocks, st); }
+  template <int NV, bool WARP> cudaError_t operator()(int threads) { return bwd<E, NV, WARP>(a, threads, blocks, st); }
 };
 
 template <class E>
 static cudaError_t forward(const Args& a, cudaStream_t st) {
   const bool group_ok = !a.y8 || a.group == a.d || a.group == 32 || a.group == 64 || a.group == 128;
   cudaError_t e = cudaErrorNotSupported;
-  if (a.d % 8 == 0 && group_ok) e = by_row<E>(a, Fwd<E>{a, st});
+  if (a.d % 8 == 0 && group_ok) e = by_row<E, false>(a, Fwd<E>{a, st});
   if (e != cudaErrorNotSupported) return e;
   TraceScope tr("k_rmsnorm_any", st);
   k_rmsnorm_any<E><<<(unsigned)(a.rows < 8 * kNumSMs ? a.rows : 8 * kNumSMs), kAnyThreads, 0, st>>>(a);
@@ -435,7 +451,7 @@ static cudaError_t backward(const Args& a, float* grad_w, cudaStream_t st) {
   int blocks = 0;
   cudaError_t e = cudaErrorNotSupported;
   if (a.rows == 0) e = cudaSuccess;              // grad_w = 0
-  else if (a.d % 8 == 0) e = by_row<E>(a, Bwd<E>{a, &blocks, st});
+  else if (a.d % 8 == 0) e = by_row<E, true>(a, Bwd<E>{a, &blocks, st});
   if (e == cudaErrorNotSupported) {
     const size_t bytes = (size_t)a.d * 4;
     if (bytes > 48 * 1024) {

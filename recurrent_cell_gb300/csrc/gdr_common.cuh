@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include "cfc_internal.cuh"
+#include "tc_common.cuh"
 
 namespace cfc {
 namespace gdr {
@@ -98,6 +99,30 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Bulk copy of `bytes` (a multiple of 16, both ends 16-byte aligned) into
+// shared memory; `bar` receives the bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+// An arrival of this thread once all its cp.async so far have landed.
+__device__ __forceinline__ void bar_arrive_cp(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Barrier over the first `threads` threads that name it (1 .. 15).
+template <int ID, int THREADS>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+constexpr uint32_t kPolls = 1u << 20;   // of a bounded wait
+
 // rows x cols elements (cols x sizeof(E) a multiple of 16) from rows `stride`
 // apart into rows `ld` apart; rows past row_end and columns past col_end are
 // zeros.  col_end is a multiple of 16 bytes.
@@ -106,10 +131,27 @@ __device__ __forceinline__ void load_tile(E* dst, int ld, const E* src, long lon
                                           int tid) {
   constexpr int V = 16 / sizeof(E);
   constexpr int PER = COLS / V;
-  for (int i = tid; i < ROWS * PER; i += THREADS) {
-    const int r = i / PER, c = (i % PER) * V;
-    const bool on = r < row_end && c < col_end;
-    cp16(dst + r * ld + c, on ? src + r * stride + c : src, on);
+  if constexpr (THREADS % PER == 0 && ROWS % (THREADS / PER) == 0) {
+    constexpr int STEP = THREADS / PER;         // a thread keeps its column
+    const int c = (tid % PER) * V;
+    int r = tid / PER;
+    const E* p = src + r * stride + c;
+    E* d = dst + r * ld + c;
+    const bool in = c < col_end;
+#pragma unroll 8
+    for (int i = 0; i < ROWS / STEP; ++i) {
+      const bool on = in && r < row_end;
+      cp16(d, on ? p : src, on);
+      r += STEP;
+      p += STEP * stride;
+      d += STEP * ld;
+    }
+  } else {
+    for (int i = tid; i < ROWS * PER; i += THREADS) {
+      const int r = i / PER, c = (i % PER) * V;
+      const bool on = r < row_end && c < col_end;
+      cp16(dst + r * ld + c, on ? src + r * stride + c : src, on);
+    }
   }
 }
 
@@ -192,6 +234,19 @@ struct MBf16 {
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+  // the same, the small products into a sum of their own: shorter chains
+  static constexpr bool two_sums(int PA, int PB) { return PA + PB > 2; }
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma(float (&d)[4], float (&lo)[4], const A<PA>& a, const B<PB>& b, int h) {
+    if constexpr (PA == 2) mma1(lo, a.r[1], b.r[0][2 * h], b.r[0][2 * h + 1]);
+    if constexpr (PB == 2) mma1(lo, a.r[0], b.r[1][2 * h], b.r[1][2 * h + 1]);
+    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
+  }
+  // with the hi plane of A alone
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma_hi(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
+    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
+  }
   template <int PA, int PB>
   __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
     if constexpr (PA == 2) mma1(d, a.r[1], b.r[0][2 * h], b.r[0][2 * h + 1]);
@@ -206,6 +261,19 @@ struct MBf16 {
     if constexpr (PL == 2)
       *reinterpret_cast<__nv_bfloat162*>(m.p + m.plane + row * m.ld + col) =
           __floats2bfloat162_rn(v0 - __bfloat162float(h.x), v1 - __bfloat162float(h.y));
+  }
+  template <int PL>
+  __device__ static __forceinline__ void put4(const Mat<E>& m, int row, int col, const float4& v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    E* p = m.p + row * m.ld + col;
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if constexpr (PL == 2) {
+      const __nv_bfloat162 c = __floats2bfloat162_rn(v.x - __bfloat162float(a.x), v.y - __bfloat162float(a.y)),
+                           d = __floats2bfloat162_rn(v.z - __bfloat162float(b.x), v.w - __bfloat162float(b.y));
+      *reinterpret_cast<uint2*>(p + m.plane) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
+    }
   }
   __device__ static __forceinline__ float2 get2(const E* p) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
@@ -270,6 +338,17 @@ struct MFp32 {
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
+  static constexpr bool two_sums(int, int) { return true; }
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma(float (&d)[4], float (&lo)[4], const A<PA>& a, const B<PB>& b, int h) {
+    mma1(lo, a.l, b.h[2 * h], b.h[2 * h + 1]);
+    mma1(lo, a.h, b.l[2 * h], b.l[2 * h + 1]);
+    mma1(d, a.h, b.h[2 * h], b.h[2 * h + 1]);
+  }
+  template <int PA, int PB>
+  __device__ static __forceinline__ void mma_hi(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
+    mma(d, a, b, h);
+  }
   template <int PA, int PB>
   __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
     mma1(d, a.l, b.h[2 * h], b.h[2 * h + 1]);
@@ -280,6 +359,10 @@ struct MFp32 {
   __device__ static __forceinline__ void put2(const Mat<E>& m, int row, int col, float v0, float v1) {
     *reinterpret_cast<float2*>(m.p + row * m.ld + col) = make_float2(v0, v1);
   }
+  template <int PL>
+  __device__ static __forceinline__ void put4(const Mat<E>& m, int row, int col, const float4& v) {
+    *reinterpret_cast<float4*>(m.p + row * m.ld + col) = v;
+  }
   __device__ static __forceinline__ float2 get2(const E* p) { return *reinterpret_cast<const float2*>(p); }
 };
 
@@ -289,14 +372,16 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------ workspace
-// Per (slot, value head): T (1 or 2 planes), P, the vectors; when the backward
+// Per (slot, value head): T - I and P (bf16: two planes each), rows padded as they lie
+// in shared memory, so that each is one bulk copy; the vectors; when the backward
 // is to follow also the state before the chunk (S0^T [d_v, d_k], in the
 // operand type the products read it in) and U^T [d_v, 64]; and the backward's
 // own dS1^T, dR^T, and per-value-head dq, dk where heads are shared.
 struct Workspace {
   size_t off_t, off_p, off_vec, off_s0, off_u, off_ds, off_dr, off_dq, off_dk, total;
-  int t_planes;
 };
+template <class P> constexpr int kLdt = kC + P::PAD;                                  // row of T - I, P
+template <class P> constexpr int kTPlanes = P::kMode == CFC_MATH_BF16 ? 2 : 1;
 Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 
 }  // namespace gdr
