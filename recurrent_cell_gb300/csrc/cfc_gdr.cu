@@ -10,29 +10,16 @@
 // is then a chain of latencies, and every block shortens it by itself), wide
 // tiles where the heads alone fill the GPU (then the tiles' shared operands
 // are read fewer times).
-#include <cstdlib>
 #include "gdr_common.cuh"
 
 namespace cfc {
 namespace gdr {
 
-struct FwdArgs {
-  Shape s;
-  const void *q, *k, *v;
-  long long ldq, ldk, ldv;        // elements from one row to the next
-  const float *g, *beta;
-  const float* init;
-  float* final_state;
-  void* o;
-  char *t, *p, *s0, *u;
-  float* vec;
-  int save;
-  int ntile;
-};
-
 __device__ int g_gdr_error = 0;   // a bounded wait gave up
 
 // ------------------------------------------------------------------- prep
+constexpr uint32_t kImage = 32768;   // bf16: [T - I; P T] in two planes of 128 rows x 128 bytes
+
 template <class P, int DK>
 struct PrepSmem {
   using E = typename P::E;
@@ -43,7 +30,9 @@ struct PrepSmem {
   static constexpr size_t kA = sizeof(float) * kC * LDA, kP = kTPlanes<P> * sizeof(E) * kC * LDT;
   // k, then A and T; q, then P: the products are done when the others begin
   static constexpr size_t kOffQ = kTile > kA ? kTile : kA;
-  static constexpr size_t kOffG = kOffQ + (kTile > kP ? kTile : kP);
+  static constexpr bool TC = P::kMode == CFC_MATH_BF16;
+  static constexpr size_t kQ = TC ? kA : kP;             // fp32 P where P T is to be formed
+  static constexpr size_t kOffG = kOffQ + (kTile > kQ ? kTile : kQ);
   static constexpr size_t kBytes = kOffG + 3 * kC * sizeof(float);
 };
 
@@ -61,6 +50,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   E* qs = reinterpret_cast<E*>(smem_raw + S::kOffQ);
   float* am = reinterpret_cast<float*>(smem_raw);
   E* ps = qs;
+  float* pm = reinterpret_cast<float*>(smem_raw + S::kOffQ);
   float* ghi = reinterpret_cast<float*>(smem_raw + S::kOffG);
   float *glo = ghi + kC, *bet = glo + kC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -146,14 +136,16 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
       const float2 h2 = *reinterpret_cast<const float2*>(ghi + col), l2 = *reinterpret_cast<const float2*>(glo + col);
       const float l0 = col <= i ? expf((hi - h2.x) + (lo - l2.x)) : 0.f;
       const float l1 = col < i ? expf((hi - h2.y) + (lo - l2.y)) : 0.f;
-      P::template put2<PL>(Mat<E>{ps, S::LDT, kC * S::LDT}, i, col, col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f,
-                          col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f);
+      const float p0 = col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f,
+                  p1 = col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f;
+      if constexpr (S::TC) *reinterpret_cast<float2*>(pm + i * S::LDA + col) = make_float2(p0, p1);
+      else P::template put2<PL>(Mat<E>{ps, S::LDT, kC * S::LDT}, i, col, p0, p1);
       *reinterpret_cast<float2*>(am + i * S::LDA + col) =
           make_float2(col < i ? be * l0 * ak[j][rr * 2] : 0.f, col + 1 < i ? be * l1 * ak[j][rr * 2 + 1] : 0.f);
     }
   }
   __syncthreads();
-  {
+  if constexpr (!S::TC) {
     E* out = reinterpret_cast<E*>(a.p) + id * (kTPlanes<P> * kC * S::LDT);
     constexpr int V = 16 / sizeof(E);
     for (int i = tid; i < PL * kC * S::LDT / V; i += 128)
@@ -234,16 +226,70 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
       __syncthreads();
     }
   }
-  E* tout = reinterpret_cast<E*>(a.t) + id * (kTPlanes<P> * kC * S::LDT);
-  const Mat<E> mt{tout, S::LDT, kC * S::LDT};
-  for (int i = tid; i < kC * kC / 4; i += 128) {
-    const int r = i / (kC / 4), col = (i % (kC / 4)) * 4;
-    float4 v = *reinterpret_cast<const float4*>(am + r * S::LDA + col);
-    if (r == col) v.x = 0.f;            // T - I: the products add R itself in fp32
-    if (r == col + 1) v.y = 0.f;
-    if (r == col + 2) v.z = 0.f;
-    if (r == col + 3) v.w = 0.f;
-    P::template put4<PL>(mt, r, col, v);
+  if constexpr (S::TC) {
+    // P T, a warp its 16 rows, in place of P
+    float d[8][4] = {};
+    const Mat<float> mp{pm, S::LDA, 0}, mt{am, S::LDA, 0};
+#pragma unroll
+    for (int k0 = 0; k0 < kC; k0 += 8) {
+      if (k0 >= m0 + 16) break;
+      MFp32::A<1> xa;
+      MFp32::load_a(xa, mp, m0, k0, lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j * 16 > k0) continue;
+        MFp32::B<1> xb;
+        MFp32::load_bk(xb, mt, j * 16, k0, lane);
+        MFp32::mma(d[2 * j], xa, xb, 0);
+        MFp32::mma(d[2 * j + 1], xa, xb, 1);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      *reinterpret_cast<float2*>(pm + (m0 + g) * S::LDA + j * 8 + t2) = make_float2(d[j][0], d[j][1]);
+      *reinterpret_cast<float2*>(pm + (m0 + g + 8) * S::LDA + j * 8 + t2) = make_float2(d[j][2], d[j][3]);
+    }
+    __syncthreads();
+    // T - I and P T as the tensor cores read them: rows of 128 bytes, 16-byte
+    // piece c of row r at piece c ^ (r % 8)
+    unsigned char* img = reinterpret_cast<unsigned char*>(a.t) + id * kImage;
+    for (int e = tid; e < 2 * kC * 8; e += 128) {
+      const int r = e >> 3, ch = e & 7, i = r & 63;
+      const float* src = (r < kC ? am : pm) + i * S::LDA + ch * 8;
+      float v[8];
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(src + 4);
+      if (r < kC && (i >> 3) == ch)            // T - I: the products add R itself in fp32
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = (i & 7) == x ? 0.f : v[x];
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
+        hi[x] = *reinterpret_cast<const uint32_t*>(&b);
+        if constexpr (PL == 2) {
+          const __nv_bfloat162 c2 =
+              __floats2bfloat162_rn(v[2 * x] - __bfloat162float(b.x), v[2 * x + 1] - __bfloat162float(b.y));
+          lo[x] = *reinterpret_cast<const uint32_t*>(&c2);
+        }
+      }
+      const int at = r * 128 + ((ch ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (PL == 2) *reinterpret_cast<uint4*>(img + kImage / 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  } else {
+    E* tout = reinterpret_cast<E*>(a.t) + id * (kTPlanes<P> * kC * S::LDT);
+    const Mat<E> mt{tout, S::LDT, kC * S::LDT};
+    for (int i = tid; i < kC * kC / 4; i += 128) {
+      const int r = i / (kC / 4), col = (i % (kC / 4)) * 4;
+      float4 v = *reinterpret_cast<const float4*>(am + r * S::LDA + col);
+      if (r == col) v.x = 0.f;            // T - I: the products add R itself in fp32
+      if (r == col + 1) v.y = 0.f;
+      if (r == col + 2) v.z = 0.f;
+      if (r == col + 3) v.w = 0.f;
+      P::template put4<PL>(mt, r, col, v);
+    }
   }
 }
 
@@ -384,9 +430,17 @@ __global__ void __launch_bounds__(ScanCfg<P, DK, MT, WM, PL, SPLIT>::THREADS) k_
     group_sync<1, C::WORK>();
     if (!SPLIT && c > 0)
       store_tile<E, kC, C::DVT, C::CHAIN>(o + (long long)(c - 1) * kC * ldo, ldo, ost, C::LDV, kC, dvn, otid);
-    if (outs && a.save)
-      store_tile<E, C::DVT, DK, C::CHAIN>(
-          reinterpret_cast<E*>(a.s0) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * dk, dk, sop_p, C::LDK, dvn, dk, otid);
+    if (chain && a.save)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
+            if (r < dvn && col < dk)
+              put(reinterpret_cast<E*>(a.s0) + (((slot0 + c) * a.s.hv + h) * dk + col) * dv + dv0 + r, s[mt][nt][e]);
+          }
 
     // S0^T k and S0^T q of this warp's 16 tokens
     float ar[MT][2][4] = {}, al[MT][2][4] = {}, ao[MT][2][4] = {};
@@ -469,15 +523,17 @@ __global__ void __launch_bounds__(ScanCfg<P, DK, MT, WM, PL, SPLIT>::THREADS) k_
             const int r = m0 + mt * 16 + g + rr * 8;
             float u0 = au[mt][hf][2 * rr], u1 = au[mt][hf][2 * rr + 1];
             if constexpr (P::two_sums(PL, PL)) { u0 += aw[mt][hf][2 * rr]; u1 += aw[mt][hf][2 * rr + 1]; }
+            if (a.save && r < dvn) {
+              E* p = reinterpret_cast<E*>(a.u) + (((slot0 + c) * a.s.hv + h) * kC + i) * dv + dv0 + r;
+              put(p, u0);
+              put(p + dv, u1);
+            }
             P::template put2<PL>(uop, r, i, u0, u1);
             P::template put2<PL>(ukop, r, i, el.x * u0, el.y * u1);
           }
       }
     }
     group_sync<1, C::WORK>();
-    if (outs && a.save)
-      store_tile<E, C::DVT, kC, C::CHAIN>(
-          reinterpret_cast<E*>(a.u) + (((slot0 + c) * a.s.hv + h) * dv + dv0) * kC, kC, uop_p, C::LDT, dvn, kC, otid);
     if (outs) {
       // O += P U
 #pragma unroll
@@ -590,19 +646,14 @@ static cudaError_t forward(const FwdArgs& a, cudaStream_t st) {
     cudaError_t e = launch_prep<P, DK, PL>(a, st);
     if (e != cudaSuccess) return e;
   }
-  // The widest tile of value columns whose blocks still reach every SM.
-  const long long heads = (long long)a.s.n_seq * a.s.hv;
-  auto blocks = [&](int w) { return heads * ((a.s.dv + w - 1) / w); };
   if constexpr (P::kMode == CFC_MATH_BF16) {
-    if constexpr (PL == 1)
-      if (a.s.dv > 64 && blocks(128) >= 114) {
-        if (getenv("GDR_X")) return launch_scan<P, DK, 4, 2, PL, false>(a, st);
-        return launch_scan<P, DK, 2, 4, PL, false>(a, st);
-      }
-    if (a.s.dv > 32 && blocks(64) >= 114) return launch_scan<P, DK, 2, 2, PL, false>(a, st);
+    return launch_scan_tc(a, DK, PL, st);
+  } else {
+    // Tiles of 32 value columns where their blocks still reach every SM, else of 16.
+    const long long heads = (long long)a.s.n_seq * a.s.hv;
+    if (a.s.dv > 16 && heads * ((a.s.dv + 31) / 32) >= 114) return launch_scan<P, DK, 1, 2, PL, true>(a, st);
+    return launch_scan<P, DK, 1, 1, PL, true>(a, st);
   }
-  if (a.s.dv > 16 && blocks(32) >= 114) return launch_scan<P, DK, 1, 2, PL, true>(a, st);
-  return launch_scan<P, DK, 1, 1, PL, true>(a, st);
 }
 
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -614,9 +665,8 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
   size_t off = 0;
   auto take = [&](size_t* at, size_t bytes) { *at = off; off = up256(off + bytes); };
   const bool bf = math == CFC_MATH_BF16;
-  const size_t row = bf ? kLdt<MBf16> : kLdt<MFp32>;
-  take(&w.off_t, slots * (bf ? kTPlanes<MBf16> : kTPlanes<MFp32>) * kC * row * e);
-  take(&w.off_p, slots * (bf ? kTPlanes<MBf16> : kTPlanes<MFp32>) * kC * row * e);
+  take(&w.off_t, slots * (bf ? kImage : kC * kLdt<MFp32> * sizeof(float)));
+  take(&w.off_p, bf ? 0 : slots * kC * kLdt<MFp32> * sizeof(float));
   take(&w.off_vec, slots * kVec * 4);
   if (save) {
     take(&w.off_s0, slots * dk * dv * e);
@@ -635,6 +685,8 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
 }  // namespace gdr
 
 int read_gdr_error(int clear) {
+  const int t = gdr::read_gdr_tc_error(clear);
+  if (t != 0) return t;
   int v = 0;
   if (cudaMemcpyFromSymbol(&v, gdr::g_gdr_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
   if (clear && v) {

@@ -28,20 +28,6 @@
 namespace cfc {
 namespace gdr {
 
-struct BwdArgs {
-  Shape s;
-  const void *q, *k, *v, *go;
-  long long ldq, ldk, ldv;
-  const float* gfinal;
-  float* ginit;
-  void *gq, *gk, *gv, *gg, *gbeta;
-  const char *t, *p, *s0, *u;
-  char *ds, *dr;
-  const float* vec;
-  float *pdq, *pdk;        // per value head [rows, hv, dk], or NULL
-  int ntile;
-};
-
 // -------------------------------------------------------------- serial pass
 // The forward scan's split of warps: dS^T in registers, 16 MT value columns by
 // a quarter of the key width a warp.
@@ -76,8 +62,7 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
   E* drk_p = dr_p + C::ROP;
   E* uop_p = sop_p + (C::ELEMS - ST * C::STAGE - 2 * C::ROP);
   E* dop_p = uop_p + C::ROP;
-  const Mat<E> sop{sop_p, C::LDK, 0}, uop{uop_p, C::LDT, 0}, dop{dop_p, C::LDT, 0}, drm{dr_p, C::LDT, 0},
-      drk{drk_p, C::LDT, 0};
+  const Mat<E> sop{sop_p, C::LDK, 0}, uop{uop_p, C::LDT, 0}, dop{dop_p, C::LDT, 0}, drk{drk_p, C::LDT, 0};
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wn = warp & 3, wm = warp >> 2;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -144,8 +129,15 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
                               s[mt][nt][2 * rr + 1]);
     __syncthreads();
     if (ST == 2 && c > 0) fetch(c - 1, (c - 1) & 1);
-    store_tile<E, C::DVT, DK, C::THREADS>(reinterpret_cast<E*>(a.ds) + (id * dv + dv0) * dk, dk, sop_p, C::LDK, dvn, dk,
-                                          tid);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
+          if (r < dvn && col < dk) put(reinterpret_cast<E*>(a.ds) + (id * dk + col) * dv + dv0 + r, s[mt][nt][e]);
+        }
     // dU of this warp's 16 tokens
     float ak[MT][2][4] = {}, ap[MT][2][4] = {}, ar[MT][2][4];
 #pragma unroll
@@ -217,15 +209,17 @@ __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
         for (int rr = 0; rr < 2; ++rr) {
           const int r = m0 + mt * 16 + g + rr * 8;
           const float r0 = ar[mt][hf][2 * rr], r1 = ar[mt][hf][2 * rr + 1];
-          P::template put2<1>(drm, r, i, r0, r1);
+          if (r < dvn) {
+            E* p = reinterpret_cast<E*>(a.dr) + (id * kC + i) * dv + dv0 + r;
+            put(p, r0);
+            put(p + dv, r1);
+          }
           P::template put2<1>(drk, r, i, -be.x * eg.x * r0, -be.y * eg.y * r1);
           put(gst + i * C::LDV + r, be.x * r0);
           put(gst + (i + 1) * C::LDV + r, be.y * r1);
         }
     }
     __syncthreads();
-    store_tile<E, C::DVT, kC, C::THREADS>(reinterpret_cast<E*>(a.dr) + (id * dv + dv0) * kC, kC, dr_p, C::LDT, dvn, kC,
-                                          tid);
     store_tile<E, kC, C::DVT, C::THREADS>(gv + (long long)c * kC * ldo, ldo, gst, C::LDV, len - c * kC, dvn, tid);
     const float d = vec[kVecD];
 #pragma unroll
@@ -281,8 +275,8 @@ struct GradSmem {
   static constexpr int LDK = DK + P::PAD, LDT = kC + P::PAD, LDV = DVS + P::PAD;
   E k[kC * LDK], q[kC * LDK];
   E go[ST][kC * LDV], v[ST][kC * LDV];
-  E u[ST][DVS * LDT], dr[ST][DVS * LDT];
-  E s0[ST][DVS * LDK], ds[ST][DVS * LDK];
+  E u[ST][kC * LDV], dr[ST][kC * LDV];
+  E s0[ST][DK * LDV], ds[ST][DK * LDV];
   static constexpr int PL = kTPlanes<P>;
   E dp[PL * kC * LDT], da[PL * kC * LDT], dm[PL * kC * LDT];    // 17 bits in bf16: dg is a difference of large sums
   float vec[kVec];
@@ -320,11 +314,10 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
     const int v0 = x * DVS, vn = min(DVS, dv - v0);
     load_tile<E, kC, DVS, 256>(sm.go[st], S::LDV, go + v0, ldo, rows, vn, tid);
     load_tile<E, kC, DVS, 256>(sm.v[st], S::LDV, v + v0, a.ldv, rows, vn, tid);
-    const long long at = id * dv + v0;
-    load_tile<E, DVS, kC, 256>(sm.u[st], S::LDT, reinterpret_cast<const E*>(a.u) + at * kC, kC, vn, kC, tid);
-    load_tile<E, DVS, kC, 256>(sm.dr[st], S::LDT, reinterpret_cast<const E*>(a.dr) + at * kC, kC, vn, kC, tid);
-    load_tile<E, DVS, DK, 256>(sm.s0[st], S::LDK, reinterpret_cast<const E*>(a.s0) + at * dk, dk, vn, dk, tid);
-    load_tile<E, DVS, DK, 256>(sm.ds[st], S::LDK, reinterpret_cast<const E*>(a.ds) + at * dk, dk, vn, dk, tid);
+    load_tile<E, kC, DVS, 256>(sm.u[st], S::LDV, reinterpret_cast<const E*>(a.u) + id * kC * dv + v0, dv, kC, vn, tid);
+    load_tile<E, kC, DVS, 256>(sm.dr[st], S::LDV, reinterpret_cast<const E*>(a.dr) + id * kC * dv + v0, dv, kC, vn, tid);
+    load_tile<E, DK, DVS, 256>(sm.s0[st], S::LDV, reinterpret_cast<const E*>(a.s0) + id * dk * dv + v0, dv, dk, vn, tid);
+    load_tile<E, DK, DVS, 256>(sm.ds[st], S::LDV, reinterpret_cast<const E*>(a.ds) + id * dk * dv + v0, dv, dk, vn, tid);
     cp_commit();
   };
   load_tile<E, kC, DK, 256>(sm.k, S::LDK, static_cast<const E*>(a.k) + row0 * a.ldk + (long long)hq * dk, a.ldk, rows,
@@ -343,19 +336,19 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
     cp_wait<0>();
     __syncthreads();
     if (ST == 2 && x + 1 < ns) fetch(x + 1, (x + 1) & 1);
-    const Mat<E> mo{sm.go[st], S::LDV, 0}, mu{sm.u[st], S::LDT, 0}, mr{sm.dr[st], S::LDT, 0}, ms{sm.s0[st], S::LDK, 0},
-        md{sm.ds[st], S::LDK, 0};
+    const Mat<E> mo{sm.go[st], S::LDV, 0}, mu{sm.u[st], S::LDV, 0}, mr{sm.dr[st], S::LDV, 0}, ms{sm.s0[st], S::LDV, 0},
+        md{sm.ds[st], S::LDV, 0};
 #pragma unroll
     for (int k0 = 0; k0 < DVS; k0 += P::KS) {
       typename P::template A<1> fo, fr, fu;
       P::load_a(fo, mo, wr * 16, k0, lane);
-      P::load_at(fr, mr, wr * 16, k0, lane);
-      P::load_at(fu, mu, wr * 16, k0, lane);
+      P::load_a(fr, mr, wr * 16, k0, lane);
+      P::load_a(fu, mu, wr * 16, k0, lane);
 #pragma unroll
       for (int j = 0; j < NT / 2; ++j) {
         typename P::template B<1> bs, bd;
-        P::load_bk(bs, ms, wc * (DK / 2) + j * 16, k0, lane);
-        P::load_bk(bd, md, wc * (DK / 2) + j * 16, k0, lane);
+        P::load_bn(bs, ms, wc * (DK / 2) + j * 16, k0, lane);
+        P::load_bn(bd, md, wc * (DK / 2) + j * 16, k0, lane);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           P::mma(aq[2 * j + hf], fo, bs, hf);
@@ -367,7 +360,7 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       for (int j = 0; j < 2; ++j) {
         if (wc * 32 + j * 16 > wr * 16) continue;        // above the diagonal
         typename P::template B<1> bu;
-        P::load_bk(bu, mu, wc * 32 + j * 16, k0, lane);
+        P::load_bn(bu, mu, wc * 32 + j * 16, k0, lane);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           P::mma(ap[2 * j + hf], fo, bu, hf);
@@ -379,11 +372,11 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       const int i = tid & 63, part = tid >> 6;
 #pragma unroll
       for (int e = 0; e < DVS / 4; ++e)
-        drv = fmaf(to_f(sm.dr[st][(part * (DVS / 4) + e) * S::LDT + i]),
+        drv = fmaf(to_f(sm.dr[st][i * S::LDV + part * (DVS / 4) + e]),
                    to_f(sm.v[st][i * S::LDV + part * (DVS / 4) + e]), drv);
       for (int e = tid; e < DVS * DK / 2; e += 256) {
-        const int r = e / (DK / 2), cc = (e % (DK / 2)) * 2;
-        const float2 x0 = P::get2(sm.s0[st] + r * S::LDK + cc), x1 = P::get2(sm.ds[st] + r * S::LDK + cc);
+        const int r = e / (DVS / 2), cc = (e % (DVS / 2)) * 2;
+        const float2 x0 = P::get2(sm.s0[st] + r * S::LDV + cc), x1 = P::get2(sm.ds[st] + r * S::LDV + cc);
         ss = fmaf(x0.x, x1.x, fmaf(x0.y, x1.y, ss));
       }
     }
@@ -581,16 +574,12 @@ static cudaError_t launch_scan_bwd(BwdArgs a, cudaStream_t st) {
 template <class P, int DK>
 static cudaError_t backward(const BwdArgs& a, cudaStream_t st) {
   using E = typename P::E;
-  const long long heads = (long long)a.s.n_seq * a.s.hv;
-  auto blocks = [&](int w) { return heads * ((a.s.dv + w - 1) / w); };
   cudaError_t e;
-  bool done = false;
   if constexpr (P::kMode == CFC_MATH_BF16) {
-    if (a.s.dv > 64 && blocks(128) >= 114) { e = launch_scan_bwd<P, DK, 2, 4>(a, st); done = true; }
-    else if (a.s.dv > 32 && blocks(64) >= 114) { e = launch_scan_bwd<P, DK, 2, 2>(a, st); done = true; }
-  }
-  if (!done) {
-    if (a.s.dv > 16 && blocks(32) >= 114) e = launch_scan_bwd<P, DK, 1, 2>(a, st);
+    e = launch_scan_bwd_tc(a, DK, st);
+  } else {
+    const long long heads = (long long)a.s.n_seq * a.s.hv;
+    if (a.s.dv > 16 && heads * ((a.s.dv + 31) / 32) >= 114) e = launch_scan_bwd<P, DK, 1, 2>(a, st);
     else e = launch_scan_bwd<P, DK, 1, 1>(a, st);
   }
   if (e != cudaSuccess || a.s.rows == 0) return e;

@@ -384,5 +384,38 @@ template <class P> constexpr int kLdt = kC + P::PAD;                            
 template <class P> constexpr int kTPlanes = P::kMode == CFC_MATH_BF16 ? 2 : 1;
 Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 
+struct FwdArgs {
+  Shape s;
+  const void *q, *k, *v;
+  long long ldq, ldk, ldv;        // elements from one row to the next
+  const float *g, *beta;
+  const float* init;
+  float* final_state;
+  void* o;
+  char *t, *p, *s0, *u;
+  float* vec;
+  int save;
+  int ntile;
+};
+
+struct BwdArgs {
+  Shape s;
+  const void *q, *k, *v, *go;
+  long long ldq, ldk, ldv;
+  const float* gfinal;
+  float* ginit;
+  void *gq, *gk, *gv, *gg, *gbeta;
+  const char *t, *p, *s0, *u;
+  char *ds, *dr;
+  const float* vec;
+  float *pdq, *pdk;        // per value head [rows, hv, dk], or NULL
+  int ntile;
+};
+
+// The serial passes in bf16 (cfc_gdr_tc.cu).
+cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st);
+cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st);
+int read_gdr_tc_error(int clear);
+
 }  // namespace gdr
 }  // namespace cfc
