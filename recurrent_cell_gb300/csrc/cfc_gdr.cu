@@ -669,11 +669,12 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
   take(&w.off_p, bf ? 0 : slots * kC * kLdt<MFp32> * sizeof(float));
   take(&w.off_vec, slots * kVec * 4);
   if (save) {
-    take(&w.off_s0, slots * dk * dv * e);
-    take(&w.off_u, slots * kC * dv * e);
-    take(&w.off_ds, slots * dk * dv * e);
-    take(&w.off_dr, slots * kC * dv * e);
-    if (hv != hk) {
+    const size_t wk = bf ? (dk <= 64 ? 64 : 128) : dk, wv = bf ? (dv + 63) / 64 * 64 : dv;
+    take(&w.off_s0, slots * wk * wv * e);
+    take(&w.off_u, slots * kC * wv * e);
+    take(&w.off_ds, slots * wk * wv * e);
+    take(&w.off_dr, slots * kC * wv * e);
+    if (hv != hk && !bf) {
       take(&w.off_dq, (size_t)rows * hv * dk * 4);
       take(&w.off_dk, (size_t)rows * hv * dk * 4);
     }
@@ -685,8 +686,8 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
 }  // namespace gdr
 
 int read_gdr_error(int clear) {
-  const int t = gdr::read_gdr_tc_error(clear);
-  if (t != 0) return t;
+  const int t = gdr::read_gdr_tc_error(clear), r = gdr::read_gdr_grad_error(clear);
+  if (t != 0 || r != 0) return t != 0 ? t : r;
   int v = 0;
   if (cudaMemcpyFromSymbol(&v, gdr::g_gdr_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
   if (clear && v) {

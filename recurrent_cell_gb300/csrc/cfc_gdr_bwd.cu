@@ -577,6 +577,7 @@ static cudaError_t backward(const BwdArgs& a, cudaStream_t st) {
   cudaError_t e;
   if constexpr (P::kMode == CFC_MATH_BF16) {
     e = launch_scan_bwd_tc(a, DK, st);
+    return e != cudaSuccess || a.s.rows == 0 ? e : launch_grad_tc(a, DK, st);
   } else {
     const long long heads = (long long)a.s.n_seq * a.s.hv;
     if (a.s.dv > 16 && heads * ((a.s.dv + 31) / 32) >= 114) e = launch_scan_bwd<P, DK, 1, 2>(a, st);
@@ -614,7 +615,7 @@ cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_
   a.t = g.ws + w.off_t; a.p = g.ws + w.off_p; a.s0 = g.ws + w.off_s0; a.u = g.ws + w.off_u;
   a.ds = g.ws + w.off_ds; a.dr = g.ws + w.off_dr;
   a.vec = reinterpret_cast<const float*>(g.ws + w.off_vec);
-  if (g.hv != g.hk) {
+  if (g.hv != g.hk && g.math == CFC_MATH_FP32) {
     a.pdq = reinterpret_cast<float*>(g.ws + w.off_dq);
     a.pdk = reinterpret_cast<float*>(g.ws + w.off_dk);
   }

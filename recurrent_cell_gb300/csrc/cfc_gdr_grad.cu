@@ -1,0 +1,453 @@
+// cfc_gdr_grad.cu -- the parallel part of the gated delta rule's backward in
+// bf16 on the tensor cores: dq, dk, dg, dbeta of every chunk (formulas at the
+// top of cfc_gdr_bwd.cu, notation of gdr_common.cuh).
+//
+// Persistent blocks, one an SM, take a chunk of a key head at a time and walk
+// over its value heads, whose parts of dq and dk add up in registers.  A head
+// takes five products; rows 0-63 and 64-127 of the accumulators are tokens:
+//   D1 = [dR; dO] S0^T     X                 | S0 dO
+//   D2 = [dR; dO] U^T      dR_i.U_j          | dO_i.U_j
+//   D3 = [U; dR] dS1^T     dS1 U             | (not used)
+//   D4 = [dA; dP] K        of E              | of dq
+//   D5 = dP^T Q + (beta dA)^T K   of dk      | (not used)
+// with dA = -L o D2 strictly below the diagonal and dP = scale L o D2 up to it,
+// each in two bf16 planes: dg is a difference of their sums.  S0, U, dS1 and dR
+// come as operand tiles, as the serial passes left them; with the inputs they
+// are the traffic, which bounds the kernel (about 160 KB a chunk and head in,
+// 32 KB out).  Fetching warps keep two 64-column stages and the next chunk's K
+// and Q on their way while the others compute.
+#include "gdr_tc.cuh"
+
+namespace cfc {
+namespace gdr {
+
+__device__ int g_gdr_grad_error = 0;
+
+struct GradArgs {
+  Shape s;
+  const bf16 *q, *k, *v, *go;
+  long long ldq, ldk, ldv;
+  bf16 *gq, *gk, *gg, *gbeta;
+  const unsigned char *s0, *u, *ds, *dr;
+  const float* vec;
+};
+
+template <int DK>
+struct GradCfg {
+  static constexpr int ATOMS = DK / 64, FETCH = 128, WORK = 256, THREADS = WORK + FETCH;
+  static constexpr uint32_t T = 8192;                   // 64 rows x 128 bytes
+  static constexpr uint32_t S = DK * 128u;
+  // a stage: U, dR, dO, V, S0, dS1 of 64 value columns, the vectors
+  static constexpr uint32_t OFF_DO = 2 * T, OFF_V = 3 * T, OFF_S0 = 4 * T, OFF_DS = OFF_S0 + S, OFF_VEC = OFF_DS + S;
+  static constexpr uint32_t STAGE = OFF_VEC + 2048;     // + what the chunk is
+  static constexpr uint32_t OPS = 6 * T;                // dA, dP, beta dA; then their lo planes
+  static constexpr uint32_t KQ = 2 * ATOMS * T;
+  static constexpr uint32_t SMALL = (4 * 2 * 64 + 4 * 64 + 8 + 128) * 4;
+  static constexpr uint32_t BYTES = 2048 + 2 * STAGE + OPS + KQ + SMALL;
+  static_assert(BYTES <= 227u * 1024u, "shared memory");
+};
+
+struct Chunk {
+  long long row0, slot;
+  int rows, hk;           // rows < 0: no more
+};
+
+template <int DK>
+__global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  using C = GradCfg<DK>;
+  unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base);      // stages 0, 1; K and Q
+  uint64_t *empty = full + 3, *done = full + 6;            // done: D1 - D3; D4, D5
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
+  unsigned char* stage = base + 1024;
+  unsigned char* ops = stage + 2 * C::STAGE;
+  unsigned char* kq = ops + C::OPS;
+  float* dot = reinterpret_cast<float*>(kq + C::KQ);       // [4][2][64]: q.dq, k.dk, k.E, k.dS1 U
+  float *drv = dot + 4 * 2 * 64, *sums = drv + 4 * 64, *gs = sums + 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = a.s.hv / a.s.hk, dk = a.s.dk, dv = a.s.dv, nt = (dv + 63) / 64;
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      tc::mbar_init(full + i, C::FETCH + (i < 2 ? 1 : 0));
+      tc::mbar_init(empty + i, C::WORK / 32 + (i < 2 ? 1 : 0));
+    }
+    tc::mbar_init(done, 1);
+    tc::mbar_init(done + 1, 1);
+    tc::mbar_init_fence();
+  }
+  if (warp == 0) tc::tmem_alloc(tmem_at, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_at;
+  bool lost = false;        // a wait gave up: no more waiting, the results are void
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!lost && !tc::mbar_wait(bar, parity, kPolls)) {
+      lost = true;
+      atomicExch(&g_gdr_grad_error, 1);
+    }
+  };
+
+  if (tid >= C::WORK) {     // ---- the fetching warps
+    const int ft = tid - C::WORK;
+    uint64_t* pending = nullptr;           // copies under way whose arrival is still to come
+    auto flush = [&]() {
+      if (!pending) return;
+      cp_wait<0>();
+      tc::fence_proxy_async_smem();
+      bar_arrive(pending);
+      pending = nullptr;
+    };
+    auto claim = [&](int i, uint32_t use) {      // buffer i for its use-th time
+      if (use == 0) return;
+      if (!lost && tc::mbar_try_wait(empty + i, (use - 1) & 1)) return;
+      flush();
+      wait(empty + i, (use - 1) & 1);
+    };
+    auto issued = [&](uint64_t* bar) {
+      cp_commit();
+      if (pending) {
+        cp_wait<1>();
+        tc::fence_proxy_async_smem();
+        bar_arrive(pending);
+      }
+      pending = bar;
+    };
+    uint32_t it = 0, kqi = 0;
+    const long long ldo = (long long)a.s.hv * dv;
+    const long long items = slot_count(a.s.rows, a.s.n_seq) * a.s.hk;
+    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+      const long long slot = item / a.s.hk;
+      const int hk = (int)(item % a.s.hk);
+      int n, len, c;
+      long long start;
+      if (!slot_chunk(a.s, slot, &n, &start, &len, &c)) continue;
+      const long long row0 = start + (long long)c * kC;
+      const int rows = min(kC, len - c * kC);
+      for (int g = 0; g < group; ++g) {
+        const int h = hk * group + g;
+        const long long id = slot * a.s.hv + h;
+        const bf16 *go = a.go + row0 * ldo + (long long)h * dv, *v = a.v + row0 * a.ldv + (long long)h * dv;
+        for (int t = 0; t < nt; ++t, ++it) {
+          const int st = it & 1;
+          claim(st, it >> 1);
+          unsigned char* b = stage + st * C::STAGE;
+          if (ft == 0) {
+            bar_arrive_tx(full + st, 2 * C::T + 2 * C::S + kVec * 4);
+            bulk_load(b, a.u + (id * nt + t) * C::T, C::T, full + st);
+            bulk_load(b + C::T, a.dr + (id * nt + t) * C::T, C::T, full + st);
+            bulk_load(b + C::OFF_S0, a.s0 + (id * nt + t) * C::S, C::S, full + st);
+            bulk_load(b + C::OFF_DS, a.ds + (id * nt + t) * C::S, C::S, full + st);
+            bulk_load(b + C::OFF_VEC, a.vec + id * kVec, kVec * 4, full + st);
+            *reinterpret_cast<Chunk*>(b + C::OFF_VEC + kVec * 4) = Chunk{row0, slot, rows, hk};
+          }
+          const int ch = ft & 7, col = t * 64 + ch * 8;
+#pragma unroll
+          for (int r = ft >> 3; r < kC; r += C::FETCH / 8) {
+            const bool on = r < rows && col < dv;
+            cp16(b + C::OFF_DO + chunk_at(r, ch), on ? go + r * ldo + col : go, on);
+            cp16(b + C::OFF_V + chunk_at(r, ch), on ? v + r * a.ldv + col : v, on);
+          }
+          issued(full + st);
+        }
+        if (g == 0) {
+          claim(2, kqi++);
+          const bf16 *k = a.k + row0 * a.ldk + (long long)hk * dk, *q = a.q + row0 * a.ldq + (long long)hk * dk;
+          constexpr int PER = DK / 8;
+          const int ch = ft % PER;
+          unsigned char* d = kq + (ch >> 3) * C::T;
+#pragma unroll 4
+          for (int r = ft / PER; r < kC; r += C::FETCH / PER) {
+            const bool on = r < rows && ch * 8 < dk;
+            cp16(d + chunk_at(r, ch & 7), on ? k + r * a.ldk + ch * 8 : k, on);
+            cp16(d + C::ATOMS * C::T + chunk_at(r, ch & 7), on ? q + r * a.ldq + ch * 8 : q, on);
+          }
+          issued(full + 2);
+        }
+      }
+    }
+    flush();
+    claim(it & 1, it >> 1);
+    if (ft == 0) {
+      reinterpret_cast<Chunk*>(stage + (it & 1) * C::STAGE + C::OFF_VEC + kVec * 4)->rows = -1;
+      bar_arrive_tx(full + (it & 1), 0);
+    }
+    bar_arrive(full + (it & 1));
+  } else {
+    constexpr int NC = DK / 2;             // columns of dq, dk a thread
+    const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane, i = row & 63;
+    const bool lower = quad < 2;
+    const uint32_t d1 = tmem, d3 = tmem + 128, d4 = tmem + 256, d5 = tmem + 384, d2 = d5;
+    const uint32_t at = (uint32_t)(quad * 32) << 16;
+    const uint32_t id_dk = tc::idesc(128, DK, tc::kFmtBF16), id_64 = tc::idesc(128, 64, tc::kFmtBF16);
+    unsigned char* krow = kq + (DK == 128 ? cg * C::T : 0);          // the block of this thread's columns
+    unsigned char* qrow = krow + C::ATOMS * C::T;
+    const int ch0 = DK == 128 ? 0 : cg * 4;
+    uint32_t it = 0, kqi = 0, heads = 0;
+    float acc[NC];                         // dk of the chunk (rows 0-63), dq
+    for (int g = 0;; ++heads) {
+      wait(full + (it & 1), (it >> 1) & 1);
+      const Chunk ck = *reinterpret_cast<const Chunk*>(stage + (it & 1) * C::STAGE + C::OFF_VEC + kVec * 4);
+      if (ck.rows < 0 || lost) break;
+      const float* vec = reinterpret_cast<const float*>(stage + (it & 1) * C::STAGE + C::OFF_VEC);
+      const float eg = vec[kVecEG + i], el = vec[kVecEGL + i], be = vec[kVecBeta + i], dec = vec[kVecD];
+      if (tid < 128) gs[tid] = vec[kVecGHi + tid];          // G as two floats
+      float ss = 0.f, dr = 0.f;
+      for (int t = 0; t < nt; ++t, ++it) {
+        const int st = it & 1;
+        unsigned char* b = stage + st * C::STAGE;
+        if (t > 0) wait(full + st, (it >> 1) & 1);
+        if (warp == 0) {
+          tc::fence_after_sync();
+          const uint64_t au = tc::sdesc_k_sw128(smem_addr(b)), ar = tc::sdesc_k_sw128(smem_addr(b + C::T)),
+                         b0 = tc::sdesc_k_sw128(smem_addr(b + C::OFF_S0)),
+                         bd = tc::sdesc_k_sw128(smem_addr(b + C::OFF_DS));
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t o = ks * kStepK, ac = (t > 0 || ks > 0) ? 1u : 0u;
+              tc::mma_bf16(d2, tc::sdesc_advance(ar, o), tc::sdesc_advance(au, o), id_64, ac);
+              tc::mma_bf16(d1, tc::sdesc_advance(ar, o), tc::sdesc_advance(b0, o), id_dk, ac);
+              tc::mma_bf16(d3, tc::sdesc_advance(au, o), tc::sdesc_advance(bd, o), id_dk, ac);
+            }
+            tc::mma_commit(empty + st);
+            if (t == nt - 1) tc::mma_commit(done);
+          }
+          __syncwarp();
+        }
+        // <S0, dS1> and dR.v meanwhile
+#pragma unroll
+        for (int e = 0; e < DK * 8 / C::WORK; ++e) {
+          const uint32_t o = (e * C::WORK + tid) * 16;
+          float x[8], y[8];
+          unpack8(x, *reinterpret_cast<const uint4*>(b + C::OFF_S0 + o));
+          unpack8(y, *reinterpret_cast<const uint4*>(b + C::OFF_DS + o));
+#pragma unroll
+          for (int z = 0; z < 8; ++z) ss = fmaf(x[z], y[z], ss);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t o = chunk_at(tid & 63, (tid >> 6) * 2 + e);
+          float x[8], y[8];
+          unpack8(x, *reinterpret_cast<const uint4*>(b + C::T + o));
+          unpack8(y, *reinterpret_cast<const uint4*>(b + C::OFF_V + o));
+#pragma unroll
+          for (int z = 0; z < 8; ++z) dr = fmaf(x[z], y[z], dr);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + st);
+      }
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      group_sync<1, C::WORK>();            // gs is there; warp 7 has done the last head's sums
+      drv[tid] = dr;
+      if (lane == 0) sums[warp] = ss;
+      wait(done, heads & 1);
+      tc::fence_after_sync();
+      {
+        float x[32];
+        ld_sum<32, 1>(d2 + at + cg * 32, x);
+        const float hi = gs[i], lo = gs[64 + i], f = lower ? -1.f : a.s.scale;
+        const bool any = cg * 32 <= i;
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int col = cg * 32 + j + e;
+            const bool in = lower ? col < i : col <= i;
+            w[e] = any && in ? f * x[j + e] * __expf((hi - gs[col]) + (lo - gs[64 + col])) : 0.f;
+          }
+          unsigned char* to = ops + (lower ? 0 : C::T);
+          const uint32_t o = chunk_at(i, cg * 4 + j / 8);
+          auto two = [&](unsigned char* p) {
+            const uint4 h = pack8(w);
+            *reinterpret_cast<uint4*>(p + o) = h;
+            float hv[8];
+            unpack8(hv, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hv[e] = w[e] - hv[e];
+            *reinterpret_cast<uint4*>(p + 3 * C::T + o) = pack8(hv);
+          };
+          two(to);
+          if (lower) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] *= be;
+            two(ops + 2 * C::T);
+          }
+        }
+      }
+      tc::fence_proxy_async_smem();
+      tc::fence_before_sync();
+      group_sync<1, C::WORK>();
+      if (g == 0) wait(full + 2, kqi & 1);
+      if (warp == 0) {
+        tc::fence_after_sync();
+        const uint64_t ap = tc::sdesc_k_sw128(smem_addr(ops)), tp = mn_desc(smem_addr(ops + C::T), C::T),
+                       tm = mn_desc(smem_addr(ops + 2 * C::T), C::T), bk = mn_desc(smem_addr(kq), C::T),
+                       bq = mn_desc(smem_addr(kq + C::ATOMS * C::T), C::T);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t lo = pl * 3 * C::T, ac = pl + ks > 0 ? 1u : 0u;
+              const uint64_t kd = tc::sdesc_advance(bk, ks * kStepMN), qd = tc::sdesc_advance(bq, ks * kStepMN);
+              tc::mma_bf16(d4, tc::sdesc_advance(ap, lo + ks * kStepK), kd, id_dk | kBmn, ac);
+              tc::mma_bf16(d5, tc::sdesc_advance(tp, lo + ks * kStepMN), qd, id_dk | kAmn | kBmn, ac);
+              tc::mma_bf16(d5, tc::sdesc_advance(tm, lo + ks * kStepMN), kd, id_dk | kAmn | kBmn, 1u);
+            }
+          tc::mma_commit(done + 1);
+        }
+        __syncwarp();
+      }
+      wait(done + 1, heads & 1);
+      tc::fence_after_sync();
+      float d0 = 0.f, e0 = 0.f, u0 = 0.f;  // k.dk or q.dq; k.E; k.dS1 U
+#pragma unroll
+      for (int j = 0; j < NC; j += 16) {
+        const uint32_t o = at + cg * NC + j;
+        float x[16], y[16];
+        ld_cols<16>(d1 + o, x);
+        ld_cols<16>(d4 + o, y);
+        if (lower) {
+          float u[16], p[16];
+          ld_cols<16>(d3 + o, u);
+          ld_cols<16>(d5 + o, p);
+          ld_wait<16>(x);
+          ld_wait<16>(y);
+          ld_wait<16>(u);
+          ld_wait<16>(p);
+#pragma unroll
+          for (int z = 0; z < 16; z += 8) {
+            float kk[8];
+            unpack8(kk, *reinterpret_cast<const uint4*>(krow + chunk_at(i, ch0 + (j + z) / 8)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float en = fmaf(-eg, x[z + e], y[z + e]), us = el * u[z + e], d = fmaf(be, en, us + p[z + e]);
+              e0 = fmaf(kk[e], en, e0);
+              u0 = fmaf(kk[e], us, u0);
+              d0 = fmaf(kk[e], d, d0);
+              acc[j + z + e] = g == 0 ? d : acc[j + z + e] + d;
+            }
+          }
+        } else {
+          ld_wait<16>(x);
+          ld_wait<16>(y);
+#pragma unroll
+          for (int z = 0; z < 16; z += 8) {
+            float qq[8];
+            unpack8(qq, *reinterpret_cast<const uint4*>(qrow + chunk_at(i, ch0 + (j + z) / 8)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float d = fmaf(a.s.scale * eg, x[z + e], y[z + e]);
+              d0 = fmaf(qq[e], d, d0);
+              acc[j + z + e] = g == 0 ? d : acc[j + z + e] + d;
+            }
+          }
+        }
+      }
+      if (lower) {
+        dot[128 + cg * 64 + i] = d0;
+        dot[256 + cg * 64 + i] = e0;
+        dot[384 + cg * 64 + i] = u0;
+      } else {
+        dot[cg * 64 + i] = d0;
+      }
+      const int h = ck.hk * group + g;
+      if (++g == group) {                  // the key head is done: dk, dq leave through K's and Q's tiles
+        g = 0;
+        ++kqi;
+        unsigned char* tile = lower ? krow : qrow;
+#pragma unroll
+        for (int j = 0; j < NC; j += 8) *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8)) = pack8(acc + j);
+        __syncwarp();
+        rows_out<64, NC>((lower ? a.gk : a.gq) + (ck.row0 * a.s.hk + ck.hk) * dk + (DK == 128 ? cg * 64 : 0),
+                         (long long)a.s.hk * dk, tile, i & 32, ch0, ck.rows, dk - (DK == 128 ? cg * 64 : 0), lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + 2);
+      }
+      tc::fence_before_sync();
+      group_sync<1, C::WORK>();
+      if (warp == 7) {
+        // dbeta, and dg: the sums of dG from each row to the chunk's end
+        float dg[2], us = 0.f, tot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 2 * lane + e;
+          const float z = dot[256 + r] + dot[320 + r];
+          const float db = ((drv[r] + drv[64 + r]) + (drv[128 + r] + drv[192 + r])) + z;
+          // beta of row r sits in another lane's register set: recomputed from the vectors
+          const float br = a.vec[(ck.slot * a.s.hv + h) * kVec + kVecBeta + r];
+          dg[e] = (dot[r] + dot[64 + r]) - (dot[128 + r] + dot[192 + r]) + 2.f * br * z;
+          us += dot[384 + r] + dot[448 + r];
+          if (r < ck.rows) a.gbeta[(ck.row0 + r) * a.s.hv + h] = __float2bfloat16_rn(db);
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) us += __shfl_xor_sync(0xffffffffu, us, m);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) tot += sums[m];
+        const float last = fmaf(dec, tot, us);
+        float run = dg[0] + dg[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, run, d);
+          run += lane + d < 32 ? y : 0.f;
+        }
+        const float g0 = run + last, g1 = run - dg[0] + last;
+        if (2 * lane < ck.rows) a.gg[(ck.row0 + 2 * lane) * a.s.hv + h] = __float2bfloat16_rn(g0);
+        if (2 * lane + 1 < ck.rows) a.gg[(ck.row0 + 2 * lane + 1) * a.s.hv + h] = __float2bfloat16_rn(g1);
+      }
+    }
+  }
+  if (lost)                  // copies and products that may still be on their way
+    for (int j = 0; j < 2; ++j) {
+      tc::mbar_wait(full + j, 0, kPolls);
+      tc::mbar_wait(done + j, 0, kPolls);
+    }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DK>
+static cudaError_t launch(const GradArgs& g, cudaStream_t st) {
+  using C = GradCfg<DK>;
+  const long long items = slot_count(g.s.rows, g.s.n_seq) * g.s.hk;
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_grad_tc<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  if (e != cudaSuccess) return e;
+  TraceScope tr("k_gdr_grad_tc", st);
+  k_gdr_grad_tc<DK><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_grad_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
+  GradArgs g{};
+  g.s = a.s;
+  g.q = static_cast<const bf16*>(a.q); g.k = static_cast<const bf16*>(a.k);
+  g.v = static_cast<const bf16*>(a.v); g.go = static_cast<const bf16*>(a.go);
+  g.ldq = a.ldq; g.ldk = a.ldk; g.ldv = a.ldv;
+  g.gq = static_cast<bf16*>(a.gq); g.gk = static_cast<bf16*>(a.gk);
+  g.gg = static_cast<bf16*>(a.gg); g.gbeta = static_cast<bf16*>(a.gbeta);
+  g.s0 = reinterpret_cast<const unsigned char*>(a.s0); g.u = reinterpret_cast<const unsigned char*>(a.u);
+  g.ds = reinterpret_cast<const unsigned char*>(a.ds); g.dr = reinterpret_cast<const unsigned char*>(a.dr);
+  g.vec = a.vec;
+  return dk_tile == 64 ? launch<64>(g, st) : launch<128>(g, st);
+}
+
+int read_gdr_grad_error(int clear) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_gdr_grad_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
+  if (clear && v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_gdr_grad_error, &zero, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
+  }
+  return v;
+}
+
+}  // namespace gdr
+}  // namespace cfc

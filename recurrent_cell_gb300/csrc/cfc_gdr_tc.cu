@@ -22,99 +22,24 @@
 // A product of 128 x 64 x 16 takes about 34 cycles at the tensor peak, 544
 // (PL = 1) a chain and chunk; a chain's latency is those plus three round
 // trips through tensor memory and the arithmetic between them.
-#include "gdr_common.cuh"
+#include "gdr_tc.cuh"
 
 namespace cfc {
 namespace gdr {
 
 __device__ int g_gdr_tc_error = 0;
 
-using bf16 = __nv_bfloat16;
-
-// ------------------------------------------------------------ shared pieces
-// 64-column (128-byte) operand tiles, 128-byte swizzle.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t next_block) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(next_block >> 4) << 16;    // the next 64 columns
-  d |= (uint64_t)(1024u >> 4) << 32;         // the next 8 rows
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-constexpr uint32_t kAmn = 1u << 15, kBmn = 1u << 16;
-constexpr uint32_t kStepK = 32, kStepMN = 2048;    // bytes of 16 along K
-
-__device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
-
-// 32 accumulator columns; two = also the 32 after them, added.
-__device__ __forceinline__ void ld32(uint32_t t, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(t)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-template <int PL>
-__device__ __forceinline__ void ld_sum(uint32_t t, float (&v)[32]) {
-  ld32(t, v);
-  if constexpr (PL == 2) {
-    float w[32];
-    ld32(t + 32, w);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += w[i];
-  }
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-}
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ void unpack8(float* v, const uint4& u) {
-  v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
-  v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
-}
-// Eight values into chunk `ch` of a tile row; PL = 2: their remainders four
-// chunks on (the second 32 columns).
-template <int PL>
-__device__ __forceinline__ void put8(unsigned char* tile, int row, int ch, const float* v) {
-  const uint4 h = pack8(v);
-  *reinterpret_cast<uint4*>(tile + chunk_at(row, ch)) = h;
-  if constexpr (PL == 2) {
-    float hv[8], l[8];
-    unpack8(hv, h);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = v[i] - hv[i];
-    *reinterpret_cast<uint4*>(tile + chunk_at(row, ch + 4)) = pack8(l);
-  }
-}
-
-__device__ __forceinline__ void chain_sync(int chain) {
-  asm volatile("bar.sync %0, 128;" ::"r"(chain + 1) : "memory");
-}
-
-template <int DK, int NV, int PL, int NCH, bool BWD>
+template <int DK, int NV, int PL, int NCH, int CW, bool BWD>
 struct TcCfg {
-  static constexpr int ATOMS = DK / 64, FETCH = 128, THREADS = 128 * NCH + FETCH;
+  static constexpr int ATOMS = DK / 64, FETCH = 128, CHAIN_T = 128 * CW, THREADS = CHAIN_T * NCH + FETCH;
+  static constexpr int NC = NV / CW;                    // columns a thread
   static constexpr uint32_t KQ = ATOMS * 16384u;        // per 64 key columns: 64 rows of K, 64 of Q
   static constexpr uint32_t A2 = PL * 16384u;
   static constexpr uint32_t VT = 64 * NV * 2;           // a chain's V (or dO): 64 rows
   static constexpr uint32_t STAGE = (KQ + A2 + NCH * VT + kVec * 4 + 1023) / 1024 * 1024;
+  // per chain: S; R, then its decayed U; U as it is (PL = 1); backward: dO scaled
   static constexpr uint32_t S = DK * 128u, R = 8192u;
-  static constexpr uint32_t CHAIN = S + R + (BWD ? R : 0);
+  static constexpr uint32_t CHAIN = S + (PL == 1 ? 2 : 1) * R + (BWD ? R : 0);
   static constexpr uint32_t BYTES = 2048 + 2 * STAGE + NCH * CHAIN;
   static constexpr uint32_t TMEM = NCH * 128;           // D1 / D2 and D3, 64 columns each
   static_assert(BYTES <= 227u * 1024u, "shared memory");
@@ -129,7 +54,8 @@ struct TcArgs {
   bf16* o;                      // the backward's grad_v
   const unsigned char* a2;
   const float* vec;
-  bf16 *st, *u;                 // per chunk: S0 [d_k, d_v], U [64, d_v] (backward: dS1, dR), or NULL
+  // per chunk and 64 value columns, as operand tiles: S0 and U (backward: dS1, dR), or NULL
+  unsigned char *st, *u;
   int ntile;
 };
 
@@ -175,8 +101,7 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
 #pragma unroll 4
       for (int r = rr; r < kC; r += STEP) {
         const bool on = in && r < rows;
-        const uint32_t at = NV == 64 ? chunk_at(r, cc) : r * 64 + ((cc ^ ((r >> 1) & 3)) << 4);
-        cp16(d + at, on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
+        cp16(d + v_at<NV>(r, cc), on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
       }
     }
     cp_commit();
@@ -187,10 +112,11 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
 }
 
 // ------------------------------------------------------------------- forward
-template <int DK, int NV, int PL, int NCH>
-__global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_scan_tc(TcArgs a) {
+template <int DK, int NV, int PL, int NCH, int CW>
+__global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a) {
+  using C = TcCfg<DK, NV, PL, NCH, CW, false>;
+  constexpr int NC = C::NC;
   extern __shared__ unsigned char smem_raw[];
-  using C = TcCfg<DK, NV, PL, NCH, false>;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4;
@@ -208,7 +134,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH);
+      tc::mbar_init(empty + i, NCH * (1 + 2 * CW));     // a chain: its last product, the warps that leave rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -226,17 +152,19 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
     }
   };
 
-  if (tid >= 128 * NCH) {
-    fetch_chunks<DK, NV, PL, NCH, C>(a, stage, full, empty, tid - 128 * NCH, h, start, len, slot0, tile * NCH * NV,
-                                     false, wait);
+  if (tid >= C::CHAIN_T * NCH) {
+    fetch_chunks<DK, NV, PL, NCH, C>(a, stage, full, empty, tid - C::CHAIN_T * NCH, h, start, len, slot0,
+                                     tile * NCH * NV, false, wait);
   } else {
-    const int chain = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-    const int v0 = (tile * NCH + chain) * NV, dk = a.s.dk, dv = a.s.dv;
+    const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
+    const int v0 = (tile * NCH + chain) * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
     const bool token = quad < 2;             // rows of K; else rows of Q
+    const bool issuer = quad == 0 && cg == 0;
     const int i = row & 63;                  // the row's token
     unsigned char* stile = stage + 2 * C::STAGE + chain * C::CHAIN;
     unsigned char* rtile = stile + C::S;
-    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, lanes = (uint32_t)(quad * 32) << 16;
+    unsigned char* utile = rtile + C::R;
+    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, at = ((uint32_t)(quad * 32) << 16) + c0;
     const uint32_t id_kq = tc::idesc(128, 64, tc::kFmtBF16) | kBmn;
     const uint32_t id_lo = tc::idesc(128, 32, tc::kFmtBF16) | kBmn;
     const uint32_t id_kt = tc::idesc(128, 64, tc::kFmtBF16) | kAmn | kBmn;
@@ -244,35 +172,30 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
     uint32_t phase = 0;
     const long long ldo = (long long)a.s.hv * dv;
     const bool srow = row < dk && row < DK;
-    float s[NV];
+    float s[NC];
 #pragma unroll
-    for (int j = 0; j < NV; j += 4) {
+    for (int j = 0; j < NC; j += 4) {
+      const int col = v0 + c0 + j;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.init && srow && v0 + j < dv) x = *reinterpret_cast<const float4*>(a.init + (sh * dk + row) * dv + v0 + j);
+      if (a.init && srow && col < dv) x = *reinterpret_cast<const float4*>(a.init + (sh * dk + row) * dv + col);
       s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
     }
     for (int c = 0; c < nc; ++c) {
       const int st = c & 1;
       unsigned char* b = stage + st * C::STAGE;
-      const unsigned char* vt = b + C::KQ + C::A2 + chain * C::VT;
+      unsigned char* vt = b + C::KQ + C::A2 + chain * C::VT;
       const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + NCH * C::VT);
       const int rows = min(kC, len - c * kC);
-      const long long id = (slot0 + c) * a.s.hv + h;
+      const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
-        for (int j = 0; j < NV; j += 8) put8<PL>(stile, row, j / 8, s + j);
-        if (a.st && srow) {
-          bf16* p = a.st + (id * dk + row) * dv + v0;
-#pragma unroll
-          for (int j = 0; j < NV; j += 8)
-            if (v0 + j < dv) *reinterpret_cast<uint4*>(p + j) = pack8(s + j);
-        }
+        for (int j = 0; j < NC; j += 8) put8<PL>(stile, row, (c0 + j) / 8, s + j);
       }
       wait(full + st, (c >> 1) & 1);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b));
         if (tc::elect_one()) {
@@ -281,41 +204,46 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
             tc::mma_bf16(d12, tc::sdesc_advance(ad, (ks >> 2) * 16384 + (ks & 3) * kStepK),
                          tc::sdesc_advance(bs, ks * kStepMN), id_kq, ks > 0);
           tc::mma_commit(done + chain);
+          if (PL == 1 && a.st && v0 < dv) bulk_store(a.st + img * C::S, stile, C::S);
         }
         __syncwarp();
       }
+      if (PL == 2 && a.st && row < DK && v0 < dv)      // half a tile: the chain's 32 columns
+#pragma unroll
+        for (int j = 0; j < NC; j += 8)
+          *reinterpret_cast<uint4*>(a.st + img * C::S + chunk_at(row, ((v0 & 63) + c0 + j) / 8)) = pack8(s + j);
       const float eg = vec[kVecEG + i], be = vec[kVecBeta + i], el = vec[kVecEGL + i], dec = vec[kVecD];
+      float r[NC];                     // beta V; then R; in the rows of Q, O
+      if (token) {
+#pragma unroll
+        for (int j = 0; j < NC; j += 8) {
+          unpack8(r + j, *reinterpret_cast<const uint4*>(vt + v_at<NV>(i, (c0 + j) / 8)));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[j + e] *= be;
+        }
+      }
+      const float f = token ? -be * eg : a.s.scale * eg;
       wait(done + chain, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      float r[NV];                     // R; in the rows of Q, O
-#pragma unroll
-      for (int hf = 0; hf < NV / 32; ++hf) {
-        float x[32];
-        ld_sum<PL>(d12 + lanes + hf * 32, x);
+      {
+        float x[NC];
+        ld_sum<NC, PL>(d12 + at, x);
         if (token) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            const int ch = hf * 4 + j / 8;
-            float vv[8];
-            unpack8(vv, *reinterpret_cast<const uint4*>(vt + (NV == 64 ? chunk_at(i, ch)
-                                                                        : i * 64 + ((ch ^ ((i >> 1) & 3)) << 4))));
+          for (int j = 0; j < NC; ++j) r[j] = fmaf(f, x[j], r[j]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[hf * 32 + j + e] = be * (vv[e] - eg * x[j + e]);
-          }
+          for (int j = 0; j < NC; j += 8) put8<PL>(rtile, i, (c0 + j) / 8, r + j);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[hf * 32 + j] = a.s.scale * eg * x[j];
+          for (int j = 0; j < NC; ++j) r[j] = f * x[j];
         }
       }
-      if (token) {
-#pragma unroll
-        for (int j = 0; j < NV; j += 8) put8<PL>(rtile, i, j / 8, r + j);
-      }
+      if (PL == 1 && issuer) bulk_store_read();      // S and the last chunk's U have left their tiles
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b + C::KQ));
         if (tc::elect_one()) {
@@ -335,26 +263,30 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
       wait(done + chain, phase);
       phase ^= 1;
       tc::fence_after_sync();
+      {
+        float x[NC];
+        ld_sum<NC, PL>(d12 + at, x);
 #pragma unroll
-      for (int hf = 0; hf < NV / 32; ++hf) {
-        float x[32];
-        ld_sum<PL>(d12 + lanes + hf * 32, x);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[hf * 32 + j] += x[j];
+        for (int j = 0; j < NC; ++j) r[j] += x[j];
       }
       if (token) {
-        float w[8];
 #pragma unroll
-        for (int j = 0; j < NV; j += 8) {
+        for (int j = 0; j < NC; j += 8) {
+          float w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = el * r[j + e];
-          put8<PL>(rtile, i, j / 8, w);
+          put8<PL>(rtile, i, (c0 + j) / 8, w);
+          if (a.u) {
+            if constexpr (PL == 1) put8<1>(utile, i, (c0 + j) / 8, r + j);
+            else if (v0 < dv)
+              *reinterpret_cast<uint4*>(a.u + img * C::R + chunk_at(i, ((v0 & 63) + c0 + j) / 8)) = pack8(r + j);
+          }
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = mn_desc(smem_addr(b), DK == 128 ? 16384 : 8192);   // DK = 64: rows 64.. unused
         if (tc::elect_one()) {
@@ -363,41 +295,39 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
             tc::mma_bf16(d3, tc::sdesc_advance(ad, ks * kStepMN), tc::sdesc_advance(br, ks * kStepMN), id_kt, ks > 0);
           tc::mma_commit(done + chain);
           tc::mma_commit(empty + st);
+          if (PL == 1 && a.u && v0 < dv) bulk_store(a.u + img * C::R, utile, C::R);
         }
         __syncwarp();
       }
-      // While it runs: the outputs, and U for the backward.
-      if (token) {
-        if (a.u) {
-          bf16* p = a.u + (id * kC + i) * dv + v0;
+      // While it runs, the outputs leave through V's tile, which has been read.
+      if (!token) {
 #pragma unroll
-          for (int j = 0; j < NV; j += 8)
-            if (v0 + j < dv) *reinterpret_cast<uint4*>(p + j) = pack8(r + j);
-        }
-      } else if (i < rows) {
-        bf16* p = a.o + (start + (long long)c * kC + i) * ldo + (long long)h * dv + v0;
-#pragma unroll
-        for (int j = 0; j < NV; j += 8)
-          if (v0 + j < dv) *reinterpret_cast<uint4*>(p + j) = pack8(r + j);
+        for (int j = 0; j < NC; j += 8)
+          *reinterpret_cast<uint4*>(vt + v_at<NV>(i, (c0 + j) / 8)) = pack8(r + j);
+        __syncwarp();
+        rows_out<NV, NC>(a.o + (start + (long long)c * kC) * ldo + (long long)h * dv + v0, ldo, vt, i & 32, c0 / 8, rows,
+                         dv - v0, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + st);
       }
       wait(done + chain, phase);
       phase ^= 1;
       tc::fence_after_sync();
+      {
+        float x[NC];
+        ld_sum<NC, PL>(d3 + at, x);
 #pragma unroll
-      for (int hf = 0; hf < NV / 32; ++hf) {
-        float x[32];
-        ld_sum<PL>(d3 + lanes + hf * 32, x);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[hf * 32 + j] = fmaf(dec, s[hf * 32 + j], x[j]);
+        for (int j = 0; j < NC; ++j) s[j] = fmaf(dec, s[j], x[j]);
       }
     }
     if (a.final_state && srow) {
 #pragma unroll
-      for (int j = 0; j < NV; j += 4)
-        if (v0 + j < dv)
-          *reinterpret_cast<float4*>(a.final_state + (sh * dk + row) * dv + v0 + j) =
+      for (int j = 0; j < NC; j += 4)
+        if (v0 + c0 + j < dv)
+          *reinterpret_cast<float4*>(a.final_state + (sh * dk + row) * dv + v0 + c0 + j) =
               make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
     }
+    if (issuer) bulk_store_done();
   }
   if (lost)                  // copies and products that may still be on their way
     for (int j = 0; j < 2; ++j) {
@@ -419,10 +349,11 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, false>::THREADS) k_gdr_
 //   D3 = Q^T (scale exp(G) dO) - K^T (beta exp(G) dR),  dS0 = exp(G_C) dS1 + D3.
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
-template <int DK, int NV, int NCH>
-__global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a) {
+template <int DK, int NV, int NCH, int CW>
+__global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a) {
+  using C = TcCfg<DK, NV, 1, NCH, CW, true>;
+  constexpr int NC = C::NC;
   extern __shared__ unsigned char smem_raw[];
-  using C = TcCfg<DK, NV, 1, NCH, true>;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4;
@@ -440,7 +371,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH);
+      tc::mbar_init(empty + i, NCH * (1 + 2 * CW));     // a chain: its last product, the warps that leave rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -450,7 +381,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_at;
-  bool lost = false;
+  bool lost = false;        // a wait gave up: no more waiting, the results are void
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!lost && !tc::mbar_wait(bar, parity, kPolls)) {
       lost = true;
@@ -458,66 +389,63 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
     }
   };
 
-  if (tid >= 128 * NCH) {
-    fetch_chunks<DK, NV, 1, NCH, C>(a, stage, full, empty, tid - 128 * NCH, h, start, len, slot0, tile * NCH * NV, true,
-                                    wait);
+  if (tid >= C::CHAIN_T * NCH) {
+    fetch_chunks<DK, NV, 1, NCH, C>(a, stage, full, empty, tid - C::CHAIN_T * NCH, h, start, len, slot0,
+                                    tile * NCH * NV, true, wait);
   } else {
-    const int chain = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-    const int v0 = (tile * NCH + chain) * NV, dk = a.s.dk, dv = a.s.dv;
-    const bool token = quad < 2;
-    const int i = row & 63;
+    const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
+    const int v0 = (tile * NCH + chain) * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
+    const bool token = quad < 2;             // rows of K; else rows of Q
+    const bool issuer = quad == 0 && cg == 0;
+    const int i = row & 63;                  // the row's token
     unsigned char* stile = stage + 2 * C::STAGE + chain * C::CHAIN;
-    unsigned char* xtile = stile + C::S;
-    unsigned char* otile = xtile + C::R;
-    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, lanes = (uint32_t)(quad * 32) << 16;
+    unsigned char* rtile = stile + C::S;
+    unsigned char* utile = rtile + C::R;
+    unsigned char* otile = utile + C::R;
+    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, at = ((uint32_t)(quad * 32) << 16) + c0;
     const uint32_t id_k = tc::idesc(128, 64, tc::kFmtBF16) | kBmn;
     const uint32_t id_t = tc::idesc(128, 64, tc::kFmtBF16) | kAmn | kBmn;
-    const uint64_t bs = mn_desc(smem_addr(stile), 8192), bx = mn_desc(smem_addr(xtile), 8192),
+    const uint64_t bs = mn_desc(smem_addr(stile), 8192), bx = mn_desc(smem_addr(rtile), 8192),
                    bo = mn_desc(smem_addr(otile), 8192);
     uint32_t phase = 0;
     const long long ldo = (long long)a.s.hv * dv;
     const bool srow = row < dk && row < DK;
-    float s[NV];
+    float s[NC];
 #pragma unroll
-    for (int j = 0; j < NV; j += 4) {
+    for (int j = 0; j < NC; j += 4) {
+      const int col = v0 + c0 + j;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.init && srow && v0 + j < dv) x = *reinterpret_cast<const float4*>(a.init + (sh * dk + row) * dv + v0 + j);
+      if (a.init && srow && col < dv) x = *reinterpret_cast<const float4*>(a.init + (sh * dk + row) * dv + col);
       s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
     }
     for (int it = 0; it < nc; ++it) {
       const int c = nc - 1 - it, st = it & 1;
       unsigned char* b = stage + st * C::STAGE;
-      const unsigned char* dot = b + C::KQ + C::A2 + chain * C::VT;
+      unsigned char* dot = b + C::KQ + C::A2 + chain * C::VT;
       const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + NCH * C::VT);
       const int rows = min(kC, len - c * kC);
-      const long long id = (slot0 + c) * a.s.hv + h;
+      const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
-        for (int j = 0; j < NV; j += 8) put8<1>(stile, row, j / 8, s + j);
-        if (srow) {
-          bf16* p = a.st + (id * dk + row) * dv + v0;
-#pragma unroll
-          for (int j = 0; j < NV; j += 8)
-            if (v0 + j < dv) *reinterpret_cast<uint4*>(p + j) = pack8(s + j);
-        }
+        for (int j = 0; j < NC; j += 8) put8<1>(stile, row, (c0 + j) / 8, s + j);
       }
       wait(full + st, (it >> 1) & 1);
       const float eg = vec[kVecEG + i], be = vec[kVecBeta + i], el = vec[kVecEGL + i], dec = vec[kVecD];
       if (!token) {
         const float f = a.s.scale * eg;
 #pragma unroll
-        for (int j = 0; j < NV / 8; ++j) {
+        for (int j = 0; j < NC; j += 8) {
           float w[8];
-          unpack8(w, *reinterpret_cast<const uint4*>(dot + chunk_at(i, j)));
+          unpack8(w, *reinterpret_cast<const uint4*>(dot + v_at<NV>(i, (c0 + j) / 8)));
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] *= f;
-          put8<1>(otile, i, j, w);
+          put8<1>(otile, i, (c0 + j) / 8, w);
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b));
         const uint64_t aq = mn_desc(smem_addr(b + 8192), DK == 128 ? 16384 : 8192);
@@ -530,36 +458,34 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d3, tc::sdesc_advance(aq, ks * kStepMN), tc::sdesc_advance(bo, ks * kStepMN), id_t, ks > 0);
+          if (v0 < dv) bulk_store(a.st + img * C::S, stile, C::S);
         }
         __syncwarp();
       }
       wait(done + chain, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      float r[NV];
+      float r[NC];
       if (token) {
+        ld_sum<NC, 1>(d12 + at, r);
 #pragma unroll
-        for (int hf = 0; hf < NV / 32; ++hf) {
-          float x[32];
-          ld32(d12 + lanes + hf * 32, x);
+        for (int j = 0; j < NC; ++j) r[j] *= el;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[hf * 32 + j] = el * x[j];
-        }
-#pragma unroll
-        for (int j = 0; j < NV; j += 8) put8<1>(xtile, i, j / 8, r + j);
+        for (int j = 0; j < NC; j += 8) put8<1>(rtile, i, (c0 + j) / 8, r + j);
       }
+      if (issuer) bulk_store_read();      // dS1 and the last chunk's dR have left their tiles
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         // transposed: columns of T - I, then of P T (the block after each is not used)
-        const uint64_t at = mn_desc(smem_addr(b + C::KQ), 8192), ap = mn_desc(smem_addr(b + C::KQ + 8192), 8192);
+        const uint64_t at_ = mn_desc(smem_addr(b + C::KQ), 8192), ap = mn_desc(smem_addr(b + C::KQ + 8192), 8192);
         const uint64_t bd = mn_desc(smem_addr(dot), 8192);
         if (tc::elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_bf16(d12, tc::sdesc_advance(at, ks * kStepMN), tc::sdesc_advance(bx, ks * kStepMN), id_t, ks > 0);
+            tc::mma_bf16(d12, tc::sdesc_advance(at_, ks * kStepMN), tc::sdesc_advance(bx, ks * kStepMN), id_t, ks > 0);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d12, tc::sdesc_advance(ap, ks * kStepMN), tc::sdesc_advance(bd, ks * kStepMN), id_t, 1u);
@@ -571,26 +497,24 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
       phase ^= 1;
       tc::fence_after_sync();
       if (token) {
+        float x[NC];
+        ld_sum<NC, 1>(d12 + at, x);
 #pragma unroll
-        for (int hf = 0; hf < NV / 32; ++hf) {
-          float x[32];
-          ld32(d12 + lanes + hf * 32, x);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[hf * 32 + j] += x[j];
-        }
+        for (int j = 0; j < NC; ++j) r[j] += x[j];
         const float f = -be * eg;
 #pragma unroll
-        for (int j = 0; j < NV; j += 8) {
+        for (int j = 0; j < NC; j += 8) {
           float w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = f * r[j + e];
-          put8<1>(xtile, i, j / 8, w);
+          put8<1>(rtile, i, (c0 + j) / 8, w);
+          put8<1>(utile, i, (c0 + j) / 8, r + j);
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync(chain);
-      if (quad == 0) {
+      chain_sync<C::CHAIN_T>(chain);
+      if (issuer) {
         tc::fence_after_sync();
         const uint64_t ak = mn_desc(smem_addr(b), DK == 128 ? 16384 : 8192);
         if (tc::elect_one()) {
@@ -599,44 +523,45 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
             tc::mma_bf16(d3, tc::sdesc_advance(ak, ks * kStepMN), tc::sdesc_advance(bx, ks * kStepMN), id_t, 1u);
           tc::mma_commit(done + chain);
           tc::mma_commit(empty + st);
+          if (v0 < dv) bulk_store(a.u + img * C::R, utile, C::R);
         }
         __syncwarp();
       }
+      // While it runs, dv leaves through dO's tile, which the products have read.
       if (token) {
-        bf16* p = a.u + (id * kC + i) * dv + v0;
-        bf16* gv = a.o + (start + (long long)c * kC + i) * ldo + (long long)h * dv + v0;
 #pragma unroll
-        for (int j = 0; j < NV; j += 8)
-          if (v0 + j < dv) {
-            *reinterpret_cast<uint4*>(p + j) = pack8(r + j);
-            if (i < rows) {
-              float w[8];
+        for (int j = 0; j < NC; j += 8) {
+          float w[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = be * r[j + e];
-              *reinterpret_cast<uint4*>(gv + j) = pack8(w);
-            }
-          }
+          for (int e = 0; e < 8; ++e) w[e] = be * r[j + e];
+          *reinterpret_cast<uint4*>(dot + v_at<NV>(i, (c0 + j) / 8)) = pack8(w);
+        }
+        __syncwarp();
+        rows_out<NV, NC>(a.o + (start + (long long)c * kC) * ldo + (long long)h * dv + v0, ldo, dot, i & 32, c0 / 8, rows,
+                         dv - v0, lane);
+        __syncwarp();
+        if (lane == 0) bar_arrive(empty + st);
       }
       wait(done + chain, phase);
       phase ^= 1;
       tc::fence_after_sync();
+      {
+        float x[NC];
+        ld_sum<NC, 1>(d3 + at, x);
 #pragma unroll
-      for (int hf = 0; hf < NV / 32; ++hf) {
-        float x[32];
-        ld32(d3 + lanes + hf * 32, x);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[hf * 32 + j] = fmaf(dec, s[hf * 32 + j], x[j]);
+        for (int j = 0; j < NC; ++j) s[j] = fmaf(dec, s[j], x[j]);
       }
     }
     if (a.final_state && srow) {
 #pragma unroll
-      for (int j = 0; j < NV; j += 4)
-        if (v0 + j < dv)
-          *reinterpret_cast<float4*>(a.final_state + (sh * dk + row) * dv + v0 + j) =
+      for (int j = 0; j < NC; j += 4)
+        if (v0 + c0 + j < dv)
+          *reinterpret_cast<float4*>(a.final_state + (sh * dk + row) * dv + v0 + c0 + j) =
               make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
     }
+    if (issuer) bulk_store_done();
   }
-  if (lost)
+  if (lost)                  // copies and products that may still be on their way
     for (int j = 0; j < 2; ++j) {
       tc::mbar_wait(full + j, 0, kPolls);
       tc::mbar_wait(done + j, 0, kPolls);
@@ -650,26 +575,28 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, true>::THREADS) k_gdr_sc
 }
 
 // ------------------------------------------------------------------- launches
-template <int DK, int NV, int PL, int NCH>
+template <int DK, int NV, int PL, int NCH, int CW>
 static cudaError_t scan(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, NV, PL, NCH, false>;
+  using C = TcCfg<DK, NV, PL, NCH, CW, false>;
   a.ntile = (a.s.dv + NCH * NV - 1) / (NCH * NV);
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, NV, PL, NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, NV, PL, NCH, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_tc", st);
-  k_gdr_scan_tc<DK, NV, PL, NCH><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_tc<DK, NV, PL, NCH, CW>
+      <<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
-template <int DK, int NV, int NCH>
+template <int DK, int NV, int NCH, int CW>
 static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, NV, 1, NCH, true>;
+  using C = TcCfg<DK, NV, 1, NCH, CW, true>;
   a.ntile = (a.s.dv + NCH * NV - 1) / (NCH * NV);
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NV, NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NV, NCH, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_bwd_tc", st);
-  k_gdr_scan_bwd_tc<DK, NV, NCH><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_bwd_tc<DK, NV, NCH, CW>
+      <<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -677,17 +604,17 @@ template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
   if (planes == 2) {
-    if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2>(t, st);
-    return scan<DK, 32, 2, 1>(t, st);
+    if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2, 2>(t, st);
+    return scan<DK, 32, 2, 1, 2>(t, st);
   }
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan<DK, 64, 1, 2>(t, st);
-  return scan<DK, 64, 1, 1>(t, st);
+  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan<DK, 64, 1, 2, 2>(t, st);
+  return scan<DK, 64, 1, 1, 2>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2>(t, st);
-  return scan_bwd<DK, 64, 1>(t, st);
+  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2, 2>(t, st);
+  return scan_bwd<DK, 64, 1, 2>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {
@@ -698,7 +625,7 @@ cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
   t.init = a.init; t.final_state = a.final_state; t.o = static_cast<bf16*>(a.o);
   t.a2 = reinterpret_cast<const unsigned char*>(a.t);
   t.vec = a.vec;
-  if (a.save) { t.st = reinterpret_cast<bf16*>(a.s0); t.u = reinterpret_cast<bf16*>(a.u); }
+  if (a.save) { t.st = reinterpret_cast<unsigned char*>(a.s0); t.u = reinterpret_cast<unsigned char*>(a.u); }
   return dk_tile == 64 ? scan_by_size<64>(t, planes, st) : scan_by_size<128>(t, planes, st);
 }
 
@@ -710,7 +637,7 @@ cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
   t.init = a.gfinal; t.final_state = a.ginit; t.o = static_cast<bf16*>(a.gv);
   t.a2 = reinterpret_cast<const unsigned char*>(a.t);
   t.vec = a.vec;
-  t.st = reinterpret_cast<bf16*>(a.ds); t.u = reinterpret_cast<bf16*>(a.dr);
+  t.st = reinterpret_cast<unsigned char*>(a.ds); t.u = reinterpret_cast<unsigned char*>(a.dr);
   return dk_tile == 64 ? scan_bwd_by_size<64>(t, st) : scan_bwd_by_size<128>(t, st);
 }
 
