@@ -33,7 +33,7 @@ struct PrepSmem {
   static constexpr bool TC = P::kMode == CFC_MATH_BF16;
   static constexpr size_t kQ = TC ? kA : kP;             // fp32 P where P T is to be formed
   static constexpr size_t kOffG = kOffQ + (kTile > kQ ? kTile : kQ);
-  static constexpr size_t kBytes = kOffG + 3 * kC * sizeof(float);
+  static constexpr size_t kBytes = kOffG + 3 * kC * sizeof(float);      // G / ln 2 in pairs, beta
 };
 
 
@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   float* am = reinterpret_cast<float*>(smem_raw);
   E* ps = qs;
   float* pm = reinterpret_cast<float*>(smem_raw + S::kOffQ);
-  float* ghi = reinterpret_cast<float*>(smem_raw + S::kOffG);
-  float *glo = ghi + kC, *bet = glo + kC;
+  float2* g2 = reinterpret_cast<float2*>(smem_raw + S::kOffG);
+  float* bet = reinterpret_cast<float*>(g2 + kC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.x % a.s.hv;
   const long long slot = blockIdx.x / a.s.hv;
@@ -91,14 +91,13 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 2 * lane + i;
-      const float hi = (float)G[i], lo = (float)(G[i] - (double)hi);
-      ghi[r] = hi;
-      glo[r] = lo;
+      const double u = G[i] * 1.4426950408889634074;      // / ln 2
+      const float hi = (float)u, lo = (float)(u - (double)hi);
+      g2[r] = make_float2(hi, lo);
       vec[kVecEG + r] = expf((float)G[i]);
       vec[kVecEGL + r] = expf((float)(total - G[i]));
       vec[kVecBeta + r] = bet[r];
-      vec[kVecGHi + r] = hi;
-      vec[kVecGLo + r] = lo;
+      reinterpret_cast<float2*>(vec + kVecG2)[r] = make_float2(hi, lo);
     }
     if (lane == 0) vec[kVecD] = expf((float)total);
   }
@@ -129,13 +128,13 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
     const int i = m0 + g + rr * 8;
-    const float hi = ghi[i], lo = glo[i], be = bet[i];
+    const float2 gi = g2[i];
+    const float be = bet[i];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = j * 8 + t2;
-      const float2 h2 = *reinterpret_cast<const float2*>(ghi + col), l2 = *reinterpret_cast<const float2*>(glo + col);
-      const float l0 = col <= i ? expf((hi - h2.x) + (lo - l2.x)) : 0.f;
-      const float l1 = col < i ? expf((hi - h2.y) + (lo - l2.y)) : 0.f;
+      const float4 gj = *reinterpret_cast<const float4*>(g2 + col);
+      const float l0 = P::exp2((gi.x - gj.x) + (gi.y - gj.y)), l1 = P::exp2((gi.x - gj.z) + (gi.y - gj.w));
       const float p0 = col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f,
                   p1 = col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f;
       if constexpr (S::TC) *reinterpret_cast<float2*>(pm + i * S::LDA + col) = make_float2(p0, p1);

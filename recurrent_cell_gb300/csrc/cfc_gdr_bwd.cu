@@ -397,9 +397,9 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       float dp[2], da[2];
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        float l = 0.f;
-        if (col + cc <= i)
-          l = expf((vec[kVecGHi + i] - vec[kVecGHi + col + cc]) + (vec[kVecGLo + i] - vec[kVecGLo + col + cc]));
+        const float2 gi = reinterpret_cast<const float2*>(vec + kVecG2)[i],
+                     gj = reinterpret_cast<const float2*>(vec + kVecG2)[col + cc];
+        const float l = P::exp2((gi.x - gj.x) + (gi.y - gj.y));
         dp[cc] = col + cc <= i ? a.s.scale * l * ap[j][2 * rr + cc] : 0.f;
         da[cc] = col + cc < i ? -l * aa[j][2 * rr + cc] : 0.f;
       }

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(full + i, C::FETCH + (i < 2 ? 1 : 0));
-      tc::mbar_init(empty + i, C::WORK / 32 + (i < 2 ? 1 : 0));
+      tc::mbar_init(empty + i, C::WORK / 32 + (i < 2 ? 1 : 0));        // K and Q: dk and dq lie in their place
     }
     tc::mbar_init(done, 1);
     tc::mbar_init(done + 1, 1);
@@ -115,6 +115,20 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       pending = bar;
     };
     uint32_t it = 0, kqi = 0;
+    Chunk last{};
+    // dk and dq of the chunk before, from K's and Q's tiles
+    auto rows_of = [&](const Chunk& c) {
+      flush();
+      wait(empty + 2, (kqi - 1) & 1);
+      const int w = ft >> 5, r0 = (w & 1) * 32;
+      const bool q = w >= 2;
+#pragma unroll
+      for (int b = 0; b < C::ATOMS; ++b)
+        rows_out<64, 64>((q ? a.gq : a.gk) + (c.row0 * a.s.hk + c.hk) * dk + b * 64, (long long)a.s.hk * dk,
+                         kq + (q ? C::ATOMS + b : b) * C::T, r0, 0, c.rows, dk - b * 64, lane);
+      // the tiles are filled again by other threads
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+    };
     const long long ldo = (long long)a.s.hv * dv;
     const long long items = slot_count(a.s.rows, a.s.n_seq) * a.s.hk;
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
@@ -152,7 +166,9 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
           issued(full + st);
         }
         if (g == 0) {
-          claim(2, kqi++);
+          if (kqi > 0) rows_of(last);
+          ++kqi;
+          last = Chunk{row0, slot, rows, hk};
           const bf16 *k = a.k + row0 * a.ldk + (long long)hk * dk, *q = a.q + row0 * a.ldq + (long long)hk * dk;
           constexpr int PER = DK / 8;
           const int ch = ft % PER;
@@ -168,6 +184,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       }
     }
     flush();
+    if (kqi > 0) rows_of(last);
     claim(it & 1, it >> 1);
     if (ft == 0) {
       reinterpret_cast<Chunk*>(stage + (it & 1) * C::STAGE + C::OFF_VEC + kVec * 4)->rows = -1;
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       if (ck.rows < 0 || lost) break;
       const float* vec = reinterpret_cast<const float*>(stage + (it & 1) * C::STAGE + C::OFF_VEC);
       const float eg = vec[kVecEG + i], el = vec[kVecEGL + i], be = vec[kVecBeta + i], dec = vec[kVecD];
-      if (tid < 128) gs[tid] = vec[kVecGHi + tid];          // G as two floats
+      if (tid < 128) gs[tid] = vec[kVecG2 + tid];
       float ss = 0.f, dr = 0.f;
       for (int t = 0; t < nt; ++t, ++it) {
         const int st = it & 1;
@@ -248,16 +265,20 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       {
         float x[32];
         ld_sum<32, 1>(d2 + at + cg * 32, x);
-        const float hi = gs[i], lo = gs[64 + i], f = lower ? -1.f : a.s.scale;
-        const bool any = cg * 32 <= i;
+        const float2 gi = reinterpret_cast<const float2*>(gs)[i];
+        const float f = lower ? -1.f : a.s.scale;
+        const int end = cg * 32 <= i ? (lower ? i : i + 1) : 0;    // columns that count
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < 8; e += 2) {
             const int col = cg * 32 + j + e;
-            const bool in = lower ? col < i : col <= i;
-            w[e] = any && in ? f * x[j + e] * __expf((hi - gs[col]) + (lo - gs[64 + col])) : 0.f;
+            const float4 gj = *reinterpret_cast<const float4*>(gs + 2 * col);
+            const float w0 = f * x[j + e] * MBf16::exp2((gi.x - gj.x) + (gi.y - gj.y));
+            const float w1 = f * x[j + e + 1] * MBf16::exp2((gi.x - gj.z) + (gi.y - gj.w));
+            w[e] = col < end ? w0 : 0.f;
+            w[e + 1] = col + 1 < end ? w1 : 0.f;
           }
           unsigned char* to = ops + (lower ? 0 : C::T);
           const uint32_t o = chunk_at(i, cg * 4 + j / 8);
@@ -356,15 +377,13 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
         dot[cg * 64 + i] = d0;
       }
       const int h = ck.hk * group + g;
-      if (++g == group) {                  // the key head is done: dk, dq leave through K's and Q's tiles
+      if (++g == group) {                  // the key head is done: dk, dq into K's and Q's tiles, from where
+                                           // the fetching warps take them
         g = 0;
         ++kqi;
         unsigned char* tile = lower ? krow : qrow;
 #pragma unroll
         for (int j = 0; j < NC; j += 8) *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8)) = pack8(acc + j);
-        __syncwarp();
-        rows_out<64, NC>((lower ? a.gk : a.gq) + (ck.row0 * a.s.hk + ck.hk) * dk + (DK == 128 ? cg * 64 : 0),
-                         (long long)a.s.hk * dk, tile, i & 32, ch0, ck.rows, dk - (DK == 128 ? cg * 64 : 0), lane);
         __syncwarp();
         if (lane == 0) bar_arrive(empty + 2);
       }

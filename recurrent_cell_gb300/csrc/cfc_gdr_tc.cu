@@ -22,6 +22,7 @@
 // A product of 128 x 64 x 16 takes about 34 cycles at the tensor peak, 544
 // (PL = 1) a chain and chunk; a chain's latency is those plus three round
 // trips through tensor memory and the arithmetic between them.
+#include <cstdlib>
 #include "gdr_tc.cuh"
 
 namespace cfc {
@@ -59,21 +60,37 @@ struct TcArgs {
   int ntile;
 };
 
-// The next chunk's tiles: the fetching threads with 16-byte copies (rows past the end and
+// The fetching warps' loop.  The chunk before last's output rows (o, or the
+// backward's dv), which lie in the place of its V (dO), go to global memory;
+// then the next chunk's tiles come into that stage: the fetching threads with 16-byte copies (rows past the end and
 // columns past d_k, d_v as zeros) and the prepared images by bulk copy.
 template <int DK, int NV, int PL, int NCH, class C, class W>
 __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* stage, uint64_t* full, uint64_t* empty,
-                                             int ft, int h, long long start, int len, long long slot0, int v0,
-                                             bool backwards, W wait) {
+                                             uint64_t* outs, int ft, int h, long long start, int len, long long slot0,
+                                             int v0, bool backwards, W wait) {
   const int hq = h / (a.s.hv / a.s.hk), dk = a.s.dk, nc = (len + kC - 1) / kC;
   const bf16* q = a.q + start * a.ldq + (long long)hq * dk;
   const bf16* k = a.k + start * a.ldk + (long long)hq * dk;
   const bf16* v = a.v + start * a.ldv + (long long)h * a.s.dv + v0;
   const int vn = a.s.dv - v0;
-  for (int i = 0; i < nc; ++i) {
+  const long long ldo = (long long)a.s.hv * a.s.dv;
+  for (int i = 0; i < nc + 2; ++i) {
     const int c = backwards ? nc - 1 - i : i, st = i & 1;
-    if (i >= 2) wait(empty + st, (i / 2 - 1) & 1);
     unsigned char* b = stage + st * C::STAGE;
+    if (i >= 2 && i - 2 < nc) {
+      const int cl = backwards ? c + 2 : c - 2;
+      bf16* o = a.o + (start + (long long)cl * kC) * ldo + (long long)h * a.s.dv + v0;
+      wait(outs + st, (i / 2 - 1) & 1);
+      // 4 warps: 32 rows by half of the chains' columns each
+      constexpr int HC = NCH * NV / 2, PART = HC < NV ? HC : NV;
+      const int w = ft >> 5, lane = ft & 31;
+      const int col = (w >> 1) * HC, ch = col / NV;
+      rows_out<NV, PART>(o + ch * NV, ldo, b + C::KQ + C::A2 + ch * C::VT, (w & 1) * 32, (col % NV) / 8,
+                         min(kC, len - cl * kC), vn - ch * NV, lane);
+      asm volatile("bar.sync 15, 128;" ::: "memory");       // the tiles are filled again by other threads
+      wait(empty + st, (i / 2 - 1) & 1);
+    }
+    if (i >= nc) continue;
     const int rows = min(kC, len - c * kC);
     const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
     if (ft == 0) {
@@ -119,7 +136,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
-  uint64_t *empty = full + 2, *done = full + 4;
+  uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -134,7 +151,8 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH * (1 + 2 * CW));     // a chain: its last product, the warps that leave rows
+      tc::mbar_init(empty + i, NCH);            // a chain's last product
+      tc::mbar_init(outs + i, NCH * 2 * CW);    // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -153,7 +171,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
   };
 
   if (tid >= C::CHAIN_T * NCH) {
-    fetch_chunks<DK, NV, PL, NCH, C>(a, stage, full, empty, tid - C::CHAIN_T * NCH, h, start, len, slot0,
+    fetch_chunks<DK, NV, PL, NCH, C>(a, stage, full, empty, outs, tid - C::CHAIN_T * NCH, h, start, len, slot0,
                                      tile * NCH * NV, false, wait);
   } else {
     const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
@@ -170,7 +188,6 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
     const uint32_t id_kt = tc::idesc(128, 64, tc::kFmtBF16) | kAmn | kBmn;
     const uint64_t bs = mn_desc(smem_addr(stile), 8192), br = mn_desc(smem_addr(rtile), 8192);
     uint32_t phase = 0;
-    const long long ldo = (long long)a.s.hv * dv;
     const bool srow = row < dk && row < DK;
     float s[NC];
 #pragma unroll
@@ -299,16 +316,13 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
         }
         __syncwarp();
       }
-      // While it runs, the outputs leave through V's tile, which has been read.
+      // While it runs, the outputs into V's tile, which has been read.
       if (!token) {
 #pragma unroll
         for (int j = 0; j < NC; j += 8)
           *reinterpret_cast<uint4*>(vt + v_at<NV>(i, (c0 + j) / 8)) = pack8(r + j);
         __syncwarp();
-        rows_out<NV, NC>(a.o + (start + (long long)c * kC) * ldo + (long long)h * dv + v0, ldo, vt, i & 32, c0 / 8, rows,
-                         dv - v0, lane);
-        __syncwarp();
-        if (lane == 0) bar_arrive(empty + st);
+        if (lane == 0) bar_arrive(outs + st);
       }
       wait(done + chain, phase);
       phase ^= 1;
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
-  uint64_t *empty = full + 2, *done = full + 4;
+  uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -371,7 +385,8 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH * (1 + 2 * CW));     // a chain: its last product, the warps that leave rows
+      tc::mbar_init(empty + i, NCH);            // a chain's last product
+      tc::mbar_init(outs + i, NCH * 2 * CW);    // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
   };
 
   if (tid >= C::CHAIN_T * NCH) {
-    fetch_chunks<DK, NV, 1, NCH, C>(a, stage, full, empty, tid - C::CHAIN_T * NCH, h, start, len, slot0,
+    fetch_chunks<DK, NV, 1, NCH, C>(a, stage, full, empty, outs, tid - C::CHAIN_T * NCH, h, start, len, slot0,
                                     tile * NCH * NV, true, wait);
   } else {
     const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
@@ -408,7 +423,6 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
     const uint64_t bs = mn_desc(smem_addr(stile), 8192), bx = mn_desc(smem_addr(rtile), 8192),
                    bo = mn_desc(smem_addr(otile), 8192);
     uint32_t phase = 0;
-    const long long ldo = (long long)a.s.hv * dv;
     const bool srow = row < dk && row < DK;
     float s[NC];
 #pragma unroll
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
         }
         __syncwarp();
       }
-      // While it runs, dv leaves through dO's tile, which the products have read.
+      // While it runs, dv into dO's tile, which the products have read.
       if (token) {
 #pragma unroll
         for (int j = 0; j < NC; j += 8) {
@@ -537,10 +551,7 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
           *reinterpret_cast<uint4*>(dot + v_at<NV>(i, (c0 + j) / 8)) = pack8(w);
         }
         __syncwarp();
-        rows_out<NV, NC>(a.o + (start + (long long)c * kC) * ldo + (long long)h * dv + v0, ldo, dot, i & 32, c0 / 8, rows,
-                         dv - v0, lane);
-        __syncwarp();
-        if (lane == 0) bar_arrive(empty + st);
+        if (lane == 0) bar_arrive(outs + st);
       }
       wait(done + chain, phase);
       phase ^= 1;
@@ -603,6 +614,14 @@ static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
 template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
+  if (getenv("GDR_CW")) {
+    if (planes == 2) {
+      if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2, 1>(t, st);
+      return scan<DK, 32, 2, 1, 1>(t, st);
+    }
+    if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan<DK, 64, 1, 2, 1>(t, st);
+    return scan<DK, 64, 1, 1, 1>(t, st);
+  }
   if (planes == 2) {
     if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2, 2>(t, st);
     return scan<DK, 32, 2, 1, 2>(t, st);
@@ -613,6 +632,10 @@ static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
+  if (getenv("GDR_CW")) {
+    if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2, 1>(t, st);
+    return scan_bwd<DK, 64, 1, 1>(t, st);
+  }
   if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2, 2>(t, st);
   return scan_bwd<DK, 64, 1, 2>(t, st);
 }

@@ -31,9 +31,10 @@ namespace gdr {
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kMaxDk = 128;     // key width limit: the state's rows stay in one block's registers
 constexpr int kMaxDv = 256;
-// Per chunk and head: exp(G), exp(G_C - G), beta, G as two floats, exp(G_C).
+// Per chunk and head: exp(G), exp(G_C - G), beta, G / ln 2 as pairs of floats
+// hi + lo, exp(G_C).
 constexpr int kVec = 384;
-constexpr int kVecEG = 0, kVecEGL = 64, kVecBeta = 128, kVecGHi = 192, kVecGLo = 256, kVecD = 320;
+constexpr int kVecEG = 0, kVecEGL = 64, kVecBeta = 128, kVecG2 = 192, kVecD = 320;
 
 // Log-decays below this are a zero factor in fp32 all the same
 // (exp(-104) underflows); holding them here keeps -inf out of differences.
@@ -189,6 +190,11 @@ struct MBf16 {
   static constexpr int KS = 16;       // k of one product step
   static constexpr int PAD = 8;       // 16 bytes: rows of an 8x8 block hit different banks
   static constexpr int STAGES = 2;
+  __device__ static __forceinline__ float exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+  }
   template <int PL> struct A { uint32_t r[PL][4]; };
   template <int PL> struct B { uint32_t r[PL][4]; };
 
@@ -288,6 +294,7 @@ struct MFp32 {
   static constexpr int KS = 8;
   static constexpr int PAD = 4;
   static constexpr int STAGES = 1;
+  __device__ static __forceinline__ float exp2(float x) { return exp2f(x); }
   template <int PL> struct A { uint32_t h[4], l[4]; };
   template <int PL> struct B { uint32_t h[4], l[4]; };
 

@@ -123,11 +123,16 @@ template <int NV, int NC>
 __device__ __forceinline__ void rows_out(bf16* dst, long long ld, const unsigned char* tile, int r0, int ch0, int row_end,
                                          int col_end, int lane) {
   constexpr int PC = NC / 8, RP = 32 / PC;
-  const int ch = ch0 + lane % PC;
+  const int ch = ch0 + lane % PC, r = r0 + lane / PC;
+  bf16* p = dst + r * ld + ch * 8;
+  uint4 v[PC];
 #pragma unroll
-  for (int r = r0 + lane / PC; r < r0 + 32; r += RP)
-    if (r < row_end && ch * 8 < col_end)
-      *reinterpret_cast<uint4*>(dst + r * ld + ch * 8) = *reinterpret_cast<const uint4*>(tile + v_at<NV>(r, ch));
+  for (int i = 0; i < PC; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + v_at<NV>(r + i * RP, ch));
+  if (ch * 8 < col_end) {
+#pragma unroll
+    for (int i = 0; i < PC; ++i)
+      if (r + i * RP < row_end) *reinterpret_cast<uint4*>(p + i * RP * ld) = v[i];
+  }
 }
 
 }  // namespace gdr
