@@ -18,8 +18,6 @@ namespace gdr {
 __device__ int g_gdr_error = 0;   // a bounded wait gave up
 
 // ------------------------------------------------------------------- prep
-constexpr uint32_t kImage = 32768;   // bf16: [T - I; P T] in two planes of 128 rows x 128 bytes
-
 template <class P, int DK>
 struct PrepSmem {
   using E = typename P::E;
@@ -30,9 +28,7 @@ struct PrepSmem {
   static constexpr size_t kA = sizeof(float) * kC * LDA, kP = kTPlanes<P> * sizeof(E) * kC * LDT;
   // k, then A and T; q, then P: the products are done when the others begin
   static constexpr size_t kOffQ = kTile > kA ? kTile : kA;
-  static constexpr bool TC = P::kMode == CFC_MATH_BF16;
-  static constexpr size_t kQ = TC ? kA : kP;             // fp32 P where P T is to be formed
-  static constexpr size_t kOffG = kOffQ + (kTile > kQ ? kTile : kQ);
+  static constexpr size_t kOffG = kOffQ + (kTile > kP ? kTile : kP);
   static constexpr size_t kBytes = kOffG + 3 * kC * sizeof(float);      // G / ln 2 in pairs, beta
 };
 
@@ -50,7 +46,6 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   E* qs = reinterpret_cast<E*>(smem_raw + S::kOffQ);
   float* am = reinterpret_cast<float*>(smem_raw);
   E* ps = qs;
-  float* pm = reinterpret_cast<float*>(smem_raw + S::kOffQ);
   float2* g2 = reinterpret_cast<float2*>(smem_raw + S::kOffG);
   float* bet = reinterpret_cast<float*>(g2 + kC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -69,38 +64,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   cp_commit();
   const long long id = slot * a.s.hv + h;
   float* vec = a.vec + id * kVec;
-  if (warp == 0) {
-    // Running sum of g in double: differences of G then carry no more than
-    // their own fp32 rounding, however far the sum has gone.
-    double x[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 2 * lane + i;
-      const float v = r < rows ? a.g[(row0 + r) * a.s.hv + h] : 0.f;
-      x[i] = v < kMinG ? kMinG : v;          // a NaN stays
-      bet[r] = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
-    }
-    double run = x[0] + x[1];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, run, d);
-      run += lane >= d ? y : 0.0;
-    }
-    const double total = __shfl_sync(0xffffffffu, run, 31);
-    const double G[2] = {run - x[1], run};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 2 * lane + i;
-      const double u = G[i] * 1.4426950408889634074;      // / ln 2
-      const float hi = (float)u, lo = (float)(u - (double)hi);
-      g2[r] = make_float2(hi, lo);
-      vec[kVecEG + r] = expf((float)G[i]);
-      vec[kVecEGL + r] = expf((float)(total - G[i]));
-      vec[kVecBeta + r] = bet[r];
-      reinterpret_cast<float2*>(vec + kVecG2)[r] = make_float2(hi, lo);
-    }
-    if (lane == 0) vec[kVecD] = expf((float)total);
-  }
+  if (warp == 0) chunk_decays(a, row0, rows, h, lane, g2, bet, vec);
   cp_wait<0>();
   __syncthreads();
 
@@ -137,147 +101,20 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
       const float l0 = P::exp2((gi.x - gj.x) + (gi.y - gj.y)), l1 = P::exp2((gi.x - gj.z) + (gi.y - gj.w));
       const float p0 = col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f,
                   p1 = col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f;
-      if constexpr (S::TC) *reinterpret_cast<float2*>(pm + i * S::LDA + col) = make_float2(p0, p1);
-      else P::template put2<PL>(Mat<E>{ps, S::LDT, kC * S::LDT}, i, col, p0, p1);
+      P::template put2<PL>(Mat<E>{ps, S::LDT, kC * S::LDT}, i, col, p0, p1);
       *reinterpret_cast<float2*>(am + i * S::LDA + col) =
           make_float2(col < i ? be * l0 * ak[j][rr * 2] : 0.f, col + 1 < i ? be * l1 * ak[j][rr * 2 + 1] : 0.f);
     }
   }
   __syncthreads();
-  if constexpr (!S::TC) {
+  {
     E* out = reinterpret_cast<E*>(a.p) + id * (kTPlanes<P> * kC * S::LDT);
     constexpr int V = 16 / sizeof(E);
     for (int i = tid; i < PL * kC * S::LDT / V; i += 128)
       reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(ps)[i];
   }
-  // Diagonal blocks.
-  if (lane < 16) {
-    float x[16];
-    const float* blk = am + m0 * S::LDA + m0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == lane ? 1.f : 0.f;
-#pragma unroll
-      for (int m = 0; m < i; ++m) v = fmaf(-blk[i * S::LDA + m], x[m], v);
-      x[i] = v;
-    }
-    __syncwarp(0xffffu);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) am[(m0 + i) * S::LDA + m0 + lane] = x[i];
-  }
-  __syncthreads();
-  const int r0 = g, r1 = g + 8;
-  // 16 -> 32: warps 0 and 1, a pair each; y = A21 T11, then -T22 y.
-  if (warp < 2) {
-    float* t21 = am + (warp * 32 + 16) * S::LDA + warp * 32;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      float d[2][4] = {};
-      const float* fa = pass == 0 ? t21 : t21 + 16;
-      const float* fb = pass == 0 ? t21 - 16 * S::LDA : t21;
-      const Mat<float> ma{const_cast<float*>(fa), S::LDA, 0}, mb{const_cast<float*>(fb), S::LDA, 0};
-#pragma unroll
-      for (int k0 = 0; k0 < 16; k0 += 8) {
-        MFp32::A<1> xa;
-        MFp32::B<1> xb;
-        MFp32::load_a(xa, ma, 0, k0, lane);
-        MFp32::load_bk(xb, mb, 0, k0, lane);
-        MFp32::mma(d[0], xa, xb, 0);
-        MFp32::mma(d[1], xa, xb, 1);
-      }
-      __syncwarp();
-      const float sg = pass == 0 ? 1.f : -1.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float2*>(t21 + r0 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
-        *reinterpret_cast<float2*>(t21 + r1 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
-      }
-      __syncwarp();
-    }
-  }
-  __syncthreads();
-  // 32 -> 64: warp w the rows 16 (w & 1) and the columns 16 (w >> 1) of each product.
+  invert<S::LDA>(am, warp, lane);
   {
-    float* t21 = am + 32 * S::LDA + (warp >> 1) * 16;
-    float* mine = t21 + (warp & 1) * 16 * S::LDA;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-      float d[2][4] = {};
-      const float* fa = am + (32 + (warp & 1) * 16) * S::LDA + (pass == 0 ? 0 : 32);
-      const float* fb = pass == 0 ? am + (warp >> 1) * 16 : t21;
-      const Mat<float> ma{const_cast<float*>(fa), S::LDA, 0}, mb{const_cast<float*>(fb), S::LDA, 0};
-#pragma unroll
-      for (int k0 = 0; k0 < 32; k0 += 8) {
-        MFp32::A<1> xa;
-        MFp32::B<1> xb;
-        MFp32::load_a(xa, ma, 0, k0, lane);
-        MFp32::load_bk(xb, mb, 0, k0, lane);
-        MFp32::mma(d[0], xa, xb, 0);
-        MFp32::mma(d[1], xa, xb, 1);
-      }
-      __syncthreads();
-      const float sg = pass == 0 ? 1.f : -1.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float2*>(mine + r0 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
-        *reinterpret_cast<float2*>(mine + r1 * S::LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
-      }
-      __syncthreads();
-    }
-  }
-  if constexpr (S::TC) {
-    // P T, a warp its 16 rows, in place of P
-    float d[8][4] = {};
-    const Mat<float> mp{pm, S::LDA, 0}, mt{am, S::LDA, 0};
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += 8) {
-      if (k0 >= m0 + 16) break;
-      MFp32::A<1> xa;
-      MFp32::load_a(xa, mp, m0, k0, lane);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j * 16 > k0) continue;
-        MFp32::B<1> xb;
-        MFp32::load_bk(xb, mt, j * 16, k0, lane);
-        MFp32::mma(d[2 * j], xa, xb, 0);
-        MFp32::mma(d[2 * j + 1], xa, xb, 1);
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      *reinterpret_cast<float2*>(pm + (m0 + g) * S::LDA + j * 8 + t2) = make_float2(d[j][0], d[j][1]);
-      *reinterpret_cast<float2*>(pm + (m0 + g + 8) * S::LDA + j * 8 + t2) = make_float2(d[j][2], d[j][3]);
-    }
-    __syncthreads();
-    // T - I and P T as the tensor cores read them: rows of 128 bytes, 16-byte
-    // piece c of row r at piece c ^ (r % 8)
-    unsigned char* img = reinterpret_cast<unsigned char*>(a.t) + id * kImage;
-    for (int e = tid; e < 2 * kC * 8; e += 128) {
-      const int r = e >> 3, ch = e & 7, i = r & 63;
-      const float* src = (r < kC ? am : pm) + i * S::LDA + ch * 8;
-      float v[8];
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(src + 4);
-      if (r < kC && (i >> 3) == ch)            // T - I: the products add R itself in fp32
-#pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = (i & 7) == x ? 0.f : v[x];
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
-        hi[x] = *reinterpret_cast<const uint32_t*>(&b);
-        if constexpr (PL == 2) {
-          const __nv_bfloat162 c2 =
-              __floats2bfloat162_rn(v[2 * x] - __bfloat162float(b.x), v[2 * x + 1] - __bfloat162float(b.y));
-          lo[x] = *reinterpret_cast<const uint32_t*>(&c2);
-        }
-      }
-      const int at = r * 128 + ((ch ^ (r & 7)) << 4);
-      *reinterpret_cast<uint4*>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if constexpr (PL == 2) *reinterpret_cast<uint4*>(img + kImage / 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-  } else {
     E* tout = reinterpret_cast<E*>(a.t) + id * (kTPlanes<P> * kC * S::LDT);
     const Mat<E> mt{tout, S::LDT, kC * S::LDT};
     for (int i = tid; i < kC * kC / 4; i += 128) {
@@ -641,13 +478,13 @@ static cudaError_t launch_scan(FwdArgs a, cudaStream_t st) {
 
 template <class P, int DK, int PL>
 static cudaError_t forward(const FwdArgs& a, cudaStream_t st) {
-  if (a.s.rows > 0) {
-    cudaError_t e = launch_prep<P, DK, PL>(a, st);
-    if (e != cudaSuccess) return e;
-  }
+  cudaError_t e = cudaSuccess;
   if constexpr (P::kMode == CFC_MATH_BF16) {
-    return launch_scan_tc(a, DK, PL, st);
+    if (a.s.rows > 0) e = launch_prep_tc(a, DK, PL, st);
+    return e != cudaSuccess ? e : launch_scan_tc(a, DK, PL, st);
   } else {
+    if (a.s.rows > 0) e = launch_prep<P, DK, PL>(a, st);
+    if (e != cudaSuccess) return e;
     // Tiles of 32 value columns where their blocks still reach every SM, else of 16.
     const long long heads = (long long)a.s.n_seq * a.s.hv;
     if (a.s.dv > 16 && heads * ((a.s.dv + 31) / 32) >= 114) return launch_scan<P, DK, 1, 2, PL, true>(a, st);

@@ -30,6 +30,168 @@ namespace gdr {
 
 __device__ int g_gdr_tc_error = 0;
 
+// ------------------------------------------------------------ all chunks at once
+// One block of 4 warps a (chunk, value head): the decays, T - I and P T.
+// T = (I + A)^{-1} comes from 16 x 16 diagonal blocks by forward substitution
+// (a warp each, a column a lane), then pairs of blocks joined by
+// T21 = -T22 A21 T11, all in fp32 or fp32-accurate products: T's entries reach
+// far above A's when keys repeat.  P T = P + P (T - I) takes P from the
+// registers that q k^T left it in and T - I as two bf16 planes.
+template <int DK>
+struct PrepTc {
+  static constexpr int LDK = DK + 8, LDA = kC + 4;
+  static constexpr uint32_t K = kC * LDK * 2, A = kC * LDA * 4;
+  // k, then A and T; q, then the image: the products are done when the others begin
+  static constexpr uint32_t OFF_I = (K > A ? K : A), OFF_G = OFF_I + (K > kImage ? K : kImage);
+  static constexpr uint32_t BYTES = OFF_G + 3 * kC * 4;
+};
+
+template <int DK, int PL>
+__global__ void __launch_bounds__(128, 4) k_gdr_prep_tc(FwdArgs a) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  using P = MBf16;
+  using S = PrepTc<DK>;
+  bf16* ks = reinterpret_cast<bf16*>(smem_raw);
+  bf16* qs = reinterpret_cast<bf16*>(smem_raw + S::OFF_I);
+  float* am = reinterpret_cast<float*>(smem_raw);
+  unsigned char* img = smem_raw + S::OFF_I;
+  float2* g2 = reinterpret_cast<float2*>(smem_raw + S::OFF_G);
+  float* bet = reinterpret_cast<float*>(g2 + kC);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % a.s.hv;
+  const long long slot = blockIdx.x / a.s.hv;
+  int n, len, c;
+  long long start;
+  if (!slot_chunk(a.s, slot, &n, &start, &len, &c)) return;
+  const long long row0 = start + (long long)c * kC;
+  const int rows = min(kC, len - c * kC);
+  const int hq = h / (a.s.hv / a.s.hk);
+  load_tile<bf16, kC, DK, 128>(ks, S::LDK, static_cast<const bf16*>(a.k) + row0 * a.ldk + (long long)hq * a.s.dk, a.ldk,
+                               rows, a.s.dk, tid);
+  load_tile<bf16, kC, DK, 128>(qs, S::LDK, static_cast<const bf16*>(a.q) + row0 * a.ldq + (long long)hq * a.s.dk, a.ldq,
+                               rows, a.s.dk, tid);
+  cp_commit();
+  const long long id = slot * a.s.hv + h;
+  float* vec = a.vec + id * kVec;
+  if (warp == 0) chunk_decays(a, row0, rows, h, lane, g2, bet, vec);
+  cp_wait<0>();
+  __syncthreads();
+
+  // Rows 16 warp .. of q k^T and k k^T, columns up to the diagonal block.
+  const Mat<bf16> mk{ks, S::LDK, 0}, mq{qs, S::LDK, 0};
+  const int m0 = warp * 16, g = lane >> 2, t2 = (lane & 3) * 2;
+  float pr[8][4] = {}, ak[8][4] = {};
+#pragma unroll 2
+  for (int k0 = 0; k0 < DK; k0 += 16) {
+    P::A<1> fq, fk;
+    P::load_a(fq, mq, m0, k0, lane);
+    P::load_a(fk, mk, m0, k0, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j > warp) continue;
+      P::B<1> fb;
+      P::load_bn(fb, mk, j * 16, k0, lane);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        P::mma(pr[2 * j + hf], fq, fb, hf);
+        P::mma(ak[2 * j + hf], fk, fb, hf);
+      }
+    }
+  }
+  __syncthreads();
+  // P in the registers, A in shared memory
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int col = j * 8 + t2;
+    float av[4] = {};
+    if (j <= 2 * warp + 1) {
+      const float4 gj = *reinterpret_cast<const float4*>(g2 + col);
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int i = m0 + g + rr * 8;
+        const float2 gi = g2[i];
+        const float l0 = P::exp2((gi.x - gj.x) + (gi.y - gj.y)), l1 = P::exp2((gi.x - gj.z) + (gi.y - gj.w));
+        const float be = bet[i];
+        av[2 * rr] = col < i ? be * l0 * ak[j][2 * rr] : 0.f;
+        av[2 * rr + 1] = col + 1 < i ? be * l1 * ak[j][2 * rr + 1] : 0.f;
+        pr[j][2 * rr] = col <= i ? a.s.scale * l0 * pr[j][2 * rr] : 0.f;
+        pr[j][2 * rr + 1] = col < i ? a.s.scale * l1 * pr[j][2 * rr + 1] : 0.f;
+      }
+    }
+    *reinterpret_cast<float2*>(am + (m0 + g) * S::LDA + col) = make_float2(av[0], av[1]);
+    *reinterpret_cast<float2*>(am + (m0 + g + 8) * S::LDA + col) = make_float2(av[2], av[3]);
+  }
+  __syncwarp();
+  invert<S::LDA>(am, warp, lane);
+  // T - I into the image, both planes
+#pragma unroll
+  for (int e = 0; e < kC * 8 / 128; ++e) {
+    const int r = (e * 128 + tid) >> 3, ch = tid & 7;
+    float v[8] = {};
+    if (ch * 8 <= r) {
+      const float* src = am + r * S::LDA + ch * 8;
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(src + 4);
+      if (r >> 3 == ch)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = (r & 7) == x ? 0.f : v[x];
+    }
+    const uint4 hi = pack8(v);
+    float hv[8];
+    unpack8(hv, hi);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) hv[x] = v[x] - hv[x];
+    *reinterpret_cast<uint4*>(img + chunk_at(r, ch)) = hi;
+    *reinterpret_cast<uint4*>(img + kImage / 2 + chunk_at(r, ch)) = pack8(hv);
+  }
+  __syncthreads();
+  // P T, 16 rows a warp
+  float d[8][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[j][e] = pr[j][e];
+#pragma unroll
+  for (int kb = 0; kb < 4; ++kb) {
+    if (kb > warp) continue;
+    P::A<2> fa;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float* p = pr[2 * kb + (x >> 1)] + (x & 1) * 2;
+      fa.r[0][x] = pack2(p[0], p[1]);
+      fa.r[1][x] = pack2(p[0] - lo_f(fa.r[0][x]), p[1] - hi_f(fa.r[0][x]));
+    }
+    const int r = kb * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb) {
+      if (jb > kb) continue;
+      P::B<2> fb;
+      const unsigned char* src = img + chunk_at(r, jb * 2 + (lane >> 4));
+      P::ldmt(fb.r[0], reinterpret_cast<const bf16*>(src));
+      P::ldmt(fb.r[1], reinterpret_cast<const bf16*>(src + kImage / 2));
+      P::mma(d[2 * jb], fa, fb, 0);
+      P::mma(d[2 * jb + 1], fa, fb, 1);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      const uint32_t o = chunk_at(kC + m0 + g + rr * 8, j) + t2 * 2;
+      const uint32_t hi = pack2(d[j][2 * rr], d[j][2 * rr + 1]);
+      *reinterpret_cast<uint32_t*>(img + o) = hi;
+      if constexpr (PL == 2)
+        *reinterpret_cast<uint32_t*>(img + kImage / 2 + o) =
+            pack2(d[j][2 * rr] - lo_f(hi), d[j][2 * rr + 1] - hi_f(hi));
+    }
+  tc::fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_store(a.t + id * kImage, img, PL * (kImage / 2));
+    bulk_store_read();
+  }
+}
+
 template <int DK, int NV, int PL, int NCH, int CW, bool BWD>
 struct TcCfg {
   static constexpr int ATOMS = DK / 64, FETCH = 128, CHAIN_T = 128 * CW, THREADS = CHAIN_T * NCH + FETCH;
@@ -609,6 +771,21 @@ static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
   k_gdr_scan_bwd_tc<DK, NV, NCH, CW>
       <<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
+}
+
+template <int DK, int PL>
+static cudaError_t prep(const FwdArgs& a, cudaStream_t st) {
+  using S = PrepTc<DK>;
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_prep_tc<DK, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::BYTES);
+  if (e != cudaSuccess) return e;
+  TraceScope tr("k_gdr_prep_tc", st);
+  k_gdr_prep_tc<DK, PL><<<(unsigned)(slot_count(a.s.rows, a.s.n_seq) * a.s.hv), 128, S::BYTES, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {
+  if (dk_tile == 64) return planes == 2 ? prep<64, 2>(a, st) : prep<64, 1>(a, st);
+  return planes == 2 ? prep<128, 2>(a, st) : prep<128, 1>(a, st);
 }
 
 template <int DK>

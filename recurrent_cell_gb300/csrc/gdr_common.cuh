@@ -69,18 +69,26 @@ __device__ __forceinline__ void seq_range(const Shape& s, int n, long long* star
 __host__ __device__ __forceinline__ long long slot_base(long long start, int n) { return start / kC + n; }
 __host__ __device__ __forceinline__ long long slot_count(long long rows, int n_seq) { return rows / kC + n_seq; }
 
-// The chunk of a slot: false if the slot is none.  A sequence's slots may
-// begin before an empty neighbour's, so the search is over slot_base, which
-// rises strictly with n.
+// The chunk of a slot, found by a whole warp (32 pivots a step, so up to 32
+// sequences take one round of loads); false if the slot is none.  A sequence's
+// slots may begin before an empty neighbour's, so the search is over
+// slot_base, which rises strictly with n.
 __device__ __forceinline__ bool slot_chunk(const Shape& s, long long slot, int* n_out, long long* start, int* len,
                                            int* c) {
-  int lo = 0, hi = s.n_seq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    long long a;
-    int l;
-    seq_range(s, mid, &a, &l);
-    if (slot_base(a, mid) <= slot) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, size = s.n_seq;
+  while (size > 1) {
+    const int step = (size + 31) / 32, n = lo + lane * step;
+    bool below = false;
+    if (lane * step < size) {
+      long long a;
+      int l;
+      seq_range(s, n, &a, &l);
+      below = slot_base(a, n) <= slot;
+    }
+    const int hits = __popc(__ballot_sync(0xffffffffu, below)), skip = (hits > 0 ? hits - 1 : 0) * step;
+    lo += skip;
+    size = min(step, size - skip);
   }
   seq_range(s, lo, start, len);
   const long long d = slot - slot_base(*start, lo);
@@ -391,6 +399,8 @@ template <class P> constexpr int kLdt = kC + P::PAD;                            
 template <class P> constexpr int kTPlanes = P::kMode == CFC_MATH_BF16 ? 2 : 1;
 Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 
+constexpr uint32_t kImage = 32768;   // bf16: [T - I; P T] in two planes of 128 rows x 128 bytes
+
 struct FwdArgs {
   Shape s;
   const void *q, *k, *v;
@@ -404,6 +414,124 @@ struct FwdArgs {
   int save;
   int ntile;
 };
+
+// The decays of a chunk's head, by one warp: into `vec`, and for the block
+// G / ln 2 as pairs hi + lo and beta.
+__device__ __forceinline__ void chunk_decays(const FwdArgs& a, long long row0, int rows, int h, int lane, float2* g2,
+                                             float* bet, float* vec) {
+  // Running sum of g in double: differences of G then carry no more than
+  // their own fp32 rounding, however far the sum has gone.
+  double x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * lane + i;
+    const float v = r < rows ? a.g[(row0 + r) * a.s.hv + h] : 0.f;
+    x[i] = v < kMinG ? kMinG : v;          // a NaN stays
+    bet[r] = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
+  }
+  double run = x[0] + x[1];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, run, d);
+    run += lane >= d ? y : 0.0;
+  }
+  const double total = __shfl_sync(0xffffffffu, run, 31);
+  const double G[2] = {run - x[1], run};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * lane + i;
+    const double u = G[i] * 1.4426950408889634074;      // / ln 2
+    const float hi = (float)u, lo = (float)(u - (double)hi);
+    g2[r] = make_float2(hi, lo);
+    vec[kVecEG + r] = expf((float)G[i]);
+    vec[kVecEGL + r] = expf((float)(total - G[i]));
+    vec[kVecBeta + r] = bet[r];
+    reinterpret_cast<float2*>(vec + kVecG2)[r] = make_float2(hi, lo);
+  }
+  if (lane == 0) vec[kVecD] = expf((float)total);
+}
+
+// T = (I + A)^{-1} in place of A, 64 x 64 and strictly lower triangular in fp32
+// with rows of LDA, by a block of 4 warps of which warp w wrote rows 16 w ..;
+// ends with a block barrier.
+template <int LDA>
+__device__ __forceinline__ void invert(float* am, int warp, int lane) {
+  const int m0 = warp * 16, g = lane >> 2, t2 = (lane & 3) * 2;
+  // Diagonal blocks.
+  if (lane < 16) {
+    float x[16];
+    const float* blk = am + m0 * LDA + m0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == lane ? 1.f : 0.f;
+#pragma unroll
+      for (int m = 0; m < i; ++m) v = fmaf(-blk[i * LDA + m], x[m], v);
+      x[i] = v;
+    }
+    __syncwarp(0xffffu);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) am[(m0 + i) * LDA + m0 + lane] = x[i];
+  }
+  __syncthreads();
+  // 16 -> 32: warps 0 and 1, a pair each; y = A21 T11, then -T22 y.
+  if (warp < 2) {
+    float* t21 = am + (warp * 32 + 16) * LDA + warp * 32;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      float d[2][4] = {};
+      const float* fa = pass == 0 ? t21 : t21 + 16;
+      const float* fb = pass == 0 ? t21 - 16 * LDA : t21;
+      const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
+#pragma unroll
+      for (int k0 = 0; k0 < 16; k0 += 8) {
+        MFp32::A<1> xa;
+        MFp32::B<1> xb;
+        MFp32::load_a(xa, ma, 0, k0, lane);
+        MFp32::load_bk(xb, mb, 0, k0, lane);
+        MFp32::mma(d[0], xa, xb, 0);
+        MFp32::mma(d[1], xa, xb, 1);
+      }
+      __syncwarp();
+      const float sg = pass == 0 ? 1.f : -1.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<float2*>(t21 + g * LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
+        *reinterpret_cast<float2*>(t21 + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // 32 -> 64: warp w the rows 16 (w & 1) and the columns 16 (w >> 1) of each product.
+  {
+    float* t21 = am + 32 * LDA + (warp >> 1) * 16;
+    float* mine = t21 + (warp & 1) * 16 * LDA;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      float d[2][4] = {};
+      const float* fa = am + (32 + (warp & 1) * 16) * LDA + (pass == 0 ? 0 : 32);
+      const float* fb = pass == 0 ? am + (warp >> 1) * 16 : t21;
+      const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
+#pragma unroll
+      for (int k0 = 0; k0 < 32; k0 += 8) {
+        MFp32::A<1> xa;
+        MFp32::B<1> xb;
+        MFp32::load_a(xa, ma, 0, k0, lane);
+        MFp32::load_bk(xb, mb, 0, k0, lane);
+        MFp32::mma(d[0], xa, xb, 0);
+        MFp32::mma(d[1], xa, xb, 1);
+      }
+      __syncthreads();
+      const float sg = pass == 0 ? 1.f : -1.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<float2*>(mine + g * LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
+        *reinterpret_cast<float2*>(mine + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+      }
+      __syncthreads();
+    }
+  }
+}
 
 struct BwdArgs {
   Shape s;
@@ -419,7 +547,8 @@ struct BwdArgs {
   int ntile;
 };
 
-// The serial passes in bf16 (cfc_gdr_tc.cu).
+// bf16 (cfc_gdr_tc.cu): what is formed for all chunks at once, the serial passes.
+cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st);
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st);
 cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st);
 int read_gdr_tc_error(int clear);
