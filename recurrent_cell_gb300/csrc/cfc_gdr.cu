@@ -546,7 +546,7 @@ cudaError_t launch_gdr_forward(const GdrArgs& g, cudaStream_t st) {
   using namespace gdr;
   const Workspace w = plan(g.rows, g.n_seq, g.hk, g.hv, g.dk, g.dv, g.math, g.save);
   FwdArgs a{};
-  a.s = Shape{g.off, g.n_seq, g.rows, g.hk, g.hv, g.dk, g.dv, g.scale};
+  a.s = Shape{g.off, g.n_seq, g.rows, g.hk, g.hv, g.dk, g.dv, g.scale, (int)(g.rows / g.n_seq)};
   a.q = g.q; a.k = g.k; a.v = g.v;
   a.ldq = g.ldq; a.ldk = g.ldk; a.ldv = g.ldv;
   a.g = g.g; a.beta = g.beta; a.init = g.init; a.final_state = g.final_state; a.o = g.o;

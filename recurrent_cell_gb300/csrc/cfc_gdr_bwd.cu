@@ -607,7 +607,7 @@ cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_
   using namespace gdr;
   const Workspace w = plan(g.rows, g.n_seq, g.hk, g.hv, g.dk, g.dv, g.math, 1);
   BwdArgs a{};
-  a.s = Shape{g.off, g.n_seq, g.rows, g.hk, g.hv, g.dk, g.dv, g.scale};
+  a.s = Shape{g.off, g.n_seq, g.rows, g.hk, g.hv, g.dk, g.dv, g.scale, (int)(g.rows / g.n_seq)};
   a.q = g.q; a.k = g.k; a.v = g.v; a.go = r.grad_o;
   a.ldq = g.ldq; a.ldk = g.ldk; a.ldv = g.ldv;
   a.gfinal = r.grad_final; a.ginit = r.grad_init;

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       tc::fence_after_sync();
       {
         float x[32];
-        ld_sum<32, 1>(d2 + at + cg * 32, x);
+        ld_sum<32, 1, 0>(d2 + at + cg * 32, x);
         const float2 gi = reinterpret_cast<const float2*>(gs)[i];
         const float f = lower ? -1.f : a.s.scale;
         const int end = cg * 32 <= i ? (lower ? i : i + 1) : 0;    // columns that count

@@ -1,11 +1,9 @@
 // cfc_gdr_tc.cu -- the serial passes of the gated delta rule in bf16 on the
 // 5th-generation tensor cores (notation of gdr_common.cuh).
 //
-// Value columns do not touch one another, so a head is split into chains of NV
-// columns, each with 4 warps of its own; a block runs NCH chains of one head
-// over shared K, Q and [T - I; P T] tiles, so that one chain's products run
-// under the other's arithmetic.  A chain and chunk take three products of 128
-// rows, each waiting for the one before:
+// Value columns do not touch one another, so a head is split into tiles of NV
+// columns, a block each.  A chunk takes three products of 128 rows, each
+// waiting for the one before:
 //   D1 = [K; Q] S0        rows 0-63:  R = beta (V - exp(G) D1)
 //                         rows 64-127: scale exp(G) D1, the outputs' first part
 //   D2 = [T - I; P T] R   rows 0-63:  U = R + D2
@@ -16,12 +14,10 @@
 // row as MN-major operand tiles.  R and S stay fp32 where they are added.
 //
 // PL = 2 (a state leaves the call): S, R, U and [T - I; P T] as two bf16
-// planes, 17 significant bits.  The planes of a chain lie side by side in the
-// operand's 64 columns (NV = 32), one product for both.
+// planes, 17 significant bits.  The planes lie side by side in the operand's
+// 64 NB columns, NV = 64 NB / PL, one product for both.
 //
-// A product of 128 x 64 x 16 takes about 34 cycles at the tensor peak, 544
-// (PL = 1) a chain and chunk; a chain's latency is those plus three round
-// trips through tensor memory and the arithmetic between them.
+// What bounds it is the length of that chain.
 #include <cstdlib>
 #include "gdr_tc.cuh"
 
@@ -41,20 +37,20 @@ template <int DK>
 struct PrepTc {
   static constexpr int LDK = DK + 8, LDA = kC + 4;
   static constexpr uint32_t K = kC * LDK * 2, A = kC * LDA * 4;
-  // k, then A and T; q, then the image: the products are done when the others begin
-  static constexpr uint32_t OFF_I = (K > A ? K : A), OFF_G = OFF_I + (K > kImage ? K : kImage);
+  // k, then A and T, then P T; q, then T - I: each is done with when the next begins
+  static constexpr uint32_t OFF_I = (K > A ? K : A), OFF_G = OFF_I + (K > kImage / 2 ? K : kImage / 2);
   static constexpr uint32_t BYTES = OFF_G + 3 * kC * 4;
 };
 
 template <int DK, int PL>
-__global__ void __launch_bounds__(128, 4) k_gdr_prep_tc(FwdArgs a) {
+__global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   using P = MBf16;
   using S = PrepTc<DK>;
   bf16* ks = reinterpret_cast<bf16*>(smem_raw);
   bf16* qs = reinterpret_cast<bf16*>(smem_raw + S::OFF_I);
   float* am = reinterpret_cast<float*>(smem_raw);
-  unsigned char* img = smem_raw + S::OFF_I;
+  unsigned char *img = smem_raw + S::OFF_I, *pimg = smem_raw;      // 64 rows each, the lo plane 8 KB on
   float2* g2 = reinterpret_cast<float2*>(smem_raw + S::OFF_G);
   float* bet = reinterpret_cast<float*>(g2 + kC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -142,7 +138,7 @@ __global__ void __launch_bounds__(128, 4) k_gdr_prep_tc(FwdArgs a) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) hv[x] = v[x] - hv[x];
     *reinterpret_cast<uint4*>(img + chunk_at(r, ch)) = hi;
-    *reinterpret_cast<uint4*>(img + kImage / 2 + chunk_at(r, ch)) = pack8(hv);
+    *reinterpret_cast<uint4*>(img + 8192 + chunk_at(r, ch)) = pack8(hv);
   }
   __syncthreads();
   // P T, 16 rows a warp
@@ -168,7 +164,7 @@ __global__ void __launch_bounds__(128, 4) k_gdr_prep_tc(FwdArgs a) {
       P::B<2> fb;
       const unsigned char* src = img + chunk_at(r, jb * 2 + (lane >> 4));
       P::ldmt(fb.r[0], reinterpret_cast<const bf16*>(src));
-      P::ldmt(fb.r[1], reinterpret_cast<const bf16*>(src + kImage / 2));
+      P::ldmt(fb.r[1], reinterpret_cast<const bf16*>(src + 8192));
       P::mma(d[2 * jb], fa, fb, 0);
       P::mma(d[2 * jb + 1], fa, fb, 1);
     }
@@ -177,36 +173,59 @@ __global__ void __launch_bounds__(128, 4) k_gdr_prep_tc(FwdArgs a) {
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
-      const uint32_t o = chunk_at(kC + m0 + g + rr * 8, j) + t2 * 2;
+      const uint32_t o = chunk_at(m0 + g + rr * 8, j) + t2 * 2;
       const uint32_t hi = pack2(d[j][2 * rr], d[j][2 * rr + 1]);
-      *reinterpret_cast<uint32_t*>(img + o) = hi;
+      *reinterpret_cast<uint32_t*>(pimg + o) = hi;
       if constexpr (PL == 2)
-        *reinterpret_cast<uint32_t*>(img + kImage / 2 + o) =
+        *reinterpret_cast<uint32_t*>(pimg + 8192 + o) =
             pack2(d[j][2 * rr] - lo_f(hi), d[j][2 * rr + 1] - hi_f(hi));
     }
   tc::fence_proxy_async_smem();
   __syncthreads();
   if (tid == 0) {
-    bulk_store(a.t + id * kImage, img, PL * (kImage / 2));
+    char* out = a.t + id * kImage;
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) {
+      bulk_store(out + pl * (kImage / 2), img + pl * 8192, 8192);
+      bulk_store(out + pl * (kImage / 2) + 8192, pimg + pl * 8192, 8192);
+    }
     bulk_store_read();
   }
 }
 
-template <int DK, int NV, int PL, int NCH, int CW, bool BWD>
+template <int DK, int PL, int NB, int CW, bool BWD>
 struct TcCfg {
-  static constexpr int ATOMS = DK / 64, FETCH = 128, CHAIN_T = 128 * CW, THREADS = CHAIN_T * NCH + FETCH;
+  static constexpr int NV = 64 * NB / PL, ATOMS = DK / 64, FETCH = 128, WORK = 128 * CW, THREADS = WORK + FETCH;
   static constexpr int NC = NV / CW;                    // columns a thread
+  static constexpr int LO = NV;                         // from the hi to the lo plane's accumulator columns
   static constexpr uint32_t KQ = ATOMS * 16384u;        // per 64 key columns: 64 rows of K, 64 of Q
   static constexpr uint32_t A2 = PL * 16384u;
-  static constexpr uint32_t VT = 64 * NV * 2;           // a chain's V (or dO): 64 rows
-  static constexpr uint32_t STAGE = (KQ + A2 + NCH * VT + kVec * 4 + 1023) / 1024 * 1024;
-  // per chain: S; R, then its decayed U; U as it is (PL = 1); backward: dO scaled
-  static constexpr uint32_t S = DK * 128u, R = 8192u;
-  static constexpr uint32_t CHAIN = S + (PL == 1 ? 2 : 1) * R + (BWD ? R : 0);
-  static constexpr uint32_t BYTES = 2048 + 2 * STAGE + NCH * CHAIN;
-  static constexpr uint32_t TMEM = NCH * 128;           // D1 / D2 and D3, 64 columns each
+  static constexpr uint32_t VT = 64 * NV * 2;           // V (or dO): 64 rows
+  static constexpr uint32_t STAGE = (KQ + A2 + VT + kVec * 4 + 1023) / 1024 * 1024;
+  // S; R, then its decayed U; U as it is (PL = 1); backward: dO scaled.  NB blocks each.
+  static constexpr uint32_t SB = DK * 128u, RB = 8192u, S = NB * SB, R = NB * RB;
+  static constexpr uint32_t BYTES = 2048 + 2 * STAGE + S + (PL == 1 ? 2 : 1) * R + (BWD ? R : 0);
+  static constexpr uint32_t TMEM = NB * 128;            // D1 / D2 and D3
   static_assert(BYTES <= 227u * 1024u, "shared memory");
 };
+
+// Columns col .. col + 7 of a row into a tile of blocks of BB bytes: PL = 1,
+// blocks of 64 columns; PL = 2, the lo plane in the second block or, with one
+// block, in its second half.
+template <int PL, int NB, uint32_t BB>
+__device__ __forceinline__ void put8(unsigned char* tile, int row, int col, const float* v) {
+  const uint4 h = pack8(v);
+  if constexpr (PL == 1) {
+    *reinterpret_cast<uint4*>(tile + (NB > 1 ? (col >> 6) * BB : 0) + chunk_at(row, (col & 63) >> 3)) = h;
+  } else {
+    *reinterpret_cast<uint4*>(tile + chunk_at(row, col >> 3)) = h;
+    float l[8];
+    unpack8(l, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = v[i] - l[i];
+    *reinterpret_cast<uint4*>(tile + (NB > 1 ? BB + chunk_at(row, col >> 3) : chunk_at(row, (col >> 3) + 4))) = pack8(l);
+  }
+}
 
 struct TcArgs {
   Shape s;
@@ -226,10 +245,11 @@ struct TcArgs {
 // backward's dv), which lie in the place of its V (dO), go to global memory;
 // then the next chunk's tiles come into that stage: the fetching threads with 16-byte copies (rows past the end and
 // columns past d_k, d_v as zeros) and the prepared images by bulk copy.
-template <int DK, int NV, int PL, int NCH, class C, class W>
+template <int DK, class C, class W>
 __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* stage, uint64_t* full, uint64_t* empty,
                                              uint64_t* outs, int ft, int h, long long start, int len, long long slot0,
                                              int v0, bool backwards, W wait) {
+  constexpr int NV = C::NV;
   const int hq = h / (a.s.hv / a.s.hk), dk = a.s.dk, nc = (len + kC - 1) / kC;
   const bf16* q = a.q + start * a.ldq + (long long)hq * dk;
   const bf16* k = a.k + start * a.ldk + (long long)hq * dk;
@@ -243,12 +263,10 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
       const int cl = backwards ? c + 2 : c - 2;
       bf16* o = a.o + (start + (long long)cl * kC) * ldo + (long long)h * a.s.dv + v0;
       wait(outs + st, (i / 2 - 1) & 1);
-      // 4 warps: 32 rows by half of the chains' columns each
-      constexpr int HC = NCH * NV / 2, PART = HC < NV ? HC : NV;
-      const int w = ft >> 5, lane = ft & 31;
-      const int col = (w >> 1) * HC, ch = col / NV;
-      rows_out<NV, PART>(o + ch * NV, ldo, b + C::KQ + C::A2 + ch * C::VT, (w & 1) * 32, (col % NV) / 8,
-                         min(kC, len - cl * kC), vn - ch * NV, lane);
+      // 4 warps: 32 rows by half of the columns each
+      const int w = ft >> 5;
+      rows_out<NV, NV / 2>(o, ldo, b + C::KQ + C::A2, (w & 1) * 32, (w >> 1) * (NV / 16), min(kC, len - cl * kC), vn,
+                           ft & 31);
       asm volatile("bar.sync 15, 128;" ::: "memory");       // the tiles are filled again by other threads
       wait(empty + st, (i / 2 - 1) & 1);
     }
@@ -258,7 +276,7 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
     if (ft == 0) {
       bar_arrive_tx(full + st, C::A2 + kVec * 4);
       bulk_load(b + C::KQ, a.a2 + id * 32768, C::A2, full + st);
-      bulk_load(b + C::KQ + C::A2 + NCH * C::VT, a.vec + id * kVec, kVec * 4, full + st);
+      bulk_load(b + C::KQ + C::A2 + C::VT, a.vec + id * kVec, kVec * 4, full + st);
     }
     {
       constexpr int PER = DK / 8, STEP = C::FETCH / PER;      // 16-byte pieces of a row; rows a pass
@@ -273,14 +291,14 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
       }
     }
     {
-      constexpr int PER = NCH * NV / 8, STEP = C::FETCH / PER, PC = NV / 8;
-      const int ch = ft % PER, rr = ft / PER, cc = ch % PC;
+      constexpr int PER = NV / 8, STEP = C::FETCH / PER;
+      const int ch = ft % PER;
       const bool in = ch * 8 < vn;
-      unsigned char* d = b + C::KQ + C::A2 + (ch / PC) * C::VT;
+      unsigned char* d = b + C::KQ + C::A2;
 #pragma unroll 4
-      for (int r = rr; r < kC; r += STEP) {
+      for (int r = ft / PER; r < kC; r += STEP) {
         const bool on = in && r < rows;
-        cp16(d + v_at<NV>(r, cc), on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
+        cp16(d + v_at<NV>(r, ch), on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
       }
     }
     cp_commit();
@@ -291,10 +309,10 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
 }
 
 // ------------------------------------------------------------------- forward
-template <int DK, int NV, int PL, int NCH, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a) {
-  using C = TcCfg<DK, NV, PL, NCH, CW, false>;
-  constexpr int NC = C::NC;
+template <int DK, int PL, int NB, int CW>
+__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a) {
+  using C = TcCfg<DK, PL, NB, CW, false>;
+  constexpr int NC = C::NC, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
@@ -313,8 +331,8 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH);            // a chain's last product
-      tc::mbar_init(outs + i, NCH * 2 * CW);    // the warps that form output rows
+      tc::mbar_init(empty + i, 1);             // a chunk's last product
+      tc::mbar_init(outs + i, 2 * CW);         // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -332,23 +350,23 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
     }
   };
 
-  if (tid >= C::CHAIN_T * NCH) {
-    fetch_chunks<DK, NV, PL, NCH, C>(a, stage, full, empty, outs, tid - C::CHAIN_T * NCH, h, start, len, slot0,
-                                     tile * NCH * NV, false, wait);
+  if (tid >= C::WORK) {
+    fetch_chunks<DK, C>(a, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+                                     tile * NV, false, wait);
   } else {
-    const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
-    const int v0 = (tile * NCH + chain) * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
+    const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
+    const int v0 = tile * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
     const bool token = quad < 2;             // rows of K; else rows of Q
     const bool issuer = quad == 0 && cg == 0;
     const int i = row & 63;                  // the row's token
-    unsigned char* stile = stage + 2 * C::STAGE + chain * C::CHAIN;
+    unsigned char* stile = stage + 2 * C::STAGE;
     unsigned char* rtile = stile + C::S;
     unsigned char* utile = rtile + C::R;
-    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, at = ((uint32_t)(quad * 32) << 16) + c0;
-    const uint32_t id_kq = tc::idesc(128, 64, tc::kFmtBF16) | kBmn;
-    const uint32_t id_lo = tc::idesc(128, 32, tc::kFmtBF16) | kBmn;
-    const uint32_t id_kt = tc::idesc(128, 64, tc::kFmtBF16) | kAmn | kBmn;
-    const uint64_t bs = mn_desc(smem_addr(stile), 8192), br = mn_desc(smem_addr(rtile), 8192);
+    const uint32_t d12 = tmem, d3 = tmem + 64 * NB, at = ((uint32_t)(quad * 32) << 16) + c0;
+    const uint32_t id_kq = tc::idesc(128, 64 * NB, tc::kFmtBF16) | kBmn;
+    const uint32_t id_lo = tc::idesc(128, NV, tc::kFmtBF16) | kBmn;
+    const uint32_t id_kt = tc::idesc(128, 64 * NB, tc::kFmtBF16) | kAmn | kBmn;
+    const uint64_t bs = mn_desc(smem_addr(stile), C::SB), br = mn_desc(smem_addr(rtile), C::RB);
     uint32_t phase = 0;
     const bool srow = row < dk && row < DK;
     float s[NC];
@@ -362,18 +380,18 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
     for (int c = 0; c < nc; ++c) {
       const int st = c & 1;
       unsigned char* b = stage + st * C::STAGE;
-      unsigned char* vt = b + C::KQ + C::A2 + chain * C::VT;
-      const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + NCH * C::VT);
+      unsigned char* vt = b + C::KQ + C::A2;
+      const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + C::VT);
       const int rows = min(kC, len - c * kC);
       const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 8) put8<PL>(stile, row, (c0 + j) / 8, s + j);
+        for (int j = 0; j < NC; j += 8) put8<PL, NB, C::SB>(stile, row, c0 + j, s + j);
       }
       wait(full + st, (c >> 1) & 1);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b));
@@ -382,15 +400,15 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
           for (int ks = 0; ks < DK / 16; ++ks)
             tc::mma_bf16(d12, tc::sdesc_advance(ad, (ks >> 2) * 16384 + (ks & 3) * kStepK),
                          tc::sdesc_advance(bs, ks * kStepMN), id_kq, ks > 0);
-          tc::mma_commit(done + chain);
-          if (PL == 1 && a.st && v0 < dv) bulk_store(a.st + img * C::S, stile, C::S);
+          tc::mma_commit(done);
+          if (PL == 1 && a.st) bulk_store(a.st + img * C::SB, stile, min(NB, (dv - v0 + 63) / 64) * C::SB);
         }
         __syncwarp();
       }
-      if (PL == 2 && a.st && row < DK && v0 < dv)      // half a tile: the chain's 32 columns
+      if (PL == 2 && a.st && row < DK)      // only the hi plane
 #pragma unroll
         for (int j = 0; j < NC; j += 8)
-          *reinterpret_cast<uint4*>(a.st + img * C::S + chunk_at(row, ((v0 & 63) + c0 + j) / 8)) = pack8(s + j);
+          *reinterpret_cast<uint4*>(a.st + img * C::SB + chunk_at(row, ((v0 & 63) + c0 + j) / 8)) = pack8(s + j);
       const float eg = vec[kVecEG + i], be = vec[kVecBeta + i], el = vec[kVecEGL + i], dec = vec[kVecD];
       float r[NC];                     // beta V; then R; in the rows of Q, O
       if (token) {
@@ -402,26 +420,27 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
         }
       }
       const float f = token ? -be * eg : a.s.scale * eg;
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      {
-        float x[NC];
-        ld_sum<NC, PL>(d12 + at, x);
+#pragma unroll
+      for (int j = 0; j < NC; j += 16) {
+        float x[16];
+        ld_sum<16, PL, C::LO>(d12 + at + j, x);
         if (token) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) r[j] = fmaf(f, x[j], r[j]);
-#pragma unroll
-          for (int j = 0; j < NC; j += 8) put8<PL>(rtile, i, (c0 + j) / 8, r + j);
+          for (int e = 0; e < 16; ++e) r[j + e] = fmaf(f, x[e], r[j + e]);
+          put8<PL, NB, C::RB>(rtile, i, c0 + j, r + j);
+          put8<PL, NB, C::RB>(rtile, i, c0 + j + 8, r + j + 8);
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) r[j] = f * x[j];
+          for (int e = 0; e < 16; ++e) r[j + e] = f * x[e];
         }
       }
       if (PL == 1 && issuer) bulk_store_read();      // S and the last chunk's U have left their tiles
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b + C::KQ));
@@ -435,18 +454,19 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
               tc::mma_bf16(d12, tc::sdesc_advance(ad, 16384 + ks * kStepK), tc::sdesc_advance(br, ks * kStepMN), id_lo,
                            1u);
           }
-          tc::mma_commit(done + chain);
+          tc::mma_commit(done);
         }
         __syncwarp();
       }
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      {
-        float x[NC];
-        ld_sum<NC, PL>(d12 + at, x);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) r[j] += x[j];
+      for (int j = 0; j < NC; j += 16) {
+        float x[16];
+        ld_sum<16, PL, C::LO>(d12 + at + j, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[j + e] += x[e];
       }
       if (token) {
 #pragma unroll
@@ -454,17 +474,17 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
           float w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = el * r[j + e];
-          put8<PL>(rtile, i, (c0 + j) / 8, w);
+          put8<PL, NB, C::RB>(rtile, i, c0 + j, w);
           if (a.u) {
-            if constexpr (PL == 1) put8<1>(utile, i, (c0 + j) / 8, r + j);
-            else if (v0 < dv)
-              *reinterpret_cast<uint4*>(a.u + img * C::R + chunk_at(i, ((v0 & 63) + c0 + j) / 8)) = pack8(r + j);
+            if constexpr (PL == 1) put8<PL, NB, C::RB>(utile, i, c0 + j, r + j);
+            else
+              *reinterpret_cast<uint4*>(a.u + img * C::RB + chunk_at(i, ((v0 & 63) + c0 + j) / 8)) = pack8(r + j);
           }
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = mn_desc(smem_addr(b), DK == 128 ? 16384 : 8192);   // DK = 64: rows 64.. unused
@@ -472,9 +492,9 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d3, tc::sdesc_advance(ad, ks * kStepMN), tc::sdesc_advance(br, ks * kStepMN), id_kt, ks > 0);
-          tc::mma_commit(done + chain);
+          tc::mma_commit(done);
           tc::mma_commit(empty + st);
-          if (PL == 1 && a.u && v0 < dv) bulk_store(a.u + img * C::R, utile, C::R);
+          if (PL == 1 && a.u) bulk_store(a.u + img * C::RB, utile, min(NB, (dv - v0 + 63) / 64) * C::RB);
         }
         __syncwarp();
       }
@@ -486,14 +506,15 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
       }
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      {
-        float x[NC];
-        ld_sum<NC, PL>(d3 + at, x);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) s[j] = fmaf(dec, s[j], x[j]);
+      for (int j = 0; j < NC; j += 16) {
+        float x[16];
+        ld_sum<16, PL, C::LO>(d3 + at + j, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
       }
     }
     if (a.final_state && srow) {
@@ -525,10 +546,10 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, PL, NCH, CW, false>::THREADS) k_
 //   D3 = Q^T (scale exp(G) dO) - K^T (beta exp(G) dR),  dS0 = exp(G_C) dS1 + D3.
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
-template <int DK, int NV, int NCH, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a) {
-  using C = TcCfg<DK, NV, 1, NCH, CW, true>;
-  constexpr int NC = C::NC;
+template <int DK, int NB, int CW>
+__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a) {
+  using C = TcCfg<DK, 1, NB, CW, true>;
+  constexpr int PL = 1, NC = C::NC, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
@@ -547,8 +568,8 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
-      tc::mbar_init(empty + i, NCH);            // a chain's last product
-      tc::mbar_init(outs + i, NCH * 2 * CW);    // the warps that form output rows
+      tc::mbar_init(empty + i, 1);             // a chunk's last product
+      tc::mbar_init(outs + i, 2 * CW);         // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -566,24 +587,24 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
     }
   };
 
-  if (tid >= C::CHAIN_T * NCH) {
-    fetch_chunks<DK, NV, 1, NCH, C>(a, stage, full, empty, outs, tid - C::CHAIN_T * NCH, h, start, len, slot0,
-                                    tile * NCH * NV, true, wait);
+  if (tid >= C::WORK) {
+    fetch_chunks<DK, C>(a, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+                                    tile * NV, true, wait);
   } else {
-    const int chain = warp / (4 * CW), quad = warp & 3, cg = (warp >> 2) % CW, row = quad * 32 + lane;
-    const int v0 = (tile * NCH + chain) * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
+    const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
+    const int v0 = tile * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
     const bool token = quad < 2;             // rows of K; else rows of Q
     const bool issuer = quad == 0 && cg == 0;
     const int i = row & 63;                  // the row's token
-    unsigned char* stile = stage + 2 * C::STAGE + chain * C::CHAIN;
+    unsigned char* stile = stage + 2 * C::STAGE;
     unsigned char* rtile = stile + C::S;
     unsigned char* utile = rtile + C::R;
     unsigned char* otile = utile + C::R;
-    const uint32_t d12 = tmem + chain * 128, d3 = d12 + 64, at = ((uint32_t)(quad * 32) << 16) + c0;
-    const uint32_t id_k = tc::idesc(128, 64, tc::kFmtBF16) | kBmn;
-    const uint32_t id_t = tc::idesc(128, 64, tc::kFmtBF16) | kAmn | kBmn;
-    const uint64_t bs = mn_desc(smem_addr(stile), 8192), bx = mn_desc(smem_addr(rtile), 8192),
-                   bo = mn_desc(smem_addr(otile), 8192);
+    const uint32_t d12 = tmem, d3 = tmem + 64 * NB, at = ((uint32_t)(quad * 32) << 16) + c0;
+    const uint32_t id_k = tc::idesc(128, 64 * NB, tc::kFmtBF16) | kBmn;
+    const uint32_t id_t = tc::idesc(128, 64 * NB, tc::kFmtBF16) | kAmn | kBmn;
+    const uint64_t bs = mn_desc(smem_addr(stile), C::SB), bx = mn_desc(smem_addr(rtile), C::RB),
+                   bo = mn_desc(smem_addr(otile), C::RB);
     uint32_t phase = 0;
     const bool srow = row < dk && row < DK;
     float s[NC];
@@ -597,13 +618,13 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
     for (int it = 0; it < nc; ++it) {
       const int c = nc - 1 - it, st = it & 1;
       unsigned char* b = stage + st * C::STAGE;
-      unsigned char* dot = b + C::KQ + C::A2 + chain * C::VT;
-      const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + NCH * C::VT);
+      unsigned char* dot = b + C::KQ + C::A2;
+      const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + C::VT);
       const int rows = min(kC, len - c * kC);
       const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 8) put8<1>(stile, row, (c0 + j) / 8, s + j);
+        for (int j = 0; j < NC; j += 8) put8<PL, NB, C::SB>(stile, row, c0 + j, s + j);
       }
       wait(full + st, (it >> 1) & 1);
       const float eg = vec[kVecEG + i], be = vec[kVecBeta + i], el = vec[kVecEGL + i], dec = vec[kVecD];
@@ -615,12 +636,12 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
           unpack8(w, *reinterpret_cast<const uint4*>(dot + v_at<NV>(i, (c0 + j) / 8)));
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] *= f;
-          put8<1>(otile, i, (c0 + j) / 8, w);
+          put8<PL, NB, C::RB>(otile, i, c0 + j, w);
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         const uint64_t ad = tc::sdesc_k_sw128(smem_addr(b));
@@ -630,29 +651,29 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
           for (int ks = 0; ks < DK / 16; ++ks)
             tc::mma_bf16(d12, tc::sdesc_advance(ad, (ks >> 2) * 16384 + (ks & 3) * kStepK),
                          tc::sdesc_advance(bs, ks * kStepMN), id_k, ks > 0);
-          tc::mma_commit(done + chain);
+          tc::mma_commit(done);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d3, tc::sdesc_advance(aq, ks * kStepMN), tc::sdesc_advance(bo, ks * kStepMN), id_t, ks > 0);
-          if (v0 < dv) bulk_store(a.st + img * C::S, stile, C::S);
+          bulk_store(a.st + img * C::SB, stile, min(NB, (dv - v0 + 63) / 64) * C::SB);
         }
         __syncwarp();
       }
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
       float r[NC];
       if (token) {
-        ld_sum<NC, 1>(d12 + at, r);
+        ld_sum<NC, 1, 0>(d12 + at, r);
 #pragma unroll
         for (int j = 0; j < NC; ++j) r[j] *= el;
 #pragma unroll
-        for (int j = 0; j < NC; j += 8) put8<1>(rtile, i, (c0 + j) / 8, r + j);
+        for (int j = 0; j < NC; j += 8) put8<PL, NB, C::RB>(rtile, i, c0 + j, r + j);
       }
       if (issuer) bulk_store_read();      // dS1 and the last chunk's dR have left their tiles
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         // transposed: columns of T - I, then of P T (the block after each is not used)
@@ -665,31 +686,34 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d12, tc::sdesc_advance(ap, ks * kStepMN), tc::sdesc_advance(bd, ks * kStepMN), id_t, 1u);
-          tc::mma_commit(done + chain);
+          tc::mma_commit(done);
         }
         __syncwarp();
       }
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
       if (token) {
-        float x[NC];
-        ld_sum<NC, 1>(d12 + at, x);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) r[j] += x[j];
+        for (int j = 0; j < NC; j += 16) {
+          float x[16];
+          ld_sum<16, PL, C::LO>(d12 + at + j, x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[j + e] += x[e];
+        }
         const float f = -be * eg;
 #pragma unroll
         for (int j = 0; j < NC; j += 8) {
           float w[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = f * r[j + e];
-          put8<1>(rtile, i, (c0 + j) / 8, w);
-          put8<1>(utile, i, (c0 + j) / 8, r + j);
+          put8<PL, NB, C::RB>(rtile, i, c0 + j, w);
+          put8<PL, NB, C::RB>(utile, i, c0 + j, r + j);
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      chain_sync<C::CHAIN_T>(chain);
+      group_sync<1, C::WORK>();
       if (issuer) {
         tc::fence_after_sync();
         const uint64_t ak = mn_desc(smem_addr(b), DK == 128 ? 16384 : 8192);
@@ -697,9 +721,9 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_bf16(d3, tc::sdesc_advance(ak, ks * kStepMN), tc::sdesc_advance(bx, ks * kStepMN), id_t, 1u);
-          tc::mma_commit(done + chain);
+          tc::mma_commit(done);
           tc::mma_commit(empty + st);
-          if (v0 < dv) bulk_store(a.u + img * C::R, utile, C::R);
+          bulk_store(a.u + img * C::RB, utile, min(NB, (dv - v0 + 63) / 64) * C::RB);
         }
         __syncwarp();
       }
@@ -715,14 +739,15 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
       }
-      wait(done + chain, phase);
+      wait(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
-      {
-        float x[NC];
-        ld_sum<NC, 1>(d3 + at, x);
 #pragma unroll
-        for (int j = 0; j < NC; ++j) s[j] = fmaf(dec, s[j], x[j]);
+      for (int j = 0; j < NC; j += 16) {
+        float x[16];
+        ld_sum<16, PL, C::LO>(d3 + at + j, x);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
       }
     }
     if (a.final_state && srow) {
@@ -748,28 +773,26 @@ __global__ void __launch_bounds__(TcCfg<DK, NV, 1, NCH, CW, true>::THREADS) k_gd
 }
 
 // ------------------------------------------------------------------- launches
-template <int DK, int NV, int PL, int NCH, int CW>
+template <int DK, int PL, int NB, int CW>
 static cudaError_t scan(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, NV, PL, NCH, CW, false>;
-  a.ntile = (a.s.dv + NCH * NV - 1) / (NCH * NV);
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, NV, PL, NCH, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = TcCfg<DK, PL, NB, CW, false>;
+  a.ntile = (a.s.dv + C::NV - 1) / C::NV;
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_tc", st);
-  k_gdr_scan_tc<DK, NV, PL, NCH, CW>
-      <<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_tc<DK, PL, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
-template <int DK, int NV, int NCH, int CW>
+template <int DK, int NB, int CW>
 static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, NV, 1, NCH, CW, true>;
-  a.ntile = (a.s.dv + NCH * NV - 1) / (NCH * NV);
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NV, NCH, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = TcCfg<DK, 1, NB, CW, true>;
+  a.ntile = (a.s.dv + C::NV - 1) / C::NV;
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_bwd_tc", st);
-  k_gdr_scan_bwd_tc<DK, NV, NCH, CW>
-      <<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_bwd_tc<DK, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -791,30 +814,23 @@ cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
 template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  if (getenv("GDR_CW")) {
-    if (planes == 2) {
-      if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2, 1>(t, st);
-      return scan<DK, 32, 2, 1, 1>(t, st);
-    }
-    if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan<DK, 64, 1, 2, 1>(t, st);
-    return scan<DK, 64, 1, 1, 1>(t, st);
-  }
+  const int cw = getenv("GDR_CW") ? atoi(getenv("GDR_CW")) : 0;
   if (planes == 2) {
-    if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114) return scan<DK, 32, 2, 2, 2>(t, st);
-    return scan<DK, 32, 2, 1, 2>(t, st);
+    if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114)
+      return cw == 2 ? scan<DK, 2, 2, 2>(t, st) : scan<DK, 2, 2, 4>(t, st);
+    return scan<DK, 2, 1, 2>(t, st);
   }
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan<DK, 64, 1, 2, 2>(t, st);
-  return scan<DK, 64, 1, 1, 2>(t, st);
+  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114)
+    return cw == 2 ? scan<DK, 1, 2, 2>(t, st) : scan<DK, 1, 2, 4>(t, st);
+  return cw == 2 ? scan<DK, 1, 1, 4>(t, st) : scan<DK, 1, 1, 2>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  if (getenv("GDR_CW")) {
-    if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2, 1>(t, st);
-    return scan_bwd<DK, 64, 1, 1>(t, st);
-  }
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114) return scan_bwd<DK, 64, 2, 2>(t, st);
-  return scan_bwd<DK, 64, 1, 2>(t, st);
+  const int cw = getenv("GDR_CW") ? atoi(getenv("GDR_CW")) : 0;
+  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114)
+    return cw == 2 ? scan_bwd<DK, 2, 2>(t, st) : scan_bwd<DK, 2, 4>(t, st);
+  return cw == 2 ? scan_bwd<DK, 1, 4>(t, st) : scan_bwd<DK, 1, 2>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {

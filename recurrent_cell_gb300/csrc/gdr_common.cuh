@@ -46,6 +46,7 @@ struct Shape {
   long long rows;
   int hk, hv, dk, dv;
   float scale;
+  int per_seq;        // rows / n_seq
 };
 
 // Rows of sequence n.  Offsets are held inside [0, rows], so nothing outside
@@ -58,9 +59,8 @@ __device__ __forceinline__ void seq_range(const Shape& s, int n, long long* star
     *start = a;
     *len = (int)(b - a);
   } else {
-    const long long t = s.rows / s.n_seq;
-    *start = n * t;
-    *len = (int)t;
+    *start = (long long)n * s.per_seq;
+    *len = s.per_seq;
   }
 }
 
@@ -415,40 +415,52 @@ struct FwdArgs {
   int ntile;
 };
 
+// Sum of two pairs hi + lo.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x, e = ((a.x - (s - t)) + (b.x - t)) + (a.y + b.y), h = s + e;
+  return make_float2(h, e - (h - s));
+}
+
 // The decays of a chunk's head, by one warp: into `vec`, and for the block
 // G / ln 2 as pairs hi + lo and beta.
 __device__ __forceinline__ void chunk_decays(const FwdArgs& a, long long row0, int rows, int h, int lane, float2* g2,
                                              float* bet, float* vec) {
-  // Running sum of g in double: differences of G then carry no more than
-  // their own fp32 rounding, however far the sum has gone.
-  double x[2];
+  // Running sum of g as a pair of floats hi + lo: differences of G then carry
+  // no more than their own fp32 rounding, however far the sum has gone.  (In
+  // double this was the longest part of the kernel: the fp64 rate is 1/64.)
+  float2 x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 2 * lane + i;
     const float v = r < rows ? a.g[(row0 + r) * a.s.hv + h] : 0.f;
-    x[i] = v < kMinG ? kMinG : v;          // a NaN stays
+    x[i] = make_float2(v < kMinG ? kMinG : v, 0.f);          // a NaN stays
     bet[r] = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
   }
-  double run = x[0] + x[1];
+  x[1] = add2(x[0], x[1]);
+  float2 run = x[1];
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, run, d);
-    run += lane >= d ? y : 0.0;
+    const float2 y = make_float2(__shfl_up_sync(0xffffffffu, run.x, d), __shfl_up_sync(0xffffffffu, run.y, d));
+    if (lane >= d) run = add2(run, y);
   }
-  const double total = __shfl_sync(0xffffffffu, run, 31);
-  const double G[2] = {run - x[1], run};
+  const float2 total = make_float2(__shfl_sync(0xffffffffu, run.x, 31), __shfl_sync(0xffffffffu, run.y, 31));
+  float2 before = make_float2(__shfl_up_sync(0xffffffffu, run.x, 1), __shfl_up_sync(0xffffffffu, run.y, 1));
+  if (lane == 0) before = make_float2(0.f, 0.f);
+  const float2 G[2] = {add2(before, x[0]), run};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 2 * lane + i;
-    const double u = G[i] * 1.4426950408889634074;      // / ln 2
-    const float hi = (float)u, lo = (float)(u - (double)hi);
-    g2[r] = make_float2(hi, lo);
-    vec[kVecEG + r] = expf((float)G[i]);
-    vec[kVecEGL + r] = expf((float)(total - G[i]));
+    // / ln 2 in the same form
+    constexpr float kH = 1.442695041f, kL = (float)(1.4426950408889634074 - (double)kH);
+    const float p = G[i].x * kH, e = fmaf(G[i].x, kH, -p) + fmaf(G[i].x, kL, G[i].y * kH), u = p + e;
+    const float2 gu = make_float2(u, e - (u - p));
+    g2[r] = gu;
+    vec[kVecEG + r] = expf(G[i].x + G[i].y);
+    vec[kVecEGL + r] = expf((total.x - G[i].x) + (total.y - G[i].y));
     vec[kVecBeta + r] = bet[r];
-    reinterpret_cast<float2*>(vec + kVecG2)[r] = make_float2(hi, lo);
+    reinterpret_cast<float2*>(vec + kVecG2)[r] = gu;
   }
-  if (lane == 0) vec[kVecD] = expf((float)total);
+  if (lane == 0) vec[kVecD] = expf(total.x + total.y);
 }
 
 // T = (I + A)^{-1} in place of A, 64 x 64 and strictly lower triangular in fp32

@@ -28,7 +28,7 @@ constexpr uint32_t kStepK = 32, kStepMN = 2048;    // bytes of 16 along K
 
 __device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
 
-// N accumulator columns of this warp's lanes; PL = 2: the columns 32 on, the
+// N accumulator columns of this warp's lanes; PL = 2: the columns LO on, the
 // products of the lo plane, added.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t t, float* v) {
@@ -53,12 +53,12 @@ __device__ __forceinline__ void ld_wait(float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i])::"memory");
 }
-template <int N, int PL>
+template <int N, int PL, int LO>
 __device__ __forceinline__ void ld_sum(uint32_t t, float (&v)[N]) {
   ld_cols<N>(t, v);
   if constexpr (PL == 2) {
     float w[N];
-    ld_cols<N>(t + 32, w);
+    ld_cols<N>(t + LO, w);
     ld_wait<N>(v);
     ld_wait<N>(w);
 #pragma unroll
@@ -81,26 +81,6 @@ __device__ __forceinline__ void unpack8(float* v, const uint4& u) {
   v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
   v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
-// Eight values into chunk `ch` of a tile row; PL = 2: their remainders four
-// chunks on (the second 32 columns).
-template <int PL>
-__device__ __forceinline__ void put8(unsigned char* tile, int row, int ch, const float* v) {
-  const uint4 h = pack8(v);
-  *reinterpret_cast<uint4*>(tile + chunk_at(row, ch)) = h;
-  if constexpr (PL == 2) {
-    float hv[8], l[8];
-    unpack8(hv, h);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = v[i] - hv[i];
-    *reinterpret_cast<uint4*>(tile + chunk_at(row, ch + 4)) = pack8(l);
-  }
-}
-
-template <int THREADS>
-__device__ __forceinline__ void chain_sync(int chain) {
-  asm volatile("bar.sync %0, %1;" ::"r"(chain + 1), "n"(THREADS) : "memory");
-}
-
 // Shared -> global copy of a tile by the calling thread, and the wait until
 // its copies have read their tiles.
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -111,10 +91,11 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void bulk_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// Row r, 16-byte piece ch of a chain's V, dO or output tile of NV columns.
+// Row r, 16-byte piece ch of a V, dO or output tile of NV columns (blocks of 64).
 template <int NV>
 __device__ __forceinline__ uint32_t v_at(int r, int ch) {
-  return NV == 64 ? chunk_at(r, ch) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  if (NV < 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+  return (NV > 64 ? (ch >> 3) * 8192 : 0) + chunk_at(r, ch & 7);
 }
 // The warp's 32 rows (from r0) x NC columns (from piece ch0) of such a tile to
 // rows of global memory, 16 bytes a lane, whole rows side by side.  Rows from
