@@ -30,6 +30,7 @@ struct GradArgs {
   bf16 *gq, *gk, *gg, *gbeta;
   const unsigned char *s0, *u, *ds, *dr;
   const float* vec;
+  int tma;
 };
 
 template <int DK>
@@ -53,7 +54,7 @@ struct Chunk {
 };
 
 template <int DK>
-__global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a) {
+__global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ unsigned char smem_raw[];
   using C = GradCfg<DK>;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
   const int group = a.s.hv / a.s.hk, dk = a.s.dk, dv = a.s.dv, nt = (dv + 63) / 64;
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) {
-      tc::mbar_init(full + i, C::FETCH + (i < 2 ? 1 : 0));
+      tc::mbar_init(full + i, C::FETCH + 1);
       tc::mbar_init(empty + i, C::WORK / 32 + (i < 2 ? 1 : 0));        // K and Q: dk and dq lie in their place
     }
     tc::mbar_init(done, 1);
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
       if (!slot_chunk(a.s, slot, &n, &start, &len, &c)) continue;
       const long long row0 = start + (long long)c * kC;
       const int rows = min(kC, len - c * kC);
+      const bool boxes = a.tma && rows == kC;    // else 16-byte copies: rows past a sequence's end are zeros
       for (int g = 0; g < group; ++g) {
         const int h = hk * group + g;
         const long long id = slot * a.s.hv + h;
@@ -148,13 +150,21 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
           claim(st, it >> 1);
           unsigned char* b = stage + st * C::STAGE;
           if (ft == 0) {
-            bar_arrive_tx(full + st, 2 * C::T + 2 * C::S + kVec * 4);
+            bar_arrive_tx(full + st, 2 * C::T + 2 * C::S + kVec * 4 + (boxes ? 2 * C::T : 0));
+            if (boxes) {
+              tma_tile(b + C::OFF_DO, &maps.go, t * 64, h, (int)row0, full + st);
+              tma_tile(b + C::OFF_V, &maps.v, t * 64, h, (int)row0, full + st);
+            }
             bulk_load(b, a.u + (id * nt + t) * C::T, C::T, full + st);
             bulk_load(b + C::T, a.dr + (id * nt + t) * C::T, C::T, full + st);
             bulk_load(b + C::OFF_S0, a.s0 + (id * nt + t) * C::S, C::S, full + st);
             bulk_load(b + C::OFF_DS, a.ds + (id * nt + t) * C::S, C::S, full + st);
             bulk_load(b + C::OFF_VEC, a.vec + id * kVec, kVec * 4, full + st);
             *reinterpret_cast<Chunk*>(b + C::OFF_VEC + kVec * 4) = Chunk{row0, slot, rows, hk};
+          }
+          if (boxes) {
+            bar_arrive(full + st);
+            continue;
           }
           const int ch = ft & 7, col = t * 64 + ch * 8;
 #pragma unroll
@@ -170,6 +180,20 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
           ++kqi;
           last = Chunk{row0, slot, rows, hk};
           const bf16 *k = a.k + row0 * a.ldk + (long long)hk * dk, *q = a.q + row0 * a.ldq + (long long)hk * dk;
+          if (ft == 0) {
+            tc::fence_proxy_async_smem();        // dk and dq were written where boxes now go
+            bar_arrive_tx(full + 2, boxes ? C::KQ : 0);
+            if (boxes)
+#pragma unroll
+              for (int x = 0; x < C::ATOMS; ++x) {
+                tma_tile(kq + x * C::T, &maps.k, x * 64, hk, (int)row0, full + 2);
+                tma_tile(kq + (C::ATOMS + x) * C::T, &maps.q, x * 64, hk, (int)row0, full + 2);
+              }
+          }
+          if (boxes) {
+            bar_arrive(full + 2);
+            continue;
+          }
           constexpr int PER = DK / 8;
           const int ch = ft % PER;
           unsigned char* d = kq + (ch >> 3) * C::T;
@@ -434,13 +458,18 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a
 }
 
 template <int DK>
-static cudaError_t launch(const GradArgs& g, cudaStream_t st) {
+static cudaError_t launch(GradArgs g, cudaStream_t st) {
   using C = GradCfg<DK>;
   const long long items = slot_count(g.s.rows, g.s.n_seq) * g.s.hk;
   cudaError_t e = cudaFuncSetAttribute(k_gdr_grad_tc<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
   if (e != cudaSuccess) return e;
+  Maps m;
+  g.tma = tile_map(&m.q, g.q, g.s.dk, g.s.hk, g.s.rows, g.ldq, 64) &&
+          tile_map(&m.k, g.k, g.s.dk, g.s.hk, g.s.rows, g.ldk, 64) &&
+          tile_map(&m.v, g.v, g.s.dv, g.s.hv, g.s.rows, g.ldv, 64) &&
+          tile_map(&m.go, g.go, g.s.dv, g.s.hv, g.s.rows, (long long)g.s.hv * g.s.dv, 64);
   TraceScope tr("k_gdr_grad_tc", st);
-  k_gdr_grad_tc<DK><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g);
+  k_gdr_grad_tc<DK><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g, m);
   return cudaGetLastError();
 }
 

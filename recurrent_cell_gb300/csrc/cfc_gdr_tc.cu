@@ -238,7 +238,7 @@ struct TcArgs {
   const float* vec;
   // per chunk and 64 value columns, as operand tiles: S0 and U (backward: dS1, dR), or NULL
   unsigned char *st, *u;
-  int ntile;
+  int ntile, tma;
 };
 
 // The fetching warps' loop.  The chunk before last's output rows (o, or the
@@ -246,7 +246,7 @@ struct TcArgs {
 // then the next chunk's tiles come into that stage: the fetching threads with 16-byte copies (rows past the end and
 // columns past d_k, d_v as zeros) and the prepared images by bulk copy.
 template <int DK, class C, class W>
-__device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* stage, uint64_t* full, uint64_t* empty,
+__device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, unsigned char* stage, uint64_t* full, uint64_t* empty,
                                              uint64_t* outs, int ft, int h, long long start, int len, long long slot0,
                                              int v0, bool backwards, W wait) {
   constexpr int NV = C::NV;
@@ -273,44 +273,60 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, unsigned char* sta
     if (i >= nc) continue;
     const int rows = min(kC, len - c * kC);
     const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
+    const bool boxes = a.tma && rows == kC;
     if (ft == 0) {
-      bar_arrive_tx(full + st, C::A2 + kVec * 4);
+      tc::fence_proxy_async_smem();      // output rows were written where boxes now go
+      bar_arrive_tx(full + st, C::A2 + kVec * 4 + (boxes ? C::KQ + C::VT : 0));
+      if (boxes) {
+        const int row = (int)(start + r0);
+#pragma unroll
+        for (int x = 0; x < C::ATOMS; ++x) {
+          tma_tile(b + x * 16384, &maps.k, x * 64, hq, row, full + st);
+          tma_tile(b + x * 16384 + 8192, &maps.q, x * 64, hq, row, full + st);
+        }
+        constexpr int VB = NV < 64 ? NV : 64;
+#pragma unroll
+        for (int x = 0; x < NV / VB; ++x)
+          tma_tile(b + C::KQ + C::A2 + x * 8192, &maps.v, v0 + x * VB, h, row, full + st);
+      }
       bulk_load(b + C::KQ, a.a2 + id * 32768, C::A2, full + st);
       bulk_load(b + C::KQ + C::A2 + C::VT, a.vec + id * kVec, kVec * 4, full + st);
     }
-    {
-      constexpr int PER = DK / 8, STEP = C::FETCH / PER;      // 16-byte pieces of a row; rows a pass
-      const int ch = ft % PER, rr = ft / PER;
-      const bool in = ch * 8 < dk;
-      unsigned char* d = b + (ch >> 3) * 16384;
+    if (!boxes) {
+      {
+        constexpr int PER = DK / 8, STEP = C::FETCH / PER;      // 16-byte pieces of a row; rows a pass
+        const int ch = ft % PER, rr = ft / PER;
+        const bool in = ch * 8 < dk;
+        unsigned char* d = b + (ch >> 3) * 16384;
 #pragma unroll 4
-      for (int r = rr; r < kC; r += STEP) {
-        const bool on = in && r < rows;
-        cp16(d + chunk_at(r, ch & 7), on ? k + (r0 + r) * a.ldk + ch * 8 : k, on);
-        cp16(d + 8192 + chunk_at(r, ch & 7), on ? q + (r0 + r) * a.ldq + ch * 8 : q, on);
+        for (int r = rr; r < kC; r += STEP) {
+          const bool on = in && r < rows;
+          cp16(d + chunk_at(r, ch & 7), on ? k + (r0 + r) * a.ldk + ch * 8 : k, on);
+          cp16(d + 8192 + chunk_at(r, ch & 7), on ? q + (r0 + r) * a.ldq + ch * 8 : q, on);
+        }
       }
-    }
-    {
-      constexpr int PER = NV / 8, STEP = C::FETCH / PER;
-      const int ch = ft % PER;
-      const bool in = ch * 8 < vn;
-      unsigned char* d = b + C::KQ + C::A2;
+      {
+        constexpr int PER = NV / 8, STEP = C::FETCH / PER;
+        const int ch = ft % PER;
+        const bool in = ch * 8 < vn;
+        unsigned char* d = b + C::KQ + C::A2;
 #pragma unroll 4
-      for (int r = ft / PER; r < kC; r += STEP) {
-        const bool on = in && r < rows;
-        cp16(d + v_at<NV>(r, ch), on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
+        for (int r = ft / PER; r < kC; r += STEP) {
+          const bool on = in && r < rows;
+          cp16(d + v_at<NV>(r, ch), on ? v + (r0 + r) * a.ldv + ch * 8 : v, on);
+        }
       }
+      cp_commit();
+      cp_wait<0>();
+      tc::fence_proxy_async_smem();      // read by the tensor cores
     }
-    cp_commit();
-    cp_wait<0>();
-    tc::fence_proxy_async_smem();      // read by the tensor cores
     bar_arrive(full + st);
   }
 }
 
 // ------------------------------------------------------------------- forward
 template <int DK, int PL, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a) {
+__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
   using C = TcCfg<DK, PL, NB, CW, false>;
   constexpr int NC = C::NC, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
   };
 
   if (tid >= C::WORK) {
-    fetch_chunks<DK, C>(a, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+    fetch_chunks<DK, C>(a, maps, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
                                      tile * NV, false, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
@@ -547,7 +563,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
 template <int DK, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a) {
+__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
   using C = TcCfg<DK, 1, NB, CW, true>;
   constexpr int PL = 1, NC = C::NC, NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
@@ -588,7 +604,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
   };
 
   if (tid >= C::WORK) {
-    fetch_chunks<DK, C>(a, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+    fetch_chunks<DK, C>(a, maps, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
                                     tile * NV, true, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
@@ -773,6 +789,33 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
 }
 
 // ------------------------------------------------------------------- launches
+bool tile_map(CUtensorMap* m, const void* base, int width, int heads, long long rows, long long ld, int box) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  if (!fn || !base || rows < 1) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t boxes[3] = {(cuuint32_t)box, 1u, (cuuint32_t)kC}, es[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int maps_of(const TcArgs& a, int v_box, Maps* m) {
+  return tile_map(&m->q, a.q, a.s.dk, a.s.hk, a.s.rows, a.ldq, 64) &&
+         tile_map(&m->k, a.k, a.s.dk, a.s.hk, a.s.rows, a.ldk, 64) &&
+         tile_map(&m->v, a.v, a.s.dv, a.s.hv, a.s.rows, a.ldv, v_box);
+}
+
 template <int DK, int PL, int NB, int CW>
 static cudaError_t scan(TcArgs a, cudaStream_t st) {
   using C = TcCfg<DK, PL, NB, CW, false>;
@@ -780,8 +823,10 @@ static cudaError_t scan(TcArgs a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
+  Maps m;
+  a.tma = maps_of(a, C::NV < 64 ? C::NV : 64, &m);
   TraceScope tr("k_gdr_scan_tc", st);
-  k_gdr_scan_tc<DK, PL, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_tc<DK, PL, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
   return cudaGetLastError();
 }
 template <int DK, int NB, int CW>
@@ -791,8 +836,10 @@ static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
+  Maps m;
+  a.tma = maps_of(a, 64, &m);
   TraceScope tr("k_gdr_scan_bwd_tc", st);
-  k_gdr_scan_bwd_tc<DK, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_bwd_tc<DK, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
   return cudaGetLastError();
 }
 

@@ -7,10 +7,28 @@
 // an MN-major one its rows are: the same tile serves both.
 #pragma once
 
+#include <cuda.h>
+
 #include "gdr_common.cuh"
 
 namespace cfc {
 namespace gdr {
+
+// Tensor maps of [rows, heads, width] bf16 tensors: boxes of up to 64 columns
+// of one head by a chunk's 64 rows, zeros past the width.
+struct Maps {
+  CUtensorMap q, k, v, go;
+};
+// False: the driver cannot say (the kernels then copy by 16 bytes).
+bool tile_map(CUtensorMap* m, const void* base, int width, int heads, long long rows, long long ld, int box);
+
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int col, int head, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
 
 using bf16 = __nv_bfloat16;
 
