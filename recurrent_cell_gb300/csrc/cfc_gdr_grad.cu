@@ -54,7 +54,7 @@ struct Chunk {
 };
 
 template <int DK>
-__global__ void __launch_bounds__(GradCfg<DK>::THREADS) k_gdr_grad_tc(GradArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ unsigned char smem_raw[];
   using C = GradCfg<DK>;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;

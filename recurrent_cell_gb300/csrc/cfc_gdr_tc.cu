@@ -326,9 +326,9 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
 
 // ------------------------------------------------------------------- forward
 template <int DK, int PL, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS, 1) k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
   using C = TcCfg<DK, PL, NB, CW, false>;
-  constexpr int NC = C::NC, NV = C::NV;
+  constexpr int NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;      // columns a thread; at a time
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
@@ -361,6 +361,12 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
   bool lost = false;        // a wait gave up: no more waiting, the results are void
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!lost && !tc::mbar_wait(bar, parity, kPolls)) {
+      lost = true;
+      atomicExch(&g_gdr_tc_error, 1);
+    }
+  };
+  auto poll = [&](uint64_t* bar, uint32_t parity) {
+    if (!lost && !poll_wait(bar, parity, kPollsBusy)) {
       lost = true;
       atomicExch(&g_gdr_tc_error, 1);
     }
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
 #pragma unroll
         for (int j = 0; j < NC; j += 8) put8<PL, NB, C::SB>(stile, row, c0 + j, s + j);
       }
-      wait(full + st, (c >> 1) & 1);
+      if (c == 0 && issuer) wait(full, 0);
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       group_sync<1, C::WORK>();
@@ -436,21 +442,21 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
         }
       }
       const float f = token ? -be * eg : a.s.scale * eg;
-      wait(done, phase);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < NC; j += 16) {
-        float x[16];
-        ld_sum<16, PL, C::LO>(d12 + at + j, x);
+      for (int j = 0; j < NC; j += NP) {
+        float x[NP];
+        ld_sum<NP, PL, C::LO>(d12 + at + j, x);
         if (token) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[j + e] = fmaf(f, x[e], r[j + e]);
-          put8<PL, NB, C::RB>(rtile, i, c0 + j, r + j);
-          put8<PL, NB, C::RB>(rtile, i, c0 + j + 8, r + j + 8);
+          for (int e = 0; e < NP; ++e) r[j + e] = fmaf(f, x[e], r[j + e]);
+#pragma unroll
+          for (int e = 0; e < NP; e += 8) put8<PL, NB, C::RB>(rtile, i, c0 + j + e, r + j + e);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[j + e] = f * x[e];
+          for (int e = 0; e < NP; ++e) r[j + e] = f * x[e];
         }
       }
       if (PL == 1 && issuer) bulk_store_read();      // S and the last chunk's U have left their tiles
@@ -474,15 +480,15 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
         }
         __syncwarp();
       }
-      wait(done, phase);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < NC; j += 16) {
-        float x[16];
-        ld_sum<16, PL, C::LO>(d12 + at + j, x);
+      for (int j = 0; j < NC; j += NP) {
+        float x[NP];
+        ld_sum<NP, PL, C::LO>(d12 + at + j, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[j + e] += x[e];
+        for (int e = 0; e < NP; ++e) r[j + e] += x[e];
       }
       if (token) {
 #pragma unroll
@@ -522,15 +528,17 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
       }
-      wait(done, phase);
+      // the next chunk's tiles, long there: the block's barrier passes it on
+      if (issuer && c + 1 < nc) wait(full + (st ^ 1), ((c + 1) >> 1) & 1);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < NC; j += 16) {
-        float x[16];
-        ld_sum<16, PL, C::LO>(d3 + at + j, x);
+      for (int j = 0; j < NC; j += NP) {
+        float x[NP];
+        ld_sum<NP, PL, C::LO>(d3 + at + j, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
+        for (int e = 0; e < NP; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
       }
     }
     if (a.final_state && srow) {
@@ -563,9 +571,9 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS) k_gdr_s
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
 template <int DK, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS, 1) k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
   using C = TcCfg<DK, 1, NB, CW, true>;
-  constexpr int PL = 1, NC = C::NC, NV = C::NV;
+  constexpr int PL = 1, NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
@@ -598,6 +606,12 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
   bool lost = false;        // a wait gave up: no more waiting, the results are void
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!lost && !tc::mbar_wait(bar, parity, kPolls)) {
+      lost = true;
+      atomicExch(&g_gdr_tc_error, 1);
+    }
+  };
+  auto poll = [&](uint64_t* bar, uint32_t parity) {
+    if (!lost && !poll_wait(bar, parity, kPollsBusy)) {
       lost = true;
       atomicExch(&g_gdr_tc_error, 1);
     }
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
         }
         __syncwarp();
       }
-      wait(done, phase);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
       float r[NC];
@@ -706,16 +720,16 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
         }
         __syncwarp();
       }
-      wait(done, phase);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
       if (token) {
 #pragma unroll
-        for (int j = 0; j < NC; j += 16) {
-          float x[16];
-          ld_sum<16, PL, C::LO>(d12 + at + j, x);
+        for (int j = 0; j < NC; j += NP) {
+          float x[NP];
+          ld_sum<NP, PL, C::LO>(d12 + at + j, x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[j + e] += x[e];
+          for (int e = 0; e < NP; ++e) r[j + e] += x[e];
         }
         const float f = -be * eg;
 #pragma unroll
@@ -755,15 +769,15 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS) k_gdr_sca
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
       }
-      wait(done, phase);
+      poll(done, phase);
       phase ^= 1;
       tc::fence_after_sync();
 #pragma unroll
-      for (int j = 0; j < NC; j += 16) {
-        float x[16];
-        ld_sum<16, PL, C::LO>(d3 + at + j, x);
+      for (int j = 0; j < NC; j += NP) {
+        float x[NP];
+        ld_sum<NP, PL, C::LO>(d3 + at + j, x);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
+        for (int e = 0; e < NP; ++e) s[j + e] = fmaf(dec, s[j + e], x[e]);
       }
     }
     if (a.final_state && srow) {
@@ -865,7 +879,7 @@ static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   if (planes == 2) {
     if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114)
       return cw == 2 ? scan<DK, 2, 2, 2>(t, st) : scan<DK, 2, 2, 4>(t, st);
-    return scan<DK, 2, 1, 2>(t, st);
+    return cw == 2 ? scan<DK, 2, 1, 2>(t, st) : scan<DK, 2, 1, 4>(t, st);
   }
   if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114)
     return cw == 2 ? scan<DK, 1, 2, 2>(t, st) : scan<DK, 1, 2, 4>(t, st);

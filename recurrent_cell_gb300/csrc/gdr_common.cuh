@@ -130,7 +130,7 @@ template <int ID, int THREADS>
 __device__ __forceinline__ void group_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
-constexpr uint32_t kPolls = 1u << 20;   // of a bounded wait
+constexpr uint32_t kPolls = 1u << 20, kPollsBusy = 1u << 24;   // of a bounded wait that suspends, that polls
 
 // rows x cols elements (cols x sizeof(E) a multiple of 16) from rows `stride`
 // apart into rows `ld` apart; rows past row_end and columns past col_end are

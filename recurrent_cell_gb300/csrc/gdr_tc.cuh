@@ -50,9 +50,19 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128
 // products of the lo plane, added.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t t, float* v) {
-  static_assert(N % 16 == 0, "columns");
+  static_assert(N % 16 == 0 || N == 8, "columns");
+  if constexpr (N == 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
 #pragma unroll
-  for (int j = 0; j < N; j += 16) {
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j + 16 <= N; j += 16) {
     uint32_t r[16];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -84,6 +94,21 @@ __device__ __forceinline__ void ld_sum(uint32_t t, float (&v)[N]) {
   } else {
     ld_wait<N>(v);
   }
+}
+
+// Bounded wait by polling: the products' round trips are the serial passes'
+// time, and a poll answers some 80 cycles sooner than a suspended wait.
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, uint32_t max_polls) {
+  for (uint32_t i = 0; i < max_polls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
