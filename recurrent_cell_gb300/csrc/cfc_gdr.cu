@@ -504,6 +504,7 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
   take(&w.off_t, slots * (bf ? kImage : kC * kLdt<MFp32> * sizeof(float)));
   take(&w.off_p, bf ? 0 : slots * kC * kLdt<MFp32> * sizeof(float));
   take(&w.off_vec, slots * kVec * 4);
+  take(&w.off_order, bf && n_seq <= kMaxOrder ? n_seq * sizeof(int) : 0);
   if (save) {
     const size_t wk = bf ? (dk <= 64 ? 64 : 128) : dk, wv = bf ? (dv + 63) / 64 * 64 : dv;
     take(&w.off_s0, slots * wk * wv * e);
@@ -552,6 +553,7 @@ cudaError_t launch_gdr_forward(const GdrArgs& g, cudaStream_t st) {
   a.g = g.g; a.beta = g.beta; a.init = g.init; a.final_state = g.final_state; a.o = g.o;
   a.t = g.ws + w.off_t; a.p = g.ws + w.off_p;
   a.vec = reinterpret_cast<float*>(g.ws + w.off_vec);
+  if (g.off && g.math == CFC_MATH_BF16 && g.n_seq <= kMaxOrder) a.order = reinterpret_cast<int*>(g.ws + w.off_order);
   a.save = g.save;
   if (g.save) { a.s0 = g.ws + w.off_s0; a.u = g.ws + w.off_u; }
   if (g.math == CFC_MATH_BF16) {

@@ -13,9 +13,10 @@
 // with dA = -L o D2 strictly below the diagonal and dP = scale L o D2 up to it,
 // each in two bf16 planes: dg is a difference of their sums.  S0, U, dS1 and dR
 // come as operand tiles, as the serial passes left them; with the inputs they
-// are the traffic, which bounds the kernel (about 160 KB a chunk and head in,
-// 32 KB out).  Fetching warps keep two 64-column stages and the next chunk's K
-// and Q on their way while the others compute.
+// are the traffic (about 160 KB a chunk and head in, 32 KB out).  Two warps
+// keep two 64-column stages and the next chunk's K and Q on their way, one
+// issues the products, eight do the arithmetic between them; a head's first
+// products run under the last one's end.
 #include "gdr_tc.cuh"
 
 namespace cfc {
@@ -35,7 +36,7 @@ struct GradArgs {
 
 template <int DK>
 struct GradCfg {
-  static constexpr int ATOMS = DK / 64, FETCH = 128, WORK = 256, THREADS = WORK + FETCH;
+  static constexpr int ATOMS = DK / 64, FETCH = 64, WORK = 256, THREADS = WORK + FETCH + 32;
   static constexpr uint32_t T = 8192;                   // 64 rows x 128 bytes
   static constexpr uint32_t S = DK * 128u;
   // a stage: U, dR, dO, V, S0, dS1 of 64 value columns, the vectors
@@ -53,13 +54,15 @@ struct Chunk {
   int rows, hk;           // rows < 0: no more
 };
 
-template <int DK>
+// SHARED: several value heads to a key head, dq and dk added up in registers.
+template <int DK, bool SHARED>
 __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ unsigned char smem_raw[];
   using C = GradCfg<DK>;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);      // stages 0, 1; K and Q
   uint64_t *empty = full + 3, *done = full + 6;            // done: D1 - D3; D4, D5
+  uint64_t *ops_in = full + 8, *acc_out = full + 9;        // dA, dP are there; the accumulators have been read
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
   unsigned char* stage = base + 1024;
   unsigned char* ops = stage + 2 * C::STAGE;
@@ -75,6 +78,8 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     }
     tc::mbar_init(done, 1);
     tc::mbar_init(done + 1, 1);
+    tc::mbar_init(ops_in, C::WORK / 32);
+    tc::mbar_init(acc_out, C::WORK / 32);
     tc::mbar_init_fence();
   }
   if (warp == 0) tc::tmem_alloc(tmem_at, 512);
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     }
   };
 
-  if (tid >= C::WORK) {     // ---- the fetching warps
+  if (tid >= C::WORK && tid < C::WORK + C::FETCH) {     // ---- the fetching warps
     const int ft = tid - C::WORK;
     uint64_t* pending = nullptr;           // copies under way whose arrival is still to come
     auto flush = [&]() {
@@ -121,14 +126,15 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     auto rows_of = [&](const Chunk& c) {
       flush();
       wait(empty + 2, (kqi - 1) & 1);
-      const int w = ft >> 5, r0 = (w & 1) * 32;
-      const bool q = w >= 2;
+      const bool q = ft >= 32;             // a warp each
+#pragma unroll 1
+      for (int r0 = 0; r0 < kC; r0 += 32)
 #pragma unroll
-      for (int b = 0; b < C::ATOMS; ++b)
-        rows_out<64, 64>((q ? a.gq : a.gk) + (c.row0 * a.s.hk + c.hk) * dk + b * 64, (long long)a.s.hk * dk,
-                         kq + (q ? C::ATOMS + b : b) * C::T, r0, 0, c.rows, dk - b * 64, lane);
+        for (int b = 0; b < C::ATOMS; ++b)
+          rows_out<64, 64>((q ? a.gq : a.gk) + (c.row0 * a.s.hk + c.hk) * dk + b * 64, (long long)a.s.hk * dk,
+                           kq + (q ? C::ATOMS + b : b) * C::T, r0, 0, c.rows, dk - b * 64, lane);
       // the tiles are filled again by other threads
-      asm volatile("bar.sync 2, 128;" ::: "memory");
+      group_sync<2, C::FETCH>();
     };
     const long long ldo = (long long)a.s.hv * dv;
     const long long items = slot_count(a.s.rows, a.s.n_seq) * a.s.hk;
@@ -215,50 +221,88 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
       bar_arrive_tx(full + (it & 1), 0);
     }
     bar_arrive(full + (it & 1));
+  } else if (tid >= C::WORK) {   // ---- the warp that issues the products
+    const uint32_t d1 = tmem, d3 = tmem + 128, d4 = tmem + 256, d5 = tmem + 384, d2 = d5;
+    const uint32_t id_dk = tc::idesc(128, DK, tc::kFmtBF16), id_64 = tc::idesc(128, 64, tc::kFmtBF16);
+    const uint64_t ap = tc::sdesc_k_sw128(smem_addr(ops)), tp = mn_desc(smem_addr(ops + C::T), C::T),
+                   tm = mn_desc(smem_addr(ops + 2 * C::T), C::T), bk = mn_desc(smem_addr(kq), C::T),
+                   bq = mn_desc(smem_addr(kq + C::ATOMS * C::T), C::T);
+    uint32_t it = 0, kqi = 0;
+    int g = 0;
+    for (uint32_t heads = 0;; ++heads) {
+      for (int t = 0; t < nt; ++t, ++it) {
+        const int st = it & 1;
+        unsigned char* b = stage + st * C::STAGE;
+        wait(full + st, (it >> 1) & 1);
+        if (t == 0) {
+          if (lost || reinterpret_cast<const Chunk*>(b + C::OFF_VEC + kVec * 4)->rows < 0) goto over;
+          if (heads > 0) wait(acc_out, (heads - 1) & 1);
+        }
+        tc::fence_after_sync();
+        const uint64_t au = tc::sdesc_k_sw128(smem_addr(b)), ar = tc::sdesc_k_sw128(smem_addr(b + C::T)),
+                       b0 = tc::sdesc_k_sw128(smem_addr(b + C::OFF_S0)), bd = tc::sdesc_k_sw128(smem_addr(b + C::OFF_DS));
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t o = ks * kStepK, ac = (t > 0 || ks > 0) ? 1u : 0u;
+            tc::mma_bf16(d2, tc::sdesc_advance(ar, o), tc::sdesc_advance(au, o), id_64, ac);
+            tc::mma_bf16(d1, tc::sdesc_advance(ar, o), tc::sdesc_advance(b0, o), id_dk, ac);
+            tc::mma_bf16(d3, tc::sdesc_advance(au, o), tc::sdesc_advance(bd, o), id_dk, ac);
+          }
+          tc::mma_commit(empty + st);
+          if (t == nt - 1) tc::mma_commit(done);
+        }
+        __syncwarp();
+      }
+      wait(ops_in, heads & 1);
+      if (g == 0) wait(full + 2, kqi & 1);
+      if (++g == group) {
+        g = 0;
+        ++kqi;
+      }
+      tc::fence_after_sync();
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t lo = pl * 3 * C::T, ac = pl + ks > 0 ? 1u : 0u;
+            const uint64_t kd = tc::sdesc_advance(bk, ks * kStepMN), qd = tc::sdesc_advance(bq, ks * kStepMN);
+            tc::mma_bf16(d4, tc::sdesc_advance(ap, lo + ks * kStepK), kd, id_dk | kBmn, ac);
+            tc::mma_bf16(d5, tc::sdesc_advance(tp, lo + ks * kStepMN), qd, id_dk | kAmn | kBmn, ac);
+            tc::mma_bf16(d5, tc::sdesc_advance(tm, lo + ks * kStepMN), kd, id_dk | kAmn | kBmn, 1u);
+          }
+        tc::mma_commit(done + 1);
+      }
+      __syncwarp();
+    }
+  over:;
   } else {
     constexpr int NC = DK / 2;             // columns of dq, dk a thread
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane, i = row & 63;
     const bool lower = quad < 2;
     const uint32_t d1 = tmem, d3 = tmem + 128, d4 = tmem + 256, d5 = tmem + 384, d2 = d5;
     const uint32_t at = (uint32_t)(quad * 32) << 16;
-    const uint32_t id_dk = tc::idesc(128, DK, tc::kFmtBF16), id_64 = tc::idesc(128, 64, tc::kFmtBF16);
     unsigned char* krow = kq + (DK == 128 ? cg * C::T : 0);          // the block of this thread's columns
-    unsigned char* qrow = krow + C::ATOMS * C::T;
+    unsigned char* tile = lower ? krow : krow + C::ATOMS * C::T;     // K, then dk; Q, then dq
     const int ch0 = DK == 128 ? 0 : cg * 4;
-    uint32_t it = 0, kqi = 0, heads = 0;
-    float acc[NC];                         // dk of the chunk (rows 0-63), dq
-    for (int g = 0;; ++heads) {
+    uint32_t it = 0;
+    float acc[SHARED ? NC : 1];            // dk of the chunk (rows 0-63), dq
+    int g = 0;
+    for (uint32_t heads = 0;; ++heads) {
       wait(full + (it & 1), (it >> 1) & 1);
       const Chunk ck = *reinterpret_cast<const Chunk*>(stage + (it & 1) * C::STAGE + C::OFF_VEC + kVec * 4);
       if (ck.rows < 0 || lost) break;
       const float* vec = reinterpret_cast<const float*>(stage + (it & 1) * C::STAGE + C::OFF_VEC);
       const float eg = vec[kVecEG + i], el = vec[kVecEGL + i], be = vec[kVecBeta + i], dec = vec[kVecD];
+      const float2 be2 = *reinterpret_cast<const float2*>(vec + kVecBeta + 2 * lane);
       if (tid < 128) gs[tid] = vec[kVecG2 + tid];
-      float ss = 0.f, dr = 0.f;
+      float ss = 0.f, dr = 0.f;            // <S0, dS1> and dR.v, while the products run
       for (int t = 0; t < nt; ++t, ++it) {
         const int st = it & 1;
         unsigned char* b = stage + st * C::STAGE;
         if (t > 0) wait(full + st, (it >> 1) & 1);
-        if (warp == 0) {
-          tc::fence_after_sync();
-          const uint64_t au = tc::sdesc_k_sw128(smem_addr(b)), ar = tc::sdesc_k_sw128(smem_addr(b + C::T)),
-                         b0 = tc::sdesc_k_sw128(smem_addr(b + C::OFF_S0)),
-                         bd = tc::sdesc_k_sw128(smem_addr(b + C::OFF_DS));
-          if (tc::elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint32_t o = ks * kStepK, ac = (t > 0 || ks > 0) ? 1u : 0u;
-              tc::mma_bf16(d2, tc::sdesc_advance(ar, o), tc::sdesc_advance(au, o), id_64, ac);
-              tc::mma_bf16(d1, tc::sdesc_advance(ar, o), tc::sdesc_advance(b0, o), id_dk, ac);
-              tc::mma_bf16(d3, tc::sdesc_advance(au, o), tc::sdesc_advance(bd, o), id_dk, ac);
-            }
-            tc::mma_commit(empty + st);
-            if (t == nt - 1) tc::mma_commit(done);
-          }
-          __syncwarp();
-        }
-        // <S0, dS1> and dR.v meanwhile
-#pragma unroll
+#pragma unroll 2
         for (int e = 0; e < DK * 8 / C::WORK; ++e) {
           const uint32_t o = (e * C::WORK + tid) * 16;
           float x[8], y[8];
@@ -287,131 +331,124 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
       wait(done, heads & 1);
       tc::fence_after_sync();
       {
-        float x[32];
-        ld_sum<32, 1, 0>(d2 + at + cg * 32, x);
         const float2 gi = reinterpret_cast<const float2*>(gs)[i];
         const float f = lower ? -1.f : a.s.scale;
         const int end = cg * 32 <= i ? (lower ? i : i + 1) : 0;    // columns that count
+        unsigned char* to = ops + (lower ? 0 : C::T);
+#pragma unroll 1
+        for (int j = 0; j < 32; j += 16) {
+          float x[16];
+          ld_sum<16, 1, 0>(d2 + at + cg * 32 + j, x);
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          float w[8];
+          for (int z = 0; z < 16; z += 8) {
+            float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int col = cg * 32 + j + e;
-            const float4 gj = *reinterpret_cast<const float4*>(gs + 2 * col);
-            const float w0 = f * x[j + e] * MBf16::exp2((gi.x - gj.x) + (gi.y - gj.y));
-            const float w1 = f * x[j + e + 1] * MBf16::exp2((gi.x - gj.z) + (gi.y - gj.w));
-            w[e] = col < end ? w0 : 0.f;
-            w[e + 1] = col + 1 < end ? w1 : 0.f;
-          }
-          unsigned char* to = ops + (lower ? 0 : C::T);
-          const uint32_t o = chunk_at(i, cg * 4 + j / 8);
-          auto two = [&](unsigned char* p) {
-            const uint4 h = pack8(w);
-            *reinterpret_cast<uint4*>(p + o) = h;
-            float hv[8];
-            unpack8(hv, h);
+            for (int e = 0; e < 8; e += 2) {
+              const int col = cg * 32 + j + z + e;
+              const float4 gj = *reinterpret_cast<const float4*>(gs + 2 * col);
+              const float w0 = f * x[z + e] * MBf16::exp2((gi.x - gj.x) + (gi.y - gj.y));
+              const float w1 = f * x[z + e + 1] * MBf16::exp2((gi.x - gj.z) + (gi.y - gj.w));
+              w[e] = col < end ? w0 : 0.f;
+              w[e + 1] = col + 1 < end ? w1 : 0.f;
+            }
+            const uint32_t o = chunk_at(i, cg * 4 + (j + z) / 8);
+            auto two = [&](unsigned char* p) {
+              const uint4 h = pack8(w);
+              *reinterpret_cast<uint4*>(p + o) = h;
+              float hv[8];
+              unpack8(hv, h);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) hv[e] = w[e] - hv[e];
-            *reinterpret_cast<uint4*>(p + 3 * C::T + o) = pack8(hv);
-          };
-          two(to);
-          if (lower) {
+              for (int e = 0; e < 8; ++e) hv[e] = w[e] - hv[e];
+              *reinterpret_cast<uint4*>(p + 3 * C::T + o) = pack8(hv);
+            };
+            two(to);
+            if (lower) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] *= be;
-            two(ops + 2 * C::T);
+              for (int e = 0; e < 8; ++e) w[e] *= be;
+              two(ops + 2 * C::T);
+            }
           }
         }
       }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
-      group_sync<1, C::WORK>();
-      if (g == 0) wait(full + 2, kqi & 1);
-      if (warp == 0) {
-        tc::fence_after_sync();
-        const uint64_t ap = tc::sdesc_k_sw128(smem_addr(ops)), tp = mn_desc(smem_addr(ops + C::T), C::T),
-                       tm = mn_desc(smem_addr(ops + 2 * C::T), C::T), bk = mn_desc(smem_addr(kq), C::T),
-                       bq = mn_desc(smem_addr(kq + C::ATOMS * C::T), C::T);
-        if (tc::elect_one()) {
-#pragma unroll
-          for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint32_t lo = pl * 3 * C::T, ac = pl + ks > 0 ? 1u : 0u;
-              const uint64_t kd = tc::sdesc_advance(bk, ks * kStepMN), qd = tc::sdesc_advance(bq, ks * kStepMN);
-              tc::mma_bf16(d4, tc::sdesc_advance(ap, lo + ks * kStepK), kd, id_dk | kBmn, ac);
-              tc::mma_bf16(d5, tc::sdesc_advance(tp, lo + ks * kStepMN), qd, id_dk | kAmn | kBmn, ac);
-              tc::mma_bf16(d5, tc::sdesc_advance(tm, lo + ks * kStepMN), kd, id_dk | kAmn | kBmn, 1u);
-            }
-          tc::mma_commit(done + 1);
-        }
-        __syncwarp();
-      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(ops_in);
       wait(done + 1, heads & 1);
       tc::fence_after_sync();
-      float d0 = 0.f, e0 = 0.f, u0 = 0.f;  // k.dk or q.dq; k.E; k.dS1 U
-#pragma unroll
-      for (int j = 0; j < NC; j += 16) {
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f;  // k.dk or q.dq; k.E; k.dS1 U
+      const float f = lower ? -eg : a.s.scale * eg;
+      // 16 columns from j of dk or dq
+      auto part = [&](int j, float* d) {
         const uint32_t o = at + cg * NC + j;
-        float x[16], y[16];
+        float x[16], y[16], u[16], p[16];
         ld_cols<16>(d1 + o, x);
         ld_cols<16>(d4 + o, y);
         if (lower) {
-          float u[16], p[16];
           ld_cols<16>(d3 + o, u);
           ld_cols<16>(d5 + o, p);
-          ld_wait<16>(x);
-          ld_wait<16>(y);
+        }
+        ld_wait<16>(x);
+        ld_wait<16>(y);
+        if (lower) {
           ld_wait<16>(u);
           ld_wait<16>(p);
+        }
 #pragma unroll
-          for (int z = 0; z < 16; z += 8) {
-            float kk[8];
-            unpack8(kk, *reinterpret_cast<const uint4*>(krow + chunk_at(i, ch0 + (j + z) / 8)));
+        for (int z = 0; z < 16; z += 8) {
+          float kk[8];
+          unpack8(kk, *reinterpret_cast<const uint4*>(tile + chunk_at(i, ch0 + (j + z) / 8)));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float en = fmaf(-eg, x[z + e], y[z + e]), us = el * u[z + e], d = fmaf(be, en, us + p[z + e]);
-              e0 = fmaf(kk[e], en, e0);
-              u0 = fmaf(kk[e], us, u0);
-              d0 = fmaf(kk[e], d, d0);
-              acc[j + z + e] = g == 0 ? d : acc[j + z + e] + d;
+          for (int e = 0; e < 8; ++e) {
+            const float en = fmaf(f, x[z + e], y[z + e]);
+            float dd = en;
+            if (lower) {
+              const float us = el * u[z + e];
+              s1 = fmaf(kk[e], en, s1);
+              s2 = fmaf(kk[e], us, s2);
+              dd = fmaf(be, en, us + p[z + e]);
             }
-          }
-        } else {
-          ld_wait<16>(x);
-          ld_wait<16>(y);
-#pragma unroll
-          for (int z = 0; z < 16; z += 8) {
-            float qq[8];
-            unpack8(qq, *reinterpret_cast<const uint4*>(qrow + chunk_at(i, ch0 + (j + z) / 8)));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float d = fmaf(a.s.scale * eg, x[z + e], y[z + e]);
-              d0 = fmaf(qq[e], d, d0);
-              acc[j + z + e] = g == 0 ? d : acc[j + z + e] + d;
-            }
+            s0 = fmaf(kk[e], dd, s0);
+            d[z + e] = dd;
           }
         }
-      }
-      if (lower) {
-        dot[128 + cg * 64 + i] = d0;
-        dot[256 + cg * 64 + i] = e0;
-        dot[384 + cg * 64 + i] = u0;
+      };
+      if constexpr (SHARED) {
+#pragma unroll
+        for (int j = 0; j < NC; j += 16) {
+          float d[16];
+          part(j, d);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[j + e] = g == 0 ? d[e] : acc[j + e] + d[e];
+        }
       } else {
-        dot[cg * 64 + i] = d0;
+#pragma unroll 1
+        for (int j = 0; j < NC; j += 16) {
+          float d[16];
+          part(j, d);                      // K or Q has been read there: the result takes its place
+          *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8)) = pack8(d);
+          *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8 + 1)) = pack8(d + 8);
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) bar_arrive(acc_out);
+      if (lower) {
+        dot[128 + cg * 64 + i] = s0;
+        dot[256 + cg * 64 + i] = s1;
+        dot[384 + cg * 64 + i] = s2;
+      } else {
+        dot[cg * 64 + i] = s0;
       }
       const int h = ck.hk * group + g;
-      if (++g == group) {                  // the key head is done: dk, dq into K's and Q's tiles, from where
-                                           // the fetching warps take them
+      if (++g == group) {                  // the fetching warps take dk and dq from K's and Q's place
         g = 0;
-        ++kqi;
-        unsigned char* tile = lower ? krow : qrow;
+        if constexpr (SHARED)
 #pragma unroll
-        for (int j = 0; j < NC; j += 8) *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8)) = pack8(acc + j);
+          for (int j = 0; j < NC; j += 8) *reinterpret_cast<uint4*>(tile + chunk_at(i, ch0 + j / 8)) = pack8(acc + j);
         __syncwarp();
         if (lane == 0) bar_arrive(empty + 2);
       }
-      tc::fence_before_sync();
       group_sync<1, C::WORK>();
       if (warp == 7) {
         // dbeta, and dg: the sums of dG from each row to the chunk's end
@@ -421,9 +458,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
           const int r = 2 * lane + e;
           const float z = dot[256 + r] + dot[320 + r];
           const float db = ((drv[r] + drv[64 + r]) + (drv[128 + r] + drv[192 + r])) + z;
-          // beta of row r sits in another lane's register set: recomputed from the vectors
-          const float br = a.vec[(ck.slot * a.s.hv + h) * kVec + kVecBeta + r];
-          dg[e] = (dot[r] + dot[64 + r]) - (dot[128 + r] + dot[192 + r]) + 2.f * br * z;
+          dg[e] = (dot[r] + dot[64 + r]) - (dot[128 + r] + dot[192 + r]) + 2.f * (e ? be2.y : be2.x) * z;
           us += dot[384 + r] + dot[448 + r];
           if (r < ck.rows) a.gbeta[(ck.row0 + r) * a.s.hv + h] = __float2bfloat16_rn(db);
         }
@@ -457,11 +492,11 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
   }
 }
 
-template <int DK>
+template <int DK, bool SHARED>
 static cudaError_t launch(GradArgs g, cudaStream_t st) {
   using C = GradCfg<DK>;
   const long long items = slot_count(g.s.rows, g.s.n_seq) * g.s.hk;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_grad_tc<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_grad_tc<DK, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   g.tma = tile_map(&m.q, g.q, g.s.dk, g.s.hk, g.s.rows, g.ldq, 64) &&
@@ -469,7 +504,7 @@ static cudaError_t launch(GradArgs g, cudaStream_t st) {
           tile_map(&m.v, g.v, g.s.dv, g.s.hv, g.s.rows, g.ldv, 64) &&
           tile_map(&m.go, g.go, g.s.dv, g.s.hv, g.s.rows, (long long)g.s.hv * g.s.dv, 64);
   TraceScope tr("k_gdr_grad_tc", st);
-  k_gdr_grad_tc<DK><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g, m);
+  k_gdr_grad_tc<DK, SHARED><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g, m);
   return cudaGetLastError();
 }
 
@@ -484,7 +519,8 @@ cudaError_t launch_grad_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
   g.s0 = reinterpret_cast<const unsigned char*>(a.s0); g.u = reinterpret_cast<const unsigned char*>(a.u);
   g.ds = reinterpret_cast<const unsigned char*>(a.ds); g.dr = reinterpret_cast<const unsigned char*>(a.dr);
   g.vec = a.vec;
-  return dk_tile == 64 ? launch<64>(g, st) : launch<128>(g, st);
+  if (a.s.hv == a.s.hk) return dk_tile == 64 ? launch<64, false>(g, st) : launch<128, false>(g, st);
+  return dk_tile == 64 ? launch<64, true>(g, st) : launch<128, true>(g, st);
 }
 
 int read_gdr_grad_error(int clear) {

@@ -18,7 +18,6 @@
 // 64 NB columns, NV = 64 NB / PL, one product for both.
 //
 // What bounds it is the length of that chain.
-#include <cstdlib>
 #include "gdr_tc.cuh"
 
 namespace cfc {
@@ -42,6 +41,21 @@ struct PrepTc {
   static constexpr uint32_t BYTES = OFF_G + 3 * kC * 4;
 };
 
+// The sequences' order by falling length (ties by number): the longest one's
+// serial pass is the least that the whole takes, so it has to begin first.
+__device__ __forceinline__ void longest_first(const FwdArgs& a, int tid) {
+  for (int n = tid; n < a.s.n_seq; n += 128) {
+    long long s;
+    int len, l, rank = 0;
+    seq_range(a.s, n, &s, &len);
+    for (int m = 0; m < a.s.n_seq; ++m) {
+      seq_range(a.s, m, &s, &l);
+      rank += l > len || (l == len && m < n);
+    }
+    a.order[rank] = n;
+  }
+}
+
 template <int DK, int PL>
 __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -58,6 +72,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   const long long slot = blockIdx.x / a.s.hv;
   int n, len, c;
   long long start;
+  if (a.order && blockIdx.x == 0) longest_first(a, tid);
   if (!slot_chunk(a.s, slot, &n, &start, &len, &c)) return;
   const long long row0 = start + (long long)c * kC;
   const int rows = min(kC, len - c * kC);
@@ -193,8 +208,9 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   }
 }
 
-template <int DK, int PL, int NB, int CW, bool BWD>
+template <int DK, int PL, int NB, bool BWD>
 struct TcCfg {
+  static constexpr int CW = 2;                           // warps that share the columns
   static constexpr int NV = 64 * NB / PL, ATOMS = DK / 64, FETCH = 128, WORK = 128 * CW, THREADS = WORK + FETCH;
   static constexpr int NC = NV / CW;                    // columns a thread
   static constexpr int LO = NV;                         // from the hi to the lo plane's accumulator columns
@@ -238,6 +254,7 @@ struct TcArgs {
   const float* vec;
   // per chunk and 64 value columns, as operand tiles: S0 and U (backward: dS1, dR), or NULL
   unsigned char *st, *u;
+  const int* order;
   int ntile, tma;
 };
 
@@ -325,9 +342,9 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
 }
 
 // ------------------------------------------------------------------- forward
-template <int DK, int PL, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS, 1) k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
-  using C = TcCfg<DK, PL, NB, CW, false>;
+template <int DK, int PL, int NB>
+__global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1) k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  using C = TcCfg<DK, PL, NB, false>;
   constexpr int NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;      // columns a thread; at a time
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -337,8 +354,9 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS, 1) k_gd
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % a.ntile;
-  const long long sh = blockIdx.x / a.ntile;
-  const int h = (int)(sh % a.s.hv), n = (int)(sh / a.s.hv);
+  const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
+  const int n = a.order ? a.order[at_n] : at_n;
+  const long long sh = (long long)n * a.s.hv + h;
   long long start;
   int len;
   seq_range(a.s, n, &start, &len);
@@ -348,7 +366,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS, 1) k_gd
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
       tc::mbar_init(empty + i, 1);             // a chunk's last product
-      tc::mbar_init(outs + i, 2 * CW);         // the warps that form output rows
+      tc::mbar_init(outs + i, 2 * C::CW);         // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -570,9 +588,9 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, CW, false>::THREADS, 1) k_gd
 //   D3 = Q^T (scale exp(G) dO) - K^T (beta exp(G) dR),  dS0 = exp(G_C) dS1 + D3.
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
-template <int DK, int NB, int CW>
-__global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS, 1) k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
-  using C = TcCfg<DK, 1, NB, CW, true>;
+template <int DK, int NB>
+__global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1) k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  using C = TcCfg<DK, 1, NB, true>;
   constexpr int PL = 1, NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
@@ -582,8 +600,9 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS, 1) k_gdr_
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % a.ntile;
-  const long long sh = blockIdx.x / a.ntile;
-  const int h = (int)(sh % a.s.hv), n = (int)(sh / a.s.hv);
+  const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
+  const int n = a.order ? a.order[at_n] : at_n;
+  const long long sh = (long long)n * a.s.hv + h;
   long long start;
   int len;
   seq_range(a.s, n, &start, &len);
@@ -593,7 +612,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, CW, true>::THREADS, 1) k_gdr_
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
       tc::mbar_init(empty + i, 1);             // a chunk's last product
-      tc::mbar_init(outs + i, 2 * CW);         // the warps that form output rows
+      tc::mbar_init(outs + i, 2 * C::CW);         // the warps that form output rows
       tc::mbar_init(done + i, 1);
     }
     tc::mbar_init_fence();
@@ -830,30 +849,30 @@ static int maps_of(const TcArgs& a, int v_box, Maps* m) {
          tile_map(&m->v, a.v, a.s.dv, a.s.hv, a.s.rows, a.ldv, v_box);
 }
 
-template <int DK, int PL, int NB, int CW>
+template <int DK, int PL, int NB>
 static cudaError_t scan(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, PL, NB, CW, false>;
+  using C = TcCfg<DK, PL, NB, false>;
   a.ntile = (a.s.dv + C::NV - 1) / C::NV;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   a.tma = maps_of(a, C::NV < 64 ? C::NV : 64, &m);
   TraceScope tr("k_gdr_scan_tc", st);
-  k_gdr_scan_tc<DK, PL, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
+  k_gdr_scan_tc<DK, PL, NB><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
   return cudaGetLastError();
 }
-template <int DK, int NB, int CW>
+template <int DK, int NB>
 static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
-  using C = TcCfg<DK, 1, NB, CW, true>;
+  using C = TcCfg<DK, 1, NB, true>;
   a.ntile = (a.s.dv + C::NV - 1) / C::NV;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NB, CW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   a.tma = maps_of(a, 64, &m);
   TraceScope tr("k_gdr_scan_bwd_tc", st);
-  k_gdr_scan_bwd_tc<DK, NB, CW><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
+  k_gdr_scan_bwd_tc<DK, NB><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
   return cudaGetLastError();
 }
 
@@ -875,23 +894,14 @@ cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
 template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  const int cw = getenv("GDR_CW") ? atoi(getenv("GDR_CW")) : 0;
-  if (planes == 2) {
-    if (t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114)
-      return cw == 2 ? scan<DK, 2, 2, 2>(t, st) : scan<DK, 2, 2, 4>(t, st);
-    return cw == 2 ? scan<DK, 2, 1, 2>(t, st) : scan<DK, 2, 1, 4>(t, st);
-  }
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114)
-    return cw == 2 ? scan<DK, 1, 2, 2>(t, st) : scan<DK, 1, 2, 4>(t, st);
-  return cw == 2 ? scan<DK, 1, 1, 4>(t, st) : scan<DK, 1, 1, 2>(t, st);
+  if (planes == 2)
+    return t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114 ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
+  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114 ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  const int cw = getenv("GDR_CW") ? atoi(getenv("GDR_CW")) : 0;
-  if (t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114)
-    return cw == 2 ? scan_bwd<DK, 2, 2>(t, st) : scan_bwd<DK, 2, 4>(t, st);
-  return cw == 2 ? scan_bwd<DK, 1, 4>(t, st) : scan_bwd<DK, 1, 2>(t, st);
+  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114 ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {
@@ -902,6 +912,7 @@ cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
   t.init = a.init; t.final_state = a.final_state; t.o = static_cast<bf16*>(a.o);
   t.a2 = reinterpret_cast<const unsigned char*>(a.t);
   t.vec = a.vec;
+  t.order = a.order;
   if (a.save) { t.st = reinterpret_cast<unsigned char*>(a.s0); t.u = reinterpret_cast<unsigned char*>(a.u); }
   return dk_tile == 64 ? scan_by_size<64>(t, planes, st) : scan_by_size<128>(t, planes, st);
 }
@@ -914,6 +925,7 @@ cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
   t.init = a.gfinal; t.final_state = a.ginit; t.o = static_cast<bf16*>(a.gv);
   t.a2 = reinterpret_cast<const unsigned char*>(a.t);
   t.vec = a.vec;
+  t.order = a.order;
   t.st = reinterpret_cast<unsigned char*>(a.ds); t.u = reinterpret_cast<unsigned char*>(a.dr);
   return dk_tile == 64 ? scan_bwd_by_size<64>(t, st) : scan_bwd_by_size<128>(t, st);
 }

@@ -393,12 +393,14 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // operand type the products read it in) and U^T [d_v, 64]; and the backward's
 // own dS1^T, dR^T, and per-value-head dq, dk where heads are shared.
 struct Workspace {
-  size_t off_t, off_p, off_vec, off_s0, off_u, off_ds, off_dr, off_dq, off_dk, total;
+  size_t off_t, off_p, off_vec, off_order, off_s0, off_u, off_ds, off_dr, off_dq, off_dk, total;
 };
 template <class P> constexpr int kLdt = kC + P::PAD;                                  // row of T - I, P
 template <class P> constexpr int kTPlanes = P::kMode == CFC_MATH_BF16 ? 2 : 1;
 Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 
+// Packed batches of up to this many sequences run longest first.
+constexpr int kMaxOrder = 2048;
 constexpr uint32_t kImage = 32768;   // bf16: [T - I; P T] in two planes of 128 rows x 128 bytes
 
 struct FwdArgs {
@@ -411,6 +413,7 @@ struct FwdArgs {
   void* o;
   char *t, *p, *s0, *u;
   float* vec;
+  int* order;         // packed batches in bf16: the sequences, longest first
   int save;
   int ntile;
 };
@@ -555,6 +558,7 @@ struct BwdArgs {
   const char *t, *p, *s0, *u;
   char *ds, *dr;
   const float* vec;
+  const int* order;
   float *pdq, *pdk;        // per value head [rows, hv, dk], or NULL
   int ntile;
 };
