@@ -165,9 +165,9 @@ def _ptr(t, name, dtype=None, shape=None, optional=False):
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -350,48 +350,49 @@ def cfc_gdr_workspace_bytes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math=MA
                                                       1 if save else 0))
 
 
-def _rows(t, name, dtype, lead, heads, width):
-    """Pointer and row stride of t [*lead, heads, width], whose rows may be
-    parts of wider ones (dense in heads and width, evenly spaced over lead)."""
+def _rows(t, name, dtype, shape):
+    """Pointer and row stride of t [..., heads, width], whose rows may be parts
+    of wider ones (dense in heads and width, evenly spaced over the rest)."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if shape != (*lead, heads, width):
-        raise ValueError(f"{name} must have shape {(*lead, heads, width)}, got {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
-        return t.data_ptr(), heads * width
+        return t.data_ptr(), shape[-2] * shape[-1]
     strides = t.stride()
-    ld = strides[-3] if shape[-3] != 1 or len(lead) == 1 else strides[0]
-    if (strides[-1] != 1 or (heads > 1 and strides[-2] != width)
-            or (len(lead) == 2 and lead[0] > 1 and strides[0] != lead[1] * ld)):
+    packed = len(shape) == 3
+    ld = strides[-3] if packed or shape[-3] != 1 else strides[0]
+    if (strides[-1] != 1 or (shape[-2] > 1 and strides[-2] != shape[-1])
+            or (not packed and shape[0] > 1 and strides[0] != shape[1] * ld)):
         raise ValueError(f"{name} must be dense in its last two axes, with evenly spaced rows")
     return t.data_ptr(), ld
 
 
-def _gdr_inputs(q, k, v, g, beta, seq_offsets, math):
+def _gdr_inputs(q, k, v, g, beta, packed, math):
     """Sizes and leading C arguments that the three calls share."""
     torch = _torch()
     st, f32 = _storage_dtype(math), torch.float32
-    if q.dim() < 2 or v.dim() < 2:
-        raise ValueError("q, k and v need a heads and a width axis")
-    hk, dk = q.shape[-2:]
-    hv, dv = v.shape[-2:]
-    lead = v.shape[:-2]
-    if len(lead) != (2 if seq_offsets is None else 1):
+    vs, qs = v.shape, q.shape
+    if len(vs) != (3 if packed else 4):
         raise ValueError("v must be [sequences, tokens, heads, d_v], or [rows, heads, d_v] with seq_offsets")
-    args = [*_rows(q, "q", st, lead, hk, dk), *_rows(k, "k", st, lead, hk, dk), *_rows(v, "v", st, lead, hv, dv),
-            _ptr(g, "g", f32, (*lead, hv)), _ptr(beta, "beta", f32, (*lead, hv))]
-    return st, lead, hk, hv, dk, dv, args
+    if len(qs) != len(vs):
+        raise ValueError("q and v must have the same number of axes")
+    ks = vs[:-2] + qs[-2:]
+    hs = vs[:-1]
+    qp, ldq = _rows(q, "q", st, ks)
+    kp, ldk = _rows(k, "k", st, ks)
+    vp, ldv = _rows(v, "v", st, vs)
+    return st, vs, ks, (qp, ldq, kp, ldk, vp, ldv, _ptr(g, "g", f32, hs), _ptr(beta, "beta", f32, hs))
 
 
-def _gdr_sequences(lead, seq_offsets):
+def _gdr_sequences(vs, seq_offsets):
     if seq_offsets is None:
-        return None, lead[0], lead[0] * lead[1]
+        return None, vs[0], vs[0] * vs[1]
     if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
         raise ValueError("seq_offsets must hold n_seq + 1 row numbers")
-    return _ptr(seq_offsets, "seq_offsets", _torch().int32), seq_offsets.numel() - 1, lead[0]
+    return _ptr(seq_offsets, "seq_offsets", _torch().int32), seq_offsets.numel() - 1, vs[0]
 
 
 def cfc_gdr_forward(q, k, v, g, beta, o, workspace, scale=None, seq_offsets=None, initial_state=None, final_state=None,
@@ -401,12 +402,14 @@ def cfc_gdr_forward(q, k, v, g, beta, o, workspace, scale=None, seq_offsets=None
     v_heads]; or [rows, ...] packed, with int32 seq_offsets [sequences + 1] on
     the device.  scale: d_k ** -0.5 if None."""
     f32 = _torch().float32
-    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, seq_offsets, math)
-    off, n, rows = _gdr_sequences(lead, seq_offsets)
+    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
+    off, n, rows = _gdr_sequences(vs, seq_offsets)
+    hk, dk, hv, dv = ks[-2], ks[-1], vs[-2], vs[-1]
+    ss = (n, hv, dk, dv)
     status = load_library().cfc_gdr_forward(
         *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
-        _ptr(initial_state, "initial_state", f32, (n, hv, dk, dv), optional=True), _ptr(o, "o", st, (*lead, hv, dv)),
-        _ptr(final_state, "final_state", f32, (n, hv, dk, dv), optional=True), 1 if save else 0,
+        _ptr(initial_state, "initial_state", f32, ss, optional=True), _ptr(o, "o", st, vs),
+        _ptr(final_state, "final_state", f32, ss, optional=True), 1 if save else 0,
         _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
     _check("cfc_gdr_forward", status)
 
@@ -416,16 +419,16 @@ def cfc_gdr_backward(q, k, v, g, beta, grad_o, grad_q, grad_k, grad_v, grad_g, g
     """Backward of the cfc_gdr_forward(save=True) that filled ``workspace``;
     every gradient is overwritten, all in the type of q."""
     f32 = _torch().float32
-    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, seq_offsets, math)
-    off, n, rows = _gdr_sequences(lead, seq_offsets)
+    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
+    off, n, rows = _gdr_sequences(vs, seq_offsets)
+    hk, dk, hv, dv = ks[-2], ks[-1], vs[-2], vs[-1]
+    hs, ss = vs[:-1], (n, hv, dk, dv)
     status = load_library().cfc_gdr_backward(
         *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
-        _ptr(grad_o, "grad_o", st, (*lead, hv, dv)),
-        _ptr(grad_final_state, "grad_final_state", f32, (n, hv, dk, dv), optional=True),
-        _ptr(grad_q, "grad_q", st, (*lead, hk, dk)), _ptr(grad_k, "grad_k", st, (*lead, hk, dk)),
-        _ptr(grad_v, "grad_v", st, (*lead, hv, dv)), _ptr(grad_g, "grad_g", st, (*lead, hv)),
-        _ptr(grad_beta, "grad_beta", st, (*lead, hv)),
-        _ptr(grad_initial_state, "grad_initial_state", f32, (n, hv, dk, dv), optional=True),
+        _ptr(grad_o, "grad_o", st, vs), _ptr(grad_final_state, "grad_final_state", f32, ss, optional=True),
+        _ptr(grad_q, "grad_q", st, ks), _ptr(grad_k, "grad_k", st, ks), _ptr(grad_v, "grad_v", st, vs),
+        _ptr(grad_g, "grad_g", st, hs), _ptr(grad_beta, "grad_beta", st, hs),
+        _ptr(grad_initial_state, "grad_initial_state", f32, ss, optional=True),
         _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
     _check("cfc_gdr_backward", status)
 
@@ -435,13 +438,16 @@ def cfc_gdr_step(q, k, v, g, beta, state, o, slots=None, scale=None, math=MATH_B
     [sequences, tokens, ...]): sequence i's state is ``state[slots[i]]``
     (int32 on the device; ``state[i]`` if None), updated in place."""
     torch = _torch()
-    st, lead, hk, hv, dk, dv, args = _gdr_inputs(q, k, v, g, beta, None, math)
-    n_slots = state.shape[0]
+    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, False, math)
+    n, tokens, hv, dv = vs
+    hk, dk = ks[2], ks[3]
+    pool = state.shape
+    if len(pool) != 4 or pool[1:] != (hv, dk, dv):
+        raise ValueError(f"state must have shape (slots, {hv}, {dk}, {dv}), got {tuple(pool)}")
     status = load_library().cfc_gdr_step(
-        *args, lead[0], lead[1], hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
-        _ptr(state, "state", torch.float32, (n_slots, hv, dk, dv)), n_slots,
-        _ptr(slots, "slots", torch.int32, lead[:1], optional=True), _ptr(o, "o", st, (*lead, hv, dv)),
-        _stream(stream))
+        *args, n, tokens, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
+        _ptr(state, "state", torch.float32), pool[0], _ptr(slots, "slots", torch.int32, (n,), optional=True),
+        _ptr(o, "o", st, vs), _stream(stream))
     _check("cfc_gdr_step", status)
 
 

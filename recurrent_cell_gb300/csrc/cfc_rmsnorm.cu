@@ -92,17 +92,30 @@ struct Sum { __device__ static __forceinline__ float of(float a, float b) { retu
 struct Max { __device__ static __forceinline__ float of(float a, float b) { return max_nan(a, b); } };
 
 // Over a row: a warp's shuffles and, where the row is a block's, its warps'
-// values through `part`, two buffers in turn, so one barrier is enough.
+// values through `part`, two buffers in turn, so one barrier is enough.  The
+// places of warps that the block lacks hold zeros, which both sums and maxima
+// of magnitudes leave out.
+constexpr int kWarps = 16;
+struct Part {
+  float4 v[2][kWarps / 4];
+  __device__ __forceinline__ void clear() {
+    if (threadIdx.x < 2 * kWarps) reinterpret_cast<float*>(v)[threadIdx.x] = 0.f;
+    __syncthreads();
+  }
+};
 template <class Op, bool WARP>
-__device__ __forceinline__ float over_row(float v, float (*part)[32], int& turn) {
+__device__ __forceinline__ float over_row(float v, Part& part, int& turn) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
   if constexpr (!WARP) {
-    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = v;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(part.v[turn])[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = part[turn][0];
-    const int warps = blockDim.x >> 5;
-    for (int i = 1; i < warps; ++i) v = Op::of(v, part[turn][i]);
+    float4 x[kWarps / 4];
+#pragma unroll
+    for (int i = 0; i < kWarps / 4; ++i) x[i] = part.v[turn][i];
+#pragma unroll
+    for (int i = 0; i < kWarps / 4; ++i) x[i].x = Op::of(Op::of(x[i].x, x[i].y), Op::of(x[i].z, x[i].w));
+    v = Op::of(Op::of(x[0].x, x[1].x), Op::of(x[2].x, x[3].x));
     turn ^= 1;
   }
   return v;
@@ -147,13 +160,14 @@ template <int NV, bool WARP, bool BWD>
 constexpr int most_threads() { return WARP ? 32 * kWarpRows : (NV > 2 && BWD ? 384 : 512); }
 
 template <class E, int NV, bool WARP>
-__global__ void __launch_bounds__(most_threads<NV, WARP, false>()) k_rmsnorm(Args a) {
+__global__ void __launch_bounds__(most_threads<NV, WARP, false>(), !WARP && NV == 2 ? 2 : 1) k_rmsnorm(Args a) {
   using R = Row<E, NV, WARP>;
   using V = typename R::V;
   using T = typename R::T;
   constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
-  __shared__ float part[2][32];
+  __shared__ Part part;
   int turn = 0;
+  if (!WARP) part.clear();
   const R r(a.d);
   float w[NV][N];
   r.weights(w, a.w);
@@ -236,8 +250,9 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
   using T = typename R::T;
   constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
   extern __shared__ float sums[];                // [RPB][d] where a block has several rows
-  __shared__ float part[2][32];
+  __shared__ Part part;
   int turn = 0;
+  if (!WARP) part.clear();
   const R r(a.d);
   float w[NV][N], gw[NV][N] = {};
   r.weights(w, a.w);
@@ -255,33 +270,39 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
   fetch(row);
   for (; row < a.rows; row += step) {
     const long long at = row * a.d;
-    // n = s rstd and dn = grad_y w of the row
-    float n[NV][N], dn[NV][N];
-    T cv[NV];
+    T cs[NV], cg[NV], cv[NV];
     const float rs = rstd;
     float dot = 0.f;
 #pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      cs[j] = sv[j];
+      cg[j] = gv[j];
+      cv[j] = rv[j];
+    }
+    fetch(row + step);
+    // n = s rstd, dn = grad_y w; formed twice rather than kept, for the registers
+#pragma unroll
     for (int j = 0; j < NV; ++j)
       if (r.in(j)) {
-        V::get(n[j], sv[j]);
-        V::get(dn[j], gv[j]);
-        cv[j] = rv[j];
+        float n[N], g[N];
+        V::get(n, cs[j]);
+        V::get(g, cg[j]);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          n[j][e] *= rs;
-          gw[j][e] = fmaf(dn[j][e], n[j][e], gw[j][e]);
-          dn[j][e] *= w[j][e];
-          dot = fmaf(dn[j][e], n[j][e], dot);
+          n[e] *= rs;
+          gw[j][e] = fmaf(g[e], n[e], gw[j][e]);
+          dot = fmaf(g[e] * w[j][e], n[e], dot);
         }
       }
-    fetch(row + step);
     dot = over_row<Sum, WARP>(dot, part, turn) * inv_d;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (r.in(j)) {
-        float o[N];
+        float n[N], g[N], o[N];
+        V::get(n, cs[j]);
+        V::get(g, cg[j]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = rs * (dn[j][e] - n[j][e] * dot);
+        for (int e = 0; e < N; ++e) o[e] = rs * (g[e] * w[j][e] - n[e] * rs * dot);
         if (a.grad_s) {
           float t[N];
           V::get(t, cv[j]);
@@ -318,8 +339,9 @@ constexpr int kAnyThreads = 256;
 
 template <class E>
 __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
-  __shared__ float part[2][32];
+  __shared__ Part part;
   int turn = 0;
+  part.clear();
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const E* x = static_cast<const E*>(a.x) + row * a.d;
     const E* r = static_cast<const E*>(a.residual) + row * a.d;
@@ -362,8 +384,9 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
 template <class E>
 __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
   extern __shared__ float gw[];                  // [d], thread i % 256 owns column i
-  __shared__ float part[2][32];
+  __shared__ Part part;
   int turn = 0;
+  part.clear();
   for (int i = threadIdx.x; i < a.d; i += kAnyThreads) gw[i] = 0.f;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const E* s = static_cast<const E*>(a.x) + row * a.d;
@@ -388,16 +411,18 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
 // Blocks of the backward: at most kMaxBlocks rows of partial sums.
 constexpr int kMaxBlocks = 4 * kNumSMs;
 
-// Blocks that the SMs hold at once, `regs` registers a thread.
-static int resident(int threads, int regs) {
-  const int n = 65536 / (threads * regs), m = 2048 / threads;
-  return (n < m ? n : m) > 0 ? (n < m ? n : m) : 1;
+// Blocks of `kernel` that an SM holds at once.
+template <class K>
+static int resident(K kernel, int threads, size_t smem) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+  return n;
 }
 
 template <class E, int NV, bool WARP>
 static cudaError_t fwd(const Args& a, int threads, cudaStream_t st) {
   constexpr int RPB = WARP ? kWarpRows : 1;
-  const long long need = (a.rows + RPB - 1) / RPB, most = (long long)resident(threads, NV > 2 ? 128 : 80) * kNumSMs;
+  const long long need = (a.rows + RPB - 1) / RPB, most = (long long)resident(k_rmsnorm<E, NV, WARP>, threads, 0) * kNumSMs;
   TraceScope tr("k_rmsnorm", st);
   k_rmsnorm<E, NV, WARP><<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
   return cudaGetLastError();
@@ -406,11 +431,12 @@ template <class E, int NV, bool WARP>
 static cudaError_t bwd(const Args& a, int threads, int* blocks, cudaStream_t st) {
   constexpr int RPB = WARP ? kWarpRows : 1;
   const long long need = (a.rows + RPB - 1) / RPB;
-  long long most = (long long)resident(threads, NV > 2 ? 168 : 112) * kNumSMs;
+  const size_t smem = WARP ? (size_t)RPB * a.d * 4 : 0;
+  long long most = (long long)resident(k_rmsnorm_bwd<E, NV, WARP>, threads, smem) * kNumSMs;
   if (most > kMaxBlocks) most = kMaxBlocks;
   *blocks = (int)(need < most ? need : most);
   TraceScope tr("k_rmsnorm_bwd", st);
-  k_rmsnorm_bwd<E, NV, WARP><<<*blocks, threads, WARP ? (size_t)RPB * a.d * 4 : 0, st>>>(a);
+  k_rmsnorm_bwd<E, NV, WARP><<<*blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
