@@ -12,9 +12,10 @@
 // fp32 and rounded once, on its way out.
 //
 // Memory is the bound in both directions (about one operation a byte), so a
-// row is read once and kept in registers: a warp a row up to 2 vectors of 16
-// bytes a lane, a block a row beyond that, of as many warps as leave each
-// thread 2 (long rows: 4) vectors.  Blocks are persistent: they keep their
+// row is read once and kept in registers: 8 to 32 lanes a row up to 2 vectors
+// of 16 bytes each, a block a row beyond that, of as many warps as leave each
+// thread 2 (long rows: 4) vectors.  Rows that are no whole number of vectors go
+// element by element in the same way.  Blocks are persistent: they keep their
 // columns' weights, and in the backward their columns' grad_w, in registers,
 // and load the next row before they finish the present one.
 #include <cuda_fp8.h>
@@ -35,15 +36,18 @@ struct Args {
   float eps;
 };
 
-template <class E> struct Vec;
-template <> struct Vec<float> {
+// N elements that a thread loads at once.
+template <class EL, int NE> struct Vec;
+template <> struct Vec<float, 4> {
+  using E = float;
   static constexpr int N = 4;
   using T = float4;
   __device__ static __forceinline__ void get(float (&f)[4], const float4& v) { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
   __device__ static __forceinline__ float4 make(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
   __device__ static __forceinline__ float round(float v) { return v; }
 };
-template <> struct Vec<__nv_bfloat16> {
+template <> struct Vec<__nv_bfloat16, 8> {
+  using E = __nv_bfloat16;
   static constexpr int N = 8;
   using T = uint4;
   __device__ static __forceinline__ void get(float (&f)[8], const uint4& v) {
@@ -65,6 +69,26 @@ template <> struct Vec<__nv_bfloat16> {
   }
   __device__ static __forceinline__ float round(float v) { return round_bf16(v); }
 };
+
+template <> struct Vec<float, 1> {
+  using E = float;
+  static constexpr int N = 1;
+  using T = float;
+  __device__ static __forceinline__ void get(float (&f)[1], float v) { f[0] = v; }
+  __device__ static __forceinline__ float make(const float (&f)[1]) { return f[0]; }
+  __device__ static __forceinline__ float round(float v) { return v; }
+};
+template <> struct Vec<__nv_bfloat16, 1> {
+  using E = __nv_bfloat16;
+  static constexpr int N = 1;
+  using T = unsigned short;
+  __device__ static __forceinline__ void get(float (&f)[1], unsigned short v) { f[0] = __uint_as_float((uint32_t)v << 16); }
+  __device__ static __forceinline__ unsigned short make(const float (&f)[1]) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+  }
+  __device__ static __forceinline__ float round(float v) { return round_bf16(v); }
+};
+template <class E> constexpr int kVecN = 16 / sizeof(E);
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -103,11 +127,12 @@ struct Part {
     __syncthreads();
   }
 };
-template <class Op, bool WARP>
+// LANES: of the warp that share the row; 0: the block's.
+template <class Op, int LANES>
 __device__ __forceinline__ float over_row(float v, Part& part, int& turn) {
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
-  if constexpr (!WARP) {
+  for (int m = (LANES ? LANES : 32) / 2; m > 0; m >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, m));
+  if constexpr (LANES == 0) {
     if ((threadIdx.x & 31) == 0) reinterpret_cast<float*>(part.v[turn])[threadIdx.x >> 5] = v;
     __syncthreads();
     float4 x[kWarps / 4];
@@ -121,18 +146,19 @@ __device__ __forceinline__ float over_row(float v, Part& part, int& turn) {
   return v;
 }
 
-constexpr int kWarpRows = 8;      // rows of a block whose rows are warps
+constexpr int kLaneThreads = 256;      // threads of a block whose rows are lanes of its warps
+template <int LANES> constexpr int kRows = LANES ? kLaneThreads / (LANES ? LANES : 1) : 1;
 
 // A thread's vectors of a row: j * L + l, L the threads of the row.
-template <class E, int NV, bool WARP>
+template <class V, int NV, int LANES>
 struct Row {
-  using V = Vec<E>;
+  using E = typename V::E;
   using T = typename V::T;
   static constexpr int N = V::N;
   int l, L, nvec;
   __device__ __forceinline__ Row(int d) {
-    L = WARP ? 32 : blockDim.x;
-    l = WARP ? threadIdx.x & 31 : threadIdx.x;
+    L = LANES ? LANES : blockDim.x;
+    l = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
     nvec = d / N;
   }
   __device__ __forceinline__ int at(int j) const { return j * L + l; }
@@ -146,45 +172,51 @@ struct Row {
   __device__ __forceinline__ void weights(float (&w)[NV][N], const float* p) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
+      if constexpr (N == 1) {
+        w[j][0] = in(j) ? __ldg(p + at(j)) : 0.f;
+      } else {
 #pragma unroll
-      for (int e = 0; e < N; e += 4) {
-        const float4 f = in(j) ? __ldg(reinterpret_cast<const float4*>(p + at(j) * N + e))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-        w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
+        for (int e = 0; e < N; e += 4) {
+          const float4 f = in(j) ? __ldg(reinterpret_cast<const float4*>(p + at(j) * N + e))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+          w[j][e] = f.x; w[j][e + 1] = f.y; w[j][e + 2] = f.z; w[j][e + 3] = f.w;
+        }
       }
   }
 };
 
 // Threads of a block at most: what leaves each the registers it needs.
-template <int NV, bool WARP, bool BWD>
-constexpr int most_threads() { return WARP ? 32 * kWarpRows : (NV > 2 && BWD ? 384 : 512); }
+template <class V, int NV, int LANES, bool BWD>
+constexpr int most_threads() { return LANES ? kLaneThreads : (BWD && V::N > 1 && NV > 2 ? 384 : 512); }
 
-template <class E, int NV, bool WARP>
-__global__ void __launch_bounds__(most_threads<NV, WARP, false>(), !WARP && NV == 2 ? 2 : 1) k_rmsnorm(Args a) {
-  using R = Row<E, NV, WARP>;
-  using V = typename R::V;
-  using T = typename R::T;
-  constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
+template <class V, int NV, int LANES>
+__global__ void __launch_bounds__(most_threads<V, NV, LANES, false>(), !LANES && NV * V::N <= 16 ? 2 : 1) k_rmsnorm(Args a) {
+  using R = Row<V, NV, LANES>;
+  using E = typename V::E;
+  using T = typename V::T;
+  constexpr int N = V::N, RPB = kRows<LANES>;
   __shared__ Part part;
   int turn = 0;
-  if (!WARP) part.clear();
+  if (!LANES) part.clear();
   const R r(a.d);
   float w[NV][N];
   r.weights(w, a.w);
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
-  long long row = (long long)blockIdx.x * RPB + (WARP ? threadIdx.x >> 5 : 0);
+  long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
   T xv[NV], rv[NV];
   r.load(xv, a.x, row, a.rows, a.d);
   if (a.residual) r.load(rv, a.residual, row, a.rows, a.d);
-  for (; row < a.rows; row += step) {
+  // (the lanes of a warp whose rows are over stay for the others' shuffles)
+  for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
+    const bool on = row < a.rows;
     float s[NV][N];
     float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int e = 0; e < N; ++e) s[j][e] = 0.f;
-      if (r.in(j)) {
+      if (on && r.in(j)) {
         V::get(s[j], xv[j]);
         if (a.residual) {
           float t[N];
@@ -199,9 +231,9 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, false>(), !WARP && NV =
     }
     r.load(xv, a.x, row + step, a.rows, a.d);
     if (a.residual) r.load(rv, a.residual, row + step, a.rows, a.d);
-    sq = over_row<Sum, WARP>(sq, part, turn);
+    sq = over_row<Sum, LANES>(sq, part, turn);
     const float rstd = 1.f / sqrtf(fmaf(sq, inv_d, a.eps));
-    if (a.rstd && r.l == 0) a.rstd[row] = rstd;
+    if (a.rstd && on && r.l == 0) a.rstd[row] = rstd;
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -210,11 +242,11 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, false>(), !WARP && NV =
         s[j][e] = s[j][e] * rstd * w[j][e];
         most = max_nan(most, fabsf(s[j][e]));
       }
-      if (a.y && r.in(j)) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), V::make(s[j]));
+      if (a.y && on && r.in(j)) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), V::make(s[j]));
     }
     if (a.y8) {
       const int gl = a.group / N;       // threads that share a scale, unless the row does
-      if (a.group == a.d) most = over_row<Max, WARP>(most, part, turn);
+      if (a.group == a.d) most = over_row<Max, LANES>(most, part, turn);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = r.at(j);
@@ -227,38 +259,42 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, false>(), !WARP && NV =
         }
         c = scale_of(c);
         const float inv = 1.f / c;
-        if (r.in(j)) {
+        if (on && r.in(j)) {
           if (a.group == a.d ? at == 0 : (at & (gl - 1)) == 0) a.scale[row * (a.d / a.group) + at * N / a.group] = c;
-          uint32_t u[N / 4];
+          if constexpr (N == 1) {
+            a.y8[row * a.d + at] = e4m3(s[j][0] * inv);
+            continue;
+          }
+          uint32_t u[(N + 3) / 4];
 #pragma unroll
           for (int e = 0; e < N / 4; ++e)
             u[e] = e4m3x2(s[j][4 * e] * inv, s[j][4 * e + 1] * inv) |
                    e4m3x2(s[j][4 * e + 2] * inv, s[j][4 * e + 3] * inv) << 16;
           uint32_t* p = reinterpret_cast<uint32_t*>(a.y8 + row * a.d + (long long)at * N);
           if constexpr (N == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(u[0], u[1]));
-          else __stcs(p, u[0]);
+          else if constexpr (N == 4) __stcs(p, u[0]);
         }
       }
     }
   }
 }
 
-template <class E, int NV, bool WARP>
-__global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(Args a) {
-  using R = Row<E, NV, WARP>;
-  using V = typename R::V;
-  using T = typename R::T;
-  constexpr int N = R::N, RPB = WARP ? kWarpRows : 1;
+template <class V, int NV, int LANES>
+__global__ void __launch_bounds__(most_threads<V, NV, LANES, true>()) k_rmsnorm_bwd(Args a) {
+  using R = Row<V, NV, LANES>;
+  using E = typename V::E;
+  using T = typename V::T;
+  constexpr int N = V::N, RPB = kRows<LANES>;
   extern __shared__ float sums[];                // [RPB][d] where a block has several rows
   __shared__ Part part;
   int turn = 0;
-  if (!WARP) part.clear();
+  if (!LANES) part.clear();
   const R r(a.d);
   float w[NV][N], gw[NV][N] = {};
   r.weights(w, a.w);
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
-  long long row = (long long)blockIdx.x * RPB + (WARP ? threadIdx.x >> 5 : 0);
+  long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
   T sv[NV], gv[NV], rv[NV];
   float rstd = 0.f;
   auto fetch = [&](long long row) {
@@ -268,7 +304,8 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
     if (row < a.rows) rstd = a.rstd_in[row];
   };
   fetch(row);
-  for (; row < a.rows; row += step) {
+  for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
+    const bool on = row < a.rows;
     const long long at = row * a.d;
     T cs[NV], cg[NV], cv[NV];
     const float rs = rstd;
@@ -283,7 +320,7 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
     // n = s rstd, dn = grad_y w; formed twice rather than kept, for the registers
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (r.in(j)) {
+      if (on && r.in(j)) {
         float n[N], g[N];
         V::get(n, cs[j]);
         V::get(g, cg[j]);
@@ -294,10 +331,10 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
           dot = fmaf(g[e] * w[j][e], n[e], dot);
         }
       }
-    dot = over_row<Sum, WARP>(dot, part, turn) * inv_d;
+    dot = over_row<Sum, LANES>(dot, part, turn) * inv_d;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (r.in(j)) {
+      if (on && r.in(j)) {
         float n[N], g[N], o[N];
         V::get(n, cs[j]);
         V::get(g, cg[j]);
@@ -312,28 +349,25 @@ __global__ void __launch_bounds__(most_threads<NV, WARP, true>()) k_rmsnorm_bwd(
         __stcs(reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at) + r.at(j), V::make(o));
       }
   }
-  // The block's row of partial sums, its rows' warps in order.
+  // The block's row of partial sums, its rows' lanes in order.
   float* out = a.part + (long long)blockIdx.x * a.d;
-  float* to = WARP ? sums + (threadIdx.x >> 5) * a.d : out;
+  float* to = LANES ? sums + threadIdx.x / (LANES ? LANES : 1) * a.d : out;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
     if (r.in(j))
 #pragma unroll
-      for (int e = 0; e < N; e += 4)
-        *reinterpret_cast<float4*>(to + r.at(j) * N + e) =
-            make_float4(gw[j][e], gw[j][e + 1], gw[j][e + 2], gw[j][e + 3]);
-  if constexpr (WARP) {
+      for (int e = 0; e < N; ++e) to[r.at(j) * N + e] = gw[j][e];
+  if constexpr (LANES > 0) {
     __syncthreads();
-    for (int i = threadIdx.x; i < a.d; i += 32 * kWarpRows) {
+    for (int i = threadIdx.x; i < a.d; i += kLaneThreads) {
       float v = sums[i];
-      for (int g = 1; g < kWarpRows; ++g) v += sums[g * a.d + i];
+      for (int g = 1; g < RPB; ++g) v += sums[g * a.d + i];
       out[i] = v;
     }
   }
 }
 
-// Rows that are no whole number of 16-byte vectors, or longer than the
-// registers hold: one block a row, element by element, each row read again
+// Rows longer than the registers hold, and scales of other widths: one block a row, element by element, each row read again
 // from cache for its second pass.
 constexpr int kAnyThreads = 256;
 
@@ -347,7 +381,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
     const E* r = static_cast<const E*>(a.residual) + row * a.d;
     auto stream = [&](int i) {
       float v = load1(x + i);
-      if (a.residual) v = Vec<E>::round(v + load1(r + i));
+      if (a.residual) v = Vec<E, 1>::round(v + load1(r + i));
       return v;
     };
     float sq = 0.f;
@@ -355,7 +389,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
       const float v = stream(i);
       sq = fmaf(v, v, sq);
     }
-    sq = over_row<Sum, false>(sq, part, turn);
+    sq = over_row<Sum, 0>(sq, part, turn);
     const float rstd = 1.f / sqrtf(fmaf(sq, 1.f / (float)a.d, a.eps));
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
@@ -368,7 +402,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(Args a) {
         float most = 0.f;
         for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads)
           most = max_nan(most, fabsf(stream(i) * rstd * a.w[i]));
-        most = scale_of(over_row<Max, false>(most, part, turn));
+        most = scale_of(over_row<Max, 0>(most, part, turn));
         const float inv = 1.f / most;
         if (threadIdx.x == 0) a.scale[row * (a.d / a.group) + g0 / a.group] = most;
         for (int i = g0 + threadIdx.x; i < g0 + a.group; i += kAnyThreads) {
@@ -398,7 +432,7 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
       gw[i] = fmaf(g, n, gw[i]);
       dot = fmaf(g * a.w[i], n, dot);
     }
-    dot = over_row<Sum, false>(dot, part, turn) / (float)a.d;
+    dot = over_row<Sum, 0>(dot, part, turn) / (float)a.d;
     for (int i = threadIdx.x; i < a.d; i += kAnyThreads) {
       float o = rstd * (load1(gy + i) * a.w[i] - load1(s + i) * rstd * dot);
       if (a.grad_s) o += load1(static_cast<const E*>(a.grad_s) + row * a.d + i);
@@ -411,61 +445,78 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(Args a) {
 // Blocks of the backward: at most kMaxBlocks rows of partial sums.
 constexpr int kMaxBlocks = 4 * kNumSMs;
 
-// Blocks of `kernel` that an SM holds at once.
-template <class K>
-static int resident(K kernel, int threads, size_t smem) {
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-  return n;
+// Blocks of `kernel` that an SM holds at once (asked once for each block size).
+template <auto KERNEL>
+static int resident(int threads, size_t smem) {
+  static int known[kWarps + 1] = {};
+  int n = known[threads / 32];
+  if (n > 0) return n;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, smem) != cudaSuccess || n < 1) n = 1;
+  return known[threads / 32] = n;
 }
 
-template <class E, int NV, bool WARP>
+template <class V, int NV, int LANES>
 static cudaError_t fwd(const Args& a, int threads, cudaStream_t st) {
-  constexpr int RPB = WARP ? kWarpRows : 1;
-  const long long need = (a.rows + RPB - 1) / RPB, most = (long long)resident(k_rmsnorm<E, NV, WARP>, threads, 0) * kNumSMs;
+  constexpr int RPB = kRows<LANES>;
+  const long long need = (a.rows + RPB - 1) / RPB, most = (long long)resident<&k_rmsnorm<V, NV, LANES>>(threads, 0) * kNumSMs;
   TraceScope tr("k_rmsnorm", st);
-  k_rmsnorm<E, NV, WARP><<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
+  k_rmsnorm<V, NV, LANES><<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
   return cudaGetLastError();
 }
-template <class E, int NV, bool WARP>
+template <class V, int NV, int LANES>
 static cudaError_t bwd(const Args& a, int threads, int* blocks, cudaStream_t st) {
-  constexpr int RPB = WARP ? kWarpRows : 1;
+  constexpr int RPB = kRows<LANES>;
+  const size_t smem = LANES ? (size_t)RPB * a.d * 4 : 0;
   const long long need = (a.rows + RPB - 1) / RPB;
-  const size_t smem = WARP ? (size_t)RPB * a.d * 4 : 0;
-  long long most = (long long)resident(k_rmsnorm_bwd<E, NV, WARP>, threads, smem) * kNumSMs;
+  long long most = (long long)resident<&k_rmsnorm_bwd<V, NV, LANES>>(threads, smem) * kNumSMs;
   if (most > kMaxBlocks) most = kMaxBlocks;
   *blocks = (int)(need < most ? need : most);
   TraceScope tr("k_rmsnorm_bwd", st);
-  k_rmsnorm_bwd<E, NV, WARP><<<*blocks, threads, smem, st>>>(a);
+  k_rmsnorm_bwd<V, NV, LANES><<<*blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-// The variant by row length: f.operator()<NV, WARP>(threads).
-template <class E, bool BWD, class F>
-static cudaError_t by_row(const Args& a, F f) {
-  const int nvec = a.d / Vec<E>::N;
+// The variant by row length, f.operator()<V, NV, LANES>(threads).  `lanes`: at
+// least so many lanes side by side (a scale's columns).
+template <class V, bool BWD, class F>
+static cudaError_t by_row(int d, int lanes, F f) {
+  const int nvec = d / V::N;
   auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
-  if (nvec <= 32) return f.template operator()<1, true>(32 * kWarpRows);
-  if (nvec <= 64) return f.template operator()<2, true>(32 * kWarpRows);
-  if (threads(2) <= most_threads<2, false, BWD>()) return f.template operator()<2, false>(threads(2));
-  if (threads(4) <= most_threads<4, false, BWD>()) return f.template operator()<4, false>(threads(4));
+  if constexpr (V::N > 1) {
+    if (nvec <= 16 && lanes <= 8) return f.template operator()<V, 2, 8>(kLaneThreads);
+    if (nvec <= 32 && lanes <= 16) return f.template operator()<V, 2, 16>(kLaneThreads);
+    if (nvec <= 64) return f.template operator()<V, 2, 32>(kLaneThreads);
+    if (threads(2) <= most_threads<V, 2, 0, BWD>()) return f.template operator()<V, 2, 0>(threads(2));
+    if (threads(4) <= most_threads<V, 4, 0, BWD>()) return f.template operator()<V, 4, 0>(threads(4));
+  } else {
+    if (threads(4) <= 128) return f.template operator()<V, 4, 0>(threads(4));
+    if (threads(8) <= 256) return f.template operator()<V, 8, 0>(threads(8));
+    if (threads(16) <= 512) return f.template operator()<V, 16, 0>(threads(16));
+  }
   return cudaErrorNotSupported;
 }
 
-template <class E> struct Fwd {
+struct Fwd {
   const Args& a; cudaStream_t st;
-  template <int NV, bool WARP> cudaError_t operator()(int threads) { return fwd<E, NV, WARP>(a, threads, st); }
+  template <class V, int NV, int LANES> cudaError_t operator()(int threads) { return fwd<V, NV, LANES>(a, threads, st); }
 };
-template <class E> struct Bwd {
+struct Bwd {
   const Args& a; int* blocks; cudaStream_t st;
-  template <int NV, bool WARP> cudaError_t operator()(int threads) { return bwd<E, NV, WARP>(a, threads, blocks, st); }
+  template <class V, int NV, int LANES> cudaError_t operator()(int threads) {
+    return bwd<V, NV, LANES>(a, threads, blocks, st);
+  }
 };
 
 template <class E>
 static cudaError_t forward(const Args& a, cudaStream_t st) {
-  const bool group_ok = !a.y8 || a.group == a.d || a.group == 32 || a.group == 64 || a.group == 128;
+  // scales of 32, 64 or 128 columns lie in neighbouring lanes
+  constexpr int N = kVecN<E>;
+  const bool parts = a.y8 && a.group != a.d;
   cudaError_t e = cudaErrorNotSupported;
-  if (a.d % 8 == 0 && group_ok) e = by_row<E, false>(a, Fwd<E>{a, st});
+  if (a.d % 8 == 0 && (!parts || a.group == 32 || a.group == 64 || a.group == 128))
+    e = by_row<Vec<E, N>, false>(a.d, parts ? a.group / N : 0, Fwd{a, st});
+  else if (!parts)
+    e = by_row<Vec<E, 1>, false>(a.d, 0, Fwd{a, st});
   if (e != cudaErrorNotSupported) return e;
   TraceScope tr("k_rmsnorm_any", st);
   k_rmsnorm_any<E><<<(unsigned)(a.rows < 8 * kNumSMs ? a.rows : 8 * kNumSMs), kAnyThreads, 0, st>>>(a);
@@ -477,7 +528,8 @@ static cudaError_t backward(const Args& a, float* grad_w, cudaStream_t st) {
   int blocks = 0;
   cudaError_t e = cudaErrorNotSupported;
   if (a.rows == 0) e = cudaSuccess;              // grad_w = 0
-  else if (a.d % 8 == 0) e = by_row<E, true>(a, Bwd<E>{a, &blocks, st});
+  else if (a.d % 8 == 0) e = by_row<Vec<E, kVecN<E>>, true>(a.d, 0, Bwd{a, &blocks, st});
+  else e = by_row<Vec<E, 1>, true>(a.d, 0, Bwd{a, &blocks, st});
   if (e == cudaErrorNotSupported) {
     const size_t bytes = (size_t)a.d * 4;
     if (bytes > 48 * 1024) {
