@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   const long long row0 = start + (long long)c * kC;
   const int rows = min(kC, len - c * kC);
   const int hq = h / (a.s.hv / a.s.hk);
+  // the gates are wanted after the products: asked for first, they are there by then
+  const float4 gb = warp == 0 ? load_gates(a, row0, rows, h, lane) : make_float4(0.f, 0.f, 0.f, 0.f);
   load_tile<E, kC, DK, 128>(ks, S::LDK, static_cast<const E*>(a.k) + row0 * a.ldk + (long long)hq * a.s.dk, a.ldk, rows,
                             a.s.dk, tid);
   load_tile<E, kC, DK, 128>(qs, S::LDK, static_cast<const E*>(a.q) + row0 * a.ldq + (long long)hq * a.s.dk, a.ldq, rows,
@@ -64,7 +66,6 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
   cp_commit();
   const long long id = slot * a.s.hv + h;
   float* vec = a.vec + id * kVec;
-  if (warp == 0) chunk_decays(a, row0, rows, h, lane, g2, bet, vec);
   cp_wait<0>();
   __syncthreads();
 
@@ -88,6 +89,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep(FwdArgs a) {
       }
     }
   }
+  if (warp == 0) chunk_decays(gb, lane, g2, bet, vec);      // the warp with the fewest products
   __syncthreads();
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {

@@ -424,21 +424,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(h, e - (h - s));
 }
 
-// The decays of a chunk's head, by one warp: into `vec`, and for the block
-// G / ln 2 as pairs hi + lo and beta.
-__device__ __forceinline__ void chunk_decays(const FwdArgs& a, long long row0, int rows, int h, int lane, float2* g2,
-                                             float* bet, float* vec) {
+// The decays of a chunk's head, by one warp whose lanes hold g (gb.x, gb.y) and
+// beta (gb.z, gb.w) of rows 2 lane and 2 lane + 1: into `vec`, and for the
+// block G / ln 2 as pairs hi + lo and beta.
+__device__ __forceinline__ float4 load_gates(const FwdArgs& a, long long row0, int rows, int h, int lane) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  const long long at = (row0 + 2 * lane) * a.s.hv + h;
+  if (2 * lane < rows) { v.x = a.g[at]; v.z = a.beta[at]; }
+  if (2 * lane + 1 < rows) { v.y = a.g[at + a.s.hv]; v.w = a.beta[at + a.s.hv]; }
+  return v;
+}
+__device__ __forceinline__ void chunk_decays(const float4& gb, int lane, float2* g2, float* bet, float* vec) {
   // Running sum of g as a pair of floats hi + lo: differences of G then carry
   // no more than their own fp32 rounding, however far the sum has gone.  (In
   // double this was the longest part of the kernel: the fp64 rate is 1/64.)
-  float2 x[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 2 * lane + i;
-    const float v = r < rows ? a.g[(row0 + r) * a.s.hv + h] : 0.f;
-    x[i] = make_float2(v < kMinG ? kMinG : v, 0.f);          // a NaN stays
-    bet[r] = r < rows ? a.beta[(row0 + r) * a.s.hv + h] : 0.f;
-  }
+  float2 x[2] = {make_float2(gb.x < kMinG ? kMinG : gb.x, 0.f), make_float2(gb.y < kMinG ? kMinG : gb.y, 0.f)};  // a NaN stays
   x[1] = add2(x[0], x[1]);
   float2 run = x[1];
 #pragma unroll
@@ -460,7 +460,7 @@ __device__ __forceinline__ void chunk_decays(const FwdArgs& a, long long row0, i
     g2[r] = gu;
     vec[kVecEG + r] = expf(G[i].x + G[i].y);
     vec[kVecEGL + r] = expf((total.x - G[i].x) + (total.y - G[i].y));
-    vec[kVecBeta + r] = bet[r];
+    bet[r] = vec[kVecBeta + r] = i ? gb.w : gb.z;
     reinterpret_cast<float2*>(vec + kVecG2)[r] = gu;
   }
   if (lane == 0) vec[kVecD] = expf(total.x + total.y);
@@ -478,10 +478,16 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
     const float* blk = am + m0 * LDA + m0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float v = i == lane ? 1.f : 0.f;
+      float v = i == lane ? 1.f : 0.f, u = 0.f;
 #pragma unroll
-      for (int m = 0; m < i; ++m) v = fmaf(-blk[i * LDA + m], x[m], v);
-      x[i] = v;
+      for (int m = 0; m < i; m += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(blk + i * LDA + m);
+        v = fmaf(-b.x, x[m], v);
+        if (m + 1 < i) u = fmaf(-b.y, x[m + 1], u);
+        if (m + 2 < i) v = fmaf(-b.z, x[m + 2], v);
+        if (m + 3 < i) u = fmaf(-b.w, x[m + 3], u);
+      }
+      x[i] = v + u;
     }
     __syncwarp(0xffffu);
 #pragma unroll
@@ -493,7 +499,7 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
     float* t21 = am + (warp * 32 + 16) * LDA + warp * 32;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-      float d[2][4] = {};
+      float d[2][4] = {}, e[2][4] = {};
       const float* fa = pass == 0 ? t21 : t21 + 16;
       const float* fb = pass == 0 ? t21 - 16 * LDA : t21;
       const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
@@ -503,15 +509,15 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
         MFp32::B<1> xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
-        MFp32::mma(d[0], xa, xb, 0);
-        MFp32::mma(d[1], xa, xb, 1);
+        MFp32::mma(d[0], e[0], xa, xb, 0);
+        MFp32::mma(d[1], e[1], xa, xb, 1);
       }
       __syncwarp();
       const float sg = pass == 0 ? 1.f : -1.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float2*>(t21 + g * LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
-        *reinterpret_cast<float2*>(t21 + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+        *reinterpret_cast<float2*>(t21 + g * LDA + j * 8 + t2) = make_float2(sg * (d[j][0] + e[j][0]), sg * (d[j][1] + e[j][1]));
+        *reinterpret_cast<float2*>(t21 + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * (d[j][2] + e[j][2]), sg * (d[j][3] + e[j][3]));
       }
       __syncwarp();
     }
@@ -523,7 +529,7 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
     float* mine = t21 + (warp & 1) * 16 * LDA;
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
-      float d[2][4] = {};
+      float d[2][4] = {}, e[2][4] = {};
       const float* fa = am + (32 + (warp & 1) * 16) * LDA + (pass == 0 ? 0 : 32);
       const float* fb = pass == 0 ? am + (warp >> 1) * 16 : t21;
       const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
@@ -533,15 +539,15 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
         MFp32::B<1> xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
-        MFp32::mma(d[0], xa, xb, 0);
-        MFp32::mma(d[1], xa, xb, 1);
+        MFp32::mma(d[0], e[0], xa, xb, 0);
+        MFp32::mma(d[1], e[1], xa, xb, 1);
       }
       __syncthreads();
       const float sg = pass == 0 ? 1.f : -1.f;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<float2*>(mine + g * LDA + j * 8 + t2) = make_float2(sg * d[j][0], sg * d[j][1]);
-        *reinterpret_cast<float2*>(mine + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * d[j][2], sg * d[j][3]);
+        *reinterpret_cast<float2*>(mine + g * LDA + j * 8 + t2) = make_float2(sg * (d[j][0] + e[j][0]), sg * (d[j][1] + e[j][1]));
+        *reinterpret_cast<float2*>(mine + (g + 8) * LDA + j * 8 + t2) = make_float2(sg * (d[j][2] + e[j][2]), sg * (d[j][3] + e[j][3]));
       }
       __syncthreads();
     }
