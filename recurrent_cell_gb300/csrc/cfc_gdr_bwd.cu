@@ -1,4 +1,5 @@
-// cfc_gdr_bwd.cu -- backward of the gated delta rule over whole sequences
+// cfc_gdr_bwd.cu -- backward of the gated delta rule over whole sequences: its
+// formulas, dispatch, and the kernels in FP32 (bf16: cfc_gdr_tc.cu, cfc_gdr_grad.cu)
 // (notation of gdr_common.cuh; the forward left T, P, the decays, S0 and U of
 // every chunk in the workspace).
 //
@@ -29,256 +30,201 @@ namespace cfc {
 namespace gdr {
 
 // -------------------------------------------------------------- serial pass
-// The forward scan's split of warps: dS^T in registers, 16 MT value columns by
-// a quarter of the key width a warp.
-template <class P, int DK, int MT, int WM>
+// The forward scan's split of the chain's warps: dS^T in registers, 16 value
+// columns by a quarter of the key width a warp.
+template <int DK, int WM>
 struct BwdCfg {
-  using E = typename P::E;
-  static constexpr int DVT = 16 * MT * WM, THREADS = 128 * WM;
-  static constexpr int LDK = DK + P::PAD, LDT = kC + P::PAD, LDV = DVT + P::PAD;
-  static constexpr int NTS = DK / 32, ST = P::STAGES;
-  static constexpr int kQ = kC * LDK, kT = kC * LDT, kV = kC * LDV;
-  static constexpr int STAGE = 2 * kQ + 2 * kT + kV;
-  static constexpr int SOP = DVT * LDK, ROP = DVT * LDT;
-  // dS operand, dU operand, scaled dO, dR, -beta exp(G) dR; the two dR matrices
-  // lie over the dS operand where shared memory is short.  dv is staged over
-  // the chunk's dO, which has been read by then.
-  static constexpr bool ALIAS = (size_t)(ST * STAGE + SOP + 4 * ROP) * sizeof(E) + 2 * kVec * 4 > 227u * 1024u;
-  static constexpr int ELEMS = ST * STAGE + (ALIAS ? (SOP > 2 * ROP ? SOP : 2 * ROP) : SOP + 2 * ROP) + 2 * ROP;
-  static constexpr size_t BYTES = (size_t)ELEMS * sizeof(E) + (size_t)ST * kVec * 4;
-  static constexpr bool FITS = BYTES <= 227u * 1024u;
+  static constexpr int DVT = 16 * WM, THREADS = 128 * WM;
+  static constexpr int LDK = DK + kPad, LDV = DVT + kPad, NTS = DK / 32;
+  static constexpr int kQ = kC * LDK, kT = kC * kLdT, kV = kC * LDV;
+  static constexpr int SOP = DVT * LDK, ROP = DVT * kLdT;
+  // k, q, T - I, P, dO (then dv), the vectors; the operands dS, dU, scaled dO, -beta exp(G) dR
+  static constexpr int ELEMS = 2 * kQ + 2 * kT + kV + kVec + SOP + 3 * ROP;
+  static constexpr size_t BYTES = ELEMS * sizeof(float);
+  static_assert(BYTES <= 227u * 1024u, "shared memory");
 };
 
-template <class P, int DK, int MT, int WM>
+template <int DK, int WM>
 __global__ void __launch_bounds__(128 * WM) k_gdr_scan_bwd(BwdArgs a) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  using C = BwdCfg<P, DK, MT, WM>;
-  using E = typename P::E;
-  constexpr int NTS = C::NTS, ST = C::ST;
-  float* vecs = reinterpret_cast<float*>(smem_raw);
-  E* stage = reinterpret_cast<E*>(vecs + ST * kVec);
-  E* sop_p = stage + ST * C::STAGE;
-  E* dr_p = C::ALIAS ? sop_p : sop_p + C::SOP;
-  E* drk_p = dr_p + C::ROP;
-  E* uop_p = sop_p + (C::ELEMS - ST * C::STAGE - 2 * C::ROP);
-  E* dop_p = uop_p + C::ROP;
-  const Mat<E> sop{sop_p, C::LDK, 0}, uop{uop_p, C::LDT, 0}, dop{dop_p, C::LDT, 0}, drk{drk_p, C::LDT, 0};
+  extern __shared__ __align__(16) float smem[];
+  using C = BwdCfg<DK, WM>;
+  constexpr int NTS = C::NTS;
+  const Mat<float> mk{smem, C::LDK}, mq{mk.p + C::kQ, C::LDK}, mt{mq.p + C::kQ, kLdT}, mp{mt.p + C::kT, kLdT},
+      mo{mp.p + C::kT, C::LDV};
+  float* vec = mo.p + C::kV;
+  const Mat<float> sop{vec + kVec, C::LDK}, uop{sop.p + C::SOP, kLdT}, dop{uop.p + C::ROP, kLdT},
+      drk{dop.p + C::ROP, kLdT};
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wn = warp & 3, wm = warp >> 2;
-  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wn = warp & 3, m0 = (warp >> 2) * 16;
+  const int g = lane >> 2, t2 = (lane & 3) * 2, i0 = wn * 16 + t2;
   const int tile = blockIdx.x % a.ntile;
   const long long sh = blockIdx.x / a.ntile;
   const int h = (int)(sh % a.s.hv), n = (int)(sh / a.s.hv);
   const int hq = h / (a.s.hv / a.s.hk);
   const int dk = a.s.dk, dv = a.s.dv, dv0 = tile * C::DVT, dvn = min(C::DVT, dv - dv0);
-  const int m0 = wm * 16 * MT;
   long long start;
   int len;
   seq_range(a.s, n, &start, &len);
   const int nc = (len + kC - 1) / kC;
   const long long slot0 = slot_base(start, n);
   const long long ldo = (long long)a.s.hv * dv;
-  const E* q = static_cast<const E*>(a.q) + start * a.ldq + (long long)hq * dk;
-  const E* k = static_cast<const E*>(a.k) + start * a.ldk + (long long)hq * dk;
-  const E* go = static_cast<const E*>(a.go) + (start * a.s.hv + h) * dv + dv0;
-  E* gv = static_cast<E*>(a.gv) + (start * a.s.hv + h) * dv + dv0;
+  const float* q = static_cast<const float*>(a.q) + start * a.ldq + (long long)hq * dk;
+  const float* k = static_cast<const float*>(a.k) + start * a.ldk + (long long)hq * dk;
+  const float* go = static_cast<const float*>(a.go) + (start * a.s.hv + h) * dv + dv0;
+  float* gv = static_cast<float*>(a.gv) + (start * a.s.hv + h) * dv + dv0;
 
-  auto fetch = [&](int c, int st) {
-    E* b = stage + st * C::STAGE;
+  auto fetch = [&](int c) {
     const int rows = min(kC, len - c * kC);
     const long long r0 = (long long)c * kC, id = (slot0 + c) * a.s.hv + h;
-    load_tile<E, kC, DK, C::THREADS>(b, C::LDK, k + r0 * a.ldk, a.ldk, rows, dk, tid);
-    load_tile<E, kC, DK, C::THREADS>(b + C::kQ, C::LDK, q + r0 * a.ldq, a.ldq, rows, dk, tid);
-    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ, C::LDT,
-                                     reinterpret_cast<const E*>(a.t) + id * (kTPlanes<P> * kC * C::LDT), C::LDT, kC, kC,
-                                     tid);
-    load_tile<E, kC, kC, C::THREADS>(b + 2 * C::kQ + C::kT, C::LDT, reinterpret_cast<const E*>(a.p) + id * (kTPlanes<P> * kC * C::LDT),
-                                     C::LDT, kC, kC, tid);
-    load_tile<E, kC, C::DVT, C::THREADS>(b + 2 * C::kQ + 2 * C::kT, C::LDV, go + r0 * ldo, ldo, rows, dvn, tid);
-    for (int i = tid; i < kVec / 4; i += C::THREADS) cp16(vecs + st * kVec + i * 4, a.vec + id * kVec + i * 4, true);
+    load_tile<float, kC, DK, C::THREADS>(mk.p, C::LDK, k + r0 * a.ldk, a.ldk, rows, dk, tid);
+    load_tile<float, kC, DK, C::THREADS>(mq.p, C::LDK, q + r0 * a.ldq, a.ldq, rows, dk, tid);
+    load_tile<float, kC, kC, C::THREADS>(mt.p, kLdT, reinterpret_cast<const float*>(a.t) + id * C::kT, kLdT, kC, kC, tid);
+    load_tile<float, kC, kC, C::THREADS>(mp.p, kLdT, reinterpret_cast<const float*>(a.p) + id * C::kT, kLdT, kC, kC, tid);
+    load_tile<float, kC, C::DVT, C::THREADS>(mo.p, C::LDV, go + r0 * ldo, ldo, rows, dvn, tid);
+    for (int i = tid; i < kVec / 4; i += C::THREADS) cp16(vec + i * 4, a.vec + id * kVec + i * 4, true);
     cp_commit();
   };
-
-  float s[MT][NTS][4];
+  // dS^T: element e of 8-column tile nt is value column m0 + g + 8 (e / 2), key column:
+  auto key = [&](int nt, int e) { return wn * (DK / 4) + nt * 8 + t2 + (e & 1); };
+  float s[NTS][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = m0 + g + (e >> 1) * 8;
+      s[nt][e] = a.gfinal && r < dvn && key(nt, e) < dk ? a.gfinal[(sh * dk + key(nt, e)) * dv + dv0 + r] : 0.f;
+    }
+
+  if (nc > 0) fetch(nc - 1);
+  for (int c = nc - 1; c >= 0; --c) {
+    const long long id = (slot0 + c) * a.s.hv + h;
+    cp_wait<0>();
+    float* ds = reinterpret_cast<float*>(a.ds) + id * dk * dv + dv0;
+#pragma unroll
+    for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = m0 + g + rr * 8;
+        F::put2(sop, r, key(nt, 0), s[nt][2 * rr], s[nt][2 * rr + 1]);
+        if (r < dvn && key(nt, 0) < dk) {
+          ds[(long long)key(nt, 0) * dv + r] = s[nt][2 * rr];
+          ds[(long long)key(nt, 1) * dv + r] = s[nt][2 * rr + 1];
+        }
+      }
+    __syncthreads();
+    // dU of this warp's 16 tokens
+    float ak[2][4] = {}, ap[2][4] = {}, al[2][4] = {}, ar[2][4], aw[2][4] = {};
+#pragma unroll
+    for (int k0 = 0; k0 < DK; k0 += F::KS) {
+      F::A fa;
+      F::B fb;
+      F::load_a(fa, sop, m0, k0, lane);
+      F::load_bn(fb, mk, wn * 16, k0, lane);
+      F::mma(ak[0], al[0], fa, fb, 0);
+      F::mma(ak[1], al[1], fa, fb, 1);
+    }
+#pragma unroll
+    for (int k0 = 0; k0 < kC; k0 += F::KS) {
+      if (k0 + F::KS <= wn * 16) continue;
+      F::A fa;
+      F::B fb;
+      F::load_at(fa, mo, m0, k0, lane);
+      F::load_bk(fb, mp, wn * 16, k0, lane);
+      F::mma(ap[0], fa, fb, 0);
+      F::mma(ap[1], fa, fb, 1);
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int i = i0 + hf * 8;
+      const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
+      const float2 el = *reinterpret_cast<const float2*>(vec + kVecEGL + i);
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = m0 + g + rr * 8;
+        ar[hf][2 * rr] = el.x * (ak[hf][2 * rr] + al[hf][2 * rr]) + ap[hf][2 * rr];
+        ar[hf][2 * rr + 1] = el.y * (ak[hf][2 * rr + 1] + al[hf][2 * rr + 1]) + ap[hf][2 * rr + 1];
+        F::put2(uop, r, i, ar[hf][2 * rr], ar[hf][2 * rr + 1]);
+        F::put2(dop, r, i, a.s.scale * eg.x * mo.p[i * C::LDV + r], a.s.scale * eg.y * mo.p[(i + 1) * C::LDV + r]);
+      }
+    }
+    __syncthreads();
+    // dR = dU + (T - I)^T dU
+#pragma unroll
+    for (int k0 = 0; k0 < kC; k0 += F::KS) {
+      if (k0 + F::KS <= wn * 16) continue;
+      F::A fa;
+      F::B fb;
+      F::load_a(fa, uop, m0, k0, lane);
+      F::load_bk(fb, mt, wn * 16, k0, lane);
+      F::mma(ar[0], aw[0], fa, fb, 0);
+      F::mma(ar[1], aw[1], fa, fb, 1);
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int i = i0 + hf * 8;
+      const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
+      const float2 be = *reinterpret_cast<const float2*>(vec + kVecBeta + i);
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const int r = m0 + g + rr * 8;
+        const float r0 = ar[hf][2 * rr] + aw[hf][2 * rr], r1 = ar[hf][2 * rr + 1] + aw[hf][2 * rr + 1];
+        if (r < dvn) {
+          float* p = reinterpret_cast<float*>(a.dr) + (id * kC + i) * dv + dv0 + r;
+          p[0] = r0;
+          p[dv] = r1;
+        }
+        F::put2(drk, r, i, -be.x * eg.x * r0, -be.y * eg.y * r1);
+        mo.p[i * C::LDV + r] = be.x * r0;              // dv, over dO
+        mo.p[(i + 1) * C::LDV + r] = be.y * r1;
+      }
+    }
+    __syncthreads();
+    store_tile<float, kC, C::DVT, C::THREADS>(gv + (long long)c * kC * ldo, ldo, mo.p, C::LDV, len - c * kC, dvn, tid);
+    // dS0 = exp(G_C) dS1 + sum_i scale exp(G_i) dO_i q_i^T - beta_i exp(G_i) dR_i k_i^T
+    const float d = vec[kVecD];
+#pragma unroll
+    for (int nt = 0; nt < NTS; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] *= d;
+#pragma unroll
+    for (int k0 = 0; k0 < kC; k0 += F::KS) {
+      F::A fd, fr;
+      F::load_a(fd, dop, m0, k0, lane);
+      F::load_a(fr, drk, m0, k0, lane);
+#pragma unroll
+      for (int j = 0; j < NTS / 2; ++j) {
+        F::B bq, bk;
+        F::load_bk(bq, mq, wn * (DK / 4) + j * 16, k0, lane);
+        F::load_bk(bk, mk, wn * (DK / 4) + j * 16, k0, lane);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          F::mma(s[2 * j + hf], fd, bq, hf);
+          F::mma(s[2 * j + hf], fr, bk, hf);
+        }
+      }
+    }
+    __syncthreads();
+    if (c > 0) fetch(c - 1);
+  }
+  if (a.ginit)
 #pragma unroll
     for (int nt = 0; nt < NTS; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
-        s[mt][nt][e] = a.gfinal && r < dvn && col < dk ? a.gfinal[(sh * dk + col) * dv + dv0 + r] : 0.f;
+        const int r = m0 + g + (e >> 1) * 8;
+        if (r < dvn && key(nt, e) < dk) a.ginit[(sh * dk + key(nt, e)) * dv + dv0 + r] = s[nt][e];
       }
-
-  if (nc > 0) fetch(nc - 1, (nc - 1) & (ST - 1));
-  for (int c = nc - 1; c >= 0; --c) {
-    const int st = c & (ST - 1);
-    E* b = stage + st * C::STAGE;
-    const Mat<E> mk{b, C::LDK, 0}, mq{b + C::kQ, C::LDK, 0}, mt_{b + 2 * C::kQ, C::LDT, 0},
-        mp{b + 2 * C::kQ + C::kT, C::LDT, 0}, mo{b + 2 * C::kQ + 2 * C::kT, C::LDV, 0};
-    const float* vec = vecs + st * kVec;
-    const long long id = (slot0 + c) * a.s.hv + h;
-    cp_wait<0>();
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr)
-          P::template put2<1>(sop, m0 + mt * 16 + g + rr * 8, wn * (DK / 4) + nt * 8 + t2, s[mt][nt][2 * rr],
-                              s[mt][nt][2 * rr + 1]);
-    __syncthreads();
-    if (ST == 2 && c > 0) fetch(c - 1, (c - 1) & 1);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
-          if (r < dvn && col < dk) put(reinterpret_cast<E*>(a.ds) + (id * dk + col) * dv + dv0 + r, s[mt][nt][e]);
-        }
-    // dU of this warp's 16 tokens
-    float ak[MT][2][4] = {}, ap[MT][2][4] = {}, ar[MT][2][4];
-#pragma unroll
-    for (int k0 = 0; k0 < DK; k0 += P::KS) {
-      typename P::template B<1> bk;
-      P::load_bn(bk, mk, wn * 16, k0, lane);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        typename P::template A<1> fa;
-        P::load_a(fa, sop, m0 + mt * 16, k0, lane);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) P::mma(ak[mt][hf], fa, bk, hf);
-      }
-    }
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      if (k0 + P::KS <= wn * 16) continue;
-      typename P::template B<1> bp;
-      P::load_bk(bp, mp, wn * 16, k0, lane);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        typename P::template A<1> fa;
-        P::load_at(fa, mo, m0 + mt * 16, k0, lane);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) P::mma(ap[mt][hf], fa, bp, hf);
-      }
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int i = wn * 16 + hf * 8 + t2;
-      const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
-      const float2 el = *reinterpret_cast<const float2*>(vec + kVecEGL + i);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = m0 + mt * 16 + g + rr * 8;
-          // dR = dU + (T - I)^T dU: dU itself stays fp32
-          ar[mt][hf][2 * rr] = el.x * ak[mt][hf][2 * rr] + ap[mt][hf][2 * rr];
-          ar[mt][hf][2 * rr + 1] = el.y * ak[mt][hf][2 * rr + 1] + ap[mt][hf][2 * rr + 1];
-          P::template put2<1>(uop, r, i, ar[mt][hf][2 * rr], ar[mt][hf][2 * rr + 1]);
-          P::template put2<1>(dop, r, i, a.s.scale * eg.x * to_f(mo.p[i * C::LDV + r]),
-                              a.s.scale * eg.y * to_f(mo.p[(i + 1) * C::LDV + r]));
-        }
-    }
-    __syncthreads();
-    E* gst = mo.p;
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      if (k0 + P::KS <= wn * 16) continue;
-      typename P::template B<1> bt;
-      P::load_bk(bt, mt_, wn * 16, k0, lane);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        typename P::template A<1> fa;
-        P::load_a(fa, uop, m0 + mt * 16, k0, lane);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) P::mma(ar[mt][hf], fa, bt, hf);
-      }
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int i = wn * 16 + hf * 8 + t2;
-      const float2 eg = *reinterpret_cast<const float2*>(vec + kVecEG + i);
-      const float2 be = *reinterpret_cast<const float2*>(vec + kVecBeta + i);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          const int r = m0 + mt * 16 + g + rr * 8;
-          const float r0 = ar[mt][hf][2 * rr], r1 = ar[mt][hf][2 * rr + 1];
-          if (r < dvn) {
-            E* p = reinterpret_cast<E*>(a.dr) + (id * kC + i) * dv + dv0 + r;
-            put(p, r0);
-            put(p + dv, r1);
-          }
-          P::template put2<1>(drk, r, i, -be.x * eg.x * r0, -be.y * eg.y * r1);
-          put(gst + i * C::LDV + r, be.x * r0);
-          put(gst + (i + 1) * C::LDV + r, be.y * r1);
-        }
-    }
-    __syncthreads();
-    store_tile<E, kC, C::DVT, C::THREADS>(gv + (long long)c * kC * ldo, ldo, gst, C::LDV, len - c * kC, dvn, tid);
-    const float d = vec[kVecD];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= d;
-#pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
-      typename P::template A<1> fd[MT], fr[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        P::load_a(fd[mt], dop, m0 + mt * 16, k0, lane);
-        P::load_a(fr[mt], drk, m0 + mt * 16, k0, lane);
-      }
-#pragma unroll
-      for (int j = 0; j < NTS / 2; ++j) {
-        typename P::template B<1> bq, bk;
-        P::load_bk(bq, mq, wn * (DK / 4) + j * 16, k0, lane);
-        P::load_bk(bk, mk, wn * (DK / 4) + j * 16, k0, lane);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            P::mma(s[mt][2 * j + hf], fd[mt], bq, hf);
-            P::mma(s[mt][2 * j + hf], fr[mt], bk, hf);
-          }
-      }
-    }
-    if (ST == 1 || C::ALIAS) __syncthreads();
-    if (ST == 1 && c > 0) fetch(c - 1, 0);
-  }
-  if (a.ginit) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NTS; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = m0 + mt * 16 + g + (e >> 1) * 8, col = wn * (DK / 4) + nt * 8 + t2 + (e & 1);
-          if (r < dvn && col < dk) a.ginit[(sh * dk + col) * dv + dv0 + r] = s[mt][nt][e];
-        }
-  }
 }
 
 // ------------------------------------------------------------- the gradients
-template <class P, int DK>
+template <int DK>
 struct GradSmem {
-  using E = typename P::E;
   static constexpr int DVS = 32;                       // value columns of a slice
-  static constexpr int ST = P::STAGES;
-  static constexpr int LDK = DK + P::PAD, LDT = kC + P::PAD, LDV = DVS + P::PAD;
-  E k[kC * LDK], q[kC * LDK];
-  E go[ST][kC * LDV], v[ST][kC * LDV];
-  E u[ST][kC * LDV], dr[ST][kC * LDV];
-  E s0[ST][DK * LDV], ds[ST][DK * LDV];
-  static constexpr int PL = kTPlanes<P>;
-  E dp[PL * kC * LDT], da[PL * kC * LDT], dm[PL * kC * LDT];    // 17 bits in bf16: dg is a difference of large sums
+  static constexpr int LDK = DK + kPad, LDV = DVS + kPad;
+  float k[kC * LDK], q[kC * LDK];
+  float go[kC * LDV], v[kC * LDV], u[kC * LDV], dr[kC * LDV];
+  float s0[DK * LDV], ds[DK * LDV];
+  float dp[kC * kLdT], da[kC * kLdT], dm[kC * kLdT];
   float vec[kVec];
   float dot[4][2][kC];    // q.dq, k.dk, k.E, k.dS1 U by half of the key width
   float drv[4][kC];
@@ -286,14 +232,13 @@ struct GradSmem {
   float dg[kC];
 };
 
-template <class P, int DK>
+template <int DK>
 __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  using S = GradSmem<P, DK>;
-  using E = typename P::E;
+  using S = GradSmem<DK>;
   S& sm = *reinterpret_cast<S*>(smem_raw);
   constexpr int NT = DK / 16;           // 8-column tiles of half the key width
-  constexpr int DVS = S::DVS, ST = S::ST;
+  constexpr int DVS = S::DVS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wr = warp & 3, wc = warp >> 2;
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   const int h = blockIdx.x % a.s.hv;
@@ -307,64 +252,62 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
   const int dk = a.s.dk, dv = a.s.dv;
   const long long id = slot * a.s.hv + h;
   const long long ldo = (long long)a.s.hv * dv;
-  const E* go = static_cast<const E*>(a.go) + row0 * ldo + (long long)h * dv;
-  const E* v = static_cast<const E*>(a.v) + row0 * a.ldv + (long long)h * dv;
+  const float* go = static_cast<const float*>(a.go) + row0 * ldo + (long long)h * dv;
+  const float* v = static_cast<const float*>(a.v) + row0 * a.ldv + (long long)h * dv;
 
-  auto fetch = [&](int x, int st) {
+  auto fetch = [&](int x) {
     const int v0 = x * DVS, vn = min(DVS, dv - v0);
-    load_tile<E, kC, DVS, 256>(sm.go[st], S::LDV, go + v0, ldo, rows, vn, tid);
-    load_tile<E, kC, DVS, 256>(sm.v[st], S::LDV, v + v0, a.ldv, rows, vn, tid);
-    load_tile<E, kC, DVS, 256>(sm.u[st], S::LDV, reinterpret_cast<const E*>(a.u) + id * kC * dv + v0, dv, kC, vn, tid);
-    load_tile<E, kC, DVS, 256>(sm.dr[st], S::LDV, reinterpret_cast<const E*>(a.dr) + id * kC * dv + v0, dv, kC, vn, tid);
-    load_tile<E, DK, DVS, 256>(sm.s0[st], S::LDV, reinterpret_cast<const E*>(a.s0) + id * dk * dv + v0, dv, dk, vn, tid);
-    load_tile<E, DK, DVS, 256>(sm.ds[st], S::LDV, reinterpret_cast<const E*>(a.ds) + id * dk * dv + v0, dv, dk, vn, tid);
+    load_tile<float, kC, DVS, 256>(sm.go, S::LDV, go + v0, ldo, rows, vn, tid);
+    load_tile<float, kC, DVS, 256>(sm.v, S::LDV, v + v0, a.ldv, rows, vn, tid);
+    load_tile<float, kC, DVS, 256>(sm.u, S::LDV, reinterpret_cast<const float*>(a.u) + id * kC * dv + v0, dv, kC, vn, tid);
+    load_tile<float, kC, DVS, 256>(sm.dr, S::LDV, reinterpret_cast<const float*>(a.dr) + id * kC * dv + v0, dv, kC, vn, tid);
+    load_tile<float, DK, DVS, 256>(sm.s0, S::LDV, reinterpret_cast<const float*>(a.s0) + id * dk * dv + v0, dv, dk, vn, tid);
+    load_tile<float, DK, DVS, 256>(sm.ds, S::LDV, reinterpret_cast<const float*>(a.ds) + id * dk * dv + v0, dv, dk, vn, tid);
     cp_commit();
   };
-  load_tile<E, kC, DK, 256>(sm.k, S::LDK, static_cast<const E*>(a.k) + row0 * a.ldk + (long long)hq * dk, a.ldk, rows,
+  load_tile<float, kC, DK, 256>(sm.k, S::LDK, static_cast<const float*>(a.k) + row0 * a.ldk + (long long)hq * dk, a.ldk, rows,
                             dk, tid);
-  load_tile<E, kC, DK, 256>(sm.q, S::LDK, static_cast<const E*>(a.q) + row0 * a.ldq + (long long)hq * dk, a.ldq, rows,
+  load_tile<float, kC, DK, 256>(sm.q, S::LDK, static_cast<const float*>(a.q) + row0 * a.ldq + (long long)hq * dk, a.ldq, rows,
                             dk, tid);
   for (int i = tid; i < kVec / 4; i += 256) cp16(sm.vec + i * 4, a.vec + id * kVec + i * 4, true);
-  fetch(0, 0);
+  fetch(0);
 
   float aq[NT][4] = {}, ax[NT][4] = {}, au[NT][4] = {};   // S0 dO, X, dS1 U
   float ap[4][4] = {}, aa[4][4] = {};                     // dO.U, dR.U over 32 columns
   float drv = 0.f, ss = 0.f;
   const int ns = (dv + DVS - 1) / DVS;
   for (int x = 0; x < ns; ++x) {
-    const int st = x & (ST - 1);
     cp_wait<0>();
     __syncthreads();
-    if (ST == 2 && x + 1 < ns) fetch(x + 1, (x + 1) & 1);
-    const Mat<E> mo{sm.go[st], S::LDV, 0}, mu{sm.u[st], S::LDV, 0}, mr{sm.dr[st], S::LDV, 0}, ms{sm.s0[st], S::LDV, 0},
-        md{sm.ds[st], S::LDV, 0};
+    const Mat<float> mo{sm.go, S::LDV}, mu{sm.u, S::LDV}, mr{sm.dr, S::LDV}, ms{sm.s0, S::LDV},
+        md{sm.ds, S::LDV};
 #pragma unroll
-    for (int k0 = 0; k0 < DVS; k0 += P::KS) {
-      typename P::template A<1> fo, fr, fu;
-      P::load_a(fo, mo, wr * 16, k0, lane);
-      P::load_a(fr, mr, wr * 16, k0, lane);
-      P::load_a(fu, mu, wr * 16, k0, lane);
+    for (int k0 = 0; k0 < DVS; k0 += F::KS) {
+      F::A fo, fr, fu;
+      F::load_a(fo, mo, wr * 16, k0, lane);
+      F::load_a(fr, mr, wr * 16, k0, lane);
+      F::load_a(fu, mu, wr * 16, k0, lane);
 #pragma unroll
       for (int j = 0; j < NT / 2; ++j) {
-        typename P::template B<1> bs, bd;
-        P::load_bn(bs, ms, wc * (DK / 2) + j * 16, k0, lane);
-        P::load_bn(bd, md, wc * (DK / 2) + j * 16, k0, lane);
+        F::B bs, bd;
+        F::load_bn(bs, ms, wc * (DK / 2) + j * 16, k0, lane);
+        F::load_bn(bd, md, wc * (DK / 2) + j * 16, k0, lane);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          P::mma(aq[2 * j + hf], fo, bs, hf);
-          P::mma(ax[2 * j + hf], fr, bs, hf);
-          P::mma(au[2 * j + hf], fu, bd, hf);
+          F::mma(aq[2 * j + hf], fo, bs, hf);
+          F::mma(ax[2 * j + hf], fr, bs, hf);
+          F::mma(au[2 * j + hf], fu, bd, hf);
         }
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (wc * 32 + j * 16 > wr * 16) continue;        // above the diagonal
-        typename P::template B<1> bu;
-        P::load_bn(bu, mu, wc * 32 + j * 16, k0, lane);
+        F::B bu;
+        F::load_bn(bu, mu, wc * 32 + j * 16, k0, lane);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          P::mma(ap[2 * j + hf], fo, bu, hf);
-          P::mma(aa[2 * j + hf], fr, bu, hf);
+          F::mma(ap[2 * j + hf], fo, bu, hf);
+          F::mma(aa[2 * j + hf], fr, bu, hf);
         }
       }
     }
@@ -372,18 +315,16 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       const int i = tid & 63, part = tid >> 6;
 #pragma unroll
       for (int e = 0; e < DVS / 4; ++e)
-        drv = fmaf(to_f(sm.dr[st][i * S::LDV + part * (DVS / 4) + e]),
-                   to_f(sm.v[st][i * S::LDV + part * (DVS / 4) + e]), drv);
+        drv = fmaf(sm.dr[i * S::LDV + part * (DVS / 4) + e],
+                   sm.v[i * S::LDV + part * (DVS / 4) + e], drv);
       for (int e = tid; e < DVS * DK / 2; e += 256) {
         const int r = e / (DVS / 2), cc = (e % (DVS / 2)) * 2;
-        const float2 x0 = P::get2(sm.s0[st] + r * S::LDV + cc), x1 = P::get2(sm.ds[st] + r * S::LDV + cc);
+        const float2 x0 = *reinterpret_cast<const float2*>(sm.s0 + r * S::LDV + cc), x1 = *reinterpret_cast<const float2*>(sm.ds + r * S::LDV + cc);
         ss = fmaf(x0.x, x1.x, fmaf(x0.y, x1.y, ss));
       }
     }
-    if (ST == 1) {
-      __syncthreads();
-      if (x + 1 < ns) fetch(x + 1, 0);
-    }
+    __syncthreads();
+    if (x + 1 < ns) fetch(x + 1);
   }
 
   const float* vec = sm.vec;
@@ -399,14 +340,14 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       for (int cc = 0; cc < 2; ++cc) {
         const float2 gi = reinterpret_cast<const float2*>(vec + kVecG2)[i],
                      gj = reinterpret_cast<const float2*>(vec + kVecG2)[col + cc];
-        const float l = P::exp2((gi.x - gj.x) + (gi.y - gj.y));
+        const float l = exp2f((gi.x - gj.x) + (gi.y - gj.y));
         dp[cc] = col + cc <= i ? a.s.scale * l * ap[j][2 * rr + cc] : 0.f;
         da[cc] = col + cc < i ? -l * aa[j][2 * rr + cc] : 0.f;
       }
       const float be = vec[kVecBeta + i];
-      P::template put2<S::PL>(Mat<E>{sm.dp, S::LDT, kC * S::LDT}, i, col, dp[0], dp[1]);
-      P::template put2<S::PL>(Mat<E>{sm.da, S::LDT, kC * S::LDT}, i, col, da[0], da[1]);
-      P::template put2<S::PL>(Mat<E>{sm.dm, S::LDT, kC * S::LDT}, i, col, be * da[0], be * da[1]);
+      F::put2(Mat<float>{sm.dp, kLdT}, i, col, dp[0], dp[1]);
+      F::put2(Mat<float>{sm.da, kLdT}, i, col, da[0], da[1]);
+      F::put2(Mat<float>{sm.dm, kLdT}, i, col, be * da[0], be * da[1]);
     }
   float dus[2] = {0.f, 0.f};
 #pragma unroll
@@ -415,7 +356,7 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
     const float eg = vec[kVecEG + i], el = vec[kVecEGL + i];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const float2 kk = P::get2(sm.k + i * S::LDK + wc * (DK / 2) + j * 8 + t2);
+      const float2 kk = *reinterpret_cast<const float2*>(sm.k + i * S::LDK + wc * (DK / 2) + j * 8 + t2);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         aq[j][2 * rr + cc] *= a.s.scale * eg;
@@ -427,38 +368,38 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
   }
   __syncthreads();
   {
-    const Mat<E> mk{sm.k, S::LDK, 0}, mq{sm.q, S::LDK, 0}, mp{sm.dp, S::LDT, kC * S::LDT},
-        ma{sm.da, S::LDT, kC * S::LDT}, mm{sm.dm, S::LDT, kC * S::LDT};
+    const Mat<float> mk{sm.k, S::LDK}, mq{sm.q, S::LDK}, mp{sm.dp, kLdT},
+        ma{sm.da, kLdT}, mm{sm.dm, kLdT};
 #pragma unroll
-    for (int k0 = 0; k0 < kC; k0 += P::KS) {
+    for (int k0 = 0; k0 < kC; k0 += F::KS) {
       if (k0 < wr * 16 + 16) {
-        typename P::template A<S::PL> fp, fa;
-        P::load_a(fp, mp, wr * 16, k0, lane);
-        P::load_a(fa, ma, wr * 16, k0, lane);
+        F::A fp, fa;
+        F::load_a(fp, mp, wr * 16, k0, lane);
+        F::load_a(fa, ma, wr * 16, k0, lane);
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
-          typename P::template B<1> bk;
-          P::load_bk(bk, mk, wc * (DK / 2) + j * 16, k0, lane);
+          F::B bk;
+          F::load_bk(bk, mk, wc * (DK / 2) + j * 16, k0, lane);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            P::mma(aq[2 * j + hf], fp, bk, hf);
-            P::mma(ax[2 * j + hf], fa, bk, hf);
+            F::mma(aq[2 * j + hf], fp, bk, hf);
+            F::mma(ax[2 * j + hf], fa, bk, hf);
           }
         }
       }
-      if (k0 + P::KS > wr * 16) {
-        typename P::template A<S::PL> fp, fm;
-        P::load_at(fp, mp, wr * 16, k0, lane);
-        P::load_at(fm, mm, wr * 16, k0, lane);
+      if (k0 + F::KS > wr * 16) {
+        F::A fp, fm;
+        F::load_at(fp, mp, wr * 16, k0, lane);
+        F::load_at(fm, mm, wr * 16, k0, lane);
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
-          typename P::template B<1> bq, bk;
-          P::load_bk(bq, mq, wc * (DK / 2) + j * 16, k0, lane);
-          P::load_bk(bk, mk, wc * (DK / 2) + j * 16, k0, lane);
+          F::B bq, bk;
+          F::load_bk(bq, mq, wc * (DK / 2) + j * 16, k0, lane);
+          F::load_bk(bk, mk, wc * (DK / 2) + j * 16, k0, lane);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            P::mma(au[2 * j + hf], fp, bq, hf);
-            P::mma(au[2 * j + hf], fm, bk, hf);
+            F::mma(au[2 * j + hf], fp, bq, hf);
+            F::mma(au[2 * j + hf], fm, bk, hf);
           }
         }
       }
@@ -473,7 +414,7 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int col = wc * (DK / 2) + j * 8 + t2;
-      const float2 kk = P::get2(sm.k + i * S::LDK + col), qq = P::get2(sm.q + i * S::LDK + col);
+      const float2 kk = *reinterpret_cast<const float2*>(sm.k + i * S::LDK + col), qq = *reinterpret_cast<const float2*>(sm.q + i * S::LDK + col);
       const float q0 = aq[j][2 * rr], q1 = aq[j][2 * rr + 1], e0 = ax[j][2 * rr], e1 = ax[j][2 * rr + 1];
       const float k0 = fmaf(be, e0, au[j][2 * rr]), k1 = fmaf(be, e1, au[j][2 * rr + 1]);
       dq_ = fmaf(qq.x, q0, fmaf(qq.y, q1, dq_));
@@ -486,8 +427,8 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
           *reinterpret_cast<float2*>(a.pdk + at) = make_float2(k0, k1);
         } else {
           const long long at = ((row0 + i) * a.s.hk + h) * dk + col;
-          P::template put2<1>(Mat<E>{static_cast<E*>(a.gq) + at, 0, 0}, 0, 0, q0, q1);
-          P::template put2<1>(Mat<E>{static_cast<E*>(a.gk) + at, 0, 0}, 0, 0, k0, k1);
+          *reinterpret_cast<float2*>(static_cast<float*>(a.gq) + at) = make_float2(q0, q1);
+          *reinterpret_cast<float2*>(static_cast<float*>(a.gk) + at) = make_float2(k0, k1);
         }
       }
     }
@@ -510,7 +451,7 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
     const float z = sm.dot[2][0][i] + sm.dot[2][1][i];
     const float db = ((sm.drv[0][i] + sm.drv[1][i]) + (sm.drv[2][i] + sm.drv[3][i])) + z;
     sm.dg[i] = (sm.dot[0][0][i] + sm.dot[0][1][i]) - (sm.dot[1][0][i] + sm.dot[1][1][i]) + 2.f * be * z;
-    if (i < rows) put(static_cast<E*>(a.gbeta) + (row0 + i) * a.s.hv + h, db);
+    if (i < rows) static_cast<float*>(a.gbeta)[(row0 + i) * a.s.hv + h] = db;
   }
   __syncthreads();
   if (warp == 0) {
@@ -529,75 +470,64 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
       const float y = __shfl_down_sync(0xffffffffu, run, d);
       run += lane + d < 32 ? y : 0.f;
     }
-    const float d0 = run + last, d1 = run - x0 + last;
-    if (2 * lane < rows) put(static_cast<E*>(a.gg) + (row0 + 2 * lane) * a.s.hv + h, d0);
-    if (2 * lane + 1 < rows) put(static_cast<E*>(a.gg) + (row0 + 2 * lane + 1) * a.s.hv + h, d1);
+    const uint2 dead = *reinterpret_cast<const uint2*>(vec + kVecDead);
+    const float d0 = alive(run + last, dead.x, lane), d1 = alive(run - x0 + last, dead.y, lane);
+    if (2 * lane < rows) static_cast<float*>(a.gg)[(row0 + 2 * lane) * a.s.hv + h] = d0;
+    if (2 * lane + 1 < rows) static_cast<float*>(a.gg)[(row0 + 2 * lane + 1) * a.s.hv + h] = d1;
   }
 }
 
 // dq, dk of a key head: its value heads' parts, first to last.
-template <class E>
-__global__ void k_gdr_heads(const float* pdq, const float* pdk, E* gq, E* gk, long long rows, int hk, int group, int dk) {
-  const long long total = rows * hk * (dk / 2);
+__global__ void k_gdr_heads(const float2* pdq, const float2* pdk, float2* gq, float2* gk, long long rows, int hk,
+                            int group, int half) {
+  const long long total = rows * hk * half;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
-    const long long rh = i / (dk / 2);
-    const int c = (int)(i % (dk / 2)) * 2;
+    const long long rh = i / half;
+    const int c = (int)(i % half);
     float2 x = make_float2(0.f, 0.f), y = x;
     for (int j = 0; j < group; ++j) {
-      const long long at = (rh * group + j) * dk + c;
-      const float2 u = *reinterpret_cast<const float2*>(pdq + at), w = *reinterpret_cast<const float2*>(pdk + at);
+      const float2 u = pdq[(rh * group + j) * half + c], w = pdk[(rh * group + j) * half + c];
       x.x += u.x; x.y += u.y;
       y.x += w.x; y.y += w.y;
     }
-    put(gq + rh * dk + c, x.x);
-    put(gq + rh * dk + c + 1, x.y);
-    put(gk + rh * dk + c, y.x);
-    put(gk + rh * dk + c + 1, y.y);
+    gq[i] = x;
+    gk[i] = y;
   }
 }
 
-template <class P, int DK, int MT, int WM>
-static cudaError_t launch_scan_bwd(BwdArgs a, cudaStream_t st) {
-  using C = BwdCfg<P, DK, MT, WM>;
-  static_assert(C::FITS, "shared memory");
+template <int DK, int WM>
+static cudaError_t scan_bwd(BwdArgs a, cudaStream_t st) {
+  using C = BwdCfg<DK, WM>;
   a.ntile = (a.s.dv + C::DVT - 1) / C::DVT;
-  const long long blocks = (long long)a.s.n_seq * a.s.hv * a.ntile;
   cudaError_t e =
-      cudaFuncSetAttribute(k_gdr_scan_bwd<P, DK, MT, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+      cudaFuncSetAttribute(k_gdr_scan_bwd<DK, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_bwd", st);
-  k_gdr_scan_bwd<P, DK, MT, WM><<<(unsigned)blocks, C::THREADS, C::BYTES, st>>>(a);
+  k_gdr_scan_bwd<DK, WM><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
-template <class P, int DK>
-static cudaError_t backward(const BwdArgs& a, cudaStream_t st) {
-  using E = typename P::E;
-  cudaError_t e;
-  if constexpr (P::kMode == CFC_MATH_BF16) {
-    e = launch_scan_bwd_tc(a, DK, st);
-    return e != cudaSuccess || a.s.rows == 0 ? e : launch_grad_tc(a, DK, st);
-  } else {
-    const long long heads = (long long)a.s.n_seq * a.s.hv;
-    if (a.s.dv > 16 && heads * ((a.s.dv + 31) / 32) >= 114) e = launch_scan_bwd<P, DK, 1, 2>(a, st);
-    else e = launch_scan_bwd<P, DK, 1, 1>(a, st);
-  }
+template <int DK>
+static cudaError_t backward_fp32(const BwdArgs& a, cudaStream_t st) {
+  const bool wide = a.s.dv > 16 && (long long)a.s.n_seq * a.s.hv * ((a.s.dv + 31) / 32) >= kFillSMs;
+  cudaError_t e = wide ? scan_bwd<DK, 2>(a, st) : scan_bwd<DK, 1>(a, st);
   if (e != cudaSuccess || a.s.rows == 0) return e;
-  const size_t bytes = sizeof(GradSmem<P, DK>);
-  static_assert(sizeof(GradSmem<P, DK>) <= 227u * 1024u, "shared memory");
-  e = cudaFuncSetAttribute(k_gdr_grad<P, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  constexpr size_t bytes = sizeof(GradSmem<DK>);
+  static_assert(bytes <= 227u * 1024u, "shared memory");
+  e = cudaFuncSetAttribute(k_gdr_grad<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   {
     TraceScope tr("k_gdr_grad", st);
-    k_gdr_grad<P, DK><<<(unsigned)(slot_count(a.s.rows, a.s.n_seq) * a.s.hv), 256, bytes, st>>>(a);
+    k_gdr_grad<DK><<<(unsigned)(slot_count(a.s.rows, a.s.n_seq) * a.s.hv), 256, bytes, st>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess || !a.pdq) return e;
   TraceScope tr("k_gdr_heads", st);
   const long long work = (a.s.rows * a.s.hk * (a.s.dk / 2) + 255) / 256;
-  k_gdr_heads<E><<<(unsigned)(work < 16 * kNumSMs ? work : 16 * kNumSMs), 256, 0, st>>>(
-      a.pdq, a.pdk, static_cast<E*>(a.gq), static_cast<E*>(a.gk), a.s.rows, a.s.hk, a.s.hv / a.s.hk, a.s.dk);
+  k_gdr_heads<<<(unsigned)(work < 16 * kNumSMs ? work : 16 * kNumSMs), 256, 0, st>>>(
+      reinterpret_cast<const float2*>(a.pdq), reinterpret_cast<const float2*>(a.pdk), static_cast<float2*>(a.gq),
+      static_cast<float2*>(a.gk), a.s.rows, a.s.hk, a.s.hv / a.s.hk, a.s.dk / 2);
   return cudaGetLastError();
 }
 
@@ -621,8 +551,10 @@ cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_
     a.pdq = reinterpret_cast<float*>(g.ws + w.off_dq);
     a.pdk = reinterpret_cast<float*>(g.ws + w.off_dk);
   }
-  if (g.math == CFC_MATH_BF16) return g.dk <= 64 ? backward<MBf16, 64>(a, st) : backward<MBf16, 128>(a, st);
-  return g.dk <= 64 ? backward<MFp32, 64>(a, st) : backward<MFp32, 128>(a, st);
+  const int tile = g.dk <= 64 ? 64 : 128;
+  if (g.math == CFC_MATH_FP32) return tile == 64 ? backward_fp32<64>(a, st) : backward_fp32<128>(a, st);
+  const cudaError_t e = launch_scan_bwd_tc(a, tile, st);
+  return e != cudaSuccess || g.rows == 0 ? e : launch_grad_tc(a, tile, st);
 }
 
 }  // namespace cfc

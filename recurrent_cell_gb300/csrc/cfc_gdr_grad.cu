@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
       const float* vec = reinterpret_cast<const float*>(stage + (it & 1) * C::STAGE + C::OFF_VEC);
       const float eg = vec[kVecEG + i], el = vec[kVecEGL + i], be = vec[kVecBeta + i], dec = vec[kVecD];
       const float2 be2 = *reinterpret_cast<const float2*>(vec + kVecBeta + 2 * lane);
+      const uint2 dead = *reinterpret_cast<const uint2*>(vec + kVecDead);
       if (tid < 128) gs[tid] = vec[kVecG2 + tid];
       float ss = 0.f, dr = 0.f;            // <S0, dS1> and dR.v, while the products run
       for (int t = 0; t < nt; ++t, ++it) {
@@ -346,8 +347,8 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
             for (int e = 0; e < 8; e += 2) {
               const int col = cg * 32 + j + z + e;
               const float4 gj = *reinterpret_cast<const float4*>(gs + 2 * col);
-              const float w0 = f * x[z + e] * MBf16::exp2((gi.x - gj.x) + (gi.y - gj.y));
-              const float w1 = f * x[z + e + 1] * MBf16::exp2((gi.x - gj.z) + (gi.y - gj.w));
+              const float w0 = f * x[z + e] * exp2_approx((gi.x - gj.x) + (gi.y - gj.y));
+              const float w1 = f * x[z + e + 1] * exp2_approx((gi.x - gj.z) + (gi.y - gj.w));
               w[e] = col < end ? w0 : 0.f;
               w[e + 1] = col + 1 < end ? w1 : 0.f;
             }
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
           const float y = __shfl_down_sync(0xffffffffu, run, d);
           run += lane + d < 32 ? y : 0.f;
         }
-        const float g0 = run + last, g1 = run - dg[0] + last;
+        const float g0 = alive(run + last, dead.x, lane), g1 = alive(run - dg[0] + last, dead.y, lane);
         if (2 * lane < ck.rows) a.gg[(ck.row0 + 2 * lane) * a.s.hv + h] = __float2bfloat16_rn(g0);
         if (2 * lane + 1 < ck.rows) a.gg[(ck.row0 + 2 * lane + 1) * a.s.hv + h] = __float2bfloat16_rn(g1);
       }

@@ -28,6 +28,11 @@ struct StepArgs {
 
 constexpr int kStepThreads = 256;
 
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 // RPT rows of the state a thread: rows rg, rg + RG, ... of RG row groups.
 template <class E, int TDV, int RPT>
 __global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {

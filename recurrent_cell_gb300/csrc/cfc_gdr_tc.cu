@@ -90,18 +90,18 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   __syncthreads();
 
   // Rows 16 warp .. of q k^T and k k^T, columns up to the diagonal block.
-  const Mat<bf16> mk{ks, S::LDK, 0}, mq{qs, S::LDK, 0};
+  const Mat<bf16> mk{ks, S::LDK}, mq{qs, S::LDK};
   const int m0 = warp * 16, g = lane >> 2, t2 = (lane & 3) * 2;
   float pr[8][4] = {}, ak[8][4] = {};
 #pragma unroll 2
   for (int k0 = 0; k0 < DK; k0 += 16) {
-    P::A<1> fq, fk;
+    P::A fq, fk;
     P::load_a(fq, mq, m0, k0, lane);
     P::load_a(fk, mk, m0, k0, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j > warp) continue;
-      P::B<1> fb;
+      P::B fb;
       P::load_bn(fb, mk, j * 16, k0, lane);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
       }
     }
   }
-  if (warp == 0) chunk_decays(gb, lane, g2, bet, vec);      // the warp with the fewest products
+  if (warp == 0) chunk_decays(gb, lane, c == 0 && !a.init, g2, bet, vec);   // the warp with the fewest products
   __syncthreads();
   // P in the registers, A in shared memory
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
       for (int rr = 0; rr < 2; ++rr) {
         const int i = m0 + g + rr * 8;
         const float2 gi = g2[i];
-        const float l0 = P::exp2((gi.x - gj.x) + (gi.y - gj.y)), l1 = P::exp2((gi.x - gj.z) + (gi.y - gj.w));
+        const float l0 = exp2_approx((gi.x - gj.x) + (gi.y - gj.y)), l1 = exp2_approx((gi.x - gj.z) + (gi.y - gj.w));
         const float be = bet[i];
         av[2 * rr] = col < i ? be * l0 * ak[j][2 * rr] : 0.f;
         av[2 * rr + 1] = col + 1 < i ? be * l1 * ak[j][2 * rr + 1] : 0.f;
@@ -167,23 +167,27 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
 #pragma unroll
   for (int kb = 0; kb < 4; ++kb) {
     if (kb > warp) continue;
-    P::A<2> fa;
+    P::A ah, al;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const float* p = pr[2 * kb + (x >> 1)] + (x & 1) * 2;
-      fa.r[0][x] = pack2(p[0], p[1]);
-      fa.r[1][x] = pack2(p[0] - lo_f(fa.r[0][x]), p[1] - hi_f(fa.r[0][x]));
+      ah[x] = pack2(p[0], p[1]);
+      al[x] = pack2(p[0] - lo_f(ah[x]), p[1] - hi_f(ah[x]));
     }
     const int r = kb * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
     for (int jb = 0; jb < 4; ++jb) {
       if (jb > kb) continue;
-      P::B<2> fb;
+      P::B bh, bl;
       const unsigned char* src = img + chunk_at(r, jb * 2 + (lane >> 4));
-      P::ldmt(fb.r[0], reinterpret_cast<const bf16*>(src));
-      P::ldmt(fb.r[1], reinterpret_cast<const bf16*>(src + 8192));
-      P::mma(d[2 * jb], fa, fb, 0);
-      P::mma(d[2 * jb + 1], fa, fb, 1);
+      P::ldmt(bh, src);
+      P::ldmt(bl, src + 8192);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        P::mma(d[2 * jb + hf], al, bh, hf);
+        P::mma(d[2 * jb + hf], ah, bl, hf);
+        P::mma(d[2 * jb + hf], ah, bh, hf);
+      }
     }
   }
 #pragma unroll
@@ -897,13 +901,13 @@ template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
   if (planes == 2)
-    return t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= 114 ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
-  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114 ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
+    return t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= kFillSMs ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
+  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= kFillSMs ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= 114 ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
+  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= kFillSMs ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {

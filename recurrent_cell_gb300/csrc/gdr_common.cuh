@@ -31,10 +31,16 @@ namespace gdr {
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kMaxDk = 128;     // key width limit: the state's rows stay in one block's registers
 constexpr int kMaxDv = 256;
+constexpr int kPad = 4;         // floats between rows in shared memory: rows of a tile in different banks
+constexpr int kLdT = kC + kPad; // a row of 64 x 64 in FP32: T - I and P in shared memory and workspace, R, U
+// Blocks that count as reaching every SM: three quarters of them.  Wider tiles
+// read the operands that tiles share fewer times, narrower ones run on more SMs.
+constexpr int kFillSMs = kNumSMs * 3 / 4;
 // Per chunk and head: exp(G), exp(G_C - G), beta, G / ln 2 as pairs of floats
-// hi + lo, exp(G_C).
+// hi + lo, exp(G_C), and two words of bits (even rows, odd rows): the tokens that
+// nothing passes, a factor of zero or a sequence's first from the zero state.
 constexpr int kVec = 384;
-constexpr int kVecEG = 0, kVecEGL = 64, kVecBeta = 128, kVecG2 = 192, kVecD = 320;
+constexpr int kVecEG = 0, kVecEGL = 64, kVecBeta = 128, kVecG2 = 192, kVecD = 320, kVecDead = 322;
 
 // Log-decays below this are a zero factor in fp32 all the same
 // (exp(-104) underflows); holding them here keeps -inf out of differences.
@@ -178,134 +184,53 @@ __device__ __forceinline__ void store_tile(E* dst, long long stride, const E* sr
 }
 
 // ------------------------------------------------------------ warp products
-// A matrix in shared memory.  In bf16 an operand made of fp32 values can be
-// held as two planes, x = hi + lo with both in bf16 (17 significant bits): the
-// products hi*hi + lo*hi + hi*lo then keep the serial state at fp32-like
-// accuracy (4e-6 relative measured), where one plane leaves 3e-3.
+// A matrix in shared memory, rows of ld elements.
 template <class E>
 struct Mat {
   E* p;
   int ld;
-  int plane;   // elements from the hi to the lo plane
 };
 
 // Fragments of D[16 x 8] += A[16 x k] B[k x 8]: lane = 4 g + t holds rows g and
 // g + 8, columns 2t and 2t + 1 of D.  load_b* fetches two adjacent 8-column
-// tiles at once.
+// tiles at once; h picks one.
+
+// bf16 operands.
 struct MBf16 {
   using E = __nv_bfloat16;
-  static constexpr int kMode = CFC_MATH_BF16;
-  static constexpr int KS = 16;       // k of one product step
-  static constexpr int PAD = 8;       // 16 bytes: rows of an 8x8 block hit different banks
-  static constexpr int STAGES = 2;
-  __device__ static __forceinline__ float exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-  }
-  template <int PL> struct A { uint32_t r[PL][4]; };
-  template <int PL> struct B { uint32_t r[PL][4]; };
-
-  __device__ static __forceinline__ void ldm(uint32_t (&r)[4], const E* p) {
+  using A = uint32_t[4];
+  using B = uint32_t[4];
+  __device__ static __forceinline__ void ldm(uint32_t (&r)[4], const void* p) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
   }
-  __device__ static __forceinline__ void ldmt(uint32_t (&r)[4], const E* p) {
+  __device__ static __forceinline__ void ldmt(uint32_t (&r)[4], const void* p) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem_addr(p)) : "memory");
   }
   // A[m][k], k contiguous
-  template <int PL>
-  __device__ static __forceinline__ void load_a(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
-    const E* p = m.p + (m0 + (lane & 15)) * m.ld + k0 + (lane >> 4) * 8;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) ldm(a.r[i], p + i * m.plane);
-  }
-  // A[m][k] stored [k][m]
-  template <int PL>
-  __device__ static __forceinline__ void load_at(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
-    const E* p = m.p + (k0 + (lane & 7) + (lane >> 4) * 8) * m.ld + m0 + ((lane >> 3) & 1) * 8;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) ldmt(a.r[i], p + i * m.plane);
+  __device__ static __forceinline__ void load_a(A& a, const Mat<E>& m, int m0, int k0, int lane) {
+    ldm(a, m.p + (m0 + (lane & 15)) * m.ld + k0 + (lane >> 4) * 8);
   }
   // B[k][n] stored [n][k], n0 .. n0 + 15
-  template <int PL>
-  __device__ static __forceinline__ void load_bn(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
-    const E* p = m.p + (n0 + (lane & 7) + (lane >> 4) * 8) * m.ld + k0 + ((lane >> 3) & 1) * 8;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) ldm(b.r[i], p + i * m.plane);
+  __device__ static __forceinline__ void load_bn(B& b, const Mat<E>& m, int n0, int k0, int lane) {
+    ldm(b, m.p + (n0 + (lane & 7) + (lane >> 4) * 8) * m.ld + k0 + ((lane >> 3) & 1) * 8);
   }
-  // B[k][n] stored [k][n]
-  template <int PL>
-  __device__ static __forceinline__ void load_bk(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
-    const E* p = m.p + (k0 + (lane & 7) + ((lane >> 3) & 1) * 8) * m.ld + n0 + (lane >> 4) * 8;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) ldmt(b.r[i], p + i * m.plane);
-  }
-  __device__ static __forceinline__ void mma1(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  __device__ static __forceinline__ void mma(float (&d)[4], const A& a, const B& b, int h) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-  // the same, the small products into a sum of their own: shorter chains
-  static constexpr bool two_sums(int PA, int PB) { return PA + PB > 2; }
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma(float (&d)[4], float (&lo)[4], const A<PA>& a, const B<PB>& b, int h) {
-    if constexpr (PA == 2) mma1(lo, a.r[1], b.r[0][2 * h], b.r[0][2 * h + 1]);
-    if constexpr (PB == 2) mma1(lo, a.r[0], b.r[1][2 * h], b.r[1][2 * h + 1]);
-    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
-  }
-  // with the hi plane of A alone
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma_hi(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
-    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
-  }
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
-    if constexpr (PA == 2) mma1(d, a.r[1], b.r[0][2 * h], b.r[0][2 * h + 1]);
-    if constexpr (PB == 2) mma1(d, a.r[0], b.r[1][2 * h], b.r[1][2 * h + 1]);
-    mma1(d, a.r[0], b.r[0][2 * h], b.r[0][2 * h + 1]);
-  }
-  // two adjacent values of a row
-  template <int PL>
-  __device__ static __forceinline__ void put2(const Mat<E>& m, int row, int col, float v0, float v1) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-    *reinterpret_cast<__nv_bfloat162*>(m.p + row * m.ld + col) = h;
-    if constexpr (PL == 2)
-      *reinterpret_cast<__nv_bfloat162*>(m.p + m.plane + row * m.ld + col) =
-          __floats2bfloat162_rn(v0 - __bfloat162float(h.x), v1 - __bfloat162float(h.y));
-  }
-  template <int PL>
-  __device__ static __forceinline__ void put4(const Mat<E>& m, int row, int col, const float4& v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    E* p = m.p + row * m.ld + col;
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    if constexpr (PL == 2) {
-      const __nv_bfloat162 c = __floats2bfloat162_rn(v.x - __bfloat162float(a.x), v.y - __bfloat162float(a.y)),
-                           d = __floats2bfloat162_rn(v.z - __bfloat162float(b.x), v.w - __bfloat162float(b.y));
-      *reinterpret_cast<uint2*>(p + m.plane) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
-    }
-  }
-  __device__ static __forceinline__ float2 get2(const E* p) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[2 * h]), "r"(b[2 * h + 1]));
   }
 };
 
-// FP32: operands stay fp32 in shared memory and are split in registers into
-// two TF32 values (22 significant bits); three TF32 products per step.
+// fp32 operands, split in registers into two TF32 values (22 significant
+// bits); three TF32 products a step, the small ones into a sum of their own
+// where a chain would otherwise be long.
 struct MFp32 {
-  using E = float;
-  static constexpr int kMode = CFC_MATH_FP32;
-  static constexpr int KS = 8;
-  static constexpr int PAD = 4;
-  static constexpr int STAGES = 1;
-  __device__ static __forceinline__ float exp2(float x) { return exp2f(x); }
-  template <int PL> struct A { uint32_t h[4], l[4]; };
-  template <int PL> struct B { uint32_t h[4], l[4]; };
-
+  static constexpr int KS = 8;        // k of one step
+  struct A { uint32_t h[4], l[4]; };
+  struct B { uint32_t h[4], l[4]; };
   __device__ static __forceinline__ uint32_t tf32(float x) {
     uint32_t r;
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
@@ -315,33 +240,33 @@ struct MFp32 {
     h = tf32(x);
     l = tf32(x - __uint_as_float(h));
   }
-  template <int PL>
-  __device__ static __forceinline__ void load_a(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
-    const E* p = m.p + (m0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
+  // A[m][k], k contiguous
+  __device__ static __forceinline__ void load_a(A& a, const Mat<float>& m, int m0, int k0, int lane) {
+    const float* p = m.p + (m0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
     split(a.h[0], a.l[0], p[0]);
     split(a.h[1], a.l[1], p[8 * m.ld]);
     split(a.h[2], a.l[2], p[4]);
     split(a.h[3], a.l[3], p[8 * m.ld + 4]);
   }
-  template <int PL>
-  __device__ static __forceinline__ void load_at(A<PL>& a, const Mat<E>& m, int m0, int k0, int lane) {
-    const E* p = m.p + (k0 + (lane & 3)) * m.ld + m0 + (lane >> 2);
+  // A[m][k] stored [k][m]
+  __device__ static __forceinline__ void load_at(A& a, const Mat<float>& m, int m0, int k0, int lane) {
+    const float* p = m.p + (k0 + (lane & 3)) * m.ld + m0 + (lane >> 2);
     split(a.h[0], a.l[0], p[0]);
     split(a.h[1], a.l[1], p[8]);
     split(a.h[2], a.l[2], p[4 * m.ld]);
     split(a.h[3], a.l[3], p[4 * m.ld + 8]);
   }
-  template <int PL>
-  __device__ static __forceinline__ void load_bn(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
-    const E* p = m.p + (n0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
+  // B[k][n] stored [n][k], n0 .. n0 + 15
+  __device__ static __forceinline__ void load_bn(B& b, const Mat<float>& m, int n0, int k0, int lane) {
+    const float* p = m.p + (n0 + (lane >> 2)) * m.ld + k0 + (lane & 3);
     split(b.h[0], b.l[0], p[0]);
     split(b.h[1], b.l[1], p[4]);
     split(b.h[2], b.l[2], p[8 * m.ld]);
     split(b.h[3], b.l[3], p[8 * m.ld + 4]);
   }
-  template <int PL>
-  __device__ static __forceinline__ void load_bk(B<PL>& b, const Mat<E>& m, int n0, int k0, int lane) {
-    const E* p = m.p + (k0 + (lane & 3)) * m.ld + n0 + (lane >> 2);
+  // B[k][n] stored [k][n]
+  __device__ static __forceinline__ void load_bk(B& b, const Mat<float>& m, int n0, int k0, int lane) {
+    const float* p = m.p + (k0 + (lane & 3)) * m.ld + n0 + (lane >> 2);
     split(b.h[0], b.l[0], p[0]);
     split(b.h[1], b.l[1], p[4 * m.ld]);
     split(b.h[2], b.l[2], p[8]);
@@ -353,50 +278,37 @@ struct MFp32 {
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
-  static constexpr bool two_sums(int, int) { return true; }
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma(float (&d)[4], float (&lo)[4], const A<PA>& a, const B<PB>& b, int h) {
+  __device__ static __forceinline__ void mma(float (&d)[4], float (&lo)[4], const A& a, const B& b, int h) {
     mma1(lo, a.l, b.h[2 * h], b.h[2 * h + 1]);
     mma1(lo, a.h, b.l[2 * h], b.l[2 * h + 1]);
     mma1(d, a.h, b.h[2 * h], b.h[2 * h + 1]);
   }
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma_hi(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
-    mma(d, a, b, h);
-  }
-  template <int PA, int PB>
-  __device__ static __forceinline__ void mma(float (&d)[4], const A<PA>& a, const B<PB>& b, int h) {
-    mma1(d, a.l, b.h[2 * h], b.h[2 * h + 1]);
-    mma1(d, a.h, b.l[2 * h], b.l[2 * h + 1]);
-    mma1(d, a.h, b.h[2 * h], b.h[2 * h + 1]);
-  }
-  template <int PL>
-  __device__ static __forceinline__ void put2(const Mat<E>& m, int row, int col, float v0, float v1) {
+  __device__ static __forceinline__ void mma(float (&d)[4], const A& a, const B& b, int h) { mma(d, d, a, b, h); }
+  // two adjacent values of a row
+  __device__ static __forceinline__ void put2(const Mat<float>& m, int row, int col, float v0, float v1) {
     *reinterpret_cast<float2*>(m.p + row * m.ld + col) = make_float2(v0, v1);
   }
-  template <int PL>
-  __device__ static __forceinline__ void put4(const Mat<E>& m, int row, int col, const float4& v) {
-    *reinterpret_cast<float4*>(m.p + row * m.ld + col) = v;
-  }
-  __device__ static __forceinline__ float2 get2(const E* p) { return *reinterpret_cast<const float2*>(p); }
 };
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+using F = MFp32;                // the FP32 kernels' products
+
+// 2^x to within 2 ulp, far below bf16's rounding.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ------------------------------------------------------------ workspace
-// Per (slot, value head): T - I and P (bf16: two planes each), rows padded as they lie
-// in shared memory, so that each is one bulk copy; the vectors; when the backward
-// is to follow also the state before the chunk (S0^T [d_v, d_k], in the
-// operand type the products read it in) and U^T [d_v, 64]; and the backward's
-// own dS1^T, dR^T, and per-value-head dq, dk where heads are shared.
+// Per (slot, value head).  FP32: T - I and P in rows of kLdT floats.  bf16: both as
+// one image of the tensor cores' operand tiles, copied whole.  In both modes the
+// vectors; when the backward is to follow also the state before the chunk and U;
+// and the backward's own dS1 and dR, with dq and dk per value head where heads are
+// shared.  (bf16: all of these as operand tiles too; FP32: plain rows.)
 struct Workspace {
   size_t off_t, off_p, off_vec, off_order, off_s0, off_u, off_ds, off_dr, off_dq, off_dk, total;
 };
-template <class P> constexpr int kLdt = kC + P::PAD;                                  // row of T - I, P
-template <class P> constexpr int kTPlanes = P::kMode == CFC_MATH_BF16 ? 2 : 1;
+
 Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);
 
 // Packed batches of up to this many sequences run longest first.
@@ -424,9 +336,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(h, e - (h - s));
 }
 
-// The decays of a chunk's head, by one warp whose lanes hold g (gb.x, gb.y) and
-// beta (gb.z, gb.w) of rows 2 lane and 2 lane + 1: into `vec`, and for the
-// block G / ln 2 as pairs hi + lo and beta.
+// dg of a row, zero where its bit says so (a NaN stays).
+__device__ __forceinline__ float alive(float dg, unsigned dead, int lane) { return (dead >> lane) & 1 ? 0.f * dg : dg; }
+
+// g and beta of rows 2 lane and 2 lane + 1: (x, y) and (z, w).
 __device__ __forceinline__ float4 load_gates(const FwdArgs& a, long long row0, int rows, int h, int lane) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   const long long at = (row0 + 2 * lane) * a.s.hv + h;
@@ -434,7 +347,14 @@ __device__ __forceinline__ float4 load_gates(const FwdArgs& a, long long row0, i
   if (2 * lane + 1 < rows) { v.y = a.g[at + a.s.hv]; v.w = a.beta[at + a.s.hv]; }
   return v;
 }
-__device__ __forceinline__ void chunk_decays(const float4& gb, int lane, float2* g2, float* bet, float* vec) {
+// The decays of a chunk's head, by one warp with load_gates' values: into
+// `vec`, and for the block G / ln 2 as pairs hi + lo and beta.
+__device__ __forceinline__ void chunk_decays(const float4& gb, int lane, bool from_zero, float2* g2, float* bet,
+                                             float* vec) {
+  // dg is zero there; the sums it is a difference of would leave their rounding.
+  const unsigned even = __ballot_sync(0xffffffffu, gb.x < kMinG || (from_zero && lane == 0));
+  const unsigned odd = __ballot_sync(0xffffffffu, gb.y < kMinG);
+  if (lane == 0) *reinterpret_cast<uint2*>(vec + kVecDead) = make_uint2(even, odd);
   // Running sum of g as a pair of floats hi + lo: differences of G then carry
   // no more than their own fp32 rounding, however far the sum has gone.  (In
   // double this was the longest part of the kernel: the fp64 rate is 1/64.)
@@ -502,11 +422,11 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
       float d[2][4] = {}, e[2][4] = {};
       const float* fa = pass == 0 ? t21 : t21 + 16;
       const float* fb = pass == 0 ? t21 - 16 * LDA : t21;
-      const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
+      const Mat<float> ma{const_cast<float*>(fa), LDA}, mb{const_cast<float*>(fb), LDA};
 #pragma unroll
       for (int k0 = 0; k0 < 16; k0 += 8) {
-        MFp32::A<1> xa;
-        MFp32::B<1> xb;
+        MFp32::A xa;
+        MFp32::B xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
         MFp32::mma(d[0], e[0], xa, xb, 0);
@@ -532,11 +452,11 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
       float d[2][4] = {}, e[2][4] = {};
       const float* fa = am + (32 + (warp & 1) * 16) * LDA + (pass == 0 ? 0 : 32);
       const float* fb = pass == 0 ? am + (warp >> 1) * 16 : t21;
-      const Mat<float> ma{const_cast<float*>(fa), LDA, 0}, mb{const_cast<float*>(fb), LDA, 0};
+      const Mat<float> ma{const_cast<float*>(fa), LDA}, mb{const_cast<float*>(fb), LDA};
 #pragma unroll
       for (int k0 = 0; k0 < 32; k0 += 8) {
-        MFp32::A<1> xa;
-        MFp32::B<1> xb;
+        MFp32::A xa;
+        MFp32::B xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
         MFp32::mma(d[0], e[0], xa, xb, 0);
