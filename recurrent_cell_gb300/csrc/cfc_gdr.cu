@@ -446,7 +446,8 @@ cudaError_t launch_gdr_forward(const GdrArgs& g, cudaStream_t st) {
   a.g = g.g; a.beta = g.beta; a.init = g.init; a.final_state = g.final_state; a.o = g.o;
   a.t = g.ws + w.off_t; a.p = g.ws + w.off_p;
   a.vec = reinterpret_cast<float*>(g.ws + w.off_vec);
-  if (g.off && g.math == CFC_MATH_BF16 && g.n_seq <= kMaxOrder) a.order = reinterpret_cast<int*>(g.ws + w.off_order);
+  if (g.off && g.rows > 0 && g.math == CFC_MATH_BF16 && g.n_seq <= kMaxOrder)
+    a.order = reinterpret_cast<int*>(g.ws + w.off_order);
   a.save = g.save;
   if (g.save) { a.s0 = g.ws + w.off_s0; a.u = g.ws + w.off_u; }
   const int tile = g.dk <= 64 ? 64 : 128;

@@ -545,7 +545,7 @@ cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_
   a.t = g.ws + w.off_t; a.p = g.ws + w.off_p; a.s0 = g.ws + w.off_s0; a.u = g.ws + w.off_u;
   a.ds = g.ws + w.off_ds; a.dr = g.ws + w.off_dr;
   a.vec = reinterpret_cast<const float*>(g.ws + w.off_vec);
-  if (g.off && g.math == CFC_MATH_BF16 && g.n_seq <= kMaxOrder)
+  if (g.off && g.rows > 0 && g.math == CFC_MATH_BF16 && g.n_seq <= kMaxOrder)
     a.order = reinterpret_cast<const int*>(g.ws + w.off_order);
   if (g.hv != g.hk && g.math == CFC_MATH_FP32) {
     a.pdq = reinterpret_cast<float*>(g.ws + w.off_dq);

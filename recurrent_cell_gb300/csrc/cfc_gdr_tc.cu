@@ -264,6 +264,12 @@ struct TcArgs {
   int ntile, tma;
 };
 
+// The n-th sequence to run; held to the batch whatever the workspace holds.
+__device__ __forceinline__ int nth(const TcArgs& a, int i) {
+  const int n = a.order ? a.order[i] : i;
+  return (unsigned)n < (unsigned)a.s.n_seq ? n : i;
+}
+
 // The fetching warps' loop.  The chunk before last's output rows (o, or the
 // backward's dv), which lie in the place of its V (dO), go to global memory;
 // then the next chunk's tiles come into that stage: the fetching threads with 16-byte copies (rows past the end and
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1) k_gdr_sc
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % a.ntile;
   const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
-  const int n = a.order ? a.order[at_n] : at_n;
+  const int n = nth(a, at_n);
   const long long sh = (long long)n * a.s.hv + h;
   long long start;
   int len;
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1) k_gdr_scan
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x % a.ntile;
   const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
-  const int n = a.order ? a.order[at_n] : at_n;
+  const int n = nth(a, at_n);
   const long long sh = (long long)n * a.s.hv + h;
   long long start;
   int len;
@@ -858,7 +864,9 @@ static int maps_of(const TcArgs& a, int v_box, Maps* m) {
 template <int DK, int PL, int NB>
 static cudaError_t scan(TcArgs a, cudaStream_t st) {
   using C = TcCfg<DK, PL, NB, false>;
-  a.ntile = (a.s.dv + C::NV - 1) / C::NV;
+  // What the backward reads is kept in tiles of 64 columns: narrower blocks also fill the last one's zeros.
+  constexpr int UP = C::NV < 64 ? 64 : C::NV;
+  a.ntile = a.st ? (a.s.dv + UP - 1) / UP * (UP / C::NV) : (a.s.dv + C::NV - 1) / C::NV;
   cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)C::BYTES);
   if (e != cudaSuccess) return e;
