@@ -244,7 +244,7 @@ def train_recall(steps=300, sequences=128, tokens=9, d=64, hidden=32, dtype=torc
         opt.step()
         losses.append(loss.detach())
         if report and (i + 1) % report == 0:
-            print(f"step {i + 1}: loss {float(loss):.4f} (0.25 without any memory)")
+            print(f"step {i + 1}: loss {float(losses[-1]):.4f} (0.25 without any memory)")
     return model, [float(v) for v in torch.stack(losses).cpu()]
 
 
