@@ -161,13 +161,18 @@ def _ptr(t, name, dtype=None, shape=None, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    try:        # the usual case in few steps: the checks are a good part of a small call
+        if (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape) and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -353,14 +358,17 @@ def cfc_gdr_workspace_bytes(rows, n_seq, n_k_heads, n_v_heads, d_k, d_v, math=MA
 def _rows(t, name, dtype, shape):
     """Pointer and row stride of t [..., heads, width], whose rows may be parts
     of wider ones (dense in heads and width, evenly spaced over the rest)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr(), shape[-2] * shape[-1]
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-2] * shape[-1]
     strides = t.stride()
     packed = len(shape) == 3
     ld = strides[-3] if packed or shape[-3] != 1 else strides[0]
@@ -371,20 +379,27 @@ def _rows(t, name, dtype, shape):
 
 
 def _gdr_inputs(q, k, v, g, beta, packed, math):
-    """Sizes and leading C arguments that the three calls share."""
-    torch = _torch()
-    st, f32 = _storage_dtype(math), torch.float32
-    vs, qs = v.shape, q.shape
+    """What the three calls share: the stored type, the shapes of v, of q and of
+    g, (k_heads, v_heads, d_k, d_v), and the leading C arguments."""
+    st = _storage_dtype(math)
+    vs, ks = v.shape, q.shape
     if len(vs) != (3 if packed else 4):
         raise ValueError("v must be [sequences, tokens, heads, d_v], or [rows, heads, d_v] with seq_offsets")
-    if len(qs) != len(vs):
+    if len(ks) != len(vs):
         raise ValueError("q and v must have the same number of axes")
-    ks = vs[:-2] + qs[-2:]
-    hs = vs[:-1]
+    if packed:
+        rows, hv, dv = vs
+        _, hk, dk = ks
+        ks, hs = (rows, hk, dk), (rows, hv)
+    else:
+        n, tokens, hv, dv = vs
+        _, _, hk, dk = ks
+        ks, hs = (n, tokens, hk, dk), (n, tokens, hv)
     qp, ldq = _rows(q, "q", st, ks)
     kp, ldk = _rows(k, "k", st, ks)
     vp, ldv = _rows(v, "v", st, vs)
-    return st, vs, ks, (qp, ldq, kp, ldk, vp, ldv, _ptr(g, "g", f32, hs), _ptr(beta, "beta", f32, hs))
+    f32 = _torch().float32
+    return st, vs, ks, hs, (hk, hv, dk, dv), (qp, ldq, kp, ldk, vp, ldv, _ptr(g, "g", f32, hs), _ptr(beta, "beta", f32, hs))
 
 
 def _gdr_sequences(vs, seq_offsets):
@@ -402,9 +417,9 @@ def cfc_gdr_forward(q, k, v, g, beta, o, workspace, scale=None, seq_offsets=None
     v_heads]; or [rows, ...] packed, with int32 seq_offsets [sequences + 1] on
     the device.  scale: d_k ** -0.5 if None."""
     f32 = _torch().float32
-    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
+    st, vs, _, _, sizes, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
     off, n, rows = _gdr_sequences(vs, seq_offsets)
-    hk, dk, hv, dv = ks[-2], ks[-1], vs[-2], vs[-1]
+    hk, hv, dk, dv = sizes
     ss = (n, hv, dk, dv)
     status = load_library().cfc_gdr_forward(
         *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
@@ -419,10 +434,10 @@ def cfc_gdr_backward(q, k, v, g, beta, grad_o, grad_q, grad_k, grad_v, grad_g, g
     """Backward of the cfc_gdr_forward(save=True) that filled ``workspace``;
     every gradient is overwritten, all in the type of q."""
     f32 = _torch().float32
-    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
+    st, vs, ks, hs, sizes, args = _gdr_inputs(q, k, v, g, beta, seq_offsets is not None, math)
     off, n, rows = _gdr_sequences(vs, seq_offsets)
-    hk, dk, hv, dv = ks[-2], ks[-1], vs[-2], vs[-1]
-    hs, ss = vs[:-1], (n, hv, dk, dv)
+    hk, hv, dk, dv = sizes
+    ss = (n, hv, dk, dv)
     status = load_library().cfc_gdr_backward(
         *args, off, n, rows, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
         _ptr(grad_o, "grad_o", st, vs), _ptr(grad_final_state, "grad_final_state", f32, ss, optional=True),
@@ -438,14 +453,13 @@ def cfc_gdr_step(q, k, v, g, beta, state, o, slots=None, scale=None, math=MATH_B
     [sequences, tokens, ...]): sequence i's state is ``state[slots[i]]``
     (int32 on the device; ``state[i]`` if None), updated in place."""
     torch = _torch()
-    st, vs, ks, args = _gdr_inputs(q, k, v, g, beta, False, math)
-    n, tokens, hv, dv = vs
-    hk, dk = ks[2], ks[3]
-    pool = state.shape
-    if len(pool) != 4 or pool[1:] != (hv, dk, dv):
-        raise ValueError(f"state must have shape (slots, {hv}, {dk}, {dv}), got {tuple(pool)}")
+    st, vs, _, _, sizes, args = _gdr_inputs(q, k, v, g, beta, False, math)
+    n, tokens = vs[0], vs[1]
+    dk, pool = sizes[2], state.shape
+    if len(pool) != 4 or pool != (pool[0], sizes[1], dk, sizes[3]):
+        raise ValueError(f"state must have shape (slots, {sizes[1]}, {dk}, {sizes[3]}), got {tuple(pool)}")
     status = load_library().cfc_gdr_step(
-        *args, n, tokens, hk, hv, dk, dv, dk ** -0.5 if scale is None else scale, math,
+        *args, n, tokens, *sizes, dk ** -0.5 if scale is None else scale, math,
         _ptr(state, "state", torch.float32), pool[0], _ptr(slots, "slots", torch.int32, (n,), optional=True),
         _ptr(o, "o", st, vs), _stream(stream))
     _check("cfc_gdr_step", status)
