@@ -27,6 +27,7 @@ struct StepArgs {
 };
 
 constexpr int kStepThreads = 256;
+constexpr int kAhead = 4;      // tokens whose rows are fetched together
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -39,7 +40,8 @@ __global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
   constexpr int AC = TDV / 4;                   // threads across the columns
   constexpr int RG = kStepThreads / AC;
   constexpr int WARPS = kStepThreads / 32;
-  __shared__ float ks[kMaxDk], qs[kMaxDk];
+  __shared__ float ks[kAhead][kMaxDk], qs[kAhead][kMaxDk], gates[kAhead][2];
+  __shared__ float4 vs[kAhead][AC];
   __shared__ float4 py[2][WARPS][AC], pz[2][WARPS][AC];
   __shared__ float pkq[2][WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -70,32 +72,44 @@ __global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
   }
   for (int t = 0; t < a.tokens; ++t) {
     const long long row = row0 + t;
-    const E* q = static_cast<const E*>(a.q) + row * a.ldq + (long long)hq * a.dk;
-    const E* k = static_cast<const E*>(a.k) + row * a.ldk + (long long)hq * a.dk;
-    if (tid < kMaxDk) {
-      ks[tid] = tid < a.dk ? to_f(k[tid]) : 0.f;
-    } else {
-      const int r = tid - kMaxDk;
-      qs[r] = r < a.dk ? to_f(q[r]) : 0.f;
+    const int ta = t % kAhead;
+    if (ta == 0) {
+      if (t > 0) __syncthreads();               // the last rows have been read
+      const int more = min(kAhead, a.tokens - t), r = tid & (kMaxDk - 1);
+      const E* kq = (tid < kMaxDk ? static_cast<const E*>(a.k) + row * a.ldk : static_cast<const E*>(a.q) + row * a.ldq) +
+                    (long long)hq * a.dk;
+      const long long ld = tid < kMaxDk ? a.ldk : a.ldq;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (x < more) (tid < kMaxDk ? ks : qs)[x][r] = r < a.dk ? to_f(kq[x * ld + r]) : 0.f;
+      if (tid < more * AC) {
+        const int x = tid / AC, cc = tile * TDV + (tid % AC) * 4;
+        float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cc < a.dv) {
+          const E* v = static_cast<const E*>(a.v) + (row + x) * a.ldv + (long long)h * a.dv + cc;
+          v4 = make_float4(to_f(v[0]), to_f(v[1]), to_f(v[2]), to_f(v[3]));
+        }
+        vs[x][tid % AC] = v4;
+      }
+      if (tid >= kStepThreads - 2 * kAhead) {
+        const int x = (tid - (kStepThreads - 2 * kAhead)) >> 1;
+        if (x < more) gates[x][tid & 1] = tid & 1 ? a.beta[(row + x) * a.hv + h] : expf(a.g[(row + x) * a.hv + h]);
+      }
+      __syncthreads();
     }
-    const float al = expf(a.g[row * a.hv + h]), be = a.beta[row * a.hv + h];
-    float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-      const E* v = static_cast<const E*>(a.v) + row * a.ldv + (long long)h * a.dv + col;
-      vv = make_float4(to_f(v[0]), to_f(v[1]), to_f(v[2]), to_f(v[3]));
-    }
-    __syncthreads();
+    const float al = gates[ta][0], be = gates[ta][1];
+    const float4 vv = vs[ta][ca];
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = rg + i * RG;
       if (r >= kMaxDk) continue;
-      const float kk = ks[r], qq = qs[r];
+      const float kk = ks[ta][r], qq = qs[ta][r];
       y.x = fmaf(s[i].x, kk, y.x); y.y = fmaf(s[i].y, kk, y.y); y.z = fmaf(s[i].z, kk, y.z); y.w = fmaf(s[i].w, kk, y.w);
       z.x = fmaf(s[i].x, qq, z.x); z.y = fmaf(s[i].y, qq, z.y); z.z = fmaf(s[i].z, qq, z.z); z.w = fmaf(s[i].w, qq, z.w);
     }
     float kq = 0.f;
-    for (int r = tid; r < kMaxDk; r += kStepThreads) kq = fmaf(ks[r], qs[r], kq);
+    for (int r = tid; r < kMaxDk; r += kStepThreads) kq = fmaf(ks[ta][r], qs[ta][r], kq);
 #pragma unroll
     for (int m = AC; m < 32; m <<= 1) {
       y.x += __shfl_xor_sync(0xffffffffu, y.x, m); y.y += __shfl_xor_sync(0xffffffffu, y.y, m);
@@ -124,7 +138,7 @@ __global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
     for (int i = 0; i < RPT; ++i) {
       const int r = rg + i * RG;
       if (r >= kMaxDk) continue;
-      const float kk = ks[r];
+      const float kk = ks[ta][r];
       s[i].x = fmaf(kk, u.x, al * s[i].x); s[i].y = fmaf(kk, u.y, al * s[i].y);
       s[i].z = fmaf(kk, u.z, al * s[i].z); s[i].w = fmaf(kk, u.w, al * s[i].w);
     }
@@ -135,7 +149,6 @@ __global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
       put(p + 2, a.scale * fmaf(kq, u.z, al * z.z));
       put(p + 3, a.scale * fmaf(kq, u.w, al * z.w));
     }
-    if (t + 1 < a.tokens) __syncthreads();      // ks, qs are rewritten
   }
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
