@@ -36,7 +36,7 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 
 // RPT rows of the state a thread: rows rg, rg + RG, ... of RG row groups.
 template <class E, int TDV, int RPT>
-__global__ void __launch_bounds__(kStepThreads, 4) k_gdr_step(StepArgs a) {
+__global__ void __launch_bounds__(kStepThreads, RPT <= 2 ? 6 : 4) k_gdr_step(StepArgs a) {
   constexpr int AC = TDV / 4;                   // threads across the columns
   constexpr int RG = kStepThreads / AC;
   constexpr int WARPS = kStepThreads / 32;
