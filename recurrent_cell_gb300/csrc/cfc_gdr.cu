@@ -380,9 +380,8 @@ static cudaError_t forward_fp32(const FwdArgs& a, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // Tiles of 32 value columns where their blocks still reach every SM, else of 16.
-  const bool wide = a.s.dv > 16 && (long long)a.s.n_seq * a.s.hv * ((a.s.dv + 31) / 32) >= kFillSMs;
-  return wide ? scan<DK, 2>(a, st) : scan<DK, 1>(a, st);
+  // Tiles of 32 value columns or of 16 (32 heads of 128, 512 tokens: 86 us, 127).
+  return wide_tiles((long long)a.s.n_seq * a.s.hv, a.s.dv, 16) ? scan<DK, 2>(a, st) : scan<DK, 1>(a, st);
 }
 
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }

@@ -510,8 +510,8 @@ static cudaError_t scan_bwd(BwdArgs a, cudaStream_t st) {
 
 template <int DK>
 static cudaError_t backward_fp32(const BwdArgs& a, cudaStream_t st) {
-  const bool wide = a.s.dv > 16 && (long long)a.s.n_seq * a.s.hv * ((a.s.dv + 31) / 32) >= kFillSMs;
-  cudaError_t e = wide ? scan_bwd<DK, 2>(a, st) : scan_bwd<DK, 1>(a, st);
+  // as in the forward (84 us, 133)
+  cudaError_t e = wide_tiles((long long)a.s.n_seq * a.s.hv, a.s.dv, 16) ? scan_bwd<DK, 2>(a, st) : scan_bwd<DK, 1>(a, st);
   if (e != cudaSuccess || a.s.rows == 0) return e;
   constexpr size_t bytes = sizeof(GradSmem<DK>);
   static_assert(bytes <= 227u * 1024u, "shared memory");

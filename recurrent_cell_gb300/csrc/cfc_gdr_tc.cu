@@ -911,17 +911,19 @@ cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
   return planes == 2 ? prep<128, 2>(a, st) : prep<128, 1>(a, st);
 }
 
+// Heads of 128, 1024 tokens, narrow tiles against wide, us:
+//   state asked for (32 columns, 64):   32 heads 32, 43;  64 heads  61,  45;  256 heads 205, 162
+//   not (64, 128):                      64 heads 36, 52;  96 heads  65,  53;  256 heads 133, 106
+//   backward (64, 128):                 64 heads 39, 60;  96 heads  74,  59;  256 heads 145, 119
 template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  if (planes == 2)
-    return t.s.dv > 32 && heads * ((t.s.dv + 63) / 64) >= kFillSMs ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
-  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= kFillSMs ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
+  if (planes == 2) return wide_tiles(heads, t.s.dv, 32) ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
+  return wide_tiles(heads, t.s.dv, 64) ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
-  const long long heads = (long long)t.s.n_seq * t.s.hv;
-  return t.s.dv > 64 && heads * ((t.s.dv + 127) / 128) >= kFillSMs ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
+  return wide_tiles((long long)t.s.n_seq * t.s.hv, t.s.dv, 64) ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {

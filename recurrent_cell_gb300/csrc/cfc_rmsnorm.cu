@@ -12,9 +12,9 @@
 // fp32 and rounded once, on its way out.
 //
 // Memory is the bound in both directions (about one operation a byte), so a
-// row is read once and kept in registers: 8 to 32 lanes a row up to 2 vectors
+// row is read once and kept in registers: 8 to 32 lanes a row up to 4 vectors
 // of 16 bytes each, a block a row beyond that, of as many warps as leave each
-// thread 2 (long rows: 4) vectors.  Rows that are no whole number of vectors go
+// thread 4 (backward, where that fits: 2) vectors.  Rows that are no whole number of vectors go
 // element by element in the same way.  Blocks are persistent: they keep their
 // columns' weights, and in the backward their columns' grad_w, in registers,
 // and load the next row before they finish the present one.
@@ -477,7 +477,12 @@ static cudaError_t bwd(const Args& a, int threads, int* blocks, cudaStream_t st)
 }
 
 // The variant by row length, f.operator()<V, NV, LANES>(threads).  `lanes`: at
-// least so many lanes side by side (a scale's columns).
+// least so many lanes side by side (a scale's columns).  Both directions, bf16,
+// a side against its neighbour: 65536 x 64 with 8 lanes a row 28 us, with 32 54;
+// 65536 x 512 with a warp a row 97, a block 167; 16384 x 1024 with a warp and 4
+// vectors a lane 61, a block 69; 16384 x 2560 with 2 vectors a thread 122, with 4
+// in the backward too 132; forward alone, 8 bits out, 16384 x 8192: 2 vectors
+// 167, 4 153.
 template <class V, bool BWD, class F>
 static cudaError_t by_row(int d, int lanes, F f) {
   const int nvec = d / V::N;
@@ -486,7 +491,9 @@ static cudaError_t by_row(int d, int lanes, F f) {
     if (nvec <= 16 && lanes <= 8) return f.template operator()<V, 2, 8>(kLaneThreads);
     if (nvec <= 32 && lanes <= 16) return f.template operator()<V, 2, 16>(kLaneThreads);
     if (nvec <= 64) return f.template operator()<V, 2, 32>(kLaneThreads);
-    if (threads(2) <= most_threads<V, 2, 0, BWD>()) return f.template operator()<V, 2, 0>(threads(2));
+    if (nvec <= 128) return f.template operator()<V, 4, 32>(kLaneThreads);
+    if constexpr (BWD)
+      if (threads(2) <= most_threads<V, 2, 0, BWD>()) return f.template operator()<V, 2, 0>(threads(2));
     if (threads(4) <= most_threads<V, 4, 0, BWD>()) return f.template operator()<V, 4, 0>(threads(4));
   } else {
     if (threads(4) <= 128) return f.template operator()<V, 4, 0>(threads(4));

@@ -33,9 +33,12 @@ constexpr int kMaxDk = 128;     // key width limit: the state's rows stay in one
 constexpr int kMaxDv = 256;
 constexpr int kPad = 4;         // floats between rows in shared memory: rows of a tile in different banks
 constexpr int kLdT = kC + kPad; // a row of 64 x 64 in FP32: T - I and P in shared memory and workspace, R, U
-// Blocks that count as reaching every SM: three quarters of them.  Wider tiles
-// read the operands that tiles share fewer times, narrower ones run on more SMs.
-constexpr int kFillSMs = kNumSMs * 3 / 4;
+// A serial pass takes tiles twice as wide where narrow ones no longer fit the
+// SMs at once: a wide tile takes 1.4 to 1.6 times a narrow one's time, a second
+// round of narrow ones 2.
+constexpr bool wide_tiles(long long heads, int dv, int narrow) {
+  return dv > narrow && heads * ((dv + narrow - 1) / narrow) > kNumSMs;
+}
 // Per chunk and head: exp(G), exp(G_C - G), beta, G / ln 2 as pairs of floats
 // hi + lo, exp(G_C), and two words of bits (even rows, odd rows): the tokens that
 // nothing passes, a factor of zero or a sequence's first from the zero state.
