@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(256) k_gdr_grad(BwdArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int col = wc * (DK / 2) + j * 8 + t2;
-      const float2 kk = *reinterpret_cast<const float2*>(sm.k + i * S::LDK + col), qq = *reinterpret_cast<const float2*>(sm.q + i * S::LDK + col);
+      const float2 kk = *reinterpret_cast<const float2*>(sm.k + i * S::LDK + col);
+      const float2 qq = *reinterpret_cast<const float2*>(sm.q + i * S::LDK + col);
       const float q0 = aq[j][2 * rr], q1 = aq[j][2 * rr + 1], e0 = ax[j][2 * rr], e1 = ax[j][2 * rr + 1];
       const float k0 = fmaf(be, e0, au[j][2 * rr]), k1 = fmaf(be, e1, au[j][2 * rr + 1]);
       dq_ = fmaf(qq.x, q0, fmaf(qq.y, q1, dq_));

@@ -8,7 +8,8 @@
 // one after another and writes back.  With a = exp(g), y = S^T k, z = S^T q
 // from one pass over the registers,
 //   u = beta (v - a y),  S <- a S + k u^T,  o = scale (a z + (k.q) u):
-// one block-wide sum a token.
+// one block-wide sum a token.  192 sequences x 32 heads of 128 x 128: 805 MB in
+// 128 us, 6.3 TB/s; one sequence of 16 heads 2.7 us, a launch's latency.
 #include "gdr_common.cuh"
 
 namespace cfc {
