@@ -137,6 +137,7 @@ def cfc_selftest_timeout(max_polls: int = 1000, stream=None) -> None:
 
 
 _torch_module = None
+_storage = {}
 
 
 def _torch():
@@ -147,12 +148,19 @@ def _torch():
     return _torch_module
 
 
+_raw_stream = None
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
         # the current stream's handle without building a Stream object: the
         # binding is most of a small call's time
-        torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            torch = _torch()
+            torch.cuda.current_device()             # brings CUDA up
+            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream[0](_raw_stream[1]())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -178,8 +186,11 @@ def _ptr(t, name, dtype=None, shape=None, optional=False):
 
 
 def _storage_dtype(math):
-    torch = _torch()
-    return torch.bfloat16 if math == MATH_BF16 else torch.float32
+    st = _storage.get(math)
+    if st is None:
+        torch = _torch()
+        st = _storage[math] = torch.bfloat16 if math == MATH_BF16 else torch.float32
+    return st
 
 
 def _check(fn, status):

@@ -362,8 +362,7 @@ template <int DK, int WM>
 static cudaError_t scan(FwdArgs a, cudaStream_t st) {
   using C = ScanCfg<DK, WM>;
   a.ntile = (a.s.dv + C::DVT - 1) / C::DVT;
-  cudaError_t e =
-      cudaFuncSetAttribute(k_gdr_scan<DK, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  cudaError_t e = allow_smem<k_gdr_scan<DK, WM>>(C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan", st);
   k_gdr_scan<DK, WM><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
@@ -374,7 +373,7 @@ template <int DK>
 static cudaError_t forward_fp32(const FwdArgs& a, cudaStream_t st) {
   if (a.s.rows > 0) {
     using S = PrepSmem<DK>;
-    cudaError_t e = cudaFuncSetAttribute(k_gdr_prep<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+    cudaError_t e = allow_smem<k_gdr_prep<DK>>(S::kBytes);
     if (e != cudaSuccess) return e;
     TraceScope tr("k_gdr_prep", st);
     k_gdr_prep<DK><<<(unsigned)(slot_count(a.s.rows, a.s.n_seq) * a.s.hv), 128, S::kBytes, st>>>(a);

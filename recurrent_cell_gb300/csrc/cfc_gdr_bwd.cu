@@ -501,8 +501,7 @@ template <int DK, int WM>
 static cudaError_t scan_bwd(BwdArgs a, cudaStream_t st) {
   using C = BwdCfg<DK, WM>;
   a.ntile = (a.s.dv + C::DVT - 1) / C::DVT;
-  cudaError_t e =
-      cudaFuncSetAttribute(k_gdr_scan_bwd<DK, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  cudaError_t e = allow_smem<k_gdr_scan_bwd<DK, WM>>(C::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_scan_bwd", st);
   k_gdr_scan_bwd<DK, WM><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a);
@@ -516,7 +515,7 @@ static cudaError_t backward_fp32(const BwdArgs& a, cudaStream_t st) {
   if (e != cudaSuccess || a.s.rows == 0) return e;
   constexpr size_t bytes = sizeof(GradSmem<DK>);
   static_assert(bytes <= 227u * 1024u, "shared memory");
-  e = cudaFuncSetAttribute(k_gdr_grad<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  e = allow_smem<k_gdr_grad<DK>>(bytes);
   if (e != cudaSuccess) return e;
   {
     TraceScope tr("k_gdr_grad", st);

@@ -498,7 +498,7 @@ template <int DK, bool SHARED>
 static cudaError_t launch(GradArgs g, cudaStream_t st) {
   using C = GradCfg<DK>;
   const long long items = slot_count(g.s.rows, g.s.n_seq) * g.s.hk;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_grad_tc<DK, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
+  cudaError_t e = allow_smem<k_gdr_grad_tc<DK, SHARED>>(C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   g.tma = tile_map(&m.q, g.q, g.s.dk, g.s.hk, g.s.rows, g.ldq, 64) &&

@@ -886,8 +886,7 @@ static cudaError_t scan(TcArgs a, cudaStream_t st) {
   // What the backward reads is kept in tiles of 64 columns: narrower blocks also fill the last one's zeros.
   constexpr int UP = C::NV < 64 ? 64 : C::NV;
   a.ntile = a.st ? (a.s.dv + UP - 1) / UP * (UP / C::NV) : (a.s.dv + C::NV - 1) / C::NV;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_tc<DK, PL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::BYTES);
+  cudaError_t e = allow_smem<k_gdr_scan_tc<DK, PL, NB>>(C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   a.tma = maps_of(a, C::NV < 64 ? C::NV : 64, &m);
@@ -899,8 +898,7 @@ template <int DK, int NB>
 static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
   using C = TcCfg<DK, 1, NB, true>;
   a.ntile = (a.s.dv + C::NV - 1) / C::NV;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_scan_bwd_tc<DK, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::BYTES);
+  cudaError_t e = allow_smem<k_gdr_scan_bwd_tc<DK, NB>>(C::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
   a.tma = maps_of(a, 64, &m);
@@ -912,7 +910,7 @@ static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
 template <int DK, int PL>
 static cudaError_t prep(const FwdArgs& a, cudaStream_t st) {
   using S = PrepTc<DK>;
-  cudaError_t e = cudaFuncSetAttribute(k_gdr_prep_tc<DK, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::BYTES);
+  cudaError_t e = allow_smem<k_gdr_prep_tc<DK, PL>>(S::BYTES);
   if (e != cudaSuccess) return e;
   TraceScope tr("k_gdr_prep_tc", st);
   k_gdr_prep_tc<DK, PL><<<(unsigned)(slot_count(a.s.rows, a.s.n_seq) * a.s.hv), 128, S::BYTES, st>>>(a);

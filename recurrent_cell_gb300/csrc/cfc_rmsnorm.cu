@@ -22,6 +22,8 @@
 // 81 us, 5.8 TB/s.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "cfc_internal.cuh"
 
 namespace cfc {
@@ -450,11 +452,12 @@ constexpr int kMaxBlocks = 4 * kNumSMs;
 // Blocks of `kernel` that an SM holds at once (asked once for each block size).
 template <auto KERNEL>
 static int resident(int threads, size_t smem) {
-  static int known[kWarps + 1] = {};
-  int n = known[threads / 32];
+  static std::atomic<int> known[kWarps + 1] = {};
+  int n = known[threads / 32].load(std::memory_order_relaxed);
   if (n > 0) return n;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, smem) != cudaSuccess || n < 1) n = 1;
-  return known[threads / 32] = n;
+  known[threads / 32].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 template <class V, int NV, int LANES>
