@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
       lost = true;
       atomicExch(&g_gdr_error, 1);
     }
+    lost = __any_sync(0xffffffffu, lost);      // a warp goes on as one
   };
 
   if (tid >= C::WORK) {     // ---- the fetching warps

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
       lost = true;
       atomicExch(&g_gdr_grad_error, 1);
     }
+    lost = __any_sync(0xffffffffu, lost);      // a warp goes on as one
   };
 
   if (tid >= C::WORK && tid < C::WORK + C::FETCH) {     // ---- the fetching warps
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     };
     auto claim = [&](int i, uint32_t use) {      // buffer i for its use-th time
       if (use == 0) return;
-      if (!lost && tc::mbar_try_wait(empty + i, (use - 1) & 1)) return;
+      if (__all_sync(0xffffffffu, !lost && tc::mbar_try_wait(empty + i, (use - 1) & 1))) return;
       flush();
       wait(empty + i, (use - 1) & 1);
     };
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     const long long ldo = (long long)a.s.hv * dv;
     const long long items = slot_count(a.s.rows, a.s.n_seq) * a.s.hk;
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+      if (group_any<2, C::FETCH>(lost)) break;       // nothing more is fetched after a wait that gave up
       const long long slot = item / a.s.hk;
       const int hk = (int)(item % a.s.hk);
       int n, len, c;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
         unsigned char* b = stage + st * C::STAGE;
         wait(full + st, (it >> 1) & 1);
         if (t == 0) {
-          if (lost || reinterpret_cast<const Chunk*>(b + C::OFF_VEC + kVec * 4)->rows < 0) goto over;
+          if (__any_sync(0xffffffffu, lost || reinterpret_cast<const Chunk*>(b + C::OFF_VEC + kVec * 4)->rows < 0)) goto over;
           if (heads > 0) wait(acc_out, (heads - 1) & 1);
         }
         tc::fence_after_sync();
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
     for (uint32_t heads = 0;; ++heads) {
       wait(full + (it & 1), (it >> 1) & 1);
       const Chunk ck = *reinterpret_cast<const Chunk*>(stage + (it & 1) * C::STAGE + C::OFF_VEC + kVec * 4);
-      if (ck.rows < 0 || lost) break;
+      // a wait that gave up ends it for all at once, so that nobody stays behind at a barrier
+      if (group_any<1, C::WORK>(ck.rows < 0 || lost)) break;
       const float* vec = reinterpret_cast<const float*>(stage + (it & 1) * C::STAGE + C::OFF_VEC);
       const float eg = vec[kVecEG + i], el = vec[kVecEGL + i], be = vec[kVecBeta + i], dec = vec[kVecD];
       const float2 be2 = *reinterpret_cast<const float2*>(vec + kVecBeta + 2 * lane);
@@ -487,6 +490,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
       tc::mbar_wait(done + j, 0, kPolls);
     }
   tc::fence_before_sync();
+  __syncwarp();
   __syncthreads();
   if (warp == 0) {
     tc::fence_after_sync();

@@ -308,12 +308,13 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
     if (i >= 2 && i - 2 < nc) {
       const int cl = backwards ? c + 2 : c - 2;
       bf16* o = a.o + (start + (long long)cl * kC) * ldo + (long long)h * a.s.dv + v0;
-      wait(outs + st, (i / 2 - 1) & 1);
+      const bool on = wait(outs + st, (i / 2 - 1) & 1);
       // 4 warps: 32 rows by half of the columns each
       const int w = ft >> 5;
       rows_out<NV, NV / 2>(o, ldo, b + C::KQ + C::A2, (w & 1) * 32, (w >> 1) * (NV / 16), min(kC, len - cl * kC), vn,
                            ft & 31);
-      asm volatile("bar.sync 15, 128;" ::: "memory");       // the tiles are filled again by other threads
+      // the tiles are filled again by other threads; nothing more is fetched after a wait that gave up
+      if (group_any<15, C::FETCH>(!on)) return;
       wait(empty + st, (i / 2 - 1) & 1);
     }
     if (i >= nc) continue;
@@ -412,7 +413,10 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
       lost = true;
       atomicExch(&g_gdr_tc_error, 1);
     }
+    lost = __any_sync(0xffffffffu, lost);      // a warp goes on as one
+    return !lost;
   };
+  // (a warp comes to it as one, and one instruction's answer is the same for all its lanes)
   auto poll = [&](uint64_t* bar, uint32_t parity) {
     if (!lost && !poll_wait(bar, parity, kPollsBusy)) {
       lost = true;
@@ -575,6 +579,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
           *reinterpret_cast<uint4*>(vt + v_at<NV>(i, (c0 + j) / 8)) = pack8(r + j);
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
+        __syncwarp();
       }
       // the next chunk's tiles, long there: the block's barrier passes it on
       if (issuer && c + 1 < nc) wait(full + (st ^ 1), ((c + 1) >> 1) & 1);
@@ -604,6 +609,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
       tc::mbar_wait(done + j, 0, kPolls);
     }
   tc::fence_before_sync();
+  __syncwarp();
   __syncthreads();
   if (warp == 0) {
     tc::fence_after_sync();
@@ -659,7 +665,10 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
       lost = true;
       atomicExch(&g_gdr_tc_error, 1);
     }
+    lost = __any_sync(0xffffffffu, lost);      // a warp goes on as one
+    return !lost;
   };
+  // (a warp comes to it as one, and one instruction's answer is the same for all its lanes)
   auto poll = [&](uint64_t* bar, uint32_t parity) {
     if (!lost && !poll_wait(bar, parity, kPollsBusy)) {
       lost = true;
@@ -818,6 +827,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
         }
         __syncwarp();
         if (lane == 0) bar_arrive(outs + st);
+        __syncwarp();
       }
       poll(done, phase);
       phase ^= 1;
@@ -845,6 +855,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
       tc::mbar_wait(done + j, 0, kPolls);
     }
   tc::fence_before_sync();
+  __syncwarp();
   __syncthreads();
   if (warp == 0) {
     tc::fence_after_sync();

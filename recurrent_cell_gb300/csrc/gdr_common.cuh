@@ -151,10 +151,24 @@ __device__ __forceinline__ void bar_arrive_tx(uint64_t* bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive_cp(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Barrier over the first `threads` threads that name it (1 .. 15).
+// Barrier over the first `threads` threads that name it (1 .. 15).  A warp has
+// to come to it as one, and the lanes of a wait may leave it one by one.
 template <int ID, int THREADS>
 __device__ __forceinline__ void group_sync() {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+// The same, and whether `p` holds for any of them: one decision for all.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool group_any(bool p) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(ID), "n"(THREADS)
+      : "memory");
+  return r != 0;
 }
 constexpr uint32_t kPolls = 1u << 20, kPollsBusy = 1u << 24;   // of a bounded wait that suspends, that polls
 

@@ -605,3 +605,24 @@ def test_binding_refuses_what_does_not_fit():
         cfc.cfc_gdr_forward(*c.dev, o, ws)                                  # rows without offsets
     with pytest.raises(ValueError):
         cfc.cfc_gdr_step(*[a[None] for a in c.dev], torch.empty(1, 2, 16, 32, device="cuda"), o[None])
+
+
+@pytest.mark.parametrize("shape", [(3, 3, 72, 136), (2, 6, 64, 96), (1, 2, 128, 256), (2, 2, 64, 64)], ids=str)
+def test_bits_depend_neither_on_the_run_nor_on_what_the_workspace_held(shape):
+    """Blocks with one, two, three and four tiles of value columns, whole and partial chunks."""
+    torch = torch_mod()
+    c = Case([64, 200, 5], *shape, BF16, seed=43)
+    c.forward(final=False, save=True)
+    go = c.go.cuda()
+    first = None
+    for run in range(40):
+        ws = c.workspace(True, fill=(255, 0, 63, 1)[run % 4])
+        o = torch.empty_like(c.dev[2])
+        grads = [torch.empty(a.shape, dtype=c.dtype, device="cuda") for a in c.dev]
+        cfc.cfc_gdr_forward(*c.dev, o, ws, seq_offsets=c.offsets, save=True, math=BF16)
+        cfc.cfc_gdr_backward(*c.dev, go, *grads, ws, seq_offsets=c.offsets, math=BF16)
+        if first is None:
+            first = [o] + grads
+            c.check({"o": o.cpu().double()}, c.oracle(), ("o",))
+        for a, b in zip(first, [o] + grads):
+            assert torch.equal(a, b), run
