@@ -47,22 +47,34 @@ struct PrepTc {
   // k, then A and T, then P T; q, then T - I: each is done with when the next begins
   static constexpr uint32_t OFF_I = (K > A ? K : A), OFF_G = OFF_I + (K > kImage / 2 ? K : kImage / 2);
   static constexpr uint32_t BYTES = OFF_G + 3 * kC * 4;
+  static_assert(BYTES >= kMaxOrder * 4, "the sequences' lengths");
 };
 
 // The sequences' order by falling length (ties by number): the longest one's
 // serial pass is the least that the whole takes, so it has to begin first (16
 // prompts of 0 to 4100 tokens x 16 heads 222 us, in their own order 233).
-__device__ __forceinline__ void longest_first(const FwdArgs& a, int tid) {
-  for (int n = tid; n < a.s.n_seq; n += 128) {
+// `lens`: kMaxOrder ints of shared memory.
+__device__ __noinline__ void longest_first(const FwdArgs& a, int* lens, int tid) {
+  const int n4 = (a.s.n_seq + 3) / 4 * 4;
+  for (int n = tid; n < n4; n += 128) {
     long long s;
-    int len, l, rank = 0;
-    seq_range(a.s, n, &s, &len);
-    for (int m = 0; m < a.s.n_seq; ++m) {
-      seq_range(a.s, m, &s, &l);
-      rank += l > len || (l == len && m < n);
+    int len = -1;
+    if (n < a.s.n_seq) seq_range(a.s, n, &s, &len);
+    lens[n] = len;
+  }
+  __syncthreads();
+  for (int n = tid; n < a.s.n_seq; n += 128) {
+    const int len = lens[n];
+    int rank = 0;
+#pragma unroll 4
+    for (int m = 0; m < n4; m += 4) {
+      const int4 l = *reinterpret_cast<const int4*>(lens + m);
+      // as long, and before it
+      rank += (l.x + (m < n) > len) + (l.y + (m + 1 < n) > len) + (l.z + (m + 2 < n) > len) + (l.w + (m + 3 < n) > len);
     }
     a.order[rank] = n;
   }
+  __syncthreads();
 }
 
 template <int DK, int PL>
@@ -81,7 +93,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   const long long slot = blockIdx.x / a.s.hv;
   int n, len, c;
   long long start;
-  if (a.order && blockIdx.x == 0) longest_first(a, tid);
+  if (a.order && blockIdx.x == 0) longest_first(a, reinterpret_cast<int*>(smem_raw), tid);
   if (!slot_chunk(a.s, slot, &n, &start, &len, &c)) return;
   const long long row0 = start + (long long)c * kC;
   const int rows = min(kC, len - c * kC);
