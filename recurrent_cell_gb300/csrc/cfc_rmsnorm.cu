@@ -267,16 +267,16 @@ __global__ void __launch_bounds__(most_threads<V, NV, LANES, false>(), !LANES &&
           if (a.group == a.d ? at == 0 : (at & (gl - 1)) == 0) a.scale[row * (a.d / a.group) + at * N / a.group] = c;
           if constexpr (N == 1) {
             a.y8[row * a.d + at] = e4m3(s[j][0] * inv);
-            continue;
-          }
-          uint32_t u[(N + 3) / 4];
+          } else {
+            uint32_t u[N / 4];
 #pragma unroll
-          for (int e = 0; e < N / 4; ++e)
-            u[e] = e4m3x2(s[j][4 * e] * inv, s[j][4 * e + 1] * inv) |
-                   e4m3x2(s[j][4 * e + 2] * inv, s[j][4 * e + 3] * inv) << 16;
-          uint32_t* p = reinterpret_cast<uint32_t*>(a.y8 + row * a.d + (long long)at * N);
-          if constexpr (N == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(u[0], u[1]));
-          else if constexpr (N == 4) __stcs(p, u[0]);
+            for (int e = 0; e < N / 4; ++e)
+              u[e] = e4m3x2(s[j][4 * e] * inv, s[j][4 * e + 1] * inv) |
+                     e4m3x2(s[j][4 * e + 2] * inv, s[j][4 * e + 3] * inv) << 16;
+            uint32_t* p = reinterpret_cast<uint32_t*>(a.y8 + row * a.d + (long long)at * N);
+            if constexpr (N == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(u[0], u[1]));
+            else __stcs(p, u[0]);
+          }
         }
       }
     }
