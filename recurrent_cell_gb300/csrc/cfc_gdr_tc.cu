@@ -320,14 +320,13 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
     if (i >= 2 && i - 2 < nc) {
       const int cl = backwards ? c + 2 : c - 2;
       bf16* o = a.o + (start + (long long)cl * kC) * ldo + (long long)h * a.s.dv + v0;
-      const bool on = wait(outs + st, (i / 2 - 1) & 1);
+      wait(outs + st, (i / 2 - 1) & 1);
       // 4 warps: 32 rows by half of the columns each
       const int w = ft >> 5;
       rows_out<NV, NV / 2>(o, ldo, b + C::KQ + C::A2, (w & 1) * 32, (w >> 1) * (NV / 16), min(kC, len - cl * kC), vn,
                            ft & 31);
-      // the tiles are filled again by other threads; nothing more is fetched after a wait that gave up
-      if (group_any<15, C::FETCH>(!on)) return;
-      wait(empty + st, (i / 2 - 1) & 1);
+      group_sync<15, C::FETCH>();          // the tiles are filled again by other threads
+      if (!wait(empty + st, (i / 2 - 1) & 1)) continue;      // nothing more is fetched after a wait that gave up
     }
     if (i >= nc) continue;
     const int rows = min(kC, len - c * kC);
