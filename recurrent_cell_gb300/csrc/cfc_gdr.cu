@@ -397,7 +397,7 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
   take(&w.off_t, slots * (bf ? kImage : kC * kLdT * sizeof(float)));
   take(&w.off_p, bf ? 0 : slots * kC * kLdT * sizeof(float));
   take(&w.off_vec, slots * kVec * 4);
-  take(&w.off_order, bf && n_seq <= kMaxOrder ? n_seq * sizeof(int) : 0);
+  take(&w.off_order, bf && n_seq <= kMaxOrder ? (n_seq + 2) * sizeof(int) : 0);
   if (save) {
     const size_t wk = bf ? (dk <= 64 ? 64 : 128) : dk, wv = bf ? (dv + 63) / 64 * 64 : dv;
     take(&w.off_s0, slots * wk * wv * e);

@@ -74,6 +74,22 @@ __device__ __noinline__ void longest_first(const FwdArgs& a, int* lens, int tid)
     }
     a.order[rank] = n;
   }
+  // How many of them to halve (see work_of), for tiles of 64 and of 128 columns.
+  if (tid < 32) {
+    long long sum = 0;
+    for (int n = tid; n < a.s.n_seq; n += 32) sum += (lens[n] + kC - 1) / kC;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const long long share = sum * a.s.hv * ((a.s.dv + (64 << w) - 1) / (64 << w)) / kNumSMs;
+      int count = 0;
+      for (int n = tid; n < a.s.n_seq; n += 32) count += 4ll * ((lens[n] + kC - 1) / kC) > 5 * share;
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) count += __shfl_xor_sync(0xffffffffu, count, m);
+      if (tid == 0) a.order[a.s.n_seq + w] = count;
+    }
+  }
   __syncthreads();
 }
 
@@ -286,14 +302,49 @@ struct TcArgs {
   const float* vec;
   // per chunk and 64 value columns, as operand tiles: S0 and U (backward: dS1, dR), or NULL
   unsigned char *st, *u;
-  const int* order;
+  const int* order;             // the sequences, longest first; then how many to halve
   int ntile, tma;
+  int twice;                    // so many of the longest may go in tiles of half the width; 0: none
 };
 
 // The n-th sequence to run; held to the batch whatever the workspace holds.
 __device__ __forceinline__ int nth(const TcArgs& a, int i) {
   const int n = a.order ? a.order[i] : i;
   return (unsigned)n < (unsigned)a.s.n_seq ? n : i;
+}
+
+// What a block does: a tile of a head of a sequence; tile < 0: nothing.  The
+// longest sequences, those that would outlast by a quarter and more an even
+// share of the whole, take tiles of half the width, two thirds of the time a
+// chunk.  (Training of 3000 of 6470 tokens x 16 heads 404 -> 292 us, prompts of 8000 of
+// 8530 tokens x 16 heads 335 -> 249; at 1.05 of the share 194 -> 220, so not there.)
+struct Work {
+  int n, h, tile, len;
+  long long start;
+  bool half;
+};
+__device__ __forceinline__ Work work_of(const TcArgs& a, int wide) {
+  Work w;
+  int b = blockIdx.x, k = 0;
+  if (a.twice > 0) {
+    k = a.order[a.s.n_seq + (wide == 128)];
+    k = k < 0 || k > a.twice ? 0 : k;
+  }
+  const int two = 2 * a.ntile, first = k * a.s.hv * two;
+  w.half = b < first;
+  const int tiles = w.half ? two : a.ntile;
+  if (!w.half) b -= first;
+  w.tile = b % tiles;
+  b /= tiles;
+  w.h = b % a.s.hv;
+  b = b / a.s.hv + (w.half ? 0 : k);
+  if (b >= a.s.n_seq) {
+    w.tile = -1;
+    return w;
+  }
+  w.n = nth(a, b);
+  seq_range(a.s, w.n, &w.start, &w.len);
+  return w;
 }
 
 // The fetching warps' loop.  The chunk before last's output rows (o, or the
@@ -304,7 +355,8 @@ __device__ __forceinline__ int nth(const TcArgs& a, int i) {
 // copies alone, both passes and the gradients: 16384 tokens x 16 heads 532 us
 // against 487, training of 8 x 2048 x 16 heads 478 against 434.
 template <int DK, class C, class W>
-__device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, unsigned char* stage, uint64_t* full,
+__device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, const CUtensorMap* v_map,
+                                             unsigned char* stage, uint64_t* full,
                                              uint64_t* empty, uint64_t* outs, int ft, int h, long long start, int len,
                                              long long slot0, int v0, bool backwards, W wait) {
   constexpr int NV = C::NV;
@@ -345,7 +397,7 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
         constexpr int VB = NV < 64 ? NV : 64;
 #pragma unroll
         for (int x = 0; x < NV / VB; ++x)
-          tma_tile(b + C::KQ + C::A2 + x * 8192, &maps.v, v0 + x * VB, h, row, full + st);
+          tma_tile(b + C::KQ + C::A2 + x * 8192, v_map, v0 + x * VB, h, row, full + st);
       }
       bulk_load(b + C::KQ, a.a2 + id * 32768, C::A2, full + st);
       bulk_load(b + C::KQ + C::A2 + C::VT, a.vec + id * kVec, kVec * 4, full + st);
@@ -383,25 +435,19 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
 }
 
 // ------------------------------------------------------------------- forward
+// A block's work: a tile of a head of sequence n, the rows start .. start + len.
 template <int DK, int PL, int NB>
-__global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
-    k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
+__device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, const CUtensorMap* v_map,
+                                          unsigned char* smem_raw, int n, int h, int tile, long long start, int len) {
   using C = TcCfg<DK, PL, NB, false>;
   constexpr int NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;      // columns a thread; at a time
-  extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tile = blockIdx.x % a.ntile;
-  const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
-  const int n = nth(a, at_n);
   const long long sh = (long long)n * a.s.hv + h;
-  long long start;
-  int len;
-  seq_range(a.s, n, &start, &len);
   const int nc = (len + kC - 1) / kC;
   const long long slot0 = slot_base(start, n);
   if (tid == 0) {
@@ -436,7 +482,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
   };
 
   if (tid >= C::WORK) {
-    fetch_chunks<DK, C>(a, maps, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+    fetch_chunks<DK, C>(a, maps, v_map, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
                                      tile * NV, false, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
@@ -628,6 +674,29 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
   }
 }
 
+template <int DK, int PL, int NB>
+__global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
+    k_gdr_scan_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  const Work w = work_of(a, 0);
+  scan_tile<DK, PL, NB>(a, maps, &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+}
+
+template <int DK, int PL>
+__global__ void __launch_bounds__(TcCfg<DK, PL, 2, false>::THREADS, 1)
+    k_gdr_scan_mixed_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  const Work w = work_of(a, TcCfg<DK, PL, 2, false>::NV);
+  if (w.tile < 0) return;
+  if (w.half) {
+    // (kept in tiles of 64 columns: two of 32 fill one)
+    if (PL == 2 || w.tile * 64 < a.s.dv)
+      scan_tile<DK, PL, 1>(a, maps, PL == 2 ? &maps.go : &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+  } else {
+    scan_tile<DK, PL, 2>(a, maps, &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+  }
+}
+
 // ------------------------------------------------------------------ backward
 // Last chunk first, the state gradient dS in registers:
 //   D1 = [K; .] dS1               X = exp(G_C - G) D1
@@ -636,24 +705,17 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, NB, false>::THREADS, 1)
 // The warps on lanes 64-127 scale dO for D3 meanwhile; its Q^T part runs under
 // the wait for D1.
 template <int DK, int NB>
-__global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
-    k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
+__device__ __forceinline__ void scan_bwd_tile(const TcArgs& a, const Maps& maps, unsigned char* smem_raw, int n, int h,
+                                              int tile, long long start, int len) {
   using C = TcCfg<DK, 1, NB, true>;
   constexpr int PL = 1, NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;
-  extern __shared__ unsigned char smem_raw[];
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(base + 128);
   unsigned char* stage = base + 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tile = blockIdx.x % a.ntile;
-  const int h = (int)(blockIdx.x / a.ntile % a.s.hv), at_n = (int)(blockIdx.x / a.ntile / a.s.hv);
-  const int n = nth(a, at_n);
   const long long sh = (long long)n * a.s.hv + h;
-  long long start;
-  int len;
-  seq_range(a.s, n, &start, &len);
   const int nc = (len + kC - 1) / kC;
   const long long slot0 = slot_base(start, n);
   if (tid == 0) {
@@ -688,7 +750,7 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
   };
 
   if (tid >= C::WORK) {
-    fetch_chunks<DK, C>(a, maps, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
+    fetch_chunks<DK, C>(a, maps, &maps.v, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
                                     tile * NV, true, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
@@ -874,6 +936,27 @@ __global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
   }
 }
 
+template <int DK, int NB>
+__global__ void __launch_bounds__(TcCfg<DK, 1, NB, true>::THREADS, 1)
+    k_gdr_scan_bwd_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  const Work w = work_of(a, 0);
+  scan_bwd_tile<DK, NB>(a, maps, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+}
+
+template <int DK>
+__global__ void __launch_bounds__(TcCfg<DK, 1, 2, true>::THREADS, 1)
+    k_gdr_scan_bwd_mixed_tc(TcArgs a, const __grid_constant__ Maps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  const Work w = work_of(a, TcCfg<DK, 1, 2, true>::NV);
+  if (w.tile < 0) return;
+  if (w.half) {
+    if (w.tile * 64 < a.s.dv) scan_bwd_tile<DK, 1>(a, maps, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+  } else {
+    scan_bwd_tile<DK, 2>(a, maps, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+  }
+}
+
 // ------------------------------------------------------------------- launches
 bool tile_map(CUtensorMap* m, const void* base, int width, int heads, long long rows, long long ld, int box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -916,6 +999,41 @@ static cudaError_t scan(TcArgs a, cudaStream_t st) {
   k_gdr_scan_tc<DK, PL, NB><<<(unsigned)((long long)a.s.n_seq * a.s.hv * a.ntile), C::THREADS, C::BYTES, st>>>(a, m);
   return cudaGetLastError();
 }
+// How many sequences can be so much longer than an even share.
+static void allow_half(TcArgs* a, int wide) {
+  a->ntile = (a->s.dv + wide - 1) / wide;
+  const int most = kNumSMs * 4 / (5 * a->s.hv * a->ntile) + 1;
+  a->twice = a->s.n_seq < most ? a->s.n_seq : most;
+}
+static unsigned mixed_blocks(const TcArgs& a) {
+  return (unsigned)((long long)(a.s.n_seq + a.twice) * a.s.hv * a.ntile);
+}
+template <int DK, int PL>
+static cudaError_t scan_mixed(TcArgs a, cudaStream_t st) {
+  using W = TcCfg<DK, PL, 2, false>;
+  static_assert(W::BYTES >= TcCfg<DK, PL, 1, false>::BYTES && W::THREADS == TcCfg<DK, PL, 1, false>::THREADS, "both fit");
+  allow_half(&a, W::NV);
+  const cudaError_t e = allow_smem<k_gdr_scan_mixed_tc<DK, PL>>(W::BYTES);
+  if (e != cudaSuccess) return e;
+  Maps m;
+  a.tma = maps_of(a, 64, &m) && (PL == 1 || tile_map(&m.go, a.v, a.s.dv, a.s.hv, a.s.rows, a.ldv, 32));
+  TraceScope tr("k_gdr_scan_tc", st);
+  k_gdr_scan_mixed_tc<DK, PL><<<mixed_blocks(a), W::THREADS, W::BYTES, st>>>(a, m);
+  return cudaGetLastError();
+}
+template <int DK>
+static cudaError_t scan_bwd_mixed(TcArgs a, cudaStream_t st) {
+  using W = TcCfg<DK, 1, 2, true>;
+  static_assert(W::BYTES >= TcCfg<DK, 1, 1, true>::BYTES && W::THREADS == TcCfg<DK, 1, 1, true>::THREADS, "both fit");
+  allow_half(&a, W::NV);
+  const cudaError_t e = allow_smem<k_gdr_scan_bwd_mixed_tc<DK>>(W::BYTES);
+  if (e != cudaSuccess) return e;
+  Maps m;
+  a.tma = maps_of(a, 64, &m);
+  TraceScope tr("k_gdr_scan_bwd_tc", st);
+  k_gdr_scan_bwd_mixed_tc<DK><<<mixed_blocks(a), W::THREADS, W::BYTES, st>>>(a, m);
+  return cudaGetLastError();
+}
 template <int DK, int NB>
 static cudaError_t scan_bwd(TcArgs a, cudaStream_t st) {
   using C = TcCfg<DK, 1, NB, true>;
@@ -951,12 +1069,17 @@ cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream
 template <int DK>
 static cudaError_t scan_by_size(const TcArgs& t, int planes, cudaStream_t st) {
   const long long heads = (long long)t.s.n_seq * t.s.hv;
-  if (planes == 2) return wide_tiles(heads, t.s.dv, 32) ? scan<DK, 2, 2>(t, st) : scan<DK, 2, 1>(t, st);
-  return wide_tiles(heads, t.s.dv, 64) ? scan<DK, 1, 2>(t, st) : scan<DK, 1, 1>(t, st);
+  if (planes == 2) {
+    if (!wide_tiles(heads, t.s.dv, 32)) return scan<DK, 2, 1>(t, st);
+    return t.order ? scan_mixed<DK, 2>(t, st) : scan<DK, 2, 2>(t, st);
+  }
+  if (!wide_tiles(heads, t.s.dv, 64)) return scan<DK, 1, 1>(t, st);
+  return t.order ? scan_mixed<DK, 1>(t, st) : scan<DK, 1, 2>(t, st);
 }
 template <int DK>
 static cudaError_t scan_bwd_by_size(const TcArgs& t, cudaStream_t st) {
-  return wide_tiles((long long)t.s.n_seq * t.s.hv, t.s.dv, 64) ? scan_bwd<DK, 2>(t, st) : scan_bwd<DK, 1>(t, st);
+  if (!wide_tiles((long long)t.s.n_seq * t.s.hv, t.s.dv, 64)) return scan_bwd<DK, 1>(t, st);
+  return t.order ? scan_bwd_mixed<DK>(t, st) : scan_bwd<DK, 2>(t, st);
 }
 
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st) {

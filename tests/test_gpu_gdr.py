@@ -626,3 +626,14 @@ def test_bits_depend_neither_on_the_run_nor_on_what_the_workspace_held(shape):
             c.check({"o": o.cpu().double()}, c.oracle(), ("o",))
         for a, b in zip(first, [o] + grads):
             assert torch.equal(a, b), run
+
+
+@pytest.mark.parametrize("dv", [96, 128])
+def test_one_long_sequence_among_many_heads(dv):
+    """Far longer than an even share: it takes tiles of half the width, beside others of the whole."""
+    c = Case([3, 700, 0, 64, 10], 12, 24, 32, dv, BF16, seed=44, init=True)
+    ref = c.oracle()
+    c.check(c.forward(), ref, ("o", "final_state"))
+    for final in (False, True):
+        c.check(c.forward(final=final, save=True), ref, ("o", "final_state") if final else ("o",))
+        c.check(c.backward(), c.oracle_back(), GRADS + ("grad_initial_state",), f"final state {final}: ")
