@@ -112,10 +112,9 @@ bool make_layout(int B, int K, int n_in, int n_hid, int math, int grad_path, Lay
   return true;
 }
 
-// Limits of the gated delta rule and the norm (32-bit block and row counts).
+// Limits of the gated delta rule (32-bit block and row counts).
 constexpr long long kMaxGdrRows = 1ll << 30;
 constexpr int kMaxGdrSeqs = 1 << 20;
-constexpr int kMaxRmsWidth = 32768;
 
 static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "../../include/cfc.h"
 
 namespace cfc {
@@ -237,6 +239,21 @@ int tc_wgrad_blocks(int n_in, int n_hid);
 // tensor-core kernels; blocks until the device is idle.
 int read_device_error(int clear);
 
+// Shared memory beyond the default 48 KB, static and dynamic together, asked for
+// once a kernel and device: the call takes as long as a launch.  `bytes`: the most
+// dynamic memory that any launch of the kernel asks for.
+template <auto KERNEL>
+static cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> devices{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e != cudaSuccess || (devices.load(std::memory_order_relaxed) & bit)) return e;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Gated delta rule over whole sequences (cfc_gdr.cu, cfc_gdr_bwd.cu) and for
 // the next tokens (cfc_gdr_step.cu); sizes and pointers already checked.
 struct GdrArgs {
@@ -279,6 +296,7 @@ cudaError_t launch_gdr_backward(const GdrArgs& g, const GdrGrads& r, cudaStream_
 cudaError_t launch_gdr_step(const GdrStepArgs& g, cudaStream_t s);
 
 // Residual RMS norm (cfc_rmsnorm.cu).
+constexpr int kMaxRmsWidth = 32768;
 size_t rmsnorm_workspace(long long rows, int d);
 cudaError_t launch_rmsnorm_forward(const void* x, const void* residual, const float* w, long long rows, int d, float eps,
                                    int math, void* y, void* residual_out, float* rstd, uint8_t* y8, float* y8_scale,

@@ -544,10 +544,8 @@ static cudaError_t backward(const Args& a, float* grad_w, cudaStream_t st) {
   else e = by_row<Vec<E, 1>, true>(a.d, 0, Bwd{a, &blocks, st});
   if (e == cudaErrorNotSupported) {
     const size_t bytes = (size_t)a.d * 4;
-    if (bytes > 48 * 1024) {
-      e = cudaFuncSetAttribute(k_rmsnorm_bwd_any<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-      if (e != cudaSuccess) return e;
-    }
+    e = allow_smem<k_rmsnorm_bwd_any<E>>(kMaxRmsWidth * sizeof(float));
+    if (e != cudaSuccess) return e;
     blocks = (int)(a.rows < kMaxBlocks ? a.rows : kMaxBlocks);
     TraceScope tr("k_rmsnorm_bwd_any", st);
     k_rmsnorm_bwd_any<E><<<blocks, kAnyThreads, bytes, st>>>(a);

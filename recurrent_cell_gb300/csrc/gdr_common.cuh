@@ -22,8 +22,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "cfc_internal.cuh"
 #include "tc_common.cuh"
 
@@ -106,21 +104,6 @@ __device__ __forceinline__ bool slot_chunk(const Shape& s, long long slot, int* 
   *n_out = lo;
   *c = (int)d;
   return d >= 0 && d * kC < *len;
-}
-
-// ------------------------------------------------------------ launches
-// Shared memory beyond 48 KB, asked for once a kernel and device: the call
-// takes as long as a launch.
-template <auto KERNEL>
-static cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> devices{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (e != cudaSuccess || (devices.load(std::memory_order_relaxed) & bit)) return e;
-  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 // ------------------------------------------------------------ async copies

@@ -11,6 +11,10 @@ difference of two terms: 1e-5 of them in fp32, 2^-8 of itself on top in
 bf16.  grad_weight: fp32 sums over rows: 1e-5 of the sum of absolute values.
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -295,3 +299,17 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(cfc.CfcError):
         cfc.cfc_rmsnorm_backward(x, w, torch.ones(4, device="cuda"), y, y, torch.empty(64, device="cuda"),
                                  torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_widths_at_the_default_limit_of_shared_memory_in_a_fresh_process():
+    """Rows that the element-wise backward takes, whose sums just fill 48 KB beside its own few words: in a
+    process that has asked for no more yet."""
+    code = ("import test_gpu_rmsnorm as t\n"
+            "for d in (12256, 12257, 12264, 12280, 12288, 12289):\n"
+            "    for math in (t.FP32, t.BF16):\n"
+            "        t.test_forward_and_backward(d, math)\n")
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.pathsep.join([here, os.path.dirname(here)])
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(here), env={**os.environ, "PYTHONPATH": path},
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
