@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
   __syncthreads();
   float4* pout = reinterpret_cast<float4*>(a.p) + id * (kC * kLdT / 4);
   for (int i = tid; i < kC * kLdT / 4; i += 128) pout[i] = reinterpret_cast<const float4*>(ps)[i];
-  invert<kLdT, true>(am, warp, lane);
+  invert<kLdT>(am, warp, lane);
   float4* tout = reinterpret_cast<float4*>(a.t) + id * (kC * kLdT / 4);
   for (int i = tid; i < kC * kC / 4; i += 128) {
     const int r = i / (kC / 4), col = (i % (kC / 4)) * 4;

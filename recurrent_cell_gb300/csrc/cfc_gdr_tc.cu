@@ -37,9 +37,10 @@ __device__ int g_gdr_tc_error = 0;
 // (a warp each, a column a lane), then pairs of blocks joined by
 // T21 = -T22 A21 T11, all in fp32 or fp32-accurate products: T's entries reach
 // far above A's when keys repeat.  P T = P + P (T - I) takes P from the
-// registers that q k^T left it in; PL = 2 takes both operands in two bf16 planes.
-// PL = 1 (T is rounded to bf16 whatever it was): products of one TF32 or bf16
-// pass, 75 -> 63 us for 4096 chunks and heads, o's error 3.0e-3 -> 3.1e-3.
+// registers that q k^T left it in and T - I, both as two bf16 planes; PL = 1 only
+// rounds the results.  One pass of TF32 and bf16 products there takes 62 us instead
+// of 74 for 4096 chunks and heads, but where keys repeat the terms cancel after their
+// rounding: o of a chunk of equal keys 1.5e-2 from exact instead of 2.5e-3.
 template <int DK>
 struct PrepTc {
   static constexpr int LDK = DK + 8, LDA = kC + 4;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
     *reinterpret_cast<float2*>(am + (m0 + g + 8) * S::LDA + col) = make_float2(av[2], av[3]);
   }
   __syncwarp();
-  invert<S::LDA, PL == 2>(am, warp, lane);
+  invert<S::LDA>(am, warp, lane);
   // T - I into the image, both planes
 #pragma unroll
   for (int e = 0; e < kC * 8 / 128; ++e) {
@@ -188,13 +189,11 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
     }
     const uint4 hi = pack8(v);
     *reinterpret_cast<uint4*>(img + chunk_at(r, ch)) = hi;
-    if constexpr (PL == 2) {
-      float hv[8];
-      unpack8(hv, hi);
+    float hv[8];
+    unpack8(hv, hi);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) hv[x] = v[x] - hv[x];
-      *reinterpret_cast<uint4*>(img + 8192 + chunk_at(r, ch)) = pack8(hv);
-    }
+    for (int x = 0; x < 8; ++x) hv[x] = v[x] - hv[x];
+    *reinterpret_cast<uint4*>(img + 8192 + chunk_at(r, ch)) = pack8(hv);
   }
   __syncthreads();
   // P T, 16 rows a warp
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
     for (int x = 0; x < 4; ++x) {
       const float* p = pr[2 * kb + (x >> 1)] + (x & 1) * 2;
       ah[x] = pack2(p[0], p[1]);
-      if constexpr (PL == 2) al[x] = pack2(p[0] - lo_f(ah[x]), p[1] - hi_f(ah[x]));
+      al[x] = pack2(p[0] - lo_f(ah[x]), p[1] - hi_f(ah[x]));
     }
     const int r = kb * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
@@ -220,13 +219,11 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
       P::B bh, bl;
       const unsigned char* src = img + chunk_at(r, jb * 2 + (lane >> 4));
       P::ldmt(bh, src);
-      if constexpr (PL == 2) P::ldmt(bl, src + 8192);
+      P::ldmt(bl, src + 8192);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        if constexpr (PL == 2) {
-          P::mma(d[2 * jb + hf], al, bh, hf);
-          P::mma(d[2 * jb + hf], ah, bl, hf);
-        }
+        P::mma(d[2 * jb + hf], al, bh, hf);
+        P::mma(d[2 * jb + hf], ah, bl, hf);
         P::mma(d[2 * jb + hf], ah, bh, hf);
       }
     }

@@ -407,9 +407,10 @@ __device__ __forceinline__ void chunk_decays(const float4& gb, int lane, bool fr
 
 // T = (I + A)^{-1} in place of A, 64 x 64 and strictly lower triangular in fp32
 // with rows of LDA, by a block of 4 warps of which warp w wrote rows 16 w ..;
-// ends with a block barrier.  The blocks off the diagonal come of products, FINE:
-// of fp32 accuracy; else of TF32's, 2^-12, for a T that is rounded to 2^-9.
-template <int LDA, bool FINE>
+// ends with a block barrier.  The blocks off the diagonal come of fp32-accurate
+// products, also where T is rounded to bf16 afterwards: an error of A21 T11 is
+// multiplied by T22, whose rows have sums far above 1 where keys repeat.
+template <int LDA>
 __device__ __forceinline__ void invert(float* am, int warp, int lane) {
   const int m0 = warp * 16, g = lane >> 2, t2 = (lane & 3) * 2;
   // Diagonal blocks.
@@ -449,13 +450,8 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
         MFp32::B xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
-        if constexpr (FINE) {
-          MFp32::mma(d[0], e[0], xa, xb, 0);
-          MFp32::mma(d[1], e[1], xa, xb, 1);
-        } else {
-          MFp32::mma1(d[0], xa.h, xb.h[0], xb.h[1]);
-          MFp32::mma1(d[1], xa.h, xb.h[2], xb.h[3]);
-        }
+        MFp32::mma(d[0], e[0], xa, xb, 0);
+        MFp32::mma(d[1], e[1], xa, xb, 1);
       }
       __syncwarp();
       const float sg = pass == 0 ? 1.f : -1.f;
@@ -484,13 +480,8 @@ __device__ __forceinline__ void invert(float* am, int warp, int lane) {
         MFp32::B xb;
         MFp32::load_a(xa, ma, 0, k0, lane);
         MFp32::load_bk(xb, mb, 0, k0, lane);
-        if constexpr (FINE) {
-          MFp32::mma(d[0], e[0], xa, xb, 0);
-          MFp32::mma(d[1], e[1], xa, xb, 1);
-        } else {
-          MFp32::mma1(d[0], xa.h, xb.h[0], xb.h[1]);
-          MFp32::mma1(d[1], xa.h, xb.h[2], xb.h[3]);
-        }
+        MFp32::mma(d[0], e[0], xa, xb, 0);
+        MFp32::mma(d[1], e[1], xa, xb, 1);
       }
       __syncthreads();
       const float sg = pass == 0 ? 1.f : -1.f;

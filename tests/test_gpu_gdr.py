@@ -637,3 +637,27 @@ def test_one_long_sequence_among_many_heads(dv):
     for final in (False, True):
         c.check(c.forward(final=final, save=True), ref, ("o", "final_state") if final else ("o",))
         c.check(c.backward(), c.oracle_back(), GRADS + ("grad_initial_state",), f"final state {final}: ")
+
+
+@pytest.mark.parametrize("beta,decay", [(1.0, 0.0), (1.9, 0.0), (1.9, 0.2), (2.0, 0.0)])
+def test_repeated_and_opposite_keys_in_training(beta, decay):
+    """One chunk from the zero state, no final state asked for.  T's entries reach 2 and its rows
+    nearly cancel, so T has to be exact before it is rounded, and P T formed from
+    more than bf16's bits: then o has the roundings of P T, R and its own, and grad_v, grad_k no more than
+    elsewhere.  dq and dbeta go by S^T k, a sum of 64 updates that nearly cancel: ten times the allowance, as
+    above.  dg is a difference of the terms in the last line, and is 0 where each token replaces the one before."""
+    c = Case([64, 40, 64, 17], 1, 2, 64, 32, BF16, seed=45, decay=decay)
+    key = np.zeros(64)
+    key[3], key[40] = 0.5, np.sqrt(0.75)
+    c.k = c.rounded(np.where(np.arange(c.rows)[:, None, None] % 3 == 2, -key, key))
+    c.beta[:] = beta
+    got, ref = c.forward(final=False, save=True), c.oracle()
+    close(got["o"], ref["o"], tolerance("o", BF16), "o")
+    got, ref = c.backward(), c.oracle_back()
+    for n in ("grad_v", "grad_k"):
+        close(got[n], ref[n], tolerance(n, BF16), n)
+    for n in ("grad_q", "grad_beta"):
+        close(got[n], ref[n], 10 * tolerance(n, BF16), n)
+    x = c.host()
+    terms = np.abs(x[0] * ref["grad_q"]).sum(-1) + np.abs(x[1] * ref["grad_k"]).sum(-1)
+    assert np.abs(got["grad_g"] - ref["grad_g"]).max() <= 10 * tolerance("grad_g", BF16) * terms.max()
