@@ -9,9 +9,10 @@ to queries, keys, values and gates, runs the rule and projects back:
 
 The stream after the last norm is the cell's input.  The plain matrix products
 and the elementwise gates are torch's; the rest are this library's calls, as
-autograd functions.  A sequence's whole state is one [v_heads, d_k, d_v] matrix a
-block and the cell's hidden vector, so decoding takes a fixed amount of memory
-however long the sequence is.
+autograd functions (first derivatives: the gradient of a gradient is an error).
+A sequence's whole state is one [v_heads, d_k, d_v] matrix a block and the cell's
+hidden vector, so decoding takes a fixed amount of memory however long the
+sequence is.
 
     python -m recurrent_cell_gb300.memory        (trains on recall, then decodes)
 """
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 from . import (GRAD_GEMM, MATH_BF16, MATH_FP32, cfc_gdr_backward, cfc_gdr_forward, cfc_gdr_step,
                cfc_gdr_workspace_bytes, cfc_kloop_backward, cfc_kloop_forward, cfc_kloop_workspace_bytes,
@@ -50,6 +52,7 @@ class _Norm(torch.autograd.Function):
         return y, s
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y, grad_s):
         s, weight, rstd = ctx.saved_tensors
         grad_x, grad_w = torch.empty_like(s), torch.empty_like(weight)
@@ -83,6 +86,7 @@ class _Rule(torch.autograd.Function):
         return o, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_o, grad_state):
         q, k, v, g, beta, seq_offsets, initial = ctx.saved_tensors
         like = lambda t: torch.empty(t.shape, dtype=q.dtype, device=q.device)  # noqa: E731
@@ -115,6 +119,7 @@ class _Cell(torch.autograd.Function):
         return h_seq
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_h):
         x, h0, W_in, W_rec, b, dt, h_seq = ctx.saved_tensors
         f32 = lambda t: torch.empty(t.shape, device=t.device)  # noqa: E731

@@ -113,3 +113,22 @@ def test_it_learns_to_recall():
     _, losses = train_recall(steps=300)
     assert np.isfinite(losses).all()
     assert np.mean(losses[-20:]) < 0.125, losses[::20]
+
+
+def test_second_derivatives_are_refused():
+    """The gradients are kernels' results, not differentiable themselves: asking for their gradient is an
+    error, also where other operations lie on the path and would give a part of it."""
+    torch = torch_mod()
+    from recurrent_cell_gb300.memory import MemoryBlock, MemoryCell, gated_delta_rule, residual_norm
+    torch.manual_seed(3)
+    leaf = lambda *s: torch.randn(*s, device="cuda").requires_grad_()  # noqa: E731
+    block, cell = MemoryBlock(32, 1, 2, 16, 16, torch.float32), MemoryCell(32, 16, dtype=torch.float32)
+    x, rows, q = leaf(2, 5, 32), leaf(6, 32), leaf(1, 5, 1, 16)
+    g, beta = -torch.rand(1, 5, 1, device="cuda"), torch.rand(1, 5, 1, device="cuda")
+    for name, at, out in (("norm", rows, residual_norm(2 * rows, block.norm.detach())[0]),
+                          ("rule", q, gated_delta_rule(q.square(), q, q, g, beta)[0]),
+                          ("block", x, block(x, None)[0]), ("cell", x, cell(x))):
+        (grad,) = torch.autograd.grad(out.square().sum(), at, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            grad.square().sum().backward()
+            pytest.fail(f"{name}: a second derivative came out")
