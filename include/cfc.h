@@ -305,7 +305,12 @@ int cfc_grn_backward(const float* h, int B, int K, int hidden, int head_mid, int
  * take bf16 operands and sum in fp32; the running state is fp32, and where a
  * final_state is asked for, every operand on the way to it keeps 17
  * significant bits, so that the state is good to about 1e-5 (o and the
- * gradients, which leave in bf16, to their own rounding). */
+ * gradients, which leave in bf16, to their own rounding).
+ *
+ * A NaN or an infinity at a token reaches o of that token and, through the
+ * state, of its sequence's later ones, as in the recurrence; no earlier token, no
+ * other sequence or head, and from v no other column.  The gradients of a
+ * sequence and head in which anything is not finite are not specified. */
 
 /* Device workspace of the two calls (save != 0: of a forward that a backward
  * follows, and of that backward).  Host-only; 0 for unsupported sizes. */

@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
       }
     }
   }
-  if (warp == 0) chunk_decays(gb, lane, c == 0 && !a.init, g2, bet, a.vec + id * kVec);   // the warp with the fewest products
+  float* vec = a.vec + id * kVec;
+  if (warp == 0) chunk_decays(gb, lane, c == 0 && !a.init, g2, bet, vec);   // the warp with the fewest products
   __syncthreads();
 #pragma unroll
   for (int rr = 0; rr < 2; ++rr) {
@@ -91,8 +92,12 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
       const float l0 = exp2f((gi.x - gj.x) + (gi.y - gj.y)), l1 = exp2f((gi.x - gj.z) + (gi.y - gj.w));
       *reinterpret_cast<float2*>(ps + i * kLdT + col) =
           make_float2(col <= i ? a.s.scale * l0 * aq[j][rr * 2] : 0.f, col < i ? a.s.scale * l1 * aq[j][rr * 2 + 1] : 0.f);
-      *reinterpret_cast<float2*>(am + i * kLdT + col) =
-          make_float2(col < i ? be * l0 * ak[j][rr * 2] : 0.f, col + 1 < i ? be * l1 * ak[j][rr * 2 + 1] : 0.f);
+      float a0 = col < i ? be * l0 * ak[j][rr * 2] : 0.f, a1 = col + 1 < i ? be * l1 * ak[j][rr * 2 + 1] : 0.f;
+      if (!finite(fabsf(a0) + fabsf(a1))) {
+        drop(a0, vec, i);
+        drop(a1, vec, i);
+      }
+      *reinterpret_cast<float2*>(am + i * kLdT + col) = make_float2(a0, a1);
     }
   }
   __syncthreads();
@@ -103,6 +108,12 @@ __global__ void __launch_bounds__(128) k_gdr_prep(FwdArgs a) {
   for (int i = tid; i < kC * kC / 4; i += 128) {
     const int r = i / (kC / 4), col = (i % (kC / 4)) * 4;
     float4 v = *reinterpret_cast<const float4*>(am + r * kLdT + col);
+    if (!finite(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w))) {
+      drop(v.x, vec, r);
+      drop(v.y, vec, r);
+      drop(v.z, vec, r);
+      drop(v.w, vec, r);
+    }
     if (r == col) v.x = 0.f;            // T - I: the products add R itself
     if (r == col + 1) v.y = 0.f;
     if (r == col + 2) v.z = 0.f;
@@ -124,7 +135,8 @@ struct ScanCfg {
   static constexpr int kQ = kC * LDK, kT = kC * kLdT, kV = kC * LDV;
   static constexpr int STAGE = 2 * kQ + 2 * kT + kV + kVec;
   static constexpr int SOP = DVT * LDK, ROP = DVT * kLdT;
-  static constexpr size_t BYTES = (STAGE + SOP + 3 * ROP + kV) * sizeof(float) + 64;
+  static constexpr size_t HEAD = 64 + 4 * DVT;        // barriers; each column's first bad token
+  static constexpr size_t BYTES = (STAGE + SOP + 3 * ROP + kV) * sizeof(float) + HEAD;
   static_assert(BYTES <= 227u * 1024u, "shared memory");
 };
 
@@ -134,7 +146,8 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
   using C = ScanCfg<DK, WM>;
   constexpr int NTS = C::NTS;
   uint64_t *full = reinterpret_cast<uint64_t*>(smem_raw), *empty = full + 1;
-  float* stage = reinterpret_cast<float*>(smem_raw + 64);
+  int *any_bad = reinterpret_cast<int*>(smem_raw + 32), *bad_from = reinterpret_cast<int*>(smem_raw + 64);
+  float* stage = reinterpret_cast<float*>(smem_raw + C::HEAD);
   float* x = stage + 2 * C::kQ + C::kV;               // T - I, P, the vectors
   const float *vs = stage + 2 * C::kQ, *vec = x + 2 * C::kT;
   float* ops = stage + C::STAGE;
@@ -234,6 +247,7 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
       }
       // R of this warp's 16 tokens
       float ar[2][4] = {}, al[2][4] = {}, au[2][4], aw[2][4] = {};
+      bool bad = false;
 #pragma unroll
       for (int k0 = 0; k0 < DK; k0 += F::KS) {
         F::A fa;
@@ -254,9 +268,30 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
           au[hf][2 * rr] = be.x * (vs[i * C::LDV + r] - eg.x * (ar[hf][2 * rr] + al[hf][2 * rr]));
           au[hf][2 * rr + 1] = be.y * (vs[(i + 1) * C::LDV + r] - eg.y * (ar[hf][2 * rr + 1] + al[hf][2 * rr + 1]));
           F::put2(rop, r, i, au[hf][2 * rr], au[hf][2 * rr + 1]);
+          bad |= !finite(fabsf(au[hf][2 * rr]) + fabsf(au[hf][2 * rr + 1]));
         }
       }
-      group_sync<2, C::CHAIN>();
+      // From a bad value of a column on its R reads as zero and its U is NaN.
+      const bool some = group_any<2, C::CHAIN>(bad);
+      if (tid == 0) *any_bad = some;
+      if (some) {
+        for (int r = tid; r < C::DVT; r += C::CHAIN) bad_from[r] = kC;
+        group_sync<2, C::CHAIN>();
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (!finite(au[x >> 2][x & 3]))
+            atomicMin(bad_from + m0 + g + ((x >> 1) & 1) * 8, i0 + (x >> 2) * 8 + (x & 1));
+        group_sync<2, C::CHAIN>();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int r = m0 + g + ((x >> 1) & 1) * 8, i = i0 + (x >> 2) * 8 + (x & 1);
+          if (i >= bad_from[r]) {
+            au[x >> 2][x & 3] = nanf("");
+            rop.p[r * kLdT + i] = 0.f;
+          }
+        }
+        group_sync<2, C::CHAIN>();
+      }
       // U = R + (T - I) R
 #pragma unroll
       for (int k0 = 0; k0 < kC; k0 += F::KS) {
@@ -281,7 +316,8 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
             p[0] = u0;
             p[dv] = u1;
           }
-          F::put2(uop, r, i, u0, u1);
+          const bool from = some && i + 1 >= bad_from[r];      // for the outputs alone: the state takes them as they are
+          F::put2(uop, r, i, from && i >= bad_from[r] ? 0.f : u0, from ? 0.f : u1);
           F::put2(ukop, r, i, el.x * u0, el.y * u1);
         }
       }
@@ -335,6 +371,10 @@ __global__ void __launch_bounds__(ScanCfg<DK, WM>::THREADS) k_gdr_scan(FwdArgs a
         F::mma(ao[0], fa, fb, 0);
         F::mma(ao[1], fa, fb, 1);
       }
+      if (*any_bad)
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (i0 + (x >> 2) * 8 + (x & 1) >= bad_from[m0 + g + ((x >> 1) & 1) * 8]) ao[x >> 2][x & 3] = nanf("");
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll

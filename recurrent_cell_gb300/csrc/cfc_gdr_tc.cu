@@ -17,6 +17,12 @@
 // planes, 17 significant bits.  The planes lie side by side in the operand's
 // 64 NB columns, NV = 64 NB / PL, one product for both.
 //
+// A NaN or an infinity reaches no earlier token although D2 multiplies it by zeros
+// for them: its place in R is zero, its U is NaN (and so the state), and the fetching
+// warps, which copy the outputs, write NaN from there on.  The preparation finds bad k, g
+// and beta, the pass itself bad V.  Looking for them takes 2 us of 78 and 8 of 410
+// (16384 tokens x 16 heads); joining a vote to a barrier of the chain took 26.
+//
 // What bounds a pass over few heads is the length of that chain: 1.6 us a chunk
 // of 32 columns with PL = 2 (16384 tokens x 16 heads 412 us; 40 us by bytes),
 // of which the products, bound by their operands' reads of shared memory, are
@@ -150,7 +156,9 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
   }
   if (warp == 0) chunk_decays(gb, lane, c == 0 && !a.init, g2, bet, vec);   // the warp with the fewest products
   __syncthreads();
-  // P in the registers, A in shared memory
+  // P in the registers, A in shared memory.  (The first row has no entries in A: its |k|^2, not a number or infinite
+  // as soon as one of k is, and its g speak for it.)
+  float sum = tid == 0 ? fabsf(ak[0][0]) + fabsf(g2[0].x) : 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int col = j * 8 + t2;
@@ -168,13 +176,23 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
         pr[j][2 * rr] = col <= i ? a.s.scale * l0 * pr[j][2 * rr] : 0.f;
         pr[j][2 * rr + 1] = col < i ? a.s.scale * l1 * pr[j][2 * rr + 1] : 0.f;
       }
+      sum += fabsf(av[0]) + fabsf(av[1]) + fabsf(av[2]) + fabsf(av[3]);
     }
     *reinterpret_cast<float2*>(am + (m0 + g) * S::LDA + col) = make_float2(av[0], av[1]);
     *reinterpret_cast<float2*>(am + (m0 + g + 8) * S::LDA + col) = make_float2(av[2], av[3]);
   }
+  if (!finite(sum)) {
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x) {
+      const int row = m0 + g + (x & 1) * 8;
+      drop(am[row * S::LDA + (x >> 2) * 8 + t2 + ((x >> 1) & 1)], vec, row);
+    }
+    if (tid == 0 && !(finite(ak[0][0]) && finite(g2[0].x))) vec[kVecBeta] = nanf("");
+  }
   __syncwarp();
   invert<S::LDA>(am, warp, lane);
   // T - I into the image, both planes
+  __nv_bfloat162 z = __float2bfloat162_rn(0.f);
 #pragma unroll
   for (int e = 0; e < kC * 8 / 128; ++e) {
     const int r = (e * 128 + tid) >> 3, ch = tid & 7;
@@ -189,11 +207,22 @@ __global__ void __launch_bounds__(128, 5) k_gdr_prep_tc(FwdArgs a) {
     }
     const uint4 hi = pack8(v);
     *reinterpret_cast<uint4*>(img + chunk_at(r, ch)) = hi;
+    z = times_zero(hi, z);
     float hv[8];
     unpack8(hv, hi);
 #pragma unroll
     for (int x = 0; x < 8; ++x) hv[x] = v[x] - hv[x];
     *reinterpret_cast<uint4*>(img + 8192 + chunk_at(r, ch)) = pack8(hv);
+  }
+  if (!zeros(z)) {                       // T has overflowed: as for A
+#pragma unroll 1
+    for (int e = 0; e < kC * 8 * 8 / 128; ++e) {
+      const int r = ((e >> 3) * 128 + tid) >> 3;
+      bf16* p = reinterpret_cast<bf16*>(img + chunk_at(r, tid & 7)) + (e & 7);
+      if (finite(__bfloat162float(*p))) continue;
+      *p = p[4096] = __float2bfloat16_rn(0.f);
+      vec[kVecBeta + r] = nanf("");
+    }
   }
   __syncthreads();
   // P T, 16 rows a warp
@@ -265,7 +294,9 @@ struct TcCfg {
   static constexpr uint32_t STAGE = (KQ + A2 + VT + kVec * 4 + 1023) / 1024 * 1024;
   // S; R, then its decayed U; U as it is (PL = 1); backward: dO scaled.  NB blocks each.
   static constexpr uint32_t SB = DK * 128u, RB = 8192u, S = NB * SB, R = NB * RB;
-  static constexpr uint32_t BYTES = 2048 + 2 * STAGE + S + (PL == 1 ? 2 : 1) * R + (BWD ? R : 0);
+  // forward, for each stage: each column's first bad token, and whether there is one
+  static constexpr uint32_t BAD = BWD ? 0 : 2 * (NV + 1) * 4;
+  static constexpr uint32_t BYTES = 2048 + 2 * STAGE + S + (PL == 1 ? 2 : 1) * R + (BWD ? R : 0) + BAD;
   static constexpr uint32_t TMEM = NB * 128;            // D1 / D2 and D3
   static_assert(BYTES <= 227u * 1024u, "shared memory");
 };
@@ -355,7 +386,7 @@ template <int DK, class C, class W>
 __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, const CUtensorMap* v_map,
                                              unsigned char* stage, uint64_t* full,
                                              uint64_t* empty, uint64_t* outs, int ft, int h, long long start, int len,
-                                             long long slot0, int v0, bool backwards, W wait) {
+                                             long long slot0, int v0, bool backwards, int* bad_from, W wait) {
   constexpr int NV = C::NV;
   const int hq = h / (a.s.hv / a.s.hk), dk = a.s.dk, nc = (len + kC - 1) / kC;
   const bf16* q = a.q + start * a.ldq + (long long)hq * dk;
@@ -370,6 +401,17 @@ __device__ __forceinline__ void fetch_chunks(const TcArgs& a, const Maps& maps, 
       const int cl = backwards ? c + 2 : c - 2;
       bf16* o = a.o + (start + (long long)cl * kC) * ldo + (long long)h * a.s.dv + v0;
       wait(outs + st, (i / 2 - 1) & 1);
+      if (bad_from && bad_from[st * (NV + 1) + NV]) {      // outputs from a bad token on
+        int* from = bad_from + st * (NV + 1);
+        group_sync<15, C::FETCH>();
+        for (int x = ft; x < NV; x += C::FETCH) {
+          for (int r = from[x]; r < kC; ++r)
+            reinterpret_cast<unsigned short*>(b + C::KQ + C::A2 + v_at<NV>(r, x / 8))[x % 8] = 0x7fff;
+          from[x] = kC;
+        }
+        if (ft == 0) from[NV] = 0;
+        group_sync<15, C::FETCH>();
+      }
       // 4 warps: 32 rows by half of the columns each
       const int w = ft >> 5;
       rows_out<NV, NV / 2>(o, ldo, b + C::KQ + C::A2, (w & 1) * 32, (w >> 1) * (NV / 16), min(kC, len - cl * kC), vn,
@@ -447,6 +489,8 @@ __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, con
   const long long sh = (long long)n * a.s.hv + h;
   const int nc = (len + kC - 1) / kC;
   const long long slot0 = slot_base(start, n);
+  int* bad_from = reinterpret_cast<int*>(stage + 2 * C::STAGE + C::S + (PL == 1 ? 2 : 1) * C::R);
+  for (int x = tid; x < 2 * (NV + 1); x += C::THREADS) bad_from[x] = x % (NV + 1) < NV ? kC : 0;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(full + i, C::FETCH + 1);
@@ -480,7 +524,7 @@ __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, con
 
   if (tid >= C::WORK) {
     fetch_chunks<DK, C>(a, maps, v_map, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
-                                     tile * NV, false, wait);
+                                     tile * NV, false, bad_from, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
     const int v0 = tile * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;
@@ -539,13 +583,25 @@ __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, con
           *reinterpret_cast<uint4*>(a.st + img * C::SB + chunk_at(row, ((v0 & 63) + c0 + j) / 8)) = pack8(s + j);
       const float eg = vec[kVecEG + i], be = vec[kVecBeta + i], el = vec[kVecEGL + i], dec = vec[kVecD];
       float r[NC];                     // beta V; then R; in the rows of Q, O
+      bool bad = false;                // a token with a NaN or an infinity, in V or marked by the preparation
       if (token) {
+        __nv_bfloat162 z = __float2bfloat162_rn(0.f);
 #pragma unroll
         for (int j = 0; j < NC; j += 8) {
-          unpack8(r + j, *reinterpret_cast<const uint4*>(vt + v_at<NV>(i, (c0 + j) / 8)));
+          const uint4 u = *reinterpret_cast<const uint4*>(vt + v_at<NV>(i, (c0 + j) / 8));
+          z = times_zero(u, z);
+          unpack8(r + j, u);
 #pragma unroll
           for (int e = 0; e < 8; ++e) r[j + e] *= be;
         }
+        bad = !zeros(z) || !finite(be);
+        if (bad) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (!finite(r[j])) atomicMin(bad_from + st * (NV + 1) + c0 + j, i);
+          bad_from[st * (NV + 1) + NV] = 1;
+        }
+        __syncwarp();
       }
       const float f = token ? -be * eg : a.s.scale * eg;
       poll(done, phase);
@@ -566,6 +622,16 @@ __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, con
         }
       }
       if (PL == 1 && issuer) bulk_store_read();      // S and the last chunk's U have left their tiles
+      if (bad) {
+        // The product reads all 64 tokens for each, the later ones with factors of zero: a bad value's place in it is zero.
+#pragma unroll
+        for (int j = 0; j < NC; j += 8) {
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = finite(r[j + e]) ? r[j + e] : 0.f;
+          put8<PL, NB, C::RB>(rtile, i, c0 + j, w);
+        }
+      }
       tc::fence_proxy_async_smem();
       tc::fence_before_sync();
       group_sync<1, C::WORK>();
@@ -748,7 +814,7 @@ __device__ __forceinline__ void scan_bwd_tile(const TcArgs& a, const Maps& maps,
 
   if (tid >= C::WORK) {
     fetch_chunks<DK, C>(a, maps, &maps.v, stage, full, empty, outs, tid - C::WORK, h, start, len, slot0,
-                                    tile * NV, true, wait);
+                                    tile * NV, true, nullptr, wait);
   } else {
     const int quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane;
     const int v0 = tile * NV, c0 = cg * NC, dk = a.s.dk, dv = a.s.dv;

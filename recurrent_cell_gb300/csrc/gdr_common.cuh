@@ -349,6 +349,18 @@ struct FwdArgs {
   int ntile;
 };
 
+// A product reads a chunk's 64 tokens for each of its rows, the later ones with
+// factors of zero: what it reads must be finite, also once rounded to bf16 or TF32.
+constexpr float kLargest = 3.38953139e38f;      // bf16's largest
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= kLargest; }
+// The preparation's part of that: entries of A or T that are not (from a NaN, an
+// infinity or an overflow) become zeros, and the row's beta a NaN, by which the serial
+// pass marks the token and all that follow.
+__device__ __forceinline__ void drop(float& v, float* vec, int row) {
+  if (finite(v)) return;
+  v = 0.f;
+  vec[kVecBeta + row] = nanf("");
+}
 // Sum of two pairs hi + lo.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const float s = a.x + b.x, t = s - a.x, e = ((a.x - (s - t)) + (b.x - t)) + (a.y + b.y), h = s + e;

@@ -124,6 +124,16 @@ __device__ __forceinline__ void unpack8(float* v, const uint4& u) {
   v[0] = lo_f(u.x); v[1] = hi_f(u.x); v[2] = lo_f(u.y); v[3] = hi_f(u.y);
   v[4] = lo_f(u.z); v[5] = hi_f(u.z); v[6] = lo_f(u.w); v[7] = hi_f(u.w);
 }
+// z + 0 x eight bf16 values: zeros as long as all of them are finite.
+__device__ __forceinline__ __nv_bfloat162 times_zero(const uint4& u, __nv_bfloat162 z) {
+  const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162*>(&u), o = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z = __hfma2(p[i], o, z);
+  return z;
+}
+__device__ __forceinline__ bool zeros(__nv_bfloat162 z) {
+  return (*reinterpret_cast<const uint32_t*>(&z) & 0x7fff7fffu) == 0;
+}
 // Shared -> global copy of a tile by the calling thread, and the wait until
 // its copies have read their tiles.
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {

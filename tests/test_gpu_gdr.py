@@ -661,3 +661,46 @@ def test_repeated_and_opposite_keys_in_training(beta, decay):
     x = c.host()
     terms = np.abs(x[0] * ref["grad_q"]).sum(-1) + np.abs(x[1] * ref["grad_k"]).sum(-1)
     assert np.abs(got["grad_g"] - ref["grad_g"]).max() <= 10 * tolerance("grad_g", BF16) * terms.max()
+
+
+@MODES
+@pytest.mark.parametrize("kind", ["q", "k", "v", "g", "beta"])
+@pytest.mark.parametrize("many", [False, True], ids=["few heads", "many heads"])
+def test_a_bad_token_reaches_no_earlier_one(many, kind, math):
+    """A NaN or an infinity at one token reaches what the recurrence hands it to, and nothing else: not the
+    tokens before it in its chunk, not other heads, nor other columns where it is in v.  Everything
+    that stays finite has the same bits as without it."""
+    lens, shape = ([66] * 9 + [150], (8, 16, 64, 128)) if many else ([70, 150], (2, 4, 64, 96))
+    c = Case(lens, *shape, math, seed=46, init=True)
+    first = c.off[-2]                               # of the last sequence
+    for final in (True, False):
+        clean = c.forward(final=final, save=not final)
+        for at, bad in ((37, float("nan")), (64 + 21, float("inf")), (149, float("nan"))):
+            if kind == "g" and bad == float("inf"):
+                bad = float("nan")                  # the log-decay is at most 0
+            t = {"q": c.q, "k": c.k, "v": c.v, "g": c.g, "beta": c.beta}[kind]
+            i = (first + at, 1, 13)[:t.dim()]
+            was = t[i].clone()
+            t[i] = bad
+            got = c.forward(final=final, save=not final)
+            with np.errstate(invalid="ignore", over="ignore"):
+                ref = c.oracle()
+            t[i] = was
+            for n in ("o", "final_state") if final else ("o",):
+                fine = np.isfinite(ref[n])
+                np.testing.assert_array_equal(np.isfinite(got[n]), fine, err_msg=f"{n} {at} {bad}")
+                np.testing.assert_array_equal(got[n][fine], clean[n][fine], err_msg=f"{n} {at} {bad}")
+            assert not np.isfinite(ref["o"][i[0]]).all()
+
+
+@MODES
+def test_an_overflow_inside_a_chunk_is_not_hidden(math):
+    """Finite keys whose product passes fp32's range: what follows is not finite, what came before is right."""
+    c = Case([60], 1, 1, 64, 32, math, seed=47)
+    c.g[:] = 0
+    c.beta[:] = 0.5
+    clean = c.forward()
+    c.k[40] = c.k[30] = c.k[30] * 1e25
+    got = c.forward()
+    np.testing.assert_array_equal(got["o"][:30], clean["o"][:30])
+    assert not np.isfinite(got["o"][40:]).any() and not np.isfinite(got["final_state"]).any()
