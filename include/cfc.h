@@ -124,8 +124,9 @@ int cfc_device_error(int clear);
 /* Diagnostic of the timeout path: launches one kernel whose bounded mbarrier
  * wait (the wait helper of the K-loop kernels) runs out after max_polls polls
  * (1 .. 2^20) because nothing completes the barrier; the kernel then sets the
- * device error word and returns, so cfc_device_error reports 1 afterwards.  No
- * other state changes; the context stays usable.  CFC_ERR_SHAPE for max_polls
+ * device error words (the K loop's and those of the gated delta rule) and
+ * returns, so cfc_device_error reports 1 until it clears them.  No other state
+ * changes; the context stays usable.  CFC_ERR_SHAPE for max_polls
  * out of range. */
 int cfc_selftest_timeout(int max_polls, void* stream);
 

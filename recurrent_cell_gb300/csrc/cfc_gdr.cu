@@ -455,16 +455,26 @@ Workspace plan(long long rows, int n_seq, int hk, int hv, int dk, int dv, int ma
 
 }  // namespace gdr
 
+bool gdr_error_words(int* (&words)[kGdrErrorWords]) {
+  void* p = nullptr;
+  words[0] = cudaGetSymbolAddress(&p, gdr::g_gdr_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
+  words[1] = gdr::gdr_tc_error_word();
+  words[2] = gdr::gdr_grad_error_word();
+  return words[0] && words[1] && words[2];
+}
+
 int read_gdr_error(int clear) {
-  const int t = gdr::read_gdr_tc_error(clear), r = gdr::read_gdr_grad_error(clear);
-  if (t != 0 || r != 0) return t != 0 ? t : r;
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, gdr::g_gdr_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
-  if (clear && v) {
+  int* words[kGdrErrorWords];
+  if (!gdr_error_words(words)) return CFC_ERR_DEVICE;
+  int any = 0;
+  for (int* word : words) {              // each is read and cleared, whatever the others hold
+    int v = 0;
     const int zero = 0;
-    if (cudaMemcpyToSymbol(gdr::g_gdr_error, &zero, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
+    if (cudaMemcpy(&v, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return CFC_ERR_DEVICE;
+    if (clear && v && cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return CFC_ERR_DEVICE;
+    any |= v;
   }
-  return v;
+  return any;
 }
 
 bool gdr_shape_supported(int hk, int hv, int dk, int dv, int math) {

@@ -529,14 +529,9 @@ cudaError_t launch_grad_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
   return dk_tile == 64 ? launch<64, true>(g, st) : launch<128, true>(g, st);
 }
 
-int read_gdr_grad_error(int clear) {
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_gdr_grad_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
-  if (clear && v) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_gdr_grad_error, &zero, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
-  }
-  return v;
+int* gdr_grad_error_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_gdr_grad_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdr

@@ -1171,14 +1171,9 @@ cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st) {
   return dk_tile == 64 ? scan_bwd_by_size<64>(t, st) : scan_bwd_by_size<128>(t, st);
 }
 
-int read_gdr_tc_error(int clear) {
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_gdr_tc_error, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
-  if (clear && v) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_gdr_tc_error, &zero, sizeof(int)) != cudaSuccess) return CFC_ERR_DEVICE;
-  }
-  return v;
+int* gdr_tc_error_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_gdr_tc_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 }  // namespace gdr

@@ -156,7 +156,7 @@ struct ReduceOut {
 cudaError_t launch_reduce(const float* in, int n_batch, long long n_tail, long long ld,
                           const ReduceOut& out, cudaStream_t stream);
 // One bounded wait that runs out (max_polls polls) and sets the device error
-// word (cfc_tc.cu); diagnostic for the timeout path.
+// words of cfc_tc.cu and of the gated delta rule; diagnostic for the timeout path.
 cudaError_t launch_selftest_wait_timeout(uint32_t max_polls, cudaStream_t s);
 
 // tau-cell K loop (cfc_tau.cu), FP32.
@@ -288,6 +288,8 @@ struct GdrStepArgs {
   int n_seq, tokens, hk, hv, dk, dv, math;
   float scale;
 };
+constexpr int kGdrErrorWords = 3;       // FP32, bf16, bf16 gradients
+bool gdr_error_words(int* (&words)[kGdrErrorWords]);
 int read_gdr_error(int clear);
 bool gdr_shape_supported(int hk, int hv, int dk, int dv, int math);
 size_t gdr_workspace(long long rows, int n_seq, int hk, int hv, int dk, int dv, int math, int save);

@@ -1356,21 +1356,30 @@ cudaError_t launch_grad_x(const Layout& L, const GradXPlan& p, const CfcArgs& a,
 
 namespace {
 // Waits, bounded by max_polls, on an mbarrier that nothing completes -- the
-// wait helper and the error word of the K-loop kernels -- so that a test can
-// see a timeout reported without any real kernel failing.
-__global__ void k_selftest_wait_timeout(uint32_t max_polls) {
+// wait helper and the error word of the K-loop kernels, and the words of the
+// gated delta rule -- so that a test can see a timeout reported without any
+// real kernel failing.
+struct ErrorWords {
+  int* p[kGdrErrorWords];
+};
+__global__ void k_selftest_wait_timeout(uint32_t max_polls, ErrorWords words) {
   __shared__ uint64_t bar;
   if (threadIdx.x == 0) {
     tc::mbar_init(&bar, 1);
     tc::mbar_init_fence();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && !tc::mbar_wait(&bar, 0, max_polls)) atomicExch(&g_cfc_device_error, 1);
+  if (threadIdx.x == 0 && !tc::mbar_wait(&bar, 0, max_polls)) {
+    atomicExch(&g_cfc_device_error, 1);
+    for (int* p : words.p) atomicExch(p, 1);
+  }
 }
 }  // namespace
 
 cudaError_t launch_selftest_wait_timeout(uint32_t max_polls, cudaStream_t s) {
-  k_selftest_wait_timeout<<<1, 32, 0, s>>>(max_polls);
+  ErrorWords words;
+  if (!gdr_error_words(words.p)) return cudaErrorInvalidSymbol;
+  k_selftest_wait_timeout<<<1, 32, 0, s>>>(max_polls, words);
   return cudaGetLastError();
 }
 

@@ -526,10 +526,10 @@ struct BwdArgs {
 cudaError_t launch_prep_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st);
 cudaError_t launch_scan_tc(const FwdArgs& a, int dk_tile, int planes, cudaStream_t st);
 cudaError_t launch_scan_bwd_tc(const BwdArgs& a, int dk_tile, cudaStream_t st);
-int read_gdr_tc_error(int clear);
+int* gdr_tc_error_word();      // on the device, or NULL
 // The gradients that follow them (cfc_gdr_grad.cu).
 cudaError_t launch_grad_tc(const BwdArgs& a, int dk_tile, cudaStream_t st);
-int read_gdr_grad_error(int clear);
+int* gdr_grad_error_word();
 
 }  // namespace gdr
 }  // namespace cfc

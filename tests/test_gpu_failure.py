@@ -33,3 +33,15 @@ def test_timed_out_wait_is_reported_and_the_context_survives():
     ref = oracle.backward(inp["x"], inp["h0"], inp["W_in"], inp["W_rec"], inp["b"], inp["dt"], y=inp["y"])
     for k in ("h_seq", "grad_W_in", "grad_W_rec", "grad_b", "grad_h0"):
         assert_close(got[k], ref[k], w.math, f"after timeout: {k}")
+
+
+def test_one_clearing_read_clears_every_word():
+    """The self-test raises the words of the K loop and of all three groups of the gated delta rule's kernels:
+    one read clears them all, so nothing stale is reported against the next call."""
+    require_gpu()
+    assert cfc.cfc_device_error(clear=True) == 0
+    for _ in range(2):
+        cfc.cfc_selftest_timeout(1000)
+        torch_mod().cuda.synchronize()
+        assert cfc.cfc_device_error(clear=True) == 1
+        assert cfc.cfc_device_error() == 0
