@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(GradCfg<DK>::THREADS, 1) k_gdr_grad_tc(GradArg
           if (ft == 0) {
             bar_arrive_tx(full + st, 2 * C::T + 2 * C::S + kVec * 4 + (boxes ? 2 * C::T : 0));
             if (boxes) {
-              tma_tile(b + C::OFF_DO, &maps.go, t * 64, h, (int)row0, full + st);
+              tma_tile(b + C::OFF_DO, &maps.w, t * 64, h, (int)row0, full + st);
               tma_tile(b + C::OFF_V, &maps.v, t * 64, h, (int)row0, full + st);
             }
             bulk_load(b, a.u + (id * nt + t) * C::T, C::T, full + st);
@@ -508,7 +508,7 @@ static cudaError_t launch(GradArgs g, cudaStream_t st) {
   g.tma = tile_map(&m.q, g.q, g.s.dk, g.s.hk, g.s.rows, g.ldq, 64) &&
           tile_map(&m.k, g.k, g.s.dk, g.s.hk, g.s.rows, g.ldk, 64) &&
           tile_map(&m.v, g.v, g.s.dv, g.s.hv, g.s.rows, g.ldv, 64) &&
-          tile_map(&m.go, g.go, g.s.dv, g.s.hv, g.s.rows, (long long)g.s.hv * g.s.dv, 64);
+          tile_map(&m.w, g.go, g.s.dv, g.s.hv, g.s.rows, (long long)g.s.hv * g.s.dv, 64);
   TraceScope tr("k_gdr_grad_tc", st);
   k_gdr_grad_tc<DK, SHARED><<<(unsigned)(items < kNumSMs ? items : kNumSMs), C::THREADS, C::BYTES, st>>>(g, m);
   return cudaGetLastError();

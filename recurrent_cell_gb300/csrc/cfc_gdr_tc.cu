@@ -479,7 +479,7 @@ template <int DK, int PL, int NB>
 __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, const CUtensorMap* v_map,
                                           unsigned char* smem_raw, int n, int h, int tile, long long start, int len) {
   using C = TcCfg<DK, PL, NB, false>;
-  constexpr int NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;      // columns a thread; at a time
+  constexpr int NC = C::NC, NV = C::NV, NP = 16;      // columns a thread; at a time
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
@@ -554,7 +554,6 @@ __device__ __forceinline__ void scan_tile(const TcArgs& a, const Maps& maps, con
       unsigned char* b = stage + st * C::STAGE;
       unsigned char* vt = b + C::KQ + C::A2;
       const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + C::VT);
-      const int rows = min(kC, len - c * kC);
       const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
@@ -754,7 +753,7 @@ __global__ void __launch_bounds__(TcCfg<DK, PL, 2, false>::THREADS, 1)
   if (w.half) {
     // (kept in tiles of 64 columns: two of 32 fill one)
     if (PL == 2 || w.tile * 64 < a.s.dv)
-      scan_tile<DK, PL, 1>(a, maps, PL == 2 ? &maps.go : &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
+      scan_tile<DK, PL, 1>(a, maps, PL == 2 ? &maps.w : &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
   } else {
     scan_tile<DK, PL, 2>(a, maps, &maps.v, smem_raw, w.n, w.h, w.tile, w.start, w.len);
   }
@@ -771,7 +770,7 @@ template <int DK, int NB>
 __device__ __forceinline__ void scan_bwd_tile(const TcArgs& a, const Maps& maps, unsigned char* smem_raw, int n, int h,
                                               int tile, long long start, int len) {
   using C = TcCfg<DK, 1, NB, true>;
-  constexpr int PL = 1, NC = C::NC, NV = C::NV, NP = NC < 16 ? NC : 16;
+  constexpr int PL = 1, NC = C::NC, NV = C::NV, NP = 16;
   unsigned char* base = smem_raw + (1024 - (smem_addr(smem_raw) & 1023)) % 1024;
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t *empty = full + 2, *done = full + 4, *outs = full + 6;
@@ -845,7 +844,6 @@ __device__ __forceinline__ void scan_bwd_tile(const TcArgs& a, const Maps& maps,
       unsigned char* b = stage + st * C::STAGE;
       unsigned char* dot = b + C::KQ + C::A2;
       const float* vec = reinterpret_cast<const float*>(b + C::KQ + C::A2 + C::VT);
-      const int rows = min(kC, len - c * kC);
       const long long img = ((slot0 + c) * a.s.hv + h) * ((dv + 63) / 64) + v0 / 64;
       if (row < DK) {
 #pragma unroll
@@ -1079,7 +1077,7 @@ static cudaError_t scan_mixed(TcArgs a, cudaStream_t st) {
   const cudaError_t e = allow_smem<k_gdr_scan_mixed_tc<DK, PL>>(W::BYTES);
   if (e != cudaSuccess) return e;
   Maps m;
-  a.tma = maps_of(a, 64, &m) && (PL == 1 || tile_map(&m.go, a.v, a.s.dv, a.s.hv, a.s.rows, a.ldv, 32));
+  a.tma = maps_of(a, 64, &m) && (PL == 1 || tile_map(&m.w, a.v, a.s.dv, a.s.hv, a.s.rows, a.ldv, 32));
   TraceScope tr("k_gdr_scan_tc", st);
   k_gdr_scan_mixed_tc<DK, PL><<<mixed_blocks(a), W::THREADS, W::BYTES, st>>>(a, m);
   return cudaGetLastError();

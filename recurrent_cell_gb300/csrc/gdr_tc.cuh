@@ -15,9 +15,10 @@ namespace cfc {
 namespace gdr {
 
 // Tensor maps of [rows, heads, width] bf16 tensors: boxes of up to 64 columns
-// of one head by a chunk's 64 rows, zeros past the width.
+// of one head by a chunk's 64 rows, zeros past the width.  w: the gradients'
+// grad_o; in a scan of both widths with PL = 2, v in boxes of 32 columns.
 struct Maps {
-  CUtensorMap q, k, v, go;
+  CUtensorMap q, k, v, w;
 };
 // False: the driver cannot say (the kernels then copy by 16 bytes).
 bool tile_map(CUtensorMap* m, const void* base, int width, int heads, long long rows, long long ld, int box);
@@ -50,17 +51,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch) { return row * 128
 // products of the lo plane, added.
 template <int N>
 __device__ __forceinline__ void ld_cols(uint32_t t, float* v) {
-  static_assert(N % 16 == 0 || N == 8, "columns");
-  if constexpr (N == 8) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(t)
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-    return;
-  }
+  static_assert(N % 16 == 0, "columns");
 #pragma unroll
   for (int j = 0; j + 16 <= N; j += 16) {
     uint32_t r[16];
