@@ -154,12 +154,16 @@ _raw_stream = None
 def _stream(stream):
     global _raw_stream
     if stream is None:
-        # the current stream's handle without building a Stream object: the
-        # binding is most of a small call's time
+        # the current stream's handle without building a Stream object, where
+        # torch has the two calls: the binding is most of a small call's time
         if _raw_stream is None:
             torch = _torch()
             torch.cuda.current_device()             # brings CUDA up
-            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            device = getattr(torch._C, "_cuda_getDevice", None)
+            if get is None or device is None:       # not public names
+                get, device = lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device
+            _raw_stream = get, device
         return _raw_stream[0](_raw_stream[1]())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 

@@ -159,3 +159,14 @@ def test_norm_workspace(lib):
     assert size(1 << 30, 64) == size(1 << 20, 64)            # a fixed number of partial sums
     for bad in [(-1, 64), (1, 0), (1, 32769)]:
         assert size(*bad) == 0
+
+
+def test_current_stream_without_torchs_private_calls(monkeypatch):
+    """The binding takes the current stream's handle from the public API where torch lacks the short way."""
+    class Cuda:
+        current_device = staticmethod(lambda: 3)
+        current_stream = staticmethod(lambda d: type("Stream", (), {"cuda_stream": 1000 + d}))
+
+    monkeypatch.setattr(cfc, "_torch_module", type("Torch", (), {"cuda": Cuda, "_C": object()}))
+    monkeypatch.setattr(cfc, "_raw_stream", None)
+    assert cfc._stream(None) == 1003
