@@ -303,10 +303,17 @@ int cfc_grn_backward(const float* h, int B, int K, int hidden, int head_mid, int
  * the workspace are 16-byte aligned, the rest 4-byte aligned.
  *
  * FP32: products of two TF32 values an operand, fp32-accurate.  BF16: products
- * take bf16 operands and sum in fp32; the running state is fp32, and where a
- * final_state is asked for, every operand on the way to it keeps 17
- * significant bits, so that the state is good to about 1e-5 (o and the
- * gradients, which leave in bf16, to their own rounding).
+ * take bf16 operands and sum in fp32, and the running state is fp32.  Where a
+ * final_state is asked for, every operand on the way to it and to o keeps 17
+ * significant bits: the state is good to about 1e-5, o to its own rounding (2e-3).
+ * Without one (training), the state, the corrections u and the chunk's inverse are
+ * rounded to bf16 where they enter a product, and what the backward reads of them is
+ * kept in bf16: o and the gradients are good to 3e-3 to 5e-3 of their norm.  The
+ * roundings grow where little decays and beta |k|^2 is near 2, since the terms then
+ * nearly cancel: without any decay o to 1.6e-2 with random keys at 2, and with one
+ * key at every token to 5e-3 at 1, 4e-2 at 1.7, and 0.4 at 1.9 (with decays of 0.025
+ * a token on average 1e-2); grad_q, grad_g and grad_beta, differences of such terms,
+ * to several times that.  Ask for a final_state (o) or use FP32 where it matters.
  *
  * A NaN or an infinity at a token reaches o of that token and, through the
  * state, of its sequence's later ones, as in the recurrence; no earlier token, no
@@ -341,7 +348,9 @@ int cfc_gdr_backward(const void* q, long long q_stride, const void* k, long long
  * sequence i's state is slots[i] of `state` [n_slots, n_v_heads, d_k, d_v]
  * (slots NULL: i), updated in place.  No two sequences may share a slot.  A
  * sequence whose slot is outside [0, n_slots) has no state: its o is zero and
- * nothing is kept.  All arithmetic is fp32. */
+ * nothing is kept.  All tokens are applied and no state in between is kept: who
+ * may have to take tokens back (rejected drafts) copies the slots before the
+ * call.  All arithmetic is fp32. */
 int cfc_gdr_step(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
                  long long v_stride, const float* g, const float* beta, int n_seq, int tokens, int n_k_heads,
                  int n_v_heads, int d_k, int d_v, float scale, int math, float* state, long long n_slots,

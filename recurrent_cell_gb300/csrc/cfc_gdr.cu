@@ -11,8 +11,8 @@
 // shared memory first, twice the bytes of a tile that already fills an SM.
 // The state's columns do not touch one another, so a head's value columns are
 // split over blocks; the serial pass is a chain of latencies, 7 us a chunk of
-// 128 keys x 16 columns (32 x 64 tokens x 2 heads of 64: prep 10 us, scan 8,
-// backward 10 and 16).
+// 128 keys x 16 columns (32 x 64 tokens x 2 heads of 64: prep 10 us, scan 9,
+// backward 10 and 16; 16384 tokens x 16 heads of 128: 1.9 ms, 80 us by bytes).
 #include "gdr_common.cuh"
 
 namespace cfc {

@@ -16,8 +16,12 @@
 // are the traffic (about 160 KB a chunk and head in, 32 KB out).  Two warps
 // keep two 64-column stages and the next chunk's K and Q on their way, one
 // issues the products, eight do the arithmetic between them; a head's first
-// products run under the last one's end.  Memory is the bound: 194 KB a chunk
-// and head of 128 x 128 in 34 ns, 5.8 TB/s (8 x 2048 x 16 heads 166 us).
+// products run under the last one's end.  194 KB a chunk and head of 128 x 128
+// in 41 ns, 4.8 TB/s (8 x 2048 x 16 heads 167 us): 71 % of a copy's rate.  What
+// holds it below is latency: the 11 warps of an SM wait for shared and tensor
+// memory in 44 % of the samples, and DRAM is active in 62 % of the cycles.  (With
+// shared heads and d_k = 128 the sums over a group cost 220 bytes of spills a thread;
+// 16 value on 8 key heads take the whole call from 460 us to 502.)
 #include "gdr_tc.cuh"
 
 namespace cfc {

@@ -24,12 +24,13 @@
 // (16384 tokens x 16 heads); joining a vote to a barrier of the chain took 26.
 //
 // What bounds a pass over few heads is the length of that chain: 1.6 us a chunk
-// of 32 columns with PL = 2 (16384 tokens x 16 heads 412 us; 40 us by bytes),
+// of 32 columns with PL = 2 (16384 tokens x 16 heads 418 us; 40 us by bytes),
 // of which the products, bound by their operands' reads of shared memory, are
 // 0.5 us and the rest three times accumulator -> registers -> operand ->
-// barrier.  With as many heads as SMs and no state asked for it is memory: a
-// chunk of 128 columns moves 128 KB, 3.5 us on each of 152 SMs, 5.6 TB/s
-// (8 x 2048 x 16 heads 102 us forward, 115 backward).
+// barrier.  With many heads and no state asked for a chunk of 128 columns moves
+// 121 KB in 3.3 us; 128 heads on as many SMs come to 4.7 TB/s forward, 4.2 backward,
+// 70 and 62 % of a copy's rate, the chain being what they wait for (8 x 2048 x 16
+// heads 108 us and 119).
 #include "gdr_tc.cuh"
 
 namespace cfc {
@@ -344,8 +345,9 @@ __device__ __forceinline__ int nth(const TcArgs& a, int i) {
 // What a block does: a tile of a head of a sequence; tile < 0: nothing.  The
 // longest sequences, those that would outlast by a quarter and more an even
 // share of the whole, take tiles of half the width, two thirds of the time a
-// chunk.  (Training of 3000 of 6470 tokens x 16 heads 404 -> 292 us, prompts of 8000 of
-// 8530 tokens x 16 heads 335 -> 249; at 1.05 of the share 194 -> 220, so not there.)
+// chunk.  (Training of 3000 of 6470 tokens x 16 heads 28 % less, now 305 us, prompts of
+// 8000 of 8530 tokens x 16 heads 26 % less, now 257; at 1.05 of the share 194 -> 220, so
+// not there.  A batch in which nothing is halved loses 5 % by the joint kernel.)
 struct Work {
   int n, h, tile, len;
   long long start;
