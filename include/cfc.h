@@ -22,6 +22,13 @@
  *                       tokens of decoding sequences (FP32, bf16);
  *   cfc_rmsnorm_*       root-mean-square norm of a residual stream, forward
  *                       (optionally to 8 bits with scales) and backward;
+ *   cfc_layernorm_*     layer norm of a residual stream, forward and backward;
+ *   cfc_conv_*          the short causal convolution of each channel over its
+ *                       sequence: forward, backward, next tokens;
+ *   cfc_ssm_*           the selective state space scan, a recurrence with a state of
+ *                       N values a channel: forward, backward, next tokens;
+ *   cfc_grad_norm, cfc_grad_clip
+ *                       the norm of many gradients together, and clipping to it;
  *   helpers             workspace sizes, status strings, the device error
  *                       word and its self-test, per-kernel event tracing.
  *
@@ -77,7 +84,8 @@ typedef enum {
   CFC_ERR_MODE = -5,      /* unknown math mode or gradient path                */
   CFC_ERR_LAUNCH = -6,    /* a kernel launch failed (cudaGetLastError != 0)    */
   CFC_ERR_DEVICE = -7,    /* no usable CUDA device / unsupported architecture  */
-  CFC_ERR_TOO_LARGE = -8  /* sizes need more than CFC_STATIC_WORKSPACE_BYTES   */
+  CFC_ERR_TOO_LARGE = -8, /* sizes need more than CFC_STATIC_WORKSPACE_BYTES   */
+  CFC_ERR_OVERLAP = -9    /* buffers that must not overlap do                  */
 } cfc_status;
 
 typedef enum { CFC_MATH_FP32 = 0, CFC_MATH_TF32 = 1, CFC_MATH_BF16 = 2 } cfc_math;
@@ -385,6 +393,170 @@ size_t cfc_rmsnorm_workspace_bytes(long long rows, int d);
 int cfc_rmsnorm_backward(const void* s, const float* weight, const float* rstd, const void* grad_y,
                          const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
                          float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm of a residual stream (FP32 and BF16 modes).
+ *   s = x + residual rounded to the stored type (s = x where residual is NULL),
+ *   mean = sum(s) / d,  rstd = 1 / sqrt(sum((s - mean)^2) / d + eps),
+ *   y = (s - mean) rstd weight + bias.
+ * x, residual, y, residual_out, grad_y, grad_residual_out, grad_x [rows, d] in
+ * the mode's type; weight, bias, grad_weight, grad_bias [d], mean, rstd [rows]
+ * float.  1 <= d <= 32768.  Pointers 16-byte aligned (mean and rstd: 4).
+ *
+ * Forward: bias NULL: none.  residual_out (= s), mean and rstd are optional, and
+ * all needed by the backward.  residual_out may be the buffer of x or residual. */
+int cfc_layernorm_forward(const void* x, const void* residual, const float* weight, const float* bias, long long rows,
+                          int d, float eps, int math, void* y, void* residual_out, float* mean, float* rstd, void* stream);
+
+/* Device workspace of the backward; 0 for unsupported sizes.  Host-only. */
+size_t cfc_layernorm_workspace_bytes(long long rows, int d);
+
+/* Backward from the stream s, mean and rstd of the forward: grad_x is the
+ * gradient of s, hence of x and of residual: the norm's own plus
+ * grad_residual_out (NULL: none).  grad_weight and grad_bias (NULL: not wanted)
+ * are sums over rows (0 for rows = 0), their partial sums added by
+ * reduce_axis0.  grad_x may be the buffer of grad_y or grad_residual_out. */
+int cfc_layernorm_backward(const void* s, const float* weight, const float* mean, const float* rstd, const void* grad_y,
+                           const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
+                           float* grad_weight, float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The short causal convolution (FP32 and BF16 modes): each channel c over the
+ * last `width` rows of its sequence,
+ *   pre_t = bias[c] + sum_j weight[c, j] x_{t - width + 1 + j}[c],
+ *   y_t = pre sigmoid(pre) where silu != 0, else pre.
+ * The rows before a sequence's first are those of its initial_state, or zeros; its
+ * final_state are its last width - 1 inputs, those of initial_state among them
+ * where it is shorter.
+ *   x [rows, channels], rows x_stride elements apart (at least channels, a multiple of
+ *         16 bytes), in the mode's type; y, grad_y, grad_x like x but dense
+ *   states [n_seq, width - 1, channels] in the mode's type
+ *   weight, grad_weight [channels, width], bias, grad_bias [channels]: float
+ * Sequences as for the gated delta rule: seq_offsets NULL, n_seq sequences of rows /
+ * n_seq rows, else a DEVICE array of n_seq + 1 non-decreasing row numbers from 0
+ * to rows; nothing outside the tensors is touched whatever it holds.
+ * Sizes: channels a multiple of 8, 2 <= width <= 8, 1 <= n_seq <= 2^20,
+ * 0 <= rows <= 2^30.  Pointers 16-byte aligned (bias, seq_offsets, slots: 4).  Outputs
+ * overlap neither inputs nor one another (CFC_ERR_OVERLAP where that is seen).
+ *
+ * Sums are fp32.  A NaN or an infinity reaches the `width` rows that see it, of
+ * its own channel and sequence. */
+
+/* Forward.  bias, initial_state and final_state may be NULL. */
+int cfc_conv_forward(const void* x, long long x_stride, const float* weight, const float* bias, const int* seq_offsets,
+                     int n_seq, long long rows, int channels, int width, int silu, int math, const void* initial_state,
+                     void* y, void* final_state, void* stream);
+
+/* Device workspace of the backward; 0 for unsupported sizes.  Host-only. */
+size_t cfc_conv_workspace_bytes(long long rows, int channels, int width, int math);
+
+/* Backward, from the forward's inputs alone.  grad_final_state NULL: zero;
+ * grad_initial_state and grad_bias NULL: not written.  grad_weight and grad_bias
+ * are sums over all rows, their partial sums added by reduce_axis0. */
+int cfc_conv_backward(const void* x, long long x_stride, const float* weight, const float* bias, const int* seq_offsets,
+                      int n_seq, long long rows, int channels, int width, int silu, int math, const void* initial_state,
+                      const void* grad_y, const void* grad_final_state, void* grad_x, float* grad_weight, float* grad_bias,
+                      void* grad_initial_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The next `tokens` rows of each of n_seq sequences (rows = n_seq * tokens):
+ * sequence i's last inputs are slot slots[i] of `state` [n_slots, width - 1,
+ * channels] (slots NULL: i), updated in place.  No two sequences may share a
+ * slot.  A sequence whose slot is outside [0, n_slots) has no state: its y is
+ * zero and nothing is kept. */
+int cfc_conv_step(const void* x, long long x_stride, const float* weight, const float* bias, int n_seq, int tokens,
+                  int channels, int width, int silu, int math, void* state, long long n_slots, const int* slots, void* y,
+                  void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The selective state space scan (FP32 and BF16 modes).  Each sequence and
+ * channel c keeps a state h [n_states], zero or initial_state at first, and per
+ * token t does
+ *   dt = softplus(delta_t[c] + delta_bias[c]),
+ *   h[n] <- exp(dt A[c, n]) h[n] + dt x_t[c] B_t[group, n],
+ *   y_t[c] = (sum_n C_t[group, n] h[n] + D[c] x_t[c]) z_t[c] sigmoid(z_t[c]),
+ * group = c / (channels / groups).  delta_bias, D and z may be NULL: 0, 0, and no
+ * gate.  For a bounded state A is negative.
+ *   x, delta, z [rows, channels], rows *_stride elements apart (at least channels, a
+ *         multiple of 16 bytes); B, C [rows, groups, n_states], rows *_stride elements
+ *         apart (at least groups * n_states); all in the mode's type
+ *   A [channels, n_states], D, delta_bias [channels]: float
+ *   y, grad_y, grad_x, grad_delta, grad_z, grad_B, grad_C like x, B and C but dense
+ *   grad_A, grad_D, grad_delta_bias: float, summed over all rows
+ *   states [n_seq, channels, n_states]: float in both modes
+ * Sequences as for cfc_conv_forward.  Sizes: channels / groups a multiple of 8,
+ * 1 <= n_states <= 64, groups * n_states <= 65536, 1 <= n_seq <= 2^20, 0 <= rows
+ * <= 2^30.  x, delta, z, y, states, gradients and the workspace are 16-byte aligned;
+ * B and C to their type (rows of whole 16-byte vectors, with 8, 16, 32 or 64
+ * states, are read faster); grad_B, grad_C, A, D, delta_bias and their gradients 4
+ * bytes.  Outputs overlap neither inputs nor one another (CFC_ERR_OVERLAP where
+ * that is seen).
+ *
+ * All arithmetic is fp32: states are good to about 1e-6 of their size times the
+ * number of tokens that they remember, outputs to their rounding.  A NaN or an infinity
+ * at a token reaches that token's and, through the state, its sequence's later
+ * outputs (of x, delta and z of its own channel); no earlier token and no other
+ * sequence.  The gradients of a sequence in which anything is not finite are
+ * not specified, nor those that sums over sequences share with it. */
+
+/* Device workspace of the two calls (save != 0: of a forward that a backward
+ * follows, and of that backward).  Host-only; 0 for unsupported sizes. */
+size_t cfc_ssm_workspace_bytes(long long rows, int n_seq, int channels, int groups, int n_states, int math, int save);
+
+/* Forward.  initial_state and final_state may be NULL.  save != 0: keeps in
+ * the workspace what the backward reads, a state for every 16 rows. */
+int cfc_ssm_forward(const void* x, long long x_stride, const void* delta, long long delta_stride, const float* A,
+                    const void* B, long long B_stride, const void* C, long long C_stride, const float* D, const void* z,
+                    long long z_stride, const float* delta_bias, const int* seq_offsets, int n_seq, long long rows,
+                    int channels, int groups, int n_states, int math, const float* initial_state, void* y,
+                    float* final_state, int save, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of the forward that filled `workspace` (same inputs, save != 0).
+ * grad_final_state NULL: zero.  grad_z is required with z; grad_D,
+ * grad_delta_bias and grad_initial_state NULL: not written.  All outputs are
+ * overwritten; grad_B and grad_C are summed over the channels of a group, grad_A,
+ * grad_D and grad_delta_bias over rows, in a fixed order. */
+int cfc_ssm_backward(const void* x, long long x_stride, const void* delta, long long delta_stride, const float* A,
+                     const void* B, long long B_stride, const void* C, long long C_stride, const float* D, const void* z,
+                     long long z_stride, const float* delta_bias, const int* seq_offsets, int n_seq, long long rows,
+                     int channels, int groups, int n_states, int math, const float* initial_state, const void* grad_y,
+                     const float* grad_final_state, void* grad_x, void* grad_delta, float* grad_A, void* grad_B,
+                     void* grad_C, float* grad_D, void* grad_z, float* grad_delta_bias, float* grad_initial_state,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The next `tokens` tokens of each of n_seq sequences (rows = n_seq * tokens):
+ * sequence i's state is slots[i] of `state` [n_slots, channels, n_states] (slots
+ * NULL: i), updated in place.  No two sequences may share a slot.  A sequence
+ * whose slot is outside [0, n_slots) has no state: its y is zero and nothing is
+ * kept. */
+int cfc_ssm_step(const void* x, long long x_stride, const void* delta, long long delta_stride, const float* A,
+                 const void* B, long long B_stride, const void* C, long long C_stride, const float* D, const void* z,
+                 long long z_stride, const float* delta_bias, int n_seq, int tokens, int channels, int groups, int n_states,
+                 int math, float* state, long long n_slots, const int* slots, void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The norm of many gradients together, and clipping to it:
+ *   norm = sqrt(sum of the squares of all values),
+ *   out = grad min(1, max_norm / (norm + 1e-6)).
+ * grads, out, n_values and math are HOST arrays of `count` entries, read before the
+ * call returns: entry i is a device tensor of n_values[i] values (0 <= n_values[i] <=
+ * 2^35; none is skipped), float for CFC_MATH_FP32 and bfloat16 for CFC_MATH_BF16,
+ * aligned to its type (to 16 bytes is faster).  norm: one float on the device.
+ * 0 <= count <= 65536.  Squares are fp32 where that holds them and 64 bits
+ * elsewhere, their sums 64 bits: values from the smallest to the largest of their
+ * type are counted.  A NaN makes the norm and the result NaN; a norm that is
+ * infinite, or too large for a float, makes the factor 0. */
+
+/* Device workspace of the two calls; 0 for unsupported counts.  Host-only. */
+size_t cfc_grad_clip_workspace_bytes(int count);
+
+int cfc_grad_norm(const void* const* grads, const long long* n_values, const int* math, int count, float* norm,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[i] may be grads[i]; otherwise no out overlaps a gradient or another out,
+ * and no gradient may be named twice where it is its own out.  max_norm >= 0
+ * (infinity: no clipping); otherwise CFC_ERR_SHAPE. */
+int cfc_grad_clip(const void* const* grads, void* const* out, const long long* n_values, const int* math, int count,
+                  float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* reduce_axis0 for `count` independent matrices with one launch per kernel
  * configuration (the pages' training step calls the reducer 17 times, once per

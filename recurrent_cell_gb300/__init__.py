@@ -93,6 +93,36 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.cfc_rmsnorm_workspace_bytes.restype = sz
     lib.cfc_rmsnorm_backward.argtypes = [vp] * 5 + [i64, i32, i32] + [vp] * 3 + [sz, vp]
     lib.cfc_rmsnorm_backward.restype = i32
+    lib.cfc_layernorm_forward.argtypes = [vp] * 4 + [i64, i32, ctypes.c_float, i32] + [vp] * 5
+    lib.cfc_layernorm_forward.restype = i32
+    lib.cfc_layernorm_workspace_bytes.argtypes = [i64, i32]
+    lib.cfc_layernorm_workspace_bytes.restype = sz
+    lib.cfc_layernorm_backward.argtypes = [vp] * 6 + [i64, i32, i32] + [vp] * 4 + [sz, vp]
+    lib.cfc_layernorm_backward.restype = i32
+    conv_in = [vp, i64, vp, vp]
+    lib.cfc_conv_forward.argtypes = conv_in + [vp, i32, i64] + [i32] * 4 + [vp] * 4
+    lib.cfc_conv_forward.restype = i32
+    lib.cfc_conv_workspace_bytes.argtypes = [i64] + [i32] * 3
+    lib.cfc_conv_workspace_bytes.restype = sz
+    lib.cfc_conv_backward.argtypes = conv_in + [vp, i32, i64] + [i32] * 4 + [vp] * 8 + [sz, vp]
+    lib.cfc_conv_backward.restype = i32
+    lib.cfc_conv_step.argtypes = conv_in + [i32] * 6 + [vp, i64, vp, vp, vp]
+    lib.cfc_conv_step.restype = i32
+    ssm_in = [vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, vp]
+    lib.cfc_ssm_workspace_bytes.argtypes = [i64] + [i32] * 6
+    lib.cfc_ssm_workspace_bytes.restype = sz
+    lib.cfc_ssm_forward.argtypes = ssm_in + [vp, i32, i64] + [i32] * 4 + [vp] * 3 + [i32, vp, sz, vp]
+    lib.cfc_ssm_forward.restype = i32
+    lib.cfc_ssm_backward.argtypes = ssm_in + [vp, i32, i64] + [i32] * 4 + [vp] * 13 + [sz, vp]
+    lib.cfc_ssm_backward.restype = i32
+    lib.cfc_ssm_step.argtypes = ssm_in + [i32] * 6 + [vp, i64, vp, vp, vp]
+    lib.cfc_ssm_step.restype = i32
+    lib.cfc_grad_clip_workspace_bytes.argtypes = [i32]
+    lib.cfc_grad_clip_workspace_bytes.restype = sz
+    lib.cfc_grad_norm.argtypes = [vp] * 3 + [i32, vp, vp, sz, vp]
+    lib.cfc_grad_norm.restype = i32
+    lib.cfc_grad_clip.argtypes = [vp] * 4 + [i32, ctypes.c_float, vp, vp, sz, vp]
+    lib.cfc_grad_clip.restype = i32
     lib.cfc_kloop_grad_splits.argtypes = [i32] * 6
     lib.cfc_kloop_grad_splits.restype = i32
     lib.cfc_device_error.argtypes = [i32]
@@ -522,6 +552,262 @@ def cfc_rmsnorm_backward(s, weight, rstd, grad_y, grad_x, grad_weight, workspace
         rows, d, math, _ptr(grad_x, "grad_x", st, shape), _ptr(grad_weight, "grad_weight", f32, (d,)),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("cfc_rmsnorm_backward", status)
+
+
+def cfc_layernorm_workspace_bytes(rows: int, d: int) -> int:
+    return int(load_library().cfc_layernorm_workspace_bytes(rows, d))
+
+
+def cfc_layernorm_forward(x, weight, y, bias=None, residual=None, residual_out=None, mean=None, rstd=None, eps=1e-5,
+                          math=MATH_BF16, stream=None):
+    """Layer norm y of the stream x + residual [rows, d]; the backward needs the
+    stream (residual_out, or x without a residual), mean and rstd [rows]."""
+    st, f32 = _storage_dtype(math), _torch().float32
+    rows, d = shape = x.shape
+    status = load_library().cfc_layernorm_forward(
+        _ptr(x, "x", st), _ptr(residual, "residual", st, shape, optional=True), _ptr(weight, "weight", f32, (d,)),
+        _ptr(bias, "bias", f32, (d,), optional=True), rows, d, eps, math, _ptr(y, "y", st, shape),
+        _ptr(residual_out, "residual_out", st, shape, optional=True), _ptr(mean, "mean", f32, (rows,), optional=True),
+        _ptr(rstd, "rstd", f32, (rows,), optional=True), _stream(stream))
+    _check("cfc_layernorm_forward", status)
+
+
+def cfc_layernorm_backward(s, weight, mean, rstd, grad_y, grad_x, grad_weight, workspace, grad_bias=None,
+                           grad_residual_out=None, math=MATH_BF16, stream=None):
+    """Backward from the stream s, mean and rstd: grad_x, the gradient of s,
+    grad_weight and (where given) grad_bias."""
+    st, f32 = _storage_dtype(math), _torch().float32
+    rows, d = shape = s.shape
+    status = load_library().cfc_layernorm_backward(
+        _ptr(s, "s", st), _ptr(weight, "weight", f32, (d,)), _ptr(mean, "mean", f32, (rows,)), _ptr(rstd, "rstd", f32, (rows,)),
+        _ptr(grad_y, "grad_y", st, shape), _ptr(grad_residual_out, "grad_residual_out", st, shape, optional=True),
+        rows, d, math, _ptr(grad_x, "grad_x", st, shape), _ptr(grad_weight, "grad_weight", f32, (d,)),
+        _ptr(grad_bias, "grad_bias", f32, (d,), optional=True), _ptr(workspace, "workspace", _torch().uint8),
+        workspace.numel(), _stream(stream))
+    _check("cfc_layernorm_backward", status)
+
+
+def _spaced(t, name, dtype, shape, tail=1):
+    """Pointer and row stride of t of `shape`, whose rows (the last `tail` axes,
+    dense) may be parts of wider ones, evenly spaced over the axes before them."""
+    width = shape[-1] if tail == 1 else shape[-1] * shape[-2]
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr(), width
+    except AttributeError:
+        pass
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    strides, lead = t.stride(), shape[:-tail]
+    dense = shape[-1] == 1 or strides[-1] == 1
+    if tail == 2:
+        dense = dense and (shape[-2] == 1 or strides[-2] == shape[-1])
+    many = [i for i in range(len(lead)) if lead[i] != 1]
+    ld = strides[many[-1]] if many else width           # one row: its stride says nothing
+    if not dense or (len(many) == 2 and strides[0] != lead[1] * ld):
+        raise ValueError(f"{name} must be dense in its last {'axis' if tail == 1 else 'two axes'}, with evenly spaced rows")
+    return t.data_ptr(), ld
+
+
+def _row_sequences(shape, seq_offsets, name="x"):
+    """(offsets, sequences, rows) of [sequences, tokens, channels], or [rows, channels] with seq_offsets."""
+    if len(shape) != (3 if seq_offsets is None else 2):
+        raise ValueError(f"{name} must be [sequences, tokens, channels], or [rows, channels] with seq_offsets")
+    return _gdr_sequences(shape, seq_offsets)
+
+
+def cfc_conv_workspace_bytes(rows: int, channels: int, width: int, math=MATH_BF16) -> int:
+    return int(load_library().cfc_conv_workspace_bytes(rows, channels, width, math))
+
+
+def _conv_inputs(x, weight, bias, math):
+    st, f32, shape = _storage_dtype(math), _torch().float32, x.shape
+    d = shape[-1]
+    if len(weight.shape) != 2:
+        raise ValueError("weight must be [channels, width]")
+    w = weight.shape[1]
+    return st, f32, shape, d, w, (*_spaced(x, "x", st, shape), _ptr(weight, "weight", f32, (d, w)),
+                                  _ptr(bias, "bias", f32, (d,), optional=True))
+
+
+def cfc_conv_forward(x, weight, y, bias=None, seq_offsets=None, initial_state=None, final_state=None, silu=True,
+                     math=MATH_BF16, stream=None):
+    """Short causal convolution of each channel of x [sequences, tokens, channels]
+    (or [rows, channels] packed, with int32 seq_offsets [sequences + 1] on the
+    device), weight [channels, width]; states [sequences, width - 1, channels]."""
+    st, f32, shape, d, w, args = _conv_inputs(x, weight, bias, math)
+    off, n, rows = _row_sequences(shape, seq_offsets)
+    ss = (n, w - 1, d)
+    status = load_library().cfc_conv_forward(
+        *args, off, n, rows, d, w, 1 if silu else 0, math, _ptr(initial_state, "initial_state", st, ss, optional=True),
+        _ptr(y, "y", st, shape), _ptr(final_state, "final_state", st, ss, optional=True), _stream(stream))
+    _check("cfc_conv_forward", status)
+
+
+def cfc_conv_backward(x, weight, grad_y, grad_x, grad_weight, workspace, bias=None, grad_bias=None, seq_offsets=None,
+                      initial_state=None, grad_final_state=None, grad_initial_state=None, silu=True, math=MATH_BF16,
+                      stream=None):
+    """Backward of cfc_conv_forward from its inputs; every gradient is overwritten."""
+    st, f32, shape, d, w, args = _conv_inputs(x, weight, bias, math)
+    off, n, rows = _row_sequences(shape, seq_offsets)
+    ss = (n, w - 1, d)
+    status = load_library().cfc_conv_backward(
+        *args, off, n, rows, d, w, 1 if silu else 0, math, _ptr(initial_state, "initial_state", st, ss, optional=True),
+        _ptr(grad_y, "grad_y", st, shape), _ptr(grad_final_state, "grad_final_state", st, ss, optional=True),
+        _ptr(grad_x, "grad_x", st, shape), _ptr(grad_weight, "grad_weight", f32, (d, w)),
+        _ptr(grad_bias, "grad_bias", f32, (d,), optional=True),
+        _ptr(grad_initial_state, "grad_initial_state", st, ss, optional=True),
+        _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
+    _check("cfc_conv_backward", status)
+
+
+def _pool(state, name, dtype, tail):
+    shape = state.shape
+    if len(shape) != len(tail) + 1 or shape[1:] != tail:
+        raise ValueError(f"{name} must have shape (slots, {', '.join(map(str, tail))}), got {tuple(shape)}")
+    return _ptr(state, name, dtype), shape[0]
+
+
+def cfc_conv_step(x, weight, state, y, bias=None, slots=None, silu=True, math=MATH_BF16, stream=None):
+    """The next tokens x [sequences, tokens, channels] of decoding sequences: sequence
+    i's last inputs are ``state[slots[i]]`` (int32 on the device; ``state[i]`` if
+    None), [slots, width - 1, channels], updated in place."""
+    st, f32, shape, d, w, args = _conv_inputs(x, weight, bias, math)
+    if len(shape) != 3:
+        raise ValueError("x must be [sequences, tokens, channels]")
+    n, tokens, _ = shape
+    status = load_library().cfc_conv_step(
+        *args, n, tokens, d, w, 1 if silu else 0, math, *_pool(state, "state", st, (w - 1, d)),
+        _ptr(slots, "slots", _torch().int32, (n,), optional=True), _ptr(y, "y", st, shape), _stream(stream))
+    _check("cfc_conv_step", status)
+
+
+def cfc_ssm_workspace_bytes(rows, n_seq, channels, groups, n_states, math=MATH_BF16, save=False) -> int:
+    return int(load_library().cfc_ssm_workspace_bytes(rows, n_seq, channels, groups, n_states, math, 1 if save else 0))
+
+
+def _ssm_inputs(x, delta, A, B, C, D, z, delta_bias, math):
+    """What the three calls share: the stored type, fp32, the shapes of x and of B,
+    (channels, groups, states), and the leading C arguments."""
+    st, f32, shape, bs = _storage_dtype(math), _torch().float32, x.shape, B.shape
+    d = shape[-1]
+    if len(bs) != len(shape) + 1 or bs[:-2] != shape[:-1]:
+        raise ValueError("B must be [..., groups, states] with the leading axes of x")
+    g, n = bs[-2:]
+    zp, ldz = (None, d) if z is None else _spaced(z, "z", st, shape)
+    args = (*_spaced(x, "x", st, shape), *_spaced(delta, "delta", st, shape), _ptr(A, "A", f32, (d, n)),
+            *_spaced(B, "B", st, bs, 2), *_spaced(C, "C", st, bs, 2), _ptr(D, "D", f32, (d,), optional=True), zp, ldz,
+            _ptr(delta_bias, "delta_bias", f32, (d,), optional=True))
+    return st, f32, shape, bs, (d, g, n), args
+
+
+def cfc_ssm_forward(x, delta, A, B, C, y, workspace, D=None, z=None, delta_bias=None, seq_offsets=None, initial_state=None,
+                    final_state=None, save=False, math=MATH_BF16, stream=None):
+    """Selective scan over whole sequences: x, delta, z and y [sequences, tokens,
+    channels], B, C [sequences, tokens, groups, states], A [channels, states]; or
+    [rows, ...] packed, with int32 seq_offsets [sequences + 1] on the device.
+    States [sequences, channels, states] are fp32."""
+    st, f32, shape, _, sizes, args = _ssm_inputs(x, delta, A, B, C, D, z, delta_bias, math)
+    off, n, rows = _row_sequences(shape, seq_offsets)
+    ss = (n, sizes[0], sizes[2])
+    status = load_library().cfc_ssm_forward(
+        *args, off, n, rows, *sizes, math, _ptr(initial_state, "initial_state", f32, ss, optional=True),
+        _ptr(y, "y", st, shape), _ptr(final_state, "final_state", f32, ss, optional=True), 1 if save else 0,
+        _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
+    _check("cfc_ssm_forward", status)
+
+
+def cfc_ssm_backward(x, delta, A, B, C, grad_y, grad_x, grad_delta, grad_A, grad_B, grad_C, workspace, D=None, z=None,
+                     delta_bias=None, grad_D=None, grad_z=None, grad_delta_bias=None, seq_offsets=None, initial_state=None,
+                     grad_final_state=None, grad_initial_state=None, math=MATH_BF16, stream=None):
+    """Backward of the cfc_ssm_forward(save=True) that filled ``workspace``; every gradient is overwritten:
+    those of x, delta, z, B and C in their type, the others in fp32."""
+    st, f32, shape, bs, sizes, args = _ssm_inputs(x, delta, A, B, C, D, z, delta_bias, math)
+    off, n, rows = _row_sequences(shape, seq_offsets)
+    d, _, N = sizes
+    ss = (n, d, N)
+    status = load_library().cfc_ssm_backward(
+        *args, off, n, rows, *sizes, math, _ptr(initial_state, "initial_state", f32, ss, optional=True),
+        _ptr(grad_y, "grad_y", st, shape), _ptr(grad_final_state, "grad_final_state", f32, ss, optional=True),
+        _ptr(grad_x, "grad_x", st, shape), _ptr(grad_delta, "grad_delta", st, shape), _ptr(grad_A, "grad_A", f32, (d, N)),
+        _ptr(grad_B, "grad_B", st, bs), _ptr(grad_C, "grad_C", st, bs), _ptr(grad_D, "grad_D", f32, (d,), optional=True),
+        _ptr(grad_z, "grad_z", st, shape, optional=True),
+        _ptr(grad_delta_bias, "grad_delta_bias", f32, (d,), optional=True),
+        _ptr(grad_initial_state, "grad_initial_state", f32, ss, optional=True),
+        _ptr(workspace, "workspace", _torch().uint8), workspace.numel(), _stream(stream))
+    _check("cfc_ssm_backward", status)
+
+
+def cfc_ssm_step(x, delta, A, B, C, state, y, D=None, z=None, delta_bias=None, slots=None, math=MATH_BF16, stream=None):
+    """The next tokens of decoding sequences (shapes as for cfc_ssm_forward,
+    [sequences, tokens, ...]): sequence i's state is ``state[slots[i]]`` (int32 on
+    the device; ``state[i]`` if None), updated in place."""
+    st, f32, shape, _, sizes, args = _ssm_inputs(x, delta, A, B, C, D, z, delta_bias, math)
+    if len(shape) != 3:
+        raise ValueError("x must be [sequences, tokens, channels]")
+    n, tokens, d = shape
+    status = load_library().cfc_ssm_step(
+        *args, n, tokens, *sizes, math, *_pool(state, "state", f32, (d, sizes[2])),
+        _ptr(slots, "slots", _torch().int32, (n,), optional=True), _ptr(y, "y", st, shape), _stream(stream))
+    _check("cfc_ssm_step", status)
+
+
+def cfc_grad_clip_workspace_bytes(count: int) -> int:
+    return int(load_library().cfc_grad_clip_workspace_bytes(count))
+
+
+def _tensor_list(tensors, name):
+    """Host arrays of the pointers, sizes and types of contiguous tensors."""
+    torch = _torch()
+    n = len(tensors)
+    kinds = {torch.float32: MATH_FP32, torch.bfloat16: MATH_BF16}
+    ptrs, sizes, maths = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name}[{i}] must be a CUDA tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        m = kinds.get(t.dtype)
+        if m is None:
+            raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
+        ptrs[i], sizes[i], maths[i] = t.data_ptr(), t.numel(), m
+    return ptrs, sizes, maths
+
+
+def cfc_grad_norm(grads, norm, workspace, stream=None):
+    """norm [1] = the square root of the sum of all squares of the tensors (float32 or bfloat16, in any mixture)."""
+    grads = list(grads)
+    ptrs, sizes, maths = _tensor_list(grads, "grads")
+    torch = _torch()
+    status = load_library().cfc_grad_norm(ptrs, sizes, maths, len(grads), _ptr(norm, "norm", torch.float32, (1,)),
+                                          _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("cfc_grad_norm", status)
+
+
+def cfc_grad_clip(grads, max_norm, norm, workspace, out=None, stream=None):
+    """norm [1] of the tensors together, and each scaled by min(1, max_norm / (norm + 1e-6)):
+    in place, or into the tensors of out (alike in shape and type)."""
+    grads = list(grads)
+    ptrs, sizes, maths = _tensor_list(grads, "grads")
+    outs = ptrs
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("out must have as many tensors as grads")
+        outs, osizes, omaths = _tensor_list(out, "out")
+        if osizes[:] != sizes[:] or omaths[:] != maths[:]:
+            raise ValueError("out must have the sizes and types of grads")
+    written = [p for p, n in zip(outs, sizes) if n]
+    if len(set(written)) != len(written):
+        raise ValueError("a tensor is written twice")
+    torch = _torch()
+    status = load_library().cfc_grad_clip(ptrs, outs, sizes, maths, len(grads), max_norm, _ptr(norm, "norm", torch.float32, (1,)),
+                                          _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+    _check("cfc_grad_clip", status)
 
 
 def reduce_axis0_multi(per_batch, out, stream=None):

@@ -136,6 +136,7 @@ const char* cfc_status_string(int status) {
     case CFC_ERR_LAUNCH: return "kernel launch failed";
     case CFC_ERR_DEVICE: return "no usable CUDA device";
     case CFC_ERR_TOO_LARGE: return "sizes need more workspace than CFC_STATIC_WORKSPACE_BYTES";
+    case CFC_ERR_OVERLAP: return "buffers that must not overlap do";
     default: return "unknown status";
   }
 }

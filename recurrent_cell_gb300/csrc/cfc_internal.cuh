@@ -307,6 +307,66 @@ cudaError_t launch_rmsnorm_backward(const void* s, const float* w, const float* 
                                     const void* grad_residual_out, long long rows, int d, int math, void* grad_x,
                                     float* grad_w, float* part, cudaStream_t st);
 
+// Residual layer norm (cfc_layernorm.cu).
+size_t layernorm_workspace(long long rows, int d);
+cudaError_t launch_layernorm_forward(const void* x, const void* residual, const float* w, const float* b, long long rows,
+                                     int d, float eps, int math, void* y, void* residual_out, float* mean, float* rstd,
+                                     cudaStream_t s);
+cudaError_t launch_layernorm_backward(const void* s, const float* w, const float* mean, const float* rstd,
+                                      const void* grad_y, const void* grad_residual_out, long long rows, int d, int math,
+                                      void* grad_x, float* grad_w, float* grad_b, float* part, cudaStream_t st);
+
+// Global gradient norm and clipping (cfc_clip.cu): host arrays of `count` tensors,
+// checked; out NULL: the norm alone.
+constexpr long long kMaxGradValues = 1ll << 35;  // of a tensor
+size_t grad_workspace(int count);
+cudaError_t launch_grad_norm(const void* const* in, void* const* out, const long long* n, const int* math, int count,
+                             float most, float* norm, double* sums, cudaStream_t s);
+
+// Short causal convolution (cfc_conv.cu).
+constexpr int kMaxConvWidth = 8;
+struct ConvArgs {
+  const void* x;
+  long long ldx;
+  const float *weight, *bias;
+  const void* init;
+  const int* off;
+  int n_seq;
+  long long rows;
+  int d, width, silu, math;
+};
+size_t conv_workspace(long long rows, int d, int width);
+cudaError_t launch_conv_forward(const ConvArgs& g, void* y, void* final_state, cudaStream_t s);
+cudaError_t launch_conv_backward(const ConvArgs& g, const void* grad_y, const void* grad_final, void* grad_x, float* grad_w,
+                                 float* grad_b, void* grad_init, float* part, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& g, int tokens, void* state, long long n_slots, const int* slots, void* y,
+                             cudaStream_t s);
+
+// Selective scan (cfc_ssm.cu, cfc_ssm_bwd.cu, cfc_ssm_step.cu).
+constexpr int kMaxSsmStates = 64;
+struct SsmArgs {
+  const void *x, *delta, *z, *B, *C;
+  long long ldx, ldd, ldz, ldb, ldc;
+  const float *A, *D, *bias;
+  const int* off;
+  int n_seq;
+  long long rows;
+  int d, groups, N, math;
+  const float* init;
+  char* ws;
+};
+struct SsmGrads {
+  const void* grad_y;
+  const float* grad_final;
+  void *grad_x, *grad_delta, *grad_z, *grad_B, *grad_C;
+  float *grad_A, *grad_D, *grad_bias, *grad_init;
+};
+size_t ssm_workspace(long long rows, int n_seq, int d, int groups, int N, int save);
+cudaError_t launch_ssm_forward(const SsmArgs& g, void* y, float* final_state, int save, cudaStream_t s);
+cudaError_t launch_ssm_backward(const SsmArgs& g, const SsmGrads& r, cudaStream_t s);
+cudaError_t launch_ssm_step(const SsmArgs& g, int tokens, float* state, long long n_slots, const int* slots, void* y,
+                            cudaStream_t s);
+
 cudaError_t launch_wgrad_simt(const Layout& L, const CfcArgs& a, float* out, int n_split,
                               long long rows_per_split, cudaStream_t s);
 

@@ -1,0 +1,279 @@
+// cfc_ssm.cu -- the selective scan over whole sequences, forward (ssm_common.cuh
+// has the formulas and the split).
+//
+//   k_ssm<., true>   the end state of each segment from its own rows, and its sum of dt
+//   k_ssm_carry      the states between segments: h_s = local_s + exp(A sum dt) h_{s-1}
+//   k_ssm<., false>  the scan itself
+//
+// The first two run only where segments cut sequences.
+#include "ssm_common.cuh"
+
+namespace cfc {
+namespace ssm {
+
+template <class G, bool LOCAL>
+struct __align__(16) FwdTiles {
+  float dt[kT][G::CW], dx[kT][G::CW];        // dt, dt x
+  float B[kT][G::NP];
+  float C[LOCAL ? 1 : kT][G::NP];
+  float y[LOCAL ? 1 : kT][4][G::CW];         // C . h, a part from each state lane
+};
+
+template <class G, bool LOCAL>
+__global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
+  using E = typename G::E;
+  constexpr int CPL = G::CPL, NS = G::NS, P = G::P, VN = G::VN;
+  __shared__ FwdTiles<G, LOCAL> sm;
+  const Tile<G> w(a, blockIdx.x);
+  const int seg = blockIdx.y;
+  float h[CPL][NS];
+
+  if (!LOCAL && seg >= a.n_seg) {            // the states after sequences without rows
+    const int step = (gridDim.y - a.n_seg) * 32;
+    for (long long i0 = (long long)(seg - a.n_seg) * 32; i0 < a.s.n; i0 += step) {
+      long long begin = 0, end = 1;
+      if (i0 + w.lane < a.s.n) seqs::range_of(a.s, (int)(i0 + w.lane), &begin, &end);
+      unsigned none = __ballot_sync(0xffffffffu, begin >= end);
+      while (none) {
+        const long long i = i0 + __ffs(none) - 1;
+        none &= none - 1;
+        load_state<G>(a, w, a.init, i, h);
+        store_state<G>(a, w, a.final_state, i, h);
+      }
+    }
+    return;
+  }
+
+  const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
+  Where q;
+  long long row = r0;
+  if constexpr (LOCAL) {
+    q = seqs::find(a.s, r1 - 1);
+    const bool cut = q.end > r1, starts = q.begin >= r0;
+    if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (starts ? kStarts : 0);
+    if (!cut) return;
+    if (starts) row = q.begin;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+      for (int j = 0; j < NS; ++j) h[i][j] = 0.f;
+  } else {
+    q = seqs::find(a.s, r0);
+    if (q.begin < r0) load_lanes<G>(a.local, (long long)(seg - 1) * a.tiles + blockIdx.x, w.lane, h);
+  }
+  float A2[CPL][NS];
+  load_A<G>(a, w, A2);
+  float bias[VN], D[VN], sum[CPL] = {};
+#pragma unroll
+  for (int e = 0; e < VN; ++e) {
+    const bool in = w.col() < w.cols;
+    bias[e] = a.bias && in ? __ldg(a.bias + w.c0 + w.col() + e) : 0.f;
+    D[e] = !LOCAL && a.D && in ? __ldg(a.D + w.c0 + w.col() + e) : 0.f;
+  }
+
+  uint4 xv[P], dv[P], zv[P];
+  Rows<G> bv, cv;
+  auto fetch = [&](long long at) {
+    const int n = r1 - at < kT ? (int)(r1 - at) : kT;      // none behind the segment
+    load_raw<G>(w, a.x, a.ldx, at, n, xv);
+    load_raw<G>(w, a.delta, a.ldd, at, n, dv);
+    bv.fetch(a, w, a.B, a.ldb, at, n);
+    if (!LOCAL) cv.fetch(a, w, a.C, a.ldc, at, n);
+  };
+  fetch(row);
+  for (int chunk = 0; row < r1; row += kT, ++chunk) {
+    const int n = r1 - row < kT ? (int)(r1 - row) : kT;
+    if (!LOCAL && save) store_lanes<G>(a.ckpt, ((long long)seg * a.cps + chunk) * a.tiles + blockIdx.x, w.lane, h);
+    float xk[P][LOCAL ? 1 : VN];                           // D x
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      float x[VN], dl[VN], dt[VN];
+      Unpack<E>::get(x, xv[k]);
+      Unpack<E>::get(dl, dv[k]);
+#pragma unroll
+      for (int e = 0; e < VN; ++e) {
+        dt[e] = softplus(dl[e] + bias[e]);
+        if constexpr (!LOCAL) xk[k][e] = D[e] * x[e];
+        x[e] *= dt[e];
+      }
+      if (w.row(k) < kT) {
+        put(&sm.dt[w.row(k)][w.col()], dt);
+        put(&sm.dx[w.row(k)][w.col()], x);
+      }
+    }
+    bv.stage(a, w, a.B, a.ldb, row, n, sm.B[0]);
+    if constexpr (!LOCAL) {
+      cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
+      if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
+    }
+    __syncwarp();
+    fetch(row + kT);
+    for (int t = 0; t < n;) {
+      if (row + t == q.begin) load_state<G>(a, w, a.init, q.i, h);
+      const int m = q.end - row < n ? (int)(q.end - row) : n;
+      for (; t < m; ++t) {
+        float dt[CPL], dx[CPL], b[NS], c[NS], y[CPL];
+        get(&sm.dt[t][w.cl * CPL], dt);
+        get(&sm.dx[t][w.cl * CPL], dx);
+        get(&sm.B[t][w.sl * NS], b);
+        if constexpr (!LOCAL) get(&sm.C[t][w.sl * NS], c);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+          y[i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
+            if constexpr (!LOCAL) y[i] = fmaf(c[j], h[i][j], y[i]);
+          }
+          if constexpr (LOCAL) sum[i] += dt[i];
+        }
+        if constexpr (!LOCAL) put(&sm.y[t][w.sl][w.cl * CPL], y);
+      }
+      if (!LOCAL && row + t == q.end) {
+        if (a.final_state) store_state<G>(a, w, a.final_state, q.i, h);
+        if (row + t < a.s.rows) q = seqs::find(a.s, row + t);
+      }
+    }
+    __syncwarp();
+    if constexpr (!LOCAL) {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (w.row(k) < n && w.col() < w.cols) {
+          float y[VN], z[VN];
+#pragma unroll
+          for (int e = 0; e < VN; ++e) y[e] = xk[k][e];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            get(&sm.y[w.row(k)][s][w.col()], z);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) y[e] += z[e];
+          }
+          if (a.z) {
+            Unpack<E>::get(z, zv[k]);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) y[e] *= z[e] * sigmoid(z[e]);
+          }
+          E* to = static_cast<E*>(a.y) + (row + w.row(k)) * a.d + w.c0 + w.col();
+          __stcs(reinterpret_cast<uint4*>(to), Unpack<E>::make(y));
+        }
+    }
+  }
+  if constexpr (LOCAL) {
+    const long long block = (long long)seg * a.tiles + blockIdx.x;
+    store_lanes<G>(a.local, block, w.lane, h);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) a.sdt[(block * CPL + i) * 32 + w.lane] = sum[i];
+  }
+}
+
+// Thread: one state of a tile, over the segments in turn; local becomes the state at
+// each segment's end.  BWD: the gradients' carries, over the segments from the last.
+constexpr int kCarryThreads = 128;
+template <class G, bool BWD>
+__global__ void __launch_bounds__(kCarryThreads) k_ssm_carry(Args a) {
+  constexpr int CN = G::CPL * G::NS;
+  const long long id = (long long)blockIdx.x * kCarryThreads + threadIdx.x;      // (tile, pair, lane, one of the pair)
+  if (id >= (long long)a.tiles * CN * 32) return;
+  const int in = (int)(id % (CN * 32)), tile = (int)(id / (CN * 32));
+  const int pair = in / 64, lane = in / 2 % 32, k = pair * 2 + in % 2, i = k / G::NS, j = k % G::NS;
+  const int c = tile % a.tpg * G::CW + (lane >> 2) * G::CPL + i, n = (lane & 3) * G::NS + j;
+  if (c >= a.per || n >= a.N) return;
+  const float A2 = __ldg(a.A + ((long long)(tile / a.tpg) * a.per + c) * a.N + n) * kLog2e;
+  float carry = 0.f;
+  constexpr int AHEAD = 8;                   // segments fetched together: only the sum is serial
+  for (int t0 = 0; t0 < a.n_seg; t0 += AHEAD) {
+    float v[AHEAD], d[AHEAD];
+    int f[AHEAD];
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t)
+      if (t0 + t < a.n_seg) {
+        const int s = BWD ? a.n_seg - 1 - t0 - t : t0 + t;
+        const long long block = (long long)s * a.tiles + tile;
+        f[t] = a.flags[s];
+        v[t] = a.local[block * CN * 32 + in];
+        d[t] = a.sdt[(block * G::CPL + i) * 32 + lane];
+      }
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t)
+      if (t0 + t < a.n_seg && (f[t] & kCut)) {   // (else nothing is handed on, and what follows starts afresh)
+        const int s = BWD ? a.n_seg - 1 - t0 - t : t0 + t;
+        carry = f[t] & kStarts ? v[t] : fmaf(ex2(A2 * d[t]), carry, v[t]);
+        a.local[((long long)s * a.tiles + tile) * CN * 32 + in] = carry;
+      }
+  }
+}
+
+template <class G>
+static cudaError_t forward(const Args& a, const Plan& p, bool save, cudaStream_t st) {
+  if (p.cut) {
+    {
+      TraceScope tr("k_ssm_local", st);
+      k_ssm<G, true><<<dim3(a.tiles, a.n_seg), 32, 0, st>>>(a, false);
+    }
+    TraceScope tr("k_ssm_carry", st);
+    const long long n = (long long)a.tiles * G::CPL * G::NS * 32;
+    k_ssm_carry<G, false><<<(unsigned)((n + kCarryThreads - 1) / kCarryThreads), kCarryThreads, 0, st>>>(a);
+  }
+  // warps behind the segments look for sequences without rows
+  const bool empty = a.final_state && (a.s.off || a.s.rows == 0);
+  const int more = empty ? (a.s.n < 32 * 64 ? (a.s.n + 31) / 32 : 64) : 0;
+  if (a.n_seg + more == 0) return cudaSuccess;
+  TraceScope tr("k_ssm", st);
+  k_ssm<G, false><<<dim3(a.tiles, a.n_seg + more), 32, 0, st>>>(a, save);
+  return cudaGetLastError();
+}
+
+template <class E>
+static cudaError_t forward_of(const Args& a, const Plan& p, bool save, cudaStream_t st) {
+  switch (p.NS) {
+    case 2: return forward<Cfg<E, 2, 4>>(a, p, save, st);
+    case 4: return forward<Cfg<E, 4, 4>>(a, p, save, st);
+    case 8: return forward<Cfg<E, 8, 2>>(a, p, save, st);
+    default: return forward<Cfg<E, 16, 1>>(a, p, save, st);
+  }
+}
+
+Args args_of(const SsmArgs& g, const Plan& p, const Work& k) {
+  Args a{};
+  a.x = g.x; a.delta = g.delta; a.z = g.z; a.B = g.B; a.C = g.C;
+  a.ldx = g.ldx; a.ldd = g.ldd; a.ldz = g.ldz; a.ldb = g.ldb; a.ldc = g.ldc;
+  a.A = g.A; a.D = g.D; a.bias = g.bias;
+  a.s = seqs::make_seqs(g.off, g.n_seq, g.rows);
+  a.d = g.d; a.groups = g.groups; a.N = g.N; a.per = g.d / g.groups; a.tpg = p.tpg;
+  const int size = g.math == CFC_MATH_BF16 ? 2 : 4;
+  a.vec_bc = g.N == 4 * p.NS &&
+             (reinterpret_cast<uintptr_t>(g.B) | reinterpret_cast<uintptr_t>(g.C) | (uintptr_t)(g.ldb * size) |
+              (uintptr_t)(g.ldc * size)) % 16 == 0;
+  a.S = p.S; a.n_seg = p.n_seg; a.tiles = p.tiles; a.cps = p.cps;
+  a.init = g.init;
+  a.flags = reinterpret_cast<int*>(g.ws + k.flags);
+  a.local = reinterpret_cast<float*>(g.ws + k.local);
+  a.sdt = reinterpret_cast<float*>(g.ws + k.sdt);
+  a.ckpt = reinterpret_cast<float*>(g.ws + k.ckpt);
+  a.part = reinterpret_cast<float*>(g.ws + k.part);
+  a.bc = reinterpret_cast<float*>(g.ws + k.bc);
+  return a;
+}
+
+}  // namespace ssm
+
+size_t ssm_workspace(long long rows, int n_seq, int d, int groups, int N, int save) {
+  size_t most = 0;
+  for (int packed = 0; packed < 2; ++packed) {
+    const ssm::Plan p = ssm::make_plan(rows, n_seq, d, groups, N, packed != 0);
+    const size_t n = ssm::make_work(p, rows, d, save != 0).total;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+cudaError_t launch_ssm_forward(const SsmArgs& g, void* y, float* final_state, int save, cudaStream_t st) {
+  const ssm::Plan p = ssm::make_plan(g.rows, g.n_seq, g.d, g.groups, g.N, g.off != nullptr);
+  ssm::Args a = ssm::args_of(g, p, ssm::make_work(p, g.rows, g.d, save != 0));
+  a.y = y;
+  a.final_state = final_state;
+  return g.math == CFC_MATH_BF16 ? ssm::forward_of<__nv_bfloat16>(a, p, save != 0, st)
+                                 : ssm::forward_of<float>(a, p, save != 0, st);
+}
+
+}  // namespace cfc
