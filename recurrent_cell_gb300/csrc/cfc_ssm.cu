@@ -166,43 +166,6 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
   }
 }
 
-// Thread: one state of a tile, over the segments in turn; local becomes the state at
-// each segment's end.  BWD: the gradients' carries, over the segments from the last.
-constexpr int kCarryThreads = 128;
-template <class G, bool BWD>
-__global__ void __launch_bounds__(kCarryThreads) k_ssm_carry(Args a) {
-  constexpr int CN = G::CPL * G::NS;
-  const long long id = (long long)blockIdx.x * kCarryThreads + threadIdx.x;      // (tile, pair, lane, one of the pair)
-  if (id >= (long long)a.tiles * CN * 32) return;
-  const int in = (int)(id % (CN * 32)), tile = (int)(id / (CN * 32));
-  const int pair = in / 64, lane = in / 2 % 32, k = pair * 2 + in % 2, i = k / G::NS, j = k % G::NS;
-  const int c = tile % a.tpg * G::CW + (lane >> 2) * G::CPL + i, n = (lane & 3) * G::NS + j;
-  if (c >= a.per || n >= a.N) return;
-  const float A2 = __ldg(a.A + ((long long)(tile / a.tpg) * a.per + c) * a.N + n) * kLog2e;
-  float carry = 0.f;
-  constexpr int AHEAD = 8;                   // segments fetched together: only the sum is serial
-  for (int t0 = 0; t0 < a.n_seg; t0 += AHEAD) {
-    float v[AHEAD], d[AHEAD];
-    int f[AHEAD];
-#pragma unroll
-    for (int t = 0; t < AHEAD; ++t)
-      if (t0 + t < a.n_seg) {
-        const int s = BWD ? a.n_seg - 1 - t0 - t : t0 + t;
-        const long long block = (long long)s * a.tiles + tile;
-        f[t] = a.flags[s];
-        v[t] = a.local[block * CN * 32 + in];
-        d[t] = a.sdt[(block * G::CPL + i) * 32 + lane];
-      }
-#pragma unroll
-    for (int t = 0; t < AHEAD; ++t)
-      if (t0 + t < a.n_seg && (f[t] & kCut)) {   // (else nothing is handed on, and what follows starts afresh)
-        const int s = BWD ? a.n_seg - 1 - t0 - t : t0 + t;
-        carry = f[t] & kStarts ? v[t] : fmaf(ex2(A2 * d[t]), carry, v[t]);
-        a.local[((long long)s * a.tiles + tile) * CN * 32 + in] = carry;
-      }
-  }
-}
-
 template <class G>
 static cudaError_t forward(const Args& a, const Plan& p, bool save, cudaStream_t st) {
   if (p.cut) {
@@ -210,9 +173,8 @@ static cudaError_t forward(const Args& a, const Plan& p, bool save, cudaStream_t
       TraceScope tr("k_ssm_local", st);
       k_ssm<G, true><<<dim3(a.tiles, a.n_seg), 32, 0, st>>>(a, false);
     }
-    TraceScope tr("k_ssm_carry", st);
-    const long long n = (long long)a.tiles * G::CPL * G::NS * 32;
-    k_ssm_carry<G, false><<<(unsigned)((n + kCarryThreads - 1) / kCarryThreads), kCarryThreads, 0, st>>>(a);
+    const cudaError_t e = launch_ssm_carry<G, false>(a, st);
+    if (e != cudaSuccess) return e;
   }
   // warps behind the segments look for sequences without rows
   const bool empty = a.final_state && (a.s.off || a.s.rows == 0);

@@ -1,4 +1,504 @@
+// cfc_ssm_bwd.cu -- the selective scan's backward (ssm_common.cuh has the formulas of
+// the forward and the split of rows and channels).
+//
+// With g = grad_y silu(z), a_t = exp(dt_t A), h_t the state after token t and dh_t
+// the gradient that reaches it,
+//   dh_t  = C_t g_t + a_{t+1} dh_{t+1},    e_t = dh_t a_t h_{t-1}   (per channel and state)
+//   dx    = dt sum_n dh B + D g            ddt = sum_n e A + x sum_n dh B
+//   dA    = sum_t dt e                     ddelta = ddt sigmoid(delta + bias)
+//   dB    = sum_c dt x dh                  dC = sum_c g h
+//   dz    = grad_y (C . h + D x) silu'(z)  dD = sum_t g x,  dbias = sum_t ddelta
+// A chunk starts from the state that the forward saved before it.  A first sweep runs
+// it forward and keeps the state before every second token; the second goes back
+// and forms the state in between anew (one multiply-add, since it needs a anyway), which
+// halves the shared memory that states take.  The two exponentials and some fifteen multiply-adds
+// a state are the bound, not memory.
+//
+// Sums over a channel's states and over a tile's channels are taken by lane steps that
+// halve the values as they go: 12 values over 4 lanes in 9 steps, 8 over 8 in 7.  Four
+// warps of a block add their dB and dC in shared memory, so that what goes to the
+// workspace is a sum over 128 channels; k_ssm_bc adds those.  dA, dD and dbias are
+// kept in registers over a segment; reduce_axis0 adds the segments.
 #include "ssm_common.cuh"
+
 namespace cfc {
-cudaError_t launch_ssm_backward(const SsmArgs& g, const SsmGrads& r, cudaStream_t s) { return cudaErrorNotSupported; }
+namespace ssm {
+
+constexpr int kBwdWarps = 4;
+
+template <class G>
+struct __align__(16) BwdTiles {
+  float dt[kT][G::CW], dx[kT][G::CW], g[kT][G::CW];          // dt, dt x, g
+  float B[kT][G::NP], C[kT][G::NP];
+  float s1[kT][G::CW], s2[kT][G::CW], y[kT][G::CW];          // sum dh B, sum e A, C . h
+  float bc[kT][2 * G::NP];                                   // dB, dC of the tile
+  float2 h[kT / 2][G::CPL * G::NS / 2][32];                  // states before rows 0, 2, 4, ...
+};
+
+// One value of each lane's quarter: v[i] summed over the lanes of a group of 4
+// (M = 1, 2) or 8 (M = 4, 8, 16), value i of N ending up in the lanes whose bits of M say i.
+template <int N>
+__device__ __forceinline__ void fold(float (&v)[N], int lane, int m) {
+  const bool up = lane & m;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float keep = up ? v[2 * i + 1] : v[2 * i], send = up ? v[2 * i] : v[2 * i + 1];
+    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+  }
 }
+template <int N>
+__device__ __forceinline__ float all(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
+
+// Sums over the 4 state lanes of v[CPL]: lane sl has channel sl % CPL's.
+template <int CPL>
+__device__ __forceinline__ float over_states(float (&v)[CPL], int lane) {
+  if constexpr (CPL == 4) {
+    fold<4>(v, lane, 1);
+    float u[2] = {v[0], v[1]};
+    fold<2>(u, lane, 2);
+    return u[0];
+  } else if constexpr (CPL == 2) {
+    fold<2>(v, lane, 1);
+    return all<1>(v[0], 2);
+  } else {
+    return all<1>(all<1>(v[0], 1), 2);
+  }
+}
+// Sums over the 8 channel lanes of v[N], N = 4, 8, 16 or 32: lane cl has those of
+// values cl + 8 k, in v[k] (N = 4: value cl % 4's).
+template <int N>
+__device__ __forceinline__ void over_channels(float (&v)[N], int lane) {
+  if constexpr (N == 4) {
+    fold<4>(v, lane, 4);
+    float u[2] = {v[0], v[1]};
+    fold<2>(u, lane, 8);
+    v[0] = all<1>(u[0], 16);
+  } else {
+    // value 8 k + 4 b2 + 2 b1 + b0 after folding by b0, b1, b2
+    fold<N>(v, lane, 4);
+    float u[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) u[i] = v[i];
+    fold<N / 2>(u, lane, 8);
+    float t[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) t[i] = u[i];
+    fold<N / 4>(t, lane, 16);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) v[i] = t[i];
+  }
+}
+
+// dt, dt x and g of a chunk's tokens, into the tiles.  dx = nullptr: only dt and g.
+template <class G>
+__device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const float (&bias)[G::VN],
+                                             float (*dt)[G::CW], float (*dx)[G::CW], float (*g)[G::CW]) {
+  using U = Unpack<typename G::E>;
+  constexpr int VN = G::VN;
+  uint4 xv[G::P], dv[G::P], zv[G::P], gv[G::P];
+  if (dx) load_raw<G>(w, a.x, a.ldx, row, n, xv);
+  load_raw<G>(w, a.delta, a.ldd, row, n, dv);
+  load_raw<G>(w, a.grad_y, a.d, row, n, gv);
+  if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
+#pragma unroll
+  for (int k = 0; k < G::P; ++k) {
+    float f[VN], t[VN], u[VN];
+    U::get(t, dv[k]);
+#pragma unroll
+    for (int e = 0; e < VN; ++e) t[e] = softplus(t[e] + bias[e]);
+    U::get(f, gv[k]);
+    if (a.z) {
+      U::get(u, zv[k]);
+#pragma unroll
+      for (int e = 0; e < VN; ++e) f[e] *= u[e] * sigmoid(u[e]);
+    }
+    if (w.row(k) < kT) {
+      put(&dt[w.row(k)][w.col()], t);
+      put(&g[w.row(k)][w.col()], f);
+    }
+    if (dx) {
+      U::get(u, xv[k]);
+#pragma unroll
+      for (int e = 0; e < VN; ++e) u[e] *= t[e];
+      if (w.row(k) < kT) put(&dx[w.row(k)][w.col()], u);
+    }
+  }
+}
+template <class G>
+__device__ __forceinline__ void load_bias(const Args& a, const Tile<G>& w, float (&bias)[G::VN]) {
+#pragma unroll
+  for (int e = 0; e < G::VN; ++e) bias[e] = a.bias && w.col() < w.cols ? __ldg(a.bias + w.c0 + w.col() + e) : 0.f;
+}
+
+// What a segment's own rows send to the state before it, and its sum of dt: for the
+// segments whose first row continues a sequence.
+template <class G>
+struct __align__(16) LocalTiles {
+  float dt[kT][G::CW], g[kT][G::CW], C[kT][G::NP];
+};
+template <class G>
+__global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
+  constexpr int CPL = G::CPL, NS = G::NS;
+  __shared__ LocalTiles<G> sm;
+  const Tile<G> w(a, blockIdx.x);
+  const int seg = blockIdx.y;
+  const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
+  const Where q = seqs::find(a.s, r0);
+  const bool cut = q.begin < r0, ends = q.end <= r1;
+  if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (ends ? kStarts : 0);
+  if (!cut) return;
+  const long long last = ends ? q.end : r1;
+  float A2[CPL][NS], dh[CPL][NS], sum[CPL] = {}, bias[G::VN];
+  load_A<G>(a, w, A2);
+  load_bias<G>(a, w, bias);
+  load_state<G>(a, w, ends ? a.grad_final : nullptr, q.i, dh);
+  Rows<G> cv;
+  for (long long row = r0 + (last - r0 - 1) / kT * kT; row >= r0; row -= kT) {
+    const int n = last - row < kT ? (int)(last - row) : kT;
+    cv.fetch(a, w, a.C, a.ldc, row, n);
+    stage_tokens<G>(a, w, row, n, bias, sm.dt, nullptr, sm.g);
+    cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
+    __syncwarp();
+    for (int t = n - 1; t >= 0; --t) {
+      float dt[CPL], g[CPL], c[NS];
+      get(&sm.dt[t][w.cl * CPL], dt);
+      get(&sm.g[t][w.cl * CPL], g);
+      get(&sm.C[t][w.sl * NS], c);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) dh[i][j] = ex2(dt[i] * A2[i][j]) * fmaf(c[j], g[i], dh[i][j]);
+        sum[i] += dt[i];
+      }
+    }
+    __syncwarp();
+  }
+  const long long block = (long long)seg * a.tiles + blockIdx.x;
+  store_lanes<G>(a.local, block, w.lane, dh);
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) a.sdt[(block * CPL + i) * 32 + w.lane] = sum[i];
+}
+
+template <class G>
+__global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
+  using E = typename G::E;
+  using U = Unpack<E>;
+  constexpr int CPL = G::CPL, NS = G::NS, VN = G::VN, NP = G::NP;
+  extern __shared__ __align__(16) unsigned char raw[];
+  BwdTiles<G>* tiles = reinterpret_cast<BwdTiles<G>*>(raw);
+  const int warp = threadIdx.x >> 5;
+  BwdTiles<G>& sm = tiles[warp];
+  const int quads = (a.tpg + kBwdWarps - 1) / kBwdWarps;     // blocks of a group
+  const int group = blockIdx.x / quads, at = blockIdx.x % quads * kBwdWarps + warp;
+  const bool on = at < a.tpg;                                // else a warp without channels, there for the barriers
+  const int tile = group * a.tpg + (on ? at : a.tpg - 1);
+  const Tile<G> w(a, tile);
+  const int seg = blockIdx.y;
+  float h[CPL][NS], dh[CPL][NS];
+
+  if (seg >= a.n_seg) {                        // sequences without rows: the gradient passes through
+    const int step = (gridDim.y - a.n_seg) * 32;
+    for (long long i0 = (long long)(seg - a.n_seg) * 32; on && i0 < a.s.n; i0 += step) {
+      long long begin = 0, end = 1;
+      if (i0 + w.lane < a.s.n) seqs::range_of(a.s, (int)(i0 + w.lane), &begin, &end);
+      unsigned none = __ballot_sync(0xffffffffu, begin >= end);
+      while (none) {
+        const long long i = i0 + __ffs(none) - 1;
+        none &= none - 1;
+        load_state<G>(a, w, a.grad_final, i, h);
+        store_state<G>(a, w, a.grad_init, i, h);
+      }
+    }
+    return;
+  }
+
+  const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
+  const int chunks = (int)((r1 - r0 + kT - 1) / kT);
+  float A2[CPL][NS], gA[CPL][NS], bias[VN], D[VN], gD[VN], gb[VN];
+  load_A<G>(a, w, A2);
+  load_bias<G>(a, w, bias);
+#pragma unroll
+  for (int e = 0; e < VN; ++e) {
+    D[e] = a.D && w.col() < w.cols ? __ldg(a.D + w.c0 + w.col() + e) : 0.f;
+    gD[e] = gb[e] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < CPL; ++i)
+#pragma unroll
+    for (int j = 0; j < NS; ++j) gA[i][j] = 0.f;
+
+  Where q = seqs::find(a.s, r1 - 1);
+  if (q.end > r1) load_lanes<G>(a.local, (long long)(seg + 1) * a.tiles + tile, w.lane, dh);
+  else load_state<G>(a, w, a.grad_final, q.i, dh);
+
+  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+    const long long row = r0 + (long long)chunk * kT;
+    const int n = r1 - row < kT ? (int)(r1 - row) : kT;
+    Rows<G> bv, cv;
+    bv.fetch(a, w, a.B, a.ldb, row, n);
+    cv.fetch(a, w, a.C, a.ldc, row, n);
+    load_lanes<G>(a.ckpt, ((long long)seg * a.cps + chunk) * a.tiles + tile, w.lane, h);
+    stage_tokens<G>(a, w, row, n, bias, sm.dt, sm.dx, sm.g);
+    bv.stage(a, w, a.B, a.ldb, row, n, sm.B[0]);
+    cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
+    unsigned starts = 0;                       // rows that begin a sequence, one bit each
+    for (Where f = seqs::find(a.s, row);;) {
+      if (f.begin >= row) starts |= 1u << (f.begin - row);
+      if (f.end >= row + n) break;
+      f = seqs::find(a.s, f.end);
+    }
+    __syncwarp();
+    // the states before even rows
+    for (int t = 0; t < n; ++t) {
+      if (starts >> t & 1) load_state<G>(a, w, a.init, seqs::find(a.s, row + t).i, h);
+      if ((t & 1) == 0)
+#pragma unroll
+        for (int i = 0; i < CPL; ++i)
+#pragma unroll
+          for (int j = 0; j < NS; j += 2) sm.h[t / 2][(i * NS + j) / 2][w.lane] = make_float2(h[i][j], h[i][j + 1]);
+      float dt[CPL], dx[CPL], b[NS];
+      get(&sm.dt[t][w.cl * CPL], dt);
+      get(&sm.dx[t][w.cl * CPL], dx);
+      get(&sm.B[t][w.sl * NS], b);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
+    }
+    // back through the chunk, h being the state before row t
+    for (int t = n - 1; t >= 0; --t) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; j += 2) {
+          const float2 v = sm.h[t / 2][(i * NS + j) / 2][w.lane];
+          h[i][j] = v.x;
+          h[i][j + 1] = v.y;
+        }
+      float dt[CPL], dx[CPL], g[CPL], b[NS], c[NS];
+      if (t & 1) {
+        if (starts >> t & 1) {
+          load_state<G>(a, w, a.init, seqs::find(a.s, row + t).i, h);
+        } else {
+          get(&sm.dt[t - 1][w.cl * CPL], dt);
+          get(&sm.dx[t - 1][w.cl * CPL], dx);
+          get(&sm.B[t - 1][w.sl * NS], b);
+#pragma unroll
+          for (int i = 0; i < CPL; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
+        }
+      }
+      get(&sm.dt[t][w.cl * CPL], dt);
+      get(&sm.dx[t][w.cl * CPL], dx);
+      get(&sm.g[t][w.cl * CPL], g);
+      get(&sm.B[t][w.sl * NS], b);
+      get(&sm.C[t][w.sl * NS], c);
+      float s1[CPL], s2[CPL], y[CPL], bc[2 * NS] = {};
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        s1[i] = s2[i] = y[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const float e = ex2(dt[i] * A2[i][j]), ah = e * h[i][j];
+          const float now = fmaf(dx[i], b[j], ah), d = fmaf(c[j], g[i], dh[i][j]), q1 = d * ah;
+          y[i] = fmaf(c[j], now, y[i]);
+          s1[i] = fmaf(d, b[j], s1[i]);
+          s2[i] = fmaf(q1, A2[i][j], s2[i]);
+          gA[i][j] = fmaf(q1, dt[i], gA[i][j]);
+          bc[j] = fmaf(d, dx[i], bc[j]);
+          bc[NS + j] = fmaf(g[i], now, bc[NS + j]);
+          dh[i][j] = e * d;
+        }
+      }
+      const float o1 = over_states<CPL>(s1, w.lane), o2 = over_states<CPL>(s2, w.lane), o3 = over_states<CPL>(y, w.lane);
+      if (w.sl < CPL) {
+        sm.s1[t][w.cl * CPL + w.sl] = o1;
+        sm.s2[t][w.cl * CPL + w.sl] = o2 * kLn2;
+        sm.y[t][w.cl * CPL + w.sl] = o3;
+      }
+      over_channels<2 * NS>(bc, w.lane);
+      if constexpr (NS == 2) {
+        if (w.cl < 4) sm.bc[t][(w.cl >> 1) * NP + w.sl * NS + (w.cl & 1)] = bc[0];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2 * NS / 8; ++k) {
+          const int v = k * 8 + w.cl;
+          sm.bc[t][v / NS * NP + w.sl * NS + v % NS] = bc[k];
+        }
+      }
+      if (starts >> t & 1) {                   // the first row of its sequence: out, and on with the one before
+        const Where f = seqs::find(a.s, row + t);
+        if (a.grad_init && on) store_state<G>(a, w, a.grad_init, f.i, dh);
+        if (row + t > 0) load_state<G>(a, w, a.grad_final, seqs::find(a.s, row + t - 1).i, dh);
+      }
+    }
+    __syncwarp();
+    // the chunk's rows, channel by channel
+#pragma unroll
+    for (int k = 0; k < G::P; ++k)
+      if (w.row(k) < n && w.col() < w.cols && on) {
+        const long long r = row + w.row(k);
+        const int col = w.c0 + w.col();
+        auto in = [&](const void* p, long long ld, float (&f)[VN]) {
+          U::get(f, __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p) + r * ld + col)));
+        };
+        auto out = [&](void* p, const float (&f)[VN]) {
+          __stcs(reinterpret_cast<uint4*>(static_cast<E*>(p) + r * a.d + col), U::make(f));
+        };
+        float x[VN], g[VN], f[VN], s1[VN], dt[VN], sig[VN];
+        in(a.x, a.ldx, x);
+        in(a.delta, a.ldd, f);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) dt[e] = softplus(f[e] + bias[e], &sig[e]);
+        in(a.grad_y, a.d, g);
+        if (a.z) {
+          float z[VN], y[VN];
+          in(a.z, a.ldz, z);
+          get(&sm.y[w.row(k)][w.col()], y);
+#pragma unroll
+          for (int e = 0; e < VN; ++e) {
+            const float s = sigmoid(z[e]);
+            y[e] = fmaf(D[e], x[e], y[e]);
+            y[e] *= g[e] * s * fmaf(z[e], 1.f - s, 1.f);
+            g[e] *= z[e] * s;
+          }
+          out(a.grad_z, y);
+        }
+        get(&sm.s1[w.row(k)][w.col()], s1);
+        get(&sm.s2[w.row(k)][w.col()], f);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+          gD[e] = fmaf(g[e], x[e], gD[e]);
+          f[e] = fmaf(x[e], s1[e], f[e]) * sig[e];
+          gb[e] += f[e];
+          g[e] = fmaf(dt[e], s1[e], D[e] * g[e]);
+        }
+        out(a.grad_delta, f);
+        out(a.grad_x, g);
+      }
+    // the block's sum of dB and dC
+    __syncthreads();
+    const int warps = a.tpg - blockIdx.x % quads * kBwdWarps;
+    for (int i = threadIdx.x; i < n * 2 * NP; i += 32 * kBwdWarps) {
+      const int t = i / (2 * NP), s = i % (2 * NP);
+      float v = tiles[0].bc[t][s];
+#pragma unroll
+      for (int k = 1; k < kBwdWarps; ++k)
+        if (k < warps) v += tiles[k].bc[t][s];
+      a.bc[((long long)blockIdx.x * a.s.rows + row + t) * (2 * NP) + s] = v;
+    }
+    __syncthreads();
+  }
+  // the segment's dA, dD, dbias: [d, N | d | d]
+  if (on) {
+    float* part = a.part + (long long)seg * a.d * (a.N + 2);
+    store_state<G>(a, w, part, 0, gA);
+#pragma unroll
+    for (int e = 0; e < VN; ++e)
+#pragma unroll
+      for (int m = G::LPR; m < 32; m <<= 1) {
+        gD[e] += __shfl_xor_sync(0xffffffffu, gD[e], m);
+        gb[e] += __shfl_xor_sync(0xffffffffu, gb[e], m);
+      }
+    if (w.lane < G::LPR && w.col() < w.cols) {
+      put(part + (long long)a.d * a.N + w.c0 + w.col(), gD);
+      put(part + (long long)a.d * (a.N + 1) + w.c0 + w.col(), gb);
+    }
+  }
+}
+
+// grad_B and grad_C from the blocks' sums.
+constexpr int kBcThreads = 256;
+template <class E>
+__global__ void __launch_bounds__(kBcThreads) k_ssm_bc(Args a, int NP, int quads) {
+  const long long id = (long long)blockIdx.x * kBcThreads + threadIdx.x;     // (row, group, B or C, state)
+  const int s = (int)(id % (2 * NP));
+  const long long rg = id / (2 * NP);
+  const int g = (int)(rg % a.groups), n = s % NP;
+  const long long row = rg / a.groups;
+  if (row >= a.s.rows || n >= a.N) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int q = 0; q < quads; ++q) v += __ldcs(a.bc + (((long long)g * quads + q) * a.s.rows + row) * (2 * NP) + s);
+  rows::store1(static_cast<E*>(s < NP ? a.grad_B : a.grad_C) + (row * a.groups + g) * a.N + n, v);
+}
+
+template <class G>
+static cudaError_t backward(const Args& a, const Plan& p, cudaStream_t st) {
+  using E = typename G::E;
+  if (p.cut) {
+    {
+      TraceScope tr("k_ssm_local_bwd", st);
+      k_ssm_local_bwd<G><<<dim3(a.tiles, a.n_seg), 32, 0, st>>>(a);
+    }
+    const cudaError_t e = launch_ssm_carry<G, true>(a, st);
+    if (e != cudaSuccess) return e;
+  }
+  const bool empty = a.grad_init && (a.s.off || a.s.rows == 0);
+  const int more = empty ? (a.s.n < 32 * 64 ? (a.s.n + 31) / 32 : 64) : 0;
+  if (a.n_seg + more == 0) return cudaSuccess;
+  constexpr size_t smem = sizeof(BwdTiles<G>) * kBwdWarps;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const cudaError_t e = allow_smem<k_ssm_bwd<G>>(smem);
+  if (e != cudaSuccess) return e;
+  const int quads = (a.tpg + kBwdWarps - 1) / kBwdWarps;
+  {
+    TraceScope tr("k_ssm_bwd", st);
+    k_ssm_bwd<G><<<dim3(quads * a.groups, a.n_seg + more), 32 * kBwdWarps, smem, st>>>(a);
+  }
+  if (a.s.rows > 0) {
+    TraceScope tr("k_ssm_bc", st);
+    const long long n = a.s.rows * a.groups * 2 * G::NP;
+    k_ssm_bc<E><<<(unsigned)((n + kBcThreads - 1) / kBcThreads), kBcThreads, 0, st>>>(a, G::NP, quads);
+  }
+  return cudaGetLastError();
+}
+
+template <class E>
+static cudaError_t backward_of(const Args& a, const Plan& p, cudaStream_t st) {
+  switch (p.NS) {
+    case 2: return backward<Cfg<E, 2, 4>>(a, p, st);
+    case 4: return backward<Cfg<E, 4, 4>>(a, p, st);
+    case 8: return backward<Cfg<E, 8, 2>>(a, p, st);
+    default: return backward<Cfg<E, 16, 1>>(a, p, st);
+  }
+}
+
+}  // namespace ssm
+
+cudaError_t launch_ssm_backward(const SsmArgs& g, const SsmGrads& r, cudaStream_t st) {
+  const ssm::Plan p = ssm::make_plan(g.rows, g.n_seq, g.d, g.groups, g.N, g.off != nullptr);
+  ssm::Args a = ssm::args_of(g, p, ssm::make_work(p, g.rows, g.d, true));
+  a.grad_y = r.grad_y; a.grad_final = r.grad_final;
+  a.grad_x = r.grad_x; a.grad_delta = r.grad_delta; a.grad_z = r.grad_z; a.grad_B = r.grad_B; a.grad_C = r.grad_C;
+  a.grad_init = r.grad_init;
+  cudaError_t e = g.math == CFC_MATH_BF16 ? ssm::backward_of<__nv_bfloat16>(a, p, st) : ssm::backward_of<float>(a, p, st);
+  if (e != cudaSuccess) return e;
+  // [dA | dD | dbias] of the segments
+  ReduceOut o{};
+  const long long d = g.d, ld = d * (g.N + 2);
+  o.ptr[0] = r.grad_A;
+  o.nseg = 1;
+  long long n = d * g.N;
+  if (r.grad_D) {
+    o.ptr[1] = r.grad_D;
+    o.begin[1] = n;
+    o.nseg = 2;
+    n += d;
+    if (r.grad_bias) {
+      o.ptr[2] = r.grad_bias;
+      o.begin[2] = n;
+      o.nseg = 3;
+      n += d;
+    }
+  }
+  e = launch_reduce(a.part, p.n_seg, n, ld, o, st);
+  if (e != cudaSuccess || r.grad_D || !r.grad_bias) return e;
+  ReduceOut b{};
+  b.ptr[0] = r.grad_bias;
+  b.nseg = 1;
+  return launch_reduce(a.part + d * (g.N + 1), p.n_seg, d, ld, b, st);
+}
+
+}  // namespace cfc
