@@ -19,14 +19,41 @@ struct __align__(16) FwdTiles {
   float y[LOCAL ? 1 : kT][4][G::CW];         // C . h, a part from each state lane
 };
 
+// One token: the states, and C . h of the lane's states.
+template <class G, bool LOCAL>
+__device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t, const F2 (&A2)[G::PAIRS],
+                                      F2 (&h)[G::PAIRS], F2 (&sum)[G::CPAIRS]) {
+  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS], c[G::SPAIRS], y[G::CPAIRS];
+  get_channels<G>(sm.dt[t], w.cl, dt);
+  get_channels<G>(sm.dx[t], w.cl, dx);
+  get_states<G>(sm.B[t], w.sl, b);
+  if constexpr (!LOCAL) get_states<G>(sm.C[t], w.sl, c);
+#pragma unroll
+  for (int p = 0; p < G::PAIRS; ++p) {
+    const int i = cpair<G>(p), j = spair<G>(p);
+    h[p] = fma2(ex2_2(mul2(dt[i], A2[p])), h[p], mul2(dx[i], b[j]));
+    if constexpr (!LOCAL) y[i] = j == 0 ? mul2(c[j], h[p]) : fma2(c[j], h[p], y[i]);
+  }
+  if constexpr (LOCAL) {
+#pragma unroll
+    for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], dt[i]);
+  } else if constexpr (G::CPL == 4) {
+    *reinterpret_cast<ulonglong2*>(&sm.y[t][w.sl][w.cl * 4]) = make_ulonglong2(y[0], y[1]);
+  } else if constexpr (G::CPL == 2) {
+    *reinterpret_cast<F2*>(&sm.y[t][w.sl][w.cl * 2]) = y[0];
+  } else {
+    sm.y[t][w.sl][w.cl] = sum2(y[0]);
+  }
+}
+
 template <class G, bool LOCAL>
 __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
   using E = typename G::E;
-  constexpr int CPL = G::CPL, NS = G::NS, P = G::P, VN = G::VN;
+  constexpr int P = G::P, VN = G::VN, VP = VN / 2;
   __shared__ FwdTiles<G, LOCAL> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
-  float h[CPL][NS];
+  F2 h[G::PAIRS];
 
   if (!LOCAL && seg >= a.n_seg) {            // the states after sequences without rows
     const int step = (gridDim.y - a.n_seg) * 32;
@@ -54,22 +81,15 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
     if (!cut) return;
     if (starts) row = q.begin;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i)
-#pragma unroll
-      for (int j = 0; j < NS; ++j) h[i][j] = 0.f;
+    for (int p = 0; p < G::PAIRS; ++p) h[p] = 0;
   } else {
     q = seqs::find(a.s, r0);
     if (q.begin < r0) load_lanes<G>(a.local, (long long)(seg - 1) * a.tiles + blockIdx.x, w.lane, h);
   }
-  float A2[CPL][NS];
+  F2 A2[G::PAIRS], bias[VP], D[VP], sum[G::CPAIRS] = {};
   load_A<G>(a, w, A2);
-  float bias[VN], D[VN], sum[CPL] = {};
-#pragma unroll
-  for (int e = 0; e < VN; ++e) {
-    const bool in = w.col() < w.cols;
-    bias[e] = a.bias && in ? __ldg(a.bias + w.c0 + w.col() + e) : 0.f;
-    D[e] = !LOCAL && a.D && in ? __ldg(a.D + w.c0 + w.col() + e) : 0.f;
-  }
+  load_pairs<G>(w, a.bias, bias);
+  load_pairs<G>(w, LOCAL ? nullptr : a.D, D);
 
   uint4 xv[P], dv[P], zv[P];
   Rows<G> bv, cv;
@@ -84,21 +104,21 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
   for (int chunk = 0; row < r1; row += kT, ++chunk) {
     const int n = r1 - row < kT ? (int)(r1 - row) : kT;
     if (!LOCAL && save) store_lanes<G>(a.ckpt, ((long long)seg * a.cps + chunk) * a.tiles + blockIdx.x, w.lane, h);
-    float xk[P][LOCAL ? 1 : VN];                           // D x
+    F2 y[P][LOCAL ? 1 : VP];                               // D x
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      float x[VN], dl[VN], dt[VN];
-      Unpack<E>::get(x, xv[k]);
-      Unpack<E>::get(dl, dv[k]);
+      F2 x[VP], dt[VP];
+      Unpack<E>::pairs(x, xv[k]);
+      Unpack<E>::pairs(dt, dv[k]);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) {
-        dt[e] = softplus(dl[e] + bias[e]);
-        if constexpr (!LOCAL) xk[k][e] = D[e] * x[e];
-        x[e] *= dt[e];
+      for (int e = 0; e < VP; ++e) {
+        dt[e] = softplus2(add2(dt[e], bias[e]));
+        if constexpr (!LOCAL) y[k][e] = mul2(D[e], x[e]);
+        x[e] = mul2(x[e], dt[e]);
       }
       if (w.row(k) < kT) {
-        put(&sm.dt[w.row(k)][w.col()], dt);
-        put(&sm.dx[w.row(k)][w.col()], x);
+        put_pairs(&sm.dt[w.row(k)][w.col()], dt);
+        put_pairs(&sm.dx[w.row(k)][w.col()], x);
       }
     }
     bv.stage(a, w, a.B, a.ldb, row, n, sm.B[0]);
@@ -108,30 +128,18 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
     }
     __syncwarp();
     fetch(row + kT);
-    for (int t = 0; t < n;) {
-      if (row + t == q.begin) load_state<G>(a, w, a.init, q.i, h);
-      const int m = q.end - row < n ? (int)(q.end - row) : n;
-      for (; t < m; ++t) {
-        float dt[CPL], dx[CPL], b[NS], c[NS], y[CPL];
-        get(&sm.dt[t][w.cl * CPL], dt);
-        get(&sm.dx[t][w.cl * CPL], dx);
-        get(&sm.B[t][w.sl * NS], b);
-        if constexpr (!LOCAL) get(&sm.C[t][w.sl * NS], c);
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) {
-          y[i] = 0.f;
-#pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
-            if constexpr (!LOCAL) y[i] = fmaf(c[j], h[i][j], y[i]);
-          }
-          if constexpr (LOCAL) sum[i] += dt[i];
+    if (n == kT && q.begin < row && q.end > row + kT) {    // inside one sequence: no state comes or goes
+#pragma unroll 4
+      for (int t = 0; t < kT; ++t) token<G, LOCAL>(sm, w, t, A2, h, sum);
+    } else {
+      for (int t = 0; t < n;) {
+        if (row + t == q.begin) load_state<G>(a, w, a.init, q.i, h);
+        const int m = q.end - row < n ? (int)(q.end - row) : n;
+        for (; t < m; ++t) token<G, LOCAL>(sm, w, t, A2, h, sum);
+        if (!LOCAL && row + t == q.end) {
+          if (a.final_state) store_state<G>(a, w, a.final_state, q.i, h);
+          if (row + t < a.s.rows) q = seqs::find(a.s, row + t);
         }
-        if constexpr (!LOCAL) put(&sm.y[t][w.sl][w.cl * CPL], y);
-      }
-      if (!LOCAL && row + t == q.end) {
-        if (a.final_state) store_state<G>(a, w, a.final_state, q.i, h);
-        if (row + t < a.s.rows) q = seqs::find(a.s, row + t);
       }
     }
     __syncwarp();
@@ -139,30 +147,27 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
 #pragma unroll
       for (int k = 0; k < P; ++k)
         if (w.row(k) < n && w.col() < w.cols) {
-          float y[VN], z[VN];
-#pragma unroll
-          for (int e = 0; e < VN; ++e) y[e] = xk[k][e];
+          F2 z[VP];
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            get(&sm.y[w.row(k)][s][w.col()], z);
+            get_pairs(&sm.y[w.row(k)][s][w.col()], z);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) y[e] += z[e];
+            for (int e = 0; e < VP; ++e) y[k][e] = add2(y[k][e], z[e]);
           }
           if (a.z) {
-            Unpack<E>::get(z, zv[k]);
+            Unpack<E>::pairs(z, zv[k]);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) y[e] *= z[e] * sigmoid(z[e]);
+            for (int e = 0; e < VP; ++e) y[k][e] = mul2(y[k][e], mul2(z[e], sigmoid2(z[e])));
           }
           E* to = static_cast<E*>(a.y) + (row + w.row(k)) * a.d + w.c0 + w.col();
-          __stcs(reinterpret_cast<uint4*>(to), Unpack<E>::make(y));
+          __stcs(reinterpret_cast<uint4*>(to), Unpack<E>::make(y[k]));
         }
     }
   }
   if constexpr (LOCAL) {
     const long long block = (long long)seg * a.tiles + blockIdx.x;
     store_lanes<G>(a.local, block, w.lane, h);
-#pragma unroll
-    for (int i = 0; i < CPL; ++i) a.sdt[(block * CPL + i) * 32 + w.lane] = sum[i];
+    store_sums<G>(a, block, w.lane, sum);
   }
 }
 

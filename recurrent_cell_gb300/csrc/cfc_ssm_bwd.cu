@@ -9,9 +9,9 @@
 //   dB    = sum_c dt x dh                  dC = sum_c g h
 //   dz    = grad_y (C . h + D x) silu'(z)  dD = sum_t g x,  dbias = sum_t ddelta
 // A chunk starts from the state that the forward saved before it.  A first sweep runs
-// it forward and keeps the state before every second token; the second goes back
-// and forms the state in between anew (one multiply-add, since it needs a anyway), which
-// halves the shared memory that states take.  The two exponentials and some fifteen multiply-adds
+// it forward and keeps the state before every second token; the second goes back two
+// tokens at a time and forms the state in between anew (one multiply-add, since it needs a
+// anyway), which halves the shared memory that states take.  The two exponentials and some fifteen multiply-adds
 // a state are the bound, not memory.
 //
 // Sums over a channel's states and over a tile's channels are taken by lane steps that
@@ -28,11 +28,11 @@ constexpr int kBwdWarps = 4;
 
 template <class G>
 struct __align__(16) BwdTiles {
-  float dt[kT][G::CW], dx[kT][G::CW], g[kT][G::CW];          // dt, dt x, g
+  float dt[kT][G::CW], dx[kT][G::CW], g[kT][G::CW];          // dt, dt x, g; then sum e A, sum dh B, C . h
   float B[kT][G::NP], C[kT][G::NP];
-  float s1[kT][G::CW], s2[kT][G::CW], y[kT][G::CW];          // sum dh B, sum e A, C . h
   float bc[kT][2 * G::NP];                                   // dB, dC of the tile
-  float2 h[kT / 2][G::CPL * G::NS / 2][32];                  // states before rows 0, 2, 4, ...
+  ulonglong2 h[kT / 2][G::PAIRS / 2][32];                    // states before rows 0, 2, 4, ...
+  F2 gA[G::PAIRS][32];                                       // dA of the chunks so far
 };
 
 // One value of each lane's quarter: v[i] summed over the lanes of a group of 4
@@ -91,10 +91,10 @@ __device__ __forceinline__ void over_channels(float (&v)[N], int lane) {
 
 // dt, dt x and g of a chunk's tokens, into the tiles.  dx = nullptr: only dt and g.
 template <class G>
-__device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const float (&bias)[G::VN],
+__device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const F2 (&bias)[G::VN / 2],
                                              float (*dt)[G::CW], float (*dx)[G::CW], float (*g)[G::CW]) {
   using U = Unpack<typename G::E>;
-  constexpr int VN = G::VN;
+  constexpr int VP = G::VN / 2;
   uint4 xv[G::P], dv[G::P], zv[G::P], gv[G::P];
   if (dx) load_raw<G>(w, a.x, a.ldx, row, n, xv);
   load_raw<G>(w, a.delta, a.ldd, row, n, dv);
@@ -102,32 +102,27 @@ __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, lo
   if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
 #pragma unroll
   for (int k = 0; k < G::P; ++k) {
-    float f[VN], t[VN], u[VN];
-    U::get(t, dv[k]);
+    F2 f[VP], t[VP], u[VP];
+    U::pairs(t, dv[k]);
 #pragma unroll
-    for (int e = 0; e < VN; ++e) t[e] = softplus(t[e] + bias[e]);
-    U::get(f, gv[k]);
+    for (int e = 0; e < VP; ++e) t[e] = softplus2(add2(t[e], bias[e]));
+    U::pairs(f, gv[k]);
     if (a.z) {
-      U::get(u, zv[k]);
+      U::pairs(u, zv[k]);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) f[e] *= u[e] * sigmoid(u[e]);
+      for (int e = 0; e < VP; ++e) f[e] = mul2(f[e], mul2(u[e], sigmoid2(u[e])));
     }
     if (w.row(k) < kT) {
-      put(&dt[w.row(k)][w.col()], t);
-      put(&g[w.row(k)][w.col()], f);
+      put_pairs(&dt[w.row(k)][w.col()], t);
+      put_pairs(&g[w.row(k)][w.col()], f);
     }
     if (dx) {
-      U::get(u, xv[k]);
+      U::pairs(u, xv[k]);
 #pragma unroll
-      for (int e = 0; e < VN; ++e) u[e] *= t[e];
-      if (w.row(k) < kT) put(&dx[w.row(k)][w.col()], u);
+      for (int e = 0; e < VP; ++e) u[e] = mul2(u[e], t[e]);
+      if (w.row(k) < kT) put_pairs(&dx[w.row(k)][w.col()], u);
     }
   }
-}
-template <class G>
-__device__ __forceinline__ void load_bias(const Args& a, const Tile<G>& w, float (&bias)[G::VN]) {
-#pragma unroll
-  for (int e = 0; e < G::VN; ++e) bias[e] = a.bias && w.col() < w.cols ? __ldg(a.bias + w.c0 + w.col() + e) : 0.f;
 }
 
 // What a segment's own rows send to the state before it, and its sum of dt: for the
@@ -138,7 +133,6 @@ struct __align__(16) LocalTiles {
 };
 template <class G>
 __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
-  constexpr int CPL = G::CPL, NS = G::NS;
   __shared__ LocalTiles<G> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
@@ -148,9 +142,9 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
   if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (ends ? kStarts : 0);
   if (!cut) return;
   const long long last = ends ? q.end : r1;
-  float A2[CPL][NS], dh[CPL][NS], sum[CPL] = {}, bias[G::VN];
+  F2 A2[G::PAIRS], dh[G::PAIRS], sum[G::CPAIRS] = {}, bias[G::VN / 2];
   load_A<G>(a, w, A2);
-  load_bias<G>(a, w, bias);
+  load_pairs<G>(w, a.bias, bias);
   load_state<G>(a, w, ends ? a.grad_final : nullptr, q.i, dh);
   Rows<G> cv;
   for (long long row = r0 + (last - r0 - 1) / kT * kT; row >= r0; row -= kT) {
@@ -159,31 +153,118 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
     stage_tokens<G>(a, w, row, n, bias, sm.dt, nullptr, sm.g);
     cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
     __syncwarp();
+#pragma unroll 4
     for (int t = n - 1; t >= 0; --t) {
-      float dt[CPL], g[CPL], c[NS];
-      get(&sm.dt[t][w.cl * CPL], dt);
-      get(&sm.g[t][w.cl * CPL], g);
-      get(&sm.C[t][w.sl * NS], c);
+      F2 dt[G::CPAIRS], g[G::CPAIRS], c[G::SPAIRS];
+      get_channels<G>(sm.dt[t], w.cl, dt);
+      get_channels<G>(sm.g[t], w.cl, g);
+      get_states<G>(sm.C[t], w.sl, c);
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j) dh[i][j] = ex2(dt[i] * A2[i][j]) * fmaf(c[j], g[i], dh[i][j]);
-        sum[i] += dt[i];
+      for (int p = 0; p < G::PAIRS; ++p) {
+        const int i = cpair<G>(p), j = spair<G>(p);
+        dh[p] = mul2(ex2_2(mul2(dt[i], A2[p])), fma2(c[j], g[i], dh[p]));
       }
+#pragma unroll
+      for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], dt[i]);
     }
     __syncwarp();
   }
   const long long block = (long long)seg * a.tiles + blockIdx.x;
   store_lanes<G>(a.local, block, w.lane, dh);
+  store_sums<G>(a, block, w.lane, sum);
+}
+
+// What a token reads of the tiles.
+template <class G>
+struct Token {
+  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS];
+  __device__ __forceinline__ Token(const BwdTiles<G>& sm, const Tile<G>& w, int t) {
+    get_channels<G>(sm.dt[t], w.cl, dt);
+    get_channels<G>(sm.dx[t], w.cl, dx);
+    get_states<G>(sm.B[t], w.sl, b);
+  }
+  // a h + dt x B, from a
+  __device__ __forceinline__ void forward(const F2 (&e)[G::PAIRS], F2 (&h)[G::PAIRS]) const {
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) a.sdt[(block * CPL + i) * 32 + w.lane] = sum[i];
+    for (int p = 0; p < G::PAIRS; ++p) h[p] = fma2(e[p], h[p], mul2(dx[cpair<G>(p)], b[spair<G>(p)]));
+  }
+  __device__ __forceinline__ void decay(const F2 (&A2)[G::PAIRS], F2 (&e)[G::PAIRS]) const {
+#pragma unroll
+    for (int p = 0; p < G::PAIRS; ++p) e[p] = ex2_2(mul2(dt[cpair<G>(p)], A2[p]));
+  }
+};
+
+// Token t backward, h being the state before it and e its decays: the token's sums into the
+// tiles, dh on to the token before it.
+template <class G>
+__device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int t, const Token<G>& k, const F2 (&e)[G::PAIRS],
+                                          const F2 (&h)[G::PAIRS], const F2 (&A2)[G::PAIRS], F2 (&dh)[G::PAIRS],
+                                          F2 (&gA)[G::PAIRS]) {
+  constexpr int CPL = G::CPL, NS = G::NS, NP = G::NP;
+  F2 g[G::CPAIRS], c[G::SPAIRS], s1[G::CPAIRS], s2[G::CPAIRS], y[G::CPAIRS], db[G::SPAIRS], dc[G::SPAIRS];
+  get_channels<G>(sm.g[t], w.cl, g);
+  get_states<G>(sm.C[t], w.sl, c);
+#pragma unroll
+  for (int p = 0; p < G::PAIRS; ++p) {
+    const int i = cpair<G>(p), j = spair<G>(p);
+    const bool first_i = G::CPL > 1 ? j == 0 : p == 0, first_j = G::CPL > 1 ? i == 0 : true;
+    const F2 ah = mul2(e[p], h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(c[j], g[i], dh[p]), q = mul2(d, ah);
+    y[i] = first_i ? mul2(c[j], now) : fma2(c[j], now, y[i]);
+    s1[i] = first_i ? mul2(d, k.b[j]) : fma2(d, k.b[j], s1[i]);
+    s2[i] = first_i ? mul2(q, A2[p]) : fma2(q, A2[p], s2[i]);
+    gA[p] = fma2(q, k.dt[i], gA[p]);
+    db[j] = first_j ? mul2(d, k.dx[i]) : fma2(d, k.dx[i], db[j]);
+    dc[j] = first_j ? mul2(g[i], now) : fma2(g[i], now, dc[j]);
+    dh[p] = mul2(e[p], d);
+  }
+  float f1[CPL], f2[CPL], f3[CPL], bc[2 * NS];
+  if constexpr (CPL > 1) {
+#pragma unroll
+    for (int i = 0; i < CPL / 2; ++i) {
+      split(s1[i], f1[2 * i], f1[2 * i + 1]);
+      split(s2[i], f2[2 * i], f2[2 * i + 1]);
+      split(y[i], f3[2 * i], f3[2 * i + 1]);
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      bc[j] = sum2(db[j]);
+      bc[NS + j] = sum2(dc[j]);
+    }
+  } else {
+    f1[0] = sum2(s1[0]);
+    f2[0] = sum2(s2[0]);
+    f3[0] = sum2(y[0]);
+#pragma unroll
+    for (int j = 0; j < NS / 2; ++j) {
+      split(db[j], bc[2 * j], bc[2 * j + 1]);
+      split(dc[j], bc[NS + 2 * j], bc[NS + 2 * j + 1]);
+    }
+  }
+  const float o1 = over_states<CPL>(f1, w.lane), o2 = over_states<CPL>(f2, w.lane), o3 = over_states<CPL>(f3, w.lane);
+  over_channels<2 * NS>(bc, w.lane);
+  // (the token's own values have been read by all lanes: the sums above took every lane)
+  __syncwarp();
+  if (w.sl < CPL) {
+    sm.dx[t][w.cl * CPL + w.sl] = o1;
+    sm.dt[t][w.cl * CPL + w.sl] = o2 * kLn2;
+    sm.g[t][w.cl * CPL + w.sl] = o3;
+  }
+  if constexpr (NS == 2) {
+    if (w.cl < 4) sm.bc[t][(w.cl >> 1) * NP + w.sl * NS + (w.cl & 1)] = bc[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * NS / 8; ++i) {
+      const int v = i * 8 + w.cl;
+      sm.bc[t][v / NS * NP + w.sl * NS + v % NS] = bc[i];
+    }
+  }
 }
 
 template <class G>
 __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
   using E = typename G::E;
   using U = Unpack<E>;
-  constexpr int CPL = G::CPL, NS = G::NS, VN = G::VN, NP = G::NP;
+  constexpr int VN = G::VN, VP = VN / 2, NP = G::NP, PAIRS = G::PAIRS;
   extern __shared__ __align__(16) unsigned char raw[];
   BwdTiles<G>* tiles = reinterpret_cast<BwdTiles<G>*>(raw);
   const int warp = threadIdx.x >> 5;
@@ -194,7 +275,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
   const int tile = group * a.tpg + (on ? at : a.tpg - 1);
   const Tile<G> w(a, tile);
   const int seg = blockIdx.y;
-  float h[CPL][NS], dh[CPL][NS];
+  F2 h[PAIRS], dh[PAIRS];
 
   if (seg >= a.n_seg) {                        // sequences without rows: the gradient passes through
     const int step = (gridDim.y - a.n_seg) * 32;
@@ -214,20 +295,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
 
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
   const int chunks = (int)((r1 - r0 + kT - 1) / kT);
-  float A2[CPL][NS], gA[CPL][NS], bias[VN], D[VN], gD[VN], gb[VN];
+  F2 A2[PAIRS], bias[VP], D[VP], gD[VP] = {}, gb[VP] = {};
   load_A<G>(a, w, A2);
-  load_bias<G>(a, w, bias);
+  load_pairs<G>(w, a.bias, bias);
+  load_pairs<G>(w, a.D, D);
 #pragma unroll
-  for (int e = 0; e < VN; ++e) {
-    D[e] = a.D && w.col() < w.cols ? __ldg(a.D + w.c0 + w.col() + e) : 0.f;
-    gD[e] = gb[e] = 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < CPL; ++i)
-#pragma unroll
-    for (int j = 0; j < NS; ++j) gA[i][j] = 0.f;
+  for (int p = 0; p < PAIRS; ++p) sm.gA[p][w.lane] = 0;
 
-  Where q = seqs::find(a.s, r1 - 1);
+  const Where q = seqs::find(a.s, r1 - 1);
   if (q.end > r1) load_lanes<G>(a.local, (long long)(seg + 1) * a.tiles + tile, w.lane, dh);
   else load_state<G>(a, w, a.grad_final, q.i, dh);
 
@@ -248,135 +323,113 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
       f = seqs::find(a.s, f.end);
     }
     __syncwarp();
-    // the states before even rows
+    // forward: the states before even rows
+    F2 gA[PAIRS], e[PAIRS];
     for (int t = 0; t < n; ++t) {
       if (starts >> t & 1) load_state<G>(a, w, a.init, seqs::find(a.s, row + t).i, h);
       if ((t & 1) == 0)
 #pragma unroll
-        for (int i = 0; i < CPL; ++i)
-#pragma unroll
-          for (int j = 0; j < NS; j += 2) sm.h[t / 2][(i * NS + j) / 2][w.lane] = make_float2(h[i][j], h[i][j + 1]);
-      float dt[CPL], dx[CPL], b[NS];
-      get(&sm.dt[t][w.cl * CPL], dt);
-      get(&sm.dx[t][w.cl * CPL], dx);
-      get(&sm.B[t][w.sl * NS], b);
-#pragma unroll
-      for (int i = 0; i < CPL; ++i)
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
+        for (int p = 0; p < PAIRS; p += 2) sm.h[t / 2][p / 2][w.lane] = make_ulonglong2(h[p], h[p + 1]);
+      const Token<G> k(sm, w, t);
+      k.decay(A2, e);
+      k.forward(e, h);
     }
-    // back through the chunk, h being the state before row t
-    for (int t = n - 1; t >= 0; --t) {
+    // back, two rows at a time
 #pragma unroll
-      for (int i = 0; i < CPL; ++i)
+    for (int p = 0; p < PAIRS; ++p) gA[p] = 0;
+    // the first row of its sequence: out, and on with the one before
+    auto begin = [&](int t) {
+      if (!(starts >> t & 1)) return;
+      if (a.grad_init && on) store_state<G>(a, w, a.grad_init, seqs::find(a.s, row + t).i, dh);
+      if (row + t > 0) load_state<G>(a, w, a.grad_final, seqs::find(a.s, row + t - 1).i, dh);
+    };
+    for (int t = (n - 1) & ~1; t >= 0; t -= 2) {
 #pragma unroll
-        for (int j = 0; j < NS; j += 2) {
-          const float2 v = sm.h[t / 2][(i * NS + j) / 2][w.lane];
-          h[i][j] = v.x;
-          h[i][j + 1] = v.y;
-        }
-      float dt[CPL], dx[CPL], g[CPL], b[NS], c[NS];
-      if (t & 1) {
-        if (starts >> t & 1) {
-          load_state<G>(a, w, a.init, seqs::find(a.s, row + t).i, h);
+      for (int p = 0; p < PAIRS; p += 2) {
+        const ulonglong2 v = sm.h[t / 2][p / 2][w.lane];
+        h[p] = v.x;
+        h[p + 1] = v.y;
+      }
+      const Token<G> k(sm, w, t);
+      k.decay(A2, e);
+      if (t + 1 < n) {
+        F2 h1[PAIRS], e1[PAIRS];
+        if (starts >> (t + 1) & 1) {
+          load_state<G>(a, w, a.init, seqs::find(a.s, row + t + 1).i, h1);
         } else {
-          get(&sm.dt[t - 1][w.cl * CPL], dt);
-          get(&sm.dx[t - 1][w.cl * CPL], dx);
-          get(&sm.B[t - 1][w.sl * NS], b);
 #pragma unroll
-          for (int i = 0; i < CPL; ++i)
-#pragma unroll
-            for (int j = 0; j < NS; ++j) h[i][j] = fmaf(ex2(dt[i] * A2[i][j]), h[i][j], dx[i] * b[j]);
+          for (int p = 0; p < PAIRS; ++p) h1[p] = h[p];
+          k.forward(e, h1);
         }
+        const Token<G> k1(sm, w, t + 1);
+        k1.decay(A2, e1);
+        token_bwd<G>(sm, w, t + 1, k1, e1, h1, A2, dh, gA);
+        begin(t + 1);
       }
-      get(&sm.dt[t][w.cl * CPL], dt);
-      get(&sm.dx[t][w.cl * CPL], dx);
-      get(&sm.g[t][w.cl * CPL], g);
-      get(&sm.B[t][w.sl * NS], b);
-      get(&sm.C[t][w.sl * NS], c);
-      float s1[CPL], s2[CPL], y[CPL], bc[2 * NS] = {};
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        s1[i] = s2[i] = y[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          const float e = ex2(dt[i] * A2[i][j]), ah = e * h[i][j];
-          const float now = fmaf(dx[i], b[j], ah), d = fmaf(c[j], g[i], dh[i][j]), q1 = d * ah;
-          y[i] = fmaf(c[j], now, y[i]);
-          s1[i] = fmaf(d, b[j], s1[i]);
-          s2[i] = fmaf(q1, A2[i][j], s2[i]);
-          gA[i][j] = fmaf(q1, dt[i], gA[i][j]);
-          bc[j] = fmaf(d, dx[i], bc[j]);
-          bc[NS + j] = fmaf(g[i], now, bc[NS + j]);
-          dh[i][j] = e * d;
-        }
-      }
-      const float o1 = over_states<CPL>(s1, w.lane), o2 = over_states<CPL>(s2, w.lane), o3 = over_states<CPL>(y, w.lane);
-      if (w.sl < CPL) {
-        sm.s1[t][w.cl * CPL + w.sl] = o1;
-        sm.s2[t][w.cl * CPL + w.sl] = o2 * kLn2;
-        sm.y[t][w.cl * CPL + w.sl] = o3;
-      }
-      over_channels<2 * NS>(bc, w.lane);
-      if constexpr (NS == 2) {
-        if (w.cl < 4) sm.bc[t][(w.cl >> 1) * NP + w.sl * NS + (w.cl & 1)] = bc[0];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2 * NS / 8; ++k) {
-          const int v = k * 8 + w.cl;
-          sm.bc[t][v / NS * NP + w.sl * NS + v % NS] = bc[k];
-        }
-      }
-      if (starts >> t & 1) {                   // the first row of its sequence: out, and on with the one before
-        const Where f = seqs::find(a.s, row + t);
-        if (a.grad_init && on) store_state<G>(a, w, a.grad_init, f.i, dh);
-        if (row + t > 0) load_state<G>(a, w, a.grad_final, seqs::find(a.s, row + t - 1).i, dh);
-      }
+      token_bwd<G>(sm, w, t, k, e, h, A2, dh, gA);
+      begin(t);
     }
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) sm.gA[p][w.lane] = add2(sm.gA[p][w.lane], gA[p]);
     __syncwarp();
     // the chunk's rows, channel by channel
+    F2 cD[VP] = {}, cb[VP] = {};               // dD and dbias of the chunk
 #pragma unroll
     for (int k = 0; k < G::P; ++k)
       if (w.row(k) < n && w.col() < w.cols && on) {
         const long long r = row + w.row(k);
         const int col = w.c0 + w.col();
-        auto in = [&](const void* p, long long ld, float (&f)[VN]) {
-          U::get(f, __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p) + r * ld + col)));
+        auto in = [&](const void* p, long long ld, F2 (&f)[VP]) {
+          U::pairs(f, __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p) + r * ld + col)));
         };
-        auto out = [&](void* p, const float (&f)[VN]) {
+        auto out = [&](void* p, const F2 (&f)[VP]) {
           __stcs(reinterpret_cast<uint4*>(static_cast<E*>(p) + r * a.d + col), U::make(f));
         };
-        float x[VN], g[VN], f[VN], s1[VN], dt[VN], sig[VN];
+        F2 x[VP], g[VP], f[VP], s1[VP], dt[VP], sig[VP];
         in(a.x, a.ldx, x);
         in(a.delta, a.ldd, f);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) dt[e] = softplus(f[e] + bias[e], &sig[e]);
+        for (int e = 0; e < VP; ++e) {
+          F2 en;
+          const F2 v = add2(f[e], bias[e]);
+          dt[e] = softplus2(v, &en);
+          float va, vb, ea, eb;                // sigmoid(v) = 1 / (1 + e), or e / (1 + e) below zero
+          split(v, va, vb);
+          split(en, ea, eb);
+          sig[e] = pack((va >= 0.f ? 1.f : ea) * rcp(1.f + ea), (vb >= 0.f ? 1.f : eb) * rcp(1.f + eb));
+        }
         in(a.grad_y, a.d, g);
         if (a.z) {
-          float z[VN], y[VN];
+          F2 z[VP], y[VP];
           in(a.z, a.ldz, z);
-          get(&sm.y[w.row(k)][w.col()], y);
+          get_pairs(&sm.g[w.row(k)][w.col()], y);
 #pragma unroll
-          for (int e = 0; e < VN; ++e) {
-            const float s = sigmoid(z[e]);
-            y[e] = fmaf(D[e], x[e], y[e]);
-            y[e] *= g[e] * s * fmaf(z[e], 1.f - s, 1.f);
-            g[e] *= z[e] * s;
+          for (int e = 0; e < VP; ++e) {
+            // silu'(z) = s (1 + z (1 - s)) = s + z s (1 - s)
+            const F2 s = sigmoid2(z[e]), zs = mul2(z[e], s);
+            y[e] = mul2(fma2(D[e], x[e], y[e]), g[e]);
+            y[e] = mul2(y[e], fma2(zs, fma2(s, twice(-1.f), twice(1.f)), s));
+            g[e] = mul2(g[e], zs);
           }
           out(a.grad_z, y);
         }
-        get(&sm.s1[w.row(k)][w.col()], s1);
-        get(&sm.s2[w.row(k)][w.col()], f);
+        get_pairs(&sm.dx[w.row(k)][w.col()], s1);
+        get_pairs(&sm.dt[w.row(k)][w.col()], f);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) {
-          gD[e] = fmaf(g[e], x[e], gD[e]);
-          f[e] = fmaf(x[e], s1[e], f[e]) * sig[e];
-          gb[e] += f[e];
-          g[e] = fmaf(dt[e], s1[e], D[e] * g[e]);
+        for (int e = 0; e < VP; ++e) {
+          cD[e] = fma2(g[e], x[e], cD[e]);
+          f[e] = mul2(fma2(x[e], s1[e], f[e]), sig[e]);
+          cb[e] = add2(cb[e], f[e]);
+          g[e] = fma2(dt[e], s1[e], mul2(D[e], g[e]));
         }
         out(a.grad_delta, f);
         out(a.grad_x, g);
       }
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+      gD[e] = add2(gD[e], cD[e]);
+      gb[e] = add2(gb[e], cb[e]);
+    }
     // the block's sum of dB and dC
     __syncthreads();
     const int warps = a.tpg - blockIdx.x % quads * kBwdWarps;
@@ -393,17 +446,26 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
   // the segment's dA, dD, dbias: [d, N | d | d]
   if (on) {
     float* part = a.part + (long long)seg * a.d * (a.N + 2);
+    F2 gA[PAIRS];
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) gA[p] = sm.gA[p][w.lane];
     store_state<G>(a, w, part, 0, gA);
+    float fD[VN], fb[VN];
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+      split(gD[e], fD[2 * e], fD[2 * e + 1]);
+      split(gb[e], fb[2 * e], fb[2 * e + 1]);
+    }
 #pragma unroll
     for (int e = 0; e < VN; ++e)
 #pragma unroll
       for (int m = G::LPR; m < 32; m <<= 1) {
-        gD[e] += __shfl_xor_sync(0xffffffffu, gD[e], m);
-        gb[e] += __shfl_xor_sync(0xffffffffu, gb[e], m);
+        fD[e] += __shfl_xor_sync(0xffffffffu, fD[e], m);
+        fb[e] += __shfl_xor_sync(0xffffffffu, fb[e], m);
       }
     if (w.lane < G::LPR && w.col() < w.cols) {
-      put(part + (long long)a.d * a.N + w.c0 + w.col(), gD);
-      put(part + (long long)a.d * (a.N + 1) + w.c0 + w.col(), gb);
+      put(part + (long long)a.d * a.N + w.c0 + w.col(), fD);
+      put(part + (long long)a.d * (a.N + 1) + w.c0 + w.col(), fb);
     }
   }
 }

@@ -65,6 +65,7 @@ struct Cfg {
   static constexpr int LPR = CW / VN, RPP = 32 / LPR;        // lanes a row, rows a pass
   static constexpr int P = (kT + RPP - 1) / RPP;             // passes of a chunk
   static constexpr int BV = NP * (int)sizeof(E) / 16;        // vectors of a row of B
+  static constexpr int PAIRS = CPL * NS / 2, CPAIRS = CPL > 1 ? CPL / 2 : 1, SPAIRS = CPL > 1 ? NS : NS / 2;
   static constexpr int BL = (kT * BV + 31) / 32;             // of a chunk, a lane
 };
 
@@ -73,36 +74,93 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// exp(v), v <= 0, to about an fp32 unit and a half: 2^hi (1 + lo ln 2), hi + lo = v / ln 2.
-__device__ __forceinline__ float exp_neg(float v) {
-  const float hi = fmaxf(v, -126.f * kLn2) * kLog2e;         // (a NaN goes to the sum below)
-  const float lo = fmaf(fmaxf(v, -126.f * kLn2), kLog2e, -hi);
-  const float e = ex2(hi);
-  return fmaf(e * lo, kLn2, e);
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
-// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|); log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
-// by its Taylor series up to s^15 (the rest is below 2e-9 of it).  sig: sigmoid(v).
-__device__ __forceinline__ float softplus(float v, float* sig = nullptr) {
-  const float e = exp_neg(-fabsf(v));
-  const float s = __fdividef(e, 2.f + e), q = s * s;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q, 1.f / 13.f);
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  p = fmaf(p, q, 1.f);
-  if (sig) {
-    const float r = __fdividef(1.f, 1.f + e);
-    *sig = v >= 0.f ? r : e * r;
-  }
-  return fmaf(2.f * s, p, v > 0.f || v != v ? v : 0.f);
+
+__device__ __forceinline__ float min_nan(float a, float b) {     // a NaN stays
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ float sigmoid(float v) {
-  const float e = exp_neg(-fabsf(v)), r = __fdividef(1.f, 1.f + e);
-  return v != v ? v : (v >= 0.f ? r : e * r);
+
+// Two floats at a time: the scan is bound by instructions issued, and one of these does
+// the work of two.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
+__device__ __forceinline__ F2 twice(float a) { return pack(a, a); }
+__device__ __forceinline__ void split(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 ex2_2(F2 v) {
+  float a, b;
+  split(v, a, b);
+  return pack(ex2(a), ex2(b));
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  float a, b;
+  split(v, a, b);
+  return a + b;
+}
+
+// softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|), of two values.  The exponent's
+// rounding is put right by a first-order term; log1p(e) = e P(e) on [0, 1] with P of
+// degree 8, fitted for the smallest relative error (3e-8; 1.7e-7 with the roundings).
+// A NaN comes through e.  e: for the caller's sigmoid.
+__device__ __forceinline__ F2 softplus2(F2 v, F2* e_out = nullptr) {
+  float a, b;
+  split(v, a, b);
+  // (beyond 100 e is zero: the parts of an infinite product would make a NaN)
+  const F2 u = pack(min_nan(fabsf(a), 100.f), min_nan(fabsf(b), 100.f)), hi = mul2(u, twice(kLog2e));
+  const F2 off = fma2(u, twice(-kLog2e), hi);                // hi less the exact product
+  float ha, hb;
+  split(hi, ha, hb);
+  F2 e = pack(ex2(-ha), ex2(-hb));
+  e = fma2(mul2(e, off), twice(kLn2), e);
+  if (e_out) *e_out = e;
+  F2 p = twice(0.0052326940931379795f);
+  p = fma2(p, e, twice(-0.029505237936973572f));
+  p = fma2(p, e, twice(0.07822595536708832f));
+  p = fma2(p, e, twice(-0.13663245737552643f));
+  p = fma2(p, e, twice(0.19106006622314453f));
+  p = fma2(p, e, twice(-0.2484298199415207f));
+  p = fma2(p, e, twice(0.3331909775733948f));
+  p = fma2(p, e, twice(-0.4999949336051941f));
+  p = fma2(p, e, twice(0.9999999403953552f));
+  return fma2(p, e, pack(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+__device__ __forceinline__ float softplus(float v) {
+  float a, b;
+  split(softplus2(twice(v)), a, b);
+  return a;
+}
+// 1 / (1 + exp(-v)) of two values: 0 where the exponential is infinite.
+__device__ __forceinline__ F2 sigmoid2(F2 v) {
+  const F2 e = add2(ex2_2(mul2(v, twice(-kLog2e))), twice(1.f));
+  float a, b;
+  split(e, a, b);
+  return pack(rcp(a), rcp(b));
+}
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(v * -kLog2e)); }
 
 // The warp's tile of channels.
 template <class G>
@@ -125,87 +183,65 @@ struct Tile {
   __device__ __forceinline__ int col() const { return lane % G::LPR * G::VN; }
 };
 
+// A thread's states go in pairs: two channels of one state, or (one channel a thread)
+// two states.  Element k of CPL * NS, pair k / 2: its channel and state.
 template <class G>
-__device__ __forceinline__ void load_A(const Args& a, const Tile<G>& w, float (&A2)[G::CPL][G::NS]) {
+__device__ __forceinline__ int channel_of(int k) { return G::CPL > 1 ? k / (2 * G::NS) * 2 + (k & 1) : 0; }
+template <class G>
+__device__ __forceinline__ int state_of(int k) { return G::CPL > 1 ? k / 2 % G::NS : k; }
+
+template <class G>
+__device__ __forceinline__ void load_A(const Args& a, const Tile<G>& w, F2 (&A2)[G::PAIRS]) {
 #pragma unroll
-  for (int i = 0; i < G::CPL; ++i)
+  for (int p = 0; p < G::PAIRS; ++p) {
+    float f[2];
 #pragma unroll
-    for (int j = 0; j < G::NS; ++j) {
-      const int n = w.sl * G::NS + j;
-      A2[i][j] = w.has(i) && n < a.N ? __ldg(a.A + (long long)w.channel(i) * a.N + n) * kLog2e : 0.f;
+    for (int m = 0; m < 2; ++m) {
+      const int i = channel_of<G>(2 * p + m), n = w.sl * G::NS + state_of<G>(2 * p + m);
+      f[m] = w.has(i) && n < a.N ? __ldg(a.A + (long long)w.channel(i) * a.N + n) * kLog2e : 0.f;
     }
+    A2[p] = pack(f[0], f[1]);
+  }
 }
 
 // States [sequence, d, N] as the caller has them.
 template <class G>
-__device__ __forceinline__ void load_state(const Args& a, const Tile<G>& w, const float* p, long long seq, float (&h)[G::CPL][G::NS]) {
+__device__ __forceinline__ void load_state(const Args& a, const Tile<G>& w, const float* s, long long seq, F2 (&h)[G::PAIRS]) {
 #pragma unroll
-  for (int i = 0; i < G::CPL; ++i)
+  for (int p = 0; p < G::PAIRS; ++p) {
+    float f[2];
 #pragma unroll
-    for (int j = 0; j < G::NS; ++j) {
-      const int n = w.sl * G::NS + j;
-      h[i][j] = p && w.has(i) && n < a.N ? p[(seq * a.d + w.channel(i)) * a.N + n] : 0.f;
+    for (int m = 0; m < 2; ++m) {
+      const int i = channel_of<G>(2 * p + m), n = w.sl * G::NS + state_of<G>(2 * p + m);
+      f[m] = s && w.has(i) && n < a.N ? s[(seq * a.d + w.channel(i)) * a.N + n] : 0.f;
     }
+    h[p] = pack(f[0], f[1]);
+  }
 }
 template <class G>
-__device__ __forceinline__ void store_state(const Args& a, const Tile<G>& w, float* p, long long seq, const float (&h)[G::CPL][G::NS]) {
+__device__ __forceinline__ void store_state(const Args& a, const Tile<G>& w, float* s, long long seq, const F2 (&h)[G::PAIRS]) {
 #pragma unroll
-  for (int i = 0; i < G::CPL; ++i)
+  for (int p = 0; p < G::PAIRS; ++p) {
+    float f[2];
+    split(h[p], f[0], f[1]);
 #pragma unroll
-    for (int j = 0; j < G::NS; ++j) {
-      const int n = w.sl * G::NS + j;
-      if (w.has(i) && n < a.N) p[(seq * a.d + w.channel(i)) * a.N + n] = h[i][j];
+    for (int m = 0; m < 2; ++m) {
+      const int i = channel_of<G>(2 * p + m), n = w.sl * G::NS + state_of<G>(2 * p + m);
+      if (w.has(i) && n < a.N) s[(seq * a.d + w.channel(i)) * a.N + n] = f[m];
     }
+  }
 }
 // States as the kernels hand them on: a warp's registers side by side.
 template <class G>
-__device__ __forceinline__ long long lane_at(long long block, int k, int lane) {
-  return (block * (G::CPL * G::NS / 2) + k) * 32 + lane;
+__device__ __forceinline__ void load_lanes(const float* s, long long block, int lane, F2 (&h)[G::PAIRS]) {
+#pragma unroll
+  for (int p = 0; p < G::PAIRS; ++p) h[p] = reinterpret_cast<const F2*>(s)[(block * G::PAIRS + p) * 32 + lane];
 }
 template <class G>
-__device__ __forceinline__ void load_lanes(const float* p, long long block, int lane, float (&h)[G::CPL][G::NS]) {
+__device__ __forceinline__ void store_lanes(float* s, long long block, int lane, const F2 (&h)[G::PAIRS]) {
 #pragma unroll
-  for (int i = 0; i < G::CPL; ++i)
-#pragma unroll
-    for (int j = 0; j < G::NS; j += 2) {
-      const float2 v = reinterpret_cast<const float2*>(p)[lane_at<G>(block, (i * G::NS + j) / 2, lane)];
-      h[i][j] = v.x;
-      h[i][j + 1] = v.y;
-    }
+  for (int p = 0; p < G::PAIRS; ++p) reinterpret_cast<F2*>(s)[(block * G::PAIRS + p) * 32 + lane] = h[p];
 }
-template <class G>
-__device__ __forceinline__ void store_lanes(float* p, long long block, int lane, const float (&h)[G::CPL][G::NS]) {
-#pragma unroll
-  for (int i = 0; i < G::CPL; ++i)
-#pragma unroll
-    for (int j = 0; j < G::NS; j += 2)
-      reinterpret_cast<float2*>(p)[lane_at<G>(block, (i * G::NS + j) / 2, lane)] = make_float2(h[i][j], h[i][j + 1]);
-}
-
-// A chunk's vectors of a [rows, channels] tensor, zeros outside.
-template <class G>
-__device__ __forceinline__ void load_raw(const Tile<G>& w, const void* p, long long ld, long long row0, int n, uint4 (&v)[G::P]) {
-  const typename G::E* q = static_cast<const typename G::E*>(p) + w.c0 + w.col();
-#pragma unroll
-  for (int k = 0; k < G::P; ++k) {
-    v[k] = make_uint4(0, 0, 0, 0);
-    if (w.row(k) < n && w.col() < w.cols) v[k] = __ldg(reinterpret_cast<const uint4*>(q + (row0 + w.row(k)) * ld));
-  }
-}
-template <class E> struct Unpack;
-template <> struct Unpack<__nv_bfloat16> {
-  using V = rows::Vec<__nv_bfloat16, 8>;
-  __device__ static __forceinline__ void get(float (&f)[8], const uint4& v) { V::get(f, v); }
-  __device__ static __forceinline__ uint4 make(const float (&f)[8]) { return V::make(f); }
-};
-template <> struct Unpack<float> {
-  __device__ static __forceinline__ void get(float (&f)[4], const uint4& v) {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
-  }
-  __device__ static __forceinline__ uint4 make(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-};
 
 // N floats to or from shared memory, 16 bytes at a time.
 template <int N>
@@ -232,6 +268,115 @@ __device__ __forceinline__ void get(const float* p, float (&v)[N]) {
     v[0] = f.x; v[1] = f.y;
   } else {
     v[0] = p[0];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void put_pairs(float* s, const F2 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) *reinterpret_cast<ulonglong2*>(s + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+}
+template <int N>
+__device__ __forceinline__ void get_pairs(const float* s, F2 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(s + 2 * i);
+    v[i] = u.x;
+    v[i + 1] = u.y;
+  }
+}
+// What a lane reads of a token, as pairs that fit its states': dt (or dt x, or g) of its
+// channels, B (or C) of its states.  A value that goes with two channels is doubled in
+// registers: from shared memory each register that a lane reads costs a quarter of the
+// SM's cycle, and those reads are as scarce as instructions.
+template <class G>
+__device__ __forceinline__ void get_channels(const float* row, int cl, F2 (&v)[G::CPAIRS]) {
+  if constexpr (G::CPL == 4) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(row + cl * 4);
+    v[0] = u.x;
+    v[1] = u.y;
+  } else if constexpr (G::CPL == 2) {
+    v[0] = *reinterpret_cast<const F2*>(row + cl * 2);
+  } else {
+    v[0] = twice(row[cl]);
+  }
+}
+template <class G>
+__device__ __forceinline__ void get_states(const float* row, int sl, F2 (&v)[G::SPAIRS]) {
+  if constexpr (G::CPL == 1) {
+    get_pairs(row + sl * G::NS, v);
+  } else {
+    float f[G::NS];
+    get(row + sl * G::NS, f);
+#pragma unroll
+    for (int j = 0; j < G::NS; ++j) v[j] = twice(f[j]);
+  }
+}
+// The pairs that state pair p needs.
+template <class G>
+constexpr __device__ __forceinline__ int cpair(int p) { return G::CPL > 1 ? p / G::NS : 0; }
+template <class G>
+constexpr __device__ __forceinline__ int spair(int p) { return G::CPL > 1 ? p % G::NS : p; }
+
+// A chunk's vectors of a [rows, channels] tensor, zeros outside.
+template <class G>
+__device__ __forceinline__ void load_raw(const Tile<G>& w, const void* p, long long ld, long long row0, int n, uint4 (&v)[G::P]) {
+  const typename G::E* q = static_cast<const typename G::E*>(p) + w.c0 + w.col();
+#pragma unroll
+  for (int k = 0; k < G::P; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    if (w.row(k) < n && w.col() < w.cols) v[k] = __ldg(reinterpret_cast<const uint4*>(q + (row0 + w.row(k)) * ld));
+  }
+}
+template <class E> struct Unpack;
+template <> struct Unpack<__nv_bfloat16> {
+  __device__ static __forceinline__ void get(float (&f)[8], const uint4& v) { rows::Vec<__nv_bfloat16, 8>::get(f, v); }
+  __device__ static __forceinline__ void pairs(F2 (&p)[4], const uint4& v) {
+    float f[8];
+    get(f, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ static __forceinline__ uint4 make(const F2 (&p)[4]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
+    return rows::Vec<__nv_bfloat16, 8>::make(f);
+  }
+};
+template <> struct Unpack<float> {
+  __device__ static __forceinline__ void get(float (&f)[4], const uint4& v) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  __device__ static __forceinline__ void pairs(F2 (&p)[2], const uint4& v) {
+    p[0] = pack(__uint_as_float(v.x), __uint_as_float(v.y));
+    p[1] = pack(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  __device__ static __forceinline__ uint4 make(const F2 (&p)[2]) {
+    float f[4];
+    split(p[0], f[0], f[1]);
+    split(p[1], f[2], f[3]);
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+// The lane's columns of a vector over channels (NULL: zeros).
+template <class G>
+__device__ __forceinline__ void load_pairs(const Tile<G>& w, const float* s, F2 (&v)[G::VN / 2]) {
+#pragma unroll
+  for (int e = 0; e < G::VN / 2; ++e) {
+    const bool in = s && w.col() < w.cols;
+    v[e] = pack(in ? __ldg(s + w.c0 + w.col() + 2 * e) : 0.f, in ? __ldg(s + w.c0 + w.col() + 2 * e + 1) : 0.f);
+  }
+}
+// A segment's sums of dt, of each of the thread's channels.
+template <class G>
+__device__ __forceinline__ void store_sums(const Args& a, long long block, int lane, const F2 (&sum)[G::CPAIRS]) {
+#pragma unroll
+  for (int i = 0; i < G::CPAIRS; ++i) {
+    float f[2];
+    split(sum[i], f[0], f[1]);
+#pragma unroll
+    for (int m = 0; m < (G::CPL > 1 ? 2 : 1); ++m) a.sdt[(block * G::CPL + 2 * i + m) * 32 + lane] = f[m];
   }
 }
 
@@ -283,7 +428,7 @@ __global__ void __launch_bounds__(kCarryThreads) k_ssm_carry(Args a) {
   const long long id = (long long)blockIdx.x * kCarryThreads + threadIdx.x;      // (tile, pair, lane, one of the pair)
   if (id >= (long long)a.tiles * CN * 32) return;
   const int in = (int)(id % (CN * 32)), tile = (int)(id / (CN * 32));
-  const int pair = in / 64, lane = in / 2 % 32, k = pair * 2 + in % 2, i = k / G::NS, j = k % G::NS;
+  const int pair = in / 64, lane = in / 2 % 32, k = pair * 2 + in % 2, i = channel_of<G>(k), j = state_of<G>(k);
   const int c = tile % a.tpg * G::CW + (lane >> 2) * G::CPL + i, n = (lane & 3) * G::NS + j;
   if (c >= a.per || n >= a.N) return;
   const float A2 = __ldg(a.A + ((long long)(tile / a.tpg) * a.per + c) * a.N + n) * kLog2e;
