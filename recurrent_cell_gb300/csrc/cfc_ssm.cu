@@ -16,38 +16,54 @@ struct __align__(16) FwdTiles {
   float dt[kT][G::CW], dx[kT][G::CW];        // dt, dt x
   float B[kT][G::NP];
   float C[LOCAL ? 1 : kT][G::NP];
-  float y[LOCAL ? 1 : kT][4][G::CW];         // C . h, a part from each state lane
+  float y[LOCAL ? 1 : kT][4 * G::CW];        // C . h, a part from each state lane
+};
+
+// Where state lane sl's part of channels c .. c + CPL - 1 of row t lies.  With 4 channels a
+// lane, 16-byte pieces permuted so that neither the lanes of a token nor those that add
+// the parts of several rows meet in a bank.
+template <class G>
+__device__ __forceinline__ int y_at(int t, int sl, int c) {
+  if constexpr (G::CPL == 4) return (c >> 3) * 32 + (((((c >> 2) & 1) * 4 + sl) ^ ((c >> 3) | (t & 1) << 2)) << 2);
+  else return sl * G::CW + c;
+}
+
+// What a token reads of the tiles.
+template <class G, bool LOCAL>
+struct Operands {
+  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS], c[G::SPAIRS];
+  __device__ __forceinline__ void read(const FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t) {
+    get_channels<G>(sm.dt[t], w.cl, dt);
+    get_channels<G>(sm.dx[t], w.cl, dx);
+    get_states<G>(sm.B[t], w.sl, b);
+    if constexpr (!LOCAL) get_states<G>(sm.C[t], w.sl, c);
+  }
 };
 
 // One token: the states, and C . h of the lane's states.
 template <class G, bool LOCAL>
-__device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t, const F2 (&A2)[G::PAIRS],
-                                      F2 (&h)[G::PAIRS], F2 (&sum)[G::CPAIRS]) {
-  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS], c[G::SPAIRS], y[G::CPAIRS];
-  get_channels<G>(sm.dt[t], w.cl, dt);
-  get_channels<G>(sm.dx[t], w.cl, dx);
-  get_states<G>(sm.B[t], w.sl, b);
-  if constexpr (!LOCAL) get_states<G>(sm.C[t], w.sl, c);
+__device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t, const Operands<G, LOCAL>& o,
+                                      const F2 (&A2)[G::PAIRS], F2 (&h)[G::PAIRS], F2 (&sum)[G::CPAIRS]) {
+  F2 y[G::CPAIRS];
 #pragma unroll
   for (int p = 0; p < G::PAIRS; ++p) {
     const int i = cpair<G>(p), j = spair<G>(p);
-    h[p] = fma2(ex2_2(mul2(dt[i], A2[p])), h[p], mul2(dx[i], b[j]));
-    if constexpr (!LOCAL) y[i] = j == 0 ? mul2(c[j], h[p]) : fma2(c[j], h[p], y[i]);
+    h[p] = fma2(ex2_2(mul2(o.dt[i], A2[p])), h[p], mul2(o.dx[i], o.b[j]));
+    if constexpr (!LOCAL) y[i] = j == 0 ? mul2(o.c[j], h[p]) : fma2(o.c[j], h[p], y[i]);
   }
   if constexpr (LOCAL) {
 #pragma unroll
-    for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], dt[i]);
-  } else if constexpr (G::CPL == 4) {
-    *reinterpret_cast<ulonglong2*>(&sm.y[t][w.sl][w.cl * 4]) = make_ulonglong2(y[0], y[1]);
-  } else if constexpr (G::CPL == 2) {
-    *reinterpret_cast<F2*>(&sm.y[t][w.sl][w.cl * 2]) = y[0];
+    for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], o.dt[i]);
   } else {
-    sm.y[t][w.sl][w.cl] = sum2(y[0]);
+    float* to = sm.y[t] + y_at<G>(t, w.sl, w.cl * G::CPL);
+    if constexpr (G::CPL == 4) *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(y[0], y[1]);
+    else if constexpr (G::CPL == 2) *reinterpret_cast<F2*>(to) = y[0];
+    else *to = sum2(y[0]);
   }
 }
 
 template <class G, bool LOCAL>
-__global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
+__global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
   using E = typename G::E;
   constexpr int P = G::P, VN = G::VN, VP = VN / 2;
   __shared__ FwdTiles<G, LOCAL> sm;
@@ -129,13 +145,23 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
     __syncwarp();
     fetch(row + kT);
     if (n == kT && q.begin < row && q.end > row + kT) {    // inside one sequence: no state comes or goes
+      Operands<G, LOCAL> now, next;
+      now.read(sm, w, 0);
 #pragma unroll 4
-      for (int t = 0; t < kT; ++t) token<G, LOCAL>(sm, w, t, A2, h, sum);
+      for (int t = 0; t < kT; ++t) {
+        next.read(sm, w, t + 1 < kT ? t + 1 : t);
+        token<G, LOCAL>(sm, w, t, now, A2, h, sum);
+        now = next;
+      }
     } else {
       for (int t = 0; t < n;) {
         if (row + t == q.begin) load_state<G>(a, w, a.init, q.i, h);
         const int m = q.end - row < n ? (int)(q.end - row) : n;
-        for (; t < m; ++t) token<G, LOCAL>(sm, w, t, A2, h, sum);
+        for (; t < m; ++t) {
+          Operands<G, LOCAL> now;
+          now.read(sm, w, t);
+          token<G, LOCAL>(sm, w, t, now, A2, h, sum);
+        }
         if (!LOCAL && row + t == q.end) {
           if (a.final_state) store_state<G>(a, w, a.final_state, q.i, h);
           if (row + t < a.s.rows) q = seqs::find(a.s, row + t);
@@ -150,9 +176,13 @@ __global__ void __launch_bounds__(32) k_ssm(Args a, bool save) {
           F2 z[VP];
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            get_pairs(&sm.y[w.row(k)][s][w.col()], z);
 #pragma unroll
-            for (int e = 0; e < VP; ++e) y[k][e] = add2(y[k][e], z[e]);
+            for (int e = 0; e < VP; e += 2) {
+              const float* part = sm.y[w.row(k)] + y_at<G>(w.row(k), s, w.col() + 2 * e);
+              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(part);
+              y[k][e] = add2(y[k][e], u.x);
+              y[k][e + 1] = add2(y[k][e + 1], u.y);
+            }
           }
           if (a.z) {
             Unpack<E>::pairs(z, zv[k]);

@@ -9,10 +9,10 @@
 //   dB    = sum_c dt x dh                  dC = sum_c g h
 //   dz    = grad_y (C . h + D x) silu'(z)  dD = sum_t g x,  dbias = sum_t ddelta
 // A chunk starts from the state that the forward saved before it.  A first sweep runs
-// it forward and keeps the state before every second token; the second goes back two
-// tokens at a time and forms the state in between anew (one multiply-add, since it needs a
-// anyway), which halves the shared memory that states take.  The two exponentials and some fifteen multiply-adds
-// a state are the bound, not memory.
+// it forward and puts every state into tensor memory, which here is nothing but memory: 64 KB
+// a warp that the other warps' traffic through shared memory, as scarce as
+// instructions in this kernel, does not see.  The second sweep goes back.  The two exponentials
+// and some fifteen multiply-adds a state are the bound, not memory.
 //
 // Sums over a channel's states and over a tile's channels are taken by lane steps that
 // halve the values as they go: 12 values over 4 lanes in 9 steps, 8 over 8 in 7.  Four
@@ -20,6 +20,7 @@
 // workspace is a sum over 128 channels; k_ssm_bc adds those.  dA, dD and dbias are
 // kept in registers over a segment; reduce_axis0 adds the segments.
 #include "ssm_common.cuh"
+#include "tc_common.cuh"
 
 namespace cfc {
 namespace ssm {
@@ -28,12 +29,56 @@ constexpr int kBwdWarps = 4;
 
 template <class G>
 struct __align__(16) BwdTiles {
-  float dt[kT][G::CW], dx[kT][G::CW], g[kT][G::CW];          // dt, dt x, g; then sum e A, sum dh B, C . h
+  float dt[kT][G::CW], sig[kT][G::CW];                       // dt and its slope sigmoid(delta + bias)
+  float dx[kT][G::CW], g[kT][G::CW];                         // dt x and g, then sum dh B and C . h
+  float s2[kT][G::CW];                                       // sum e A
   float B[kT][G::NP], C[kT][G::NP];
   float bc[kT][2 * G::NP];                                   // dB, dC of the tile
-  ulonglong2 h[kT / 2][G::PAIRS / 2][32];                    // states before rows 0, 2, 4, ...
   F2 gA[G::PAIRS][32];                                       // dA of the chunks so far
+  uint4 raw[4][G::P][32];                                    // the next chunk's x, delta, z, grad_y as the lanes take them,
+  uint4 rawB[2][G::BL][32];                                  // B and C,
+  F2 h0[G::PAIRS][32];                                       // and the state before it
 };
+
+// A thread's states to and from tensor memory, at `at` of its warp's part.
+template <int N>
+__device__ __forceinline__ void tmem_put(uint32_t at, const F2 (&h)[N]) {
+  static_assert(N == 4 || N == 8, "8 or 16 columns");
+  uint32_t r[2 * N];
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    float a, b;
+    split(h[p], a, b);
+    r[2 * p] = __float_as_uint(a);
+    r[2 * p + 1] = __float_as_uint(b);
+  }
+  if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_get(uint32_t at, F2 (&h)[N]) {
+  float f[2 * N];
+  if constexpr (N == 8) tc::tmem_ld16(at, f);
+  else tc::tmem_ld8(at, f);
+#pragma unroll
+  for (int p = 0; p < N; ++p) h[p] = pack(f[2 * p], f[2 * p + 1]);
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 bytes of global memory (or zeros) to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() {
+  asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+}
 
 // One value of each lane's quarter: v[i] summed over the lanes of a group of 4
 // (M = 1, 2) or 8 (M = 4, 8, 16), value i of N ending up in the lanes whose bits of M say i.
@@ -178,29 +223,26 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
 template <class G>
 struct Token {
   F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS];
-  __device__ __forceinline__ Token(const BwdTiles<G>& sm, const Tile<G>& w, int t) {
+  __device__ __forceinline__ void read(const BwdTiles<G>& sm, const Tile<G>& w, int t) {
     get_channels<G>(sm.dt[t], w.cl, dt);
     get_channels<G>(sm.dx[t], w.cl, dx);
     get_states<G>(sm.B[t], w.sl, b);
   }
-  // a h + dt x B, from a
-  __device__ __forceinline__ void forward(const F2 (&e)[G::PAIRS], F2 (&h)[G::PAIRS]) const {
+  __device__ __forceinline__ void forward(const F2 (&A2)[G::PAIRS], F2 (&h)[G::PAIRS]) const {
 #pragma unroll
-    for (int p = 0; p < G::PAIRS; ++p) h[p] = fma2(e[p], h[p], mul2(dx[cpair<G>(p)], b[spair<G>(p)]));
-  }
-  __device__ __forceinline__ void decay(const F2 (&A2)[G::PAIRS], F2 (&e)[G::PAIRS]) const {
-#pragma unroll
-    for (int p = 0; p < G::PAIRS; ++p) e[p] = ex2_2(mul2(dt[cpair<G>(p)], A2[p]));
+    for (int p = 0; p < G::PAIRS; ++p)
+      h[p] = fma2(ex2_2(mul2(dt[cpair<G>(p)], A2[p])), h[p], mul2(dx[cpair<G>(p)], b[spair<G>(p)]));
   }
 };
 
-// Token t backward, h being the state before it and e its decays: the token's sums into the
-// tiles, dh on to the token before it.
+// Token t backward, h being the state before it: the token's sums into the tiles, dh on to the
+// token before it.
 template <class G>
-__device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int t, const Token<G>& k, const F2 (&e)[G::PAIRS],
-                                          const F2 (&h)[G::PAIRS], const F2 (&A2)[G::PAIRS], F2 (&dh)[G::PAIRS],
-                                          F2 (&gA)[G::PAIRS]) {
+__device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int t, const F2 (&h)[G::PAIRS],
+                                          const F2 (&A2)[G::PAIRS], F2 (&dh)[G::PAIRS], F2 (&gA)[G::PAIRS]) {
   constexpr int CPL = G::CPL, NS = G::NS, NP = G::NP;
+  Token<G> k;
+  k.read(sm, w, t);
   F2 g[G::CPAIRS], c[G::SPAIRS], s1[G::CPAIRS], s2[G::CPAIRS], y[G::CPAIRS], db[G::SPAIRS], dc[G::SPAIRS];
   get_channels<G>(sm.g[t], w.cl, g);
   get_states<G>(sm.C[t], w.sl, c);
@@ -208,14 +250,15 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
   for (int p = 0; p < G::PAIRS; ++p) {
     const int i = cpair<G>(p), j = spair<G>(p);
     const bool first_i = G::CPL > 1 ? j == 0 : p == 0, first_j = G::CPL > 1 ? i == 0 : true;
-    const F2 ah = mul2(e[p], h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(c[j], g[i], dh[p]), q = mul2(d, ah);
+    const F2 e = ex2_2(mul2(k.dt[i], A2[p]));
+    const F2 ah = mul2(e, h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(c[j], g[i], dh[p]), q = mul2(d, ah);
     y[i] = first_i ? mul2(c[j], now) : fma2(c[j], now, y[i]);
     s1[i] = first_i ? mul2(d, k.b[j]) : fma2(d, k.b[j], s1[i]);
     s2[i] = first_i ? mul2(q, A2[p]) : fma2(q, A2[p], s2[i]);
     gA[p] = fma2(q, k.dt[i], gA[p]);
     db[j] = first_j ? mul2(d, k.dx[i]) : fma2(d, k.dx[i], db[j]);
     dc[j] = first_j ? mul2(g[i], now) : fma2(g[i], now, dc[j]);
-    dh[p] = mul2(e[p], d);
+    dh[p] = mul2(e, d);
   }
   float f1[CPL], f2[CPL], f3[CPL], bc[2 * NS];
   if constexpr (CPL > 1) {
@@ -246,7 +289,7 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
   __syncwarp();
   if (w.sl < CPL) {
     sm.dx[t][w.cl * CPL + w.sl] = o1;
-    sm.dt[t][w.cl * CPL + w.sl] = o2 * kLn2;
+    sm.s2[t][w.cl * CPL + w.sl] = o2 * kLn2;
     sm.g[t][w.cl * CPL + w.sl] = o3;
   }
   if constexpr (NS == 2) {
@@ -261,11 +304,13 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
 }
 
 template <class G>
-__global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
   using E = typename G::E;
   using U = Unpack<E>;
-  constexpr int VN = G::VN, VP = VN / 2, NP = G::NP, PAIRS = G::PAIRS;
+  constexpr int VN = G::VN, VP = VN / 2, NP = G::NP, PAIRS = G::PAIRS, P = G::P;
+  constexpr uint32_t kColumns = 2 * PAIRS * kT;              // of tensor memory
   extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ uint32_t tmem;
   BwdTiles<G>* tiles = reinterpret_cast<BwdTiles<G>*>(raw);
   const int warp = threadIdx.x >> 5;
   BwdTiles<G>& sm = tiles[warp];
@@ -293,8 +338,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
     return;
   }
 
+  if (warp == 0) tc::tmem_alloc(&tmem, kColumns);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t states = tmem + ((uint32_t)warp * 32u << 16);
+
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
-  const int chunks = (int)((r1 - r0 + kT - 1) / kT);
   F2 A2[PAIRS], bias[VP], D[VP], gD[VP] = {}, gb[VP] = {};
   load_A<G>(a, w, A2);
   load_pairs<G>(w, a.bias, bias);
@@ -302,72 +352,132 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
 #pragma unroll
   for (int p = 0; p < PAIRS; ++p) sm.gA[p][w.lane] = 0;
 
-  const Where q = seqs::find(a.s, r1 - 1);
+  Where q = seqs::find(a.s, r1 - 1);           // the sequence of the row at hand, from the last back
   if (q.end > r1) load_lanes<G>(a.local, (long long)(seg + 1) * a.tiles + tile, w.lane, dh);
   else load_state<G>(a, w, a.grad_final, q.i, dh);
 
-  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+  // a chunk's inputs, on their way while the chunk behind it is worked on
+  auto vector = [&](const void* p, long long ld, long long r) {
+    return static_cast<const E*>(p) + r * ld + w.c0 + w.col();
+  };
+  auto fetch = [&](int chunk) {
     const long long row = r0 + (long long)chunk * kT;
     const int n = r1 - row < kT ? (int)(r1 - row) : kT;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const bool in = w.row(k) < n && w.col() < w.cols;
+      const long long r = in ? row + w.row(k) : 0;
+      copy16(&sm.raw[0][k][w.lane], in ? vector(a.x, a.ldx, r) : a.x, in);
+      copy16(&sm.raw[1][k][w.lane], in ? vector(a.delta, a.ldd, r) : a.delta, in);
+      if (a.z) copy16(&sm.raw[2][k][w.lane], in ? vector(a.z, a.ldz, r) : a.z, in);
+      copy16(&sm.raw[3][k][w.lane], in ? vector(a.grad_y, a.d, r) : a.grad_y, in);
+    }
+    if (a.vec_bc)
+#pragma unroll
+      for (int k = 0; k < G::BL; ++k) {
+        const int i = k * 32 + w.lane, r = i / G::BV;
+        const bool in = r < n;
+        const long long off = w.g * a.N + i % G::BV * VN;
+        copy16(&sm.rawB[0][k][w.lane], in ? static_cast<const E*>(a.B) + (row + r) * a.ldb + off : a.B, in);
+        copy16(&sm.rawB[1][k][w.lane], in ? static_cast<const E*>(a.C) + (row + r) * a.ldc + off : a.C, in);
+      }
+    const F2* from = reinterpret_cast<const F2*>(a.ckpt) + (((long long)seg * a.cps + chunk) * a.tiles + tile) * PAIRS * 32;
+#pragma unroll
+    for (int p = 0; p < PAIRS; p += 2) copy16(&sm.h0[0][0] + p * 32 + w.lane * 2, from + p * 32 + w.lane * 2, true);
+  };
+
+  int chunk = (int)((r1 - r0 + kT - 1) / kT) - 1;
+  fetch(chunk);
+  for (; chunk >= 0; --chunk) {
+    const long long row = r0 + (long long)chunk * kT;
+    const int n = r1 - row < kT ? (int)(r1 - row) : kT;
+    copies_done();
+    __syncwarp();
+    // dt, its slope, dt x and g of the chunk's tokens
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      F2 x[VP], dt[VP], sig[VP], z[VP], g[VP];
+      U::pairs(x, sm.raw[0][k][w.lane]);
+      U::pairs(dt, sm.raw[1][k][w.lane]);
+      U::pairs(g, sm.raw[3][k][w.lane]);
+      if (a.z) {
+        U::pairs(z, sm.raw[2][k][w.lane]);
+#pragma unroll
+        for (int e = 0; e < VP; ++e) g[e] = mul2(g[e], mul2(z[e], sigmoid2(z[e])));
+      }
+#pragma unroll
+      for (int e = 0; e < VP; ++e) {
+        F2 en;
+        const F2 v = add2(dt[e], bias[e]);
+        dt[e] = softplus2(v, &en);
+        float va, vb, ea, eb;                  // sigmoid(v) = 1 / (1 + e), or e / (1 + e) below zero
+        split(v, va, vb);
+        split(en, ea, eb);
+        sig[e] = pack((va >= 0.f ? 1.f : ea) * rcp(1.f + ea), (vb >= 0.f ? 1.f : eb) * rcp(1.f + eb));
+        x[e] = mul2(x[e], dt[e]);
+      }
+      if (w.row(k) < kT) {
+        put_pairs(&sm.dt[w.row(k)][w.col()], dt);
+        put_pairs(&sm.sig[w.row(k)][w.col()], sig);
+        put_pairs(&sm.dx[w.row(k)][w.col()], x);
+        put_pairs(&sm.g[w.row(k)][w.col()], g);
+      }
+    }
     Rows<G> bv, cv;
-    bv.fetch(a, w, a.B, a.ldb, row, n);
-    cv.fetch(a, w, a.C, a.ldc, row, n);
-    load_lanes<G>(a.ckpt, ((long long)seg * a.cps + chunk) * a.tiles + tile, w.lane, h);
-    stage_tokens<G>(a, w, row, n, bias, sm.dt, sm.dx, sm.g);
+    if (a.vec_bc)
+#pragma unroll
+      for (int k = 0; k < G::BL; ++k) {
+        bv.v[k] = sm.rawB[0][k][w.lane];
+        cv.v[k] = sm.rawB[1][k][w.lane];
+      }
     bv.stage(a, w, a.B, a.ldb, row, n, sm.B[0]);
     cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
-    unsigned starts = 0;                       // rows that begin a sequence, one bit each
-    for (Where f = seqs::find(a.s, row);;) {
-      if (f.begin >= row) starts |= 1u << (f.begin - row);
-      if (f.end >= row + n) break;
-      f = seqs::find(a.s, f.end);
-    }
-    __syncwarp();
-    // forward: the states before even rows
-    F2 gA[PAIRS], e[PAIRS];
-    for (int t = 0; t < n; ++t) {
-      if (starts >> t & 1) load_state<G>(a, w, a.init, seqs::find(a.s, row + t).i, h);
-      if ((t & 1) == 0)
 #pragma unroll
-        for (int p = 0; p < PAIRS; p += 2) sm.h[t / 2][p / 2][w.lane] = make_ulonglong2(h[p], h[p + 1]);
-      const Token<G> k(sm, w, t);
-      k.decay(A2, e);
-      k.forward(e, h);
-    }
-    // back, two rows at a time
+    for (int p = 0; p < PAIRS; ++p) h[p] = sm.h0[p][w.lane];
+    __syncwarp();
+    if (chunk > 0) fetch(chunk - 1);
+
+    F2 gA[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) gA[p] = 0;
-    // the first row of its sequence: out, and on with the one before
-    auto begin = [&](int t) {
-      if (!(starts >> t & 1)) return;
-      if (a.grad_init && on) store_state<G>(a, w, a.grad_init, seqs::find(a.s, row + t).i, dh);
-      if (row + t > 0) load_state<G>(a, w, a.grad_final, seqs::find(a.s, row + t - 1).i, dh);
-    };
-    for (int t = (n - 1) & ~1; t >= 0; t -= 2) {
-#pragma unroll
-      for (int p = 0; p < PAIRS; p += 2) {
-        const ulonglong2 v = sm.h[t / 2][p / 2][w.lane];
-        h[p] = v.x;
-        h[p + 1] = v.y;
-      }
-      const Token<G> k(sm, w, t);
-      k.decay(A2, e);
-      if (t + 1 < n) {
-        F2 h1[PAIRS], e1[PAIRS];
-        if (starts >> (t + 1) & 1) {
-          load_state<G>(a, w, a.init, seqs::find(a.s, row + t + 1).i, h1);
-        } else {
-#pragma unroll
-          for (int p = 0; p < PAIRS; ++p) h1[p] = h[p];
-          k.forward(e, h1);
+    if (q.begin < row && n == kT) {            // inside one sequence
+#pragma unroll 4
+      for (int t = 0; t < kT; ++t) {
+        tmem_put(states + t * 2 * PAIRS, h);
+        if (t + 1 < kT) {
+          Token<G> k;
+          k.read(sm, w, t);
+          k.forward(A2, h);
         }
-        const Token<G> k1(sm, w, t + 1);
-        k1.decay(A2, e1);
-        token_bwd<G>(sm, w, t + 1, k1, e1, h1, A2, dh, gA);
-        begin(t + 1);
       }
-      token_bwd<G>(sm, w, t, k, e, h, A2, dh, gA);
-      begin(t);
+      tmem_put_wait();
+#pragma unroll 2
+      for (int t = kT - 1; t >= 0; --t) {
+        tmem_get(states + t * 2 * PAIRS, h);
+        token_bwd<G>(sm, w, t, h, A2, dh, gA);
+      }
+    } else {
+      Where f = seqs::find(a.s, row);
+      for (int t = 0; t < n; ++t) {
+        if (row + t >= f.end) f = seqs::find(a.s, row + t);
+        if (row + t == f.begin) load_state<G>(a, w, a.init, f.i, h);
+        tmem_put(states + t * 2 * PAIRS, h);
+        Token<G> k;
+        k.read(sm, w, t);
+        k.forward(A2, h);
+      }
+      tmem_put_wait();
+      for (int t = n - 1; t >= 0; --t) {
+        tmem_get(states + t * 2 * PAIRS, h);
+        token_bwd<G>(sm, w, t, h, A2, dh, gA);
+        if (row + t == q.begin) {              // the first row of its sequence: out, and on with the one before
+          if (a.grad_init && on) store_state<G>(a, w, a.grad_init, q.i, dh);
+          if (row + t > r0) {
+            q = seqs::find(a.s, row + t - 1);
+            load_state<G>(a, w, a.grad_final, q.i, dh);
+          }
+        }
+      }
     }
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) sm.gA[p][w.lane] = add2(sm.gA[p][w.lane], gA[p]);
@@ -375,54 +485,45 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
     // the chunk's rows, channel by channel
     F2 cD[VP] = {}, cb[VP] = {};               // dD and dbias of the chunk
 #pragma unroll
-    for (int k = 0; k < G::P; ++k)
+    for (int k = 0; k < P; ++k)
       if (w.row(k) < n && w.col() < w.cols && on) {
         const long long r = row + w.row(k);
-        const int col = w.c0 + w.col();
-        auto in = [&](const void* p, long long ld, F2 (&f)[VP]) {
-          U::pairs(f, __ldg(reinterpret_cast<const uint4*>(static_cast<const E*>(p) + r * ld + col)));
-        };
         auto out = [&](void* p, const F2 (&f)[VP]) {
-          __stcs(reinterpret_cast<uint4*>(static_cast<E*>(p) + r * a.d + col), U::make(f));
+          __stcs(reinterpret_cast<uint4*>(static_cast<E*>(p) + r * a.d + w.c0 + w.col()), U::make(f));
         };
-        F2 x[VP], g[VP], f[VP], s1[VP], dt[VP], sig[VP];
-        in(a.x, a.ldx, x);
-        in(a.delta, a.ldd, f);
-#pragma unroll
-        for (int e = 0; e < VP; ++e) {
-          F2 en;
-          const F2 v = add2(f[e], bias[e]);
-          dt[e] = softplus2(v, &en);
-          float va, vb, ea, eb;                // sigmoid(v) = 1 / (1 + e), or e / (1 + e) below zero
-          split(v, va, vb);
-          split(en, ea, eb);
-          sig[e] = pack((va >= 0.f ? 1.f : ea) * rcp(1.f + ea), (vb >= 0.f ? 1.f : eb) * rcp(1.f + eb));
-        }
-        in(a.grad_y, a.d, g);
+        F2 x[VP], g[VP], f[VP], s1[VP], u[VP];
+        const uint4 xv = load_here(vector(a.x, a.ldx, r)), gv = load_here(vector(a.grad_y, a.d, r));
+        uint4 zv = make_uint4(0, 0, 0, 0);
+        if (a.z) zv = load_here(vector(a.z, a.ldz, r));
+        U::pairs(x, xv);
+        U::pairs(g, gv);
         if (a.z) {
-          F2 z[VP], y[VP];
-          in(a.z, a.ldz, z);
-          get_pairs(&sm.g[w.row(k)][w.col()], y);
+          F2 z[VP];
+          U::pairs(z, zv);
+          get_pairs(&sm.g[w.row(k)][w.col()], u);
 #pragma unroll
           for (int e = 0; e < VP; ++e) {
             // silu'(z) = s (1 + z (1 - s)) = s + z s (1 - s)
             const F2 s = sigmoid2(z[e]), zs = mul2(z[e], s);
-            y[e] = mul2(fma2(D[e], x[e], y[e]), g[e]);
-            y[e] = mul2(y[e], fma2(zs, fma2(s, twice(-1.f), twice(1.f)), s));
+            u[e] = mul2(fma2(D[e], x[e], u[e]), g[e]);
+            u[e] = mul2(u[e], fma2(zs, fma2(s, twice(-1.f), twice(1.f)), s));
             g[e] = mul2(g[e], zs);
           }
-          out(a.grad_z, y);
+          out(a.grad_z, u);
         }
         get_pairs(&sm.dx[w.row(k)][w.col()], s1);
-        get_pairs(&sm.dt[w.row(k)][w.col()], f);
+        get_pairs(&sm.s2[w.row(k)][w.col()], f);
+        get_pairs(&sm.sig[w.row(k)][w.col()], u);
 #pragma unroll
         for (int e = 0; e < VP; ++e) {
           cD[e] = fma2(g[e], x[e], cD[e]);
-          f[e] = mul2(fma2(x[e], s1[e], f[e]), sig[e]);
+          f[e] = mul2(fma2(x[e], s1[e], f[e]), u[e]);
           cb[e] = add2(cb[e], f[e]);
-          g[e] = fma2(dt[e], s1[e], mul2(D[e], g[e]));
         }
         out(a.grad_delta, f);
+        get_pairs(&sm.dt[w.row(k)][w.col()], u);
+#pragma unroll
+        for (int e = 0; e < VP; ++e) g[e] = fma2(u[e], s1[e], mul2(D[e], g[e]));
         out(a.grad_x, g);
       }
 #pragma unroll
@@ -443,6 +544,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps) k_ssm_bwd(Args a) {
     }
     __syncthreads();
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, kColumns);
   // the segment's dA, dD, dbias: [d, N | d | d]
   if (on) {
     float* part = a.part + (long long)seg * a.d * (a.N + 2);

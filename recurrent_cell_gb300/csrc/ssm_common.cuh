@@ -30,6 +30,7 @@ namespace ssm {
 using seqs::Seqs;
 using seqs::Where;
 
+constexpr int kResident = 12;                  // warps of an SM at once
 constexpr int kT = 16;                       // rows of a chunk
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
@@ -318,6 +319,14 @@ constexpr __device__ __forceinline__ int cpair(int p) { return G::CPL > 1 ? p / 
 template <class G>
 constexpr __device__ __forceinline__ int spair(int p) { return G::CPL > 1 ? p % G::NS : p; }
 
+// A read that stays where it is written: the compiler would move one whose value is
+// needed late down to where it is, and its latency with it.
+__device__ __forceinline__ uint4 load_here(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // A chunk's vectors of a [rows, channels] tensor, zeros outside.
 template <class G>
 __device__ __forceinline__ void load_raw(const Tile<G>& w, const void* p, long long ld, long long row0, int n, uint4 (&v)[G::P]) {
@@ -325,7 +334,7 @@ __device__ __forceinline__ void load_raw(const Tile<G>& w, const void* p, long l
 #pragma unroll
   for (int k = 0; k < G::P; ++k) {
     v[k] = make_uint4(0, 0, 0, 0);
-    if (w.row(k) < n && w.col() < w.cols) v[k] = __ldg(reinterpret_cast<const uint4*>(q + (row0 + w.row(k)) * ld));
+    if (w.row(k) < n && w.col() < w.cols) v[k] = load_here(q + (row0 + w.row(k)) * ld);
   }
 }
 template <class E> struct Unpack;
@@ -392,7 +401,7 @@ struct Rows {
     for (int k = 0; k < G::BL; ++k) {
       const int i = k * 32 + w.lane, r = i / G::BV;
       v[k] = make_uint4(0, 0, 0, 0);
-      if (r < n) v[k] = __ldg(reinterpret_cast<const uint4*>(q + (row0 + r) * ld + i % G::BV * G::VN));
+      if (r < n) v[k] = load_here(q + (row0 + r) * ld + i % G::BV * G::VN);
     }
   }
   __device__ __forceinline__ void stage(const Args& a, const Tile<G>& w, const void* p, long long ld, long long row0, int n,
@@ -473,7 +482,7 @@ struct Plan {
   long long S;
   bool cut;
 };
-constexpr long long kPlanWarps = 16ll * kNumSMs, kPlanEnough = 4ll * kNumSMs;
+constexpr long long kPlanWarps = (long long)kResident * kNumSMs, kPlanEnough = 4ll * kNumSMs;
 inline Plan make_plan(long long rows, int n_seq, int d, int groups, int N, bool packed) {
   Plan p{};
   p.NS = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16;
