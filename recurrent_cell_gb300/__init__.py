@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 from .workloads import (  # noqa: F401
     MATH_FP32, MATH_TF32, MATH_BF16, GRAD_SCRATCH, GRAD_GEMM,
@@ -592,8 +593,15 @@ def _spaced(t, name, dtype, shape, tail=1):
     dense) may be parts of wider ones, evenly spaced over the axes before them."""
     width = shape[-1] if tail == 1 else shape[-1] * shape[-2]
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-            return t.data_ptr(), width
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            if t.is_contiguous():
+                return t.data_ptr(), width
+            s = t.stride()
+            if s[-1] == 1 and (tail == 1 or s[-2] == shape[-1]):        # the usual part of a projection
+                if len(shape) == tail + 1:
+                    return t.data_ptr(), s[0] if shape[0] != 1 else width
+                if shape[1] != 1 and (shape[0] == 1 or s[0] == shape[1] * s[1]):
+                    return t.data_ptr(), s[1]
     except AttributeError:
         pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
@@ -760,22 +768,33 @@ def cfc_grad_clip_workspace_bytes(count: int) -> int:
     return int(load_library().cfc_grad_clip_workspace_bytes(count))
 
 
+_grad_kinds = {}
+
+
 def _tensor_list(tensors, name):
     """Host arrays of the pointers, sizes and types of contiguous tensors."""
+    if not _grad_kinds:
+        torch = _torch()
+        _grad_kinds.update({torch.float32: MATH_FP32, torch.bfloat16: MATH_BF16})
+    try:        # many small tensors: a few list comprehensions, and the reasons only where something is wrong
+        if all([t.is_cuda and t.is_contiguous() for t in tensors]):
+            return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]),
+                    array("i", [_grad_kinds[t.dtype] for t in tensors]))
+    except (AttributeError, KeyError):
+        pass
     torch = _torch()
-    n = len(tensors)
-    kinds = {torch.float32: MATH_FP32, torch.bfloat16: MATH_BF16}
-    ptrs, sizes, maths = (ctypes.c_void_p * n)(), (ctypes.c_longlong * n)(), (ctypes.c_int * n)()
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name}[{i}] must be a CUDA tensor")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
-        m = kinds.get(t.dtype)
-        if m is None:
+        if t.dtype not in _grad_kinds:
             raise TypeError(f"{name}[{i}] must be torch.float32 or torch.bfloat16, got {t.dtype}")
-        ptrs[i], sizes[i], maths[i] = t.data_ptr(), t.numel(), m
-    return ptrs, sizes, maths
+    raise TypeError(f"{name} must be a list of CUDA tensors")
+
+
+def _host(a):
+    return a.buffer_info()[0]
 
 
 def cfc_grad_norm(grads, norm, workspace, stream=None):
@@ -783,7 +802,7 @@ def cfc_grad_norm(grads, norm, workspace, stream=None):
     grads = list(grads)
     ptrs, sizes, maths = _tensor_list(grads, "grads")
     torch = _torch()
-    status = load_library().cfc_grad_norm(ptrs, sizes, maths, len(grads), _ptr(norm, "norm", torch.float32, (1,)),
+    status = load_library().cfc_grad_norm(_host(ptrs), _host(sizes), _host(maths), len(grads), _ptr(norm, "norm", torch.float32, (1,)),
                                           _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("cfc_grad_norm", status)
 
@@ -799,13 +818,12 @@ def cfc_grad_clip(grads, max_norm, norm, workspace, out=None, stream=None):
         if len(out) != len(grads):
             raise ValueError("out must have as many tensors as grads")
         outs, osizes, omaths = _tensor_list(out, "out")
-        if osizes[:] != sizes[:] or omaths[:] != maths[:]:
+        if osizes != sizes or omaths != maths:
             raise ValueError("out must have the sizes and types of grads")
-    written = [p for p, n in zip(outs, sizes) if n]
-    if len(set(written)) != len(written):
+    if len(set(outs)) != len(outs) and len(set(p for p, n in zip(outs, sizes) if n)) != len(sizes) - sizes.count(0):
         raise ValueError("a tensor is written twice")
     torch = _torch()
-    status = load_library().cfc_grad_clip(ptrs, outs, sizes, maths, len(grads), max_norm, _ptr(norm, "norm", torch.float32, (1,)),
+    status = load_library().cfc_grad_clip(_host(ptrs), _host(outs), _host(sizes), _host(maths), len(grads), max_norm, _ptr(norm, "norm", torch.float32, (1,)),
                                           _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check("cfc_grad_clip", status)
 

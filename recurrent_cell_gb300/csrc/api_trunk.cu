@@ -276,7 +276,7 @@ int cfc_ssm_step(const void* x, long long x_stride, const void* delta, long long
   int st = ssm_check(channels, groups, n_states, math);
   if (st == CFC_OK) st = check_step(n_seq, tokens, n_slots, slots);
   if (st != CFC_OK) return st;
-  if ((long long)n_seq * (channels / 8 + 1) > 0x7fffffffll) return CFC_ERR_SHAPE;
+  if ((long long)n_seq * (channels / 32 + 1) > 0x7fffffffll) return CFC_ERR_SHAPE;
   if (n_seq == 0 || tokens == 0) return CFC_OK;
   const SsmIn in = ssm_in(x, x_stride, delta, delta_stride, A, B, B_stride, C, C_stride, D, z, z_stride, delta_bias,
                           nullptr, n_seq, (long long)n_seq * tokens, channels, groups, n_states, math, nullptr, nullptr);

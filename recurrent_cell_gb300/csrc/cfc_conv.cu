@@ -8,20 +8,21 @@
 // Before a sequence's first row lie the W - 1 inputs of its state (or zeros); its
 // state afterwards is its last W - 1 inputs.
 //
-// Memory is the bound, W + 10 operations a value or not.  A thread owns 16 bytes
-// of channels (backward: 4 channels, for the registers of grad_w) and walks down a
-// tile of rows with the last W - 1 rows in registers, the next kBatch rows in
-// flight; a tile reads W - 1 rows of its neighbours' again, from cache.  The
-// backward walks its rows once: p_t is formed as soon as row t is there, and
-// grad_x follows W - 1 rows behind.  Its tiles are as long as the GPU has threads
-// for, since each is a row of partial grad_w that reduce_axis0 adds.
-#include "row_ops.cuh"
+// Memory is the bound, if the arithmetic (W + 10 operations a value, the gate's
+// exponential and reciprocal among them) is taken two channels at a time.  A thread owns
+// 16 bytes of channels (backward: 4 channels, for the registers of grad_w) and walks down
+// a tile of rows with the last W - 1 rows in registers and the next kBatch in flight; a
+// tile reads W - 1 rows of its neighbours' again, from cache.  The backward walks its rows
+// once: p_t is formed as soon as row t is there, and grad_x follows W - 1 rows behind.
+// Its tiles are as long as the GPU has threads for, since each is a row of partial grad_w
+// that reduce_axis0 adds.
+#include "pair_math.cuh"
 #include "seq_rows.cuh"
 
 namespace cfc {
 namespace conv {
 
-using rows::Vec;
+using namespace pairs;
 using seqs::Seqs;
 using seqs::Where;
 
@@ -36,78 +37,83 @@ struct Args {
 };
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 8;
-constexpr int kTileFwd = 32;                 // rows of a forward tile
+constexpr int kBatch = 4;
+constexpr int kTileFwd = 64;                 // rows of a forward tile
 
-// pre sigmoid(pre).  bf16: the fast exponential and division, good to 1e-6.
-template <bool EXACT>
-__device__ __forceinline__ float sigmoid(float v) {
-  return EXACT ? 1.f / (1.f + expf(-v)) : __fdividef(1.f, 1.f + __expf(-v));
-}
+// A thread's channels: N of type E, as pairs.
+template <class E_, int N_>
+struct Chan {
+  using E = E_;
+  static constexpr int N = N_, H = N / 2;
+  using P = Pairs<E, N>;
+  using T = typename P::T;
+  __device__ static __forceinline__ void read(F2 (&f)[H], const void* p, long long at) {
+    P::get(f, P::load(static_cast<const E*>(p) + at));
+  }
+  __device__ static __forceinline__ void write(void* p, long long at, const F2 (&f)[H]) {
+    __stcs(reinterpret_cast<T*>(static_cast<E*>(p) + at), P::make(f));
+  }
+  __device__ static __forceinline__ F2 sigmoid(F2 v) { return sizeof(E) == 4 ? sigmoid2_exact(v) : sigmoid2(v); }
+};
 
-template <class V, int W>
-__device__ __forceinline__ void load_weights(const Args& a, int c, float (&w)[W][V::N], float (&b)[V::N]) {
+// The weights [channels, W] of channels c on, as pairs of channels.
+template <class C, int W>
+__device__ __forceinline__ void load_weights(const Args& a, int c, F2 (&w)[W][C::H], F2 (&b)[C::H]) {
+  float f[C::N * W];
 #pragma unroll
-  for (int e = 0; e < V::N; ++e) {
+  for (int i = 0; i < C::N * W; i += 4) {    // (c is a multiple of 4, so c W floats are whole vectors)
+    const float4 v = __ldg(reinterpret_cast<const float4*>(a.w + (long long)c * W + i));
+    f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+  }
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = __ldg(a.w + (long long)(c + e) * W + j);
-    b[e] = a.b ? __ldg(a.b + c + e) : 0.f;
+  for (int e = 0; e < C::H; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][e] = pack(f[2 * e * W + j], f[(2 * e + 1) * W + j]);
+    b[e] = a.b ? pack(__ldg(a.b + c + 2 * e), __ldg(a.b + c + 2 * e + 1)) : 0;
   }
 }
 
-// N channels of a row of x; of row `at` (negative) of a sequence's state.
-template <class V>
-__device__ __forceinline__ typename V::T x_at(const Args& a, long long row, int c) {
-  return __ldg(reinterpret_cast<const typename V::T*>(static_cast<const typename V::E*>(a.x) + row * a.ldx + c));
-}
-template <class V, int W>
-__device__ __forceinline__ void state_at(const Args& a, int seq, int at, int c, float (&f)[V::N]) {
+// Row `at` (negative) of what lies before a sequence.
+template <class C, int W>
+__device__ __forceinline__ void state_at(const Args& a, int seq, int at, int c, F2 (&f)[C::H]) {
 #pragma unroll
-  for (int e = 0; e < V::N; ++e) f[e] = 0.f;
-  if (a.init)
-    V::get(f, __ldg(reinterpret_cast<const typename V::T*>(static_cast<const typename V::E*>(a.init) +
-                                                             ((long long)seq * (W - 1) + at + W - 1) * a.d + c)));
+  for (int e = 0; e < C::H; ++e) f[e] = 0;
+  if (a.init) C::read(f, a.init, ((long long)seq * (W - 1) + at + W - 1) * a.d + c);
 }
 
 // The W - 1 rows before `row`, h[W - 2] being the last.
-template <class V, int W>
-__device__ __forceinline__ void window(const Args& a, const Where& q, long long row, int c, float (&h)[W - 1][V::N]) {
+template <class C, int W>
+__device__ __forceinline__ void window(const Args& a, const Where& q, long long row, int c, F2 (&h)[W - 1][C::H]) {
 #pragma unroll
   for (int j = 1; j < W; ++j) {
-    if (row - j >= q.begin) V::get(h[W - 1 - j], x_at<V>(a, row - j, c));
-    else state_at<V, W>(a, q.i, (int)(row - q.begin) - j, c, h[W - 1 - j]);
+    if (row - j >= q.begin) C::read(h[W - 1 - j], a.x, (row - j) * a.ldx + c);
+    else state_at<C, W>(a, q.i, (int)(row - q.begin) - j, c, h[W - 1 - j]);
   }
 }
 
-template <class V, int W>
-__device__ __forceinline__ void pre_of(const float (&w)[W][V::N], const float (&b)[V::N], const float (&h)[W - 1][V::N],
-                                       const float (&x)[V::N], float (&pre)[V::N]) {
+template <int W, int H>
+__device__ __forceinline__ void pre_of(const F2 (&w)[W][H], const F2 (&b)[H], const F2 (&h)[W - 1][H], const F2 (&x)[H],
+                                       F2 (&pre)[H]) {
 #pragma unroll
-  for (int e = 0; e < V::N; ++e) {
+  for (int e = 0; e < H; ++e) {
     pre[e] = b[e];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) pre[e] = fmaf(w[j][e], h[j][e], pre[e]);
-    pre[e] = fmaf(w[W - 1][e], x[e], pre[e]);
+    for (int j = 0; j < W - 1; ++j) pre[e] = fma2(w[j][e], h[j][e], pre[e]);
+    pre[e] = fma2(w[W - 1][e], x[e], pre[e]);
   }
 }
-template <int W, int N>
-__device__ __forceinline__ void shift(float (&h)[W][N], const float (&x)[N]) {
+template <int W, int H>
+__device__ __forceinline__ void shift(F2 (&h)[W][H], const F2 (&x)[H]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
+  for (int e = 0; e < H; ++e) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) h[j][e] = h[j + 1][e];
     h[W - 1][e] = x[e];
   }
 }
-template <class V>
-__device__ __forceinline__ void activate(int silu, float (&v)[V::N]) {
-  if (silu)
-#pragma unroll
-    for (int e = 0; e < V::N; ++e) v[e] *= sigmoid<sizeof(typename V::E) == 4>(v[e]);
-}
 
 // The last W - 1 inputs of sequence seq, from its rows or the state before them.
-template <class V, int W>
+template <class C, int W>
 __device__ __forceinline__ void final_rows(const Args& a, int seq, int c) {
   long long begin, end;
   seqs::range_of(a.s, seq, &begin, &end);
@@ -115,208 +121,226 @@ __device__ __forceinline__ void final_rows(const Args& a, int seq, int c) {
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) {
     const long long at = len - (W - 1) + i;
-    float f[V::N];
-    if (at >= 0) V::get(f, x_at<V>(a, begin + at, c));
-    else state_at<V, W>(a, seq, (int)at, c, f);
-    *reinterpret_cast<typename V::T*>(static_cast<typename V::E*>(a.final_state) +
-                                      ((long long)seq * (W - 1) + i) * a.d + c) = V::make(f);
+    F2 f[C::H];
+    if (at >= 0) C::read(f, a.x, (begin + at) * a.ldx + c);
+    else state_at<C, W>(a, seq, (int)at, c, f);
+    C::write(a.final_state, ((long long)seq * (W - 1) + i) * a.d + c, f);
   }
 }
 
-template <class V, int W>
+template <class C, int W>
 __global__ void __launch_bounds__(kThreads) k_conv(Args a) {
-  constexpr int N = V::N;
-  const int nvec = a.d / N;
+  using P = typename C::P;
+  constexpr int H = C::H;
+  const int nvec = a.d / C::N;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const long long tile = id / nvec;
-  const int c = (int)(id % nvec) * N;
+  const int c = (int)(id % nvec) * C::N;
   if (tile >= a.n_tiles) {                   // behind the tiles: the states
     const long long seq = tile - a.n_tiles;
-    if (a.final_state && seq < a.s.n) final_rows<V, W>(a, (int)seq, c);
+    if (a.final_state && seq < a.s.n) final_rows<C, W>(a, (int)seq, c);
     return;
   }
-  float w[W][N], b[N], h[W - 1][N];
-  load_weights<V, W>(a, c, w, b);
-  const long long r0 = tile * a.tile;
-  const int n = a.s.rows - r0 < a.tile ? (int)(a.s.rows - r0) : a.tile;
+  const long long r0 = tile * a.tile, r1 = a.s.rows - r0 < a.tile ? a.s.rows : r0 + a.tile;
+  typename C::T in[kBatch], next[kBatch];
+  auto fetch = [&](long long row) {
+    const typename C::E* p = static_cast<const typename C::E*>(a.x) + row * a.ldx + c;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) next[i] = P::load(p + i * a.ldx, row + i < r1);
+  };
+  fetch(r0);
+  F2 w[W][H], b[H], h[W - 1][H];
+  load_weights<C, W>(a, c, w, b);
   Where q = seqs::find(a.s, r0);
-  window<V, W>(a, q, r0, c, h);
-  typename V::E* y = static_cast<typename V::E*>(a.y) + r0 * a.d + c;
-  for (int i0 = 0; i0 < n; i0 += kBatch) {
-    typename V::T in[kBatch];
+  window<C, W>(a, q, r0, c, h);
+  for (long long row = r0; row < r1; row += kBatch) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < n) in[i] = x_at<V>(a, r0 + i0 + i, c);
+    for (int i = 0; i < kBatch; ++i) in[i] = next[i];
+    fetch(row + kBatch);
+    const bool one = row + kBatch <= q.end;  // no sequence begins within the batch
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < n) {
-        const long long row = r0 + i0 + i;
-        if (row >= q.end) {                  // the next sequence's first row
-          q = seqs::find(a.s, row);
-          window<V, W>(a, q, row, c, h);
+    for (int i = 0; i < kBatch; ++i) {
+      if (row + i < r1) {
+        if (!one && row + i >= q.end) {      // the next sequence's first row
+          q = seqs::find(a.s, row + i);
+          window<C, W>(a, q, row + i, c, h);
         }
-        float x[N], pre[N];
-        V::get(x, in[i]);
-        pre_of<V, W>(w, b, h, x, pre);
-        shift<W - 1, N>(h, x);
-        activate<V>(a.silu, pre);
-        __stcs(reinterpret_cast<typename V::T*>(y + (long long)(i0 + i) * a.d), V::make(pre));
-      }
-  }
-}
-
-// p_t from pre_t and grad_y_t.
-template <class V>
-__device__ __forceinline__ void p_of(int silu, const float (&pre)[V::N], const float (&gy)[V::N], float (&p)[V::N]) {
+        F2 x[H], pre[H];
+        P::get(x, in[i]);
+        pre_of<W, H>(w, b, h, x, pre);
+        shift<W - 1, H>(h, x);
+        if (a.silu)
 #pragma unroll
-  for (int e = 0; e < V::N; ++e) {
-    p[e] = gy[e];
-    if (silu) {
-      const float s = sigmoid<sizeof(typename V::E) == 4>(pre[e]);
-      p[e] *= s * fmaf(pre[e], 1.f - s, 1.f);
+          for (int e = 0; e < H; ++e) pre[e] = mul2(pre[e], C::sigmoid(pre[e]));
+        C::write(a.y, (row + i) * a.d + c, pre);
+      }
     }
   }
 }
-template <class V>
-__device__ __forceinline__ typename V::T gy_at(const Args& a, long long row, int c) {
-  return __ldg(reinterpret_cast<const typename V::T*>(static_cast<const typename V::E*>(a.grad_y) + row * a.d + c));
+
+// p_t from pre_t and grad_y_t: act' = s (1 + pre (1 - s)) = s + pre s (1 - s).
+template <class C>
+__device__ __forceinline__ void p_of(int silu, const F2 (&pre)[C::H], const F2 (&gy)[C::H], F2 (&p)[C::H]) {
+#pragma unroll
+  for (int e = 0; e < C::H; ++e) {
+    p[e] = gy[e];
+    if (silu) {
+      const F2 s = C::sigmoid(pre[e]);
+      p[e] = mul2(p[e], fma2(mul2(pre[e], s), fma2(s, twice(-1.f), twice(1.f)), s));
+    }
+  }
 }
 // Adds to g the gradient that the state after sequence seq sends to its input of place `at`.
-template <class V, int W>
-__device__ __forceinline__ void add_final(const Args& a, int seq, long long at, long long len, int c, float (&g)[V::N]) {
+template <class C, int W>
+__device__ __forceinline__ void add_final(const Args& a, int seq, long long at, long long len, int c, F2 (&g)[C::H]) {
   const long long i = at - (len - (W - 1));
   if (!a.grad_final || i < 0) return;
-  float f[V::N];
-  V::get(f, __ldg(reinterpret_cast<const typename V::T*>(static_cast<const typename V::E*>(a.grad_final) +
-                                                           ((long long)seq * (W - 1) + i) * a.d + c)));
+  F2 f[C::H];
+  C::read(f, a.grad_final, ((long long)seq * (W - 1) + i) * a.d + c);
 #pragma unroll
-  for (int e = 0; e < V::N; ++e) g[e] += f[e];
+  for (int e = 0; e < C::H; ++e) g[e] = add2(g[e], f[e]);
 }
 
 // The gradient of the state before sequence seq: of its inputs of places -(W-1) .. -1.
-template <class V, int W>
+template <class C, int W>
 __device__ __forceinline__ void init_rows(const Args& a, int seq, int c) {
-  constexpr int N = V::N;
-  float w[W][N], b[N], h[W - 1][N], p[W - 1][N];
-  load_weights<V, W>(a, c, w, b);
-  Where q;
-  q.i = seq;
-  seqs::range_of(a.s, seq, &q.begin, &q.end);
-  const long long len = q.end - q.begin;
+  constexpr int H = C::H;
+  F2 w[W][H], b[H], h[W - 1][H], p[W - 1][H];
+  load_weights<C, W>(a, c, w, b);
+  long long begin, end;
+  seqs::range_of(a.s, seq, &begin, &end);
+  const long long len = end - begin;
 #pragma unroll
-  for (int j = 1; j < W; ++j) state_at<V, W>(a, seq, -j, c, h[W - 1 - j]);
+  for (int j = 1; j < W; ++j) state_at<C, W>(a, seq, -j, c, h[W - 1 - j]);
 #pragma unroll
   for (int t = 0; t < W - 1; ++t) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) p[t][e] = 0.f;
+    for (int e = 0; e < H; ++e) p[t][e] = 0;
     if (t < len) {
-      float x[N], pre[N], gy[N];
-      V::get(x, x_at<V>(a, q.begin + t, c));
-      V::get(gy, gy_at<V>(a, q.begin + t, c));
-      pre_of<V, W>(w, b, h, x, pre);
-      shift<W - 1, N>(h, x);
-      p_of<V>(a.silu, pre, gy, p[t]);
+      F2 x[H], pre[H], gy[H];
+      C::read(x, a.x, (begin + t) * a.ldx + c);
+      C::read(gy, a.grad_y, (begin + t) * a.d + c);
+      pre_of<W, H>(w, b, h, x, pre);
+      shift<W - 1, H>(h, x);
+      p_of<C>(a.silu, pre, gy, p[t]);
     }
   }
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) {
-    float g[N] = {};
+    F2 g[H] = {};
 #pragma unroll
     for (int k = 0; k <= i; ++k)
 #pragma unroll
-      for (int e = 0; e < N; ++e) g[e] = fmaf(w[k][e], p[i - k][e], g[e]);
-    add_final<V, W>(a, seq, i - (W - 1), len, c, g);
-    *reinterpret_cast<typename V::T*>(static_cast<typename V::E*>(a.grad_init) +
-                                      ((long long)seq * (W - 1) + i) * a.d + c) = V::make(g);
+      for (int e = 0; e < H; ++e) g[e] = fma2(w[k][e], p[i - k][e], g[e]);
+    add_final<C, W>(a, seq, i - (W - 1), len, c, g);
+    C::write(a.grad_init, ((long long)seq * (W - 1) + i) * a.d + c, g);
   }
 }
 
-template <class V, int W>
+template <class C, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_bwd(Args a) {
-  constexpr int N = V::N;
-  const int nvec = a.d / N;
+  using P = typename C::P;
+  constexpr int H = C::H;
+  const int nvec = a.d / C::N;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const long long tile = id / nvec;
-  const int c = (int)(id % nvec) * N;
+  const int c = (int)(id % nvec) * C::N;
   if (tile >= a.n_tiles) {
     const long long seq = tile - a.n_tiles;
-    if (a.grad_init && seq < a.s.n) init_rows<V, W>(a, (int)seq, c);
+    if (a.grad_init && seq < a.s.n) init_rows<C, W>(a, (int)seq, c);
     return;
   }
-  float w[W][N], b[N], h[W - 1][N], p[W][N] = {}, gw[W][N] = {}, gb[N] = {};
-  load_weights<V, W>(a, c, w, b);
-  const long long r0 = tile * a.tile;
-  const long long r1 = a.s.rows - r0 < a.tile ? a.s.rows : r0 + a.tile;
+  const long long r0 = tile * a.tile, r1 = a.s.rows - r0 < a.tile ? a.s.rows : r0 + a.tile;
+  typename C::T in[kBatch], gin[kBatch], next[kBatch], gnext[kBatch];
+  auto fetch = [&](long long row) {
+    const typename C::E* p = static_cast<const typename C::E*>(a.x) + row * a.ldx + c;
+    const typename C::E* g = static_cast<const typename C::E*>(a.grad_y) + row * a.d + c;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      next[i] = P::load(p + i * a.ldx, row + i < r1);
+      gnext[i] = P::load(g + i * (long long)a.d, row + i < r1);
+    }
+  };
+  fetch(r0);
+  F2 w[W][H], b[H], h[W - 1][H], p[W][H] = {}, gw[W][H] = {}, gb[H] = {};
+  load_weights<C, W>(a, c, w, b);
   Where q = seqs::find(a.s, r0);
-  window<V, W>(a, q, r0, c, h);
+  window<C, W>(a, q, r0, c, h);
   // p moved on by one row, and grad_x of the row that then has all of its W
-  auto emit = [&](long long row, const float (&now)[N]) {
-    shift<W, N>(p, now);
+  auto emit = [&](long long row, const F2 (&now)[H]) {
+    shift<W, H>(p, now);
     const long long at = row - (W - 1);
     if (at < r0 || at < q.begin) return;
-    float g[N] = {};
+    F2 g[H] = {};
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int e = 0; e < N; ++e) g[e] = fmaf(w[j][e], p[W - 1 - j][e], g[e]);
-    add_final<V, W>(a, q.i, at - q.begin, q.end - q.begin, c, g);
-    __stcs(reinterpret_cast<typename V::T*>(static_cast<typename V::E*>(a.grad_x) + at * a.d + c), V::make(g));
+      for (int e = 0; e < H; ++e) g[e] = fma2(w[j][e], p[W - 1 - j][e], g[e]);
+    add_final<C, W>(a, q.i, at - q.begin, q.end - q.begin, c, g);
+    C::write(a.grad_x, at * a.d + c, g);
   };
-  const float none[N] = {};
-  for (long long i0 = r0; i0 < r1; i0 += kBatch) {
-    typename V::T in[kBatch], gin[kBatch];
+  const F2 none[H] = {};
+  for (long long row = r0; row < r1; row += kBatch) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < r1) {
-        in[i] = x_at<V>(a, i0 + i, c);
-        gin[i] = gy_at<V>(a, i0 + i, c);
-      }
+    for (int i = 0; i < kBatch; ++i) {
+      in[i] = next[i];
+      gin[i] = gnext[i];
+    }
+    fetch(row + kBatch);
+    const bool one = row + kBatch <= q.end;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (i0 + i < r1) {
-        const long long row = i0 + i;
-        if (row >= q.end) {                  // the last rows of the one before, then the next sequence
+    for (int i = 0; i < kBatch; ++i) {
+      if (row + i < r1) {
+        if (!one && row + i >= q.end) {      // the last rows of the one before, then the next sequence
 #pragma unroll 1
-          for (int k = 0; k < W - 1; ++k) emit(row + k, none);
-          q = seqs::find(a.s, row);
-          window<V, W>(a, q, row, c, h);
+          for (int k = 0; k < W - 1; ++k) emit(row + i + k, none);
+          q = seqs::find(a.s, row + i);
+          window<C, W>(a, q, row + i, c, h);
         }
-        float x[N], gy[N], pre[N], now[N];
-        V::get(x, in[i]);
-        V::get(gy, gin[i]);
-        pre_of<V, W>(w, b, h, x, pre);
-        p_of<V>(a.silu, pre, gy, now);
+        F2 x[H], gy[H], pre[H], now[H];
+        P::get(x, in[i]);
+        P::get(gy, gin[i]);
+        pre_of<W, H>(w, b, h, x, pre);
+        p_of<C>(a.silu, pre, gy, now);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
+        for (int e = 0; e < H; ++e) {
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) gw[j][e] = fmaf(now[e], h[j][e], gw[j][e]);
-          gw[W - 1][e] = fmaf(now[e], x[e], gw[W - 1][e]);
-          gb[e] += now[e];
+          for (int j = 0; j < W - 1; ++j) gw[j][e] = fma2(now[e], h[j][e], gw[j][e]);
+          gw[W - 1][e] = fma2(now[e], x[e], gw[W - 1][e]);
+          gb[e] = add2(gb[e], now[e]);
         }
-        shift<W - 1, N>(h, x);
-        emit(row, now);
+        shift<W - 1, H>(h, x);
+        emit(row + i, now);
       }
+    }
   }
   // rows of the next tile, as far as they reach back into this one
 #pragma unroll 1
   for (long long row = r1; row < r1 + W - 1; ++row) {
-    float now[N] = {};
+    F2 now[H] = {};
     if (row < q.end) {
-      float x[N], gy[N], pre[N];
-      V::get(x, x_at<V>(a, row, c));
-      V::get(gy, gy_at<V>(a, row, c));
-      pre_of<V, W>(w, b, h, x, pre);
-      p_of<V>(a.silu, pre, gy, now);
-      shift<W - 1, N>(h, x);
+      F2 x[H], gy[H], pre[H];
+      C::read(x, a.x, row * a.ldx + c);
+      C::read(gy, a.grad_y, row * a.d + c);
+      pre_of<W, H>(w, b, h, x, pre);
+      p_of<C>(a.silu, pre, gy, now);
+      shift<W - 1, H>(h, x);
     }
     emit(row, now);
   }
   float* part = a.part + tile * ((W + 1ll) * a.d);          // [grad_w | grad_b]
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
+  for (int e = 0; e < H; ++e) {
+    float f[2];
 #pragma unroll
-    for (int j = 0; j < W; ++j) part[(long long)(c + e) * W + j] = gw[j][e];
-    part[(long long)W * a.d + c + e] = gb[e];
+    for (int j = 0; j < W; ++j) {
+      split(gw[j][e], f[0], f[1]);
+      part[(long long)(c + 2 * e) * W + j] = f[0];
+      part[(long long)(c + 2 * e + 1) * W + j] = f[1];
+    }
+    split(gb[e], f[0], f[1]);
+    part[(long long)W * a.d + c + 2 * e] = f[0];
+    part[(long long)W * a.d + c + 2 * e + 1] = f[1];
   }
 }
 
@@ -329,40 +353,42 @@ struct StepArgs {
   int tokens;
 };
 
-template <class V, int W>
+template <class C, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_step(StepArgs g) {
-  constexpr int N = V::N;
-  using E = typename V::E;
-  using T = typename V::T;
+  constexpr int H = C::H;
   const Args& a = g.a;
-  const int nvec = a.d / N;
+  const int nvec = a.d / C::N;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const long long seq = id / nvec;
-  const int c = (int)(id % nvec) * N;
+  const int c = (int)(id % nvec) * C::N;
   if (seq >= a.s.n) return;
-  const long long slot = g.slots ? g.slots[seq] : seq;
-  const bool on = slot >= 0 && slot < g.n_slots;
-  float w[W][N], b[N], h[W - 1][N] = {};
-  E* state = static_cast<E*>(g.state) + (on ? slot : 0) * (W - 1) * a.d + c;
-  if (on) {
-    load_weights<V, W>(a, c, w, b);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) V::get(h[j], *reinterpret_cast<const T*>(state + (long long)j * a.d));
+  const long long slot = g.slots ? g.slots[seq] : seq, row0 = seq * g.tokens;
+  if (slot < 0 || slot >= g.n_slots) {       // a sequence without a state: zeros out, nothing kept
+    const F2 none[H] = {};
+    for (int t = 0; t < g.tokens; ++t) C::write(a.y, (row0 + t) * a.d + c, none);
+    return;
   }
+  const long long at = slot * (W - 1) * a.d + c;
+  F2 w[W][H], b[H], h[W - 1][H], x[H], pre[H];
+  typename C::T s[W - 1];                    // (the state is written below: plain reads)
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+    s[j] = *reinterpret_cast<const typename C::T*>(static_cast<const typename C::E*>(g.state) + at + (long long)j * a.d);
+  C::read(x, a.x, row0 * a.ldx + c);
+  load_weights<C, W>(a, c, w, b);
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) C::P::get(h[j], s[j]);
   for (int t = 0; t < g.tokens; ++t) {
-    const long long row = seq * g.tokens + t;
-    float x[N], pre[N] = {};
-    if (on) {
-      V::get(x, x_at<V>(a, row, c));
-      pre_of<V, W>(w, b, h, x, pre);
-      shift<W - 1, N>(h, x);
-      activate<V>(a.silu, pre);
-    }
-    *reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d + c) = V::make(pre);
-  }
-  if (on)
+    if (t > 0) C::read(x, a.x, (row0 + t) * a.ldx + c);
+    pre_of<W, H>(w, b, h, x, pre);
+    shift<W - 1, H>(h, x);
+    if (a.silu)
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<T*>(state + (long long)j * a.d) = V::make(h[j]);
+      for (int e = 0; e < H; ++e) pre[e] = mul2(pre[e], C::sigmoid(pre[e]));
+    C::write(a.y, (row0 + t) * a.d + c, pre);
+  }
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) C::write(g.state, at + (long long)j * a.d, h[j]);
 }
 
 template <class F>
@@ -381,31 +407,31 @@ static cudaError_t by_width(int w, F f) {
 
 static unsigned blocks_of(long long threads) { return (unsigned)((threads + kThreads - 1) / kThreads); }
 
-template <class V> struct Forward {
+template <class C> struct Forward {
   Args& a; cudaStream_t st;
   template <int W> cudaError_t operator()() {
     const long long items = a.n_tiles + (a.final_state ? a.s.n : 0);
     if (items == 0) return cudaSuccess;
     TraceScope tr("k_conv", st);
-    k_conv<V, W><<<blocks_of(items * (a.d / V::N)), kThreads, 0, st>>>(a);
+    k_conv<C, W><<<blocks_of(items * (a.d / C::N)), kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
 };
-template <class V> struct Backward {
+template <class C> struct Backward {
   Args& a; cudaStream_t st;
   template <int W> cudaError_t operator()() {
     const long long items = a.n_tiles + (a.grad_init ? a.s.n : 0);
     if (items == 0) return cudaSuccess;
     TraceScope tr("k_conv_bwd", st);
-    k_conv_bwd<V, W><<<blocks_of(items * (a.d / V::N)), kThreads, 0, st>>>(a);
+    k_conv_bwd<C, W><<<blocks_of(items * (a.d / C::N)), kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
 };
-template <class V> struct Step {
+template <class C> struct Step {
   StepArgs& g; cudaStream_t st;
   template <int W> cudaError_t operator()() {
     TraceScope tr("k_conv_step", st);
-    k_conv_step<V, W><<<blocks_of((long long)g.a.s.n * (g.a.d / V::N)), kThreads, 0, st>>>(g);
+    k_conv_step<C, W><<<blocks_of((long long)g.a.s.n * (g.a.d / C::N)), kThreads, 0, st>>>(g);
     return cudaGetLastError();
   }
 };
@@ -438,8 +464,8 @@ cudaError_t launch_conv_forward(const ConvArgs& g, void* y, void* final_state, c
   a.final_state = final_state;
   a.tile = conv::kTileFwd;
   a.n_tiles = (int)((g.rows + a.tile - 1) / a.tile);
-  return g.math == CFC_MATH_BF16 ? conv::by_width(g.width, conv::Forward<rows::Vec<__nv_bfloat16, 8>>{a, st})
-                                 : conv::by_width(g.width, conv::Forward<rows::Vec<float, 4>>{a, st});
+  return g.math == CFC_MATH_BF16 ? conv::by_width(g.width, conv::Forward<conv::Chan<__nv_bfloat16, 8>>{a, st})
+                                 : conv::by_width(g.width, conv::Forward<conv::Chan<float, 4>>{a, st});
 }
 
 cudaError_t launch_conv_backward(const ConvArgs& g, const void* grad_y, const void* grad_final, void* grad_x, float* grad_w,
@@ -453,8 +479,8 @@ cudaError_t launch_conv_backward(const ConvArgs& g, const void* grad_y, const vo
   a.tile = conv::bwd_tile(g.rows, g.d);
   a.n_tiles = (int)((g.rows + a.tile - 1) / a.tile);
   const cudaError_t e = g.math == CFC_MATH_BF16
-                            ? conv::by_width(g.width, conv::Backward<rows::Vec<__nv_bfloat16, 4>>{a, st})
-                            : conv::by_width(g.width, conv::Backward<rows::Vec<float, 4>>{a, st});
+                            ? conv::by_width(g.width, conv::Backward<conv::Chan<__nv_bfloat16, 4>>{a, st})
+                            : conv::by_width(g.width, conv::Backward<conv::Chan<float, 4>>{a, st});
   if (e != cudaSuccess) return e;
   ReduceOut o{};
   o.nseg = grad_b ? 2 : 1;
@@ -473,8 +499,8 @@ cudaError_t launch_conv_step(const ConvArgs& g, int tokens, void* state, long lo
   s.n_slots = n_slots;
   s.slots = slots;
   s.tokens = tokens;
-  return g.math == CFC_MATH_BF16 ? conv::by_width(g.width, conv::Step<rows::Vec<__nv_bfloat16, 8>>{s, st})
-                                 : conv::by_width(g.width, conv::Step<rows::Vec<float, 4>>{s, st});
+  return g.math == CFC_MATH_BF16 ? conv::by_width(g.width, conv::Step<conv::Chan<__nv_bfloat16, 8>>{s, st})
+                                 : conv::by_width(g.width, conv::Step<conv::Chan<float, 4>>{s, st});
 }
 
 }  // namespace cfc

@@ -65,6 +65,7 @@ __device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, 
 template <class G, bool LOCAL>
 __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
   using E = typename G::E;
+  using U = Pairs<E, G::VN>;
   constexpr int P = G::P, VN = G::VN, VP = VN / 2;
   __shared__ FwdTiles<G, LOCAL> sm;
   const Tile<G> w(a, blockIdx.x);
@@ -124,8 +125,8 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       F2 x[VP], dt[VP];
-      Unpack<E>::pairs(x, xv[k]);
-      Unpack<E>::pairs(dt, dv[k]);
+      U::get(x, xv[k]);
+      U::get(dt, dv[k]);
 #pragma unroll
       for (int e = 0; e < VP; ++e) {
         dt[e] = softplus2(add2(dt[e], bias[e]));
@@ -185,12 +186,12 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
             }
           }
           if (a.z) {
-            Unpack<E>::pairs(z, zv[k]);
+            U::get(z, zv[k]);
 #pragma unroll
             for (int e = 0; e < VP; ++e) y[k][e] = mul2(y[k][e], mul2(z[e], sigmoid2(z[e])));
           }
           E* to = static_cast<E*>(a.y) + (row + w.row(k)) * a.d + w.c0 + w.col();
-          __stcs(reinterpret_cast<uint4*>(to), Unpack<E>::make(y[k]));
+          __stcs(reinterpret_cast<uint4*>(to), U::make(y[k]));
         }
     }
   }

@@ -30,8 +30,8 @@ constexpr int kBwdWarps = 4;
 template <class G>
 struct __align__(16) BwdTiles {
   float dt[kT][G::CW], sig[kT][G::CW];                       // dt and its slope sigmoid(delta + bias)
-  float dx[kT][G::CW], g[kT][G::CW];                         // dt x and g, then sum dh B and C . h
-  float s2[kT][G::CW];                                       // sum e A
+  float dx[kT][G::CW], g[kT][G::CW];                         // dt x, g
+  float s1[kT][G::CW], s2[kT][G::CW], y[kT][G::CW];          // sum dh B, sum e A, C . h
   float B[kT][G::NP], C[kT][G::NP];
   float bc[kT][2 * G::NP];                                   // dB, dC of the tile
   F2 gA[G::PAIRS][32];                                       // dA of the chunks so far
@@ -55,22 +55,32 @@ __device__ __forceinline__ void tmem_put(uint32_t at, const F2 (&h)[N]) {
   if constexpr (N == 8)
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
   else
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 template <int N>
 __device__ __forceinline__ void tmem_get(uint32_t at, F2 (&h)[N]) {
-  float f[2 * N];
-  if constexpr (N == 8) tc::tmem_ld16(at, f);
-  else tc::tmem_ld8(at, f);
+  // (no memory clobber: it takes part in nothing but tensor memory, and volatile statements keep their order)
+  uint32_t r[2 * N];
+  if constexpr (N == 8)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(at));
 #pragma unroll
-  for (int p = 0; p < N; ++p) h[p] = pack(f[2 * p], f[2 * p + 1]);
+  for (int p = 0; p < N; ++p) h[p] = pack(__uint_as_float(r[2 * p]), __uint_as_float(r[2 * p + 1]));
 }
-__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;"); }
 
 // 16 bytes of global memory (or zeros) to shared memory, asynchronously.
 __device__ __forceinline__ void copy16(void* to, const void* from, bool on) {
@@ -138,7 +148,7 @@ __device__ __forceinline__ void over_channels(float (&v)[N], int lane) {
 template <class G>
 __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const F2 (&bias)[G::VN / 2],
                                              float (*dt)[G::CW], float (*dx)[G::CW], float (*g)[G::CW]) {
-  using U = Unpack<typename G::E>;
+  using U = Pairs<typename G::E, G::VN>;
   constexpr int VP = G::VN / 2;
   uint4 xv[G::P], dv[G::P], zv[G::P], gv[G::P];
   if (dx) load_raw<G>(w, a.x, a.ldx, row, n, xv);
@@ -148,12 +158,12 @@ __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, lo
 #pragma unroll
   for (int k = 0; k < G::P; ++k) {
     F2 f[VP], t[VP], u[VP];
-    U::pairs(t, dv[k]);
+    U::get(t, dv[k]);
 #pragma unroll
     for (int e = 0; e < VP; ++e) t[e] = softplus2(add2(t[e], bias[e]));
-    U::pairs(f, gv[k]);
+    U::get(f, gv[k]);
     if (a.z) {
-      U::pairs(u, zv[k]);
+      U::get(u, zv[k]);
 #pragma unroll
       for (int e = 0; e < VP; ++e) f[e] = mul2(f[e], mul2(u[e], sigmoid2(u[e])));
     }
@@ -162,7 +172,7 @@ __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, lo
       put_pairs(&g[w.row(k)][w.col()], f);
     }
     if (dx) {
-      U::pairs(u, xv[k]);
+      U::get(u, xv[k]);
 #pragma unroll
       for (int e = 0; e < VP; ++e) u[e] = mul2(u[e], t[e]);
       if (w.row(k) < kT) put_pairs(&dx[w.row(k)][w.col()], u);
@@ -220,13 +230,17 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
 }
 
 // What a token reads of the tiles.
-template <class G>
+template <class G, bool BACK>
 struct Token {
-  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS];
+  F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS], g[G::CPAIRS], c[G::SPAIRS];
   __device__ __forceinline__ void read(const BwdTiles<G>& sm, const Tile<G>& w, int t) {
     get_channels<G>(sm.dt[t], w.cl, dt);
     get_channels<G>(sm.dx[t], w.cl, dx);
     get_states<G>(sm.B[t], w.sl, b);
+    if constexpr (BACK) {
+      get_channels<G>(sm.g[t], w.cl, g);
+      get_states<G>(sm.C[t], w.sl, c);
+    }
   }
   __device__ __forceinline__ void forward(const F2 (&A2)[G::PAIRS], F2 (&h)[G::PAIRS]) const {
 #pragma unroll
@@ -238,26 +252,23 @@ struct Token {
 // Token t backward, h being the state before it: the token's sums into the tiles, dh on to the
 // token before it.
 template <class G>
-__device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int t, const F2 (&h)[G::PAIRS],
-                                          const F2 (&A2)[G::PAIRS], F2 (&dh)[G::PAIRS], F2 (&gA)[G::PAIRS]) {
+__device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int t, const Token<G, true>& k,
+                                          const F2 (&h)[G::PAIRS], const F2 (&A2)[G::PAIRS], F2 (&dh)[G::PAIRS],
+                                          F2 (&gA)[G::PAIRS]) {
   constexpr int CPL = G::CPL, NS = G::NS, NP = G::NP;
-  Token<G> k;
-  k.read(sm, w, t);
-  F2 g[G::CPAIRS], c[G::SPAIRS], s1[G::CPAIRS], s2[G::CPAIRS], y[G::CPAIRS], db[G::SPAIRS], dc[G::SPAIRS];
-  get_channels<G>(sm.g[t], w.cl, g);
-  get_states<G>(sm.C[t], w.sl, c);
+  F2 s1[G::CPAIRS], s2[G::CPAIRS], y[G::CPAIRS], db[G::SPAIRS], dc[G::SPAIRS];
 #pragma unroll
   for (int p = 0; p < G::PAIRS; ++p) {
     const int i = cpair<G>(p), j = spair<G>(p);
     const bool first_i = G::CPL > 1 ? j == 0 : p == 0, first_j = G::CPL > 1 ? i == 0 : true;
     const F2 e = ex2_2(mul2(k.dt[i], A2[p]));
-    const F2 ah = mul2(e, h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(c[j], g[i], dh[p]), q = mul2(d, ah);
-    y[i] = first_i ? mul2(c[j], now) : fma2(c[j], now, y[i]);
+    const F2 ah = mul2(e, h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(k.c[j], k.g[i], dh[p]), q = mul2(d, ah);
+    y[i] = first_i ? mul2(k.c[j], now) : fma2(k.c[j], now, y[i]);
     s1[i] = first_i ? mul2(d, k.b[j]) : fma2(d, k.b[j], s1[i]);
     s2[i] = first_i ? mul2(q, A2[p]) : fma2(q, A2[p], s2[i]);
     gA[p] = fma2(q, k.dt[i], gA[p]);
     db[j] = first_j ? mul2(d, k.dx[i]) : fma2(d, k.dx[i], db[j]);
-    dc[j] = first_j ? mul2(g[i], now) : fma2(g[i], now, dc[j]);
+    dc[j] = first_j ? mul2(k.g[i], now) : fma2(k.g[i], now, dc[j]);
     dh[p] = mul2(e, d);
   }
   float f1[CPL], f2[CPL], f3[CPL], bc[2 * NS];
@@ -285,12 +296,10 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
   }
   const float o1 = over_states<CPL>(f1, w.lane), o2 = over_states<CPL>(f2, w.lane), o3 = over_states<CPL>(f3, w.lane);
   over_channels<2 * NS>(bc, w.lane);
-  // (the token's own values have been read by all lanes: the sums above took every lane)
-  __syncwarp();
   if (w.sl < CPL) {
-    sm.dx[t][w.cl * CPL + w.sl] = o1;
+    sm.s1[t][w.cl * CPL + w.sl] = o1;
     sm.s2[t][w.cl * CPL + w.sl] = o2 * kLn2;
-    sm.g[t][w.cl * CPL + w.sl] = o3;
+    sm.y[t][w.cl * CPL + w.sl] = o3;
   }
   if constexpr (NS == 2) {
     if (w.cl < 4) sm.bc[t][(w.cl >> 1) * NP + w.sl * NS + (w.cl & 1)] = bc[0];
@@ -306,7 +315,7 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
 template <class G>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
   using E = typename G::E;
-  using U = Unpack<E>;
+  using U = Pairs<E, G::VN>;
   constexpr int VN = G::VN, VP = VN / 2, NP = G::NP, PAIRS = G::PAIRS, P = G::P;
   constexpr uint32_t kColumns = 2 * PAIRS * kT;              // of tensor memory
   extern __shared__ __align__(16) unsigned char raw[];
@@ -397,11 +406,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       F2 x[VP], dt[VP], sig[VP], z[VP], g[VP];
-      U::pairs(x, sm.raw[0][k][w.lane]);
-      U::pairs(dt, sm.raw[1][k][w.lane]);
-      U::pairs(g, sm.raw[3][k][w.lane]);
+      U::get(x, sm.raw[0][k][w.lane]);
+      U::get(dt, sm.raw[1][k][w.lane]);
+      U::get(g, sm.raw[3][k][w.lane]);
       if (a.z) {
-        U::pairs(z, sm.raw[2][k][w.lane]);
+        U::get(z, sm.raw[2][k][w.lane]);
 #pragma unroll
         for (int e = 0; e < VP; ++e) g[e] = mul2(g[e], mul2(z[e], sigmoid2(z[e])));
       }
@@ -441,20 +450,27 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) gA[p] = 0;
     if (q.begin < row && n == kT) {            // inside one sequence
-#pragma unroll 4
-      for (int t = 0; t < kT; ++t) {
-        tmem_put(states + t * 2 * PAIRS, h);
-        if (t + 1 < kT) {
-          Token<G> k;
-          k.read(sm, w, t);
+      {
+        Token<G, false> k, ahead;
+        k.read(sm, w, 0);
+#pragma unroll 5
+        for (int t = 0; t < kT - 1; ++t) {
+          ahead.read(sm, w, t + 1);
+          tmem_put(states + t * 2 * PAIRS, h);
           k.forward(A2, h);
+          k = ahead;
         }
+        tmem_put(states + (kT - 1) * 2 * PAIRS, h);
+        tmem_put_wait();
       }
-      tmem_put_wait();
+      Token<G, true> k, ahead;
+      k.read(sm, w, kT - 1);
 #pragma unroll 2
       for (int t = kT - 1; t >= 0; --t) {
-        tmem_get(states + t * 2 * PAIRS, h);
-        token_bwd<G>(sm, w, t, h, A2, dh, gA);
+        ahead.read(sm, w, t > 0 ? t - 1 : 0);
+        if (t < kT - 1) tmem_get(states + t * 2 * PAIRS, h);
+        token_bwd<G>(sm, w, t, k, h, A2, dh, gA);
+        k = ahead;
       }
     } else {
       Where f = seqs::find(a.s, row);
@@ -462,14 +478,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
         if (row + t >= f.end) f = seqs::find(a.s, row + t);
         if (row + t == f.begin) load_state<G>(a, w, a.init, f.i, h);
         tmem_put(states + t * 2 * PAIRS, h);
-        Token<G> k;
+        Token<G, false> k;
         k.read(sm, w, t);
         k.forward(A2, h);
       }
       tmem_put_wait();
       for (int t = n - 1; t >= 0; --t) {
         tmem_get(states + t * 2 * PAIRS, h);
-        token_bwd<G>(sm, w, t, h, A2, dh, gA);
+        Token<G, true> k;
+        k.read(sm, w, t);
+        token_bwd<G>(sm, w, t, k, h, A2, dh, gA);
         if (row + t == q.begin) {              // the first row of its sequence: out, and on with the one before
           if (a.grad_init && on) store_state<G>(a, w, a.grad_init, q.i, dh);
           if (row + t > r0) {
@@ -493,14 +511,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
         };
         F2 x[VP], g[VP], f[VP], s1[VP], u[VP];
         const uint4 xv = load_here(vector(a.x, a.ldx, r)), gv = load_here(vector(a.grad_y, a.d, r));
-        uint4 zv = make_uint4(0, 0, 0, 0);
-        if (a.z) zv = load_here(vector(a.z, a.ldz, r));
-        U::pairs(x, xv);
-        U::pairs(g, gv);
+        const uint4 zv = load_here(vector(a.z, a.ldz, r), a.z != nullptr);
+        U::get(x, xv);
+        U::get(g, gv);
         if (a.z) {
           F2 z[VP];
-          U::pairs(z, zv);
-          get_pairs(&sm.g[w.row(k)][w.col()], u);
+          U::get(z, zv);
+          get_pairs(&sm.y[w.row(k)][w.col()], u);
 #pragma unroll
           for (int e = 0; e < VP; ++e) {
             // silu'(z) = s (1 + z (1 - s)) = s + z s (1 - s)
@@ -511,7 +528,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
           }
           out(a.grad_z, u);
         }
-        get_pairs(&sm.dx[w.row(k)][w.col()], s1);
+        get_pairs(&sm.s1[w.row(k)][w.col()], s1);
         get_pairs(&sm.s2[w.row(k)][w.col()], f);
         get_pairs(&sm.sig[w.row(k)][w.col()], u);
 #pragma unroll

@@ -43,23 +43,6 @@ template <> struct Vec<__nv_bfloat16, 8> {
   __device__ static __forceinline__ float round(float v) { return round_bf16(v); }
 };
 
-template <> struct Vec<__nv_bfloat16, 4> {
-  using E = __nv_bfloat16;
-  static constexpr int N = 4;
-  using T = uint2;
-  __device__ static __forceinline__ void get(float (&f)[4], const uint2& v) {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-  __device__ static __forceinline__ uint2 make(const float (&f)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-  __device__ static __forceinline__ float round(float v) { return round_bf16(v); }
-};
-
 template <> struct Vec<float, 1> {
   using E = float;
   static constexpr int N = 1;

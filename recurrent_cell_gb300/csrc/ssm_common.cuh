@@ -21,18 +21,19 @@
 // sum) and a short serial pass over segments.
 #pragma once
 
+#include "pair_math.cuh"
 #include "row_ops.cuh"
 #include "seq_rows.cuh"
 
 namespace cfc {
 namespace ssm {
 
+using namespace pairs;
 using seqs::Seqs;
 using seqs::Where;
 
 constexpr int kResident = 12;                  // warps of an SM at once
 constexpr int kT = 16;                       // rows of a chunk
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 struct Args {
   const void *x, *delta, *z, *B, *C;
@@ -70,59 +71,6 @@ struct Cfg {
   static constexpr int BL = (kT * BV + 31) / 32;             // of a chunk, a lane
 };
 
-__device__ __forceinline__ float ex2(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp(float v) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-__device__ __forceinline__ float min_nan(float a, float b) {     // a NaN stays
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// Two floats at a time: the scan is bound by instructions issued, and one of these does
-// the work of two.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pack(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 twice(float a) { return pack(a, a); }
-__device__ __forceinline__ void split(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ F2 ex2_2(F2 v) {
-  float a, b;
-  split(v, a, b);
-  return pack(ex2(a), ex2(b));
-}
-__device__ __forceinline__ float sum2(F2 v) {
-  float a, b;
-  split(v, a, b);
-  return a + b;
-}
-
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|), of two values.  The exponent's
 // rounding is put right by a first-order term; log1p(e) = e P(e) on [0, 1] with P of
 // degree 8, fitted for the smallest relative error (3e-8; 1.7e-7 with the roundings).
@@ -154,15 +102,6 @@ __device__ __forceinline__ float softplus(float v) {
   split(softplus2(twice(v)), a, b);
   return a;
 }
-// 1 / (1 + exp(-v)) of two values: 0 where the exponential is infinite.
-__device__ __forceinline__ F2 sigmoid2(F2 v) {
-  const F2 e = add2(ex2_2(mul2(v, twice(-kLog2e))), twice(1.f));
-  float a, b;
-  split(e, a, b);
-  return pack(rcp(a), rcp(b));
-}
-__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(v * -kLog2e)); }
-
 // The warp's tile of channels.
 template <class G>
 struct Tile {
@@ -319,55 +258,15 @@ constexpr __device__ __forceinline__ int cpair(int p) { return G::CPL > 1 ? p / 
 template <class G>
 constexpr __device__ __forceinline__ int spair(int p) { return G::CPL > 1 ? p % G::NS : p; }
 
-// A read that stays where it is written: the compiler would move one whose value is
-// needed late down to where it is, and its latency with it.
-__device__ __forceinline__ uint4 load_here(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 // A chunk's vectors of a [rows, channels] tensor, zeros outside.
 template <class G>
 __device__ __forceinline__ void load_raw(const Tile<G>& w, const void* p, long long ld, long long row0, int n, uint4 (&v)[G::P]) {
   const typename G::E* q = static_cast<const typename G::E*>(p) + w.c0 + w.col();
 #pragma unroll
   for (int k = 0; k < G::P; ++k) {
-    v[k] = make_uint4(0, 0, 0, 0);
-    if (w.row(k) < n && w.col() < w.cols) v[k] = load_here(q + (row0 + w.row(k)) * ld);
+    v[k] = load_here(q + (row0 + w.row(k)) * ld, w.row(k) < n && w.col() < w.cols);
   }
 }
-template <class E> struct Unpack;
-template <> struct Unpack<__nv_bfloat16> {
-  __device__ static __forceinline__ void get(float (&f)[8], const uint4& v) { rows::Vec<__nv_bfloat16, 8>::get(f, v); }
-  __device__ static __forceinline__ void pairs(F2 (&p)[4], const uint4& v) {
-    float f[8];
-    get(f, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack(f[2 * i], f[2 * i + 1]);
-  }
-  __device__ static __forceinline__ uint4 make(const F2 (&p)[4]) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) split(p[i], f[2 * i], f[2 * i + 1]);
-    return rows::Vec<__nv_bfloat16, 8>::make(f);
-  }
-};
-template <> struct Unpack<float> {
-  __device__ static __forceinline__ void get(float (&f)[4], const uint4& v) {
-    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
-  }
-  __device__ static __forceinline__ void pairs(F2 (&p)[2], const uint4& v) {
-    p[0] = pack(__uint_as_float(v.x), __uint_as_float(v.y));
-    p[1] = pack(__uint_as_float(v.z), __uint_as_float(v.w));
-  }
-  __device__ static __forceinline__ uint4 make(const F2 (&p)[2]) {
-    float f[4];
-    split(p[0], f[0], f[1]);
-    split(p[1], f[2], f[3]);
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-};
 // The lane's columns of a vector over channels (NULL: zeros).
 template <class G>
 __device__ __forceinline__ void load_pairs(const Tile<G>& w, const float* s, F2 (&v)[G::VN / 2]) {
@@ -400,8 +299,7 @@ struct Rows {
 #pragma unroll
     for (int k = 0; k < G::BL; ++k) {
       const int i = k * 32 + w.lane, r = i / G::BV;
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (r < n) v[k] = load_here(q + (row0 + r) * ld + i % G::BV * G::VN);
+      v[k] = load_here(q + (row0 + r) * ld + i % G::BV * G::VN, r < n);
     }
   }
   __device__ __forceinline__ void stage(const Args& a, const Tile<G>& w, const void* p, long long ld, long long row0, int n,
@@ -410,9 +308,9 @@ struct Rows {
 #pragma unroll
       for (int k = 0; k < G::BL; ++k) {
         const int i = k * 32 + w.lane;
-        float f[G::VN];
-        Unpack<typename G::E>::get(f, v[k]);
-        if (i < kT * G::BV) put(tile + i * G::VN, f);
+        F2 f[G::VN / 2];
+        Pairs<typename G::E, G::VN>::get(f, v[k]);
+        if (i < kT * G::BV) put_pairs(tile + i * G::VN, f);
       }
     } else {
       const typename G::E* q = static_cast<const typename G::E*>(p) + w.g * a.N;
