@@ -102,6 +102,16 @@ __device__ __forceinline__ void pre_of(const F2 (&w)[W][H], const F2 (&b)[H], co
     pre[e] = fma2(w[W - 1][e], x[e], pre[e]);
   }
 }
+// The same from W rows of an array, x[i] being the first.
+template <int W, int H, int R>
+__device__ __forceinline__ void pre_at(const F2 (&w)[W][H], const F2 (&b)[H], const F2 (&x)[R][H], int i, F2 (&pre)[H]) {
+#pragma unroll
+  for (int e = 0; e < H; ++e) {
+    pre[e] = b[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) pre[e] = fma2(w[j][e], x[i + j][e], pre[e]);
+  }
+}
 template <int W, int H>
 __device__ __forceinline__ void shift(F2 (&h)[W][H], const F2 (&x)[H]) {
 #pragma unroll
@@ -157,16 +167,35 @@ __global__ void __launch_bounds__(kThreads) k_conv(Args a) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) in[i] = next[i];
     fetch(row + kBatch);
-    const bool one = row + kBatch <= q.end;  // no sequence begins within the batch
+    if (row + kBatch <= q.end && row + kBatch <= r1) {       // a whole batch of one sequence: no row asks
+      F2 x[W - 1 + kBatch][H];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (row + i < r1) {
-        if (!one && row + i >= q.end) {      // the next sequence's first row
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < H; ++e) x[j][e] = h[j][e];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        F2 pre[H];
+        P::get(x[W - 1 + i], in[i]);
+        pre_at<W, H>(w, b, x, i, pre);
+        if (a.silu)
+#pragma unroll
+          for (int e = 0; e < H; ++e) pre[e] = mul2(pre[e], C::sigmoid(pre[e]));
+        C::write(a.y, (row + i) * a.d + c, pre);
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < H; ++e) h[j][e] = x[kBatch + j][e];
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kBatch && row + i < r1; ++i) {
+        if (row + i >= q.end) {              // the next sequence's first row
           q = seqs::find(a.s, row + i);
           window<C, W>(a, q, row + i, c, h);
         }
         F2 x[H], pre[H];
-        P::get(x, in[i]);
+        C::read(x, a.x, (row + i) * a.ldx + c);
         pre_of<W, H>(w, b, h, x, pre);
         shift<W - 1, H>(h, x);
         if (a.silu)
@@ -287,19 +316,53 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(Args a) {
       gin[i] = gnext[i];
     }
     fetch(row + kBatch);
-    const bool one = row + kBatch <= q.end;
+    const bool inside = row - (W - 1) >= r0 && row - (W - 1) >= q.begin;       // grad_x of all the batch's rows is due
+    if (inside && row + kBatch <= q.end && row + kBatch <= r1) {
+      F2 x[W - 1 + kBatch][H], pp[W - 1 + kBatch][H];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (row + i < r1) {
-        if (!one && row + i >= q.end) {      // the last rows of the one before, then the next sequence
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          x[j][e] = h[j][e];
+          pp[j][e] = p[j + 1][e];
+        }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        F2 gy[H], pre[H], g[H];
+        P::get(x[W - 1 + i], in[i]);
+        P::get(gy, gin[i]);
+        pre_at<W, H>(w, b, x, i, pre);
+        p_of<C>(a.silu, pre, gy, pp[W - 1 + i]);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            gw[j][e] = fma2(pp[W - 1 + i][e], x[i + j][e], gw[j][e]);
+            g[e] = j == 0 ? mul2(w[0][e], pp[W - 1 + i][e]) : fma2(w[j][e], pp[W - 1 + i - j][e], g[e]);
+          }
+          gb[e] = add2(gb[e], pp[W - 1 + i][e]);
+        }
+        C::write(a.grad_x, (row + i - (W - 1)) * a.d + c, g);
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          h[j][e] = x[kBatch + j][e];
+          p[j + 1][e] = pp[kBatch + j][e];
+        }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kBatch && row + i < r1; ++i) {
+        if (row + i >= q.end) {              // the last rows of the one before, then the next sequence
 #pragma unroll 1
           for (int k = 0; k < W - 1; ++k) emit(row + i + k, none);
           q = seqs::find(a.s, row + i);
           window<C, W>(a, q, row + i, c, h);
         }
         F2 x[H], gy[H], pre[H], now[H];
-        P::get(x, in[i]);
-        P::get(gy, gin[i]);
+        C::read(x, a.x, (row + i) * a.ldx + c);
+        C::read(gy, a.grad_y, (row + i) * a.d + c);
         pre_of<W, H>(w, b, h, x, pre);
         p_of<C>(a.silu, pre, gy, now);
 #pragma unroll

@@ -17,6 +17,7 @@
 // read two or three times, from L2 after the first, and their grad_w and grad_b
 // come from a pass over columns.  The block's partial grad_w and grad_b are rows of
 // the workspace that reduce_axis0 adds: no atomics, the same bits every time.
+#include "pair_math.cuh"
 #include "row_ops.cuh"
 
 namespace cfc {
@@ -34,8 +35,57 @@ struct Args {
   float eps;
 };
 
+// Arithmetic on a vector's values, two at a time where there are two: r = a op b.
+template <int N, class F2op, class F1op>
+__device__ __forceinline__ void each(F2op two, F1op one) {
+  if constexpr (N == 1) {
+    one(0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) two(e);
+  }
+}
+using pairs::F2;
+template <int N> __device__ __forceinline__ F2 at2(const float (&f)[N], int e) { return pairs::pack(f[e], f[(e + 1) % N]); }
+template <int N> __device__ __forceinline__ void to2(float (&f)[N], int e, F2 v) { pairs::split(v, f[e], f[(e + 1) % N]); }
+template <int N>
+__device__ __forceinline__ void add(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+  each<N>([&](int e) { to2(r, e, pairs::add2(at2(a, e), at2(b, e))); }, [&](int) { r[0] = a[0] + b[0]; });
+}
+template <int N>
+__device__ __forceinline__ void add(float (&r)[N], const float (&a)[N], float b) {
+  each<N>([&](int e) { to2(r, e, pairs::add2(at2(a, e), pairs::twice(b))); }, [&](int) { r[0] = a[0] + b; });
+}
+template <int N>
+__device__ __forceinline__ void mul(float (&r)[N], const float (&a)[N], float b) {
+  each<N>([&](int e) { to2(r, e, pairs::mul2(at2(a, e), pairs::twice(b))); }, [&](int) { r[0] = a[0] * b; });
+}
+template <int N>
+__device__ __forceinline__ void mul(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
+  each<N>([&](int e) { to2(r, e, pairs::mul2(at2(a, e), at2(b, e))); }, [&](int) { r[0] = a[0] * b[0]; });
+}
+template <int N>
+__device__ __forceinline__ void fma(float (&r)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+  each<N>([&](int e) { to2(r, e, pairs::fma2(at2(a, e), at2(b, e), at2(c, e))); }, [&](int) { r[0] = fmaf(a[0], b[0], c[0]); });
+}
+template <int N>
+__device__ __forceinline__ void fma(float (&r)[N], const float (&a)[N], float b, const float (&c)[N]) {
+  each<N>([&](int e) { to2(r, e, pairs::fma2(at2(a, e), pairs::twice(b), at2(c, e))); }, [&](int) { r[0] = fmaf(a[0], b, c[0]); });
+}
+template <int N>
+__device__ __forceinline__ float sum(const float (&a)[N]) {
+  float s[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) s[e] = a[e];
+#pragma unroll
+  for (int m = N / 2; m > 0; m >>= 1)
+#pragma unroll
+    for (int e = 0; e < m; ++e) s[e] += s[e + m];
+  return s[0];
+}
+
 // Two sums over a row at once, after the manner of over_row.
-struct Part2 {
+struct __align__(16) Part2 {
   float2 v[2][kWarps];
   __device__ __forceinline__ void clear() {
     if (threadIdx.x < 2 * kWarps) v[0][threadIdx.x] = make_float2(0.f, 0.f);
@@ -52,27 +102,94 @@ __device__ __forceinline__ float2 over_row2(float2 v, Part2& part, int& turn) {
   if constexpr (LANES == 0) {
     if ((threadIdx.x & 31) == 0) part.v[turn][threadIdx.x >> 5] = v;
     __syncthreads();
-    float2 s[4];
+    F2 s[2] = {};
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float2 p = part.v[turn][i];
-      s[i & 3] = i < 4 ? p : make_float2(s[i & 3].x + p.x, s[i & 3].y + p.y);
+    for (int i = 0; i < kWarps; i += 2) {
+      const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(&part.v[turn][i]);
+      s[0] = pairs::add2(s[0], p.x);
+      s[1] = pairs::add2(s[1], p.y);
     }
-    v = make_float2((s[0].x + s[1].x) + (s[2].x + s[3].x), (s[0].y + s[1].y) + (s[2].y + s[3].y));
+    pairs::split(pairs::add2(s[0], s[1]), v.x, v.y);
     turn ^= 1;
   }
   return v;
 }
 
+// A thread's vectors of the rows ahead, K tensors: 16-byte vectors are copied into shared memory, each thread
+// its own, STAGES - 1 rows ahead (no registers, and no barrier, since nobody else reads them);
+// single values, too small for such copies, one row ahead into registers.
+template <class V, int NV, int LANES, int K, int STAGES>
+struct Ahead {
+  using R = Row<V, NV, LANES>;
+  using T = typename V::T;
+  static constexpr bool RING = V::N > 1;
+  static constexpr int kBytes = RING ? STAGES * K * NV * 16 : 0;       // of shared memory, a thread
+  T regs[K][RING ? 1 : NV];
+  unsigned char* base;
+  const T* from[K];                    // the thread's first vector of the row that is sent for next (NULL: no such tensor)
+  int stage = 0;
+  __device__ __forceinline__ uint4* at(int s, int k, int j) const {
+    return reinterpret_cast<uint4*>(base) + ((s * K + k) * NV + j) * blockDim.x + threadIdx.x;
+  }
+  __device__ __forceinline__ void fetch(const R& r, bool on, long long step, int s) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (from[k]) {
+        if (on) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if constexpr (RING) {
+              if (r.in(j)) pairs::copy16(at(s, k, j), from[k] + j * r.L, true);
+            } else {
+              if (r.in(j)) regs[k][j] = __ldcs(from[k] + j * r.L);
+            }
+          }
+        }
+        from[k] += step;
+      }
+    if constexpr (RING) pairs::copies_end();
+  }
+  // p: the tensors; step, in rows, from one row of the thread's to the next.
+  __device__ __forceinline__ void start(const R& r, const void* const (&p)[K], long long row, long long step, long long rows, int d) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      from[k] = p[k] ? reinterpret_cast<const T*>(static_cast<const typename V::E*>(p[k]) + row * d) + r.l : nullptr;
+#pragma unroll
+    for (int s = 0; s < (RING ? STAGES - 1 : 1); ++s) fetch(r, row + s * step < rows, step * r.nvec, s);
+  }
+  // The row at hand into v; the row STAGES - 1 (1) steps on is sent for.
+  __device__ __forceinline__ void next(const R& r, long long row, long long step, long long rows, T (&v)[K][NV]) {
+    if constexpr (RING) {
+      pairs::copies_wait<STAGES - 2>();
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (from[k])
+#pragma unroll
+          for (int j = 0; j < NV; ++j) v[k][j] = *reinterpret_cast<const T*>(at(stage, k, j));
+      // into the stage that was read in the last round
+      fetch(r, row + (STAGES - 1) * step < rows, step * r.nvec, stage == 0 ? STAGES - 1 : stage - 1);
+      stage = stage == STAGES - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[k][j] = regs[k][j];
+      fetch(r, row + step < rows, step * r.nvec, 0);
+    }
+  }
+};
+template <class V, int NV, int LANES> using FwdAhead = Ahead<V, NV, LANES, 2, 3>;
+template <class V, int NV, int LANES> using BwdAhead = Ahead<V, NV, LANES, 3, (NV > 2 ? 2 : 3)>;
+
 template <class V, int NV, int LANES>
-__global__ void __launch_bounds__(LANES ? kLaneThreads : 512, !LANES && NV * V::N <= 16 ? 2 : 1) k_layernorm(Args a) {
+__global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm(Args a) {
   using R = Row<V, NV, LANES>;
   using E = typename V::E;
   using T = typename V::T;
   constexpr int N = V::N, RPB = kRows<LANES>;
-  __shared__ Part part;
+  __shared__ Part part_;
   int turn = 0;
-  if (!LANES) part.clear();
+  if (!LANES) part_.clear();
   const R r(a.d);
   float w[NV][N], b[NV][N] = {};
   r.weights(w, a.w);
@@ -80,45 +197,46 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512, !LANES && NV * V::
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-  T xv[NV], rv[NV];
-  r.load(xv, a.x, row, a.rows, a.d);
-  if (a.residual) r.load(rv, a.residual, row, a.rows, a.d);
+  extern __shared__ __align__(16) unsigned char ring[];
+  FwdAhead<V, NV, LANES> ahead;
+  ahead.base = ring;
+  const void* const in[2] = {a.x, a.residual};
+  ahead.start(r, in, row, step, a.rows, a.d);
   // (the lanes of a warp whose rows are over stay for the others' shuffles)
   for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
     const bool on = row < a.rows;
-    float s[NV][N];
-    float sum = 0.f, sq = 0.f;
+    T v[2][NV];
+    ahead.next(r, row, step, a.rows, v);
+    float s[NV][N], part[N] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int e = 0; e < N; ++e) s[j][e] = 0.f;
       if (on && r.in(j)) {
-        V::get(s[j], xv[j]);
+        V::get(s[j], v[0][j]);
+        T stored = v[0][j];
         if (a.residual) {
           float t[N];
-          V::get(t, rv[j]);
-#pragma unroll
-          for (int e = 0; e < N; ++e) s[j][e] = V::round(s[j][e] + t[e]);
+          V::get(t, v[1][j]);
+          add(t, s[j], t);
+          stored = V::make(t);               // rounded once, for the store and for what follows
+          V::get(s[j], stored);
         }
-        if (a.s_out) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d) + r.at(j), V::make(s[j]));
+        if (a.s_out) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d) + r.at(j), stored);
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) sum += s[j][e];
+      add(part, part, s[j]);
     }
-    r.load(xv, a.x, row + step, a.rows, a.d);
-    if (a.residual) r.load(rv, a.residual, row + step, a.rows, a.d);
-    const float mean = over_row<Sum, LANES>(sum, part, turn) * inv_d;
+    const float mean = over_row<Sum, LANES>(sum(part), part_, turn) * inv_d;
+    float sq[N] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (r.in(j))
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          s[j][e] -= mean;
-          sq = fmaf(s[j][e], s[j][e], sq);
-        }
-    sq = over_row<Sum, LANES>(sq, part, turn);
+      if (r.in(j)) {
+        add(s[j], s[j], -mean);
+        fma(sq, s[j], s[j], sq);
+      }
+    const float var = over_row<Sum, LANES>(sum(sq), part_, turn);
     if (!LANES && a.b) r.weights(b, a.b);        // from L1: kept, it would spill
-    const float rstd = 1.f / sqrtf(fmaf(sq, inv_d, a.eps));
+    const float rstd = 1.f / sqrtf(fmaf(var, inv_d, a.eps));
     if (on && r.l == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -126,8 +244,8 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512, !LANES && NV * V::
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s[j][e] = fmaf(s[j][e] * rstd, w[j][e], b[j][e]);
+        mul(s[j], s[j], rstd);
+        fma(s[j], s[j], w[j], b[j]);
         __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), V::make(s[j]));
       }
   }
@@ -139,7 +257,7 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm_bwd(Ar
   using E = typename V::E;
   using T = typename V::T;
   constexpr int N = V::N, RPB = kRows<LANES>;
-  extern __shared__ float sums[];                // [RPB][d] where a block has several rows
+  extern __shared__ __align__(16) float sums[];  // the rows ahead; in the end [RPB][d] where a block has several rows
   __shared__ Part2 part;
   int turn = 0;
   if (!LANES) part.clear();
@@ -149,68 +267,59 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm_bwd(Ar
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-  T sv[NV], gv[NV], rv[NV];
+  BwdAhead<V, NV, LANES> ahead;
+  ahead.base = reinterpret_cast<unsigned char*>(sums);
+  const void* const in[3] = {a.x, a.grad_y, a.grad_s};
+  ahead.start(r, in, row, step, a.rows, a.d);
   float mean = 0.f, rstd = 0.f;
-  auto fetch = [&](long long row) {
-    r.load(sv, a.x, row, a.rows, a.d);
-    r.load(gv, a.grad_y, row, a.rows, a.d);
-    if (a.grad_s) r.load(rv, a.grad_s, row, a.rows, a.d);
+  auto scalars = [&](long long row) {
     if (row < a.rows) {
       mean = a.mean_in[row];
       rstd = a.rstd_in[row];
     }
   };
-  fetch(row);
+  scalars(row);
   for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
     const bool on = row < a.rows;
     const long long at = row * a.d;
-    T cs[NV], cg[NV], cv[NV];
     const float rs = rstd, mu = mean;
-    float2 dot = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      cs[j] = sv[j];
-      cg[j] = gv[j];
-      cv[j] = rv[j];
-    }
-    fetch(row + step);
-    // n = (s - mean) rstd, dn = grad_y w; formed twice rather than kept, for the registers
+    T v[3][NV];
+    ahead.next(r, row, step, a.rows, v);
+    scalars(row + step);
+    // n = (s - mean) rstd, dn = grad_y w
+    float sn[N] = {}, sg[N] = {}, n[NV][N], g[NV][N];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-        float n[N], g[N];
-        V::get(n, cs[j]);
-        V::get(g, cg[j]);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          n[e] = (n[e] - mu) * rs;
-          gw[j][e] = fmaf(g[e], n[e], gw[j][e]);
-          gb[j][e] += g[e];
-          g[e] *= w[j][e];
-          dot.x += g[e];
-          dot.y = fmaf(g[e], n[e], dot.y);
-        }
+        V::get(n[j], v[0][j]);
+        V::get(g[j], v[1][j]);
+        add(gb[j], gb[j], g[j]);
+        add(n[j], n[j], -mu);
+        mul(n[j], n[j], rs);
+        fma(gw[j], g[j], n[j], gw[j]);
+        mul(g[j], g[j], w[j]);
+        add(sg, sg, g[j]);
+        fma(sn, g[j], n[j], sn);
       }
-    dot = over_row2<LANES>(dot, part, turn);
-    dot.x *= inv_d;
-    dot.y *= inv_d;
+    const float2 dot = over_row2<LANES>(make_float2(sum(sg), sum(sn)), part, turn);
+    const float k = -rs * (dot.y * inv_d), l = -rs * (dot.x * inv_d);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-        float n[N], g[N], o[N];
-        V::get(n, cs[j]);
-        V::get(g, cg[j]);
+        float o[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = rs * (fmaf(g[e], w[j][e], -dot.x) - (n[e] - mu) * rs * dot.y);
+        for (int e = 0; e < N; ++e) o[e] = l;
+        fma(o, n[j], k, o);
+        fma(o, g[j], rs, o);
         if (a.grad_s) {
           float t[N];
-          V::get(t, cv[j]);
-#pragma unroll
-          for (int e = 0; e < N; ++e) o[e] += t[e];
+          V::get(t, v[2][j]);
+          add(o, o, t);
         }
         __stcs(reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at) + r.at(j), V::make(o));
       }
   }
+  if constexpr (BwdAhead<V, NV, LANES>::RING) pairs::copies_wait<0>();
   // The block's row of partial sums [grad_w | grad_b], its rows' lanes in order.
   float* out = a.part + (long long)blockIdx.x * 2 * a.d;
   if constexpr (LANES > 0) {
@@ -232,12 +341,19 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm_bwd(Ar
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (r.in(j))
+      if (r.in(j)) {
+        if constexpr (N == 1) {
+          out[r.at(j)] = gw[j][0];
+          out[a.d + r.at(j)] = gb[j][0];
+        } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          out[r.at(j) * N + e] = gw[j][e];
-          out[a.d + r.at(j) * N + e] = gb[j][e];
+          for (int e = 0; e < N; e += 4) {
+            *reinterpret_cast<float4*>(out + r.at(j) * N + e) = make_float4(gw[j][e], gw[j][e + 1], gw[j][e + 2], gw[j][e + 3]);
+            *reinterpret_cast<float4*>(out + a.d + r.at(j) * N + e) =
+                make_float4(gb[j][e], gb[j][e + 1], gb[j][e + 2], gb[j][e + 3]);
+          }
         }
+      }
   }
 }
 
@@ -381,16 +497,24 @@ constexpr int kMaxBlocks = 4 * kNumSMs;          // rows of partial sums at most
 template <class V, int NV, int LANES>
 static cudaError_t fwd(const Args& a, int threads, cudaStream_t st) {
   constexpr int RPB = kRows<LANES>;
+  using Ring = FwdAhead<V, NV, LANES>;
+  const size_t smem = (size_t)threads * Ring::kBytes;
+  const cudaError_t e = allow_smem<k_layernorm<V, NV, LANES>>((LANES ? kLaneThreads : 512) * Ring::kBytes);
+  if (e != cudaSuccess) return e;
   const long long need = (a.rows + RPB - 1) / RPB;
-  const long long most = (long long)resident<&k_layernorm<V, NV, LANES>>(threads, 0) * kNumSMs;
+  const long long most = (long long)resident<&k_layernorm<V, NV, LANES>>(threads, smem) * kNumSMs;
   TraceScope tr("k_layernorm", st);
-  k_layernorm<V, NV, LANES><<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
+  k_layernorm<V, NV, LANES><<<(unsigned)(need < most ? need : most), threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <class V, int NV, int LANES>
 static cudaError_t bwd(const Args& a, int threads, int* blocks, cudaStream_t st) {
   constexpr int RPB = kRows<LANES>;
-  const size_t smem = LANES ? (size_t)RPB * a.d * 4 : 0;
+  using Ring = BwdAhead<V, NV, LANES>;
+  size_t smem = (size_t)threads * Ring::kBytes;
+  if (LANES && smem < (size_t)RPB * a.d * 4) smem = (size_t)RPB * a.d * 4;
+  cudaError_t e = allow_smem<k_layernorm_bwd<V, NV, LANES>>((LANES ? kLaneThreads : 512) * Ring::kBytes);
+  if (e != cudaSuccess) return e;
   const long long need = (a.rows + RPB - 1) / RPB;
   long long most = (long long)resident<&k_layernorm_bwd<V, NV, LANES>>(threads, smem) * kNumSMs;
   if (most > kMaxBlocks) most = kMaxBlocks;
@@ -413,11 +537,9 @@ static cudaError_t by_row(int d, F f) {
     if (nvec <= 32) return f.template operator()<V, 2, 16>(kLaneThreads);
     if (nvec <= 64) return f.template operator()<V, 2, 32>(kLaneThreads);
     if (nvec <= 128) return f.template operator()<V, 4, 32>(kLaneThreads);
-    if constexpr (BWD) {
-      if (threads(2) <= 512) return f.template operator()<V, 2, 0>(threads(2));
-    } else {
+    if (threads(2) <= 512) return f.template operator()<V, 2, 0>(threads(2));
+    if constexpr (!BWD)
       if (threads(4) <= 512) return f.template operator()<V, 4, 0>(threads(4));
-    }
   } else {
     if (threads(4) <= 128) return f.template operator()<V, 4, 0>(threads(4));
     if (threads(8) <= 512) return f.template operator()<V, 8, 0>(threads(8));

@@ -82,14 +82,6 @@ __device__ __forceinline__ void tmem_get(uint32_t at, F2 (&h)[N]) {
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;"); }
 
-// 16 bytes of global memory (or zeros) to shared memory, asynchronously.
-__device__ __forceinline__ void copy16(void* to, const void* from, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copies_done() {
-  asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
-}
-
 // One value of each lane's quarter: v[i] summed over the lanes of a group of 4
 // (M = 1, 2) or 8 (M = 4, 8, 16), value i of N ending up in the lanes whose bits of M say i.
 template <int N>
@@ -400,7 +392,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
   for (; chunk >= 0; --chunk) {
     const long long row = r0 + (long long)chunk * kT;
     const int n = r1 - row < kT ? (int)(r1 - row) : kT;
-    copies_done();
+    copies_end();
+    copies_wait<0>();
     __syncwarp();
     // dt, its slope, dt x and g of the chunk's tokens
 #pragma unroll

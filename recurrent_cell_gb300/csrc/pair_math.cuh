@@ -104,6 +104,15 @@ __device__ __forceinline__ uint2 load_here8(const void* p, bool on = true) {
   return v;
 }
 
+// 16 bytes of global memory (or zeros) to shared memory, asynchronously; the copies since the
+// last call as one group; the wait until at most N groups are on their way.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // N stored values as pairs, and back (rounded to nearest even).
 template <class E, int N> struct Pairs;
 template <> struct Pairs<__nv_bfloat16, 8> {
