@@ -48,7 +48,7 @@ __device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, 
 #pragma unroll
   for (int p = 0; p < G::PAIRS; ++p) {
     const int i = cpair<G>(p), j = spair<G>(p);
-    h[p] = fma2(ex2_2(mul2(o.dt[i], A2[p])), h[p], mul2(o.dx[i], o.b[j]));
+    h[p] = fma2(decay2(o.dt[i], A2[p]), h[p], mul2(o.dx[i], o.b[j]));
     if constexpr (!LOCAL) y[i] = j == 0 ? mul2(o.c[j], h[p]) : fma2(o.c[j], h[p], y[i]);
   }
   if constexpr (LOCAL) {

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
 #pragma unroll
       for (int p = 0; p < G::PAIRS; ++p) {
         const int i = cpair<G>(p), j = spair<G>(p);
-        dh[p] = mul2(ex2_2(mul2(dt[i], A2[p])), fma2(c[j], g[i], dh[p]));
+        dh[p] = mul2(decay2(dt[i], A2[p]), fma2(c[j], g[i], dh[p]));
       }
 #pragma unroll
       for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], dt[i]);
@@ -237,7 +237,7 @@ struct Token {
   __device__ __forceinline__ void forward(const F2 (&A2)[G::PAIRS], F2 (&h)[G::PAIRS]) const {
 #pragma unroll
     for (int p = 0; p < G::PAIRS; ++p)
-      h[p] = fma2(ex2_2(mul2(dt[cpair<G>(p)], A2[p])), h[p], mul2(dx[cpair<G>(p)], b[spair<G>(p)]));
+      h[p] = fma2(decay2(dt[cpair<G>(p)], A2[p]), h[p], mul2(dx[cpair<G>(p)], b[spair<G>(p)]));
   }
 };
 
@@ -253,7 +253,7 @@ __device__ __forceinline__ void token_bwd(BwdTiles<G>& sm, const Tile<G>& w, int
   for (int p = 0; p < G::PAIRS; ++p) {
     const int i = cpair<G>(p), j = spair<G>(p);
     const bool first_i = G::CPL > 1 ? j == 0 : p == 0, first_j = G::CPL > 1 ? i == 0 : true;
-    const F2 e = ex2_2(mul2(k.dt[i], A2[p]));
+    const F2 e = decay2(k.dt[i], A2[p]);
     const F2 ah = mul2(e, h[p]), now = fma2(k.dx[i], k.b[j], ah), d = fma2(k.c[j], k.g[i], dh[p]), q = mul2(d, ah);
     y[i] = first_i ? mul2(k.c[j], now) : fma2(k.c[j], now, y[i]);
     s1[i] = first_i ? mul2(d, k.b[j]) : fma2(d, k.b[j], s1[i]);

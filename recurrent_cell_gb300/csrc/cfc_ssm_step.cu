@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kStepThreads) k_ssm_step(StepArgs g) {
           lane_states<float, NS, VEC>(a.A + (long long)(c0 + 8 * k + cl) * a.N + sl * NS, left, A);
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
-            h[k][j] = fmaf(ex2(dtk * (A[j] * kLog2e)), h[k][j], dxk * b[j]);
+            h[k][j] = fmaf(decay(dtk, A[j] * kLog2e), h[k][j], dxk * b[j]);
             part[k] = fmaf(c[j], h[k][j], part[k]);
           }
         }
