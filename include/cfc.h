@@ -432,9 +432,12 @@ int cfc_layernorm_backward(const void* s, const float* weight, const float* mean
  *         16 bytes), in the mode's type; y, grad_y, grad_x like x but dense
  *   states [n_seq, width - 1, channels] in the mode's type
  *   weight, grad_weight [channels, width], bias, grad_bias [channels]: float
- * Sequences as for the gated delta rule: seq_offsets NULL, n_seq sequences of rows /
- * n_seq rows, else a DEVICE array of n_seq + 1 non-decreasing row numbers from 0
- * to rows; nothing outside the tensors is touched whatever it holds.
+ * Sequences: seq_offsets NULL, n_seq sequences of rows / n_seq rows, else a DEVICE
+ * array of n_seq + 1 non-decreasing row numbers from 0, sequence i having the rows
+ * from seq_offsets[i] up to seq_offsets[i + 1] (none is allowed).  Rows from
+ * seq_offsets[n_seq] on are nobody's: not read, and left as they are in every
+ * output, so that a batch may be padded.  Nothing outside the tensors is touched
+ * whatever the array holds.
  * Sizes: channels a multiple of 8, 2 <= width <= 8, 1 <= n_seq <= 2^20,
  * 0 <= rows <= 2^30.  Pointers 16-byte aligned (bias, seq_offsets, slots: 4).  Outputs
  * overlap neither inputs nor one another (CFC_ERR_OVERLAP where that is seen).

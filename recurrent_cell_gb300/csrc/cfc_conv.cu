@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kThreads) k_conv(Args a) {
     if (a.final_state && seq < a.s.n) final_rows<C, W>(a, (int)seq, c);
     return;
   }
+  a.s = seqs::trim(a.s);
   const long long r0 = tile * a.tile, r1 = a.s.rows - r0 < a.tile ? a.s.rows : r0 + a.tile;
+  if (r0 >= r1) return;                      // rows behind the last sequence
   typename C::T in[kBatch], next[kBatch];
   auto fetch = [&](long long row) {
     const typename C::E* p = static_cast<const typename C::E*>(a.x) + row * a.ldx + c;
@@ -279,7 +281,18 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(Args a) {
     if (a.grad_init && seq < a.s.n) init_rows<C, W>(a, (int)seq, c);
     return;
   }
+  a.s = seqs::trim(a.s);
   const long long r0 = tile * a.tile, r1 = a.s.rows - r0 < a.tile ? a.s.rows : r0 + a.tile;
+  float* part = a.part + tile * ((W + 1ll) * a.d);          // [grad_w | grad_b]
+  if (r0 >= r1) {                            // rows behind the last sequence: sums of nothing
+#pragma unroll
+    for (int e = 0; e < C::N; ++e) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) part[(long long)(c + e) * W + j] = 0.f;
+      part[(long long)W * a.d + c + e] = 0.f;
+    }
+    return;
+  }
   typename C::T in[kBatch], gin[kBatch], next[kBatch], gnext[kBatch];
   auto fetch = [&](long long row) {
     const typename C::E* p = static_cast<const typename C::E*>(a.x) + row * a.ldx + c;
@@ -391,7 +404,6 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(Args a) {
     }
     emit(row, now);
   }
-  float* part = a.part + tile * ((W + 1ll) * a.d);          // [grad_w | grad_b]
 #pragma unroll
   for (int e = 0; e < H; ++e) {
     float f[2];

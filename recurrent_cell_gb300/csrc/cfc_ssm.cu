@@ -88,9 +88,14 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
     return;
   }
 
+  a.s = seqs::trim(a.s);
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
   Where q;
   long long row = r0;
+  if (r0 >= r1) {                            // rows behind the last sequence
+    if (LOCAL && blockIdx.x == 0 && w.lane == 0) a.flags[seg] = 0;
+    return;
+  }
   if constexpr (LOCAL) {
     q = seqs::find(a.s, r1 - 1);
     const bool cut = q.end > r1, starts = q.begin >= r0;

@@ -183,7 +183,12 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
   __shared__ LocalTiles<G> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
+  a.s = seqs::trim(a.s);
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
+  if (r0 >= r1) {                            // rows behind the last sequence
+    if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = 0;
+    return;
+  }
   const Where q = seqs::find(a.s, r0);
   const bool cut = q.begin < r0, ends = q.end <= r1;
   if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (ends ? kStarts : 0);
@@ -339,13 +344,23 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
     return;
   }
 
+  const long long all_rows = a.s.rows;
+  a.s = seqs::trim(a.s);
+  const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
+  float* part = a.part + (long long)seg * a.d * (a.N + 2);   // the segment's dA, dD, dbias: [d, N | d | d]
+  if (r0 >= r1) {                              // rows behind the last sequence: sums of nothing
+    const int n = on ? w.cols : 0;
+    for (int i = w.lane; i < n * a.N; i += 32) part[(long long)w.c0 * a.N + i] = 0.f;
+    for (int i = w.lane; i < n; i += 32) part[(long long)a.d * a.N + w.c0 + i] = part[(long long)a.d * (a.N + 1) + w.c0 + i] = 0.f;
+    return;
+  }
+
   if (warp == 0) tc::tmem_alloc(&tmem, kColumns);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t states = tmem + ((uint32_t)warp * 32u << 16);
 
-  const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
   F2 A2[PAIRS], bias[VP], D[VP], gD[VP] = {}, gb[VP] = {};
   load_A<G>(a, w, A2);
   load_pairs<G>(w, a.bias, bias);
@@ -550,7 +565,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
 #pragma unroll
       for (int k = 1; k < kBwdWarps; ++k)
         if (k < warps) v += tiles[k].bc[t][s];
-      a.bc[((long long)blockIdx.x * a.s.rows + row + t) * (2 * NP) + s] = v;
+      a.bc[((long long)blockIdx.x * all_rows + row + t) * (2 * NP) + s] = v;
     }
     __syncthreads();
   }
@@ -558,9 +573,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 0) tc::tmem_dealloc(tmem, kColumns);
-  // the segment's dA, dD, dbias: [d, N | d | d]
   if (on) {
-    float* part = a.part + (long long)seg * a.d * (a.N + 2);
     F2 gA[PAIRS];
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) gA[p] = sm.gA[p][w.lane];
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kBcThreads) k_ssm_bc(Args a, int NP, int quads
   const long long rg = id / (2 * NP);
   const int g = (int)(rg % a.groups), n = s % NP;
   const long long row = rg / a.groups;
-  if (row >= a.s.rows || n >= a.N) return;
+  if (row >= seqs::trim(a.s).rows || n >= a.N) return;
   float v = 0.f;
 #pragma unroll 8
   for (int q = 0; q < quads; ++q) v += __ldcs(a.bc + (((long long)g * quads + q) * a.s.rows + row) * (2 * NP) + s);

@@ -14,6 +14,16 @@ struct Seqs {
 };
 __host__ __forceinline__ Seqs make_seqs(const int* off, int n, long long rows) { return Seqs{off, n, rows, rows / n}; }
 
+// The same with the rows that belong to a sequence: those behind the last are nobody's,
+// neither read nor written.
+__device__ __forceinline__ Seqs trim(Seqs s) {
+  if (s.off) {
+    const long long end = __ldg(s.off + s.n);
+    s.rows = end < 0 ? 0 : (end < s.rows ? end : s.rows);
+  }
+  return s;
+}
+
 // Rows [begin, end) of sequence i.  Offsets are held inside [0, rows], so that
 // nothing outside the tensors is touched whatever the array holds.
 __device__ __forceinline__ void range_of(const Seqs& s, int i, long long* begin, long long* end) {
