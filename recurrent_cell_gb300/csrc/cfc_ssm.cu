@@ -11,38 +11,31 @@
 namespace cfc {
 namespace ssm {
 
+// Two of each: the chunk that the states run through, and the next or the one before.
 template <class G, bool LOCAL>
 struct __align__(16) FwdTiles {
-  float dt[kT][G::CW], dx[kT][G::CW];        // dt, dt x
-  float B[kT][G::NP];
-  float C[LOCAL ? 1 : kT][G::NP];
-  float y[LOCAL ? 1 : kT][4 * G::CW];        // C . h, a part from each state lane
+  float dt[2][kT][G::CW], dx[2][kT][G::CW];  // dt, dt x
+  float B[2][kT][G::NP];
+  float C[LOCAL ? 1 : 2][kT][G::NP];
+  float y[LOCAL ? 1 : 2][kT][G::CW];         // C . h
+  uint4 raw[2][G::P][32], rawB[LOCAL ? 1 : 2][G::BL][32];    // x, delta; B, C: the chunk to come as the lanes take it
 };
-
-// Where state lane sl's part of channels c .. c + CPL - 1 of row t lies.  With 4 channels a
-// lane, 16-byte pieces permuted so that neither the lanes of a token nor those that add
-// the parts of several rows meet in a bank.
-template <class G>
-__device__ __forceinline__ int y_at(int t, int sl, int c) {
-  if constexpr (G::CPL == 4) return (c >> 3) * 32 + (((((c >> 2) & 1) * 4 + sl) ^ ((c >> 3) | (t & 1) << 2)) << 2);
-  else return sl * G::CW + c;
-}
 
 // What a token reads of the tiles.
 template <class G, bool LOCAL>
 struct Operands {
   F2 dt[G::CPAIRS], dx[G::CPAIRS], b[G::SPAIRS], c[G::SPAIRS];
-  __device__ __forceinline__ void read(const FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t) {
-    get_channels<G>(sm.dt[t], w.cl, dt);
-    get_channels<G>(sm.dx[t], w.cl, dx);
-    get_states<G>(sm.B[t], w.sl, b);
-    if constexpr (!LOCAL) get_states<G>(sm.C[t], w.sl, c);
+  __device__ __forceinline__ void read(const FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int k, int t) {
+    get_channels<G>(sm.dt[k][t], w.cl, dt);
+    get_channels<G>(sm.dx[k][t], w.cl, dx);
+    get_states<G>(sm.B[k][t], w.sl, b);
+    if constexpr (!LOCAL) get_states<G>(sm.C[k][t], w.sl, c);
   }
 };
 
-// One token: the states, and C . h of the lane's states.
+// One token: the states, and C . h.
 template <class G, bool LOCAL>
-__device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int t, const Operands<G, LOCAL>& o,
+__device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, int k, int t, const Operands<G, LOCAL>& o,
                                       const F2 (&A2)[G::PAIRS], F2 (&h)[G::PAIRS], F2 (&sum)[G::CPAIRS]) {
   F2 y[G::CPAIRS];
 #pragma unroll
@@ -55,26 +48,45 @@ __device__ __forceinline__ void token(FwdTiles<G, LOCAL>& sm, const Tile<G>& w, 
 #pragma unroll
     for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], o.dt[i]);
   } else {
-    float* to = sm.y[t] + y_at<G>(t, w.sl, w.cl * G::CPL);
-    if constexpr (G::CPL == 4) *reinterpret_cast<ulonglong2*>(to) = make_ulonglong2(y[0], y[1]);
-    else if constexpr (G::CPL == 2) *reinterpret_cast<F2*>(to) = y[0];
-    else *to = sum2(y[0]);
+    float f[G::CPL];
+    if constexpr (G::CPL > 1) {
+#pragma unroll
+      for (int i = 0; i < G::CPAIRS; ++i) split(y[i], f[2 * i], f[2 * i + 1]);
+    } else {
+      f[0] = sum2(y[0]);
+    }
+    const float v = over_states<G::CPL>(f, w.lane);
+    if (w.sl < G::CPL) sm.y[k][t][w.cl * G::CPL + w.sl] = v;
   }
 }
 
+// A block is two warps: one runs the states through a chunk's tokens while the other
+// stages the next chunk (dt, dt x, B and C as floats) and finishes the one before (D x,
+// the gate, the store).  Alone, a warp's phases follow one another's latencies; there
+// are too few tiles of channels for more warps to fill them.
 template <class G, bool LOCAL>
-__global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
+__global__ void __launch_bounds__(64, kResident) k_ssm(Args a, bool save) {
   using E = typename G::E;
   using U = Pairs<E, G::VN>;
   constexpr int P = G::P, VN = G::VN, VP = VN / 2;
   __shared__ FwdTiles<G, LOCAL> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
-  F2 h[G::PAIRS];
+  // Which of the two warps helps: a warp's scheduler is its slot's, and blocks of two take slots in
+  // pairs, so were it always the second, the states would run on two of the four.
+  __shared__ int swap;
+  if (threadIdx.x == 0) {
+    uint32_t slot;
+    asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+    swap = slot >> 2 & 1;
+  }
+  __syncthreads();
+  const bool helper = (threadIdx.x >= 32) != (swap != 0);
 
   if (!LOCAL && seg >= a.n_seg) {            // the states after sequences without rows
-    const int step = (gridDim.y - a.n_seg) * 32;
-    for (long long i0 = (long long)(seg - a.n_seg) * 32; i0 < a.s.n; i0 += step) {
+    F2 h[G::PAIRS];
+    const int step = (gridDim.y - a.n_seg) * 64;
+    for (long long i0 = (long long)(seg - a.n_seg) * 64 + (helper ? 32 : 0); i0 < a.s.n; i0 += step) {
       long long begin = 0, end = 1;
       if (i0 + w.lane < a.s.n) seqs::range_of(a.s, (int)(i0 + w.lane), &begin, &end);
       unsigned none = __ballot_sync(0xffffffffu, begin >= end);
@@ -90,73 +102,147 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
 
   a.s = seqs::trim(a.s);
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
-  Where q;
-  long long row = r0;
   if (r0 >= r1) {                            // rows behind the last sequence
-    if (LOCAL && blockIdx.x == 0 && w.lane == 0) a.flags[seg] = 0;
+    if (LOCAL && blockIdx.x == 0 && threadIdx.x == 0) a.flags[seg] = 0;
     return;
   }
+  Where q = seqs::find(a.s, LOCAL ? r1 - 1 : r0);
+  long long row = r0;
   if constexpr (LOCAL) {
-    q = seqs::find(a.s, r1 - 1);
     const bool cut = q.end > r1, starts = q.begin >= r0;
-    if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (starts ? kStarts : 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.flags[seg] = (cut ? kCut : 0) | (starts ? kStarts : 0);
     if (!cut) return;
     if (starts) row = q.begin;
+  }
+  const int chunks = (int)((r1 - row + kT - 1) / kT);
+
+  if (helper) {
+    F2 bias[VP], D[VP];
+    load_pairs<G>(w, a.bias, bias);
+    load_pairs<G>(w, LOCAL ? nullptr : a.D, D);
+    auto count = [&](int chunk) {
+      const long long at = row + (long long)chunk * kT;
+      return r1 - at < kT ? (int)(r1 - at) : kT;
+    };
+    auto vector = [&](const void* p, long long ld, long long r) { return static_cast<const E*>(p) + r * ld + w.c0 + w.col(); };
+    auto fetch = [&](int chunk) {
+      const long long at = row + (long long)chunk * kT;
+      const int n = count(chunk);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const bool in = w.row(k) < n && w.col() < w.cols;
+        const long long r = in ? at + w.row(k) : at;
+        copy16(&sm.raw[0][k][w.lane], in ? vector(a.x, a.ldx, r) : a.x, in);
+        copy16(&sm.raw[1][k][w.lane], in ? vector(a.delta, a.ldd, r) : a.delta, in);
+      }
+      if (a.vec_bc)
+#pragma unroll
+        for (int k = 0; k < G::BL; ++k) {
+          const int i = k * 32 + w.lane, r = i / G::BV;
+          const bool in = r < n;
+          const long long off = w.g * a.N + i % G::BV * VN;
+          copy16(&sm.rawB[0][k][w.lane], in ? static_cast<const E*>(a.B) + (at + r) * a.ldb + off : a.B, in);
+          if constexpr (!LOCAL)
+            copy16(&sm.rawB[1][k][w.lane], in ? static_cast<const E*>(a.C) + (at + r) * a.ldc + off : a.C, in);
+        }
+      copies_end();
+    };
+    auto stage = [&](int chunk) {
+      const long long at = row + (long long)chunk * kT;
+      const int n = count(chunk), to = chunk & 1;
+      copies_wait<0>();
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        F2 x[VP], dt[VP];
+        U::get(x, sm.raw[0][k][w.lane]);
+        U::get(dt, sm.raw[1][k][w.lane]);
+#pragma unroll
+        for (int e = 0; e < VP; ++e) {
+          dt[e] = softplus2(add2(dt[e], bias[e]));
+          x[e] = mul2(x[e], dt[e]);
+        }
+        if (w.row(k) < kT) {
+          put_pairs(&sm.dt[to][w.row(k)][w.col()], dt);
+          put_pairs(&sm.dx[to][w.row(k)][w.col()], x);
+        }
+      }
+      Rows<G> bv, cv;
+      if (a.vec_bc)
+#pragma unroll
+        for (int k = 0; k < G::BL; ++k) {
+          bv.v[k] = sm.rawB[0][k][w.lane];
+          if constexpr (!LOCAL) cv.v[k] = sm.rawB[1][k][w.lane];
+        }
+      bv.stage(a, w, a.B, a.ldb, at, n, sm.B[to][0]);
+      if constexpr (!LOCAL) cv.stage(a, w, a.C, a.ldc, at, n, sm.C[to][0]);
+    };
+    uint4 xv[P], zv[P];
+    auto reload = [&](int chunk) {             // x and z of a chunk that is about to be finished
+      const long long at = row + (long long)chunk * kT;
+      load_raw<G>(w, a.x, a.ldx, at, count(chunk), xv);
+      if (a.z) load_raw<G>(w, a.z, a.ldz, at, count(chunk), zv);
+    };
+    auto finish = [&](int chunk) {
+      const long long at = row + (long long)chunk * kT;
+      const int n = count(chunk);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        use_here(xv[k]);
+        if (a.z) use_here(zv[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (w.row(k) < n && w.col() < w.cols) {
+          F2 y[VP], x[VP];
+          U::get(x, xv[k]);
+          get_pairs(&sm.y[chunk & 1][w.row(k)][w.col()], y);
+#pragma unroll
+          for (int e = 0; e < VP; ++e) y[e] = fma2(D[e], x[e], y[e]);
+          if (a.z) {
+            U::get(x, zv[k]);
+#pragma unroll
+            for (int e = 0; e < VP; ++e) y[e] = mul2(y[e], mul2(x[e], sigmoid2(x[e])));
+          }
+          __stcs(reinterpret_cast<uint4*>(static_cast<E*>(a.y) + (at + w.row(k)) * a.d + w.c0 + w.col()), U::make(y));
+        }
+    };
+    fetch(0);
+    stage(0);
+    if (chunks > 1) fetch(1);
+    for (int i = 0; i < chunks; ++i) {
+      __syncthreads();                         // chunk i is staged, chunk i - 1 has been run through
+      if (!LOCAL && i > 0) reload(i - 1);
+      if (i + 1 < chunks) stage(i + 1);
+      if (i + 2 < chunks) fetch(i + 2);
+      if (!LOCAL && i > 0) finish(i - 1);
+    }
+    __syncthreads();
+    if constexpr (!LOCAL) {
+      reload(chunks - 1);
+      finish(chunks - 1);
+    }
+    return;
+  }
+
+  F2 h[G::PAIRS], A2[G::PAIRS], sum[G::CPAIRS] = {};
+  load_A<G>(a, w, A2);
+  if (LOCAL || q.begin == r0) {
 #pragma unroll
     for (int p = 0; p < G::PAIRS; ++p) h[p] = 0;
   } else {
-    q = seqs::find(a.s, r0);
-    if (q.begin < r0) load_lanes<G>(a.local, (long long)(seg - 1) * a.tiles + blockIdx.x, w.lane, h);
+    load_lanes<G>(a.local, (long long)(seg - 1) * a.tiles + blockIdx.x, w.lane, h);
   }
-  F2 A2[G::PAIRS], bias[VP], D[VP], sum[G::CPAIRS] = {};
-  load_A<G>(a, w, A2);
-  load_pairs<G>(w, a.bias, bias);
-  load_pairs<G>(w, LOCAL ? nullptr : a.D, D);
-
-  uint4 xv[P], dv[P], zv[P];
-  Rows<G> bv, cv;
-  auto fetch = [&](long long at) {
-    const int n = r1 - at < kT ? (int)(r1 - at) : kT;      // none behind the segment
-    load_raw<G>(w, a.x, a.ldx, at, n, xv);
-    load_raw<G>(w, a.delta, a.ldd, at, n, dv);
-    bv.fetch(a, w, a.B, a.ldb, at, n);
-    if (!LOCAL) cv.fetch(a, w, a.C, a.ldc, at, n);
-  };
-  fetch(row);
-  for (int chunk = 0; row < r1; row += kT, ++chunk) {
-    const int n = r1 - row < kT ? (int)(r1 - row) : kT;
+  for (int chunk = 0; chunk < chunks; ++chunk, row += kT) {
+    const int n = r1 - row < kT ? (int)(r1 - row) : kT, k = chunk & 1;
     if (!LOCAL && save) store_lanes<G>(a.ckpt, ((long long)seg * a.cps + chunk) * a.tiles + blockIdx.x, w.lane, h);
-    F2 y[P][LOCAL ? 1 : VP];                               // D x
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      F2 x[VP], dt[VP];
-      U::get(x, xv[k]);
-      U::get(dt, dv[k]);
-#pragma unroll
-      for (int e = 0; e < VP; ++e) {
-        dt[e] = softplus2(add2(dt[e], bias[e]));
-        if constexpr (!LOCAL) y[k][e] = mul2(D[e], x[e]);
-        x[e] = mul2(x[e], dt[e]);
-      }
-      if (w.row(k) < kT) {
-        put_pairs(&sm.dt[w.row(k)][w.col()], dt);
-        put_pairs(&sm.dx[w.row(k)][w.col()], x);
-      }
-    }
-    bv.stage(a, w, a.B, a.ldb, row, n, sm.B[0]);
-    if constexpr (!LOCAL) {
-      cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
-      if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
-    }
-    __syncwarp();
-    fetch(row + kT);
-    if (n == kT && q.begin < row && q.end > row + kT) {    // inside one sequence: no state comes or goes
+    __syncthreads();
+    if (n == kT && q.begin < row && q.end > row + kT) {      // inside one sequence: no state comes or goes
       Operands<G, LOCAL> now, next;
-      now.read(sm, w, 0);
-#pragma unroll 4
+      now.read(sm, w, k, 0);
+#pragma unroll
       for (int t = 0; t < kT; ++t) {
-        next.read(sm, w, t + 1 < kT ? t + 1 : t);
-        token<G, LOCAL>(sm, w, t, now, A2, h, sum);
+        next.read(sm, w, k, t + 1 < kT ? t + 1 : t);
+        token<G, LOCAL>(sm, w, k, t, now, A2, h, sum);
         now = next;
       }
     } else {
@@ -165,8 +251,8 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
         const int m = q.end - row < n ? (int)(q.end - row) : n;
         for (; t < m; ++t) {
           Operands<G, LOCAL> now;
-          now.read(sm, w, t);
-          token<G, LOCAL>(sm, w, t, now, A2, h, sum);
+          now.read(sm, w, k, t);
+          token<G, LOCAL>(sm, w, k, t, now, A2, h, sum);
         }
         if (!LOCAL && row + t == q.end) {
           if (a.final_state) store_state<G>(a, w, a.final_state, q.i, h);
@@ -174,32 +260,8 @@ __global__ void __launch_bounds__(32, kResident) k_ssm(Args a, bool save) {
         }
       }
     }
-    __syncwarp();
-    if constexpr (!LOCAL) {
-#pragma unroll
-      for (int k = 0; k < P; ++k)
-        if (w.row(k) < n && w.col() < w.cols) {
-          F2 z[VP];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-#pragma unroll
-            for (int e = 0; e < VP; e += 2) {
-              const float* part = sm.y[w.row(k)] + y_at<G>(w.row(k), s, w.col() + 2 * e);
-              const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(part);
-              y[k][e] = add2(y[k][e], u.x);
-              y[k][e + 1] = add2(y[k][e + 1], u.y);
-            }
-          }
-          if (a.z) {
-            U::get(z, zv[k]);
-#pragma unroll
-            for (int e = 0; e < VP; ++e) y[k][e] = mul2(y[k][e], mul2(z[e], sigmoid2(z[e])));
-          }
-          E* to = static_cast<E*>(a.y) + (row + w.row(k)) * a.d + w.c0 + w.col();
-          __stcs(reinterpret_cast<uint4*>(to), U::make(y[k]));
-        }
-    }
   }
+  __syncthreads();
   if constexpr (LOCAL) {
     const long long block = (long long)seg * a.tiles + blockIdx.x;
     store_lanes<G>(a.local, block, w.lane, h);
@@ -212,7 +274,7 @@ static cudaError_t forward(const Args& a, const Plan& p, bool save, cudaStream_t
   if (p.cut) {
     {
       TraceScope tr("k_ssm_local", st);
-      k_ssm<G, true><<<dim3(a.tiles, a.n_seg), 32, 0, st>>>(a, false);
+      k_ssm<G, true><<<dim3(a.tiles, a.n_seg), 64, 0, st>>>(a, false);
     }
     const cudaError_t e = launch_ssm_carry<G, false>(a, st);
     if (e != cudaSuccess) return e;
@@ -222,7 +284,7 @@ static cudaError_t forward(const Args& a, const Plan& p, bool save, cudaStream_t
   const int more = empty ? (a.s.n < 32 * 64 ? (a.s.n + 31) / 32 : 64) : 0;
   if (a.n_seg + more == 0) return cudaSuccess;
   TraceScope tr("k_ssm", st);
-  k_ssm<G, false><<<dim3(a.tiles, a.n_seg + more), 32, 0, st>>>(a, save);
+  k_ssm<G, false><<<dim3(a.tiles, a.n_seg + more), 64, 0, st>>>(a, save);
   return cudaGetLastError();
 }
 

@@ -95,6 +95,9 @@ __device__ __forceinline__ uint4 load_here(const void* p, bool on = true) {
   return v;
 }
 
+// What was read ahead may be used from here on, and not before: the compiler would move its
+// unpacking up to the read, and the wait for it with it.
+__device__ __forceinline__ void use_here(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
 __device__ __forceinline__ uint2 load_here8(const void* p, bool on = true) {
   uint2 v;
   asm volatile(

@@ -32,7 +32,7 @@ using namespace pairs;
 using seqs::Seqs;
 using seqs::Where;
 
-constexpr int kResident = 12;                  // warps of an SM at once
+constexpr int kResident = 8;                   // blocks of an SM at once, forward
 constexpr int kT = 16;                       // rows of a chunk
 
 struct Args {
@@ -296,6 +296,35 @@ __device__ __forceinline__ void store_sums(const Args& a, long long block, int l
   }
 }
 
+// One value of each lane's quarter: v[i] summed over the lanes of a group of 4
+// (M = 1, 2) or 8 (M = 4, 8, 16), value i of N ending up in the lanes whose bits of M say i.
+template <int N>
+__device__ __forceinline__ void fold(float (&v)[N], int lane, int m) {
+  const bool up = lane & m;
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float keep = up ? v[2 * i + 1] : v[2 * i], send = up ? v[2 * i] : v[2 * i + 1];
+    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+  }
+}
+template <int N>
+__device__ __forceinline__ float all(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
+
+// Sums over the 4 state lanes of v[CPL]: lane sl has channel sl % CPL's.
+template <int CPL>
+__device__ __forceinline__ float over_states(float (&v)[CPL], int lane) {
+  if constexpr (CPL == 4) {
+    fold<4>(v, lane, 1);
+    float u[2] = {v[0], v[1]};
+    fold<2>(u, lane, 2);
+    return u[0];
+  } else if constexpr (CPL == 2) {
+    fold<2>(v, lane, 1);
+    return all<1>(v[0], 2);
+  } else {
+    return all<1>(all<1>(v[0], 1), 2);
+  }
+}
 // A chunk's rows of B or C: fetched into registers ahead (whole vectors), or element
 // by element when they are put into the tile [kT][NP].
 template <class G>
