@@ -5,7 +5,7 @@
 //
 // Memory is the bound: one operation a value.  The tensors are cut into items of
 // kItem values that a fixed grid takes in turn; the table of tensors is a kernel
-// parameter, so a captured launch keeps it.  A thread adds the squares of its 64
+// parameter, so a captured launch keeps it.  A thread adds the squares of its 128
 // values of an item in fp32, its items in 64 bits, and a block writes one sum: no
 // atomics, and an order that depends on the sizes alone.  Every block of the second
 // kernel adds those sums in the same order, which costs it a few kilobytes from L2
@@ -17,8 +17,9 @@ namespace cfc {
 namespace clip {
 
 constexpr int kThreads = 256;
-constexpr int kItem = 16384;
+constexpr int kItem = 32768;
 constexpr int kMaxBlocks = 6 * kNumSMs;          // partial sums of a launch
+constexpr int kScaleBlocks = 8 * kNumSMs;
 
 enum : uint8_t { kBf16 = 1, kVector = 2 };       // what a tensor's flag says
 
@@ -186,9 +187,9 @@ static cudaError_t tables(const void* const* in, void* const* out, const long lo
 }
 
 template <int MAX>
-static int grid_of(const Table<MAX>& t) {
+static int grid_of(const Table<MAX>& t, int most) {
   const int items = t.first[t.count];
-  return items < 1 ? 1 : items < kMaxBlocks ? items : kMaxBlocks;
+  return items < 1 ? 1 : items < most ? items : most;
 }
 
 template <int MAX>
@@ -198,15 +199,15 @@ static cudaError_t run(const void* const* in, void* const* out, const long long*
   cudaError_t e = tables<MAX>(in, out, n, math, count, [&](const Table<MAX>& t) {
     if (t.count == 0) return cudaSuccess;
     TraceScope tr("k_grad_squares", st);
-    k_grad_squares<MAX><<<grid_of(t), kThreads, 0, st>>>(t, sums + n_sums);
-    n_sums += grid_of(t);
+    k_grad_squares<MAX><<<grid_of(t, kMaxBlocks), kThreads, 0, st>>>(t, sums + n_sums);
+    n_sums += grid_of(t, kMaxBlocks);
     return cudaGetLastError();
   });
   if (e != cudaSuccess) return e;
   // (no table: one block that writes the norm)
   return tables<MAX>(in, out, n, math, out ? count : 0, [&](const Table<MAX>& t) {
     TraceScope tr("k_grad_scale", st);
-    k_grad_scale<MAX><<<grid_of(t), kThreads, 0, st>>>(t, sums, n_sums, most, norm);
+    k_grad_scale<MAX><<<grid_of(t, kScaleBlocks), kThreads, 0, st>>>(t, sums, n_sums, most, norm);
     return cudaGetLastError();
   });
 }

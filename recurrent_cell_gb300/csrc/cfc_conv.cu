@@ -38,7 +38,7 @@ struct Args {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 4;
-constexpr int kTileFwd = 64;                 // rows of a forward tile
+constexpr int kTileFwd = 128;                // rows of a forward tile
 
 // A thread's channels: N of type E, as pairs.
 template <class E_, int N_>
@@ -511,9 +511,12 @@ template <class C> struct Step {
   }
 };
 
-// Rows of a backward tile: about 16 warps of threads an SM.
-static int bwd_tile(long long rows, int d) {
-  const long long tiles = (16ll * 32 * kNumSMs + d / 4 - 1) / (d / 4);
+// Rows of a backward tile: as many threads as the GPU holds at once, 12 warps an SM up to 5
+// weights a channel and 8 beyond, by their registers (16384 x 4096 in bf16, 4 weights: 12
+// warps 92 us, 16, a second round of blocks, 116).
+static int bwd_tile(long long rows, int d, int width) {
+  const long long warps = width <= 5 ? 12 : 8;
+  const long long tiles = (warps * 32 * kNumSMs + d / 4 - 1) / (d / 4);
   const long long n = (rows + tiles - 1) / tiles;
   return n < 16 ? 16 : (int)n;
 }
@@ -528,7 +531,7 @@ static Args args_of(const ConvArgs& g) {
 }  // namespace conv
 
 size_t conv_workspace(long long rows, int d, int width) {
-  const int tile = conv::bwd_tile(rows, d);
+  const int tile = conv::bwd_tile(rows, d, width);
   const long long n = (rows + tile - 1) / tile;
   return ((size_t)(n > 0 ? n : 1) * (width + 1) * d * 4 + 255) & ~size_t(255);
 }
@@ -551,7 +554,7 @@ cudaError_t launch_conv_backward(const ConvArgs& g, const void* grad_y, const vo
   a.grad_x = grad_x;
   a.grad_init = grad_init;
   a.part = part;
-  a.tile = conv::bwd_tile(g.rows, g.d);
+  a.tile = conv::bwd_tile(g.rows, g.d, g.width);
   a.n_tiles = (int)((g.rows + a.tile - 1) / a.tile);
   const cudaError_t e = g.math == CFC_MATH_BF16
                             ? conv::by_width(g.width, conv::Backward<conv::Chan<__nv_bfloat16, 4>>{a, st})

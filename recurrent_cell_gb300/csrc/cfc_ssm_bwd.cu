@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
       {
         Token<G, false> k, ahead;
         k.read(sm, w, 0);
-#pragma unroll 5
+#pragma unroll
         for (int t = 0; t < kT - 1; ++t) {
           ahead.read(sm, w, t + 1);
           tmem_put(states + t * 2 * PAIRS, h);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) k_ssm_bwd(Args a) {
       }
       Token<G, true> k, ahead;
       k.read(sm, w, kT - 1);
-#pragma unroll 2
+#pragma unroll 4
       for (int t = kT - 1; t >= 0; --t) {
         ahead.read(sm, w, t > 0 ? t - 1 : 0);
         if (t < kT - 1) tmem_get(states + t * 2 * PAIRS, h);

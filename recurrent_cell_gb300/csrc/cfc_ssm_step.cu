@@ -55,54 +55,37 @@ __global__ void __launch_bounds__(kStepThreads) k_ssm_step(StepArgs g) {
   const bool in = c0 + lane < a.d;
   const float bias = a.bias && in ? __ldg(a.bias + c0 + lane) : 0.f, D = a.D && in ? __ldg(a.D + c0 + lane) : 0.f;
   const bool one = c0 / a.per == (min(c0 + 31, a.d - 1)) / a.per;      // one group's channels
-  // this lane's states are of channels c0 + 8 k + cl; those of the next sequence are read ahead
-  const long long step = 8ll * a.N, mine = (long long)(c0 + cl) * a.N + sl * NS;
-  const long long last = first + g.each < a.s.n ? first + g.each : a.s.n;
-  auto slot_of = [&](long long seq) -> long long {
-    if (seq >= last) return -1;
-    const long long s = g.slots ? __ldg(g.slots + seq) : seq;
-    return s < g.n_slots ? s : -1;
-  };
-  auto load = [&](long long slot, float (&h)[4][NS]) {
-    const float* st = g.state + (slot < 0 ? 0 : slot) * a.d * a.N + mine;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool on = slot >= 0 && c0 + 8 * k < a.d;
-      if constexpr (VEC) {
-#pragma unroll
-        for (int j = 0; j < NS; j += NS >= 4 ? 4 : 2) {
-          if constexpr (NS >= 4) {
-            const uint4 v = load_here(st + k * step + j, on);
-            h[k][j] = __uint_as_float(v.x); h[k][j + 1] = __uint_as_float(v.y);
-            h[k][j + 2] = __uint_as_float(v.z); h[k][j + 3] = __uint_as_float(v.w);
-          } else {
-            const uint2 v = load_here8(st + k * step + j, on);
-            h[k][j] = __uint_as_float(v.x); h[k][j + 1] = __uint_as_float(v.y);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NS; ++j) h[k][j] = on && j < left ? __ldg(st + k * step + j) : 0.f;
-      }
-    }
-  };
-  float h[4][NS], ahead[4][NS];
-  long long slot = slot_of(first), next = slot_of(first + 1);
-  load(slot, ahead);
-  for (long long seq = first; seq < last; ++seq, slot = next, next = slot_of(seq + 1)) {
-    const long long row0 = seq * g.tokens;
+  for (long long seq = first; seq < first + g.each && seq < a.s.n; ++seq) {
+    const long long slot = g.slots ? g.slots[seq] : seq, row0 = seq * g.tokens;
     E* y = static_cast<E*>(a.y) + row0 * a.d + c0 + lane;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int j = 0; j < NS; ++j) h[k][j] = ahead[k][j];
-    load(next, ahead);
-    if (slot < 0) {                            // a sequence without a state: zeros out, nothing kept
+    if (slot < 0 || slot >= g.n_slots) {       // a sequence without a state: zeros out, nothing kept
       for (int t = 0; t < g.tokens; ++t)
         if (in) rows::store1(y + (long long)t * a.d, 0.f);
       continue;
     }
-    float* st = g.state + slot * a.d * a.N + mine;
+    // this lane's channels are c0 + 8 k + cl
+    float* st = g.state + (slot * a.d + c0 + cl) * a.N + sl * NS;
+    const long long step = 8ll * a.N;
+    float h[4][NS];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool on = c0 + 8 * k < a.d;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < NS; j += NS >= 4 ? 4 : 2) {
+          if constexpr (NS >= 4) {
+            const float4 v = on ? __ldcs(reinterpret_cast<const float4*>(st + k * step + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            h[k][j] = v.x; h[k][j + 1] = v.y; h[k][j + 2] = v.z; h[k][j + 3] = v.w;
+          } else {
+            const float2 v = on ? __ldcs(reinterpret_cast<const float2*>(st + k * step + j)) : make_float2(0.f, 0.f);
+            h[k][j] = v.x; h[k][j + 1] = v.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) h[k][j] = on && j < left ? st[k * step + j] : 0.f;
+      }
+    }
     for (int t = 0; t < g.tokens; ++t) {
       const long long row = row0 + t;
       float x = 0.f, dt = 0.f, gate = 1.f;
@@ -198,8 +181,8 @@ cudaError_t launch_ssm_step(const SsmArgs& g, int tokens, float* state, long lon
   s.a.y = y;
   s.state = state; s.slots = slots; s.n_slots = n_slots; s.tokens = tokens;
   s.tiles = (g.d + 31) / 32;
-  const long long each = ((long long)g.n_seq * s.tiles + 16 * kNumSMs - 1) / (16 * kNumSMs);      // 16 warps an SM
-  s.each = each < 1 ? 1 : each > 64 ? 64 : (int)each;
+  const long long each = (long long)g.n_seq * s.tiles / (32 * kNumSMs);
+  s.each = each < 1 ? 1 : each > 8 ? 8 : (int)each;
   return g.math == CFC_MATH_BF16 ? ssm::step<__nv_bfloat16>(s, st) : ssm::step<float>(s, st);
 }
 

@@ -1,6 +1,6 @@
 """The norm of many gradients together and clipping, on the GPU against 64 bits.
 
-Tolerances.  A thread adds 64 squares in fp32 (64 x 2^-24 / 2 = 2e-6 of their sum at worst, 2e-7 in practice) and the
+Tolerances.  A thread adds 128 squares in fp32, 32 of them in a row (32 x 2^-24 = 2e-6 of their sum at worst, 2e-7 in practice) and the
 rest in 64 bits; the root halves it: 2e-6 on the norm.  The factor carries that and two roundings, the product one more:
 2.5e-6 relative in fp32, in bf16 half a step, 2^-8, on top."""
 
