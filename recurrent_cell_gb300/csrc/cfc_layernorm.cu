@@ -35,53 +35,61 @@ struct Args {
   float eps;
 };
 
-// Arithmetic on a vector's values, two at a time where there are two: r = a op b.
-template <int N, class F2op, class F1op>
-__device__ __forceinline__ void each(F2op two, F1op one) {
-  if constexpr (N == 1) {
-    one(0);
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; e += 2) two(e);
-  }
-}
+// A vector's values as the arithmetic takes them: pairs, or (rows of no whole vectors)
+// one float.
 using pairs::F2;
-template <int N> __device__ __forceinline__ F2 at2(const float (&f)[N], int e) { return pairs::pack(f[e], f[(e + 1) % N]); }
-template <int N> __device__ __forceinline__ void to2(float (&f)[N], int e, F2 v) { pairs::split(v, f[e], f[(e + 1) % N]); }
-template <int N>
-__device__ __forceinline__ void add(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
-  each<N>([&](int e) { to2(r, e, pairs::add2(at2(a, e), at2(b, e))); }, [&](int) { r[0] = a[0] + b[0]; });
+template <class V>
+struct Vals {
+  using X = F2;
+  static constexpr int H = V::N / 2;
+  using P = pairs::Pairs<typename V::E, V::N>;
+  __device__ static __forceinline__ void get(F2 (&f)[H], const typename V::T& v) { P::get(f, *reinterpret_cast<const uint4*>(&v)); }
+  __device__ static __forceinline__ typename V::T make(const F2 (&f)[H]) {
+    const uint4 u = P::make(f);
+    return *reinterpret_cast<const typename V::T*>(&u);
+  }
+};
+template <class E>
+struct Vals<Vec<E, 1>> {
+  using X = float;
+  static constexpr int H = 1;
+  __device__ static __forceinline__ void get(float (&f)[1], const typename Vec<E, 1>::T& v) { Vec<E, 1>::get(f, v); }
+  __device__ static __forceinline__ typename Vec<E, 1>::T make(const float (&f)[1]) { return Vec<E, 1>::make(f); }
+};
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) { return pairs::add2(a, b); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b) { return pairs::mul2(a, b); }
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) { return pairs::fma2(a, b, c); }
+template <class X> __device__ __forceinline__ X all(float v) {
+  if constexpr (sizeof(X) == 8) return pairs::twice(v);
+  else return v;
 }
-template <int N>
-__device__ __forceinline__ void add(float (&r)[N], const float (&a)[N], float b) {
-  each<N>([&](int e) { to2(r, e, pairs::add2(at2(a, e), pairs::twice(b))); }, [&](int) { r[0] = a[0] + b; });
-}
-template <int N>
-__device__ __forceinline__ void mul(float (&r)[N], const float (&a)[N], float b) {
-  each<N>([&](int e) { to2(r, e, pairs::mul2(at2(a, e), pairs::twice(b))); }, [&](int) { r[0] = a[0] * b; });
-}
-template <int N>
-__device__ __forceinline__ void mul(float (&r)[N], const float (&a)[N], const float (&b)[N]) {
-  each<N>([&](int e) { to2(r, e, pairs::mul2(at2(a, e), at2(b, e))); }, [&](int) { r[0] = a[0] * b[0]; });
-}
-template <int N>
-__device__ __forceinline__ void fma(float (&r)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
-  each<N>([&](int e) { to2(r, e, pairs::fma2(at2(a, e), at2(b, e), at2(c, e))); }, [&](int) { r[0] = fmaf(a[0], b[0], c[0]); });
-}
-template <int N>
-__device__ __forceinline__ void fma(float (&r)[N], const float (&a)[N], float b, const float (&c)[N]) {
-  each<N>([&](int e) { to2(r, e, pairs::fma2(at2(a, e), pairs::twice(b), at2(c, e))); }, [&](int) { r[0] = fmaf(a[0], b, c[0]); });
-}
-template <int N>
-__device__ __forceinline__ float sum(const float (&a)[N]) {
-  float s[N];
+template <int H> __device__ __forceinline__ float sum(const F2 (&a)[H]) {
+  F2 s[H];
 #pragma unroll
-  for (int e = 0; e < N; ++e) s[e] = a[e];
+  for (int e = 0; e < H; ++e) s[e] = a[e];
 #pragma unroll
-  for (int m = N / 2; m > 0; m >>= 1)
+  for (int m = H / 2; m > 0; m >>= 1)
 #pragma unroll
-    for (int e = 0; e < m; ++e) s[e] += s[e + m];
-  return s[0];
+    for (int e = 0; e < m; ++e) s[e] = pairs::add2(s[e], s[e + m]);
+  return pairs::sum2(s[0]);
+}
+template <int H> __device__ __forceinline__ float sum(const float (&a)[H]) { return a[0]; }
+// A row's weights of a thread.
+template <class V, int NV, int LANES>
+__device__ __forceinline__ void weights(const Row<V, NV, LANES>& r, typename Vals<V>::X (&w)[NV][Vals<V>::H], const float* p) {
+  float f[NV][V::N];
+  r.weights(f, p);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if constexpr (V::N == 1) {
+      w[j][0] = f[j][0];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V::N / 2; ++e) w[j][e] = pairs::pack(f[j][2 * e], f[j][2 * e + 1]);
+    }
 }
 
 // Two sums over a row at once, after the manner of over_row.
@@ -157,6 +165,11 @@ struct Ahead {
 #pragma unroll
     for (int s = 0; s < (RING ? STAGES - 1 : 1); ++s) fetch(r, row + s * step < rows, step * r.nvec, s);
   }
+  // The row at hand once more, after next() (k, j: of its tensors and vectors).
+  __device__ __forceinline__ T again(const T (&v)[K][NV], int k, int j) const {
+    if constexpr (RING) return *reinterpret_cast<const T*>(at(stage == 0 ? STAGES - 1 : stage - 1, k, j));
+    else return v[k][j];
+  }
   // The row at hand into v; the row STAGES - 1 (1) steps on is sent for.
   __device__ __forceinline__ void next(const R& r, long long row, long long step, long long rows, T (&v)[K][NV]) {
     if constexpr (RING) {
@@ -182,18 +195,19 @@ template <class V, int NV, int LANES> using FwdAhead = Ahead<V, NV, LANES, 2, 3>
 template <class V, int NV, int LANES> using BwdAhead = Ahead<V, NV, LANES, 3, (NV > 2 ? 2 : 3)>;
 
 template <class V, int NV, int LANES>
-__global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm(Args a) {
+__global__ void __launch_bounds__(LANES ? kLaneThreads : V::N > 1 && NV <= 2 ? 640 : 512) k_layernorm(Args a) {
   using R = Row<V, NV, LANES>;
   using E = typename V::E;
   using T = typename V::T;
-  constexpr int N = V::N, RPB = kRows<LANES>;
+  using X = typename Vals<V>::X;
+  constexpr int H = Vals<V>::H, RPB = kRows<LANES>;
   __shared__ Part part_;
   int turn = 0;
   if (!LANES) part_.clear();
   const R r(a.d);
-  float w[NV][N], b[NV][N] = {};
-  r.weights(w, a.w);
-  if (LANES && a.b) r.weights(b, a.b);
+  X w[NV][H], b[NV][H] = {};
+  weights<V, NV, LANES>(r, w, a.w);
+  if (LANES && a.b) weights<V, NV, LANES>(r, b, a.b);
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
@@ -207,35 +221,39 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm(Args a
     const bool on = row < a.rows;
     T v[2][NV];
     ahead.next(r, row, step, a.rows, v);
-    float s[NV][N], part[N] = {};
+    X s[NV][H], part[H] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) s[j][e] = 0.f;
+      for (int e = 0; e < H; ++e) s[j][e] = 0;
       if (on && r.in(j)) {
-        V::get(s[j], v[0][j]);
+        Vals<V>::get(s[j], v[0][j]);
         T stored = v[0][j];
         if (a.residual) {
-          float t[N];
-          V::get(t, v[1][j]);
-          add(t, s[j], t);
-          stored = V::make(t);               // rounded once, for the store and for what follows
-          V::get(s[j], stored);
+          X t[H];
+          Vals<V>::get(t, v[1][j]);
+#pragma unroll
+          for (int e = 0; e < H; ++e) t[e] = add(s[j][e], t[e]);
+          stored = Vals<V>::make(t);         // rounded once, for the store and for what follows
+          Vals<V>::get(s[j], stored);
         }
         if (a.s_out) __stcs(reinterpret_cast<T*>(static_cast<E*>(a.s_out) + row * a.d) + r.at(j), stored);
       }
-      add(part, part, s[j]);
+#pragma unroll
+      for (int e = 0; e < H; ++e) part[e] = add(part[e], s[j][e]);
     }
     const float mean = over_row<Sum, LANES>(sum(part), part_, turn) * inv_d;
-    float sq[N] = {};
+    X sq[H] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (r.in(j)) {
-        add(s[j], s[j], -mean);
-        fma(sq, s[j], s[j], sq);
-      }
+      if (r.in(j))
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          s[j][e] = add(s[j][e], all<X>(-mean));
+          sq[e] = fma(s[j][e], s[j][e], sq[e]);
+        }
     const float var = over_row<Sum, LANES>(sum(sq), part_, turn);
-    if (!LANES && a.b) r.weights(b, a.b);        // from L1: kept, it would spill
+    if (!LANES && a.b) weights<V, NV, LANES>(r, b, a.b);     // from L1: kept, it would spill
     const float rstd = 1.f / sqrtf(fmaf(var, inv_d, a.eps));
     if (on && r.l == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -244,26 +262,27 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm(Args a
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-        mul(s[j], s[j], rstd);
-        fma(s[j], s[j], w[j], b[j]);
-        __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), V::make(s[j]));
+#pragma unroll
+        for (int e = 0; e < H; ++e) s[j][e] = fma(mul(s[j][e], all<X>(rstd)), w[j][e], b[j][e]);
+        __stcs(reinterpret_cast<T*>(static_cast<E*>(a.y) + row * a.d) + r.at(j), Vals<V>::make(s[j]));
       }
   }
 }
 
 template <class V, int NV, int LANES>
-__global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm_bwd(Args a) {
+__global__ void __launch_bounds__(LANES ? kLaneThreads : V::N > 1 ? 640 : 512) k_layernorm_bwd(Args a) {
   using R = Row<V, NV, LANES>;
   using E = typename V::E;
   using T = typename V::T;
-  constexpr int N = V::N, RPB = kRows<LANES>;
+  using X = typename Vals<V>::X;
+  constexpr int N = V::N, H = Vals<V>::H, RPB = kRows<LANES>;
   extern __shared__ __align__(16) float sums[];  // the rows ahead; in the end [RPB][d] where a block has several rows
   __shared__ Part2 part;
   int turn = 0;
   if (!LANES) part.clear();
   const R r(a.d);
-  float w[NV][N], gw[NV][N] = {}, gb[NV][N] = {};
-  r.weights(w, a.w);
+  X w[NV][H], gwx[NV][H] = {}, gbx[NV][H] = {};
+  weights<V, NV, LANES>(r, w, a.w);
   const float inv_d = 1.f / (float)a.d;
   const long long step = (long long)gridDim.x * RPB;
   long long row = (long long)blockIdx.x * RPB + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
@@ -271,54 +290,73 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : 512) k_layernorm_bwd(Ar
   ahead.base = reinterpret_cast<unsigned char*>(sums);
   const void* const in[3] = {a.x, a.grad_y, a.grad_s};
   ahead.start(r, in, row, step, a.rows, a.d);
-  float mean = 0.f, rstd = 0.f;
+  float mean, rstd;
   auto scalars = [&](long long row) {
-    if (row < a.rows) {
-      mean = a.mean_in[row];
-      rstd = a.rstd_in[row];
-    }
+    mean = pairs::load_here4(a.mean_in + row, row < a.rows);
+    rstd = pairs::load_here4(a.rstd_in + row, row < a.rows);
   };
   scalars(row);
   for (long long first = (long long)blockIdx.x * RPB; first < a.rows; first += step, row += step) {
     const bool on = row < a.rows;
-    const long long at = row * a.d;
-    const float rs = rstd, mu = mean;
+    pairs::use_here(mean);
+    pairs::use_here(rstd);
+    const float rs = rstd;
+    const X mu = all<X>(-mean), rx = all<X>(rstd);
     T v[3][NV];
     ahead.next(r, row, step, a.rows, v);
     scalars(row + step);
-    // n = (s - mean) rstd, dn = grad_y w
-    float sn[N] = {}, sg[N] = {}, n[NV][N], g[NV][N];
+    // n = (s - mean) rstd, dn = grad_y w; formed twice, from shared memory, rather than kept: with 96
+    // registers a block of 5 warps fits an SM four times, with 128 three times
+    X sn[H] = {}, sg[H] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-        V::get(n[j], v[0][j]);
-        V::get(g[j], v[1][j]);
-        add(gb[j], gb[j], g[j]);
-        add(n[j], n[j], -mu);
-        mul(n[j], n[j], rs);
-        fma(gw[j], g[j], n[j], gw[j]);
-        mul(g[j], g[j], w[j]);
-        add(sg, sg, g[j]);
-        fma(sn, g[j], n[j], sn);
+        X n[H], g[H];
+        Vals<V>::get(n, v[0][j]);
+        Vals<V>::get(g, v[1][j]);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          gbx[j][e] = add(gbx[j][e], g[e]);
+          n[e] = mul(add(n[e], mu), rx);
+          gwx[j][e] = fma(g[e], n[e], gwx[j][e]);
+          g[e] = mul(g[e], w[j][e]);
+          sg[e] = add(sg[e], g[e]);
+          sn[e] = fma(g[e], n[e], sn[e]);
+        }
       }
     const float2 dot = over_row2<LANES>(make_float2(sum(sg), sum(sn)), part, turn);
-    const float k = -rs * (dot.y * inv_d), l = -rs * (dot.x * inv_d);
+    // rs (dn - mean(dn) - n mean(dn n)) = rs dn + k (s - mu) + l
+    const X k = all<X>(-rs * rs * (dot.y * inv_d)), l = all<X>(-rs * (dot.x * inv_d));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (on && r.in(j)) {
-        float o[N];
+        X n[H], g[H], o[H];
+        Vals<V>::get(n, ahead.again(v, 0, j));
+        Vals<V>::get(g, ahead.again(v, 1, j));
 #pragma unroll
-        for (int e = 0; e < N; ++e) o[e] = l;
-        fma(o, n[j], k, o);
-        fma(o, g[j], rs, o);
+        for (int e = 0; e < H; ++e) o[e] = fma(mul(g[e], w[j][e]), rx, fma(add(n[e], mu), k, l));
         if (a.grad_s) {
-          float t[N];
-          V::get(t, v[2][j]);
-          add(o, o, t);
+          X t[H];
+          Vals<V>::get(t, ahead.again(v, 2, j));
+#pragma unroll
+          for (int e = 0; e < H; ++e) o[e] = add(o[e], t[e]);
         }
-        __stcs(reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + at) + r.at(j), V::make(o));
+        __stcs(reinterpret_cast<T*>(static_cast<E*>(a.grad_x) + row * a.d) + r.at(j), Vals<V>::make(o));
       }
   }
+  float gw[NV][N], gb[NV][N];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if constexpr (N == 1) {
+      gw[j][0] = gwx[j][0];
+      gb[j][0] = gbx[j][0];
+    } else {
+#pragma unroll
+      for (int e = 0; e < H; ++e) {
+        pairs::split(gwx[j][e], gw[j][2 * e], gw[j][2 * e + 1]);
+        pairs::split(gbx[j][e], gb[j][2 * e], gb[j][2 * e + 1]);
+      }
+    }
   if constexpr (BwdAhead<V, NV, LANES>::RING) pairs::copies_wait<0>();
   // The block's row of partial sums [grad_w | grad_b], its rows' lanes in order.
   float* out = a.part + (long long)blockIdx.x * 2 * a.d;

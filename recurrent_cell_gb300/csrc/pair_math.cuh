@@ -98,6 +98,14 @@ __device__ __forceinline__ uint4 load_here(const void* p, bool on = true) {
 // What was read ahead may be used from here on, and not before: the compiler would move its
 // unpacking up to the read, and the wait for it with it.
 __device__ __forceinline__ void use_here(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+__device__ __forceinline__ void use_here(float& v) { asm volatile("" : "+f"(v)); }
+__device__ __forceinline__ float load_here4(const float* p, bool on = true) {
+  float v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.nc.f32 %0, [%1];\n}"
+               : "=&f"(v)
+               : "l"(p), "r"((int)on));
+  return v;
+}
 __device__ __forceinline__ uint2 load_here8(const void* p, bool on = true) {
   uint2 v;
   asm volatile(
