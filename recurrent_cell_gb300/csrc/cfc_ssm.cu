@@ -5,7 +5,13 @@
 //   k_ssm_carry      the states between segments: h_s = local_s + exp(A sum dt) h_{s-1}
 //   k_ssm<., false>  the scan itself
 //
-// The first two run only where segments cut sequences.
+// The first two run only where segments cut sequences.  The third is bound by instructions and
+// their latencies, not by memory: with 16 states a thread has 16 exponentials (4 cycles of a
+// scheduler each) and 32 multiply-adds of pairs (2) a token, 122 instructions with the reads and the sums,
+// and two such warps a scheduler issue 56 % of its cycles.  More warps have no room: at 128
+// registers it took 235 us where it now takes 168, partial sums of y through shared memory instead of
+// lane steps 182.  bfloat16, 16 states: 1 x 16384 rows x 2048 channels 115 + 8 + 168 us,
+// 8 x 2048 x 4096 (whole) 389 us.
 #include "ssm_common.cuh"
 
 namespace cfc {

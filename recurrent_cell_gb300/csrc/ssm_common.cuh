@@ -6,12 +6,12 @@
 //   y = (C . h + D x) silu(z),
 // B and C [N] shared by the channels of a group.
 //
-// A warp takes a tile of channels of one group over a segment of rows: 4 lanes
+// A warp runs a tile of channels of one group over a segment of rows: 4 lanes
 // share a channel's states and 8 lanes the tile's channels, so a thread keeps
 // CPL channels x NS states in registers and sums over states need two lane steps,
 // sums over channels three.  Rows go by chunks of kT: what depends on a token and
-// channel alone (softplus, dt x, the gate) is formed once by whichever lane loaded
-// it, through shared memory; the loop over tokens is left with an exponential and
+// channel alone (softplus, dt x, the gate) is formed once, by a second warp and through
+// shared memory; the loop over tokens is left with an exponential and
 // four multiply-adds a state.
 //
 // Segments are ranges of the rows of all sequences together, whatever the sequences'
@@ -32,7 +32,7 @@ using namespace pairs;
 using seqs::Seqs;
 using seqs::Where;
 
-constexpr int kResident = 8;                   // blocks of an SM at once, forward
+constexpr int kResident = 8;                 // blocks of an SM at once, forward
 constexpr int kT = 16;                       // rows of a chunk
 
 struct Args {
@@ -296,8 +296,8 @@ __device__ __forceinline__ void store_sums(const Args& a, long long block, int l
   }
 }
 
-// One value of each lane's quarter: v[i] summed over the lanes of a group of 4
-// (M = 1, 2) or 8 (M = 4, 8, 16), value i of N ending up in the lanes whose bits of M say i.
+// Half of a sum over lanes: v[2 i] plus the lane across m's for lanes without that bit, v[2 i + 1] for those
+// with it, in v[i].
 template <int N>
 __device__ __forceinline__ void fold(float (&v)[N], int lane, int m) {
   const bool up = lane & m;
@@ -408,16 +408,20 @@ static cudaError_t launch_ssm_carry(const Args& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The plan: rows of a segment, segments, channels of a tile.  Enough warps for every SM
-// (kWarps in all) where sequences are long enough; sequences of one length stay whole
-// where there are kEnough of them and their tiles, since the pass that hands states on costs
-// about as much as half of the scan.
+// The plan: rows of a segment, segments, channels of a tile.  Cut into segments, every SM has its
+// kResident warps, but the pass that hands states on costs half as much again as the scan, and two
+// launches more; whole, a sequence takes the latency of all its tokens.  So sequences of one length
+// stay whole where there are kEnough of them and their tiles, and earlier the shorter they are.
+// Measured, bfloat16, 16 states, whole | cut in us: 2048 tokens with 256 tiles in all 187 | 166,
+// 384 221 | 234, 576 226 | 331; 512 tokens with 160 56 | 53, 256 58 | 66, 512 67 | 103; 128 tokens
+// with 160 26 | 41.
 struct Plan {
   int NS, CPL, tpg, tiles, n_seg, cps;
   long long S;
   bool cut;
 };
-constexpr long long kPlanWarps = (long long)kResident * kNumSMs, kPlanEnough = 4ll * kNumSMs;
+constexpr long long kPlanWarps = (long long)kResident * kNumSMs, kPlanEnough = 5ll * kNumSMs / 2,
+                    kPlanShort = 100000;     // tokens x tiles that the launches and the handing on are worth
 inline Plan make_plan(long long rows, int n_seq, int d, int groups, int N, bool packed) {
   Plan p{};
   p.NS = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16;
@@ -428,7 +432,7 @@ inline Plan make_plan(long long rows, int n_seq, int d, int groups, int N, bool 
   const long long tokens = packed || n_seq == 0 ? 0 : rows / n_seq;
   if (rows <= 0) {
     p.S = kT;
-  } else if (tokens > 0 && n_seq * (long long)p.tiles >= kPlanEnough) {
+  } else if (tokens > 0 && n_seq * (long long)p.tiles * tokens >= kPlanEnough * tokens - kPlanShort) {
     long long k = n_seq * (long long)p.tiles / kPlanWarps;
     p.S = tokens * (k < 1 ? 1 : k);
   } else {

@@ -136,6 +136,13 @@ def test_uniform_sequences(n, t, math):
 
 
 @MODES
+@pytest.mark.parametrize("n,t,d", [(1, 700, 32), (2, 500, 64), (9, 263, 8), (9, 264, 8), (3, 401, 40)])
+def test_long_uniform_sequences(n, t, d, math):
+    """Few of them and long: cut into segments; short ones stay whole."""
+    check(Scan([t] * n, d, 1, 16, math, seed=t + n, uniform=True))
+
+
+@MODES
 @pytest.mark.parametrize("N", [1, 3, 4, 8, 12, 16, 24, 32, 40, 64])
 @pytest.mark.parametrize("d,groups", [(8, 1), (48, 2)])
 def test_states_and_groups(N, d, groups, math):
