@@ -209,6 +209,29 @@ def test_step_is_the_scan_continued(N, d, groups, math):
     assert torch.equal(own, pool[slots.long()])
 
 
+@MODES
+@pytest.mark.parametrize("N,tokens,none", [(16, 1, ()), (16, 2, (0, 3, 4)), (16, 1, (6,)), (8, 3, (2,)), (12, 1, (1,))])
+def test_channels_for_every_warp_and_sequences_one_after_another(N, tokens, none, math):
+    """More tiles of channels than half of the GPU's warps: each takes all sequences, with and without states."""
+    torch = torch_mod()
+    n, d = 7, 65536 + 24
+    s = Scan([tokens] * n, d, 1, N, math, seed=N + tokens, uniform=True)
+    ref = ssm_forward(**s.host())
+    pool = torch.full((n + 2, d, N), 7.0, device="cuda")
+    slots = torch.tensor([8, 1, 0, 6, 3, 5, 2], dtype=torch.int32)
+    good = np.setdiff1d(np.arange(n), none)
+    pool[slots.long()[good]] = s.init[good]
+    before, at = pool.clone(), slots.long()[good]
+    slots[list(none)] = -1
+    y = s.nan(s.x)
+    cfc.cfc_ssm_step(s.x, s.delta, s.A, s.B, s.C, pool, y, D=s.D, z=s.z, delta_bias=s.bias, slots=slots.cuda(), math=math)
+    assert not y[list(none)].any()
+    close(y[good], ref["y"].reshape(n, tokens, d)[good], 5e-6, "y", math == BF16)
+    close(pool[at], ref["final_state"][good], 5e-6, "state")
+    rest = np.setdiff1d(np.arange(n + 2), at.numpy())
+    assert torch.equal(pool[rest], before[rest])
+
+
 def test_many_sequences_a_warp_and_slots_outside_the_pool():
     torch = torch_mod()
     n, d, N = 700, 64, 16
