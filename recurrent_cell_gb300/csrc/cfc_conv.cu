@@ -14,7 +14,7 @@
 // a tile of rows with the last W - 1 rows in registers and the next kBatch in flight; a
 // tile reads W - 1 rows of its neighbours' again, from cache.  The backward walks its rows
 // once: p_t is formed as soon as row t is there, and grad_x follows W - 1 rows behind.
-// Its tiles are as long as the GPU has threads for, since each is a row of partial grad_w
+// Tiles are as long as the GPU has threads for; a backward tile is a row of partial grad_w
 // that reduce_axis0 adds.
 #include "pair_math.cuh"
 #include "seq_rows.cuh"
@@ -38,7 +38,6 @@ struct Args {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 4;
-constexpr int kTileFwd = 128;                // rows of a forward tile
 
 // A thread's channels: N of type E, as pairs.
 template <class E_, int N_>
@@ -521,6 +520,16 @@ static int bwd_tile(long long rows, int d, int width) {
   return n < 16 ? 16 : (int)n;
 }
 
+// Rows of a forward tile: 16 warps an SM, what it holds at once up to 4 weights a channel and
+// twice beyond (16384 x 4096 in bf16, 4 weights: 16 warps 48.5 us, 12 52.8, 32 52.0, tiles of 128 rows
+// 52.0; 8 weights 69.8, 85, 82, 78), and a batch at least (64 rows: tiles of 4 4.9 us, of 16 7.2,
+// of 128 13.2).
+static int fwd_tile(long long rows, int vectors) {
+  const long long tiles = 16ll * 32 * kNumSMs / vectors;
+  const long long n = tiles < 1 ? rows : (rows + tiles - 1) / tiles;
+  return n < 1 ? kBatch : (int)((n + kBatch - 1) / kBatch * kBatch);
+}
+
 static Args args_of(const ConvArgs& g) {
   Args a{};
   a.x = g.x; a.ldx = g.ldx; a.w = g.weight; a.b = g.bias; a.init = g.init; a.silu = g.silu; a.d = g.d;
@@ -540,7 +549,7 @@ cudaError_t launch_conv_forward(const ConvArgs& g, void* y, void* final_state, c
   conv::Args a = conv::args_of(g);
   a.y = y;
   a.final_state = final_state;
-  a.tile = conv::kTileFwd;
+  a.tile = conv::fwd_tile(g.rows, g.d / (g.math == CFC_MATH_BF16 ? 8 : 4));
   a.n_tiles = (int)((g.rows + a.tile - 1) / a.tile);
   return g.math == CFC_MATH_BF16 ? conv::by_width(g.width, conv::Forward<conv::Chan<__nv_bfloat16, 8>>{a, st})
                                  : conv::by_width(g.width, conv::Forward<conv::Chan<float, 4>>{a, st});
