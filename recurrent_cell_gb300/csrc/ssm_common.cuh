@@ -411,7 +411,8 @@ static cudaError_t launch_ssm_carry(const Args& a, cudaStream_t st) {
 // The plan: rows of a segment, segments, channels of a tile.  Cut into segments, every SM has its
 // kResident warps, but the pass that hands states on costs half as much again as the scan, and two
 // launches more; whole, a sequence takes the latency of all its tokens.  So sequences of one length
-// stay whole where there are kEnough of them and their tiles, and earlier the shorter they are.
+// (and packed rows, as if they were one) stay whole where there are kEnough of them and their tiles, and
+// earlier the shorter they are.
 // Measured, bfloat16, 16 states, whole | cut in us: 2048 tokens with 256 tiles in all 187 | 166,
 // 384 221 | 234, 576 226 | 331; 512 tokens with 160 56 | 53, 256 58 | 66, 512 67 | 103; 128 tokens
 // with 160 26 | 41.
@@ -429,12 +430,14 @@ inline Plan make_plan(long long rows, int n_seq, int d, int groups, int N, bool 
   const int per = d / groups, cw = 8 * p.CPL;
   p.tpg = (per + cw - 1) / cw;
   p.tiles = p.tpg * groups;
-  const long long tokens = packed || n_seq == 0 ? 0 : rows / n_seq;
+  // (packed rows may be one sequence)
+  const int n = packed ? 1 : n_seq;
+  const long long tokens = n > 0 ? rows / n : 0;
   if (rows <= 0) {
     p.S = kT;
-  } else if (tokens > 0 && n_seq * (long long)p.tiles * tokens >= kPlanEnough * tokens - kPlanShort) {
-    long long k = n_seq * (long long)p.tiles / kPlanWarps;
-    p.S = tokens * (k < 1 ? 1 : k);
+  } else if (tokens > 0 && n * (long long)p.tiles * tokens >= kPlanEnough * tokens - kPlanShort) {
+    long long k = n * (long long)p.tiles / kPlanWarps;
+    p.S = tokens * (k < 1 ? 1 : k < n ? k : n);
   } else {
     p.S = (rows * p.tiles + kPlanWarps - 1) / kPlanWarps;
     if (p.S < 4 * kT) p.S = 4 * kT;

@@ -120,7 +120,7 @@ def check(s, gfinal=True):
         close(v, want[k], 1e-5, k, half and k in ("grad_x", "grad_delta", "grad_z", "grad_B", "grad_C"), scale)
 
 
-LENS = [[1], [16], [17], [300], [0, 1, 2, 15, 16, 17, 33, 0], [0, 70, 200, 1, 0, 5, 64, 130], [5, 3] * 20]
+LENS = [[1], [16], [17], [300], [0, 300, 1, 16, 0, 15, 70, 33, 0, 8], [0, 1, 2, 15, 16, 17, 33, 0], [0, 70, 200, 1, 0, 5, 64, 130], [5, 3] * 20]
 
 
 @MODES
@@ -147,6 +147,22 @@ def test_long_uniform_sequences(n, t, d, math):
 @pytest.mark.parametrize("d,groups", [(8, 1), (48, 2)])
 def test_states_and_groups(N, d, groups, math):
     check(Scan([37, 0, 90], d, groups, N, math, seed=N))
+
+
+@MODES
+@pytest.mark.parametrize("N", [3, 8, 16, 24, 32, 64])
+@pytest.mark.parametrize("d,groups", [(8, 1), (48, 2)])
+def test_states_and_groups_of_long_sequences(N, d, groups, math):
+    """More rows than one warp takes: sequences that a segment's end cuts, once and more often."""
+    check(Scan([150, 0, 1, 237], d, groups, N, math, seed=N))
+
+
+def test_channels_enough_for_whole_packed_rows():
+    """Tiles of channels for every warp of the GPU: packed rows in one segment, and a workspace of their size."""
+    d, N = 40000, 2
+    small, big = (cfc.cfc_ssm_workspace_bytes(r, 3, d, 1, N, BF16, save=True) for r in (320, 640))
+    assert big < 2.1 * small
+    check(Scan([100, 0, 220], d, 1, N, BF16, seed=3))
 
 
 @pytest.mark.parametrize("d,groups", [(8, 1), (24, 3), (136, 1), (128, 1), (160, 2), (1000, 1)])
