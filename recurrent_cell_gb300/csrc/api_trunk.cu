@@ -3,7 +3,9 @@
 //
 // As in api.cu every argument is checked on the host before anything is enqueued;
 // no allocation, no synchronisation, no host read of device data.
+#include <algorithm>
 #include <initializer_list>
+#include <new>
 
 #include "cfc_internal.cuh"
 
@@ -292,6 +294,36 @@ size_t cfc_grad_clip_workspace_bytes(int count) {
   return count < 0 || count > kMaxTensors ? 0 : grad_workspace(count);
 }
 
+// Whether an output shares a byte with another tensor, its own gradient (in place) aside.
+struct Span {
+  uintptr_t at, end;
+  bool out;
+};
+static int check_apart(const void* const* grads, void* const* out, const long long* n_values, const int* math, int count) {
+  constexpr int kFew = 128;
+  Span few[2 * kFew];
+  Span* const spans = count <= kFew ? few : new (std::nothrow) Span[2 * (size_t)count];
+  if (!spans) return CFC_ERR_LAUNCH;
+  int n = 0;
+  for (int i = 0; i < count; ++i) {
+    if (n_values[i] == 0) continue;
+    const uintptr_t bytes = (uintptr_t)n_values[i] * size_of(math[i]), p = reinterpret_cast<uintptr_t>(grads[i]),
+                    q = reinterpret_cast<uintptr_t>(out[i]);
+    spans[n++] = Span{q, q + bytes, true};
+    if (p != q) spans[n++] = Span{p, p + bytes, false};
+  }
+  std::sort(spans, spans + n, [](const Span& a, const Span& b) { return a.at < b.at; });
+  uintptr_t any = 0, written = 0;              // where those so far end
+  bool meet = false;
+  for (int i = 0; i < n; ++i) {
+    meet |= spans[i].at < (spans[i].out ? any : written);
+    any = std::max(any, spans[i].end);
+    if (spans[i].out) written = std::max(written, spans[i].end);
+  }
+  if (spans != few) delete[] spans;
+  return meet ? CFC_ERR_OVERLAP : CFC_OK;
+}
+
 static int grad_call(const void* const* grads, void* const* out, bool clip, const long long* n_values, const int* math,
                      int count, float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
   if (count < 0 || count > kMaxTensors || !(max_norm >= 0.f)) return CFC_ERR_SHAPE;
@@ -302,11 +334,10 @@ static int grad_call(const void* const* grads, void* const* out, bool clip, cons
     if (n_values[i] == 0) continue;
     if (!grads[i] || (clip && !out[i])) return CFC_ERR_NULL;
     if (!aligned({grads[i], clip ? out[i] : nullptr}, size_of(math[i]))) return CFC_ERR_ALIGN;
-    const long long bytes = n_values[i] * size_of(math[i]);
-    if (clip && out[i] != grads[i] && overlap(grads[i], bytes, out[i], bytes)) return CFC_ERR_OVERLAP;
   }
   if (!workspace || workspace_bytes < grad_workspace(count)) return CFC_ERR_WORKSPACE;
   if (!aligned({workspace}, 16) || !aligned({norm}, 4)) return CFC_ERR_ALIGN;
+  if (const int st = clip ? check_apart(grads, out, n_values, math, count) : CFC_OK; st != CFC_OK) return st;
   return done(launch_grad_norm(grads, clip ? out : nullptr, n_values, math, count, max_norm, norm,
                                static_cast<double*>(workspace), as_stream(stream)));
 }

@@ -236,6 +236,10 @@ def test_grad_refusals(lib, clip):
             assert grads(lib, True, most=most) == ERR_SHAPE
         assert grads(lib, True, outs=(far(0) + 4, far(3))) == ERR_OVERLAP
         assert grads(lib, True, outs=(None, far(3))) == ERR_NULL
+        assert grads(lib, True, ptrs=(far(0), far(1)), outs=(far(1), far(0))) == ERR_OVERLAP       # of each other
+        assert grads(lib, True, ptrs=(far(0), far(1)), outs=(far(2), far(2))) == ERR_OVERLAP
+        assert grads(lib, True, ptrs=(far(0), far(0)), outs=(far(0), far(0))) == ERR_OVERLAP       # in place twice
+        assert grads(lib, True, ptrs=(far(0), far(0)), outs=(far(0), far(3))) == ERR_OVERLAP
     assert cfc.cfc_grad_clip_workspace_bytes(-1) == 0 and cfc.cfc_grad_clip_workspace_bytes(65537) == 0
     assert cfc.cfc_grad_clip_workspace_bytes(0) > 0
 

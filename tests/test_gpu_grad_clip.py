@@ -174,6 +174,22 @@ def test_more_than_2_32_bytes():
     assert float(big[-1]) == 0.125 and float(big[0]) == 0.125 and float(big[1 << 30]) == 0.125
 
 
+@pytest.mark.parametrize("pieces", [3, 200])
+def test_parts_of_one_buffer_and_a_gradient_named_twice(pieces):
+    torch = torch_mod()
+    flat = torch.randn(pieces * 37, device="cuda")
+    before = flat.double()
+    parts = [flat[i * 37:(i + 1) * 37] for i in range(pieces)][::-1]
+    norm, ws = torch.empty(1, device="cuda"), workspace(pieces)
+    cfc.cfc_grad_clip(parts, 1.0, norm, ws)
+    want = float(before.norm())
+    assert abs(float(norm) - want) <= 1e-6 * want
+    assert (flat.double() - before / (want + 1e-6)).abs().max() <= 1e-6 * before.abs().max() / want
+    out = [torch.empty_like(parts[0]) for _ in range(2)]
+    cfc.cfc_grad_clip([parts[0], parts[0]], 1e-3, norm, workspace(2), out=out)
+    assert torch.equal(out[0], out[1]) and abs(float(norm) - 2 ** 0.5 * float(parts[0].double().norm())) <= 1e-6 * float(norm)
+
+
 def test_refusals_of_the_binding():
     torch = torch_mod()
     g = tensors([8, 8])
