@@ -18,26 +18,25 @@ namespace cfc {
 namespace clip {
 
 constexpr int kThreads = 256;
+constexpr int kTensors = 512;                    // of a launch: 15 KB of parameters (a table of 64 is no faster)
 constexpr int kItem = 32768, kSmallItem = 2048;  // values of an item: the most, the fewest
 constexpr int kMaxBlocks = 6 * kNumSMs;          // partial sums of a launch
 constexpr int kScaleBlocks = 8 * kNumSMs;
 
 enum : uint8_t { kBf16 = 1, kVector = 2 };       // what a tensor's flag says
 
-template <int MAX>
 struct Table {
-  const void* in[MAX];
-  void* out[MAX];
-  long long n[MAX];
-  int first[MAX + 1];                            // items before the tensor
+  const void* in[kTensors];
+  void* out[kTensors];
+  long long n[kTensors];
+  int first[kTensors + 1];                            // items before the tensor
   int item;                                      // values of an item
-  uint8_t flags[MAX];
+  uint8_t flags[kTensors];
   int count;
 };
 
 // The tensor of an item: the last that starts at or before it.
-template <int MAX>
-__device__ __forceinline__ int tensor_of(const Table<MAX>& t, int item) {
+__device__ __forceinline__ int tensor_of(const Table& t, int item) {
   int lo = 0, hi = t.count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -99,8 +98,7 @@ struct Span {
   long long at;
   uint8_t flags;
 };
-template <int MAX>
-__device__ __forceinline__ Span span_of(const Table<MAX>& t, int item) {
+__device__ __forceinline__ Span span_of(const Table& t, int item) {
   Span s;
   s.k = tensor_of(t, item);
   s.at = (long long)(item - t.first[s.k]) * t.item;
@@ -110,8 +108,7 @@ __device__ __forceinline__ Span span_of(const Table<MAX>& t, int item) {
   return s;
 }
 
-template <int MAX>
-__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table<MAX> t, double* sums) {
+__global__ void __launch_bounds__(kThreads) k_grad_squares(const __grid_constant__ Table t, double* sums) {
   double sum = 0;
   const int items = t.first[t.count];
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -143,8 +140,7 @@ __device__ __forceinline__ void scale(const void* in, void* out, int n, float c)
 }
 
 // c = min(1, most / (norm + 1e-6)); a NaN stays one, and an infinite norm gives 0.
-template <int MAX>
-__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ Table<MAX> t, const double* sums, int n_sums,
+__global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ Table t, const double* sums, int n_sums,
                                                          float most, float* norm) {
   double v = 0;
   for (int i = threadIdx.x; i < n_sums; i += kThreads) v += sums[i];
@@ -174,17 +170,17 @@ static int item_of(const long long* n, int count) {
   return item;
 }
 
-// `go` is given tables of up to MAX tensors, in order.
-template <int MAX, class F>
+// `go` is given tables of up to kTensors tensors, in order.
+template <class F>
 static cudaError_t tables(const void* const* in, void* const* out, const long long* n, const int* math, int count, F go) {
   int at = 0;
   const int item = item_of(n, count);
   do {
-    Table<MAX> t;
+    Table t;
     t.item = item;
     t.count = 0;
     t.first[0] = 0;
-    for (; at < count && t.count < MAX; ++at) {
+    for (; at < count && t.count < kTensors; ++at) {
       if (n[at] == 0) continue;
       const int j = t.count++;
       t.in[j] = in[at];
@@ -192,7 +188,7 @@ static cudaError_t tables(const void* const* in, void* const* out, const long lo
       t.n[j] = n[at];
       const uintptr_t bits = reinterpret_cast<uintptr_t>(t.in[j]) | reinterpret_cast<uintptr_t>(t.out[j]);
       t.flags[j] = (math[at] == CFC_MATH_BF16 ? kBf16 : 0) | (bits % 16 == 0 ? kVector : 0);
-      t.first[j + 1] = t.first[j] + (int)((n[at] + item - 1) / item);   // kMany x kMaxGradValues stay below 2^31
+      t.first[j + 1] = t.first[j] + (int)((n[at] + item - 1) / item);   // kTensors x kMaxGradValues stay below 2^31
     }
     const cudaError_t e = go(t);
     if (e != cudaSuccess) return e;
@@ -200,46 +196,41 @@ static cudaError_t tables(const void* const* in, void* const* out, const long lo
   return cudaSuccess;
 }
 
-template <int MAX>
-static int grid_of(const Table<MAX>& t, int most) {
+static int grid_of(const Table& t, int most) {
   const int items = t.first[t.count];
   return items < 1 ? 1 : items < most ? items : most;
 }
 
-template <int MAX>
 static cudaError_t run(const void* const* in, void* const* out, const long long* n, const int* math, int count, float most,
                        float* norm, double* sums, cudaStream_t st) {
   int n_sums = 0;
-  cudaError_t e = tables<MAX>(in, out, n, math, count, [&](const Table<MAX>& t) {
+  cudaError_t e = tables(in, out, n, math, count, [&](const Table& t) {
     if (t.count == 0) return cudaSuccess;
     TraceScope tr("k_grad_squares", st);
-    k_grad_squares<MAX><<<grid_of(t, kMaxBlocks), kThreads, 0, st>>>(t, sums + n_sums);
+    k_grad_squares<<<grid_of(t, kMaxBlocks), kThreads, 0, st>>>(t, sums + n_sums);
     n_sums += grid_of(t, kMaxBlocks);
     return cudaGetLastError();
   });
   if (e != cudaSuccess) return e;
   // (no table: one block that writes the norm)
-  return tables<MAX>(in, out, n, math, out ? count : 0, [&](const Table<MAX>& t) {
+  return tables(in, out, n, math, out ? count : 0, [&](const Table& t) {
     TraceScope tr("k_grad_scale", st);
-    k_grad_scale<MAX><<<grid_of(t, kScaleBlocks), kThreads, 0, st>>>(t, sums, n_sums, most, norm);
+    k_grad_scale<<<grid_of(t, kScaleBlocks), kThreads, 0, st>>>(t, sums, n_sums, most, norm);
     return cudaGetLastError();
   });
 }
 
-// Tensors of one table: what a launch's parameters hold, 2 KB or 15 KB.
-constexpr int kFew = 64, kMany = 512;
-static_assert(kMany * (kMaxGradValues / kItem + 1) < (1ll << 31), "items of a launch");
+static_assert(kTensors * (kMaxGradValues / kItem + 1) < (1ll << 31), "items of a launch");
 
 }  // namespace clip
 
 size_t grad_workspace(int count) {
-  return (size_t)(count / clip::kMany + 1) * clip::kMaxBlocks * sizeof(double);     // the sums of each launch
+  return (size_t)(count / clip::kTensors + 1) * clip::kMaxBlocks * sizeof(double);     // the sums of each launch
 }
 
 cudaError_t launch_grad_norm(const void* const* in, void* const* out, const long long* n, const int* math, int count,
                              float most, float* norm, double* sums, cudaStream_t st) {
-  return count <= clip::kFew ? clip::run<clip::kFew>(in, out, n, math, count, most, norm, sums, st)
-                             : clip::run<clip::kMany>(in, out, n, math, count, most, norm, sums, st);
+  return clip::run(in, out, n, math, count, most, norm, sums, st);
 }
 
 }  // namespace cfc

@@ -118,14 +118,13 @@ __device__ __forceinline__ void over_channels(float (&v)[N], int lane) {
   }
 }
 
-// dt, dt x and g of a chunk's tokens, into the tiles.  dx = nullptr: only dt and g.
+// dt and g of a chunk's tokens, into the tiles.
 template <class G>
 __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const F2 (&bias)[G::VN / 2],
-                                             float (*dt)[G::CW], float (*dx)[G::CW], float (*g)[G::CW]) {
+                                             float (*dt)[G::CW], float (*g)[G::CW]) {
   using U = Pairs<typename G::E, G::VN>;
   constexpr int VP = G::VN / 2;
-  uint4 xv[G::P], dv[G::P], zv[G::P], gv[G::P];
-  if (dx) load_raw<G>(w, a.x, a.ldx, row, n, xv);
+  uint4 dv[G::P], zv[G::P], gv[G::P];
   load_raw<G>(w, a.delta, a.ldd, row, n, dv);
   load_raw<G>(w, a.grad_y, a.d, row, n, gv);
   if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
@@ -144,12 +143,6 @@ __device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, lo
     if (w.row(k) < kT) {
       put_pairs(&dt[w.row(k)][w.col()], t);
       put_pairs(&g[w.row(k)][w.col()], f);
-    }
-    if (dx) {
-      U::get(u, xv[k]);
-#pragma unroll
-      for (int e = 0; e < VP; ++e) u[e] = mul2(u[e], t[e]);
-      if (w.row(k) < kT) put_pairs(&dx[w.row(k)][w.col()], u);
     }
   }
 }
@@ -184,7 +177,7 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
   for (long long row = r0 + (last - r0 - 1) / kT * kT; row >= r0; row -= kT) {
     const int n = last - row < kT ? (int)(last - row) : kT;
     cv.fetch(a, w, a.C, a.ldc, row, n);
-    stage_tokens<G>(a, w, row, n, bias, sm.dt, nullptr, sm.g);
+    stage_tokens<G>(a, w, row, n, bias, sm.dt, sm.g);
     cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
     __syncwarp();
 #pragma unroll 4

