@@ -78,16 +78,7 @@ __global__ void __launch_bounds__(64, kResident) k_ssm(Args a, bool save) {
   __shared__ FwdTiles<G, LOCAL> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
-  // Which of the two warps helps: a warp's scheduler is its slot's, and blocks of two take slots in
-  // pairs, so were it always the second, the states would run on two of the four.
-  __shared__ int swap;
-  if (threadIdx.x == 0) {
-    uint32_t slot;
-    asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
-    swap = slot >> 2 & 1;
-  }
-  __syncthreads();
-  const bool helper = (threadIdx.x >= 32) != (swap != 0);
+  const bool helper = helper_of_two();
 
   if (!LOCAL && seg >= a.n_seg) {            // the states after sequences without rows
     F2 h[G::PAIRS];

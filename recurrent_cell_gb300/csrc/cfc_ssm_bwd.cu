@@ -118,74 +118,109 @@ __device__ __forceinline__ void over_channels(float (&v)[N], int lane) {
   }
 }
 
-// dt and g of a chunk's tokens, into the tiles.
-template <class G>
-__device__ __forceinline__ void stage_tokens(const Args& a, const Tile<G>& w, long long row, int n, const F2 (&bias)[G::VN / 2],
-                                             float (*dt)[G::CW], float (*g)[G::CW]) {
-  using U = Pairs<typename G::E, G::VN>;
-  constexpr int VP = G::VN / 2;
-  uint4 dv[G::P], zv[G::P], gv[G::P];
-  load_raw<G>(w, a.delta, a.ldd, row, n, dv);
-  load_raw<G>(w, a.grad_y, a.d, row, n, gv);
-  if (a.z) load_raw<G>(w, a.z, a.ldz, row, n, zv);
-#pragma unroll
-  for (int k = 0; k < G::P; ++k) {
-    F2 f[VP], t[VP], u[VP];
-    U::get(t, dv[k]);
-#pragma unroll
-    for (int e = 0; e < VP; ++e) t[e] = softplus2(add2(t[e], bias[e]));
-    U::get(f, gv[k]);
-    if (a.z) {
-      U::get(u, zv[k]);
-#pragma unroll
-      for (int e = 0; e < VP; ++e) f[e] = mul2(f[e], mul2(u[e], sigmoid2(u[e])));
-    }
-    if (w.row(k) < kT) {
-      put_pairs(&dt[w.row(k)][w.col()], t);
-      put_pairs(&g[w.row(k)][w.col()], f);
-    }
-  }
-}
-
 // What a segment's own rows send to the state before it, and its sum of dt: for the
-// segments whose first row continues a sequence.
+// segments whose first row continues a sequence.  Two warps as in the forward (16384 x 2048 channels
+// x 16 states: 127 us, one warp that does both 174).
 template <class G>
 struct __align__(16) LocalTiles {
-  float dt[kT][G::CW], g[kT][G::CW], C[kT][G::NP];
+  float dt[2][kT][G::CW], g[2][kT][G::CW], C[2][kT][G::NP];
+  uint4 raw[3][G::P][32], rawC[G::BL][32];                   // delta, z, grad_y; C: the chunk to come
 };
 template <class G>
-__global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
+__global__ void __launch_bounds__(64, kResident) k_ssm_local_bwd(Args a) {
+  using E = typename G::E;
+  using U = Pairs<E, G::VN>;
+  constexpr int VN = G::VN, VP = VN / 2, P = G::P;
   __shared__ LocalTiles<G> sm;
   const Tile<G> w(a, blockIdx.x);
   const int seg = blockIdx.y;
+  const bool helper = helper_of_two();
   a.s = seqs::trim(a.s);
   const long long r0 = seg * a.S, r1 = a.s.rows - r0 < a.S ? a.s.rows : r0 + a.S;
   if (r0 >= r1) {                            // rows behind the last sequence
-    if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.flags[seg] = 0;
     return;
   }
   const Where q = seqs::find(a.s, r0);
   const bool cut = q.begin < r0, ends = q.end <= r1;
-  if (blockIdx.x == 0 && w.lane == 0) a.flags[seg] = (cut ? kCut : 0) | (ends ? kStarts : 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.flags[seg] = (cut ? kCut : 0) | (ends ? kStarts : 0);
   if (!cut) return;
   const long long last = ends ? q.end : r1;
-  F2 A2[G::PAIRS], dh[G::PAIRS], sum[G::CPAIRS] = {}, bias[G::VN / 2];
+  const int chunks = (int)((last - r0 + kT - 1) / kT);
+  auto count = [&](int chunk) { return last - (r0 + (long long)chunk * kT) < kT ? (int)(last - (r0 + (long long)chunk * kT)) : kT; };
+
+  if (helper) {
+    F2 bias[VP];
+    load_pairs<G>(w, a.bias, bias);
+    auto vector = [&](const void* p, long long ld, long long r) { return static_cast<const E*>(p) + r * ld + w.c0 + w.col(); };
+    auto fetch = [&](int chunk) {
+      const long long at = r0 + (long long)chunk * kT;
+      const int n = count(chunk);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const bool in = w.row(k) < n && w.col() < w.cols;
+        const long long r = in ? at + w.row(k) : at;
+        copy16(&sm.raw[0][k][w.lane], in ? vector(a.delta, a.ldd, r) : a.delta, in);
+        if (a.z) copy16(&sm.raw[1][k][w.lane], in ? vector(a.z, a.ldz, r) : a.z, in);
+        copy16(&sm.raw[2][k][w.lane], in ? vector(a.grad_y, a.d, r) : a.grad_y, in);
+      }
+      if (a.vec_bc)
+#pragma unroll
+        for (int k = 0; k < G::BL; ++k) {
+          const int i = k * 32 + w.lane, r = i / G::BV;
+          const bool in = r < n;
+          copy16(&sm.rawC[k][w.lane], in ? static_cast<const E*>(a.C) + (at + r) * a.ldc + w.g * a.N + i % G::BV * VN : a.C, in);
+        }
+      copies_end();
+    };
+    auto stage = [&](int chunk) {
+      const int to = chunk & 1;
+      copies_wait<0>();
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        F2 f[VP], t[VP], u[VP];
+        U::get(t, sm.raw[0][k][w.lane]);
+#pragma unroll
+        for (int e = 0; e < VP; ++e) t[e] = softplus2(add2(t[e], bias[e]));
+        U::get(f, sm.raw[2][k][w.lane]);
+        if (a.z) {
+          U::get(u, sm.raw[1][k][w.lane]);
+#pragma unroll
+          for (int e = 0; e < VP; ++e) f[e] = mul2(f[e], mul2(u[e], sigmoid2(u[e])));
+        }
+        if (w.row(k) < kT) {
+          put_pairs(&sm.dt[to][w.row(k)][w.col()], t);
+          put_pairs(&sm.g[to][w.row(k)][w.col()], f);
+        }
+      }
+      Rows<G> cv;
+      if (a.vec_bc)
+#pragma unroll
+        for (int k = 0; k < G::BL; ++k) cv.v[k] = sm.rawC[k][w.lane];
+      cv.stage(a, w, a.C, a.ldc, r0 + (long long)chunk * kT, count(chunk), sm.C[to][0]);
+    };
+    fetch(chunks - 1);
+    stage(chunks - 1);
+    if (chunks > 1) fetch(chunks - 2);
+    for (int i = chunks - 1; i >= 0; --i) {
+      __syncthreads();                         // chunk i is staged, chunk i + 1 has been run through
+      if (i > 0) stage(i - 1);
+      if (i > 1) fetch(i - 2);
+    }
+    return;
+  }
+
+  F2 A2[G::PAIRS], dh[G::PAIRS], sum[G::CPAIRS] = {};
   load_A<G>(a, w, A2);
-  load_pairs<G>(w, a.bias, bias);
   load_state<G>(a, w, ends ? a.grad_final : nullptr, q.i, dh);
-  Rows<G> cv;
-  for (long long row = r0 + (last - r0 - 1) / kT * kT; row >= r0; row -= kT) {
-    const int n = last - row < kT ? (int)(last - row) : kT;
-    cv.fetch(a, w, a.C, a.ldc, row, n);
-    stage_tokens<G>(a, w, row, n, bias, sm.dt, sm.g);
-    cv.stage(a, w, a.C, a.ldc, row, n, sm.C[0]);
-    __syncwarp();
-#pragma unroll 4
-    for (int t = n - 1; t >= 0; --t) {
+  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
+    const int n = count(chunk), k = chunk & 1;
+    __syncthreads();
+    auto token = [&](int t) {
       F2 dt[G::CPAIRS], g[G::CPAIRS], c[G::SPAIRS];
-      get_channels<G>(sm.dt[t], w.cl, dt);
-      get_channels<G>(sm.g[t], w.cl, g);
-      get_states<G>(sm.C[t], w.sl, c);
+      get_channels<G>(sm.dt[k][t], w.cl, dt);
+      get_channels<G>(sm.g[k][t], w.cl, g);
+      get_states<G>(sm.C[k][t], w.sl, c);
 #pragma unroll
       for (int p = 0; p < G::PAIRS; ++p) {
         const int i = cpair<G>(p), j = spair<G>(p);
@@ -193,8 +228,14 @@ __global__ void __launch_bounds__(32) k_ssm_local_bwd(Args a) {
       }
 #pragma unroll
       for (int i = 0; i < G::CPAIRS; ++i) sum[i] = add2(sum[i], dt[i]);
+    };
+    if (n == kT) {
+#pragma unroll
+      for (int t = kT - 1; t >= 0; --t) token(t);
+    } else {
+#pragma unroll 1
+      for (int t = n - 1; t >= 0; --t) token(t);
     }
-    __syncwarp();
   }
   const long long block = (long long)seg * a.tiles + blockIdx.x;
   store_lanes<G>(a.local, block, w.lane, dh);
@@ -660,7 +701,7 @@ static cudaError_t backward(const Args& a, const Plan& p, cudaStream_t st) {
   if (p.cut) {
     {
       TraceScope tr("k_ssm_local_bwd", st);
-      k_ssm_local_bwd<G><<<dim3(a.tiles, a.n_seg), 32, 0, st>>>(a);
+      k_ssm_local_bwd<G><<<dim3(a.tiles, a.n_seg), 64, 0, st>>>(a);
     }
     const cudaError_t e = launch_ssm_carry<G, true>(a, st);
     if (e != cudaSuccess) return e;

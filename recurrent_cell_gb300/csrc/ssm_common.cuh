@@ -326,20 +326,23 @@ __device__ __forceinline__ float over_states(float (&v)[CPL], int lane) {
     return all<1>(all<1>(v[0], 1), 2);
   }
 }
-// A chunk's rows of B or C: fetched into registers ahead (whole vectors), or element
-// by element when they are put into the tile [kT][NP].
+// Whether this warp is the one of its block's two that helps.  A warp's scheduler is its slot's, and blocks of two
+// take slots in pairs, so were it always the second, the states would run on two of the four.
+__device__ __forceinline__ bool helper_of_two() {
+  __shared__ int swap;
+  if (threadIdx.x == 0) {
+    uint32_t slot;
+    asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+    swap = slot >> 2 & 1;
+  }
+  __syncthreads();
+  return (threadIdx.x >= 32) != (swap != 0);
+}
+
+// A chunk's rows of B or C as the lanes have them (whole vectors), or element by element, into the tile [kT][NP].
 template <class G>
 struct Rows {
   uint4 v[G::BL];
-  __device__ __forceinline__ void fetch(const Args& a, const Tile<G>& w, const void* p, long long ld, long long row0, int n) {
-    if (!a.vec_bc) return;
-    const typename G::E* q = static_cast<const typename G::E*>(p) + w.g * a.N;
-#pragma unroll
-    for (int k = 0; k < G::BL; ++k) {
-      const int i = k * 32 + w.lane, r = i / G::BV;
-      v[k] = load_here(q + (row0 + r) * ld + i % G::BV * G::VN, r < n);
-    }
-  }
   __device__ __forceinline__ void stage(const Args& a, const Tile<G>& w, const void* p, long long ld, long long row0, int n,
                                         float* tile) const {
     if (a.vec_bc) {
