@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kStepThreads, kAheadBlocks) k_ssm_step_ahead(S
 }
 
 // Sequences of a warp: the fewest that fill the `resident` warps of the GPU a whole number of times, kMaxEach
-// at most (192 sequences x 4096 channels: 7, all at once, 23.4 us; 6 at most, two rounds, 25.7).
+// at most (192 sequences x 4096 channels: 7, all at once, 23.4 us; 6 at most, in two waves, 25.7).
 constexpr int kMaxEach = 10;
 inline int sequences_of_a_warp(int n, int tiles, int resident) {
   for (int k = 1;; ++k) {

@@ -417,16 +417,17 @@ static cudaError_t launch_ssm_carry(const Args& a, cudaStream_t st) {
 // launches more; whole, a sequence takes the latency of all its tokens.  So sequences of one length
 // (and packed rows, as if they were one) stay whole where there are kEnough of them and their tiles, and
 // earlier the shorter they are.
-// Measured, bfloat16, 16 states, whole | cut in us: 2048 tokens with 256 tiles in all 187 | 166,
-// 384 221 | 234, 576 226 | 331; 512 tokens with 160 56 | 53, 256 58 | 66, 512 67 | 103; 128 tokens
-// with 160 26 | 41.
+// Measured, bfloat16, 16 states, whole | cut in us: 2048 tokens with 384 tiles in all 221 | 234 forward and
+// 996 | 786 both ways, 512 226 | 298 and 1005 | 1014; 512 tokens with 256 58 | 66 and 269 | 201, 512 67 | 103 and
+// 287 | 327; 128 tokens with 160 26 | 41.  One rule for both, between the two: a forward gives the
+// same bits whether or not it saves.
 struct Plan {
   int NS, CPL, tpg, tiles, n_seg, cps;
   long long S;
   bool cut;
 };
-constexpr long long kPlanWarps = (long long)kResident * kNumSMs, kPlanEnough = 5ll * kNumSMs / 2,
-                    kPlanShort = 100000;     // tokens x tiles that the launches and the handing on are worth
+constexpr long long kPlanWarps = (long long)kResident * kNumSMs, kPlanEnough = 3ll * kNumSMs,
+                    kPlanShort = 75000;      // tokens x tiles that the launches and the handing on are worth
 inline Plan make_plan(long long rows, int n_seq, int d, int groups, int N, bool packed) {
   Plan p{};
   p.NS = N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16;
