@@ -112,7 +112,7 @@ class _Rule(torch.autograd.Function):
 def gated_delta_rule(q, k, v, g, beta, seq_offsets=None, initial_state=None, want_state=False):
     """(o, final state or None) over whole sequences: q, k [sequences, tokens, k_heads, d_k],
     v [sequences, tokens, v_heads, d_v], g, beta [sequences, tokens, v_heads], or
-    all of them packed [rows, ...] with seq_offsets.  scale = d_k ** -0.5."""
+    all of them packed [rows, ...] with seq_offsets, the last of which is rows (no padding).  scale = d_k ** -0.5."""
     return _Rule.apply(q, k, v, g, beta, seq_offsets, initial_state, want_state)
 
 
@@ -148,11 +148,17 @@ def _dense(t):
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
+def _by_rows(t, seq_offsets):
+    """A dense tensor like t for the calls to write.  Of a packed batch they leave the rows behind the last sequence as
+    they are, and what follows (dense products, norms, sums over rows) takes all rows: zeros, for nothing to come of them."""
+    return _dense(t) if seq_offsets is None else _dense(t).zero_()
+
+
 class _Conv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, seq_offsets, initial_state, want_state, silu):
         n = x.shape[0] if seq_offsets is None else seq_offsets.numel() - 1
-        y = _dense(x)
+        y = _by_rows(x, seq_offsets)
         state = torch.empty(n, weight.shape[1] - 1, x.shape[-1], dtype=x.dtype, device=x.device) if want_state else None
         cfc_conv_forward(x, weight, y, bias=bias, seq_offsets=seq_offsets, initial_state=initial_state, final_state=state,
                          silu=silu, math=_math(x.dtype))
@@ -165,7 +171,7 @@ class _Conv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_y, grad_state):
         x, weight, bias, seq_offsets, initial = ctx.saved_tensors
-        math, gx, gw = _math(x.dtype), _dense(x), torch.empty_like(weight)
+        math, gx, gw = _math(x.dtype), _by_rows(x, seq_offsets), torch.empty_like(weight)
         gb = None if bias is None else torch.empty_like(bias)
         grad_init = None if initial is None else torch.empty_like(initial)
         grad_y = _dense(x).zero_() if grad_y is None else grad_y.contiguous()
@@ -179,7 +185,8 @@ class _Conv(torch.autograd.Function):
 
 def causal_conv(x, weight, bias=None, seq_offsets=None, initial_state=None, want_state=False, silu=True):
     """(y, final state or None): each channel of x [sequences, tokens, channels] (or packed [rows, channels] with
-    seq_offsets) over its last weight.shape[1] rows; a state is the last inputs, [sequences, width - 1, channels]."""
+    seq_offsets; rows from seq_offsets[-1] on are padding: y is zero there) over its last weight.shape[1] rows; a state is
+    the last inputs, [sequences, width - 1, channels]."""
     return _Conv.apply(x, weight, bias, seq_offsets, initial_state, want_state, silu)
 
 
@@ -190,7 +197,7 @@ class _Scan(torch.autograd.Function):
         (d, N), groups, rows, math = A.shape, B.shape[-2], x[..., 0].numel(), _math(x.dtype)
         save = any(ctx.needs_input_grad)
         ws = _workspace(cfc_ssm_workspace_bytes(rows, n, d, groups, N, math, save), x.device)
-        y = _dense(x)
+        y = _by_rows(x, seq_offsets)
         state = torch.empty(n, d, N, device=x.device) if want_state else None
         cfc_ssm_forward(x, delta, A, B, C, y, ws, D=D, z=z, delta_bias=delta_bias, seq_offsets=seq_offsets,
                         initial_state=initial_state, final_state=state, save=save, math=math)
@@ -204,7 +211,8 @@ class _Scan(torch.autograd.Function):
     def backward(ctx, grad_y, grad_state):
         x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial = ctx.saved_tensors
         like = lambda t: None if t is None else _dense(t)  # noqa: E731
-        gx, gdelta, gA, gB, gC, gD, gz, gbias, ginit = map(like, (x, delta, A, B, C, D, z, delta_bias, initial))
+        gA, gD, gbias, ginit = map(like, (A, D, delta_bias, initial))
+        gx, gdelta, gB, gC, gz = (None if t is None else _by_rows(t, seq_offsets) for t in (x, delta, B, C, z))
         grad_y = _dense(x).zero_() if grad_y is None else grad_y.contiguous()
         cfc_ssm_backward(x, delta, A, B, C, grad_y, gx, gdelta, gA, gB, gC, ctx.ws, D=D, z=z, delta_bias=delta_bias,
                          grad_D=gD, grad_z=gz, grad_delta_bias=gbias, seq_offsets=seq_offsets, initial_state=initial,
@@ -215,7 +223,8 @@ class _Scan(torch.autograd.Function):
 
 def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, seq_offsets=None, initial_state=None, want_state=False):
     """(y, final state or None) over whole sequences: x, delta, z [sequences, tokens, channels], A [channels, states],
-    B, C [sequences, tokens, groups, states], or all but A packed [rows, ...] with seq_offsets."""
+    B, C [sequences, tokens, groups, states], or all but A packed [rows, ...] with seq_offsets (rows from seq_offsets[-1]
+    on are padding: y is zero there, and they have no part in any gradient)."""
     return _Scan.apply(x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial_state, want_state)
 
 
@@ -336,7 +345,8 @@ class ScanBlock(torch.nn.Module):
         return r @ self.w_dt, B.unsqueeze(-2), C.unsqueeze(-2)
 
     def forward(self, delta, stream, seq_offsets=None, state=None, want_state=False):
-        """As MemoryBlock.forward."""
+        """As MemoryBlock.forward; packed rows may go on behind the last sequence (a padded batch): this block adds zero
+        to them."""
         y, s = layer_norm(_rows_of(delta), self.norm, self.norm_bias, _rows_of(stream))
         x, z = (y.view_as(delta) @ self.w_in).chunk(2, -1)
         last, h = (None, None) if state is None else state

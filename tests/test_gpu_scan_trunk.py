@@ -169,3 +169,64 @@ def test_second_derivatives_are_refused():
         (grad,) = torch.autograd.grad(out.square().sum(), at, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             grad.square().sum().backward()
+
+
+@pytest.fixture
+def stale():
+    """Memory that is allocated and not written holds NaN, as memory may that something else has used."""
+    torch = torch_mod()
+    torch.use_deterministic_algorithms(True, warn_only=True)
+    try:
+        assert torch.empty(4, device="cuda").isnan().all()
+        yield
+    finally:
+        torch.use_deterministic_algorithms(False)
+
+
+@pytest.mark.filterwarnings("ignore:.*deterministic")
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_a_padded_batch_is_the_batch_without_its_padding(stale, dtype):
+    """Rows behind the last sequence, whatever the allocator left: outputs of zeros there, and nothing in any gradient.
+
+    A block is good to 2e-4 of 64 bits in FP32 (above), so two runs differ by 4e-4 at most; in bf16 the same values
+    are rounded alike but for sums in another order: a step of a value, 2^-7, through the four roundings of a path."""
+    torch = torch_mod()
+    from recurrent_cell_gb300.memory import ScanBlock
+    torch.manual_seed(6)
+    dt, tol = getattr(torch, dtype), 4e-4 if dtype == "float32" else 4 * 2.0 ** -7
+    blocks = [ScanBlock(48, dtype=dt) for _ in range(2)]
+    x = torch.randn(100, 48, device="cuda").to(dt)
+    w = torch.randn(70, 48, device="cuda")
+    off = torch.tensor([0, 33, 33, 70], dtype=torch.int32, device="cuda")
+    got = []
+    for rows in (70, 100):
+        leaf = x[:rows].clone().requires_grad_()
+        delta, stream, last = blocks[0](leaf, None, off, want_state=True)
+        delta, stream, _ = blocks[1](delta, stream, off)
+        assert not delta[70:].any()
+        ((delta + stream)[:70].float() * w).sum().backward()
+        got.append({"out": delta[:70], "window": last[0], "state": last[1], "x": leaf.grad[:70],
+                    **{f"{i}.{n}": p.grad for i, b in enumerate(blocks) for n, p in b.named_parameters()}})
+        assert not leaf.grad[70:].any()
+        for b in blocks:
+            b.zero_grad(set_to_none=True)
+    for name, want in got[0].items():
+        near(got[1][name], want.cpu(), tol, name)
+
+
+@pytest.mark.filterwarnings("ignore:.*deterministic")
+def test_padding_of_the_operators_is_zero(stale):
+    torch = torch_mod()
+    from recurrent_cell_gb300.memory import causal_conv, selective_scan
+    torch.manual_seed(7)
+    off = torch.tensor([0, 5, 30], dtype=torch.int32, device="cuda")
+    leaf = lambda *s: torch.randn(*s, device="cuda").requires_grad_()  # noqa: E731
+    x, delta, z, B, C = leaf(41, 16), leaf(41, 16), leaf(41, 16), leaf(41, 1, 8), leaf(41, 1, 8)
+    weight, A = leaf(16, 4), -torch.rand(16, 8, device="cuda")
+    y, _ = causal_conv(x, weight, seq_offsets=off)
+    o, _ = selective_scan(y, delta, A, B, C, z=z, seq_offsets=off)
+    assert not y[30:].any() and not o[30:].any() and y[:30].all() and o[:30].all()
+    o.sum().backward()
+    for t in (x, delta, z, B, C):
+        assert t.grad.isfinite().all() and not t.grad[30:].any() and t.grad[:30].any()
+    assert weight.grad.isfinite().all()
