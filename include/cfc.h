@@ -547,7 +547,7 @@ int cfc_ssm_step(const void* x, long long x_stride, const void* delta, long long
  * 0 <= count <= 65536.  Squares are fp32 where that holds them and 64 bits
  * elsewhere, their sums 64 bits: values from the smallest to the largest of their
  * type are counted.  A NaN makes the norm and the result NaN; a norm that is
- * infinite, or too large for a float, makes the factor 0. */
+ * infinite, or too large for a float, makes the factor 0 (for a finite max_norm). */
 
 /* Device workspace of the two calls; 0 for unsupported counts.  Host-only. */
 size_t cfc_grad_clip_workspace_bytes(int count);
@@ -557,7 +557,7 @@ int cfc_grad_norm(const void* const* grads, const long long* n_values, const int
 
 /* out[i] may be grads[i]; otherwise no out overlaps a gradient or another out,
  * and no gradient may be named twice where it is its own out.  max_norm >= 0
- * (infinity: no clipping); otherwise CFC_ERR_SHAPE. */
+ * (infinity: no clipping, whatever the norm but a NaN); otherwise CFC_ERR_SHAPE. */
 int cfc_grad_clip(const void* const* grads, void* const* out, const long long* n_values, const int* math, int count,
                   float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -139,7 +139,8 @@ __device__ __forceinline__ void scale(const void* in, void* out, int n, float c)
     rows::store1(static_cast<typename V::E*>(out) + i, rows::load1(static_cast<const typename V::E*>(in) + i) * c);
 }
 
-// c = min(1, most / (norm + 1e-6)); a NaN stays one, and an infinite norm gives 0.
+// c = min(1, most / (norm + 1e-6)); a NaN stays one, and an infinite norm gives 0, but for
+// most = infinity, which is 1 whatever the norm (the quotient of the two would be a NaN).
 __global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__ Table t, const double* sums, int n_sums,
                                                          float most, float* norm) {
   double v = 0;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) k_grad_scale(const __grid_constant__
   const float length = (float)sqrt(block_sum(v));
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = length;
   float c = most / (length + 1e-6f);
-  if (c > 1.f) c = 1.f;
+  if (c > 1.f || (isinf(most) && !isnan(length))) c = 1.f;
   const int items = t.first[t.count];
   for (int j = blockIdx.x; j < items; j += gridDim.x) {
     const Span s = span_of(t, items - 1 - j);

@@ -206,3 +206,18 @@ def test_refusals_of_the_binding():
         flat = torch.zeros(32, device="cuda")
         cfc.cfc_grad_clip([flat[:16]], 1.0, norm, ws, out=[flat[8:24]])
     assert np.isfinite(norm_of(g))
+
+
+def test_infinity_never_clips():
+    """max_norm infinite: gradients stay as they are, also where the norm itself is infinite or too large for a float."""
+    torch = torch_mod()
+    inf = float("inf")
+    for grads in ([torch.full((300,), 1e38, device="cuda"), torch.randn(7, device="cuda")],
+                  [torch.tensor([inf, 1.0, -2.0], device="cuda"), torch.randn(40000, device="cuda").to(torch.bfloat16)]):
+        before = [g.clone() for g in grads]
+        out = [torch.full_like(g, float("nan")) for g in grads]
+        assert clip(grads, inf, out) == inf and clip(grads, inf) == inf
+        for b, o, g in zip(before, out, grads):
+            assert torch.equal(b, o) and torch.equal(b, g)
+    grads = [torch.tensor([float("nan"), 1.0], device="cuda"), torch.ones(5, device="cuda")]
+    assert math.isnan(clip(grads, inf)) and all(g.isnan().all() for g in grads)        # a NaN is not hidden
