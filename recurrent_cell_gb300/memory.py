@@ -77,14 +77,20 @@ def residual_norm(x, weight, residual=None, eps=1e-6):
     return _Norm.apply(x, residual, weight, eps)
 
 
+def _backward_may_come(ctx, graded):
+    """Whether a forward has to keep what its backward reads.  graded: whether gradients were on around the call; inside
+    of it they never are, and needs_input_grad says only which inputs would want one."""
+    return graded and any(ctx.needs_input_grad)
+
+
 class _Rule(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, seq_offsets, initial_state, want_state):
+    def forward(ctx, q, k, v, g, beta, seq_offsets, initial_state, want_state, graded):
         packed = seq_offsets is not None
         n = seq_offsets.numel() - 1 if packed else v.shape[0]
         hk, dk, hv, dv = *q.shape[-2:], *v.shape[-2:]
         rows, math = v[..., 0, 0].numel(), _math(q.dtype)
-        save = any(ctx.needs_input_grad)
+        save = _backward_may_come(ctx, graded)
         ws = _workspace(cfc_gdr_workspace_bytes(rows, n, hk, hv, dk, dv, math, save), q.device)
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         state = torch.empty(n, hv, dk, dv, device=q.device) if want_state else None
@@ -106,14 +112,14 @@ class _Rule(torch.autograd.Function):
         cfc_gdr_backward(q, k, v, g, beta, grad_o, *grads, ctx.ws, seq_offsets=seq_offsets,
                          grad_final_state=None if grad_state is None else grad_state.contiguous(),
                          grad_initial_state=grad_init, math=_math(q.dtype))
-        return *grads[:3], grads[3].float(), grads[4].float(), None, grad_init, None
+        return *grads[:3], grads[3].float(), grads[4].float(), None, grad_init, None, None
 
 
 def gated_delta_rule(q, k, v, g, beta, seq_offsets=None, initial_state=None, want_state=False):
     """(o, final state or None) over whole sequences: q, k [sequences, tokens, k_heads, d_k],
     v [sequences, tokens, v_heads, d_v], g, beta [sequences, tokens, v_heads], or
     all of them packed [rows, ...] with seq_offsets, the last of which is rows (no padding).  scale = d_k ** -0.5."""
-    return _Rule.apply(q, k, v, g, beta, seq_offsets, initial_state, want_state)
+    return _Rule.apply(q, k, v, g, beta, seq_offsets, initial_state, want_state, torch.is_grad_enabled())
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -192,10 +198,10 @@ def causal_conv(x, weight, bias=None, seq_offsets=None, initial_state=None, want
 
 class _Scan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial_state, want_state):
+    def forward(ctx, x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial_state, want_state, graded):
         n = x.shape[0] if seq_offsets is None else seq_offsets.numel() - 1
         (d, N), groups, rows, math = A.shape, B.shape[-2], x[..., 0].numel(), _math(x.dtype)
-        save = any(ctx.needs_input_grad)
+        save = _backward_may_come(ctx, graded)
         ws = _workspace(cfc_ssm_workspace_bytes(rows, n, d, groups, N, math, save), x.device)
         y = _by_rows(x, seq_offsets)
         state = torch.empty(n, d, N, device=x.device) if want_state else None
@@ -218,14 +224,14 @@ class _Scan(torch.autograd.Function):
                          grad_D=gD, grad_z=gz, grad_delta_bias=gbias, seq_offsets=seq_offsets, initial_state=initial,
                          grad_final_state=None if grad_state is None else grad_state.contiguous(),
                          grad_initial_state=ginit, math=_math(x.dtype))
-        return gx, gdelta, gA, gB, gC, gD, gz, gbias, None, ginit, None
+        return gx, gdelta, gA, gB, gC, gD, gz, gbias, None, ginit, None, None
 
 
 def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, seq_offsets=None, initial_state=None, want_state=False):
     """(y, final state or None) over whole sequences: x, delta, z [sequences, tokens, channels], A [channels, states],
     B, C [sequences, tokens, groups, states], or all but A packed [rows, ...] with seq_offsets (rows from seq_offsets[-1]
     on are padding: y is zero there, and they have no part in any gradient)."""
-    return _Scan.apply(x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial_state, want_state)
+    return _Scan.apply(x, delta, A, B, C, D, z, delta_bias, seq_offsets, initial_state, want_state, torch.is_grad_enabled())
 
 
 @torch.no_grad()

@@ -230,3 +230,31 @@ def test_padding_of_the_operators_is_zero(stale):
     for t in (x, delta, z, B, C):
         assert t.grad.isfinite().all() and not t.grad[30:].any() and t.grad[:30].any()
     assert weight.grad.isfinite().all()
+
+
+@pytest.mark.parametrize("kind", ["scan", "rule"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_a_prompt_without_gradients_takes_less_memory_and_gives_the_same_bits(kind, dtype):
+    torch = torch_mod()
+    from recurrent_cell_gb300.memory import MemoryBlock, ScanBlock
+    torch.manual_seed(8)
+    dt = getattr(torch, dtype)
+    block = ScanBlock(64, dtype=dt) if kind == "scan" else MemoryBlock(64, 2, 2, 32, 32, dt)
+    x = torch.randn(2, 300, 64, device="cuda").to(dt)
+
+    def run():
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out, stream, state = block(x, None, want_state=True)
+        return out, stream, state if kind == "scan" else (state,), torch.cuda.max_memory_allocated() - before
+
+    out, stream, state, most = run()
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            o, s, last, some = run()
+            assert torch.equal(o, out) and torch.equal(s, stream) and some < most
+            assert all(torch.equal(a, b) for a, b in zip(last, state))
+    out = block(x, None)[0]
+    with torch.no_grad():
+        assert torch.equal(block(x, None)[0], out)                 # nor without a final state

@@ -43,3 +43,33 @@ def test_rows_behind_the_last_sequence_are_zero(stale, monkeypatch):
     o.sum().backward()
     for t in (y, o, x.grad, delta.grad, z.grad, B.grad, C.grad):
         assert (t[:USED] == 1).all() and (t[USED:] == 0).all()
+
+
+@pytest.fixture
+def saves(monkeypatch):
+    """What the workspaces and the forwards of the scan and the rule are told about a backward to come."""
+    told = []
+    for op in ("ssm", "gdr"):
+        monkeypatch.setattr(memory, f"cfc_{op}_workspace_bytes", lambda *a: told.append(("size", bool(a[-1]))) or 16)
+        monkeypatch.setattr(memory, f"cfc_{op}_forward", lambda *a, save, **kw: told.append(("call", save)))
+    return told
+
+
+def scan(of):
+    return memory.selective_scan(of(2, 5, D), of(2, 5, D), of(D, N), of(2, 5, 1, N), of(2, 5, 1, N), of(D), of(2, 5, D), of(D))
+
+
+def rule(of):
+    return memory.gated_delta_rule(of(2, 5, 1, D), of(2, 5, 1, D), of(2, 5, 1, D), of(2, 5, 1), of(2, 5, 1))
+
+
+@pytest.mark.parametrize("op", [scan, rule])
+def test_a_forward_keeps_what_a_backward_needs_only_where_one_can_come(saves, op):
+    leaf, plain = (lambda *s: torch.zeros(*s, requires_grad=True)), torch.zeros
+    for of, mode, want in ((leaf, torch.enable_grad, True), (leaf, torch.no_grad, False), (leaf, torch.inference_mode, False),
+                           (plain, torch.enable_grad, False), (plain, torch.no_grad, False)):
+        saves.clear()
+        with mode():
+            out, _ = op(of)
+        assert saves == [("size", want), ("call", want)], mode
+        assert out.requires_grad == want
