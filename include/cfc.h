@@ -439,8 +439,9 @@ int cfc_layernorm_backward(const void* s, const float* weight, const float* mean
  * output, so that a batch may be padded.  Nothing outside the tensors is touched
  * whatever the array holds.
  * Sizes: channels a multiple of 8, 2 <= width <= 8, 1 <= n_seq <= 2^20,
- * 0 <= rows <= 2^30.  Pointers 16-byte aligned (bias, seq_offsets, slots: 4).  Outputs
- * overlap neither inputs nor one another (CFC_ERR_OVERLAP where that is seen).
+ * 0 <= rows <= 2^30.  Pointers 16-byte aligned (bias, seq_offsets, slots: 4).  Outputs,
+ * a step's pool and the workspace among them, overlap neither inputs nor one another:
+ * CFC_ERR_OVERLAP (rows that are parts of wider ones count by what they hold).
  *
  * Sums are fp32.  A NaN or an infinity reaches the `width` rows that see it, of
  * its own channel and sequence. */
@@ -491,8 +492,7 @@ int cfc_conv_step(const void* x, long long x_stride, const float* weight, const 
  * <= 2^30.  x, delta, z, y, states, gradients and the workspace are 16-byte aligned;
  * B and C to their type (rows of whole 16-byte vectors, with 8, 16, 32 or 64
  * states, are read faster); grad_B, grad_C, A, D, delta_bias and their gradients 4
- * bytes.  Outputs overlap neither inputs nor one another (CFC_ERR_OVERLAP where
- * that is seen).
+ * bytes.  Nothing that is written overlaps anything else, as for cfc_conv_forward.
  *
  * All arithmetic is fp32: states are good to about 1e-6 of their size times the
  * number of tokens that they remember, outputs to their rounding.  A NaN or an infinity

@@ -4,6 +4,7 @@
 // As in api.cu every argument is checked on the host before anything is enqueued;
 // no allocation, no synchronisation, no host read of device data.
 #include <algorithm>
+#include <climits>
 #include <initializer_list>
 #include <new>
 
@@ -27,15 +28,38 @@ bool missing(std::initializer_list<const void*> ptrs) {
     if (!p) return true;
   return false;
 }
-// Whether two buffers (NULL: none) share a byte.
-bool overlap(const void* a, long long na, const void* b, long long nb) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a && b && na > 0 && nb > 0 && p < q + (uintptr_t)nb && q < p + (uintptr_t)na;
-}
 int size_of(int math) { return math == CFC_MATH_BF16 ? 2 : 4; }
-// Bytes from the first to the last element of rows that are ld apart.
-long long extent(long long rows, long long ld, long long width, int math) {
-  return rows < 1 ? 0 : ((rows - 1) * ld + width) * size_of(math);
+// a b, or the largest number where that is more (of a pool whose number of slots is the caller's).
+long long times(long long a, long long b) {
+  long long r;
+  return __builtin_mul_overflow(a, b, &r) ? LLONG_MAX : r;
+}
+// What a call reads or writes: `rows` rows of `bytes` bytes, `pitch` apart (NULL: nothing).
+struct Area {
+  const void* at;
+  long long rows, pitch, bytes;
+};
+Area dense(const void* p, long long bytes) { return Area{p, 1, 0, bytes}; }
+Area spaced(const void* p, long long rows, long long ld, long long width, int math) {
+  return Area{p, rows, ld * size_of(math), width * size_of(math)};
+}
+// Whether a dense area shares a byte with a row of another: with the first that ends behind its beginning.
+bool meet(const Area& a, const Area& b) {
+  if (!a.at || !b.at || a.rows < 1 || b.rows < 1 || a.bytes < 1 || b.bytes < 1) return false;
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+  const uintptr_t end = p + (uintptr_t)a.bytes, first = q + (uintptr_t)b.bytes;
+  const uintptr_t k = p < first ? 0 : b.rows > 1 ? (p - first) / (uintptr_t)b.pitch + 1 : 1;
+  return k < (uintptr_t)b.rows && q + k * (uintptr_t)b.pitch < end;
+}
+// Whether outputs (all dense) overlap neither inputs nor one another.
+bool apart(std::initializer_list<Area> outs, std::initializer_list<Area> ins) {
+  for (const Area* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Area* other = outs.begin(); other != o; ++other)
+      if (meet(*o, *other)) return false;
+    for (const Area& in : ins)
+      if (meet(*o, in)) return false;
+  }
+  return true;
 }
 bool mode_ok(int math) { return math == CFC_MATH_FP32 || math == CFC_MATH_BF16; }
 // Rows at least as far apart as they are wide, whole 16-byte vectors.
@@ -68,6 +92,11 @@ int conv_check(int channels, int width, int math) {
   return channels < 8 || channels > kMaxChannels || channels % 8 != 0 || width < 2 || width > kMaxConvWidth ? CFC_ERR_SHAPE
                                                                                                         : CFC_OK;
 }
+// Its outputs against its inputs and up to three more.
+bool conv_apart(const ConvArgs& a, std::initializer_list<Area> outs, Area first = {}, Area second = {}, Area third = {}) {
+  return apart(outs, {spaced(a.x, a.rows, a.ldx, a.d, a.math), dense(a.weight, 4ll * a.d * a.width), dense(a.bias, 4ll * a.d),
+                      dense(a.off, 4ll * (a.n_seq + 1)), first, second, third});
+}
 // Blocks of a launch, one a tile of 16 rows and 128 vectors of 4 channels at most, and the states'.
 bool conv_blocks_ok(long long rows, int n_seq, int channels) {
   return (rows / 16 + 1 + n_seq) * (channels / 4) / 128 < 0x7ffffff0ll;
@@ -95,13 +124,14 @@ struct SsmIn {
            aligned({a.A, a.D, a.bias, a.off}, 4);
   }
   bool null() const { return a.rows > 0 && missing({a.x, a.delta, a.A, a.B, a.C}); }
-  // whether a dense output [rows, channels] overlaps an input of that kind
-  bool meets(const void* y) const {
-    const long long n = extent(a.rows, a.d, a.d, a.math);
-    return overlap(y, n, a.x, extent(a.rows, a.ldx, a.d, a.math)) ||
-           overlap(y, n, a.delta, extent(a.rows, a.ldd, a.d, a.math)) ||
-           overlap(y, n, a.z, extent(a.rows, a.ldz, a.d, a.math));
+  bool apart(std::initializer_list<Area> outs, Area first = {}, Area second = {}) const {
+    const long long bc = (long long)a.groups * a.N, d4 = 4ll * a.d;
+    return cfc::apart(outs, {spaced(a.x, a.rows, a.ldx, a.d, a.math), spaced(a.delta, a.rows, a.ldd, a.d, a.math),
+                             spaced(a.z, a.rows, a.ldz, a.d, a.math), spaced(a.B, a.rows, a.ldb, bc, a.math),
+                             spaced(a.C, a.rows, a.ldc, bc, a.math), dense(a.A, d4 * a.N), dense(a.D, d4), dense(a.bias, d4),
+                             dense(a.off, 4ll * (a.n_seq + 1)), dense(a.init, state_bytes()), first, second});
   }
+  long long row_bytes() const { return a.rows * a.d * size_of(a.math); }
   long long state_bytes() const { return 4ll * a.n_seq * a.d * a.N; }
 };
 SsmIn ssm_in(const void* x, long long ldx, const void* delta, long long ldd, const float* A, const void* B, long long ldb,
@@ -161,12 +191,9 @@ int cfc_conv_forward(const void* x, long long x_stride, const float* weight, con
   if (!stride_ok(x_stride, channels, math) || !conv_blocks_ok(rows, n_seq, channels)) return CFC_ERR_SHAPE;
   if (!weight || (rows > 0 && missing({x, y}))) return CFC_ERR_NULL;
   if (!aligned({x, weight, initial_state, y, final_state}, 16) || !aligned({bias, seq_offsets}, 4)) return CFC_ERR_ALIGN;
-  const long long state = (long long)n_seq * (width - 1) * channels * size_of(math), out = extent(rows, channels, channels, math);
-  const long long in = extent(rows, x_stride, channels, math);
-  if (overlap(y, out, x, in) || overlap(final_state, state, initial_state, state) || overlap(final_state, state, x, in) ||
-      overlap(y, out, initial_state, state) || overlap(y, out, final_state, state))
-    return CFC_ERR_OVERLAP;
-  ConvArgs a{x, x_stride, weight, bias, initial_state, seq_offsets, n_seq, rows, channels, width, silu != 0, math};
+  const ConvArgs a{x, x_stride, weight, bias, initial_state, seq_offsets, n_seq, rows, channels, width, silu != 0, math};
+  const long long state = (long long)n_seq * (width - 1) * channels * size_of(math), out = rows * channels * size_of(math);
+  if (!conv_apart(a, {dense(y, out), dense(final_state, state)}, dense(initial_state, state))) return CFC_ERR_OVERLAP;
   return done(launch_conv_forward(a, y, final_state, as_stream(stream)));
 }
 
@@ -188,13 +215,12 @@ int cfc_conv_backward(const void* x, long long x_stride, const float* weight, co
   if (!aligned({x, weight, initial_state, grad_y, grad_final_state, grad_x, grad_weight, grad_initial_state, workspace}, 16) ||
       !aligned({bias, seq_offsets, grad_bias}, 4))
     return CFC_ERR_ALIGN;
-  const long long state = (long long)n_seq * (width - 1) * channels * size_of(math), out = extent(rows, channels, channels, math);
-  if (overlap(grad_x, out, x, extent(rows, x_stride, channels, math)) || overlap(grad_x, out, grad_y, out) ||
-      overlap(grad_initial_state, state, initial_state, state) ||
-      overlap(grad_initial_state, state, grad_final_state, state) || overlap(grad_initial_state, state, grad_x, out) ||
-      overlap(grad_x, out, initial_state, state) || overlap(grad_x, out, grad_final_state, state))
+  const ConvArgs a{x, x_stride, weight, bias, initial_state, seq_offsets, n_seq, rows, channels, width, silu != 0, math};
+  const long long state = (long long)n_seq * (width - 1) * channels * size_of(math), out = rows * channels * size_of(math);
+  if (!conv_apart(a, {dense(grad_x, out), dense(grad_weight, 4ll * channels * width), dense(grad_bias, 4ll * channels),
+                      dense(grad_initial_state, state), dense(workspace, conv_workspace(rows, channels, width))},
+                  dense(initial_state, state), dense(grad_y, out), dense(grad_final_state, state)))
     return CFC_ERR_OVERLAP;
-  ConvArgs a{x, x_stride, weight, bias, initial_state, seq_offsets, n_seq, rows, channels, width, silu != 0, math};
   return done(launch_conv_backward(a, grad_y, grad_final_state, grad_x, grad_weight, grad_bias, grad_initial_state,
                                    static_cast<float*>(workspace), as_stream(stream)));
 }
@@ -210,8 +236,10 @@ int cfc_conv_step(const void* x, long long x_stride, const float* weight, const 
   if (missing({x, weight, y}) || (n_slots > 0 && !state)) return CFC_ERR_NULL;
   if (!aligned({x, weight, state, y}, 16) || !aligned({bias, slots}, 4)) return CFC_ERR_ALIGN;
   const long long rows = (long long)n_seq * tokens;
-  if (overlap(y, extent(rows, channels, channels, math), x, extent(rows, x_stride, channels, math))) return CFC_ERR_OVERLAP;
-  ConvArgs a{x, x_stride, weight, bias, nullptr, nullptr, n_seq, rows, channels, width, silu != 0, math};
+  const ConvArgs a{x, x_stride, weight, bias, nullptr, nullptr, n_seq, rows, channels, width, silu != 0, math};
+  if (!conv_apart(a, {dense(y, rows * channels * size_of(math)),
+                      dense(state, times(n_slots, (width - 1ll) * channels * size_of(math)))}, dense(slots, 4ll * n_seq)))
+    return CFC_ERR_OVERLAP;
   return done(launch_conv_step(a, tokens, state, n_slots, slots, y, as_stream(stream)));
 }
 
@@ -233,10 +261,10 @@ int cfc_ssm_forward(const void* x, long long x_stride, const void* delta, long l
                           seq_offsets, n_seq, rows, channels, groups, n_states, math, initial_state, workspace);
   if ((st = in.check_strides()) != CFC_OK) return st;
   if (in.null() || (rows > 0 && !y)) return CFC_ERR_NULL;
-  if (!workspace || workspace_bytes < ssm_workspace(rows, n_seq, channels, groups, n_states, save != 0))
-    return CFC_ERR_WORKSPACE;
+  const size_t need = ssm_workspace(rows, n_seq, channels, groups, n_states, save != 0);
+  if (!workspace || workspace_bytes < need) return CFC_ERR_WORKSPACE;
   if (!in.aligned_ok() || !aligned({y, final_state}, 16)) return CFC_ERR_ALIGN;
-  if (in.meets(y) || overlap(initial_state, in.state_bytes(), final_state, in.state_bytes())) return CFC_ERR_OVERLAP;
+  if (!in.apart({dense(y, in.row_bytes()), dense(final_state, in.state_bytes()), dense(workspace, need)})) return CFC_ERR_OVERLAP;
   return done(launch_ssm_forward(in.a, y, final_state, save != 0, as_stream(stream)));
 }
 
@@ -255,16 +283,16 @@ int cfc_ssm_backward(const void* x, long long x_stride, const void* delta, long 
   if ((st = in.check_strides()) != CFC_OK) return st;
   if (in.null() || !grad_A || (rows > 0 && (missing({grad_y, grad_x, grad_delta, grad_B, grad_C}) || (z && !grad_z))))
     return CFC_ERR_NULL;
-  if (!workspace || workspace_bytes < ssm_workspace(rows, n_seq, channels, groups, n_states, 1)) return CFC_ERR_WORKSPACE;
+  const size_t need = ssm_workspace(rows, n_seq, channels, groups, n_states, 1);
+  if (!workspace || workspace_bytes < need) return CFC_ERR_WORKSPACE;
   if (!in.aligned_ok() || !aligned({grad_y, grad_final_state, grad_x, grad_delta, grad_z, grad_initial_state}, 16) ||
       !aligned({grad_A, grad_B, grad_C, grad_D, grad_delta_bias}, 4))
     return CFC_ERR_ALIGN;
-  const long long out = extent(rows, channels, channels, math);
-  if (in.meets(grad_x) || in.meets(grad_delta) || in.meets(grad_z) || overlap(grad_x, out, grad_delta, out) ||
-      overlap(grad_x, out, grad_z, out) || overlap(grad_delta, out, grad_z, out) || overlap(grad_x, out, grad_y, out) ||
-      overlap(grad_delta, out, grad_y, out) || overlap(grad_z, out, grad_y, out) ||
-      overlap(grad_initial_state, in.state_bytes(), initial_state, in.state_bytes()) ||
-      overlap(grad_initial_state, in.state_bytes(), grad_final_state, in.state_bytes()))
+  const long long out = in.row_bytes(), bc = rows * groups * n_states * size_of(math), d4 = 4ll * channels;
+  if (!in.apart({dense(grad_x, out), dense(grad_delta, out), dense(z ? grad_z : nullptr, out), dense(grad_B, bc), dense(grad_C, bc),
+                 dense(grad_A, d4 * n_states), dense(grad_D, d4), dense(grad_delta_bias, d4),
+                 dense(grad_initial_state, in.state_bytes()), dense(workspace, need)},
+                dense(grad_y, out), dense(grad_final_state, in.state_bytes())))
     return CFC_ERR_OVERLAP;
   const SsmGrads r{grad_y, grad_final_state, grad_x, grad_delta, z ? grad_z : nullptr, grad_B, grad_C,
                    grad_A, grad_D, grad_delta_bias, grad_initial_state};
@@ -285,7 +313,8 @@ int cfc_ssm_step(const void* x, long long x_stride, const void* delta, long long
   if ((st = in.check_strides()) != CFC_OK) return st;
   if (in.null() || !y || (n_slots > 0 && !state)) return CFC_ERR_NULL;
   if (!in.aligned_ok() || !aligned({state, y}, 16) || !aligned({slots}, 4)) return CFC_ERR_ALIGN;
-  if (in.meets(y)) return CFC_ERR_OVERLAP;
+  if (!in.apart({dense(y, in.row_bytes()), dense(state, times(n_slots, 4ll * channels * n_states))}, dense(slots, 4ll * n_seq)))
+    return CFC_ERR_OVERLAP;
   return done(launch_ssm_step(in.a, tokens, state, n_slots, slots, y, as_stream(stream)));
 }
 

@@ -266,3 +266,44 @@ def test_a_trunk_of_an_unknown_kind_is_refused():
     from recurrent_cell_gb300.memory import MemoryCell
     with pytest.raises(ValueError, match="kind"):
         MemoryCell(16, 8, device="cpu", kind="other")
+
+
+# (call, what it writes, a pool of states and the workspace among it, and what it only reads)
+APART = [
+    (conv_forward, "y final", "x w b off init"),
+    (conv_backward, "gx gw gb ginit ws", "x w b off init gy gfinal"),
+    (conv_step, "y state", "x w b slots"),
+    (scan_forward, "y final ws", "x delta A B C D z bias off init"),
+    (scan_backward, "gx gdelta gA gB gC gD gz gbias ginit ws", "x delta A B C D z bias off init gy gfinal"),
+    (scan_step, "y state", "x delta A B C D z bias slots"),
+]
+
+
+@pytest.mark.parametrize("call,outs,ins", APART, ids=lambda v: getattr(v, "__name__", ""))
+def test_no_output_may_overlap_anything(lib, call, outs, ins):
+    """Every output against every input and every other output."""
+    outs, ins = outs.split(), ins.split()
+    where = {n: far(100 + i) for i, n in enumerate(outs + ins)}
+    given = dict(where)
+    if "slots" in ins:
+        given["n_slots"] = 5                     # a pool of more slots than sequences
+    for i, out in enumerate(outs):
+        for other in ins + outs[:i]:
+            for a, b in ((out, other), (other, out)):
+                assert call(lib, **dict(given, **{a: where[b]})) == ERR_OVERLAP, (a, "at", b)
+
+
+def test_the_last_rows_and_slots_count(lib):
+    """Ranges end where the tensors do: in rows that are parts of wider ones, and in the last slot of a pool."""
+    row = 2 * 40                                 # of B and C, in bytes; x's are 256 and hold 128, delta's 128
+    for call in (scan_forward, scan_step):
+        rows = 30 if call is scan_forward else 6
+        for n in ("B", "C"):
+            assert call(lib, y=SCAN[n] + (rows - 1) * row // 16 * 16) == ERR_OVERLAP
+        assert call(lib, y=SCAN["z"] + (rows - 1) * 256 + 112) == ERR_OVERLAP
+    slot = 64 * 16 * 4
+    assert scan_step(lib, n_slots=9, y=far(8) + 9 * slot - 16) == ERR_OVERLAP
+    assert scan_step(lib, n_slots=9, x=far(8) + 9 * slot - 16) == ERR_OVERLAP
+    assert conv_step(lib, n_slots=9, y=far(3) + 9 * 3 * 64 * 2 - 16) == ERR_OVERLAP
+    assert conv_step(lib, n_slots=1 << 62, slots=far(30), y=far(50)) == ERR_OVERLAP
+    assert scan_backward(lib, gB=far(18) + 16, gC=far(18)) == ERR_OVERLAP and scan_backward(lib, gA=far(21)) == ERR_OVERLAP

@@ -275,3 +275,22 @@ def test_refusals_of_the_binding():
         cfc.cfc_conv_forward(c.x, c.w, y, initial_state=c.init, final_state=c.init)
     with pytest.raises(ValueError, match="slots"):
         cfc.cfc_conv_step(c.x, c.w, c.init[:, :2], y)
+
+
+@MODES
+def test_an_output_between_the_rows_of_an_input(math):
+    """Overlap is seen row by row: y may lie in what the rows of a wider tensor leave of it, and not a vector further."""
+    torch = torch_mod()
+    c = Conv([3], 16, 4, math, seed=21, uniform=True, wide=False)
+    want, _ = c.forward()
+    buffer = torch.full((3, 128), float("nan"), dtype=c.dt, device="cuda")
+    x = buffer[None, :, :16]
+    x.copy_(c.x)
+    y = buffer[1, 16:16 + 48].view(1, 3, 16)
+    call = lambda y: cfc.cfc_conv_forward(x, c.w, y, bias=c.b, initial_state=c.init, math=math)  # noqa: E731
+    call(y)
+    assert torch.equal(y, want) and torch.equal(x, c.x)
+    with pytest.raises(cfc.CfcError, match="overlap"):
+        call(buffer[1, 8:56].view(1, 3, 16))
+    with pytest.raises(cfc.CfcError, match="overlap"):
+        call(buffer.view(-1)[128 + 88:][:48].view(1, 3, 16))       # runs into the third row
