@@ -556,7 +556,8 @@ int cfc_grad_norm(const void* const* grads, const long long* n_values, const int
                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* out[i] may be grads[i]; otherwise no out overlaps a gradient or another out,
- * and no gradient may be named twice where it is its own out.  max_norm >= 0
+ * and no gradient may be named twice where it is its own out; norm overlaps
+ * neither, and in both calls the workspace nothing at all (CFC_ERR_OVERLAP).  max_norm >= 0
  * (infinity: no clipping, whatever the norm but a NaN); otherwise CFC_ERR_SHAPE. */
 int cfc_grad_clip(const void* const* grads, void* const* out, const long long* n_values, const int* math, int count,
                   float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream);

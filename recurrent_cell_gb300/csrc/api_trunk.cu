@@ -357,15 +357,22 @@ static int grad_call(const void* const* grads, void* const* out, bool clip, cons
                      int count, float max_norm, float* norm, void* workspace, size_t workspace_bytes, void* stream) {
   if (count < 0 || count > kMaxTensors || !(max_norm >= 0.f)) return CFC_ERR_SHAPE;
   if (!norm || (count > 0 && (!grads || !n_values || !math || (clip && !out)))) return CFC_ERR_NULL;
+  const long long need = grad_workspace(count);
+  bool meets = meet(dense(norm, 4), dense(workspace, need));
   for (int i = 0; i < count; ++i) {
     if (!mode_ok(math[i])) return CFC_ERR_MODE;
     if (n_values[i] < 0 || n_values[i] > kMaxGradValues) return CFC_ERR_SHAPE;
     if (n_values[i] == 0) continue;
     if (!grads[i] || (clip && !out[i])) return CFC_ERR_NULL;
     if (!aligned({grads[i], clip ? out[i] : nullptr}, size_of(math[i]))) return CFC_ERR_ALIGN;
+    // the sums, and in clipping the norm, are written while tensors are still to be read
+    const long long bytes = n_values[i] * size_of(math[i]);
+    for (const void* p : {grads[i], clip ? static_cast<const void*>(out[i]) : nullptr})
+      meets |= meet(dense(workspace, need), dense(p, bytes)) || (clip && meet(dense(norm, 4), dense(p, bytes)));
   }
-  if (!workspace || workspace_bytes < grad_workspace(count)) return CFC_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < (size_t)need) return CFC_ERR_WORKSPACE;
   if (!aligned({workspace}, 16) || !aligned({norm}, 4)) return CFC_ERR_ALIGN;
+  if (meets) return CFC_ERR_OVERLAP;
   if (const int st = clip ? check_apart(grads, out, n_values, math, count) : CFC_OK; st != CFC_OK) return st;
   return done(launch_grad_norm(grads, clip ? out : nullptr, n_values, math, count, max_norm, norm,
                                static_cast<double*>(workspace), as_stream(stream)));

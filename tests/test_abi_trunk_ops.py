@@ -307,3 +307,16 @@ def test_the_last_rows_and_slots_count(lib):
     assert conv_step(lib, n_slots=9, y=far(3) + 9 * 3 * 64 * 2 - 16) == ERR_OVERLAP
     assert conv_step(lib, n_slots=1 << 62, slots=far(30), y=far(50)) == ERR_OVERLAP
     assert scan_backward(lib, gB=far(18) + 16, gC=far(18)) == ERR_OVERLAP and scan_backward(lib, gA=far(21)) == ERR_OVERLAP
+
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_the_norm_and_the_sums_lie_in_no_tensor(lib, clip):
+    need = cfc.cfc_grad_clip_workspace_bytes(2)
+    assert grads(lib, clip, ws=far(0) + 32) == ERR_OVERLAP and grads(lib, clip, ws=far(1) - need + 16) == ERR_OVERLAP
+    assert grads(lib, clip, ws=far(60), norm=far(60) + need - 4) == ERR_OVERLAP
+    if clip:
+        for at in (far(0), far(0) + 36, far(1) + 4):
+            assert grads(lib, clip, outs=(far(2), far(3)), norm=at) == ERR_OVERLAP        # written while others are read
+            assert grads(lib, clip, norm=at) == ERR_OVERLAP
+        assert grads(lib, clip, outs=(far(2), far(3)), norm=far(2) + 36) == ERR_OVERLAP
+        assert grads(lib, clip, outs=(far(2), far(3)), ws=far(3) - need + 16) == ERR_OVERLAP
