@@ -221,3 +221,25 @@ def test_infinity_never_clips():
             assert torch.equal(b, o) and torch.equal(b, g)
     grads = [torch.tensor([float("nan"), 1.0], device="cuda"), torch.ones(5, device="cuda")]
     assert math.isnan(clip(grads, inf)) and all(g.isnan().all() for g in grads)        # a NaN is not hidden
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_what_lies_beside_unaligned_parts_is_left_alone(dtype):
+    """In place and into other tensors: nothing before, between or behind the parts is written."""
+    torch = torch_mod()
+    for into in (False, True):
+        flat = torch.randn(100_011, device="cuda").to(getattr(torch, dtype))
+        other = torch.randn(100_011, device="cuda").to(flat.dtype)
+        kept, kept_other = flat.clone(), other.clone()
+        spans = [(1, 40_000), (40_001, 40_004), (40_007, 100_003)]
+        parts = [flat[a:b] for a, b in spans]
+        before = [p.clone() for p in parts]
+        after = [other[a:b] for a, b in spans] if into else parts
+        check(before, after, clip(parts, 1.0, after if into else None), 1.0)
+        beside = torch.ones(flat.numel(), dtype=torch.bool, device="cuda")
+        for a, b in spans:
+            beside[a:b] = False
+        assert int(beside.sum()) == 1 + 1 + 3 + 8
+        assert torch.equal(flat[beside], kept[beside]) and torch.equal(other[beside], kept_other[beside])
+        if into:
+            assert torch.equal(flat, kept)
