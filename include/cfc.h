@@ -495,7 +495,8 @@ int cfc_conv_step(const void* x, long long x_stride, const float* weight, const 
  * bytes.  Nothing that is written overlaps anything else, as for cfc_conv_forward.
  *
  * All arithmetic is fp32: states are good to about 1e-6 of their size times the
- * number of tokens that they remember, outputs to their rounding.  A NaN or an infinity
+ * number of tokens that they remember, outputs as their sums of states, with |z| 6e-8
+ * of the gate and their rounding on top.  A NaN or an infinity
  * at a token reaches that token's and, through the state, its sequence's later
  * outputs (of x, delta and z of its own channel); no earlier token and no other
  * sequence.  The gradients of a sequence in which anything is not finite are

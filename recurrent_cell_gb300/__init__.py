@@ -809,7 +809,7 @@ def cfc_grad_norm(grads, norm, workspace, stream=None):
 
 def cfc_grad_clip(grads, max_norm, norm, workspace, out=None, stream=None):
     """norm [1] of the tensors together, and each scaled by min(1, max_norm / (norm + 1e-6)):
-    in place, or into the tensors of out (alike in shape and type)."""
+    in place, or into the tensors of out (each with as many values, of the same type)."""
     grads = list(grads)
     ptrs, sizes, maths = _tensor_list(grads, "grads")
     outs = ptrs

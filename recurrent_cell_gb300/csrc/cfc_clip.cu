@@ -10,7 +10,8 @@
 // atomics, and an order that depends on the sizes alone.  Every block of the second
 // kernel adds those sums in the same order, which costs it a few kilobytes from L2
 // and saves a launch; it takes the items backwards, so that it first meets those
-// that the first kernel left in L2.  588 million values of both types: 165 us for the norm (1.18 GB,
+// that the first kernel left in L2.  (Those sums are of all tables of kTensors: beyond some thousands of
+// tensors each launch reads ever more of them.)  588 million values of both types: 165 us for the norm (1.18 GB,
 // 7.1 TB/s), 360 to scale (2.35 GB, 6.4 TB/s, a copy's rate); with items of 8192 values 585 us in all.
 #include "row_ops.cuh"
 

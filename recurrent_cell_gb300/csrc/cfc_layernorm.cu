@@ -14,8 +14,9 @@
 // Memory is the bound in both directions, so a row is read once: 8 to 32 lanes a row up to 4
 // vectors of 16 bytes each, a block a row beyond that (row_ops.cuh).  Vectors are copied into
 // shared memory two rows ahead, each thread its own, and values go in pairs, since issue is
-// the next bound: 16383 x 2560 in bfloat16 takes 55 us forward (6.1 TB/s) and 71 backward, with four
-// blocks of five warps an SM (three, at 128 registers: 77).
+// the next bound: 16383 x 2560 in bfloat16 takes 55 us forward (6.1 TB/s) and 71 backward (4.7), with four
+// blocks of five warps an SM (three, at 128 registers: 77); neither issue (64 and 61 %) nor DRAM (64 and 55 %)
+// is at its end.  In fp32 119 us forward and 218 both ways, floors 99 and 198.
 // Rows that outgrow the registers (k_*_wide) are
 // read two or three times, from L2 after the first, and their grad_w and grad_b
 // come from a pass over columns.  The block's partial grad_w and grad_b are rows of
@@ -256,7 +257,8 @@ __global__ void __launch_bounds__(LANES ? kLaneThreads : V::N > 1 && NV <= 2 ? 6
           sq[e] = fma(s[j][e], s[j][e], sq[e]);
         }
     const float var = over_row<Sum, LANES>(sum(sq), part_, turn);
-    if (!LANES && a.b) weights<V, NV, LANES>(r, b, a.b);     // from L1: kept, it would spill
+    if (!LANES && a.b) weights<V, NV, LANES>(r, b, a.b);     // from L1: kept, it would spill (4 vectors of bfloat16
+                                                              // spill 176 bytes as it is)
     const float rstd = 1.f / sqrtf(fmaf(var, inv_d, a.eps));
     if (on && r.l == 0) {
       if (a.mean) a.mean[row] = mean;

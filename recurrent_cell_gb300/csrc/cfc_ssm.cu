@@ -10,8 +10,8 @@
 // scheduler each) and 32 multiply-adds of pairs (2) a token, 122 instructions with the reads and the sums,
 // and two such warps a scheduler issue 56 % of its cycles.  More warps have no room: at 128
 // registers it took 235 us where it now takes 168, partial sums of y through shared memory instead of
-// lane steps 182.  bfloat16, 16 states: 1 x 16384 rows x 2048 channels 115 + 8 + 168 us,
-// 8 x 2048 x 4096 (whole) 389 us.
+// lane steps 182.  bfloat16, 16 states: 1 x 16384 rows x 2048 channels 109 + 7 + 167 us
+// (281 the call), 8 x 2048 x 4096 (whole) 378 us; fp32 317 and 425 the calls.
 #include "ssm_common.cuh"
 
 namespace cfc {
@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(64, kResident) k_ssm(Args a, bool save) {
 #pragma unroll
           for (int e = 0; e < VP; ++e) y[e] = fma2(D[e], x[e], y[e]);
           if (a.z) {
+            // (fp32 too: the exponent's rounding is |z| 6e-8 of the gate, below what C . h has gathered by then, where
+            // the convolution, whose sums are a few terms, puts it right)
             U::get(x, zv[k]);
 #pragma unroll
             for (int e = 0; e < VP; ++e) y[e] = mul2(y[e], mul2(x[e], sigmoid2(x[e])));

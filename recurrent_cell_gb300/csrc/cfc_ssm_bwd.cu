@@ -19,7 +19,9 @@
 // the next one's arithmetic.  16384 rows x 4096 channels x 16 states, bfloat16: 1261 us; with one
 // warp that does everything 1360; helpers without the delayed sums 1311; registers 152 | 104,
 // 168 | 88, 184 | 72: 1343, 1314, 1269; the second sweep unrolled 1, 3, 5, 15 times: 1470,
-// 1261, 1327, 1442 (its code leaves the instruction cache); states read a token ahead: 1312.
+// 1261, 1327, 1442 (its code leaves the instruction cache); states read a token ahead: 1312.  The
+// compiler still spills there: 192 bytes stored and 224 loaded a thread (180 and 240 with 64 states).  32 and
+// 64 states, whose tiles are 16 and 8 channels wide: 2.6 and 8.4 ms; fp32 1314 us.
 //
 // Sums over a channel's states and over a tile's channels are taken by lane steps that
 // halve the values as they go: 12 values over 4 lanes in 9 steps, 8 over 8 in 7.  Four
@@ -712,7 +714,8 @@ static cudaError_t backward(const Args& a, const Plan& p, cudaStream_t st) {
   constexpr size_t smem = sizeof(BwdBlock<G>);
   static_assert(smem <= 226 * 1024, "shared memory");
   cudaError_t e = allow_smem<k_ssm_bwd<G>>(smem);
-  // a block launched with fewer registers than the split hands out would wait for them for ever
+  // A block launched with fewer registers than the split hands out would wait for them for ever.  (By the count that
+  // the compiler reports, which is 128 for every variant; that the hardware may round a smaller one up is not relied on.)
   if (e == cudaSuccess) e = launch_regs<k_ssm_bwd<G>>() >= kLaunchRegs ? cudaSuccess : cudaErrorLaunchOutOfResources;
   if (e != cudaSuccess) return e;
   const int quads = (a.tpg + kBwdWarps - 1) / kBwdWarps;

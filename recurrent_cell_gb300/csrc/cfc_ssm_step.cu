@@ -2,14 +2,14 @@
 // sequences, each with its state in a slot of a pool, updated in place.
 //
 // A step reads a state and writes it: 8 N bytes a channel, against an exponential and
-// four multiply-adds a state, so memory is the bound.  A warp takes 32 channels: each
+// four multiply-adds a state, so memory is the floor.  A warp takes 32 channels: each
 // lane forms dt, dt x and the gate of one of them, then eight channels at a time have four
 // lanes each, with a quarter of the states in registers, and the sums over states
 // come back to their channels' lanes.  Where there are sequences enough for every SM, a
 // warp takes several with the same channels, so that A comes from L1 (192 sequences x 4096
 // channels x 16 states: one a warp 32 us, 5 a warp 27).  Up to 16 states the next sequence is copied
-// ahead into shared memory meanwhile (k_ssm_step_ahead): 23.4 us, 68 % of memory's rate; 512 sequences
-// 59 -> 54.  Ahead into registers it was slower (29), as were copies ahead of 32 states (42 -> 58): the
+// ahead into shared memory meanwhile (k_ssm_step_ahead): 23.4 us, 68 % of memory's rate, bound by instructions
+// (596 a warp and sequence, 61 % of the issue slots) with the one round's start and end; 512 sequences 59 -> 54.  Ahead into registers it was slower (29), as were copies ahead of 32 states (42 -> 58): the
 // blocks that fit are too few.
 #include "ssm_common.cuh"
 

@@ -42,8 +42,8 @@ struct Args {
   Seqs s;
   int d, groups, N;
   int per, tpg;                              // channels of a group, its tiles
-  int vec_bc;                                // rows of B and C are whole 16-byte vectors (a prompt of 16384 x 2048:
-                                             // 115 + 168 us, value by value 149 + 215)
+  int vec_bc;                                // rows of B and C are whole 16-byte vectors (a prompt of 16384 x 2048, both
+                                             // passes by events: 115 + 168 us, value by value 149 + 215)
   long long S;                               // rows of a segment
   int n_seg, tiles, cps;                     // chunks of a segment
   const float* init;
